@@ -310,6 +310,66 @@ wl_status weightless_decompose_als(const void *d_w, int32_t m, int32_t N, int32_
                                    int32_t power_iters, int32_t sweeps, const float *d_omega, void *d_w0, float *d_s,
                                    void *d_u, void *d_v, void *d_ws, size_t ws_bytes, void *stream);
 
+/* ---- 8-bit coded operands and their product ----
+ * For projections that stay dense beside the shared ones, and for the
+ * activations a training step keeps: an operand coded in OCP E4M3 with one
+ * power-of-two scale per block of 128 along K -- 128 elements of one token row
+ * for activations, 128 rows x 128 k for weights (the last blocks short).
+ * Coding of a block: e = the smallest integer with max|x| <= 448 * 2^e, at
+ * least -118, and 0 for a block of zeros; code = E4M3(x * 2^-e), nearest even;
+ * the block stands for code * 2^e, which is a bf16 value exactly (for that,
+ * |code| stops at 240 in a block with e = 120, the largest there is).  An element
+ * that is infinite or NaN gets the NaN code (0x7F or 0xFF) and does not count
+ * in max|x|; it makes NaN of every product it enters and of nothing else.
+ *
+ * A coded buffer (device memory, 256-byte aligned, caller-owned) of R rows by
+ * K, with Kq = K rounded up to 128 and nb = Kq / 128:
+ *   codes  [R][Kq] bytes, row-major (codes at k >= K are zero), at offset 0
+ *   scales [nb][Rp] bytes e + 127 (E8M0), at the next multiple of 256 bytes;
+ *          activations: Rp = T rounded up to 16, byte [b][t] for token t;
+ *          weights: Rp = ceil(N / 128) rounded up to 4, byte [b][n / 128].
+ * K % 8 == 0 as everywhere; N, K, T in [1, 2^20], T 0 allowed (no-op), and
+ * T * nb < 2^30.  WL_ESHAPE otherwise.  Buffers of one call must not overlap
+ * (WL_EINVAL). */
+
+/* Bytes of a coded buffer of activations x [T, K] (tokens are rows) or of a
+ * weight [N, K]; 0 with wl_last_error() set on error. */
+size_t weightless_act_code_bytes(int32_t T, int32_t K);
+size_t weightless_weight_code_bytes(int32_t N, int32_t K);
+
+/* Code d_x bf16 [T, K] (16-byte aligned) into d_code (code_bytes of at least
+ * weightless_act_code_bytes(T, K), else WL_ENOSPACE).  This is the 8-bit
+ * checkpoint the backward entry points read.  One launch. */
+wl_status weightless_act_encode(const void *d_x, int32_t T, int32_t K, void *d_code, size_t code_bytes, void *stream);
+
+/* The values a coded activation buffer stands for: d_x bf16 [T, K] (16-byte
+ * aligned) = code * 2^e, exact.  One launch. */
+wl_status weightless_act_expand(const void *d_code, size_t code_bytes, int32_t T, int32_t K, void *d_x, void *stream);
+
+/* Code d_w bf16 [N, K] (16-byte aligned) into d_code.  One launch. */
+wl_status weightless_weight_encode(const void *d_w, int32_t N, int32_t K, void *d_code, size_t code_bytes,
+                                   void *stream);
+
+/* y = x w^T of coded operands: d_y bf16 [T, N],
+ *   y[t][n] = sum_b 2^(ex[t][b] + ew[n/128][b]) sum_{k in b} cx[t][k] cw[n][k],
+ * on the 8-bit matrix cores: the products of 8 consecutive k are added on a
+ * grid 2^-13 of the largest one (the instruction's own), those sums in
+ * float32, with one rounding to bf16.
+ *  d_wcode: weight [N, K] from weightless_weight_encode.
+ *  d_x: bf16 [T, K] (16-byte aligned) to be coded into d_xcode first, or NULL
+ *    if d_xcode already holds coded activations.  With d_x, d_xcode receives
+ *    exactly what weightless_act_encode writes (a checkpoint to keep).
+ *  d_ws: weightless_coded_linear_workspace_bytes(N, K, T) bytes, 256-byte
+ *    aligned, no initialization, nothing kept; may be NULL if that is 0 bytes
+ *    (always so for T <= 16).  Concurrent calls need distinct workspaces.
+ *  T <= 16 streams the weights once through registers (one launch, and one for
+ *  coding x); T > 16 runs LDS-tiled matrix-core products, K split over
+ *  workgroups and summed by a second launch when there are few output tiles. */
+size_t weightless_coded_linear_workspace_bytes(int32_t N, int32_t K, int32_t T);
+wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32_t N, int32_t K, const void *d_x,
+                                  void *d_xcode, size_t xcode_bytes, int32_t T, void *d_y, void *d_ws,
+                                  size_t ws_bytes, void *stream);
+
 /* Output width N of a single-family call, or of a stacked call (stack >= 0
  * with family < 0); 0 on error.  Host-only. */
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack);

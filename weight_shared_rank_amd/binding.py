@@ -34,7 +34,10 @@ EXPORTS = ("theta_bundle_arena_bytes", "theta_bundle_load", "theta_bundle_free",
            "weightless_linear", "weightless_linear_noalloc", "weightless_stacked_linear", "weightless_out_dim", "wl_last_error",
            "weightless_materialize_workspace_bytes", "weightless_materialize", "weightless_gate_up_act",
            "weightless_decompose_workspace_bytes", "weightless_decompose",
-           "weightless_decompose_als_workspace_bytes", "weightless_decompose_als")
+           "weightless_decompose_als_workspace_bytes", "weightless_decompose_als",
+           "weightless_act_code_bytes", "weightless_weight_code_bytes", "weightless_act_encode",
+           "weightless_act_expand", "weightless_weight_encode",
+           "weightless_coded_linear_workspace_bytes", "weightless_coded_linear")
 
 
 class WlBundleSpec(ctypes.Structure):
@@ -92,6 +95,13 @@ def lib():
         "weightless_decompose": (i32, [vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
         "weightless_decompose_als_workspace_bytes": (sz, [i32, i32, i32, i32]),
         "weightless_decompose_als": (i32, [vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "weightless_act_code_bytes": (sz, [i32, i32]),
+        "weightless_weight_code_bytes": (sz, [i32, i32]),
+        "weightless_act_encode": (i32, [vp, i32, i32, vp, sz, vp]),
+        "weightless_act_expand": (i32, [vp, sz, i32, i32, vp, vp]),
+        "weightless_weight_encode": (i32, [vp, i32, i32, vp, sz, vp]),
+        "weightless_coded_linear_workspace_bytes": (sz, [i32, i32, i32]),
+        "weightless_coded_linear": (i32, [vp, sz, i32, i32, vp, vp, sz, i32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -328,3 +338,164 @@ def decompose(w, rank: int, omega=None, oversample: int = 16, power_iters: int =
               u.data_ptr() if rank > 0 else None, v.data_ptr() if rank > 0 else None,
               ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
     return w0, s, u, v
+
+
+# ---- 8-bit coded operands -------------------------------------------------
+
+CODE_BLOCK = 128
+
+
+def _scope(device, stream):
+    """The device and stream a call runs on: the given stream, or the current
+    stream of the tensors' device.  Everything the call allocates is then
+    allocated on that stream."""
+    import contextlib
+
+    import torch
+    if stream is not None:
+        if stream.device != device:
+            raise WlError(-1, f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _check_tensor(t, name, shape, dtype, device=None):
+    """A contiguous device tensor of this shape (None: any extent) and dtype."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() \
+            or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise WlError(-1, f"{name} must be a contiguous {dtype} [{want}] device tensor, got {t.dtype} "
+                          f"{list(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise WlError(-1, f"{name} is on {t.device}, expected {device}")
+
+
+class _Code:
+    """A coded buffer and its shape (rows R by K); layout in include/weightless.h."""
+
+    _rows_per_scale, _run_multiple, _bytes = 1, 16, "weightless_act_code_bytes"
+
+    def __init__(self, rows: int, K: int, device="cuda", buf=None):
+        import torch
+        self.rows, self.K = rows, K
+        need = getattr(lib(), self._bytes)(rows, K)
+        if need == 0:
+            raise WlError(-2, last_error())
+        self.buf = torch.empty(need, dtype=torch.uint8, device=device) if buf is None else buf
+        _check_tensor(self.buf, "code buffer", (None,), torch.uint8)
+        if self.buf.numel() < need:
+            raise WlError(-5, f"code buffer has {self.buf.numel()} bytes, needs {need}")
+
+    @property
+    def blocks(self) -> int:
+        return -(-self.K // CODE_BLOCK)
+
+    @property
+    def codes(self):
+        """The E4M3 codes [rows, K] (a view)."""
+        import torch
+        kq = self.blocks * CODE_BLOCK
+        return self.buf[:self.rows * kq].view(torch.float8_e4m3fn).view(self.rows, kq)[:, :self.K]
+
+    @property
+    def scales(self):
+        """The scale bytes e + 127, [rows (or 128-row blocks), blocks of K] (a view)."""
+        n = -(-self.rows // self._rows_per_scale)
+        run = -(-n // self._run_multiple) * self._run_multiple
+        at = -(-self.rows * self.blocks * CODE_BLOCK // 256) * 256
+        return self.buf[at:at + self.blocks * run].view(self.blocks, run)[:, :n].t()
+
+
+class ActCode(_Code):
+    """8-bit activations [T, K]: one scale per token and 128 k.  The coded
+    operand of coded_linear and the checkpoint of the backward calls."""
+
+    @property
+    def T(self) -> int:
+        return self.rows
+
+    def expand(self, out=None, stream=None):
+        """The bf16 values [T, K] the codes stand for."""
+        import torch
+        with _scope(self.buf.device, stream):
+            if out is None:
+                out = torch.empty((self.rows, self.K), dtype=torch.bfloat16, device=self.buf.device)
+            _check_tensor(out, "out", (self.rows, self.K), torch.bfloat16, self.buf.device)
+            _check(lib().weightless_act_expand(self.buf.data_ptr(), self.buf.numel(), self.rows, self.K,
+                                               out.data_ptr(), _stream_ptr(None)))
+        return out
+
+
+class WeightCode(_Code):
+    """8-bit weight [N, K]: one scale per 128 x 128 block."""
+
+    _rows_per_scale, _run_multiple, _bytes = CODE_BLOCK, 4, "weightless_weight_code_bytes"
+
+    @property
+    def N(self) -> int:
+        return self.rows
+
+
+def _code_out(cls, rows, K, device, out):
+    if out is None:
+        return cls(rows, K, device)
+    if not isinstance(out, cls) or (out.rows, out.K) != (rows, K) or out.buf.device != device:
+        raise WlError(-1, f"out must be a {cls.__name__} of {rows} x {K} on {device}")
+    return out
+
+
+def encode_act(x, out: Optional[ActCode] = None, stream=None) -> ActCode:
+    """Code activations x bf16 [T, K] (weightless_act_encode)."""
+    import torch
+    _check_tensor(x, "x", (None, None), torch.bfloat16)
+    with _scope(x.device, stream):
+        out = _code_out(ActCode, x.shape[0], x.shape[1], x.device, out)
+        _check(lib().weightless_act_encode(x.data_ptr(), out.rows, out.K, out.buf.data_ptr(), out.buf.numel(),
+                                           _stream_ptr(None)))
+    return out
+
+
+def encode_weight(w, out: Optional[WeightCode] = None, stream=None) -> WeightCode:
+    """Code a weight w bf16 [N, K] (weightless_weight_encode)."""
+    import torch
+    _check_tensor(w, "w", (None, None), torch.bfloat16)
+    with _scope(w.device, stream):
+        out = _code_out(WeightCode, w.shape[0], w.shape[1], w.device, out)
+        _check(lib().weightless_weight_encode(w.data_ptr(), out.rows, out.K, out.buf.data_ptr(), out.buf.numel(),
+                                              _stream_ptr(None)))
+    return out
+
+
+def coded_linear(w: WeightCode, x, y=None, code: Optional[ActCode] = None, ws=None, stream=None):
+    """y = x w^T in 8 bits, bf16 [T, N] (weightless_coded_linear).
+
+    x: bf16 [T, K], coded first (into `code`, if given: the checkpoint to
+    keep), or an ActCode that already holds the coded activations."""
+    import torch
+    dev = w.buf.device
+    with _scope(dev, stream):
+        if isinstance(x, ActCode):
+            if code is not None:
+                raise WlError(-1, "code is only for a bf16 x")
+            if x.K != w.K or x.buf.device != dev:
+                raise WlError(-1, f"x is coded as [{x.T}, {x.K}] on {x.buf.device}, the weight is "
+                                  f"[{w.N}, {w.K}] on {dev}")
+            code, src = x, None
+        else:
+            _check_tensor(x, "x", (None, w.K), torch.bfloat16, dev)
+            code, src = _code_out(ActCode, x.shape[0], w.K, dev, code), x.data_ptr()
+        T = code.rows
+        if y is None:
+            y = torch.empty((T, w.rows), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_tensor(y, "y", (T, w.rows), torch.bfloat16, dev)
+        if ws is None and T > DECODE_MAX_T:
+            need = lib().weightless_coded_linear_workspace_bytes(w.rows, w.K, T)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(lib().weightless_coded_linear(w.buf.data_ptr(), w.buf.numel(), w.rows, w.K, src, code.buf.data_ptr(),
+                                             code.buf.numel(), T, y.data_ptr(),
+                                             ws.data_ptr() if ws is not None else None,
+                                             ws.numel() if ws is not None else 0, _stream_ptr(None)))
+    return y

@@ -488,6 +488,74 @@ wl_status scratch_of_current_device(void **out) {
   return WL_OK;
 }
 
+// ---- 8-bit coded operands ----
+
+constexpr int kCodeBlock = 128;
+
+// Sizes of a coded buffer of R rows by K whose scale runs hold rp bytes.
+struct CodeShape {
+  int32_t nb;
+  int64_t rp;
+  size_t scales_off, bytes;
+};
+
+CodeShape code_shape(int32_t R, int32_t K, bool weight) {
+  CodeShape c;
+  c.nb = (K + kCodeBlock - 1) / kCodeBlock;
+  c.rp = weight ? ((static_cast<int64_t>(R) + kCodeBlock - 1) / kCodeBlock + 3) & ~int64_t{3}
+                : (static_cast<int64_t>(R) + 15) & ~int64_t{15};
+  c.scales_off = align256(static_cast<size_t>(R) * c.nb * kCodeBlock);
+  c.bytes = std::max<size_t>(256, c.scales_off + align256(static_cast<size_t>(c.nb) * c.rp));
+  return c;
+}
+
+wl::CodedView code_view(const void *d_code, const CodeShape &c) {
+  const uint8_t *p = static_cast<const uint8_t *>(d_code);
+  return wl::CodedView{p, p + c.scales_off, c.nb, static_cast<int32_t>(c.rp)};
+}
+
+wl_status check_code_k(int32_t K) {
+  if (K < 1 || K > kMaxDim) return fail(WL_ESHAPE, "K = %d out of range", K);
+  if (K % 8) return fail(WL_ESHAPE, "K = %d is not a multiple of 8", K);
+  return WL_OK;
+}
+
+wl_status check_act_shape(int32_t T, int32_t K) {
+  const wl_status st = check_code_k(K);
+  if (st != WL_OK) return st;
+  if (T < 0) return fail(WL_EINVAL, "T = %d is negative", T);
+  if (T > kMaxDim) return fail(WL_ESHAPE, "T = %d too large", T);
+  const CodeShape c = code_shape(T, K, false);
+  if (c.nb * c.rp >= (int64_t{1} << 30)) return fail(WL_ESHAPE, "T = %d by K = %d exceeds 2^30 blocks", T, K);
+  return WL_OK;
+}
+
+wl_status check_weight_shape(int32_t N, int32_t K) {
+  const wl_status st = check_code_k(K);
+  if (st != WL_OK) return st;
+  if (N < 1 || N > kMaxDim) return fail(WL_ESHAPE, "N = %d out of range", N);
+  return WL_OK;
+}
+
+// A coded buffer argument: present, aligned, large enough.
+wl_status check_code_buffer(const void *d_code, size_t have, size_t need, const char *what) {
+  if (!d_code) return fail(WL_EINVAL, "%s is NULL", what);
+  if (reinterpret_cast<uintptr_t>(d_code) % 256) return fail(WL_EINVAL, "%s must be 256-byte aligned", what);
+  if (have < need) return fail(WL_ENOSPACE, "%s has %zu bytes, needs %zu", what, have, need);
+  return WL_OK;
+}
+
+wl_status check_aligned(const void *p, size_t align, const char *what) {
+  if (!p) return fail(WL_EINVAL, "%s is NULL", what);
+  if (reinterpret_cast<uintptr_t>(p) % align) return fail(WL_EINVAL, "%s must be %zu-byte aligned", what, align);
+  return WL_OK;
+}
+
+bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an && bn && x < y + bn && y < x + an;
+}
+
 }  // namespace
 
 namespace wl {
@@ -733,6 +801,93 @@ wl_status weightless_materialize(const wl_bundle *bundle, int32_t layer, int32_t
                              reinterpret_cast<const uint16_t *>(bundle->arena + bundle->lo.zero_off), s);
   if (e != hipSuccess) return hip_fail(e, "kernel launch");
   return WL_OK;
+}
+
+size_t weightless_act_code_bytes(int32_t T, int32_t K) {
+  if (check_act_shape(T, K) != WL_OK) return 0;
+  return code_shape(T, K, false).bytes;
+}
+
+size_t weightless_weight_code_bytes(int32_t N, int32_t K) {
+  if (check_weight_shape(N, K) != WL_OK) return 0;
+  return code_shape(N, K, true).bytes;
+}
+
+wl_status weightless_act_encode(const void *d_x, int32_t T, int32_t K, void *d_code, size_t code_bytes, void *stream) {
+  wl_status st = check_act_shape(T, K);
+  if (st != WL_OK || T == 0) return st;
+  const CodeShape c = code_shape(T, K, false);
+  if ((st = check_aligned(d_x, 16, "x")) != WL_OK) return st;
+  if ((st = check_code_buffer(d_code, code_bytes, c.bytes, "code buffer")) != WL_OK) return st;
+  if (overlap(d_x, static_cast<size_t>(T) * K * 2, d_code, c.bytes)) return fail(WL_EINVAL, "code buffer must not overlap x");
+  const hipError_t e = wl::launch_encode_act(static_cast<const uint16_t *>(d_x), T, K, code_view(d_code, c),
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "encode launch");
+}
+
+wl_status weightless_act_expand(const void *d_code, size_t code_bytes, int32_t T, int32_t K, void *d_x, void *stream) {
+  wl_status st = check_act_shape(T, K);
+  if (st != WL_OK || T == 0) return st;
+  const CodeShape c = code_shape(T, K, false);
+  if ((st = check_aligned(d_x, 16, "x")) != WL_OK) return st;
+  if ((st = check_code_buffer(d_code, code_bytes, c.bytes, "code buffer")) != WL_OK) return st;
+  if (overlap(d_x, static_cast<size_t>(T) * K * 2, d_code, c.bytes)) return fail(WL_EINVAL, "x must not overlap the code buffer");
+  const hipError_t e = wl::launch_expand_act(code_view(d_code, c), T, static_cast<uint16_t *>(d_x), K,
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "expand launch");
+}
+
+wl_status weightless_weight_encode(const void *d_w, int32_t N, int32_t K, void *d_code, size_t code_bytes,
+                                   void *stream) {
+  wl_status st = check_weight_shape(N, K);
+  if (st != WL_OK) return st;
+  const CodeShape c = code_shape(N, K, true);
+  if ((st = check_aligned(d_w, 16, "w")) != WL_OK) return st;
+  if ((st = check_code_buffer(d_code, code_bytes, c.bytes, "code buffer")) != WL_OK) return st;
+  if (overlap(d_w, static_cast<size_t>(N) * K * 2, d_code, c.bytes)) return fail(WL_EINVAL, "code buffer must not overlap w");
+  const hipError_t e = wl::launch_encode_weight(static_cast<const uint16_t *>(d_w), N, K, code_view(d_code, c),
+                                                static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "encode launch");
+}
+
+size_t weightless_coded_linear_workspace_bytes(int32_t N, int32_t K, int32_t T) {
+  if (check_weight_shape(N, K) != WL_OK || check_act_shape(T, K) != WL_OK) return 0;
+  g_err.clear();
+  return align256(wl::coded_partial_bytes(N, T, K));
+}
+
+wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32_t N, int32_t K, const void *d_x,
+                                  void *d_xcode, size_t xcode_bytes, int32_t T, void *d_y, void *d_ws,
+                                  size_t ws_bytes, void *stream) {
+  wl_status st = check_weight_shape(N, K);
+  if (st == WL_OK) st = check_act_shape(T, K);
+  if (st != WL_OK || T == 0) return st;
+  const CodeShape cw = code_shape(N, K, true), cx = code_shape(T, K, false);
+  if ((st = check_code_buffer(d_wcode, wcode_bytes, cw.bytes, "weight code buffer")) != WL_OK) return st;
+  if ((st = check_code_buffer(d_xcode, xcode_bytes, cx.bytes, "activation code buffer")) != WL_OK) return st;
+  if (d_x && (st = check_aligned(d_x, 16, "x")) != WL_OK) return st;
+  if ((st = check_aligned(d_y, 2, "y")) != WL_OK) return st;
+  const size_t need = align256(wl::coded_partial_bytes(N, T, K));
+  if (need) {
+    if ((st = check_aligned(d_ws, 256, "workspace")) != WL_OK) return st;
+    if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
+  }
+  const size_t xb = static_cast<size_t>(T) * K * 2, yb = static_cast<size_t>(T) * N * 2;
+  if (overlap(d_y, yb, d_x, xb) || overlap(d_y, yb, d_xcode, cx.bytes) || overlap(d_y, yb, d_wcode, cw.bytes) ||
+      overlap(d_xcode, cx.bytes, d_x, xb) || overlap(d_xcode, cx.bytes, d_wcode, cw.bytes))
+    return fail(WL_EINVAL, "x, y and the code buffers must not overlap");
+  if (need && (overlap(d_ws, need, d_y, yb) || overlap(d_ws, need, d_x, xb) || overlap(d_ws, need, d_xcode, cx.bytes) ||
+               overlap(d_ws, need, d_wcode, cw.bytes)))
+    return fail(WL_EINVAL, "the workspace must not overlap x, y or the code buffers");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const wl::CodedView x = code_view(d_xcode, cx);
+  if (d_x) {
+    const hipError_t e = wl::launch_encode_act(static_cast<const uint16_t *>(d_x), T, K, x, s);
+    if (e != hipSuccess) return hip_fail(e, "encode launch");
+  }
+  const hipError_t e = wl::launch_coded_linear(code_view(d_wcode, cw), N, x, T, static_cast<uint16_t *>(d_y),
+                                               static_cast<float *>(d_ws), s);
+  return e == hipSuccess ? WL_OK : hip_fail(e, "kernel launch");
 }
 
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack) {
