@@ -370,6 +370,54 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
                                   void *d_xcode, size_t xcode_bytes, int32_t T, void *d_y, void *d_ws,
                                   size_t ws_bytes, void *stream);
 
+/* ---- Backward pass of the weightless linear ----
+ * Gradients of y = s (.) (x W0^T) + (x V) U^T from the 8-bit checkpoint of x
+ * (weightless_act_encode) instead of x itself; with X the values the
+ * checkpoint stands for and dy the gradient of y:
+ *   dx  = (dy (.) s) W0 + (dy U) V^T
+ *   ds_n = sum_k G[n][k] W0[n][k],  dW0 = diag(s) G,  G = dy^T X
+ *   dU  = dy^T (X V),  dV = X^T (dy U)
+ * W0 is the block the bundle holds (FP8 and MXFP4 bundles: the values of its
+ * codes).  Products of bf16 operands with float32 sums; dy (.) s, X V and
+ * dy U are rounded to bf16 once as operands, dx, dU and dV once at the end;
+ * G, ds and dW0 are float32 throughout.  Results are the same bits from run
+ * to run. */
+typedef struct {
+  void *dx;         /* bf16 [T, K] */
+  float *ds;        /* float32 [N] */
+  void *du[3];      /* bf16 [N_c, r_c] of child c */
+  void *dv[3];      /* bf16 [K, r_c] of child c */
+  float *dw0;       /* float32 [N, K] */
+  int32_t accumulate_dw0; /* nonzero: dw0 += (the layers of a band share W0) */
+} wl_grads;
+
+/* Workspace bytes of any backward call on this bundle with T tokens; 0 with
+ * wl_last_error() set on error. */
+size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T);
+
+/* Gradients of weightless_linear (one family) and of weightless_stacked_linear.
+ *  d_xcode: coded activations [T, K] (xcode_bytes >= weightless_act_code_bytes).
+ *  d_dy bf16 [T, N] with y's columns (the stacked call's layout, the tied v
+ *    slot included: its gradient adds to k's); 2-byte aligned (16-byte aligned
+ *    with every child's N a multiple of 8 saves a copy of it).
+ *  grads: the outputs wanted; NULL members are not computed.  Children of a
+ *    stacked call in the order q, k, v / gate, up; a tied type has the children
+ *    q, k, and a single-family call child 0 (WL_V on a tied type: k's bundle).
+ *    ds and dw0 hold the children's rows concatenated (N their sum, without the
+ *    tied slot).  Members of children the call lacks, and of rank 0, are not
+ *    looked at.  dx and dw0 16-byte, ds 4-byte, du and dv 2-byte aligned; no
+ *    output may overlap another, dy, the checkpoint, the workspace or the arena
+ *    (WL_EINVAL).
+ *  T = 0: ds, du, dv and dw0 (unless accumulated) are zeroed.
+ *  d_ws: weightless_backward_workspace_bytes(bundle, T), 256-byte aligned, no
+ *    initialization, nothing kept; concurrent calls need distinct workspaces. */
+wl_status weightless_linear_backward(const wl_bundle *bundle, int32_t layer, int32_t family, const void *d_xcode,
+                                     size_t xcode_bytes, const void *d_dy, int32_t T, const wl_grads *grads,
+                                     void *d_ws, size_t ws_bytes, void *stream);
+wl_status weightless_stacked_backward(const wl_bundle *bundle, int32_t layer, int32_t stack, const void *d_xcode,
+                                      size_t xcode_bytes, const void *d_dy, int32_t T, const wl_grads *grads,
+                                      void *d_ws, size_t ws_bytes, void *stream);
+
 /* Output width N of a single-family call, or of a stacked call (stack >= 0
  * with family < 0); 0 on error.  Host-only. */
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack);

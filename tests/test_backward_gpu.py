@@ -1,0 +1,440 @@
+"""GPU: gradients of the weightless linear from an 8-bit checkpoint.
+
+The reference is torch autograd over the forward written out in float64 (on
+the GPU), at the checkpoint's own values; a second test holds the results to
+differences of that forward.  Tolerances, derived before the first run, per
+element: a bf16 rounding 2^-8 of the value, a float32 sum of n terms n * 2^-23
+of the sum of their magnitudes; with |.| elementwise and X, D = dy:
+
+  ds   (T + K + 8) 2^-23  sum_k (|D|^T |X|) |W0|
+  dW0  |s| (T + 8) 2^-23  |D|^T |X|
+  z    e_z = 2^-8 |X V| + K 2^-23 |X| |V|        (g likewise with D, U)
+  dU   |D|^T e_z + (T + 8) 2^-23 |D|^T |X V| + 2^-8 |dU|
+  dV   |X|^T e_g + (T + 8) 2^-23 |X|^T |D U| + 2^-8 |dV|
+  dx   (2^-8 + (N + r + 8) 2^-23) (|D| |s|) |W0| + e_g |V|^T
+       + (N + r + 8) 2^-23 |D U| |V|^T + 2^-8 |dx|
+
+and, the roundings of many terms being independent, the error's norm within
+2 * 2^-8 of the result's (two roundings on the way to a bf16 result)."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from weight_shared_rank_amd import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+H, F = 2.0 ** -8, 2.0 ** -23
+ALL = ("dx", "ds", "du", "dv", "dw0")
+
+
+def announce(msg):
+    sys.__stderr__.write(f"[gpu] {msg}\n")
+    sys.__stderr__.flush()
+
+
+def randn(seed, *shape, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).to(DEV)
+
+
+class Layer:
+    """One group of families over one K, as a bundle and as float64 tensors."""
+
+    def __init__(self, fams, rows, K, ranks, tied=False, fmt="bf16", seed=0, layers=1):
+        self.fams, self.rows, self.K, self.ranks, self.tied = fams, rows, K, ranks, tied
+        own = [f for f in fams if not (tied and f == "v")]
+        spec = binding.make_spec(layers, 1, {(0, f): (n, K) for f, n in zip(own, rows)},
+                                 {(0, f): r for f, r in zip(own, ranks)}, k_eq_v_types=(0,) if tied else (),
+                                 w0_format=fmt)
+        src, self.w0, self.s, self.u, self.v = [], [], [], [], []
+        for i, (f, n, r) in enumerate(zip(own, rows, ranks)):
+            at = seed * 100 + i * 10
+            self.w0.append(randn(at, n, K, std=K ** -0.5))
+            src.append(("w0", 0, 0, f, self.w0[-1]))
+            for l in range(layers):
+                s = 1 + 0.2 * randn(at + 1 + 1000 * l, n, dtype=torch.float32)
+                u, v = randn(at + 2 + 1000 * l, n, r, std=0.2), randn(at + 3 + 1000 * l, K, r, std=0.2)
+                src.append(("s", l, 0, f, s))
+                if r:
+                    src += [("u", l, 0, f, u), ("v", l, 0, f, v)]
+            self.s.append(s)
+            self.u.append(u)
+            self.v.append(v)
+        self.layer = layers - 1
+        self.bundle = binding.ThetaBundle(spec, src, device=DEV)
+        if fmt != "bf16":  # the values of the codes: s = 1, rank 0 materializes them exactly
+            plain = binding.ThetaBundle(
+                binding.make_spec(1, 1, {(0, f): (n, K) for f, n in zip(own, rows)}, {}, w0_format=fmt),
+                [x for f, n, w in zip(own, rows, self.w0)
+                 for x in (("w0", 0, 0, f, w), ("s", 0, 0, f, torch.ones(n, device=DEV)))], device=DEV)
+            self.w0 = [plain.materialize(0, f) for f in own]
+
+    @property
+    def stack(self):
+        return {3: "qkv", 2: "gate_up", 1: None}[len(self.fams)]
+
+    @property
+    def width(self):
+        return sum(self.rows) + (self.rows[-1] if self.tied else 0)
+
+    def backward(self, code, dy, want=ALL, **kw):
+        if self.stack:
+            return self.bundle.stacked_backward(self.layer, self.stack, code, dy, want=want, **kw)
+        g = self.bundle.linear_backward(self.layer, self.fams[0], code, dy, want=want, **kw)
+        return g._replace(du=None if g.du is None else (g.du,), dv=None if g.dv is None else (g.dv,))
+
+    def slots(self, dy):
+        """dy's columns per child (a tied v slot's as a second block of k's)."""
+        edges = np.cumsum([0] + list(self.rows) + ([self.rows[-1]] if self.tied else []))
+        parts = [dy[:, a:b] for a, b in zip(edges, edges[1:])]
+        return [[p] for p in parts[:-1]][:-1] + [[parts[-2], parts[-1]]] if self.tied else [[p] for p in parts]
+
+
+def check(lay, x, dy, g):
+    """The gradients g against autograd in float64 (and the tolerances above)."""
+    X = x.expand().double().requires_grad_(True)
+    s, u, v = ([t.double().requires_grad_(True) for t in ts] for ts in (lay.s, lay.u, lay.v))
+    w = [t.double().requires_grad_(True) for t in lay.w0]
+    D = lay.slots(dy.double())
+    loss = 0.0
+    for i, ds in enumerate(D):
+        y = (X @ w[i].t().contiguous()) * s[i] + (X @ v[i]) @ u[i].t().contiguous()
+        for d in ds:
+            loss = loss + (y * d).sum()
+    loss.backward()
+    X = X.detach()
+    T, K, N = X.shape[0], lay.K, sum(lay.rows)
+    tol = {"dx": torch.zeros_like(X), "ds": [], "dw0": [], "du": [], "dv": []}
+    depth = sum(len(ds) * n for ds, n in zip(D, lay.rows)) + sum(lay.ranks) + 8
+    for i, ds in enumerate(D):
+        a, b = X.abs(), sum(d.abs() for d in ds)
+        n2 = len(ds) * T + 8
+        wi, si, ui, vi = w[i].detach(), s[i].detach(), u[i].detach(), v[i].detach()
+        big = b.t().contiguous() @ a
+        tol["ds"].append((n2 + K) * F * (big * wi.abs()).sum(1))
+        tol["dw0"].append(si.abs()[:, None] * n2 * F * big)
+        z, gg = X @ vi, sum(d @ ui for d in ds)
+        ez = H * z.abs() + K * F * (a @ vi.abs())
+        eg = H * gg.abs() + depth * F * (b @ ui.abs())
+        tol["du"].append(b.t().contiguous() @ (ez + n2 * F * z.abs()) + H * u[i].grad.abs())
+        tol["dv"].append(a.t().contiguous() @ (eg + n2 * F * gg.abs()) + H * v[i].grad.abs())
+        tol["dx"] += (H + depth * F) * ((b * si.abs()) @ wi.abs()) + (eg + depth * F * gg.abs()) @ vi.abs().t().contiguous()
+    ref = {"dx": x_grad(X, lay, D, s, u, v, w), "ds": torch.cat([t.grad for t in s]),
+           "dw0": torch.cat([t.grad for t in w]), "du": [t.grad for t in u], "dv": [t.grad for t in v]}
+    tol["dx"] += H * ref["dx"].abs()
+    tol["ds"], tol["dw0"] = torch.cat(tol["ds"]), torch.cat(tol["dw0"])
+
+    def one(name, got, want, bound, norm):
+        assert got.shape == want.shape, name
+        err = (got.double() - want).abs()
+        bad = torch.nonzero(~(err <= bound))
+        assert len(bad) == 0, (name, bad[:3], got[tuple(bad[0])].item(), want[tuple(bad[0])].item())
+        if want.numel() >= 64:  # a norm over a handful of elements averages nothing
+            assert err.norm() <= norm * want.norm(), (name, (err.norm() / want.norm()).item())
+    for name in ("dx", "ds", "dw0"):
+        if getattr(g, name) is not None:
+            one(name, getattr(g, name), ref[name], tol[name], 2 * H if name == "dx" else 1e-5)
+    for name in ("du", "dv"):
+        if getattr(g, name) is not None:
+            assert len(getattr(g, name)) == len(D)
+            for i, t in enumerate(getattr(g, name)):
+                one(f"{name}[{i}]", t, ref[name][i], tol[name][i], 2 * H)
+
+
+def x_grad(X, lay, D, s, u, v, w):
+    out = torch.zeros_like(X)
+    for i, ds in enumerate(D):
+        d = sum(ds)
+        out += (d * s[i].detach()) @ w[i].detach() + (d @ u[i].detach()) @ v[i].detach().t().contiguous()
+    return out
+
+
+def same_bits(a, b):
+    for x, y in zip(a, b):
+        if isinstance(x, tuple):
+            same_bits(x, y)
+        elif x is not None:
+            assert torch.equal(x, y)
+
+
+O, GU, QKV = ("o",), ("gate", "up"), ("q", "k", "v")
+CASES = [(O, (16,), 8, (1,), 1), (O, (40,), 64, (4,), 1), (O, (1,), 128, (0,), 3), (O, (128,), 128, (32,), 64),
+         (O, (1001,), 712, (20,), 77), (O, (300,), 264, (0,), 130), (O, (64,), 2056, (64,), 17),
+         (O, (520,), 136, (130,), 300), (O, (72,), 72, (8,), 3000), (O, (2048,), 1024, (96,), 257),
+         (GU, (200, 200), 264, (5, 33), 65), (GU, (513, 513), 520, (64, 0), 40), (GU, (1000, 1000), 904, (70, 40), 513),
+         (QKV, (200, 72, 72), 264, (40, 33, 1), 100), (QKV, (33, 7, 9), 40, (5, 2, 3), 2),
+         (QKV, (1024, 256, 256), 1152, (64, 64, 64), 600)]
+
+
+@pytest.mark.parametrize("fams,rows,K,ranks,T", CASES)
+def test_gradients_match_autograd(gpu_lib, fams, rows, K, ranks, T):
+    lay = Layer(fams, rows, K, ranks, seed=T % 7)
+    x = randn(T, T, K)
+    x[:, K // 2] *= 24
+    announce(f"backward {fams} {rows} K={K} r={ranks} T={T}")
+    code = binding.encode_act(x)
+    dy = randn(T + 1, T, lay.width, std=T ** -0.5)
+    check(lay, code, dy, lay.backward(code, dy))
+
+
+@pytest.mark.parametrize("rows,T", [((40, 24), 9), ((130, 70), 70), ((256, 128), 400)])
+def test_tied_v_adds_to_k(gpu_lib, rows, T):
+    """K = V tying: dy has three slots, q, k and v; k's gradients sum both."""
+    lay = Layer(QKV, rows, 392, (17, 8), tied=True, seed=3)
+    code, dy = binding.encode_act(randn(1, T, 392)), randn(2, T, lay.width, std=T ** -0.5)
+    announce(f"tied {rows} T={T}")
+    check(lay, code, dy, lay.backward(code, dy))
+    # the single call for v runs k's bundle
+    g = lay.bundle.linear_backward(0, "v", code, dy[:, -rows[1]:].contiguous(), want=ALL)
+    h = lay.bundle.linear_backward(0, "k", code, dy[:, -rows[1]:].contiguous(), want=ALL)
+    same_bits(g, h)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("T", [5, 90])
+def test_coded_shared_blocks(gpu_lib, fmt, T):
+    lay = Layer(GU, (136, 136), 264, (9, 9), fmt=fmt, seed=4, layers=2)
+    code, dy = binding.encode_act(randn(3, T, 264)), randn(4, T, lay.width, std=T ** -0.5)
+    announce(f"{fmt} T={T}")
+    check(lay, code, dy, lay.backward(code, dy))
+
+
+def test_gradients_match_differences(gpu_lib):
+    """Directional central differences of the float64 forward (it is linear in
+    each of x, s, W0, U and V, so they are exact up to float64) against the
+    inner products of the gradients with the directions."""
+    lay = Layer(QKV, (96, 40, 24), 200, (6, 4, 3), seed=5)
+    T = 33
+    code, dy = binding.encode_act(randn(5, T, 200)), randn(6, T, lay.width)
+    g = lay.backward(code, dy)
+    base = {"dx": [code.expand().double()], "ds": [t.double() for t in lay.s], "dw0": [t.double() for t in lay.w0],
+            "du": [t.double() for t in lay.u], "dv": [t.double() for t in lay.v]}
+    D = lay.slots(dy.double())
+
+    def loss(p):
+        x = p["dx"][0]
+        return sum(((x @ w.t().contiguous()) * s + (x @ v) @ u.t().contiguous()).mul(d[0]).sum().item()
+                   for w, s, u, v, d in zip(p["dw0"], p["ds"], p["du"], p["dv"], D))
+    for name in ALL:
+        got = getattr(g, name)
+        got = list(got) if isinstance(got, tuple) else list(torch.split(got, [t.shape[0] for t in base[name]]))
+        for i, t in enumerate(base[name]):
+            d = randn(70 + i, *t.shape, dtype=torch.float32).double()
+            up, dn = (dict(base, **{name: [b + e * d if j == i else b for j, b in enumerate(base[name])]})
+                      for e in (0.5, -0.5))
+            want, have = loss(up) - loss(dn), (got[i].double() * d).sum().item()
+            # <grad, d> is off by at most |error| |d|, the error's norm within 2 * 2^-8 of the gradient's
+            assert abs(have - want) <= 2 * H * got[i].double().norm().item() * d.norm().item(), (name, i)
+
+
+def test_subsets_give_the_same_bits(gpu_lib):
+    lay = Layer(QKV, (200, 72, 40), 264, (40, 33, 8), seed=6)
+    code, dy = binding.encode_act(randn(7, 100, 264)), randn(8, 100, lay.width)
+    full = lay.backward(code, dy)
+    for want in (("dx",), ("ds",), ("du",), ("dv",), ("dw0",), ("dx", "dv"), ("ds", "du"), ()):
+        announce(f"want {want}")
+        part = lay.backward(code, dy, want=want)
+        for name in ALL:
+            a, b = getattr(full, name), getattr(part, name)
+            assert (b is None) == (name not in want)
+            if b is not None:
+                same_bits((a,), (b,))
+
+
+@pytest.mark.parametrize("T,rows", [(40, 300), (2500, 24)])
+def test_accumulated_block_gradient(gpu_lib, T, rows):
+    """dw0 += over the layers of a band: the sum of the calls' own gradients,
+    one float32 rounding per addition; both with and without a split."""
+    lay = Layer(O, (rows,), 264, (8,), seed=7)
+    code, dy = binding.encode_act(randn(9, T, 264)), randn(10, T, rows)
+    announce(f"accumulate T={T}")
+    one = lay.backward(code, dy, want=("dw0",)).dw0
+    acc = randn(11, rows, 264, dtype=torch.float32)
+    want = acc + one
+    got = lay.backward(code, dy, want=("dw0", "ds"), dw0=acc, accumulate=True)
+    assert got.dw0 is acc
+    assert ((acc - want).abs() <= 2.0 ** -23 * (one.abs() + want.abs())).all()
+
+
+def test_unaligned_dy_and_neighbouring_memory(gpu_lib):
+    """dy that starts at an odd element; outputs at odd places in larger
+    buffers whose other elements stay as they were."""
+    lay = Layer(O, (136,), 264, (8,), seed=8)
+    T = 50
+    code, dy = binding.encode_act(randn(12, T, 264)), randn(13, T, 136)
+    want = lay.backward(code, dy)
+    flat = torch.empty(T * 136 + 1, dtype=torch.bfloat16, device=DEV)
+    flat[1:] = dy.flatten()
+    announce("unaligned dy")
+    same_bits(lay.backward(code, flat[1:].view(T, 136)), want)
+    # raw call with outputs inside larger buffers
+    sizes = {"dx": (T * 264, 2, 8), "du": (136 * 8, 2, 1), "dv": (264 * 8, 2, 1), "ds": (136, 4, 1), "dw0": (136 * 264, 4, 4)}
+    bufs = {k: torch.full((n + 2 * o,), 7.0, dtype=torch.bfloat16 if b == 2 else torch.float32, device=DEV)
+            for k, (n, b, o) in sizes.items()}
+    g = binding.WlGrads()
+    for k, (n, b, o) in sizes.items():
+        p = bufs[k].data_ptr() + o * b
+        if k in ("du", "dv"):
+            getattr(g, k)[0] = p
+        else:
+            setattr(g, k, p)
+    L = binding.lib()
+    need = L.weightless_backward_workspace_bytes(lay.bundle.handle, T)
+    ws = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device=DEV)
+    import ctypes
+    st = L.weightless_linear_backward(lay.bundle.handle, 0, binding.FAMILY["o"], code.buf.data_ptr(), code.buf.numel(),
+                                      dy.data_ptr(), T, ctypes.byref(g), ws.data_ptr(), need,
+                                      ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0, binding.last_error()
+    assert (ws[need:] == 0x5A).all()
+    for k, (n, b, o) in sizes.items():
+        t = getattr(want, k)
+        t = t[0] if isinstance(t, tuple) else t
+        assert torch.equal(bufs[k][o:o + n], t.flatten()) and (bufs[k][:o] == 7).all() and (bufs[k][o + n:] == 7).all(), k
+
+
+def test_non_finite_values_stay_where_they_belong(gpu_lib):
+    lay = Layer(O, (77,), 264, (8,), seed=9)
+    T = 40
+    x, dy = randn(14, T, 264), randn(15, T, 77)
+    dy[3, 76] = float("nan")
+    x[5, 263] = float("inf")
+    announce("non-finite")
+    g = lay.backward(binding.encode_act(x), dy)
+    nan = torch.isnan(g.dx).any(1)
+    assert nan[3] and nan.sum() == 1                       # dx: that token only (x does not enter dx)
+    rows = torch.isnan(g.dw0)
+    assert rows[76].all() and rows[:, 263].all() and rows[:76, :263].sum() == 0
+    assert torch.isnan(g.dv[0]).all() and torch.isnan(g.du[0]).all()   # g's and z's token enter every sum
+    assert torch.isfinite(lay.backward(binding.encode_act(randn(14, T, 264)), randn(15, T, 77)).dx).all()
+
+
+def test_no_tokens_zero_the_sums(gpu_lib):
+    lay = Layer(GU, (40, 40), 64, (4, 0), seed=10)
+    code = binding.ActCode(0, 64)
+    dy = torch.empty(0, 80, dtype=torch.bfloat16, device=DEV)
+    g = lay.backward(code, dy)
+    assert g.dx.shape == (0, 64) and not g.ds.any() and not g.dw0.any() and not g.du[0].any() and not g.dv[0].any()
+    acc = torch.ones(80, 64, device=DEV)
+    lay.backward(code, dy, want=("dw0",), dw0=acc, accumulate=True)
+    assert (acc == 1).all()
+
+
+def test_side_stream_graph_and_two_at_once(gpu_lib):
+    lay = Layer(QKV, (256, 128, 128), 512, (32, 16, 16), seed=11)
+    T = 150
+    codes = [binding.encode_act(randn(20 + i, T, 512)) for i in range(3)]
+    dys = [randn(30 + i, T, lay.width) for i in range(3)]
+    want = [lay.backward(c, d) for c, d in zip(codes, dys)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    announce("two streams")
+    got = [[], []]
+    for _ in range(4):
+        for i in (0, 1):
+            got[i].append(lay.backward(codes[i], dys[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for g in got[i]:
+            same_bits(g, want[i])
+    code, dy = binding.ActCode(T, 512, buf=codes[0].buf.clone()), dys[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    announce("capture")
+    with torch.cuda.graph(graph):
+        g = lay.backward(code, dy)
+    for i in (1, 2, 0, 1):
+        code.buf.copy_(codes[i].buf)
+        dy.copy_(dys[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        same_bits(g, want[i])
+        same_bits(lay.backward(codes[2 - i], dys[2 - i]), want[2 - i])
+
+
+def test_forward_checkpoint_backward_together(gpu_lib):
+    """A training step's calls as they are used: the forward on x, its
+    checkpoint, the backward; and the forward's own change when s moves by a
+    multiple of ds is what ds says (<y, dy> is linear in s, so up to the
+    roundings of the outputs and of the checkpoint)."""
+    lay = Layer(GU, (256, 256), 384, (16, 16), seed=12)
+    T = 64
+    x = randn(40, T, 384)
+    dy = randn(41, T, lay.width, std=T ** -0.5)
+    announce("forward, checkpoint, backward")
+    y0 = lay.bundle.stacked(0, "gate_up", x).double()
+    code = binding.encode_act(x)
+    g = lay.backward(code, dy)
+    check(lay, code, dy, g)
+    step = 0.25
+    spec = lay.bundle.spec
+    src = []
+    for i, f in enumerate(GU):
+        s = lay.s[i] - step * g.ds[i * 256:(i + 1) * 256]
+        src += [("w0", 0, 0, f, lay.w0[i]), ("s", 0, 0, f, s), ("u", 0, 0, f, lay.u[i]), ("v", 0, 0, f, lay.v[i])]
+    y1 = binding.ThetaBundle(spec, src, device=DEV).stacked(0, "gate_up", x).double()
+    drop = ((y0 - y1) * dy.double()).sum().item()
+    # ds at the checkpoint's values against the drop at x itself: E4M3 rounds x by at most 2^-4 of each
+    # element, the outputs by 2^-8; the errors' inner products with dy are bounded by their norms
+    xe = x.double()
+    full = sum((((xe @ lay.w0[i].double().t().contiguous()) * g.ds[i * 256:(i + 1) * 256].double())
+                * dy.double()[:, i * 256:(i + 1) * 256]).sum().item() for i in (0, 1))
+    assert abs(drop - step * full) <= 2 * H * (y0.norm() * dy.double().norm()).item()
+    mass = sum(((xe.abs() @ lay.w0[i].double().abs().t().contiguous()) * g.ds[i * 256:(i + 1) * 256].double().abs()
+                * dy.double()[:, i * 256:(i + 1) * 256].abs()).sum().item() for i in (0, 1))
+    assert abs(full - (g.ds.double() ** 2).sum().item()) <= 2.0 ** -4 * mass
+
+
+def test_binding_refusals(gpu_lib):
+    lay = Layer(GU, (40, 40), 64, (4, 4), seed=13)
+    code, dy = binding.encode_act(randn(50, 6, 64)), randn(51, 6, 80)
+    E = binding.WlError
+    with pytest.raises(E, match="ActCode"):
+        lay.backward(randn(50, 6, 64), dy)
+    with pytest.raises(E, match="K = 64"):
+        lay.backward(binding.encode_act(randn(50, 6, 72)), dy)
+    with pytest.raises(E, match="dy must be"):
+        lay.backward(code, dy[:5])
+    with pytest.raises(E, match="dy must be"):
+        lay.backward(code, dy.float())
+    with pytest.raises(E, match="dy must be"):
+        lay.backward(code, randn(51, 80, 6).t())
+    with pytest.raises(E, match="unknown"):
+        lay.backward(code, dy, want=("dq",))
+    with pytest.raises(E, match="accumulate"):
+        lay.backward(code, dy, want=("dw0",), accumulate=True)
+    with pytest.raises(E, match="not wanted"):
+        lay.backward(code, dy, want=("dx",), dw0=torch.zeros(80, 64, device=DEV))
+    with pytest.raises(E, match="dw0 must be"):
+        lay.backward(code, dy, want=("dw0",), dw0=torch.zeros(80, 64, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(E, match="WL_ENOSPACE"):
+        lay.backward(code, dy, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(E, match="WL_ERANGE"):
+        lay.bundle.stacked_backward(0, "qkv", code, dy)
+    # outputs that overlap an input or each other, and misaligned ones (host checks, nothing runs)
+    import ctypes
+    L = binding.lib()
+    need = L.weightless_backward_workspace_bytes(lay.bundle.handle, 6)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    dx = torch.empty(6, 64, dtype=torch.bfloat16, device=DEV)
+
+    def call(**kw):
+        g = binding.WlGrads()
+        for k, v in kw.items():
+            if k in ("du", "dv"):
+                getattr(g, k)[0] = v
+            else:
+                setattr(g, k, v)
+        st = L.weightless_stacked_backward(lay.bundle.handle, 0, 1, code.buf.data_ptr(), code.buf.numel(), dy.data_ptr(),
+                                           6, ctypes.byref(g), ws.data_ptr(), need, None)
+        return st, binding.last_error()
+    for kw, frag in (({"dx": dy.data_ptr()}, "overlap"), ({"dx": code.buf.data_ptr()}, "overlap"),
+                     ({"dx": ws.data_ptr()}, "overlap"), ({"ds": lay.bundle.arena.data_ptr()}, "overlap"),
+                     ({"dx": dx.data_ptr(), "ds": dx.data_ptr() + 64}, "overlap"),
+                     ({"du": dx.data_ptr(), "dv": dx.data_ptr()}, "overlap"),
+                     ({"dx": dx.data_ptr() + 2}, "aligned"), ({"ds": dx.data_ptr() + 2}, "aligned"),
+                     ({"dw0": dx.data_ptr() + 4}, "aligned"), ({"du": dx.data_ptr() + 1}, "aligned")):
+        st, err = call(**kw)
+        assert st == -1 and frag in err, (kw, err)

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Iterable, Optional, Sequence, Tuple
+from typing import Dict, Iterable, NamedTuple, Optional, Sequence, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIBPATH = os.path.join(HERE, "libweightless.so")
@@ -37,7 +37,8 @@ EXPORTS = ("theta_bundle_arena_bytes", "theta_bundle_load", "theta_bundle_free",
            "weightless_decompose_als_workspace_bytes", "weightless_decompose_als",
            "weightless_act_code_bytes", "weightless_weight_code_bytes", "weightless_act_encode",
            "weightless_act_expand", "weightless_weight_encode",
-           "weightless_coded_linear_workspace_bytes", "weightless_coded_linear")
+           "weightless_coded_linear_workspace_bytes", "weightless_coded_linear",
+           "weightless_backward_workspace_bytes", "weightless_linear_backward", "weightless_stacked_backward")
 
 
 class WlBundleSpec(ctypes.Structure):
@@ -52,6 +53,21 @@ class WlSrc(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("index", ctypes.c_int32), ("layer_type", ctypes.c_int32),
                 ("family", ctypes.c_int32), ("dtype", ctypes.c_int32), ("on_device", ctypes.c_int32),
                 ("ptr", ctypes.c_void_p)]
+
+
+class WlGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("ds", ctypes.c_void_p), ("du", ctypes.c_void_p * 3),
+                ("dv", ctypes.c_void_p * 3), ("dw0", ctypes.c_void_p), ("accumulate_dw0", ctypes.c_int32)]
+
+
+class Grads(NamedTuple):
+    """Gradients of one call (None: not asked for).  du, dv: tensors, or for a
+    stacked call tuples over its children."""
+    dx: object = None
+    ds: object = None
+    du: object = None
+    dv: object = None
+    dw0: object = None
 
 
 class WlError(RuntimeError):
@@ -102,6 +118,9 @@ def lib():
         "weightless_weight_encode": (i32, [vp, i32, i32, vp, sz, vp]),
         "weightless_coded_linear_workspace_bytes": (sz, [i32, i32, i32]),
         "weightless_coded_linear": (i32, [vp, sz, i32, i32, vp, vp, sz, i32, vp, vp, sz, vp]),
+        "weightless_backward_workspace_bytes": (sz, [vp, i32]),
+        "weightless_linear_backward": (i32, [vp, i32, i32, vp, sz, vp, i32, ctypes.POINTER(WlGrads), vp, sz, vp]),
+        "weightless_stacked_backward": (i32, [vp, i32, i32, vp, sz, vp, i32, ctypes.POINTER(WlGrads), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -272,6 +291,83 @@ class ThetaBundle:
         """h = act(gate) * up of one layer's gate|up stack, bf16 [T, N_gate]."""
         return self._call(lambda hd, l, code, *rest: lib().weightless_gate_up_act(hd, l, ACTS[act], *rest),
                           layer, 0, x, h, ws, stream, self.out_dim(layer, family="gate"))
+
+    def _children(self, layer: int, families):
+        """(N, K, r) of the bundles behind these families of a layer (a tied
+        type's v is k's and no child of its own in a stack)."""
+        t = self.spec.layer_type[layer] if self.spec.layer_type else 0
+        tied = (self.spec.k_eq_v_type_mask >> t) & 1
+        fams = ["k" if f == "v" and tied else f for f in families]
+        fams = [f for i, f in enumerate(fams) if f not in fams[:i]]
+        return [(self.spec.out_dim[t][FAMILY[f]], self.spec.in_dim[t][FAMILY[f]], self.spec.rank[t][FAMILY[f]])
+                for f in fams]
+
+    def _backward(self, fn, layer, code, width, families, stacked, x, dy, want, dw0, accumulate, ws, stream):
+        import torch
+        dev = self.arena.device
+        unknown = set(want) - {"dx", "ds", "du", "dv", "dw0"}
+        if unknown:
+            raise WlError(-1, f"unknown gradients {sorted(unknown)}")
+        kids = self._children(layer, families)
+        rows, K = sum(n for n, _, _ in kids), kids[0][1]
+        if not isinstance(x, ActCode) or x.K != K or x.buf.device != dev:
+            raise WlError(-1, f"x must be an ActCode of K = {K} on {dev}")
+        T = x.T
+        with _scope(dev, stream):
+            _check_tensor(dy, "dy", (T, width), torch.bfloat16, dev)
+            g, bf = WlGrads(), dict(dtype=torch.bfloat16, device=dev)
+            out = {}
+            if "dx" in want:
+                out["dx"] = torch.empty((T, K), **bf)
+                g.dx = out["dx"].data_ptr()
+            if "ds" in want:
+                out["ds"] = torch.empty((rows,), dtype=torch.float32, device=dev)
+                g.ds = out["ds"].data_ptr()
+            for name, arr in (("du", g.du), ("dv", g.dv)):
+                if name in want:
+                    ts = tuple(torch.empty((n if name == "du" else K, r), **bf) for n, _, r in kids)
+                    for i, t in enumerate(ts):
+                        arr[i] = t.data_ptr() or None
+                    out[name] = ts if stacked else ts[0]
+            if "dw0" in want:
+                if dw0 is None:
+                    if accumulate:
+                        raise WlError(-1, "accumulate needs a dw0 to add to")
+                    dw0 = torch.empty((rows, K), dtype=torch.float32, device=dev)
+                _check_tensor(dw0, "dw0", (rows, K), torch.float32, dev)
+                out["dw0"] = dw0
+                g.dw0 = dw0.data_ptr()
+                g.accumulate_dw0 = 1 if accumulate else 0
+            elif dw0 is not None or accumulate:
+                raise WlError(-1, "dw0 is given but not wanted")
+            if ws is None:
+                need = lib().weightless_backward_workspace_bytes(self.handle, T)
+                if need == 0:
+                    raise WlError(-1, last_error())
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            _check(fn(self.handle, layer, code, x.buf.data_ptr(), x.buf.numel(), dy.data_ptr(), T, ctypes.byref(g),
+                      ws.data_ptr(), ws.numel(), _stream_ptr(None)))
+        return Grads(**out)
+
+    def linear_backward(self, layer: int, family: str, x, dy, want=("dx", "ds", "du", "dv"), dw0=None,
+                        accumulate: bool = False, ws=None, stream=None) -> Grads:
+        """Gradients of linear() (weightless_linear_backward).
+
+        x: the ActCode checkpoint of the call's input; dy: bf16 [T, N];
+        want: which of dx, ds, du, dv, dw0.  dw0: float32 [N, K] to write (or,
+        with accumulate, to add to); allocated if not given."""
+        return self._backward(lib().weightless_linear_backward, layer, FAMILY[family],
+                              self.out_dim(layer, family=family), (family,), False, x, dy, want, dw0, accumulate, ws,
+                              stream)
+
+    def stacked_backward(self, layer: int, stack: str, x, dy, want=("dx", "ds", "du", "dv"), dw0=None,
+                         accumulate: bool = False, ws=None, stream=None) -> Grads:
+        """Gradients of stacked() (weightless_stacked_backward): dy with the
+        stacked call's columns; ds and dw0 over the children's rows, du and dv
+        one per child."""
+        return self._backward(lib().weightless_stacked_backward, layer, STACKS[stack],
+                              self.out_dim(layer, stack=stack), ("q", "k", "v") if stack == "qkv" else ("gate", "up"),
+                              True, x, dy, want, dw0, accumulate, ws, stream)
 
     def in_dim(self, layer: int, family: str) -> int:
         """K of one family of one layer (from the spec)."""

@@ -1,0 +1,789 @@
+// Backward pass of the weightless linear from an 8-bit activation checkpoint.
+//
+// Forward: y = s (.) (x W0^T) + (x V) U^T, the rows of a stacked call's
+// children concatenated.  With X the values of the checkpoint (code * 2^e,
+// bf16 exactly) and dy the output's gradient:
+//
+//   z = X V,  g = dy U                      (thin products, bf16)
+//   dx  = (dy (.) s) W0 + g V^T
+//   G   = dy^T X                            (fp32, never stored)
+//   dW0 = diag(s) G        ds_n = sum_k G[n][k] W0[n][k]
+//   dU  = dy^T z           dV = X^T g
+//
+// ds needs y's shared part only through G: sum_t dy[t][n] (x W0^T)[t][n] =
+// sum_k G[n][k] W0[n][k], so one product gives both dW0 and ds and the
+// forward product is not recomputed.
+//
+// Every product is C[b][a] = sum_c A(a, c) B(b, c) with the output's
+// contiguous dimension on the A side (the MFMA's rows: a lane holds four
+// consecutive a of one b).  An operand is stored either with c contiguous
+// ("k-rows": row a holds its c's) or with a contiguous ("k-columns": row c
+// holds all a's, as W0, V^T and U are for dx and g, and dy and X for G).
+// Both come from HBM straight into LDS as they lie; a k-column operand is
+// transposed on its way to the registers by ds_read_b64_tr_b16, so no
+// transposed copy of a weight or of dy is ever written.
+//
+// What is rounded to bf16 on the way: dy (.) s, z and g, each once, as
+// operands of the matrix cores (z as in the forward).  G is exact products of
+// bf16 values summed in fp32, and dW0 and ds stay fp32.
+#include <algorithm>
+
+#include "common.h"
+#include "internal.h"
+#include "lds_dma.h"
+
+namespace wl {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kBK = 64;  // contraction steps
+constexpr int kCUs = 256;
+constexpr int kMaxSeg = 4;
+constexpr int kMaxProb = 9;
+constexpr int kGroupN = 8;  // output tiles along b that run together
+
+// A run of the contraction: A and B hold `len` values of it.
+struct Seg {
+  const uint16_t *A, *B;
+  int64_t lda, ldb;
+  int32_t len;
+};
+
+enum ProbMode : int32_t { kBf16 = 0, kWeight = 1 };
+
+// One product C[N][M] of a launch.
+struct Prob {
+  Seg seg[kMaxSeg];
+  int32_t nseg;
+  int32_t M, N;       // extent along A (contiguous in C) and along B
+  int32_t mode;
+  int32_t nM, nN, ksplit, per;  // tiles, slices of the contraction, steps per slice
+  int32_t unit0;      // first workgroup
+  uint16_t *out;      // kBf16: [N][ldo]
+  int64_t ldo;
+  float *P;           // ksplit > 1: partials [ksplit][N][ldp]
+  int32_t ldp;
+  // kWeight: G's consumers
+  const float *s;     // [N]
+  const uint16_t *W0; // [N][M]
+  float *dw0;         // [N][M] or null
+  int32_t accumulate;
+  float *dsp;         // ksplit == 1: partial sums of ds, [nM * WM][ldds] (null: not wanted)
+  int32_t ldds;
+  float *ds;          // ksplit > 1: [N] (null: not wanted)
+};
+
+struct BwdArgs {
+  int32_t nprob, total;
+  Prob p[kMaxProb];
+};
+
+// Chunk swizzle of a k-column stage row (16-byte chunk c of row k sits in slot
+// c ^ swz(k)).  A transposing read takes 32-byte pieces of rows k = 8 g + 0..3
+// (lane group g); two lane groups at once then touch 8 rows, which the swizzle
+// puts in 8 different 32-byte places of the 256-byte bank period: rows of
+// >= 256 bytes all start at bank 0, 128-byte rows alternate between the halves.
+template <int W>
+__device__ __forceinline__ int swz(int k) {
+  return W >= 128 ? 2 * ((k & 3) | ((k >> 1) & 4)) : 2 * (((k >> 1) & 1) | ((k >> 2) & 2));
+}
+
+// One operand of a staged product: W rows of the tile, 64 of the contraction
+// per stage, W * 128 bytes of LDS.  TR: k-columns.
+template <int W, bool TR>
+struct Operand {
+  static constexpr int CPR = TR ? W / 8 : 8;  // 16-byte chunks of an LDS row
+
+  // This lane's part of load instruction q (1 KB of the stage): byte offset
+  // from the stage's base, or kBufNoRow where the tile has no such row or
+  // column; kpos is the lane's first contraction index in the stage.
+  static __device__ __forceinline__ uint32_t source(int q, int lane, int64_t ld, int lim, int &kpos) {
+    const int id = q * 64 + lane, row = id / CPR, slot = id % CPR;
+    if constexpr (TR) {
+      const int c = slot ^ swz<W>(row);
+      kpos = row;
+      return c * 8 < lim ? static_cast<uint32_t>(row * ld * 2 + c * 16) : kBufNoRow;
+    } else {
+      const int c = slot ^ (row & 7);
+      kpos = c * 8;
+      return row < lim ? static_cast<uint32_t>(row * ld * 2 + c * 16) : kBufNoRow;
+    }
+  }
+  static __device__ __forceinline__ const uint16_t *base(const uint16_t *p, int64_t ld, int m0, int step) {
+    return TR ? p + static_cast<int64_t>(step) * kBK * ld + m0 : p + m0 * ld + step * kBK;
+  }
+  static __device__ __forceinline__ int64_t advance(int64_t ld) { return TR ? kBK * ld : kBK; }
+
+  // Fragment of 16 rows from row m of the tile, contraction 32 h + 8 g .. + 7.
+  static __device__ __forceinline__ u32x4 frag(uint8_t *sb, int m, int h, int r16, int g) {
+    if constexpr (TR) {
+      const int k = 32 * h + 8 * g + (r16 >> 2);
+      const int c = (m / 8 + ((r16 >> 1) & 1)) ^ swz<W>(k);
+      uint8_t *p = sb + k * (2 * W) + c * 16 + (r16 & 1) * 8;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * 2 * W));
+      const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+      return u32x4{a[0], a[1], b[0], b[1]};
+    } else {
+      return *reinterpret_cast<const u32x4 *>(sb + (m + r16) * kRowBytes + ((4 * h + g) ^ (r16 & 7)) * 16);
+    }
+  }
+};
+
+template <int BM_, int BN_, int WM_, int WN_, int NST_>
+struct BTile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
+  static constexpr int NW = WM * WN;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  static constexpr int GA = BM / 8, GB = BN / 8, LPW = (GA + GB) / NW;
+  static constexpr int STAGE = (BM + BN) * kRowBytes;
+  static constexpr int PITCH = 2 * BM + 16;      // staged bf16 output: bytes per b
+  static constexpr int WPITCH = 4 * TM + 16;     // a wave's staged fp32 rows of G
+  static constexpr size_t RING = static_cast<size_t>(NST) * STAGE, OUT = static_cast<size_t>(BN) * PITCH;
+  static constexpr size_t WOUT = static_cast<size_t>(NW) * 16 * WPITCH;
+  static constexpr size_t MX = RING > OUT ? RING : OUT;
+  static constexpr size_t LDS = MX > WOUT ? MX : WOUT;
+  static_assert((GA + GB) % NW == 0 && TM % 16 == 0 && TN % 16 == 0 && LDS <= 160 * 1024, "tile shape");
+};
+
+// Rows of G (a wave's TM x TN part) leave through LDS, 16 n at a time, so that
+// W0 is read and dW0 is read and written in whole runs of TM elements of one
+// row; the ds sums run along those rows.
+template <typename TL>
+__device__ __forceinline__ void store_weight_grad(const f32x4 (&acc)[TL::FM][TL::FN], const Prob &p, int f, int m0,
+                                                  int n0, uint8_t *lds) {
+  constexpr int LPR = TL::TM / 4;     // lanes per row
+  constexpr int RPI = 64 / LPR;       // rows per instruction
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WN, wn = wave % TL::WN, r16 = lane & 15, g = lane >> 4;
+  uint8_t *mine = lds + wave * 16 * TL::WPITCH;
+  const int kl = (lane % LPR) * 4, k = m0 + wm * TL::TM + kl;
+  const bool kin = k < p.M;           // M % 8 == 0: whole groups of 4
+#pragma unroll
+  for (int j = 0; j < TL::FN; ++j) {
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+      *reinterpret_cast<f32x4 *>(mine + r16 * TL::WPITCH + (i * 16 + g * 4) * 4) = acc[i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int r = it * RPI + lane / LPR;
+      const int n = n0 + wn * TL::TN + j * 16 + r;
+      const bool in = n < p.N && kin;
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + r * TL::WPITCH + kl * 4);
+      if (p.dw0 && in) {
+        f32x4 *d = reinterpret_cast<f32x4 *>(p.dw0 + static_cast<int64_t>(n) * p.M + k);
+        const float sc = p.s[n];
+        f32x4 o = v * sc;
+        if (p.accumulate) o += *d;
+        *d = o;
+      }
+      if (p.dsp) {
+        float t = 0.f;
+        if (in) {
+          const u32x2 w = *reinterpret_cast<const u32x2 *>(p.W0 + static_cast<int64_t>(n) * p.M + k);
+          t = v[0] * __uint_as_float(w[0] << 16) + v[1] * __uint_as_float(w[0] & 0xffff0000u) +
+              v[2] * __uint_as_float(w[1] << 16) + v[3] * __uint_as_float(w[1] & 0xffff0000u);
+        }
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) t += __shfl_xor(t, d, 64);
+        if (lane % LPR == 0 && n < p.N) p.dsp[static_cast<int64_t>(f * TL::WM + wm) * p.ldds + n] = t;
+      }
+    }
+  }
+}
+
+template <typename TL, bool ATR, bool BTR>
+__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 2))) void product_kernel(BwdArgs args) {
+  using OA = Operand<TL::BM, ATR>;
+  using OB = Operand<TL::BN, BTR>;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / TL::WN, wn = wave % TL::WN;
+  const int r16 = lane & 15, g = lane >> 4;
+  // workgroup -> unit, XCD-major; unit -> product, slice, tile.  kGroupN tiles
+  // along b share their A panels, then the next panel, then the next group.
+  const int u = xcd_unit(blockIdx.x, args.total);
+  int pi = 0;
+  while (pi + 1 < args.nprob && u >= args.p[pi + 1].unit0) ++pi;
+  const Prob &p = args.p[pi];
+  const int v = u - p.unit0;
+  const int sl = v / (p.nM * p.nN), w = v % (p.nM * p.nN);
+  const int grp = w / (p.nM * kGroupN), gn = min(kGroupN, p.nN - grp * kGroupN);
+  const int wg = w - grp * p.nM * kGroupN;
+  const int f = wg / gn, t = grp * kGroupN + wg % gn;
+  const int m0 = f * TL::BM, n0 = t * TL::BN;
+  int s_lo = sl * p.per, s_hi = s_lo + p.per;  // steps of this slice, counted through the segments
+
+  f32x4 acc[TL::FM][TL::FN];
+#pragma unroll
+  for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int si = 0; si < p.nseg; ++si) {
+    const Seg &sg = p.seg[si];
+    const int steps = (sg.len + kBK - 1) / kBK;
+    const int b0 = max(0, s_lo), nk = min(steps, s_hi) - b0;
+    s_lo -= steps;
+    s_hi -= steps;
+    if (nk <= 0) continue;
+    uint32_t off[TL::LPW];
+    int kpos[TL::LPW];
+#pragma unroll
+    for (int q = 0; q < TL::LPW; ++q) {
+      const int gq = wave * TL::LPW + q;
+      off[q] = gq < TL::GA ? OA::source(gq, lane, sg.lda, p.M - m0, kpos[q])
+                           : OB::source(gq - TL::GA, lane, sg.ldb, p.N - n0, kpos[q]);
+    }
+    const uint16_t *pa = OA::base(sg.A, sg.lda, m0, b0), *pb = OB::base(sg.B, sg.ldb, n0, b0);
+    const int64_t adv_a = OA::advance(sg.lda), adv_b = OB::advance(sg.ldb);
+    const int full = sg.len / kBK;
+    int step = b0;
+    auto issue = [&](int stage) {
+      const auto ra = tile_rsrc(pa), rb = tile_rsrc(pb);
+      const int left = step < full ? kBK : sg.len - step * kBK;  // contraction values of this step
+      uint8_t *st = lds + stage * TL::STAGE;
+#pragma unroll
+      for (int q = 0; q < TL::LPW; ++q) {
+        const int gq = wave * TL::LPW + q;
+        load_lds<16>(gq < TL::GA ? ra : rb, kpos[q] < left ? off[q] : kBufNoRow, st + gq * 1024);
+      }
+      pa += adv_a;
+      pb += adv_b;
+      ++step;
+    };
+#pragma unroll
+    for (int st = 0; st < TL::NST - 1; ++st)
+      if (st < nk) issue(st);
+    for (int kt = 0; kt < nk; ++kt) {
+      if (kt + TL::NST - 2 < nk)
+        wait_and_sync<(TL::NST - 2) * TL::LPW>();
+      else
+        wait_and_sync<0>();
+      if (kt + TL::NST - 1 < nk) issue((kt + TL::NST - 1) % TL::NST);
+      uint8_t *sa = lds + (kt % TL::NST) * TL::STAGE, *sb = sa + TL::BM * kRowBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 fa[TL::FM], fb[TL::FN];
+#pragma unroll
+        for (int j = 0; j < TL::FN; ++j) fb[j] = OB::frag(sb, wn * TL::TN + j * 16, h, r16, g);
+#pragma unroll
+        for (int i = 0; i < TL::FM; ++i) fa[i] = OA::frag(sa, wm * TL::TM + i * 16, h, r16, g);
+#pragma unroll
+        for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma16x16x32(fa[i], fb[j], acc[i][j]);
+      }
+    }
+    wait_and_sync<0>();  // the ring is idle
+  }
+
+  if (p.ksplit > 1) {
+    float *P = p.P + static_cast<int64_t>(sl) * p.N * p.ldp;
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) {
+      const int n = n0 + wn * TL::TN + j * 16 + r16;
+      if (n >= p.N) continue;
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i) {
+        const int m = m0 + wm * TL::TM + i * 16 + g * 4;
+        if (m < p.ldp) *reinterpret_cast<f32x4 *>(P + static_cast<int64_t>(n) * p.ldp + m) = acc[i][j];
+      }
+    }
+    return;
+  }
+  if (p.mode == kWeight) {
+    if constexpr (ATR && BTR) store_weight_grad<TL>(acc, p, f, m0, n0, lds);
+    return;
+  }
+  // bf16 tile in LDS, b-major, then whole 16-byte chunks of output rows
+#pragma unroll
+  for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const int tl = wn * TL::TN + j * 16 + r16, fl = wm * TL::TM + i * 16 + g * 4;
+      *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) =
+          make_uint2(f32_to_bf16(acc[i][j][0]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][1])) << 16),
+                     f32_to_bf16(acc[i][j][2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][3])) << 16));
+    }
+  __syncthreads();
+  constexpr int CPR = TL::BM / 8;
+  for (int c = threadIdx.x; c < TL::BN * CPR; c += TL::NW * 64) {
+    const int tl = c / CPR, fl = (c % CPR) * 8;
+    const int n = n0 + tl, m = m0 + fl;
+    if (n >= p.N || m >= p.M) continue;
+    const uint4 val = *reinterpret_cast<const uint4 *>(lds + tl * TL::PITCH + fl * 2);
+    uint16_t *o = p.out + static_cast<int64_t>(n) * p.ldo + m;
+    if (m + 8 <= p.M && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+      *reinterpret_cast<uint4 *>(o) = val;
+    } else {
+      const uint32_t e[4] = {val.x, val.y, val.z, val.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (m + i < p.M) o[i] = static_cast<uint16_t>(e[i / 2] >> (16 * (i & 1)));
+    }
+  }
+}
+
+// Split products: the slices' partials, summed in slice order.  kBf16: rows of
+// C rounded to bf16; kWeight: a workgroup per row n of G forms dW0's row and
+// ds[n].
+struct SumArgs {
+  int32_t nprob;
+  int32_t first[kMaxProb];  // first workgroup of each
+  Prob p[kMaxProb];
+};
+
+__global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
+  int pi = 0;
+  while (pi + 1 < a.nprob && static_cast<int>(blockIdx.x) >= a.first[pi + 1]) ++pi;
+  const Prob &p = a.p[pi];
+  const int64_t b = blockIdx.x - a.first[pi];
+  const int q = p.ldp / 4;
+  if (p.mode == kBf16) {
+    const int64_t id = b * 256 + threadIdx.x;
+    if (id >= static_cast<int64_t>(p.N) * q) return;
+    const int64_t n = id / q;
+    const int m = static_cast<int>(id % q) * 4;
+    f32x4 s{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < p.ksplit; ++i)
+      s += *reinterpret_cast<const f32x4 *>(p.P + (static_cast<int64_t>(i) * p.N + n) * p.ldp + m);
+    uint16_t *o = p.out + n * p.ldo + m;
+    if (m + 4 <= p.M && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+      *reinterpret_cast<uint2 *>(o) = make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
+                                                 f32_to_bf16(s[2]) | (static_cast<uint32_t>(f32_to_bf16(s[3])) << 16));
+    } else {
+      for (int e = 0; e < 4 && m + e < p.M; ++e) o[e] = f32_to_bf16(s[e]);
+    }
+    return;
+  }
+  const int64_t n = b;
+  const float sc = p.s[n];
+  float t = 0.f;
+  for (int c = threadIdx.x; c < q; c += 256) {
+    f32x4 s{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < p.ksplit; ++i)
+      s += *reinterpret_cast<const f32x4 *>(p.P + (static_cast<int64_t>(i) * p.N + n) * p.ldp + c * 4);
+    if (p.dw0) {
+      f32x4 *d = reinterpret_cast<f32x4 *>(p.dw0 + n * p.M + c * 4);
+      f32x4 o = s * sc;
+      if (p.accumulate) o += *d;
+      *d = o;
+    }
+    const u32x2 w = *reinterpret_cast<const u32x2 *>(p.W0 + n * p.M + c * 4);
+    t += s[0] * __uint_as_float(w[0] << 16) + s[1] * __uint_as_float(w[0] & 0xffff0000u) +
+         s[2] * __uint_as_float(w[1] << 16) + s[3] * __uint_as_float(w[1] & 0xffff0000u);
+  }
+  if (!p.ds) return;
+  __shared__ float part[4];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) t += __shfl_xor(t, d, 64);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = t;
+  __syncthreads();
+  if (threadIdx.x == 0) p.ds[n] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// ds[n] = sum of the column tiles' partial sums, in order.
+__global__ __launch_bounds__(256) void sum_ds_kernel(const float *dsp, int parts, int ldds, int N, float *ds) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float t = 0.f;
+  for (int i = 0; i < parts; ++i) t += dsp[static_cast<int64_t>(i) * ldds + n];
+  ds[n] = t;
+}
+
+// dy [T][ldy] -> rows of ldd columns in which every child's slot starts at a
+// multiple of 8 (zeros behind a slot's last column): the plain copy `dyp`
+// and/or dy (.) s rounded to bf16, `dys`.
+struct PrepArgs {
+  const uint16_t *dy;
+  int32_t T, ldy, ldd, nslot;
+  int32_t start[kMaxChildren + 1];  // slot -> first column in the padded rows (start[nslot] = ldd)
+  int32_t from[kMaxChildren];       // slot -> first column in dy
+  int32_t n[kMaxChildren];          // slot -> columns
+  const float *s[kMaxChildren];
+  uint16_t *dyp, *dys;
+};
+
+__global__ __launch_bounds__(256) void prep_dy_kernel(PrepArgs a) {
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= a.ldd) return;
+  const int64_t t = blockIdx.x;
+  int i = 0;
+  while (i + 1 < a.nslot && c >= a.start[i + 1]) ++i;
+  const int j = c - a.start[i];
+  const uint16_t *src = a.dy + t * a.ldy + a.from[i] + j;
+  alignas(16) uint16_t e[8];
+  if (j + 8 <= a.n[i] && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+    *reinterpret_cast<u32x4 *>(e) = ld16(src);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = j + k < a.n[i] ? src[k] : 0;
+  }
+  if (a.dyp) *reinterpret_cast<u32x4 *>(a.dyp + t * a.ldd + c) = *reinterpret_cast<const u32x4 *>(e);
+  if (a.dys) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = j + k < a.n[i] ? f32_to_bf16(bf16_to_f32(e[k]) * a.s[i][j + k]) : 0;
+    *reinterpret_cast<u32x4 *>(a.dys + t * a.ldd + c) = *reinterpret_cast<const u32x4 *>(e);
+  }
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t n) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+    p[i] = 0;
+}
+
+hipError_t launch_zero(void *p, int64_t halves, hipStream_t stream) {
+  if (!p || halves <= 0) return hipSuccess;
+  const int64_t blocks = std::min<int64_t>((halves + 255) / 256, 4096);
+  hipLaunchKernelGGL(zero_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, static_cast<uint16_t *>(p),
+                     halves);
+  return hipGetLastError();
+}
+
+// ---- host side --------------------------------------------------------------
+
+using Big = BTile<256, 256, 2, 4, 2>;
+using Mid = BTile<128, 128, 2, 4, 4>;
+using Thin = BTile<64, 128, 2, 4, 4>;
+constexpr int kShapes = 3;
+constexpr struct {
+  int BM, BN, WM;
+  double step;  // us of one contraction step of a workgroup
+} kShape[kShapes] = {{Big::BM, Big::BN, Big::WM, 1.9}, {Mid::BM, Mid::BN, Mid::WM, 0.75}, {Thin::BM, Thin::BN, Thin::WM, 0.6}};
+
+struct BPlan {
+  int shape, ksplit, per, nM, nN;
+  size_t partial_bytes(int M, int N) const {
+    return ksplit > 1 ? (static_cast<size_t>(ksplit) * N * ((M + 3) & ~3) * 4 + 255) & ~size_t{255} : 0;
+  }
+};
+
+// Tile shape and split of one product: the smallest estimated time, rounds of
+// workgroups over the CUs times the steps of one, plus writing, reading and
+// launching the sum of the partials when the contraction is split.
+BPlan plan_product(int M, int N, int steps) {
+  BPlan best{};
+  double best_us = 1e300;
+  for (int i = 0; i < kShapes; ++i) {
+    const int nM = (M + kShape[i].BM - 1) / kShape[i].BM, nN = (N + kShape[i].BN - 1) / kShape[i].BN;
+    const int64_t tiles = static_cast<int64_t>(nM) * nN;
+    for (int ks = 1; ks <= 32 && (ks == 1 || ks * 2 <= steps); ++ks) {
+      const int per = (steps + ks - 1) / ks;
+      if ((ks - 1) * per >= steps) continue;  // an empty slice
+      const double rounds = static_cast<double>((tiles * ks + kCUs - 1) / kCUs);
+      double us = rounds * (per + 3) * kShape[i].step;
+      if (ks > 1) us += 4.0 + 2.0 * ks * static_cast<double>(N) * M * 4 / 3e6;
+      if (us < best_us) {
+        best_us = us;
+        best = BPlan{i, ks, per, nM, nN};
+      }
+    }
+  }
+  return best;
+}
+
+int steps_of(int64_t len) { return static_cast<int>((len + kBK - 1) / kBK); }
+int pad8(int n) { return (n + 7) & ~7; }
+size_t pad256(size_t n) { return (n + 255) & ~size_t{255}; }
+
+// Column slots of dy: every child's, then the tied v slot (k's rows again).
+struct Slots {
+  int n = 0, ldy = 0, ldd = 0;
+  int child[kMaxChildren] = {}, from[kMaxChildren] = {}, start[kMaxChildren + 1] = {}, cols[kMaxChildren] = {};
+  bool even = true;  // every slot already starts at a multiple of 8 of dy's rows
+};
+
+Slots slots_of(const CallDesc &c) {
+  Slots s;
+  auto add = [&](int child, int from, int cols) {
+    s.child[s.n] = child;
+    s.from[s.n] = from;
+    s.cols[s.n] = cols;
+    s.start[s.n] = s.ldd;
+    s.ldd += pad8(cols);
+    s.ldy = std::max(s.ldy, from + cols);
+    if (from % 8 || cols % 8) s.even = false;
+    ++s.n;
+  };
+  for (int i = 0; i < c.nchild; ++i) add(i, c.ch[i].y_off, c.ch[i].N);
+  for (int i = 0; i < c.nchild; ++i)
+    if (c.ch[i].dup_off >= 0) add(i, c.ch[i].dup_off, c.ch[i].N);
+  s.start[s.n] = s.ldd;
+  return s;
+}
+
+int slots_of_child(const Slots &s, int child) {
+  int n = 0;
+  for (int i = 0; i < s.n; ++i) n += s.child[i] == child;
+  return n;
+}
+
+int dx_steps(const Slots &s, int Rz) {
+  int n = steps_of(Rz);
+  for (int i = 0; i < s.n; ++i) n += steps_of(s.cols[i]);
+  return n;
+}
+
+// Workspace: X bf16 [T][K], dy copies [T][ldd] x 2, z and g [T][Rz], the ds
+// partial sums, and the K-split partials of every product.
+struct Offsets {
+  size_t x, dyp, dys, z, g, dsp, part, bytes;
+};
+
+Offsets offsets_of(const CallDesc &c, const Slots &s, int T) {
+  Offsets o{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += pad256(n);
+    return here;
+  };
+  o.x = take(static_cast<size_t>(T) * c.K * 2);
+  o.dyp = take(static_cast<size_t>(T) * s.ldd * 2);
+  o.dys = take(static_cast<size_t>(T) * s.ldd * 2);
+  o.z = take(static_cast<size_t>(T) * c.Rz * 2);
+  o.g = take(static_cast<size_t>(T) * c.Rz * 2);
+  o.dsp = take(static_cast<size_t>((c.K + 63) / 64) * 2 * c.Ntot * 4);
+  // the products of one launch have partials of their own; launches reuse them
+  size_t zg = 0, tt = 0;
+  if (c.Rz > 0) zg = plan_product(c.Rz, T, steps_of(c.K)).partial_bytes(c.Rz, T);
+  for (int i = 0; i < c.nchild; ++i) {
+    const ChildDesc &ch = c.ch[i];
+    const int ns = slots_of_child(s, i);
+    if (ch.rpad) {
+      zg += plan_product(ch.rpad, T, ns * steps_of(ch.N)).partial_bytes(ch.rpad, T);
+      tt += plan_product(ch.rpad, ch.N, ns * steps_of(T)).partial_bytes(ch.rpad, ch.N);
+      tt += plan_product(ch.rpad, c.K, steps_of(T)).partial_bytes(ch.rpad, c.K);
+    }
+    tt += plan_product(c.K, ch.N, ns * steps_of(T)).partial_bytes(c.K, ch.N);
+  }
+  const size_t dx = plan_product(c.K, T, dx_steps(s, c.Rz)).partial_bytes(c.K, T);
+  o.part = take(std::max({zg, tt, dx}));
+  o.bytes = at;
+  return o;
+}
+
+// Products of one kind that run together; one launch per tile shape they use.
+struct Batch {
+  int n = 0;
+  Prob p[kMaxProb];
+  int shape[kMaxProb];
+};
+
+template <typename TL, bool ATR, bool BTR>
+hipError_t launch_shape(const BwdArgs &a, hipStream_t stream) {
+  const hipError_t e = ensure_lds<product_kernel<TL, ATR, BTR>>(TL::LDS);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((product_kernel<TL, ATR, BTR>), dim3(a.total), dim3(TL::NW * 64), TL::LDS, stream, a);
+  return hipGetLastError();
+}
+
+template <bool ATR, bool BTR>
+hipError_t launch_batch(const Batch &b, hipStream_t stream) {
+  for (int sh = 0; sh < kShapes; ++sh) {
+    BwdArgs a{};
+    for (int i = 0; i < b.n; ++i) {
+      if (b.shape[i] != sh) continue;
+      Prob &p = a.p[a.nprob++];
+      p = b.p[i];
+      p.unit0 = a.total;
+      a.total += p.nM * p.nN * p.ksplit;
+    }
+    if (!a.nprob) continue;
+    const hipError_t e = sh == 0   ? launch_shape<Big, ATR, BTR>(a, stream)
+                         : sh == 1 ? launch_shape<Mid, ATR, BTR>(a, stream)
+                                   : launch_shape<Thin, ATR, BTR>(a, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// The sums of a batch's split products.
+hipError_t launch_sums(const Batch &b, hipStream_t stream) {
+  SumArgs a{};
+  int blocks = 0;
+  for (int i = 0; i < b.n; ++i) {
+    if (b.p[i].ksplit == 1) continue;
+    a.first[a.nprob] = blocks;
+    a.p[a.nprob] = b.p[i];
+    blocks += b.p[i].mode == kWeight
+                  ? b.p[i].N
+                  : static_cast<int>((static_cast<int64_t>(b.p[i].N) * (b.p[i].ldp / 4) + 255) / 256);
+    ++a.nprob;
+  }
+  if (!a.nprob) return hipSuccess;
+  hipLaunchKernelGGL(sum_kernel, dim3(blocks), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+// Add a product to a batch; returns it for its segments and epilogue.  Its
+// partials are taken from `part`.  Mp >= M (M or the padded rank) is the
+// extent the workspace was sized for: the plan goes by it.
+Prob &add_product(Batch &b, int M, int Mp, int N, int steps, uint16_t *out, int64_t ldo, uint8_t *&part) {
+  const BPlan pl = plan_product(Mp, N, steps);
+  Prob &p = b.p[b.n];
+  p = Prob{};
+  b.shape[b.n++] = pl.shape;
+  p.M = M;
+  p.N = N;
+  p.nM = pl.nM;
+  p.nN = pl.nN;
+  p.ksplit = pl.ksplit;
+  p.per = pl.per;
+  p.out = out;
+  p.ldo = ldo;
+  p.ldp = (Mp + 3) & ~3;
+  p.P = reinterpret_cast<float *>(part);
+  part += pl.partial_bytes(Mp, N);
+  return p;
+}
+
+void add_seg(Prob &p, const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int len) {
+  p.seg[p.nseg++] = Seg{A, B, lda, ldb, len};
+}
+
+}  // namespace
+
+size_t backward_workspace_bytes(const CallDesc &c, int T) { return offsets_of(c, slots_of(c), T).bytes; }
+
+int backward_dy_columns(const CallDesc &c) { return slots_of(c).ldy; }
+
+hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_t *dy, const GradOut &o, void *ws_,
+                           hipStream_t stream) {
+  const int T = c.T, K = c.K;
+  const Slots s = slots_of(c);
+  uint8_t *ws = static_cast<uint8_t *>(ws_);
+  const Offsets at = offsets_of(c, s, T);
+  hipError_t e;
+  bool want_u = false, want_v = false;
+  for (int i = 0; i < c.nchild; ++i) {
+    want_u |= o.du[i] && o.r[i];
+    want_v |= o.dv[i] && o.r[i];
+  }
+  const bool want_w = o.ds || o.dw0, want_g = c.Rz > 0 && (o.dx || want_v);
+  if (T == 0) {  // sums over no tokens
+    if (o.ds && (e = launch_zero(o.ds, 2 * static_cast<int64_t>(c.Ntot), stream)) != hipSuccess) return e;
+    if (o.dw0 && !o.accumulate && (e = launch_zero(o.dw0, 2 * static_cast<int64_t>(c.Ntot) * K, stream)) != hipSuccess)
+      return e;
+    for (int i = 0; i < c.nchild; ++i) {
+      if ((e = launch_zero(o.du[i], static_cast<int64_t>(c.ch[i].N) * o.r[i], stream)) != hipSuccess) return e;
+      if ((e = launch_zero(o.dv[i], static_cast<int64_t>(K) * o.r[i], stream)) != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+
+  uint16_t *X = reinterpret_cast<uint16_t *>(ws + at.x);
+  uint16_t *z = reinterpret_cast<uint16_t *>(ws + at.z), *g = reinterpret_cast<uint16_t *>(ws + at.g);
+  uint16_t *dys = reinterpret_cast<uint16_t *>(ws + at.dys);
+  // dy as the products read it: itself where its slots lie on multiples of 8
+  // columns and 16 bytes, else a copy where they do
+  const bool direct = s.even && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
+  const uint16_t *dyp = direct ? dy : reinterpret_cast<const uint16_t *>(ws + at.dyp);
+  const int64_t ldp = direct ? s.ldy : s.ldd;
+  if (want_u || want_v || want_w) {
+    e = launch_expand_act(xc, T, X, K, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (o.dx || !direct) {
+    PrepArgs a{};
+    a.dy = dy;
+    a.T = T;
+    a.ldy = s.ldy;
+    a.ldd = s.ldd;
+    a.nslot = s.n;
+    for (int i = 0; i < s.n; ++i) {
+      a.start[i] = s.start[i];
+      a.from[i] = s.from[i];
+      a.n[i] = s.cols[i];
+      a.s[i] = c.s + c.ch[s.child[i]].row_start;
+    }
+    a.start[s.n] = s.ldd;
+    a.dyp = direct ? nullptr : reinterpret_cast<uint16_t *>(ws + at.dyp);
+    a.dys = o.dx ? dys : nullptr;
+    hipLaunchKernelGGL(prep_dy_kernel, dim3(T, (s.ldd / 8 + 255) / 256), dim3(256), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  // z = X V and g = dy U
+  uint8_t *part = ws + at.part;
+  Batch zb{}, gb{};
+  if (want_u) {
+    Prob &p = add_product(zb, c.Rz, c.Rz, T, steps_of(K), z, c.Rz, part);
+    add_seg(p, c.Vt, K, X, K, K);
+  }
+  if (want_g)
+    for (int i = 0; i < c.nchild; ++i) {
+      const ChildDesc &ch = c.ch[i];
+      if (!ch.rpad) continue;
+      Prob &p = add_product(gb, ch.rpad, ch.rpad, T, slots_of_child(s, i) * steps_of(ch.N), g + ch.zoff, c.Rz, part);
+      for (int j = 0; j < s.n; ++j)
+        if (s.child[j] == i) add_seg(p, ch.U, ch.rpad, dyp + (direct ? s.from[j] : s.start[j]), ldp, ch.N);
+    }
+  if ((e = launch_batch<false, false>(zb, stream)) != hipSuccess) return e;
+  if ((e = launch_batch<true, false>(gb, stream)) != hipSuccess) return e;
+  for (int i = 0; i < gb.n; ++i) zb.p[zb.n++] = gb.p[i];
+  if ((e = launch_sums(zb, stream)) != hipSuccess) return e;
+  // dx = (dy (.) s) W0 + g V^T
+  if (o.dx) {
+    part = ws + at.part;
+    Batch b{};
+    Prob &p = add_product(b, K, K, T, dx_steps(s, c.Rz), o.dx, K, part);
+    for (int j = 0; j < s.n; ++j)
+      add_seg(p, c.W0 + static_cast<int64_t>(c.ch[s.child[j]].row_start) * K, K, dys + s.start[j], s.ldd, s.cols[j]);
+    if (c.Rz > 0) add_seg(p, c.Vt, K, g, c.Rz, c.Rz);
+    if ((e = launch_batch<true, false>(b, stream)) != hipSuccess) return e;
+    if ((e = launch_sums(b, stream)) != hipSuccess) return e;
+  }
+  // G (dW0 and ds), dU and dV: contractions over the tokens
+  if (want_w || want_u || want_v) {
+    part = ws + at.part;
+    float *dsp = reinterpret_cast<float *>(ws + at.dsp);
+    Batch b{};
+    for (int i = 0; i < c.nchild; ++i) {
+      const ChildDesc &ch = c.ch[i];
+      const int ns = slots_of_child(s, i);
+      auto add_tokens = [&](Prob &p, const uint16_t *A, int64_t lda) {
+        for (int j = 0; j < s.n; ++j)
+          if (s.child[j] == i) add_seg(p, A, lda, dyp + (direct ? s.from[j] : s.start[j]), ldp, T);
+      };
+      if (want_w) {
+        Prob &p = add_product(b, K, K, ch.N, ns * steps_of(T), nullptr, 0, part);
+        add_tokens(p, X, K);
+        p.mode = kWeight;
+        p.s = c.s + ch.row_start;
+        p.W0 = c.W0 + static_cast<int64_t>(ch.row_start) * K;
+        p.dw0 = o.dw0 ? o.dw0 + static_cast<int64_t>(ch.row_start) * K : nullptr;
+        p.accumulate = o.accumulate;
+        p.ds = o.ds ? o.ds + ch.row_start : nullptr;
+        p.dsp = o.ds ? dsp + ch.row_start : nullptr;
+        p.ldds = c.Ntot;
+      }
+      if (o.du[i] && o.r[i]) {
+        Prob &p = add_product(b, o.r[i], ch.rpad, ch.N, ns * steps_of(T), o.du[i], o.r[i], part);
+        add_tokens(p, z + ch.zoff, c.Rz);
+      }
+      if (o.dv[i] && o.r[i]) {
+        Prob &p = add_product(b, o.r[i], ch.rpad, K, steps_of(T), o.dv[i], o.r[i], part);
+        add_seg(p, g + ch.zoff, c.Rz, X, K, T);
+      }
+    }
+    if ((e = launch_batch<true, true>(b, stream)) != hipSuccess) return e;
+    if ((e = launch_sums(b, stream)) != hipSuccess) return e;
+    if (o.ds)
+      for (int i = 0; i < b.n; ++i) {
+        const Prob &p = b.p[i];
+        if (p.mode != kWeight || p.ksplit > 1) continue;
+        hipLaunchKernelGGL(sum_ds_kernel, dim3((p.N + 255) / 256), dim3(256), 0, stream,
+                           static_cast<const float *>(p.dsp), p.nM * kShape[b.shape[i]].WM, p.ldds, p.N, p.ds);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+      }
+  }
+  return hipSuccess;
+}
+
+}  // namespace wl

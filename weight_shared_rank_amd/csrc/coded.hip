@@ -411,8 +411,10 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
     if (row + 8 <= a.N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
       *reinterpret_cast<uint4 *>(p) = v;
     } else {
-      const uint16_t *o = reinterpret_cast<const uint16_t *>(&v);
-      for (int e = 0; e < 8 && row + e < a.N; ++e) p[e] = o[e];
+      const uint32_t o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (row + e < a.N) p[e] = static_cast<uint16_t>(o[e / 2] >> (16 * (e & 1)));
     }
   }
 }

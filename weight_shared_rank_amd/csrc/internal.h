@@ -108,6 +108,23 @@ size_t coded_partial_bytes(int N, int T, int K);
 hipError_t launch_coded_linear(const CodedView &w, int N, const CodedView &x, int T, uint16_t *y, float *partials,
                                hipStream_t stream);
 
+// Backward pass of one call (backward.hip has the formulas).  c describes the
+// call (x and y unused, W0 bf16), T its tokens; dy [T][columns] with the
+// columns of the call's y, the tied v slot included.  Every output may be null.
+struct GradOut {
+  uint16_t *dx;                 // [T][K]
+  float *ds;                    // [Ntot]
+  uint16_t *du[kMaxChildren];   // [N][r] per child
+  uint16_t *dv[kMaxChildren];   // [K][r] per child
+  int32_t r[kMaxChildren];      // ranks (unpadded)
+  float *dw0;                   // [Ntot][K]
+  int32_t accumulate;           // dw0 is added to
+};
+size_t backward_workspace_bytes(const CallDesc &c, int T);
+int backward_dy_columns(const CallDesc &c);
+hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_t *dy, const GradOut &o, void *ws,
+                           hipStream_t stream);
+
 // Decomposition (one band of one family): W0 = bf16(mean of the m layers
 // W [m][nk]); per layer s [N] (LS row scale of W - D against W0, fp32; D =
 // the layer's delta U V^T in fp32 [N][K], or NULL) and R = W - s W0 (fp32

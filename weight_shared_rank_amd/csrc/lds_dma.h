@@ -88,13 +88,18 @@ __device__ __forceinline__ void wait_and_sync() {
   asm volatile("" ::: "memory");
 }
 
-// Workgroup index -> (feature tile, K slice, token tile), XCD-major: hardware
-// sends workgroup w to XCD w % 8; XCD x is given the contiguous unit range
-// [x * per + min(x, rem), ...) of the total units, token tile fastest.
-__device__ __forceinline__ void unit_of(int id, int total, int nT, int nslices, int &f, int &sl, int &t) {
+// Workgroup index -> unit, XCD-major: hardware sends workgroup w to XCD w % 8;
+// XCD x is given the contiguous unit range [x * per + min(x, rem), ...) of the
+// total units.
+__device__ __forceinline__ int xcd_unit(int id, int total) {
   const int x = id & 7, j = id >> 3;
   const int per = total >> 3, rem = total & 7;
-  const int u = x * per + min(x, rem) + j;
+  return x * per + min(x, rem) + j;
+}
+
+// Workgroup index -> (feature tile, K slice, token tile), token tile fastest.
+__device__ __forceinline__ void unit_of(int id, int total, int nT, int nslices, int &f, int &sl, int &t) {
+  const int u = xcd_unit(id, total);
   f = u / (nslices * nT);
   const int r = u % (nslices * nT);
   sl = r / nT;

@@ -316,6 +316,7 @@ namespace {
 struct Resolved {
   wl::CallDesc c;
   int out_dim;
+  int rank[3];  // children's ranks (unpadded)
 };
 
 // Fill a CallDesc for (layer, family) or (layer, stack).
@@ -384,6 +385,7 @@ wl_status resolve(const wl_bundle *h, int32_t layer, int32_t family, int32_t sta
     ch.N = gs.N[i];
     ch.rpad = gs.rpad[i];
     ch.zoff = gs.zoff[i] - z0;
+    rv.rank[i - first] = gs.r[i];
     ch.y_off = ycol;
     ycol += gs.N[i];
     ch.dup_off = -1;
@@ -554,6 +556,119 @@ wl_status check_aligned(const void *p, size_t align, const char *what) {
 bool overlap(const void *a, size_t an, const void *b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && an && bn && x < y + bn && y < x + an;
+}
+
+// ---- backward ----
+
+// Dimensions of a group's stacked call (first..last its children) as the
+// backward planner reads them; no pointers.
+wl::CallDesc call_shape(const GroupShape &gs, int first, int last, bool dup) {
+  wl::CallDesc c;
+  std::memset(&c, 0, sizeof c);
+  c.K = gs.K;
+  c.nchild = last - first;
+  int ycol = 0;
+  for (int i = first; i < last; ++i) {
+    wl::ChildDesc &ch = c.ch[i - first];
+    ch.row_start = gs.row_start[i] - gs.row_start[first];
+    ch.N = gs.N[i];
+    ch.rpad = gs.rpad[i];
+    ch.zoff = gs.zoff[i] - gs.zoff[first];
+    ch.y_off = ycol;
+    ch.dup_off = -1;
+    ycol += gs.N[i];
+    c.Ntot += gs.N[i];
+    c.Rz += gs.rpad[i];
+  }
+  if (dup) c.ch[gs.child_of_fam[WL_K] - first].dup_off = ycol;
+  return c;
+}
+
+size_t ws_backward_products(const Layout &lo, int32_t T) {
+  size_t n = 256;
+  for (int t = 0; t < lo.NT; ++t)
+    for (int g = 0; g < kGroups; ++g) {
+      const GroupShape &gs = lo.gs[t][g];
+      if (!gs.any) continue;
+      n = std::max(n, wl::backward_workspace_bytes(call_shape(gs, 0, gs.nchild, gs.tied), T));
+      for (int c = 0; c < gs.nchild; ++c) n = std::max(n, wl::backward_workspace_bytes(call_shape(gs, c, c + 1, false), T));
+    }
+  return align256(n);
+}
+
+size_t ws_backward_bytes(const Layout &lo, int32_t T) { return ws_backward_products(lo, T) + ws_w0_expand_bytes(lo); }
+
+wl_status run_backward(const wl_bundle *h, int32_t layer, int32_t family, int32_t stack, const void *d_xcode,
+                       size_t xcode_bytes, const void *d_dy, int32_t T, const wl_grads *gr, void *d_ws,
+                       size_t ws_bytes, void *stream) {
+  Resolved rv;
+  wl_status st = resolve(h, layer, family, stack, rv);
+  if (st != WL_OK) return st;
+  if (!gr) return fail(WL_EINVAL, "grads is NULL");
+  wl::CallDesc &c = rv.c;
+  if ((st = check_act_shape(T, c.K)) != WL_OK) return st;
+  c.T = T;
+  // the outputs: alignment, and ranges that must not meet
+  struct Range {
+    const void *p;
+    size_t n;
+    const char *what;
+  };
+  Range r[16];
+  int no = 0;
+  wl::GradOut o{};
+  auto out = [&](const void *p, size_t n, size_t align, const char *what) -> wl_status {
+    if (!p || !n) return WL_OK;
+    if (reinterpret_cast<uintptr_t>(p) % align) return fail(WL_EINVAL, "%s must be %zu-byte aligned", what, align);
+    r[no++] = Range{p, n, what};
+    return WL_OK;
+  };
+  const size_t sK = static_cast<size_t>(c.K), sN = static_cast<size_t>(c.Ntot);
+  o.dx = static_cast<uint16_t *>(gr->dx);
+  o.ds = gr->ds;
+  o.dw0 = gr->dw0;
+  o.accumulate = gr->accumulate_dw0 ? 1 : 0;
+  if ((st = out(gr->dx, T * sK * 2, 16, "dx")) != WL_OK) return st;
+  if ((st = out(gr->ds, sN * 4, 4, "ds")) != WL_OK) return st;
+  if ((st = out(gr->dw0, sN * sK * 4, 16, "dw0")) != WL_OK) return st;
+  for (int i = 0; i < c.nchild; ++i) {
+    o.r[i] = rv.rank[i];
+    if (!rv.rank[i]) continue;
+    o.du[i] = static_cast<uint16_t *>(gr->du[i]);
+    o.dv[i] = static_cast<uint16_t *>(gr->dv[i]);
+    if ((st = out(gr->du[i], static_cast<size_t>(c.ch[i].N) * rv.rank[i] * 2, 2, "du")) != WL_OK) return st;
+    if ((st = out(gr->dv[i], sK * rv.rank[i] * 2, 2, "dv")) != WL_OK) return st;
+  }
+  const int nout = no;
+  const CodeShape cs = code_shape(T, c.K, false);
+  size_t need = 0;
+  if (T > 0) {
+    if ((st = check_code_buffer(d_xcode, xcode_bytes, cs.bytes, "checkpoint")) != WL_OK) return st;
+    if ((st = check_aligned(d_dy, 2, "dy")) != WL_OK) return st;
+    if ((st = check_aligned(d_ws, 256, "workspace")) != WL_OK) return st;
+    need = ws_backward_bytes(h->lo, T);
+    if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
+    r[no++] = Range{d_xcode, cs.bytes, "the checkpoint"};
+    r[no++] = Range{d_dy, static_cast<size_t>(T) * rv.out_dim * 2, "dy"};
+    r[no++] = Range{d_ws, need, "the workspace"};
+  }
+  r[no++] = Range{h->arena, h->arena_bytes, "the arena"};
+  for (int i = 0; i < no; ++i)
+    for (int j = i + 1; j < no; ++j) {
+      // among the inputs only the workspace is written
+      if (i >= nout && r[i].p != d_ws && r[j].p != d_ws) continue;
+      if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return fail(WL_EINVAL, "%s must not overlap %s", r[i].what, r[j].what);
+    }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T > 0 && h->lo.coded() && (o.dx || o.ds)) {
+    uint16_t *w0 = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(d_ws) + ws_backward_products(h->lo, T));
+    const hipError_t e = h->lo.fp8 ? wl::launch_dequantize_rows(c.W0f8, c.ldw0, c.q, c.Ntot, c.K, w0, s)
+                                   : wl::launch_dequantize_mxfp4(c.W0f4, 2 * c.ldw0, c.sc4, c.Ntot, c.K, w0, s);
+    if (e != hipSuccess) return hip_fail(e, "W0 expand launch");
+    c.W0 = w0;
+  }
+  const hipError_t e = wl::launch_backward(c, code_view(d_xcode, cs), static_cast<const uint16_t *>(d_dy), o, d_ws, s);
+  return e == hipSuccess ? WL_OK : hip_fail(e, "backward launch");
 }
 
 }  // namespace
@@ -888,6 +1003,31 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
   const hipError_t e = wl::launch_coded_linear(code_view(d_wcode, cw), N, x, T, static_cast<uint16_t *>(d_y),
                                                static_cast<float *>(d_ws), s);
   return e == hipSuccess ? WL_OK : hip_fail(e, "kernel launch");
+}
+
+size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T) {
+  if (!bundle) {
+    fail(WL_EINVAL, "bundle is NULL");
+    return 0;
+  }
+  if (T < 0 || T > kMaxDim) {
+    fail(WL_EINVAL, "T = %d outside [0, %d]", T, kMaxDim);
+    return 0;
+  }
+  return ws_backward_bytes(bundle->lo, T);
+}
+
+wl_status weightless_linear_backward(const wl_bundle *bundle, int32_t layer, int32_t family, const void *d_xcode,
+                                     size_t xcode_bytes, const void *d_dy, int32_t T, const wl_grads *grads,
+                                     void *d_ws, size_t ws_bytes, void *stream) {
+  return run_backward(bundle, layer, family, -1, d_xcode, xcode_bytes, d_dy, T, grads, d_ws, ws_bytes, stream);
+}
+
+wl_status weightless_stacked_backward(const wl_bundle *bundle, int32_t layer, int32_t stack, const void *d_xcode,
+                                      size_t xcode_bytes, const void *d_dy, int32_t T, const wl_grads *grads,
+                                      void *d_ws, size_t ws_bytes, void *stream) {
+  if (stack < 0) return fail(WL_ERANGE, "stack %d out of range", stack);
+  return run_backward(bundle, layer, -1, stack, d_xcode, xcode_bytes, d_dy, T, grads, d_ws, ws_bytes, stream);
 }
 
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack) {
