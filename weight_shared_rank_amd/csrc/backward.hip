@@ -27,6 +27,7 @@
 // operands of the matrix cores (z as in the forward).  G is exact products of
 // bf16 values summed in fp32, and dW0 and ds stay fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "internal.h"
@@ -37,9 +38,11 @@ namespace wl {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-constexpr int kBK = 64;  // contraction steps
+constexpr int kStep = 64;  // contraction values a product is planned and split in
 constexpr int kCUs = 256;
 constexpr int kMaxSeg = 4;
 constexpr int kMaxProb = 9;
@@ -81,127 +84,207 @@ struct BwdArgs {
   Prob p[kMaxProb];
 };
 
-// Chunk swizzle of a k-column stage row (16-byte chunk c of row k sits in slot
-// c ^ swz(k)).  A transposing read takes 32-byte pieces of rows k = 8 g + 0..3
-// (lane group g); two lane groups at once then touch 8 rows, which the swizzle
-// puts in 8 different 32-byte places of the 256-byte bank period: rows of
-// >= 256 bytes all start at bank 0, 128-byte rows alternate between the halves.
-template <int W>
-__device__ __forceinline__ int swz(int k) {
-  return W >= 128 ? 2 * ((k & 3) | ((k >> 1) & 4)) : 2 * (((k >> 1) & 1) | ((k >> 2) & 2));
+// One operand of a staged product: W rows of the tile by BK (32 or 64) of the
+// contraction per stage, in 1 KB load instructions.
+//
+// k-rows (TR false): LDS row r is the BK values of tile row r.  64-byte rows
+// keep 16-byte chunk c in slot c ^ (r / 4 % 4), 128-byte rows in c ^ (r % 8):
+// a fragment read (8 lanes per phase: 8 rows, one chunk) then touches every
+// bank once.
+//
+// k-columns (TR): LDS row k is W elements of contraction index k, its chunk c
+// in slot c ^ swz(k).  A transposing read takes 32-byte pieces of rows 8 g +
+// 0..3 (lane group g); two lane groups at once touch 8 rows, which the swizzle
+// puts in 8 different 32-byte places of the 256-byte bank period.  Rows of >=
+// 256 bytes all start at bank 0: swz = 2 (k & 3) + 8 (k >> 3 & 1).  128-byte
+// rows alternate between its halves: swz = 2 (k >> 1 & 1) + 4 (k >> 3 & 1).
+//
+// A lane's place in a load is a per-lane part (kept in two registers) and a
+// part of the instruction's number, so the addresses of the loads cost no
+// registers of their own.
+template <int W, bool TR, int BK>
+struct Operand {
+  static constexpr int READS = TR ? 2 : 1;          // LDS reads of a fragment
+  static constexpr int CPR = TR ? W / 8 : BK / 8;       // 16-byte chunks of an LDS row
+  static constexpr int RPQ = 64 / CPR;              // LDS rows of a load instruction
+  static_assert(W == 64 || W == 128 || W == 256, "tile width");
+
+  int lrow, chunk;   // this lane's row of a load and its chunk, without the instruction's swizzle
+  uint32_t lo;       // byte offset of lrow's start
+  int rd;            // fragment reads: byte offset of the lane's first row
+
+  // mw: the wave's first row of the tile
+  __device__ __forceinline__ Operand(int lane, int64_t ld, int mw) {
+    const int r16 = lane & 15, g = lane >> 4;
+    lrow = lane / CPR;
+    lo = static_cast<uint32_t>(lrow * ld * 2);
+    const int slot = lane % CPR;
+    if constexpr (TR) {
+      chunk = slot ^ (W >= 128 ? 2 * (lrow & 3) : 2 * ((lrow >> 1) & 1));
+      const int k = 8 * g + (r16 >> 2);
+      const int sw = W >= 128 ? 2 * (k & 3) + 8 * ((k >> 3) & 1) : 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1);
+      rd = k * (2 * W) + (((mw / 8 + ((r16 >> 1) & 1)) ^ sw) * 16) + (r16 & 1) * 8;
+    } else {
+      chunk = slot ^ (BK == 64 ? lrow & 7 : (lrow >> 2) & 3);
+      rd = (mw + r16) * (2 * BK) + (g ^ (BK == 64 ? r16 & 7 : (r16 >> 2) & 3)) * 16;
+    }
+  }
+  // Swizzle part of load instruction q (the bits of its first row).
+  static __device__ __forceinline__ int sw_of(int q) {
+    if constexpr (!TR) return 0;
+    return W == 256 ? 4 * (q & 1) + 8 * ((q >> 2) & 1) : W == 128 ? 8 * ((q >> 1) & 1) : 4 * (q & 1);
+  }
+  // Load instruction q of a stage at `base`; lim rows (k-rows) or columns
+  // (k-columns) of the tile exist, `left` values of the contraction.
+  __device__ __forceinline__ void load(const uint16_t *base, int q, int64_t ld, int lim, int left, lds_u8 *dst) const {
+    const int c = chunk ^ sw_of(q), row = q * RPQ + lrow;
+    const bool in = TR ? c * 8 < lim && row < left : row < lim && c * 8 < left;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_rsrc(base), (lds_void *)(dst + q * 1024), 16,
+                                             in ? lo + c * 16 : kBufNoRow, static_cast<int>(q * RPQ * ld * 2), 0, 0);
+  }
+  static __device__ __forceinline__ const uint16_t *base(const uint16_t *p, int64_t ld, int m0, int k) {
+    return TR ? p + k * ld + m0 : p + m0 * ld + k;
+  }
+  static __device__ __forceinline__ int64_t advance(int64_t ld) { return TR ? BK * ld : BK; }
+
+  // Fragment i (rows 16 i .. of the wave's), contraction 32 h + 8 g .. + 7 in
+  // lane group g.  Stages start at multiples of 1 KB, so an exclusive or moves
+  // between the chunks of a row.
+  __device__ __forceinline__ u32x4 frag(const lds_u8 *lds, int stage, int i, int h) const {
+    if constexpr (TR) {
+      const lds_u8 *p = lds + ((stage + rd) ^ (32 * i)) + 32 * h * 2 * W;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * 2 * W));
+      const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+      return u32x4{x[0], x[1], y[0], y[1]};
+    } else {
+      return *(const lds_u32x4 *)(lds + ((stage + rd) ^ (64 * h)) + i * 16 * 2 * BK);
+    }
+  }
+};
+
+// Scheduling of a region with M MFMAs and R LDS reads: the reads spread evenly
+// among the MFMAs (they feed the next region, so none has to come first).
+template <int M, int R>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+    constexpr int per = M / R > 0 ? M / R : 1;
+    __builtin_amdgcn_sched_group_barrier(0x008, per, 0);  // MFMAs
+  }
 }
 
-// One operand of a staged product: W rows of the tile, 64 of the contraction
-// per stage, W * 128 bytes of LDS.  TR: k-columns.
-template <int W, bool TR>
-struct Operand {
-  static constexpr int CPR = TR ? W / 8 : 8;  // 16-byte chunks of an LDS row
-
-  // This lane's part of load instruction q (1 KB of the stage): byte offset
-  // from the stage's base, or kBufNoRow where the tile has no such row or
-  // column; kpos is the lane's first contraction index in the stage.
-  static __device__ __forceinline__ uint32_t source(int q, int lane, int64_t ld, int lim, int &kpos) {
-    const int id = q * 64 + lane, row = id / CPR, slot = id % CPR;
-    if constexpr (TR) {
-      const int c = slot ^ swz<W>(row);
-      kpos = row;
-      return c * 8 < lim ? static_cast<uint32_t>(row * ld * 2 + c * 16) : kBufNoRow;
-    } else {
-      const int c = slot ^ (row & 7);
-      kpos = c * 8;
-      return row < lim ? static_cast<uint32_t>(row * ld * 2 + c * 16) : kBufNoRow;
-    }
-  }
-  static __device__ __forceinline__ const uint16_t *base(const uint16_t *p, int64_t ld, int m0, int step) {
-    return TR ? p + static_cast<int64_t>(step) * kBK * ld + m0 : p + m0 * ld + step * kBK;
-  }
-  static __device__ __forceinline__ int64_t advance(int64_t ld) { return TR ? kBK * ld : kBK; }
-
-  // Fragment of 16 rows from row m of the tile, contraction 32 h + 8 g .. + 7.
-  static __device__ __forceinline__ u32x4 frag(uint8_t *sb, int m, int h, int r16, int g) {
-    if constexpr (TR) {
-      const int k = 32 * h + 8 * g + (r16 >> 2);
-      const int c = (m / 8 + ((r16 >> 1) & 1)) ^ swz<W>(k);
-      uint8_t *p = sb + k * (2 * W) + c * 16 + (r16 & 1) * 8;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * 2 * W));
-      const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-      return u32x4{a[0], a[1], b[0], b[1]};
-    } else {
-      return *reinterpret_cast<const u32x4 *>(sb + (m + r16) * kRowBytes + ((4 * h + g) ^ (r16 & 7)) * 16);
-    }
-  }
-};
-
-template <int BM_, int BN_, int WM_, int WN_, int NST_>
+// NST stages of BK contraction values of a BM x BN tile, on WM x WN waves.
+// WPS: waves per SIMD that the registers are allotted for.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int NST_, int WPS_ = 2>
 struct BTile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
+  static constexpr int WPS = WPS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, NST = NST_;
   static constexpr int NW = WM * WN;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
-  static constexpr int GA = BM / 8, GB = BN / 8, LPW = (GA + GB) / NW;
-  static constexpr int STAGE = (BM + BN) * kRowBytes;
+  static constexpr int LA = BM * BK / 512 / NW, LB = BN * BK / 512 / NW;  // load instructions of a wave per stage
+  static constexpr int LPW = LA + LB;
+  static constexpr int BOFF = BM * BK * 2, STAGE = BOFF + BN * BK * 2;    // B behind A in a stage
   static constexpr int PITCH = 2 * BM + 16;      // staged bf16 output: bytes per b
-  static constexpr int WPITCH = 4 * TM + 16;     // a wave's staged fp32 rows of G
   static constexpr size_t RING = static_cast<size_t>(NST) * STAGE, OUT = static_cast<size_t>(BN) * PITCH;
-  static constexpr size_t WOUT = static_cast<size_t>(NW) * 16 * WPITCH;
-  static constexpr size_t MX = RING > OUT ? RING : OUT;
-  static constexpr size_t LDS = MX > WOUT ? MX : WOUT;
-  static_assert((GA + GB) % NW == 0 && TM % 16 == 0 && TN % 16 == 0 && LDS <= 160 * 1024, "tile shape");
+  static constexpr size_t LDS = RING > OUT ? RING : OUT;
+  static_assert(BM * BK / 512 % NW == 0 && BN * BK / 512 % NW == 0 && TM % 16 == 0 && TN % 16 == 0 && LDS <= 160 * 1024, "tile shape");
 };
 
-// Rows of G (a wave's TM x TN part) leave through LDS, 16 n at a time, so that
-// W0 is read and dW0 is read and written in whole runs of TM elements of one
-// row; the ds sums run along those rows.
+// G's consumers, from the accumulators as they lie (a lane holds k = 16 i +
+// 4 g .. + 3 of rows n = 16 j + r16): W0 and dW0 move as 8- and 16-byte pieces
+// whose neighbours (i) complete each cache line, every load of a j is in flight
+// before the first is used, and ds needs two lane exchanges per j.  (Rows
+// staged through LDS for whole-row accesses took 25 us per 256 x 256 tile: a
+// load latency and five exchanges for every two rows.)
 template <typename TL>
 __device__ __forceinline__ void store_weight_grad(const f32x4 (&acc)[TL::FM][TL::FN], const Prob &p, int f, int m0,
-                                                  int n0, uint8_t *lds) {
-  constexpr int LPR = TL::TM / 4;     // lanes per row
-  constexpr int RPI = 64 / LPR;       // rows per instruction
+                                                  int n0) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / TL::WN, wn = wave % TL::WN, r16 = lane & 15, g = lane >> 4;
-  uint8_t *mine = lds + wave * 16 * TL::WPITCH;
-  const int kl = (lane % LPR) * 4, k = m0 + wm * TL::TM + kl;
-  const bool kin = k < p.M;           // M % 8 == 0: whole groups of 4
+  const int k0 = m0 + wm * TL::TM + g * 4;  // M % 8 == 0: whole groups of 4
+  constexpr int H = TL::FM / 2;             // the loads of half a j at a time: more would not fit the registers
 #pragma unroll
   for (int j = 0; j < TL::FN; ++j) {
-    asm volatile("" ::: "memory");
+    const int n = n0 + wn * TL::TN + j * 16 + r16;
+    const bool row = n < p.N;
+    const int64_t at = static_cast<int64_t>(row ? n : 0) * p.M + k0;
+    const float sc = p.dw0 && row ? p.s[n] : 0.f;
+    float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < TL::FM; ++i)
-      *reinterpret_cast<f32x4 *>(mine + r16 * TL::WPITCH + (i * 16 + g * 4) * 4) = acc[i][j];
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    for (int h = 0; h < TL::FM; h += H) {
+      asm volatile("" ::: "memory");
+      u32x2 w[H];
+      f32x4 d[H];
 #pragma unroll
-    for (int it = 0; it < 16 / RPI; ++it) {
-      const int r = it * RPI + lane / LPR;
-      const int n = n0 + wn * TL::TN + j * 16 + r;
-      const bool in = n < p.N && kin;
-      const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + r * TL::WPITCH + kl * 4);
-      if (p.dw0 && in) {
-        f32x4 *d = reinterpret_cast<f32x4 *>(p.dw0 + static_cast<int64_t>(n) * p.M + k);
-        const float sc = p.s[n];
-        f32x4 o = v * sc;
-        if (p.accumulate) o += *d;
-        *d = o;
+      for (int i = 0; i < H; ++i) {
+        const bool in = row && k0 + 16 * (h + i) < p.M;
+        w[i] = u32x2{0u, 0u};
+        d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (p.dsp && in) w[i] = *reinterpret_cast<const u32x2 *>(p.W0 + at + 16 * (h + i));
+        if (p.accumulate && in) d[i] = *reinterpret_cast<const f32x4 *>(p.dw0 + at + 16 * (h + i));
       }
-      if (p.dsp) {
-        float t = 0.f;
-        if (in) {
-          const u32x2 w = *reinterpret_cast<const u32x2 *>(p.W0 + static_cast<int64_t>(n) * p.M + k);
-          t = v[0] * __uint_as_float(w[0] << 16) + v[1] * __uint_as_float(w[0] & 0xffff0000u) +
-              v[2] * __uint_as_float(w[1] << 16) + v[3] * __uint_as_float(w[1] & 0xffff0000u);
-        }
 #pragma unroll
-        for (int d = 1; d < LPR; d <<= 1) t += __shfl_xor(t, d, 64);
-        if (lane % LPR == 0 && n < p.N) p.dsp[static_cast<int64_t>(f * TL::WM + wm) * p.ldds + n] = t;
+      for (int i = 0; i < H; ++i) {
+        const f32x4 v = acc[h + i][j];
+        if (p.dw0 && row && k0 + 16 * (h + i) < p.M)
+          *reinterpret_cast<f32x4 *>(p.dw0 + at + 16 * (h + i)) = d[i] + v * sc;
+        // columns past M hold no G (their operand columns are zeros)
+        t += v[0] * __uint_as_float(w[i][0] << 16) + v[1] * __uint_as_float(w[i][0] & 0xffff0000u) +
+             v[2] * __uint_as_float(w[i][1] << 16) + v[3] * __uint_as_float(w[i][1] & 0xffff0000u);
       }
     }
+    if (p.dsp) {
+      t += __shfl_xor(t, 16, 64);
+      t += __shfl_xor(t, 32, 64);
+      if (g == 0 && row) p.dsp[static_cast<int64_t>(f * TL::WM + wm) * p.ldds + n] = t;
+    }
   }
+}
+
+// Loads of a stage into `w`: all of it, or all but the last instruction (the
+// first of its two steps when a stage is two halves deep), or that last one.
+enum Part : int { kAll = 0, kFirst = 1, kLast = 2 };
+
+template <typename TL, Part PART, typename OA, typename OB>
+__device__ __forceinline__ void load_stage(const OA &oa, const OB &ob, const uint16_t *pa, const uint16_t *pb,
+                                           int64_t lda, int64_t ldb, int lima, int limb, int left, int wave,
+                                           lds_u8 *w) {
+  if constexpr (PART != kLast) {
+#pragma unroll
+    for (int q = 0; q < TL::LA; ++q) oa.load(pa, wave * TL::LA + q, lda, lima, left, w);
+  }
+#pragma unroll
+  for (int q = 0; q < TL::LB; ++q)
+    if (PART == kAll || (PART == kLast) == (q == TL::LB - 1)) ob.load(pb, wave * TL::LB + q, ldb, limb, left, w + TL::BOFF);
+}
+
+// One pipeline step's memory work: loads of a stage into `w`, and the
+// fragments of half h of the stage at r + stage.  They are different stages,
+// and saying so (restrict, on accesses of one call) keeps the compiler from
+// draining the loads in flight before the transposing reads, whose addresses
+// it does not follow (it did: 1.8x the time of a 256 x 256 tile's step).
+// What orders a stage's loads before its own reads is the counted wait and
+// barrier between them.
+template <typename TL, Part PART, typename OA, typename OB>
+__device__ __forceinline__ void move_stage(const OA &oa, const OB &ob, const uint16_t *pa, const uint16_t *pb,
+                                           int64_t lda, int64_t ldb, int lima, int limb, int left, int wave,
+                                           lds_u8 *__restrict__ w, const lds_u8 *__restrict__ r, int stage, int h,
+                                           u32x4 (&fa)[TL::FM], u32x4 (&fb)[TL::FN]) {
+  load_stage<TL, PART>(oa, ob, pa, pb, lda, ldb, lima, limb, left, wave, w);
+#pragma unroll
+  for (int j = 0; j < TL::FN; ++j) fb[j] = ob.frag(r, stage + TL::BOFF, j, h);
+#pragma unroll
+  for (int i = 0; i < TL::FM; ++i) fa[i] = oa.frag(r, stage, i, h);
 }
 
 template <typename TL, bool ATR, bool BTR>
-__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 2))) void product_kernel(BwdArgs args) {
-  using OA = Operand<TL::BM, ATR>;
-  using OB = Operand<TL::BN, BTR>;
+__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, TL::WPS))) void product_kernel(BwdArgs args) {
+  using OA = Operand<TL::BM, ATR, TL::BK>;
+  using OB = Operand<TL::BN, BTR, TL::BK>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  lds_u8 *const ring = (lds_u8 *)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
   const int r16 = lane & 15, g = lane >> 4;
@@ -227,58 +310,71 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
 
   for (int si = 0; si < p.nseg; ++si) {
     const Seg &sg = p.seg[si];
-    const int steps = (sg.len + kBK - 1) / kBK;
-    const int b0 = max(0, s_lo), nk = min(steps, s_hi) - b0;
+    const int steps = (sg.len + kStep - 1) / kStep;
+    const int b0 = max(0, s_lo), ns = min(steps, s_hi) - b0;
     s_lo -= steps;
     s_hi -= steps;
-    if (nk <= 0) continue;
-    uint32_t off[TL::LPW];
-    int kpos[TL::LPW];
-#pragma unroll
-    for (int q = 0; q < TL::LPW; ++q) {
-      const int gq = wave * TL::LPW + q;
-      off[q] = gq < TL::GA ? OA::source(gq, lane, sg.lda, p.M - m0, kpos[q])
-                           : OB::source(gq - TL::GA, lane, sg.ldb, p.N - n0, kpos[q]);
-    }
-    const uint16_t *pa = OA::base(sg.A, sg.lda, m0, b0), *pb = OB::base(sg.B, sg.ldb, n0, b0);
+    if (ns <= 0) continue;
+    const OA oa(lane, sg.lda, wm * TL::TM);
+    const OB ob(lane, sg.ldb, wn * TL::TN);
+    const uint16_t *pa = OA::base(sg.A, sg.lda, m0, b0 * kStep), *pb = OB::base(sg.B, sg.ldb, n0, b0 * kStep);
     const int64_t adv_a = OA::advance(sg.lda), adv_b = OB::advance(sg.ldb);
-    const int full = sg.len / kBK;
-    int step = b0;
-    auto issue = [&](int stage) {
-      const auto ra = tile_rsrc(pa), rb = tile_rsrc(pb);
-      const int left = step < full ? kBK : sg.len - step * kBK;  // contraction values of this step
-      uint8_t *st = lds + stage * TL::STAGE;
-#pragma unroll
-      for (int q = 0; q < TL::LPW; ++q) {
-        const int gq = wave * TL::LPW + q;
-        load_lds<16>(gq < TL::GA ? ra : rb, kpos[q] < left ? off[q] : kBufNoRow, st + gq * 1024);
-      }
+    int left = min(sg.len, (b0 + ns) * kStep) - b0 * kStep;  // values from the next stage to load on
+    auto advance = [&]() {
       pa += adv_a;
       pb += adv_b;
-      ++step;
+      left -= TL::BK;
     };
+    auto multiply = [&](const u32x4(&fa)[TL::FM], const u32x4(&fb)[TL::FN]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int st = 0; st < TL::NST - 1; ++st)
-      if (st < nk) issue(st);
-    for (int kt = 0; kt < nk; ++kt) {
-      if (kt + TL::NST - 2 < nk)
-        wait_and_sync<(TL::NST - 2) * TL::LPW>();
-      else
-        wait_and_sync<0>();
-      if (kt + TL::NST - 1 < nk) issue((kt + TL::NST - 1) % TL::NST);
-      uint8_t *sa = lds + (kt % TL::NST) * TL::STAGE, *sb = sa + TL::BM * kRowBytes;
+      for (int i = 0; i < TL::FM; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 fa[TL::FM], fb[TL::FN];
+        for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma16x16x32(fa[i], fb[j], acc[i][j]);
+      interleave<TL::FM * TL::FN, OA::READS * TL::FM + OB::READS * TL::FN>();
+    };
+    // Software pipeline over 32-deep halves: while one is multiplied from
+    // registers, the next is read from LDS, and the stages after that are in
+    // flight.  A step into a new stage opens with the barrier: there every
+    // wave has read all of the stage before, so its buffer takes the loads of
+    // the stage NST ahead, and the new stage has landed.  Loads past the last
+    // stage read no rows (zeros), so that the loop needs no branches and
+    // counts the same loads in flight at every step.
+    u32x4 a0[TL::FM], b0f[TL::FN], a1[TL::FM], b1f[TL::FN];
+    constexpr bool kHalves = TL::BK == 64;
+    const int lima = p.M - m0, limb = p.N - n0;
 #pragma unroll
-        for (int j = 0; j < TL::FN; ++j) fb[j] = OB::frag(sb, wn * TL::TN + j * 16, h, r16, g);
-#pragma unroll
-        for (int i = 0; i < TL::FM; ++i) fa[i] = OA::frag(sa, wm * TL::TM + i * 16, h, r16, g);
-#pragma unroll
-        for (int i = 0; i < TL::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma16x16x32(fa[i], fb[j], acc[i][j]);
+    for (int st = 0; st < TL::NST; ++st) {
+      if (kHalves && st == TL::NST - 1) {
+        load_stage<TL, kFirst>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + st * TL::STAGE);
+      } else {
+        load_stage<TL, kAll>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + st * TL::STAGE);
+        advance();
       }
+    }
+    wait_and_sync<(TL::NST - 1) * TL::LPW - (kHalves ? 1 : 0)>();
+    int cur = 0, old = (TL::NST - 1) * TL::STAGE;  // the stage read, the stage loaded last
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) b0f[j] = ob.frag(ring, TL::BOFF, j, 0);
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) a0[i] = oa.frag(ring, 0, i, 0);
+    auto into_stage = [&](u32x4(&fa)[TL::FM], u32x4(&fb)[TL::FN]) __attribute__((always_inline)) {
+      wait_and_sync<(TL::NST - 2) * TL::LPW>();
+      old = cur;
+      cur = cur + TL::STAGE == static_cast<int>(TL::RING) ? 0 : cur + TL::STAGE;
+      move_stage<TL, kHalves ? kFirst : kAll>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + old, ring,
+                                              cur, 0, fa, fb);
+      if (!kHalves) advance();
+    };
+    for (int kt = 0; kt < ns; ++kt) {
+      if constexpr (kHalves) {
+        move_stage<TL, kLast>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + old, ring, cur, 1, a1, b1f);
+        advance();
+      } else {
+        into_stage(a1, b1f);
+      }
+      multiply(a0, b0f);
+      into_stage(a0, b0f);
+      multiply(a1, b1f);
     }
     wait_and_sync<0>();  // the ring is idle
   }
@@ -298,7 +394,7 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
     return;
   }
   if (p.mode == kWeight) {
-    if constexpr (ATR && BTR) store_weight_grad<TL>(acc, p, f, m0, n0, lds);
+    if constexpr (ATR && BTR) store_weight_grad<TL>(acc, p, f, m0, n0);
     return;
   }
   // bf16 tile in LDS, b-major, then whole 16-byte chunks of output rows
@@ -388,13 +484,23 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
   if (threadIdx.x == 0) p.ds[n] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// ds[n] = sum of the column tiles' partial sums, in order.
+// ds[n] = sum of the column tiles' partial sums: 16 rows n per workgroup, 16
+// lanes per row each summing every 16th part, joined in a fixed tree (one lane
+// per row took 18 us for 42 parts, a load latency each).
 __global__ __launch_bounds__(256) void sum_ds_kernel(const float *dsp, int parts, int ldds, int N, float *ds) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  const int n = blockIdx.x * 16 + (threadIdx.x & 15), l = threadIdx.x >> 4;
   float t = 0.f;
-  for (int i = 0; i < parts; ++i) t += dsp[static_cast<int64_t>(i) * ldds + n];
-  ds[n] = t;
+  if (n < N)
+    for (int i = l; i < parts; i += 16) t += dsp[static_cast<int64_t>(i) * ldds + n];
+  __shared__ float part[16][17];
+  part[l][threadIdx.x & 15] = t;
+  __syncthreads();
+  if (threadIdx.x < 16 && n < N) {
+    t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += part[i][threadIdx.x];
+    ds[n] = t;
+  }
 }
 
 // dy [T][ldy] -> rows of ldd columns in which every child's slot starts at a
@@ -410,26 +516,53 @@ struct PrepArgs {
   uint16_t *dyp, *dys;
 };
 
+// A thread takes 8 columns of kPrepT tokens: s is read once for all of them.
+constexpr int kPrepT = 4;
+
 __global__ __launch_bounds__(256) void prep_dy_kernel(PrepArgs a) {
   const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
   if (c >= a.ldd) return;
-  const int64_t t = blockIdx.x;
   int i = 0;
   while (i + 1 < a.nslot && c >= a.start[i + 1]) ++i;
-  const int j = c - a.start[i];
-  const uint16_t *src = a.dy + t * a.ldy + a.from[i] + j;
-  alignas(16) uint16_t e[8];
-  if (j + 8 <= a.n[i] && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    *reinterpret_cast<u32x4 *>(e) = ld16(src);
+  const int j = c - a.start[i], n = a.n[i] - j;  // n: columns of the slot from here on (>= 1)
+  float s[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = a.dys && k < n ? a.s[i][j + k] : 0.f;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kPrepT;
+  const uint16_t *src = a.dy + t0 * a.ldy + a.from[i] + j;
+  const int nt = static_cast<int>(min<int64_t>(kPrepT, a.T - t0));
+  u32x4 v[kPrepT];
+  if (n >= 8 && a.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+#pragma unroll
+    for (int t = 0; t < kPrepT; ++t)
+      if (t < nt) v[t] = ld16(src + static_cast<int64_t>(t) * a.ldy);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = j + k < a.n[i] ? src[k] : 0;
-  }
-  if (a.dyp) *reinterpret_cast<u32x4 *>(a.dyp + t * a.ldd + c) = *reinterpret_cast<const u32x4 *>(e);
-  if (a.dys) {
+    for (int t = 0; t < kPrepT; ++t)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = j + k < a.n[i] ? f32_to_bf16(bf16_to_f32(e[k]) * a.s[i][j + k]) : 0;
-    *reinterpret_cast<u32x4 *>(a.dys + t * a.ldd + c) = *reinterpret_cast<const u32x4 *>(e);
+      for (int k = 0; k < 4; ++k) {
+        const uint16_t *q = src + static_cast<int64_t>(t) * a.ldy + 2 * k;
+        const uint32_t lo = t < nt && 2 * k < n ? q[0] : 0u, hi = t < nt && 2 * k + 1 < n ? q[1] : 0u;
+        v[t][k] = lo | (hi << 16);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < kPrepT; ++t) {
+    if (t >= nt) break;
+    const int64_t at = (t0 + t) * a.ldd + c;
+    if (a.dyp) *reinterpret_cast<u32x4 *>(a.dyp + at) = v[t];
+    if (a.dys) {
+      u32x4 o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = 2 * k >= n ? 0u
+                          : f32_to_bf16(__uint_as_float(v[t][k] << 16) * s[2 * k]) |
+                                (2 * k + 1 >= n ? 0u
+                                                : static_cast<uint32_t>(f32_to_bf16(
+                                                      __uint_as_float(v[t][k] & 0xffff0000u) * s[2 * k + 1]))
+                                                      << 16);
+      *reinterpret_cast<u32x4 *>(a.dys + at) = o;
+    }
   }
 }
 
@@ -448,14 +581,22 @@ hipError_t launch_zero(void *p, int64_t halves, hipStream_t stream) {
 
 // ---- host side --------------------------------------------------------------
 
-using Big = BTile<256, 256, 2, 4, 2>;
-using Mid = BTile<128, 128, 2, 4, 4>;
-using Thin = BTile<64, 128, 2, 4, 4>;
+// Stage depth by the operands: k-column rows are long whatever the depth, so
+// four shallow stages keep more loads in flight; a k-row operand wants whole
+// 128-byte lines (with 64-byte rows a plain load loop ran at 57 KB/us per CU
+// instead of 92).
+template <bool ATR, bool BTR>
+struct Shapes {
+  static constexpr bool kCols = ATR && BTR;
+  using Big = std::conditional_t<kCols, BTile<256, 256, 2, 4, 32, 4>, BTile<256, 256, 2, 4, 64, 2>>;
+  using Mid = std::conditional_t<kCols, BTile<128, 128, 2, 4, 32, 5>, BTile<128, 128, 2, 4, 64, 2>>;
+  using Thin = std::conditional_t<kCols, BTile<64, 128, 2, 2, 32, 6>, BTile<64, 128, 2, 2, 64, 3>>;
+};
 constexpr int kShapes = 3;
 constexpr struct {
   int BM, BN, WM;
   double step;  // us of one contraction step of a workgroup
-} kShape[kShapes] = {{Big::BM, Big::BN, Big::WM, 1.9}, {Mid::BM, Mid::BN, Mid::WM, 0.75}, {Thin::BM, Thin::BN, Thin::WM, 0.6}};
+} kShape[kShapes] = {{256, 256, 2, 1.6}, {128, 128, 2, 0.6}, {64, 128, 2, 0.5}};
 
 struct BPlan {
   int shape, ksplit, per, nM, nN;
@@ -488,7 +629,7 @@ BPlan plan_product(int M, int N, int steps) {
   return best;
 }
 
-int steps_of(int64_t len) { return static_cast<int>((len + kBK - 1) / kBK); }
+int steps_of(int64_t len) { return static_cast<int>((len + kStep - 1) / kStep); }
 int pad8(int n) { return (n + 7) & ~7; }
 size_t pad256(size_t n) { return (n + 255) & ~size_t{255}; }
 
@@ -596,9 +737,10 @@ hipError_t launch_batch(const Batch &b, hipStream_t stream) {
       a.total += p.nM * p.nN * p.ksplit;
     }
     if (!a.nprob) continue;
-    const hipError_t e = sh == 0   ? launch_shape<Big, ATR, BTR>(a, stream)
-                         : sh == 1 ? launch_shape<Mid, ATR, BTR>(a, stream)
-                                   : launch_shape<Thin, ATR, BTR>(a, stream);
+    using S = Shapes<ATR, BTR>;
+    const hipError_t e = sh == 0   ? launch_shape<typename S::Big, ATR, BTR>(a, stream)
+                         : sh == 1 ? launch_shape<typename S::Mid, ATR, BTR>(a, stream)
+                                   : launch_shape<typename S::Thin, ATR, BTR>(a, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -706,7 +848,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     a.start[s.n] = s.ldd;
     a.dyp = direct ? nullptr : reinterpret_cast<uint16_t *>(ws + at.dyp);
     a.dys = o.dx ? dys : nullptr;
-    hipLaunchKernelGGL(prep_dy_kernel, dim3(T, (s.ldd / 8 + 255) / 256), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(prep_dy_kernel, dim3((T + kPrepT - 1) / kPrepT, (s.ldd / 8 + 255) / 256), dim3(256), 0, stream, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   // z = X V and g = dy U
@@ -758,7 +900,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
         p.s = c.s + ch.row_start;
         p.W0 = c.W0 + static_cast<int64_t>(ch.row_start) * K;
         p.dw0 = o.dw0 ? o.dw0 + static_cast<int64_t>(ch.row_start) * K : nullptr;
-        p.accumulate = o.accumulate;
+        p.accumulate = o.dw0 ? o.accumulate : 0;
         p.ds = o.ds ? o.ds + ch.row_start : nullptr;
         p.dsp = o.ds ? dsp + ch.row_start : nullptr;
         p.ldds = c.Ntot;
@@ -778,7 +920,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
       for (int i = 0; i < b.n; ++i) {
         const Prob &p = b.p[i];
         if (p.mode != kWeight || p.ksplit > 1) continue;
-        hipLaunchKernelGGL(sum_ds_kernel, dim3((p.N + 255) / 256), dim3(256), 0, stream,
+        hipLaunchKernelGGL(sum_ds_kernel, dim3((p.N + 15) / 16), dim3(256), 0, stream,
                            static_cast<const float *>(p.dsp), p.nM * kShape[b.shape[i]].WM, p.ldds, p.N, p.ds);
         if ((e = hipGetLastError()) != hipSuccess) return e;
       }
