@@ -31,6 +31,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "coded.h"
 #include "lds_dma.h"
 
 namespace wl {
@@ -45,7 +46,7 @@ typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 constexpr int kStep = 64;  // contraction values a product is planned and split in
 constexpr int kCUs = 256;
 constexpr int kMaxSeg = 4;
-constexpr int kMaxProb = 9;
+constexpr int kMaxProb = 1 + 3 * kMaxChildren;  // dx; G, dU and dV of every child
 constexpr int kGroupN = 8;  // output tiles along b that run together
 
 // A run of the contraction: A and B hold `len` values of it.
@@ -55,6 +56,9 @@ struct Seg {
   int32_t len;
 };
 
+// How the operands lie: A and B k-rows; A k-columns, B k-rows; both k-columns.
+enum Kind : int32_t { kRowsRows = 0, kColsRows = 1, kColsCols = 2 };
+// What becomes of C: bf16 rows, or (G) dW0 and ds.
 enum ProbMode : int32_t { kBf16 = 0, kWeight = 1 };
 
 // One product C[N][M] of a launch.
@@ -62,9 +66,9 @@ struct Prob {
   Seg seg[kMaxSeg];
   int32_t nseg;
   int32_t M, N;       // extent along A (contiguous in C) and along B
-  int32_t mode;
+  int32_t kind, mode;
   int32_t nM, nN, ksplit, per;  // tiles, slices of the contraction, steps per slice
-  int32_t unit0;      // first workgroup
+  int32_t unit0;      // first workgroup of its launch
   uint16_t *out;      // kBf16: [N][ldo]
   int64_t ldo;
   float *P;           // ksplit > 1: partials [ksplit][N][ldp]
@@ -74,9 +78,9 @@ struct Prob {
   const uint16_t *W0; // [N][M]
   float *dw0;         // [N][M] or null
   int32_t accumulate;
-  float *dsp;         // ksplit == 1: partial sums of ds, [nM * WM][ldds] (null: not wanted)
+  float *ds;          // [N] (null: not wanted)
+  float *dsp;         // ksplit == 1: its partial sums [nM * 2][ldds], a row per wave row of the column tiles
   int32_t ldds;
-  float *ds;          // ksplit > 1: [N] (null: not wanted)
 };
 
 struct BwdArgs {
@@ -176,10 +180,8 @@ __device__ __forceinline__ void interleave() {
 }
 
 // NST stages of BK contraction values of a BM x BN tile, on WM x WN waves.
-// WPS: waves per SIMD that the registers are allotted for.
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int NST_, int WPS_ = 2>
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int NST_>
 struct BTile {
-  static constexpr int WPS = WPS_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, NST = NST_;
   static constexpr int NW = WM * WN;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -194,51 +196,59 @@ struct BTile {
 
 // G's consumers, from the accumulators as they lie (a lane holds k = 16 i +
 // 4 g .. + 3 of rows n = 16 j + r16): W0 and dW0 move as 8- and 16-byte pieces
-// whose neighbours (i) complete each cache line, every load of a j is in flight
-// before the first is used, and ds needs two lane exchanges per j.  (Rows
-// staged through LDS for whole-row accesses took 25 us per 256 x 256 tile: a
-// load latency and five exchanges for every two rows.)
+// whose neighbours (i) complete each cache line, all of W0's loads are in
+// flight before the first is used, and ds needs two lane exchanges per j.
+// (Rows staged through LDS for whole-row accesses took 25 us per 256 x 256
+// tile: a load latency and five exchanges for every two rows.)
 template <typename TL>
 __device__ __forceinline__ void store_weight_grad(const f32x4 (&acc)[TL::FM][TL::FN], const Prob &p, int f, int m0,
                                                   int n0) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / TL::WN, wn = wave % TL::WN, r16 = lane & 15, g = lane >> 4;
   const int k0 = m0 + wm * TL::TM + g * 4;  // M % 8 == 0: whole groups of 4
-  constexpr int H = TL::FM / 2;             // the loads of half a j at a time: more would not fit the registers
+  u32x2 w[TL::FN][TL::FM];
+  if (p.ds) {
 #pragma unroll
-  for (int j = 0; j < TL::FN; ++j) {
-    const int n = n0 + wn * TL::TN + j * 16 + r16;
-    const bool row = n < p.N;
-    const int64_t at = static_cast<int64_t>(row ? n : 0) * p.M + k0;
-    const float sc = p.dw0 && row ? p.s[n] : 0.f;
-    float t = 0.f;
+    for (int j = 0; j < TL::FN; ++j) {
+      const int n = n0 + wn * TL::TN + j * 16 + r16;
+      const uint16_t *src = p.W0 + static_cast<int64_t>(n < p.N ? n : 0) * p.M + k0;
 #pragma unroll
-    for (int h = 0; h < TL::FM; h += H) {
-      asm volatile("" ::: "memory");
-      u32x2 w[H];
-      f32x4 d[H];
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const bool in = row && k0 + 16 * (h + i) < p.M;
-        w[i] = u32x2{0u, 0u};
-        d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (p.dsp && in) w[i] = *reinterpret_cast<const u32x2 *>(p.W0 + at + 16 * (h + i));
-        if (p.accumulate && in) d[i] = *reinterpret_cast<const f32x4 *>(p.dw0 + at + 16 * (h + i));
-      }
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const f32x4 v = acc[h + i][j];
-        if (p.dw0 && row && k0 + 16 * (h + i) < p.M)
-          *reinterpret_cast<f32x4 *>(p.dw0 + at + 16 * (h + i)) = d[i] + v * sc;
-        // columns past M hold no G (their operand columns are zeros)
-        t += v[0] * __uint_as_float(w[i][0] << 16) + v[1] * __uint_as_float(w[i][0] & 0xffff0000u) +
-             v[2] * __uint_as_float(w[i][1] << 16) + v[3] * __uint_as_float(w[i][1] & 0xffff0000u);
+      for (int i = 0; i < TL::FM; ++i) {
+        w[j][i] = u32x2{0u, 0u};
+        if (n < p.N && k0 + 16 * i < p.M) w[j][i] = *reinterpret_cast<const u32x2 *>(src + 16 * i);
       }
     }
-    if (p.dsp) {
+  }
+  if (p.dw0) {
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) {
+      const int n = n0 + wn * TL::TN + j * 16 + r16;
+      if (n >= p.N) continue;
+      float *dst = p.dw0 + static_cast<int64_t>(n) * p.M + k0;
+      const float sc = p.s[n];
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i) {
+        if (k0 + 16 * i >= p.M) continue;
+        f32x4 o = acc[i][j] * sc;
+        if (p.accumulate) o += *reinterpret_cast<const f32x4 *>(dst + 16 * i);
+        *reinterpret_cast<f32x4 *>(dst + 16 * i) = o;
+      }
+    }
+  }
+  if (p.ds) {
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) {
+      const int n = n0 + wn * TL::TN + j * 16 + r16;
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i) {
+        const f32x4 v = acc[i][j];  // columns past M hold no G (their operand columns are zeros)
+        t += v[0] * __uint_as_float(w[j][i][0] << 16) + v[1] * __uint_as_float(w[j][i][0] & 0xffff0000u) +
+             v[2] * __uint_as_float(w[j][i][1] << 16) + v[3] * __uint_as_float(w[j][i][1] & 0xffff0000u);
+      }
       t += __shfl_xor(t, 16, 64);
       t += __shfl_xor(t, 32, 64);
-      if (g == 0 && row) p.dsp[static_cast<int64_t>(f * TL::WM + wm) * p.ldds + n] = t;
+      if (g == 0 && n < p.N) p.dsp[static_cast<int64_t>(f * TL::WM + wm) * p.ldds + n] = t;
     }
   }
 }
@@ -279,22 +289,17 @@ __device__ __forceinline__ void move_stage(const OA &oa, const OB &ob, const uin
   for (int i = 0; i < TL::FM; ++i) fa[i] = oa.frag(r, stage, i, h);
 }
 
+// Unit v of product p: a tile of C over one slice of the contraction.
 template <typename TL, bool ATR, bool BTR>
-__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, TL::WPS))) void product_kernel(BwdArgs args) {
+__device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds) {
   using OA = Operand<TL::BM, ATR, TL::BK>;
   using OB = Operand<TL::BN, BTR, TL::BK>;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   lds_u8 *const ring = (lds_u8 *)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
   const int r16 = lane & 15, g = lane >> 4;
-  // workgroup -> unit, XCD-major; unit -> product, slice, tile.  kGroupN tiles
-  // along b share their A panels, then the next panel, then the next group.
-  const int u = xcd_unit(blockIdx.x, args.total);
-  int pi = 0;
-  while (pi + 1 < args.nprob && u >= args.p[pi + 1].unit0) ++pi;
-  const Prob &p = args.p[pi];
-  const int v = u - p.unit0;
+  // kGroupN tiles along b share their A panels, then the next panel, then the
+  // next group
   const int sl = v / (p.nM * p.nN), w = v % (p.nM * p.nN);
   const int grp = w / (p.nM * kGroupN), gn = min(kGroupN, p.nN - grp * kGroupN);
   const int wg = w - grp * p.nM * kGroupN;
@@ -426,14 +431,57 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
   }
 }
 
-// Split products: the slices' partials, summed in slice order.  kBf16: rows of
-// C rounded to bf16; kWeight: a workgroup per row n of G forms dW0's row and
-// ds[n].
+// Workgroup -> product and its unit.  The units of each product are numbered
+// XCD-major, so that the tiles an XCD runs at a time share panels in its L2.
+__device__ __forceinline__ const Prob &find_unit(const BwdArgs &a, int &v) {
+  int pi = 0;
+  while (pi + 1 < a.nprob && static_cast<int>(blockIdx.x) >= a.p[pi + 1].unit0) ++pi;
+  const Prob &p = a.p[pi];
+  v = xcd_unit(blockIdx.x - p.unit0, p.nM * p.nN * p.ksplit);
+  return p;
+}
+
+template <typename TL, bool ATR, bool BTR>
+__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 2))) void product_kernel(BwdArgs args) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  int v;
+  const Prob &p = find_unit(args, v);
+  product_unit<TL, ATR, BTR>(p, v, lds);
+}
+
+// Products of any kind in one launch.
+template <typename TL>
+__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 4))) void products_kernel(BwdArgs args) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  int v;
+  const Prob &p = find_unit(args, v);
+  if (p.kind == kColsCols)
+    product_unit<TL, true, true>(p, v, lds);
+  else if (p.kind == kColsRows)
+    product_unit<TL, true, false>(p, v, lds);
+  else
+    product_unit<TL, false, false>(p, v, lds);
+}
+
+// What is left after the products, one launch: for a split product the sum of
+// its slices' partials in slice order -- rows of C rounded to bf16 (a thread
+// per 4 elements), or dW0's row and ds[n] (a workgroup per row n of G) -- and
+// for an unsplit G ds from its column tiles' partial sums (16 rows n per
+// workgroup, 16 lanes per row each summing every 16th part, joined in order).
 struct SumArgs {
   int32_t nprob;
   int32_t first[kMaxProb];  // first workgroup of each
   Prob p[kMaxProb];
 };
+
+static_assert(sizeof(BwdArgs) <= 4096 && sizeof(SumArgs) <= 4096, "kernel arguments");
+
+__device__ __forceinline__ f32x4 sum_slices(const Prob &p, int64_t n, int m) {
+  f32x4 s{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < p.ksplit; ++i)
+    s += *reinterpret_cast<const f32x4 *>(p.P + (static_cast<int64_t>(i) * p.N + n) * p.ldp + m);
+  return s;
+}
 
 __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
   int pi = 0;
@@ -441,14 +489,29 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
   const Prob &p = a.p[pi];
   const int64_t b = blockIdx.x - a.first[pi];
   const int q = p.ldp / 4;
+  if (p.ksplit == 1) {
+    const int c = threadIdx.x & 15, l = threadIdx.x >> 4;
+    const int64_t n = b * 16 + c;
+    float t = 0.f;
+    if (n < p.N)
+      for (int i = l; i < 2 * p.nM; i += 16) t += p.dsp[static_cast<int64_t>(i) * p.ldds + n];
+    __shared__ float part[16][17];
+    part[l][c] = t;
+    __syncthreads();
+    if (threadIdx.x < 16 && n < p.N) {
+      t = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t += part[i][c];
+      p.ds[n] = t;
+    }
+    return;
+  }
   if (p.mode == kBf16) {
     const int64_t id = b * 256 + threadIdx.x;
     if (id >= static_cast<int64_t>(p.N) * q) return;
     const int64_t n = id / q;
     const int m = static_cast<int>(id % q) * 4;
-    f32x4 s{0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < p.ksplit; ++i)
-      s += *reinterpret_cast<const f32x4 *>(p.P + (static_cast<int64_t>(i) * p.N + n) * p.ldp + m);
+    const f32x4 s = sum_slices(p, n, m);
     uint16_t *o = p.out + n * p.ldo + m;
     if (m + 4 <= p.M && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
       *reinterpret_cast<uint2 *>(o) = make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
@@ -462,18 +525,18 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
   const float sc = p.s[n];
   float t = 0.f;
   for (int c = threadIdx.x; c < q; c += 256) {
-    f32x4 s{0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < p.ksplit; ++i)
-      s += *reinterpret_cast<const f32x4 *>(p.P + (static_cast<int64_t>(i) * p.N + n) * p.ldp + c * 4);
+    const f32x4 s = sum_slices(p, n, c * 4);
     if (p.dw0) {
       f32x4 *d = reinterpret_cast<f32x4 *>(p.dw0 + n * p.M + c * 4);
       f32x4 o = s * sc;
       if (p.accumulate) o += *d;
       *d = o;
     }
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(p.W0 + n * p.M + c * 4);
-    t += s[0] * __uint_as_float(w[0] << 16) + s[1] * __uint_as_float(w[0] & 0xffff0000u) +
-         s[2] * __uint_as_float(w[1] << 16) + s[3] * __uint_as_float(w[1] & 0xffff0000u);
+    if (p.ds) {
+      const u32x2 w = *reinterpret_cast<const u32x2 *>(p.W0 + n * p.M + c * 4);
+      t += s[0] * __uint_as_float(w[0] << 16) + s[1] * __uint_as_float(w[0] & 0xffff0000u) +
+           s[2] * __uint_as_float(w[1] << 16) + s[3] * __uint_as_float(w[1] & 0xffff0000u);
+    }
   }
   if (!p.ds) return;
   __shared__ float part[4];
@@ -484,28 +547,10 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
   if (threadIdx.x == 0) p.ds[n] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// ds[n] = sum of the column tiles' partial sums: 16 rows n per workgroup, 16
-// lanes per row each summing every 16th part, joined in a fixed tree (one lane
-// per row took 18 us for 42 parts, a load latency each).
-__global__ __launch_bounds__(256) void sum_ds_kernel(const float *dsp, int parts, int ldds, int N, float *ds) {
-  const int n = blockIdx.x * 16 + (threadIdx.x & 15), l = threadIdx.x >> 4;
-  float t = 0.f;
-  if (n < N)
-    for (int i = l; i < parts; i += 16) t += dsp[static_cast<int64_t>(i) * ldds + n];
-  __shared__ float part[16][17];
-  part[l][threadIdx.x & 15] = t;
-  __syncthreads();
-  if (threadIdx.x < 16 && n < N) {
-    t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += part[i][threadIdx.x];
-    ds[n] = t;
-  }
-}
-
 // dy [T][ldy] -> rows of ldd columns in which every child's slot starts at a
 // multiple of 8 (zeros behind a slot's last column): the plain copy `dyp`
-// and/or dy (.) s rounded to bf16, `dys`.
+// and/or dy (.) s rounded to bf16, `dys`; and the checkpoint's values X (bf16
+// [T][K]).  One launch: the first dyb workgroups in y take dy, the others X.
 struct PrepArgs {
   const uint16_t *dy;
   int32_t T, ldy, ldd, nslot;
@@ -514,12 +559,26 @@ struct PrepArgs {
   int32_t n[kMaxChildren];          // slot -> columns
   const float *s[kMaxChildren];
   uint16_t *dyp, *dys;
+  int32_t dyb;
+  CodedView xc;
+  int32_t K;
+  uint16_t *X;
 };
 
 // A thread takes 8 columns of kPrepT tokens: s is read once for all of them.
 constexpr int kPrepT = 4;
 
-__global__ __launch_bounds__(256) void prep_dy_kernel(PrepArgs a) {
+__global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
+  if (static_cast<int>(blockIdx.y) >= a.dyb) {
+    const int k = ((blockIdx.y - a.dyb) * 256 + threadIdx.x) * 8;
+    if (k >= a.K) return;
+#pragma unroll
+    for (int i = 0; i < kPrepT; ++i) {
+      const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepT + i;
+      if (t < a.T) *reinterpret_cast<u32x4 *>(a.X + t * a.K + k) = expand8(a.xc, t, k);
+    }
+    return;
+  }
   const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
   if (c >= a.ldd) return;
   int i = 0;
@@ -581,52 +640,109 @@ hipError_t launch_zero(void *p, int64_t halves, hipStream_t stream) {
 
 // ---- host side --------------------------------------------------------------
 
-// Stage depth by the operands: k-column rows are long whatever the depth, so
-// four shallow stages keep more loads in flight; a k-row operand wants whole
-// 128-byte lines (with 64-byte rows a plain load loop ran at 57 KB/us per CU
-// instead of 92).
+// 256 x 256 tiles, a launch per kind.  Stage depth by the operands: k-column
+// rows are long whatever the depth, so four shallow stages keep more loads in
+// flight; a k-row operand wants whole 128-byte lines (with 64-byte rows a bare
+// load loop ran at 57 KB/us per CU instead of 92).
 template <bool ATR, bool BTR>
-struct Shapes {
-  static constexpr bool kCols = ATR && BTR;
-  using Big = std::conditional_t<kCols, BTile<256, 256, 2, 4, 32, 4>, BTile<256, 256, 2, 4, 64, 2>>;
-  using Mid = std::conditional_t<kCols, BTile<128, 128, 2, 4, 32, 5>, BTile<128, 128, 2, 4, 64, 2>>;
-  using Thin = std::conditional_t<kCols, BTile<64, 128, 2, 2, 32, 6>, BTile<64, 128, 2, 2, 64, 3>>;
-};
-constexpr int kShapes = 3;
-constexpr struct {
-  int BM, BN, WM;
-  double step;  // us of one contraction step of a workgroup
-} kShape[kShapes] = {{256, 256, 2, 1.6}, {128, 128, 2, 0.6}, {64, 128, 2, 0.5}};
+using Big = std::conditional_t<ATR && BTR, BTile<256, 256, 2, 4, 32, 4>, BTile<256, 256, 2, 4, 64, 2>>;
+// 128 x 128 tiles, every kind in one launch: with a ring of two stages two
+// workgroups share a CU, with four one keeps as many loads in flight.
+using Mid2 = BTile<128, 128, 2, 4, 64, 2>;
+using Mid4 = BTile<128, 128, 2, 4, 64, 4>;
 
 struct BPlan {
-  int shape, ksplit, per, nM, nN;
+  bool big;
+  int ksplit, per, nM, nN;
   size_t partial_bytes(int M, int N) const {
     return ksplit > 1 ? (static_cast<size_t>(ksplit) * N * ((M + 3) & ~3) * 4 + 255) & ~size_t{255} : 0;
   }
 };
 
-// Tile shape and split of one product: the smallest estimated time, rounds of
-// workgroups over the CUs times the steps of one, plus writing, reading and
-// launching the sum of the partials when the contraction is split.
-BPlan plan_product(int M, int N, int steps) {
-  BPlan best{};
-  double best_us = 1e300;
-  for (int i = 0; i < kShapes; ++i) {
-    const int nM = (M + kShape[i].BM - 1) / kShape[i].BM, nN = (N + kShape[i].BN - 1) / kShape[i].BN;
-    const int64_t tiles = static_cast<int64_t>(nM) * nN;
-    for (int ks = 1; ks <= 32 && (ks == 1 || ks * 2 <= steps); ++ks) {
-      const int per = (steps + ks - 1) / ks;
-      if ((ks - 1) * per >= steps) continue;  // an empty slice
-      const double rounds = static_cast<double>((tiles * ks + kCUs - 1) / kCUs);
-      double us = rounds * (per + 3) * kShape[i].step;
-      if (ks > 1) us += 4.0 + 2.0 * ks * static_cast<double>(N) * M * 4 / 3e6;
-      if (us < best_us) {
-        best_us = us;
-        best = BPlan{i, ks, per, nM, nN};
+// A product as the planner sees it: extents and contraction steps.
+struct Item {
+  int M, N, steps;
+};
+
+// Microseconds (fitted to the 31B and 1B shapes): a step and the fixed part of
+// a 256 x 256 workgroup, of a 128 x 128 workgroup alone on its CU and of one
+// of two that share it; bytes per us of the partials' way out and back.
+constexpr double kBigStep = 1.7, kBigFix = 10.0;
+constexpr double kMidStep = 0.6, kMidPairStep = 1.0, kMidFix = 4.0;
+constexpr double kSumFix = 4.0, kPartialRate = 3e6;
+
+double split_cost(int ks, int M, int N) { return ks > 1 ? 2.0 * ks * static_cast<double>(N) * M * 4 / kPartialRate : 0.0; }
+
+// Tiles and splits of the products that run together.  A product takes big
+// tiles when its best estimate alone on the chip beats 128 x 128 tiles'
+// throughput; the others share a launch and are cut into slices of at most
+// `len` steps each, for the len with the least estimated time (the longest
+// workgroup, or all of them over the CUs).
+void plan_batch(const Item *it, int n, BPlan *out) {
+  auto split = [](int steps, int ks, BPlan &p) {
+    p.per = std::max(1, (steps + ks - 1) / ks);
+    p.ksplit = std::max(1, (steps + p.per - 1) / p.per);
+  };
+  bool any_mid = false;
+  for (int i = 0; i < n; ++i) {
+    BPlan &p = out[i];
+    p.nM = (it[i].M + 255) / 256;
+    p.nN = (it[i].N + 255) / 256;
+    const int64_t tiles = static_cast<int64_t>(p.nM) * p.nN;
+    double best = 1e300;
+    for (int ks = 1; ks <= 8 && ks * 8 <= std::max(8, it[i].steps); ++ks) {
+      BPlan q{};
+      split(it[i].steps, ks, q);
+      const double rounds = static_cast<double>((tiles * q.ksplit + kCUs - 1) / kCUs);
+      const double us = rounds * (q.per * kBigStep + kBigFix) + split_cost(q.ksplit, it[i].M, it[i].N) +
+                        (q.ksplit > 1 ? kSumFix : 0.0);
+      if (us < best) {
+        best = us;
+        p.per = q.per;
+        p.ksplit = q.ksplit;
       }
     }
+    const int mM = (it[i].M + 127) / 128, mN = (it[i].N + 127) / 128;
+    p.big = best < static_cast<double>(mM) * mN * (it[i].steps * kMidPairStep + kMidFix) / (2 * kCUs) &&
+            tiles * p.ksplit * 2 >= kCUs;
+    if (!p.big) {
+      p.nM = mM;
+      p.nN = mN;
+      any_mid = true;
+    }
   }
-  return best;
+  if (!any_mid) return;
+  double best = 1e300;
+  int best_len = 1 << 30;
+  for (int len : {4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 1 << 20}) {
+    double units = 0, work = 0, longest = 0, extra = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      const double step = pass && units > kCUs ? kMidPairStep : kMidStep;
+      if (pass) work = longest = 0;
+      for (int i = 0; i < n; ++i) {
+        if (out[i].big) continue;
+        BPlan q{};
+        split(it[i].steps, std::clamp((it[i].steps + len - 1) / len, 1, 16), q);
+        const double cnt = static_cast<double>(out[i].nM) * out[i].nN * q.ksplit, us = q.per * step + kMidFix;
+        if (!pass) {
+          units += cnt;
+          extra += split_cost(q.ksplit, it[i].M, it[i].N);
+          if (q.ksplit > 1 && extra < kSumFix) extra += kSumFix;
+        } else {
+          work += cnt * us;
+          longest = std::max(longest, us);
+        }
+      }
+    }
+    const double slots = units > kCUs ? 2.0 * kCUs : kCUs;
+    const double us = (units <= slots ? longest : std::max(longest, work / slots) + 0.5 * longest) + extra;
+    if (us < best) {
+      best = us;
+      best_len = len;
+    }
+  }
+  for (int i = 0; i < n; ++i)
+    if (!out[i].big) split(it[i].steps, std::clamp((it[i].steps + best_len - 1) / best_len, 1, 16), out[i]);
 }
 
 int steps_of(int64_t len) { return static_cast<int>((len + kStep - 1) / kStep); }
@@ -665,19 +781,57 @@ int slots_of_child(const Slots &s, int child) {
   return n;
 }
 
-int dx_steps(const Slots &s, int Rz) {
-  int n = steps_of(Rz);
-  for (int i = 0; i < s.n; ++i) n += steps_of(s.cols[i]);
-  return n;
+// The two batches of a call, planned as if every gradient were wanted (so that
+// asking for fewer changes no bits): z and every g; then dx and every child's
+// G, dU and dV.  A product of extent 0 (no rank) keeps its place.
+struct Plans {
+  BPlan z, g[kMaxChildren], dx, G[kMaxChildren], du[kMaxChildren], dv[kMaxChildren];
+  size_t part;  // bytes of the larger batch's partials
+};
+
+Plans plans_of(const CallDesc &c, const Slots &s, int T) {
+  Plans p{};
+  Item it[kMaxProb];
+  BPlan *to[kMaxProb], got[kMaxProb];
+  int n = 0;
+  auto add = [&](int M, int N, int steps, BPlan &dst) {
+    if (M == 0) return;
+    it[n] = Item{M, N, steps};
+    to[n++] = &dst;
+  };
+  auto done = [&] {
+    plan_batch(it, n, got);
+    size_t bytes = 0;
+    for (int i = 0; i < n; ++i) {
+      *to[i] = got[i];
+      bytes += got[i].partial_bytes(it[i].M, it[i].N);
+    }
+    p.part = std::max(p.part, bytes);
+    n = 0;
+  };
+  add(c.Rz, T, steps_of(c.K), p.z);
+  for (int i = 0; i < c.nchild; ++i) add(c.ch[i].rpad, T, slots_of_child(s, i) * steps_of(c.ch[i].N), p.g[i]);
+  done();
+  int dx_steps = steps_of(c.Rz);
+  for (int i = 0; i < s.n; ++i) dx_steps += steps_of(s.cols[i]);
+  add(c.K, T, dx_steps, p.dx);
+  for (int i = 0; i < c.nchild; ++i) {
+    const int steps = slots_of_child(s, i) * steps_of(T);
+    add(c.K, c.ch[i].N, steps, p.G[i]);
+    add(c.ch[i].rpad, c.ch[i].N, steps, p.du[i]);
+    add(c.ch[i].rpad, c.K, steps_of(T), p.dv[i]);
+  }
+  done();
+  return p;
 }
 
 // Workspace: X bf16 [T][K], dy copies [T][ldd] x 2, z and g [T][Rz], the ds
-// partial sums, and the K-split partials of every product.
+// partial sums, and the K-split partials of a batch.
 struct Offsets {
   size_t x, dyp, dys, z, g, dsp, part, bytes;
 };
 
-Offsets offsets_of(const CallDesc &c, const Slots &s, int T) {
+Offsets offsets_of(const CallDesc &c, const Slots &s, const Plans &p, int T) {
   Offsets o{};
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -690,74 +844,73 @@ Offsets offsets_of(const CallDesc &c, const Slots &s, int T) {
   o.dys = take(static_cast<size_t>(T) * s.ldd * 2);
   o.z = take(static_cast<size_t>(T) * c.Rz * 2);
   o.g = take(static_cast<size_t>(T) * c.Rz * 2);
-  o.dsp = take(static_cast<size_t>((c.K + 63) / 64) * 2 * c.Ntot * 4);
-  // the products of one launch have partials of their own; launches reuse them
-  size_t zg = 0, tt = 0;
-  if (c.Rz > 0) zg = plan_product(c.Rz, T, steps_of(c.K)).partial_bytes(c.Rz, T);
-  for (int i = 0; i < c.nchild; ++i) {
-    const ChildDesc &ch = c.ch[i];
-    const int ns = slots_of_child(s, i);
-    if (ch.rpad) {
-      zg += plan_product(ch.rpad, T, ns * steps_of(ch.N)).partial_bytes(ch.rpad, T);
-      tt += plan_product(ch.rpad, ch.N, ns * steps_of(T)).partial_bytes(ch.rpad, ch.N);
-      tt += plan_product(ch.rpad, c.K, steps_of(T)).partial_bytes(ch.rpad, c.K);
-    }
-    tt += plan_product(c.K, ch.N, ns * steps_of(T)).partial_bytes(c.K, ch.N);
-  }
-  const size_t dx = plan_product(c.K, T, dx_steps(s, c.Rz)).partial_bytes(c.K, T);
-  o.part = take(std::max({zg, tt, dx}));
+  o.dsp = take(static_cast<size_t>((c.K + 127) / 128) * 2 * c.Ntot * 4);
+  o.part = take(p.part);
   o.bytes = at;
   return o;
 }
 
-// Products of one kind that run together; one launch per tile shape they use.
+// Products that run together.
 struct Batch {
   int n = 0;
   Prob p[kMaxProb];
-  int shape[kMaxProb];
+  bool big[kMaxProb];
 };
 
-template <typename TL, bool ATR, bool BTR>
-hipError_t launch_shape(const BwdArgs &a, hipStream_t stream) {
-  const hipError_t e = ensure_lds<product_kernel<TL, ATR, BTR>>(TL::LDS);
+template <typename TL, auto KERN>
+hipError_t launch_kernel(const BwdArgs &a, hipStream_t stream) {
+  const hipError_t e = ensure_lds<KERN>(TL::LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((product_kernel<TL, ATR, BTR>), dim3(a.total), dim3(TL::NW * 64), TL::LDS, stream, a);
+  hipLaunchKernelGGL(KERN, dim3(a.total), dim3(TL::NW * 64), TL::LDS, stream, a);
   return hipGetLastError();
 }
 
 template <bool ATR, bool BTR>
-hipError_t launch_batch(const Batch &b, hipStream_t stream) {
-  for (int sh = 0; sh < kShapes; ++sh) {
-    BwdArgs a{};
-    for (int i = 0; i < b.n; ++i) {
-      if (b.shape[i] != sh) continue;
-      Prob &p = a.p[a.nprob++];
-      p = b.p[i];
-      p.unit0 = a.total;
-      a.total += p.nM * p.nN * p.ksplit;
-    }
-    if (!a.nprob) continue;
-    using S = Shapes<ATR, BTR>;
-    const hipError_t e = sh == 0   ? launch_shape<typename S::Big, ATR, BTR>(a, stream)
-                         : sh == 1 ? launch_shape<typename S::Mid, ATR, BTR>(a, stream)
-                                   : launch_shape<typename S::Thin, ATR, BTR>(a, stream);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+hipError_t launch_big(const BwdArgs &a, hipStream_t stream) {
+  return launch_kernel<Big<ATR, BTR>, product_kernel<Big<ATR, BTR>, ATR, BTR>>(a, stream);
 }
 
-// The sums of a batch's split products.
-hipError_t launch_sums(const Batch &b, hipStream_t stream) {
+void add_units(BwdArgs &a, const Prob &p) {
+  a.p[a.nprob] = p;
+  a.p[a.nprob++].unit0 = a.total;
+  a.total += p.nM * p.nN * p.ksplit;
+}
+
+// The products of a batch -- big tiles by kind, then all others, the longest
+// workgroups first -- and the launch that sums what they left.
+hipError_t launch_batch(const Batch &b, hipStream_t stream) {
+  hipError_t e;
+  for (int kind = kRowsRows; kind <= kColsCols; ++kind) {
+    BwdArgs a{};
+    for (int i = 0; i < b.n; ++i)
+      if (b.big[i] && b.p[i].kind == kind) add_units(a, b.p[i]);
+    if (!a.nprob) continue;
+    e = kind == kColsCols   ? launch_big<true, true>(a, stream)
+        : kind == kColsRows ? launch_big<true, false>(a, stream)
+                            : launch_big<false, false>(a, stream);
+    if (e != hipSuccess) return e;
+  }
+  int order[kMaxProb], nmid = 0;
+  for (int i = 0; i < b.n; ++i)
+    if (!b.big[i]) order[nmid++] = i;
+  std::stable_sort(order, order + nmid, [&](int x, int y) { return b.p[x].per > b.p[y].per; });
+  if (nmid) {
+    BwdArgs a{};
+    for (int i = 0; i < nmid; ++i) add_units(a, b.p[order[i]]);
+    e = a.total > kCUs ? launch_kernel<Mid2, products_kernel<Mid2>>(a, stream)
+                       : launch_kernel<Mid4, products_kernel<Mid4>>(a, stream);
+    if (e != hipSuccess) return e;
+  }
   SumArgs a{};
   int blocks = 0;
   for (int i = 0; i < b.n; ++i) {
-    if (b.p[i].ksplit == 1) continue;
+    const Prob &p = b.p[i];
+    if (p.ksplit == 1 && !(p.mode == kWeight && p.ds)) continue;
     a.first[a.nprob] = blocks;
-    a.p[a.nprob] = b.p[i];
-    blocks += b.p[i].mode == kWeight
-                  ? b.p[i].N
-                  : static_cast<int>((static_cast<int64_t>(b.p[i].N) * (b.p[i].ldp / 4) + 255) / 256);
-    ++a.nprob;
+    a.p[a.nprob++] = p;
+    blocks += p.ksplit == 1       ? (p.N + 15) / 16
+              : p.mode == kWeight ? p.N
+                                  : static_cast<int>((static_cast<int64_t>(p.N) * (p.ldp / 4) + 255) / 256);
   }
   if (!a.nprob) return hipSuccess;
   hipLaunchKernelGGL(sum_kernel, dim3(blocks), dim3(256), 0, stream, a);
@@ -765,13 +918,14 @@ hipError_t launch_sums(const Batch &b, hipStream_t stream) {
 }
 
 // Add a product to a batch; returns it for its segments and epilogue.  Its
-// partials are taken from `part`.  Mp >= M (M or the padded rank) is the
-// extent the workspace was sized for: the plan goes by it.
-Prob &add_product(Batch &b, int M, int Mp, int N, int steps, uint16_t *out, int64_t ldo, uint8_t *&part) {
-  const BPlan pl = plan_product(Mp, N, steps);
-  Prob &p = b.p[b.n];
+// partials, sized for the planned extent Mp >= M (the padded rank), come from
+// `part`.
+Prob &add_product(Batch &b, const BPlan &pl, Kind kind, int M, int Mp, int N, uint16_t *out, int64_t ldo,
+                  uint8_t *&part) {
+  b.big[b.n] = pl.big;
+  Prob &p = b.p[b.n++];
   p = Prob{};
-  b.shape[b.n++] = pl.shape;
+  p.kind = kind;
   p.M = M;
   p.N = N;
   p.nM = pl.nM;
@@ -792,16 +946,14 @@ void add_seg(Prob &p, const uint16_t *A, int64_t lda, const uint16_t *B, int64_t
 
 }  // namespace
 
-size_t backward_workspace_bytes(const CallDesc &c, int T) { return offsets_of(c, slots_of(c), T).bytes; }
-
-int backward_dy_columns(const CallDesc &c) { return slots_of(c).ldy; }
+size_t backward_workspace_bytes(const CallDesc &c, int T) {
+  const Slots s = slots_of(c);
+  return offsets_of(c, s, plans_of(c, s, T), T).bytes;
+}
 
 hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_t *dy, const GradOut &o, void *ws_,
                            hipStream_t stream) {
   const int T = c.T, K = c.K;
-  const Slots s = slots_of(c);
-  uint8_t *ws = static_cast<uint8_t *>(ws_);
-  const Offsets at = offsets_of(c, s, T);
   hipError_t e;
   bool want_u = false, want_v = false;
   for (int i = 0; i < c.nchild; ++i) {
@@ -820,6 +972,10 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     return hipSuccess;
   }
 
+  const Slots s = slots_of(c);
+  const Plans pl = plans_of(c, s, T);
+  uint8_t *ws = static_cast<uint8_t *>(ws_);
+  const Offsets at = offsets_of(c, s, pl, T);
   uint16_t *X = reinterpret_cast<uint16_t *>(ws + at.x);
   uint16_t *z = reinterpret_cast<uint16_t *>(ws + at.z), *g = reinterpret_cast<uint16_t *>(ws + at.g);
   uint16_t *dys = reinterpret_cast<uint16_t *>(ws + at.dys);
@@ -828,11 +984,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
   const bool direct = s.even && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
   const uint16_t *dyp = direct ? dy : reinterpret_cast<const uint16_t *>(ws + at.dyp);
   const int64_t ldp = direct ? s.ldy : s.ldd;
-  if (want_u || want_v || want_w) {
-    e = launch_expand_act(xc, T, X, K, stream);
-    if (e != hipSuccess) return e;
-  }
-  if (o.dx || !direct) {
+  {
     PrepArgs a{};
     a.dy = dy;
     a.T = T;
@@ -848,84 +1000,73 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     a.start[s.n] = s.ldd;
     a.dyp = direct ? nullptr : reinterpret_cast<uint16_t *>(ws + at.dyp);
     a.dys = o.dx ? dys : nullptr;
-    hipLaunchKernelGGL(prep_dy_kernel, dim3((T + kPrepT - 1) / kPrepT, (s.ldd / 8 + 255) / 256), dim3(256), 0, stream, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  // z = X V and g = dy U
-  uint8_t *part = ws + at.part;
-  Batch zb{}, gb{};
-  if (want_u) {
-    Prob &p = add_product(zb, c.Rz, c.Rz, T, steps_of(K), z, c.Rz, part);
-    add_seg(p, c.Vt, K, X, K, K);
-  }
-  if (want_g)
-    for (int i = 0; i < c.nchild; ++i) {
-      const ChildDesc &ch = c.ch[i];
-      if (!ch.rpad) continue;
-      Prob &p = add_product(gb, ch.rpad, ch.rpad, T, slots_of_child(s, i) * steps_of(ch.N), g + ch.zoff, c.Rz, part);
-      for (int j = 0; j < s.n; ++j)
-        if (s.child[j] == i) add_seg(p, ch.U, ch.rpad, dyp + (direct ? s.from[j] : s.start[j]), ldp, ch.N);
+    a.dyb = o.dx || !direct ? (s.ldd / 8 + 255) / 256 : 0;
+    a.xc = xc;
+    a.K = K;
+    a.X = X;
+    const int xb = want_u || want_v || want_w ? (K / 8 + 255) / 256 : 0;
+    if (a.dyb + xb > 0) {
+      hipLaunchKernelGGL(prepare_kernel, dim3((T + kPrepT - 1) / kPrepT, a.dyb + xb), dim3(256), 0, stream, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-  if ((e = launch_batch<false, false>(zb, stream)) != hipSuccess) return e;
-  if ((e = launch_batch<true, false>(gb, stream)) != hipSuccess) return e;
-  for (int i = 0; i < gb.n; ++i) zb.p[zb.n++] = gb.p[i];
-  if ((e = launch_sums(zb, stream)) != hipSuccess) return e;
-  // dx = (dy (.) s) W0 + g V^T
+  }
+  auto column = [&](int slot) { return dyp + (direct ? s.from[slot] : s.start[slot]); };
+  {
+    // z = X V and g = dy U
+    uint8_t *part = ws + at.part;
+    Batch b;
+    if (want_u) {
+      Prob &p = add_product(b, pl.z, kRowsRows, c.Rz, c.Rz, T, z, c.Rz, part);
+      add_seg(p, c.Vt, K, X, K, K);
+    }
+    if (want_g)
+      for (int i = 0; i < c.nchild; ++i) {
+        const ChildDesc &ch = c.ch[i];
+        if (!ch.rpad) continue;
+        Prob &p = add_product(b, pl.g[i], kColsRows, ch.rpad, ch.rpad, T, g + ch.zoff, c.Rz, part);
+        for (int j = 0; j < s.n; ++j)
+          if (s.child[j] == i) add_seg(p, ch.U, ch.rpad, column(j), ldp, ch.N);
+      }
+    if ((e = launch_batch(b, stream)) != hipSuccess) return e;
+  }
+  uint8_t *part = ws + at.part;
+  Batch b;
   if (o.dx) {
-    part = ws + at.part;
-    Batch b{};
-    Prob &p = add_product(b, K, K, T, dx_steps(s, c.Rz), o.dx, K, part);
+    // dx = (dy (.) s) W0 + g V^T
+    Prob &p = add_product(b, pl.dx, kColsRows, K, K, T, o.dx, K, part);
     for (int j = 0; j < s.n; ++j)
       add_seg(p, c.W0 + static_cast<int64_t>(c.ch[s.child[j]].row_start) * K, K, dys + s.start[j], s.ldd, s.cols[j]);
     if (c.Rz > 0) add_seg(p, c.Vt, K, g, c.Rz, c.Rz);
-    if ((e = launch_batch<true, false>(b, stream)) != hipSuccess) return e;
-    if ((e = launch_sums(b, stream)) != hipSuccess) return e;
   }
-  // G (dW0 and ds), dU and dV: contractions over the tokens
-  if (want_w || want_u || want_v) {
-    part = ws + at.part;
-    float *dsp = reinterpret_cast<float *>(ws + at.dsp);
-    Batch b{};
-    for (int i = 0; i < c.nchild; ++i) {
-      const ChildDesc &ch = c.ch[i];
-      const int ns = slots_of_child(s, i);
-      auto add_tokens = [&](Prob &p, const uint16_t *A, int64_t lda) {
-        for (int j = 0; j < s.n; ++j)
-          if (s.child[j] == i) add_seg(p, A, lda, dyp + (direct ? s.from[j] : s.start[j]), ldp, T);
-      };
-      if (want_w) {
-        Prob &p = add_product(b, K, K, ch.N, ns * steps_of(T), nullptr, 0, part);
-        add_tokens(p, X, K);
-        p.mode = kWeight;
-        p.s = c.s + ch.row_start;
-        p.W0 = c.W0 + static_cast<int64_t>(ch.row_start) * K;
-        p.dw0 = o.dw0 ? o.dw0 + static_cast<int64_t>(ch.row_start) * K : nullptr;
-        p.accumulate = o.dw0 ? o.accumulate : 0;
-        p.ds = o.ds ? o.ds + ch.row_start : nullptr;
-        p.dsp = o.ds ? dsp + ch.row_start : nullptr;
-        p.ldds = c.Ntot;
-      }
-      if (o.du[i] && o.r[i]) {
-        Prob &p = add_product(b, o.r[i], ch.rpad, ch.N, ns * steps_of(T), o.du[i], o.r[i], part);
-        add_tokens(p, z + ch.zoff, c.Rz);
-      }
-      if (o.dv[i] && o.r[i]) {
-        Prob &p = add_product(b, o.r[i], ch.rpad, K, steps_of(T), o.dv[i], o.r[i], part);
-        add_seg(p, g + ch.zoff, c.Rz, X, K, T);
-      }
+  for (int i = 0; i < c.nchild; ++i) {
+    // G (dW0 and ds), dU and dV: contractions over the tokens
+    const ChildDesc &ch = c.ch[i];
+    auto add_tokens = [&](Prob &p, const uint16_t *A, int64_t lda) {
+      for (int j = 0; j < s.n; ++j)
+        if (s.child[j] == i) add_seg(p, A, lda, column(j), ldp, T);
+    };
+    if (want_w) {
+      Prob &p = add_product(b, pl.G[i], kColsCols, K, K, ch.N, nullptr, 0, part);
+      add_tokens(p, X, K);
+      p.mode = kWeight;
+      p.s = c.s + ch.row_start;
+      p.W0 = c.W0 + static_cast<int64_t>(ch.row_start) * K;
+      p.dw0 = o.dw0 ? o.dw0 + static_cast<int64_t>(ch.row_start) * K : nullptr;
+      p.accumulate = o.dw0 ? o.accumulate : 0;
+      p.ds = o.ds ? o.ds + ch.row_start : nullptr;
+      p.dsp = reinterpret_cast<float *>(ws + at.dsp) + ch.row_start;
+      p.ldds = c.Ntot;
     }
-    if ((e = launch_batch<true, true>(b, stream)) != hipSuccess) return e;
-    if ((e = launch_sums(b, stream)) != hipSuccess) return e;
-    if (o.ds)
-      for (int i = 0; i < b.n; ++i) {
-        const Prob &p = b.p[i];
-        if (p.mode != kWeight || p.ksplit > 1) continue;
-        hipLaunchKernelGGL(sum_ds_kernel, dim3((p.N + 15) / 16), dim3(256), 0, stream,
-                           static_cast<const float *>(p.dsp), p.nM * kShape[b.shape[i]].WM, p.ldds, p.N, p.ds);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-      }
+    if (o.du[i] && o.r[i]) {
+      Prob &p = add_product(b, pl.du[i], kColsCols, o.r[i], ch.rpad, ch.N, o.du[i], o.r[i], part);
+      add_tokens(p, z + ch.zoff, c.Rz);
+    }
+    if (o.dv[i] && o.r[i]) {
+      Prob &p = add_product(b, pl.dv[i], kColsCols, o.r[i], ch.rpad, K, o.dv[i], o.r[i], part);
+      add_seg(p, g + ch.zoff, c.Rz, X, K, T);
+    }
   }
-  return hipSuccess;
+  return launch_batch(b, stream);
 }
 
 }  // namespace wl

@@ -1,0 +1,27 @@
+// Device access to 8-bit coded activations (coded.hip describes the coding).
+#pragma once
+
+#include "common.h"
+#include "internal.h"
+
+namespace wl {
+
+constexpr int kCodeBlock = 128;
+
+// Elements k .. k + 7 (k % 8 == 0) of row t: code * 2^e as bf16, exact.
+__device__ __forceinline__ u32x4 expand8(const CodedView &c, int64_t t, int k) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 v = *reinterpret_cast<const u32x2 *>(c.codes + t * (c.nb * kCodeBlock) + k);
+  const float f = __uint_as_float(static_cast<uint32_t>(c.scales[static_cast<int64_t>(k / kCodeBlock) * c.ldsc + t]) << 23);
+  u32x4 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), false);
+    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), true);
+    o[2 * h] = f32_to_bf16(a[0] * f) | (static_cast<uint32_t>(f32_to_bf16(a[1] * f)) << 16);
+    o[2 * h + 1] = f32_to_bf16(b[0] * f) | (static_cast<uint32_t>(f32_to_bf16(b[1] * f)) << 16);
+  }
+  return o;
+}
+
+}  // namespace wl

@@ -30,6 +30,7 @@
 // instructions would add exactly at half the rate.
 #include <algorithm>
 
+#include "coded.h"
 #include "common.h"
 #include "internal.h"
 #include "lds_dma.h"
@@ -41,7 +42,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kBlk = 128;
+constexpr int kBlk = kCodeBlock;
 constexpr int kCUs = 256;
 
 // D += 2^(sa-127) 2^(sb-127) A B for a 16 x 16 tile over 128 k of E4M3 codes.
@@ -180,24 +181,11 @@ __global__ __launch_bounds__(256) void encode_weight_kernel(const uint16_t *w, i
 // x[t][k] = code * 2^e as bf16 (exact), 8 elements per thread; ldx >= K
 // columns per row, those at k >= K (up to Kq) written only if ldx covers them
 // (their codes are zero).
-__global__ __launch_bounds__(256) void expand_act_kernel(const uint8_t *codes, const uint8_t *scales, int ldsc, int T,
-                                                         int nb, uint16_t *x, int ldx) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const int c = blockIdx.y * 256 + threadIdx.x;  // 8-element chunk of the row
+__global__ __launch_bounds__(256) void expand_act_kernel(CodedView c, uint16_t *x, int ldx) {
+  const int k = (blockIdx.y * 256 + threadIdx.x) * 8;
   const int64_t tok = blockIdx.x;
-  const int k = c * 8;
-  if (k >= nb * kBlk || k >= ldx) return;
-  const u32x2 v = *reinterpret_cast<const u32x2 *>(codes + tok * (nb * kBlk) + k);
-  const float f = __uint_as_float(static_cast<uint32_t>(scales[static_cast<int64_t>(k / kBlk) * ldsc + tok]) << 23);
-  u32x4 o;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), false);
-    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), true);
-    o[2 * h] = f32_to_bf16(a[0] * f) | (static_cast<uint32_t>(f32_to_bf16(a[1] * f)) << 16);
-    o[2 * h + 1] = f32_to_bf16(b[0] * f) | (static_cast<uint32_t>(f32_to_bf16(b[1] * f)) << 16);
-  }
-  *reinterpret_cast<u32x4 *>(x + tok * ldx + k) = o;
+  if (k >= c.nb * kBlk || k >= ldx) return;
+  *reinterpret_cast<u32x4 *>(x + tok * ldx + k) = expand8(c, tok, k);
 }
 
 struct CodedArgs {
@@ -505,7 +493,7 @@ hipError_t launch_encode_weight(const uint16_t *w, int N, int K, const CodedView
 
 hipError_t launch_expand_act(const CodedView &c, int T, uint16_t *x, int ldx, hipStream_t stream) {
   const dim3 grid(T, (c.nb * (kBlk / 8) + 255) / 256);
-  hipLaunchKernelGGL(expand_act_kernel, grid, dim3(256), 0, stream, c.codes, c.scales, c.ldsc, T, c.nb, x, ldx);
+  hipLaunchKernelGGL(expand_act_kernel, grid, dim3(256), 0, stream, c, x, ldx);
   return hipGetLastError();
 }
 

@@ -121,7 +121,6 @@ struct GradOut {
   int32_t accumulate;           // dw0 is added to
 };
 size_t backward_workspace_bytes(const CallDesc &c, int T);
-int backward_dy_columns(const CallDesc &c);
 hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_t *dy, const GradOut &o, void *ws,
                            hipStream_t stream);
 
