@@ -106,6 +106,11 @@ struct BwdArgs {
 // A lane's place in a load is a per-lane part (kept in two registers) and a
 // part of the instruction's number, so the addresses of the loads cost no
 // registers of their own.
+// A uniform value held in a scalar register: without it the compiler loads a
+// kernel argument again at every use, and a scalar load in the loop makes the
+// next use wait for every LDS read in flight (they share a counter).
+__device__ __forceinline__ int keep(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 template <int W, bool TR, int BK>
 struct Operand {
   static constexpr int READS = TR ? 2 : 1;          // LDS reads of a fragment
@@ -116,11 +121,13 @@ struct Operand {
   int lrow, chunk;   // this lane's row of a load and its chunk, without the instruction's swizzle
   uint32_t lo;       // byte offset of lrow's start
   int rd;            // fragment reads: byte offset of the lane's first row
+  int sq;            // bytes from a load instruction's rows to the next's (uniform)
 
   // mw: the wave's first row of the tile
   __device__ __forceinline__ Operand(int lane, int64_t ld, int mw) {
     const int r16 = lane & 15, g = lane >> 4;
     lrow = lane / CPR;
+    sq = keep(static_cast<int>(RPQ * ld * 2));
     lo = static_cast<uint32_t>(lrow * ld * 2);
     const int slot = lane % CPR;
     if constexpr (TR) {
@@ -140,11 +147,11 @@ struct Operand {
   }
   // Load instruction q of a stage at `base`; lim rows (k-rows) or columns
   // (k-columns) of the tile exist, `left` values of the contraction.
-  __device__ __forceinline__ void load(const uint16_t *base, int q, int64_t ld, int lim, int left, lds_u8 *dst) const {
+  __device__ __forceinline__ void load(const uint16_t *base, int q, int lim, int left, lds_u8 *dst) const {
     const int c = chunk ^ sw_of(q), row = q * RPQ + lrow;
     const bool in = TR ? c * 8 < lim && row < left : row < lim && c * 8 < left;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_rsrc(base), (lds_void *)(dst + q * 1024), 16,
-                                             in ? lo + c * 16 : kBufNoRow, static_cast<int>(q * RPQ * ld * 2), 0, 0);
+                                             in ? lo + c * 16 : kBufNoRow, q * sq, 0, 0);
   }
   static __device__ __forceinline__ const uint16_t *base(const uint16_t *p, int64_t ld, int m0, int k) {
     return TR ? p + k * ld + m0 : p + m0 * ld + k;
@@ -167,15 +174,18 @@ struct Operand {
   }
 };
 
-// Scheduling of a region with M MFMAs and R LDS reads: the reads spread evenly
-// among the MFMAs (they feed the next region, so none has to come first).
-template <int M, int R>
+// Scheduling of a pipeline step of M MFMAs, R LDS reads and V loads into LDS:
+// MFMAs first (their operands are there), the reads and loads -- for later
+// steps -- spread among them, with the address arithmetic two at a time.
+template <int M, int R, int V>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
-    constexpr int per = M / R > 0 ? M / R : 1;
-    __builtin_amdgcn_sched_group_barrier(0x008, per, 0);  // MFMAs
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+    if ((i + 1) * V / M > i * V / M) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // one load
+#pragma unroll
+    for (int k = i * R / M; k < (i + 1) * R / M; ++k) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+    __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // VALU
   }
 }
 
@@ -259,15 +269,15 @@ enum Part : int { kAll = 0, kFirst = 1, kLast = 2 };
 
 template <typename TL, Part PART, typename OA, typename OB>
 __device__ __forceinline__ void load_stage(const OA &oa, const OB &ob, const uint16_t *pa, const uint16_t *pb,
-                                           int64_t lda, int64_t ldb, int lima, int limb, int left, int wave,
+                                           int lima, int limb, int left, int wave,
                                            lds_u8 *w) {
   if constexpr (PART != kLast) {
 #pragma unroll
-    for (int q = 0; q < TL::LA; ++q) oa.load(pa, wave * TL::LA + q, lda, lima, left, w);
+    for (int q = 0; q < TL::LA; ++q) oa.load(pa, wave * TL::LA + q, lima, left, w);
   }
 #pragma unroll
   for (int q = 0; q < TL::LB; ++q)
-    if (PART == kAll || (PART == kLast) == (q == TL::LB - 1)) ob.load(pb, wave * TL::LB + q, ldb, limb, left, w + TL::BOFF);
+    if (PART == kAll || (PART == kLast) == (q == TL::LB - 1)) ob.load(pb, wave * TL::LB + q, limb, left, w + TL::BOFF);
 }
 
 // One pipeline step's memory work: loads of a stage into `w`, and the
@@ -279,10 +289,10 @@ __device__ __forceinline__ void load_stage(const OA &oa, const OB &ob, const uin
 // barrier between them.
 template <typename TL, Part PART, typename OA, typename OB>
 __device__ __forceinline__ void move_stage(const OA &oa, const OB &ob, const uint16_t *pa, const uint16_t *pb,
-                                           int64_t lda, int64_t ldb, int lima, int limb, int left, int wave,
+                                           int lima, int limb, int left, int wave,
                                            lds_u8 *__restrict__ w, const lds_u8 *__restrict__ r, int stage, int h,
                                            u32x4 (&fa)[TL::FM], u32x4 (&fb)[TL::FN]) {
-  load_stage<TL, PART>(oa, ob, pa, pb, lda, ldb, lima, limb, left, wave, w);
+  load_stage<TL, PART>(oa, ob, pa, pb, lima, limb, left, wave, w);
 #pragma unroll
   for (int j = 0; j < TL::FN; ++j) fb[j] = ob.frag(r, stage + TL::BOFF, j, h);
 #pragma unroll
@@ -323,7 +333,7 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
     const OA oa(lane, sg.lda, wm * TL::TM);
     const OB ob(lane, sg.ldb, wn * TL::TN);
     const uint16_t *pa = OA::base(sg.A, sg.lda, m0, b0 * kStep), *pb = OB::base(sg.B, sg.ldb, n0, b0 * kStep);
-    const int64_t adv_a = OA::advance(sg.lda), adv_b = OB::advance(sg.ldb);
+    const int adv_a = keep(static_cast<int>(OA::advance(sg.lda))), adv_b = keep(static_cast<int>(OB::advance(sg.ldb)));
     int left = min(sg.len, (b0 + ns) * kStep) - b0 * kStep;  // values from the next stage to load on
     auto advance = [&]() {
       pa += adv_a;
@@ -335,7 +345,7 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
       for (int i = 0; i < TL::FM; ++i)
 #pragma unroll
         for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma16x16x32(fa[i], fb[j], acc[i][j]);
-      interleave<TL::FM * TL::FN, OA::READS * TL::FM + OB::READS * TL::FN>();
+      interleave<TL::FM * TL::FN, OA::READS * TL::FM + OB::READS * TL::FN, TL::LPW>();
     };
     // Software pipeline over 32-deep halves: while one is multiplied from
     // registers, the next is read from LDS, and the stages after that are in
@@ -346,13 +356,13 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
     // counts the same loads in flight at every step.
     u32x4 a0[TL::FM], b0f[TL::FN], a1[TL::FM], b1f[TL::FN];
     constexpr bool kHalves = TL::BK == 64;
-    const int lima = p.M - m0, limb = p.N - n0;
+    const int lima = keep(p.M - m0), limb = keep(p.N - n0);
 #pragma unroll
     for (int st = 0; st < TL::NST; ++st) {
       if (kHalves && st == TL::NST - 1) {
-        load_stage<TL, kFirst>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + st * TL::STAGE);
+        load_stage<TL, kFirst>(oa, ob, pa, pb, lima, limb, left, wave, ring + st * TL::STAGE);
       } else {
-        load_stage<TL, kAll>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + st * TL::STAGE);
+        load_stage<TL, kAll>(oa, ob, pa, pb, lima, limb, left, wave, ring + st * TL::STAGE);
         advance();
       }
     }
@@ -366,13 +376,13 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
       wait_and_sync<(TL::NST - 2) * TL::LPW>();
       old = cur;
       cur = cur + TL::STAGE == static_cast<int>(TL::RING) ? 0 : cur + TL::STAGE;
-      move_stage<TL, kHalves ? kFirst : kAll>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + old, ring,
+      move_stage<TL, kHalves ? kFirst : kAll>(oa, ob, pa, pb, lima, limb, left, wave, ring + old, ring,
                                               cur, 0, fa, fb);
       if (!kHalves) advance();
     };
     for (int kt = 0; kt < ns; ++kt) {
       if constexpr (kHalves) {
-        move_stage<TL, kLast>(oa, ob, pa, pb, sg.lda, sg.ldb, lima, limb, left, wave, ring + old, ring, cur, 1, a1, b1f);
+        move_stage<TL, kLast>(oa, ob, pa, pb, lima, limb, left, wave, ring + old, ring, cur, 1, a1, b1f);
         advance();
       } else {
         into_stage(a1, b1f);
