@@ -174,21 +174,6 @@ struct Operand {
   }
 };
 
-// Scheduling of a pipeline step of M MFMAs, R LDS reads and V loads into LDS:
-// MFMAs first (their operands are there), the reads and loads -- for later
-// steps -- spread among them, with the address arithmetic two at a time.
-template <int M, int R, int V>
-__device__ __forceinline__ void interleave() {
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
-    if ((i + 1) * V / M > i * V / M) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // one load
-#pragma unroll
-    for (int k = i * R / M; k < (i + 1) * R / M; ++k) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
-    __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // VALU
-  }
-}
-
 // NST stages of BK contraction values of a BM x BN tile, on WM x WN waves.
 template <int BM_, int BN_, int WM_, int WN_, int BK_, int NST_>
 struct BTile {
@@ -345,7 +330,7 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
       for (int i = 0; i < TL::FM; ++i)
 #pragma unroll
         for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma16x16x32(fa[i], fb[j], acc[i][j]);
-      interleave<TL::FM * TL::FN, OA::READS * TL::FM + OB::READS * TL::FN, TL::LPW>();
+      interleave_mfma<TL::FM * TL::FN, OA::READS * TL::FM + OB::READS * TL::FN, TL::LPW>();
     };
     // Software pipeline over 32-deep halves: while one is multiplied from
     // registers, the next is read from LDS, and the stages after that are in

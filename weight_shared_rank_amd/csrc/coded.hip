@@ -257,110 +257,148 @@ __global__ __launch_bounds__(NW * 64) void coded_stream_kernel(CodedArgs a) {
 }
 
 // ---- many tokens: LDS-tiled product --------------------------------------------
+// A workgroup owns BM weight rows (A operand) x BN tokens.  A stage is one
+// 128-k block: 128 bytes of every row, 16-byte chunk c of row r in slot c ^
+// (r / 2 % 8) -- the 16 lanes of a read phase hold 16 rows of a 32-row fragment
+// and one chunk, and that spreads them over all 64 banks (c ^ (r % 8), which
+// suits 16-row fragments, met in half of them) -- and behind the rows each wave's copy of the
+// block's scale bytes of its tokens; the weights' one scale byte per wave and
+// block comes from a register that holds the next 64 blocks', one per lane.
+// The waves work in 64-deep halves of it with the 32 x 32 x 64 instruction,
+// whose fragments are half a stage deep: while one half is multiplied from
+// registers the next is read from LDS and further stages are in flight.  (The
+// 16 x 16 x 128 instruction needs all of a stage's fragments at once: with
+// loads, reads and MFMAs in turn a 2048 x 21504 x 5376 call took 231 us.)
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// D += 2^(sa-127) 2^(sb-127) A B for a 32 x 32 tile over 64 k: lane l supplies
+// 32 codes of A row l & 31 and of B column l & 31 and the scale byte of each;
+// element i of D is row 8 (i / 4) + 4 (l >> 5) + i % 4, column l & 31.
+__device__ __forceinline__ f32x16 mfma_coded32(i32x8 a, i32x8 b, f32x16 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
+}
+
 template <int BM_, int BN_, int WM_, int WN_, int NST_>
 struct CTile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
   static constexpr int NW = WM * WN;
-  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
-  static constexpr int GA = BM / 8, GB = BN / 8;
-  static constexpr int LPW = (GA + GB) / NW;
-  static constexpr int SCALES = (BM + BN) * kRowBytes;  // offset of a stage's scale bytes: 256 token, 256 weight
-  static constexpr int STAGE = SCALES + 512;
-  static constexpr int PITCH = 2 * BM + 16;             // staged output tile: bytes per token row
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW, LPW = LA + LB + 1;  // load instructions of a wave per stage
+  static constexpr int BOFF = BM * kRowBytes, SCALES = BOFF + BN * kRowBytes;  // 256 scale bytes per wave
+  static constexpr int STAGE = SCALES + NW * 256;
+  static constexpr int PITCH = 2 * BM + 16;  // staged output tile: bytes per token row
   static constexpr size_t RING = static_cast<size_t>(NST) * STAGE, OUT = static_cast<size_t>(BN) * PITCH;
   static constexpr size_t LDS = RING > OUT ? RING : OUT;
-  static_assert((GA + GB) % NW == 0 && kBlk % TM == 0 && BN <= 256 && NW >= 2, "tile shape");
+  static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && kBlk % TM == 0 && BN <= 256 && NW >= 2, "tile shape");
   static_assert(LDS <= 160 * 1024, "ring");
 };
 
 template <typename TL>
-__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 2))) void coded_gemm_kernel(CodedArgs a) {
+__global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, TL::LDS > 80 * 1024 ? 2 : 4))) void
+coded_gemm_kernel(CodedArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int lrow = lane >> 3, lchunk = (lane & 7) ^ (lrow & 7);
+  const int r32 = lane & 31, g = lane >> 5;
   int f, sl, t;
   unit_of(blockIdx.x, a.nM * a.nT * a.ksplit, a.nT, a.ksplit, f, sl, t);
   const int m0 = f * TL::BM, n0 = t * TL::BN;
   const int s0 = min(a.nb, sl * a.steps_per_slice), nk = min(a.nb, s0 + a.steps_per_slice) - s0;
 
   // One descriptor per operand, based at the tile's first row and this slice's
-  // first k; a lane's offset spans at most 256 rows of 2^20 codes.
+  // first k; a load instruction covers 8 rows, its first by the scalar offset.
   const auto rw = tile_rsrc(a.W + static_cast<int64_t>(m0) * a.K + static_cast<int64_t>(s0) * kBlk);
   const auto rx = tile_rsrc(a.X + static_cast<int64_t>(n0) * a.K + static_cast<int64_t>(s0) * kBlk);
-  uint32_t off[TL::LPW], inc[TL::LPW];
+  const int lrow = lane >> 3;
+  const uint32_t lo = static_cast<uint32_t>(lrow) * a.K + ((lane & 7) ^ (lrow >> 1)) * 16;
+  const int limw = a.N - m0, limx = a.T - n0, K8 = __builtin_amdgcn_readfirstlane(8 * a.K);
+  // This wave's token scales of a block: a dword of four tokens per lane.
+  const int tok0 = n0 + wn * TL::TN;
+  const auto rs = tile_rsrc(a.sx + static_cast<int64_t>(s0) * a.ldsx);
+  const uint32_t slo = lane * 4 < TL::TN && tok0 + lane * 4 < a.ldsx ? tok0 + lane * 4 : kBufNoRow;
+  const uint8_t *swp = a.sw + static_cast<int64_t>(s0) * a.ldsw + (m0 + wm * TL::TM) / kBlk;
+  auto weight_scales = [&](int kt) { return static_cast<int>(swp[static_cast<int64_t>(min(kt + lane, nk - 1)) * a.ldsw]); };
+  // Stage loads past the last block read no rows (zeros), so that the loop
+  // needs no branches and counts the same loads in flight at every step.
+  int issued = 0;
+  auto issue = [&](int stage) __attribute__((always_inline)) {
+    const bool live = issued < nk;
+    uint8_t *st = lds + stage;
 #pragma unroll
-  for (int q = 0; q < TL::LPW; ++q) {
-    const int gq = wave * TL::LPW + q;
-    const int row = (gq < TL::GA ? gq : gq - TL::GA) * 8 + lrow;
-    const bool in = gq < TL::GA ? m0 + row < a.N : n0 + row < a.T;
-    off[q] = in ? static_cast<uint32_t>(row) * a.K + lchunk * 16 : kBufNoRow;
-    inc[q] = in ? kRowBytes : 0;
-  }
-  // Scales of a stage: wave 0 brings the tile's token scales (a dword of four
-  // tokens per lane), wave 1 the dword with the tile's weight scales.
-  const auto rs = tile_rsrc(wave == 0 ? a.sx + static_cast<int64_t>(s0) * a.ldsx + n0
-                                      : a.sw + static_cast<int64_t>(s0) * a.ldsw + ((m0 / kBlk) & ~3));
-  const bool sin = wave == 0 ? lane * 4 < TL::BN && n0 + lane * 4 < a.ldsx : lane == 0;
-  uint32_t soff = sin ? lane * 4 : kBufNoRow;
-  const uint32_t sinc = sin ? (wave == 0 ? a.ldsx : a.ldsw) : 0;
-  auto issue = [&](int stage) {
-    uint8_t *st = lds + stage * TL::STAGE;
+    for (int q = 0; q < TL::LA; ++q) {
+      const int gq = wave * TL::LA + q;
+      load_lds<16>(rw, live && gq * 8 + lrow < limw ? lo ^ (64 * (gq & 1)) : kBufNoRow, st + gq * 1024, gq * K8 + issued * kBlk);
+    }
 #pragma unroll
-    for (int q = 0; q < TL::LPW; ++q) {
-      const int gq = wave * TL::LPW + q;
-      load_lds<16>(gq < TL::GA ? rw : rx, off[q], st + gq * 1024);
-      off[q] += inc[q];
+    for (int q = 0; q < TL::LB; ++q) {
+      const int gq = wave * TL::LB + q;
+      load_lds<16>(rx, live && gq * 8 + lrow < limx ? lo ^ (64 * (gq & 1)) : kBufNoRow, st + TL::BOFF + gq * 1024, gq * K8 + issued * kBlk);
     }
-    if (wave < 2) {
-      load_lds<4>(rs, soff, st + TL::SCALES + wave * 256);
-      soff += sinc;
-    }
+    load_lds<4>(rs, live ? slo : kBufNoRow, st + TL::SCALES + wave * 256, live ? issued * a.ldsx : 0);
+    ++issued;
   };
 
-  f32x4 acc[TL::FM][TL::FN];
+  f32x16 acc[TL::FM][TL::FN];
 #pragma unroll
   for (int i = 0; i < TL::FM; ++i)
 #pragma unroll
-    for (int j = 0; j < TL::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int arow = (wm * TL::TM + r16) * kRowBytes;
-  const int brow = TL::BM * kRowBytes + (wn * TL::TN + r16) * kRowBytes;
-  const int sw0 = (g ^ (r16 & 7)) * 16, sw1 = ((4 + g) ^ (r16 & 7)) * 16;
-  const int swoff = TL::SCALES + 256 + ((m0 / kBlk) & 3) + (wm * TL::TM) / kBlk;
-  const int sxoff = TL::SCALES + wn * TL::TN + r16;
+    for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  // fragment reads: chunks 4 h + 2 g and + 1 of the row
+  const int arow = (wm * TL::TM + r32) * kRowBytes, brow = TL::BOFF + (wn * TL::TN + r32) * kRowBytes;
+  const int c0 = ((2 * g) ^ ((r32 >> 1) & 7)) * 16, c1 = ((2 * g + 1) ^ ((r32 >> 1) & 7)) * 16;
+  const int sxoff = TL::SCALES + wave * 256 + r32;
+  auto read = [&](i32x8(&fa)[TL::FM], i32x8(&fb)[TL::FN], int stage, int h) __attribute__((always_inline)) {
+    const uint8_t *sb = lds + stage;
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j)
+      fb[j] = join(*reinterpret_cast<const u32x4 *>(sb + brow + j * 32 * kRowBytes + (c0 ^ (64 * h))),
+                   *reinterpret_cast<const u32x4 *>(sb + brow + j * 32 * kRowBytes + (c1 ^ (64 * h))));
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+      fa[i] = join(*reinterpret_cast<const u32x4 *>(sb + arow + i * 32 * kRowBytes + (c0 ^ (64 * h))),
+                   *reinterpret_cast<const u32x4 *>(sb + arow + i * 32 * kRowBytes + (c1 ^ (64 * h))));
+  };
+  int sx[TL::FN], nx[TL::FN], sw = 0;
+  auto read_scales = [&](int(&x)[TL::FN], int stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) x[j] = lds[stage + sxoff + j * 32];
+  };
+  auto multiply = [&](const i32x8(&fa)[TL::FM], const i32x8(&fb)[TL::FN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma_coded32(fa[i], fb[j], acc[i][j], sw, sx[j]);
+  };
 
+  i32x8 a0[TL::FM], b0[TL::FN], a1[TL::FM], b1[TL::FN];
 #pragma unroll
-  for (int st = 0; st < TL::NST - 1; ++st)
-    if (st < nk) issue(st);
-  for (int kt = 0; kt < nk; ++kt) {
-    if (kt + TL::NST - 2 < nk) {
-      if (wave < 2)
-        wait_and_sync<(TL::NST - 2) * (TL::LPW + 1)>();
-      else
-        wait_and_sync<(TL::NST - 2) * TL::LPW>();
-    } else {
-      wait_and_sync<0>();
+  for (int st = 0; st < TL::NST; ++st) issue(st * TL::STAGE);
+  wait_and_sync<(TL::NST - 1) * TL::LPW>();
+  int cur = 0;
+  read(a0, b0, 0, 0);
+  read_scales(sx, 0);
+  constexpr int kMfma = TL::FM * TL::FN, kReads = 2 * (TL::FM + TL::FN);
+  for (int base = 0; base < nk; base += 64) {
+    const int wv = weight_scales(base), n = min(64, nk - base);
+    for (int kt = 0; kt < n; ++kt) {
+      sw = __builtin_amdgcn_readlane(wv, kt);
+      read(a1, b1, cur, 1);
+      multiply(a0, b0);
+      lead_mfma<kMfma, kReads, 0>();
+      // every wave has read all of this stage: its buffer takes the loads of
+      // the stage NST ahead; the next stage has landed
+      wait_and_sync<(TL::NST - 2) * TL::LPW>();
+      issue(cur);
+      cur = cur + TL::STAGE == static_cast<int>(TL::RING) ? 0 : cur + TL::STAGE;
+      read_scales(nx, cur);
+      read(a0, b0, cur, 0);
+      multiply(a1, b1);
+      lead_mfma<kMfma, kReads + TL::FN, TL::LPW>();
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j) sx[j] = nx[j];
     }
-    if (kt + TL::NST - 1 < nk) issue((kt + TL::NST - 1) % TL::NST);
-    const uint8_t *sb = lds + (kt % TL::NST) * TL::STAGE;
-    i32x8 fa[TL::FM], fb[TL::FN];
-    int sx[TL::FN];
-    const int sw = sb[swoff];
-#pragma unroll
-    for (int j = 0; j < TL::FN; ++j) {
-      fb[j] = join(*reinterpret_cast<const u32x4 *>(sb + brow + j * 16 * kRowBytes + sw0),
-                   *reinterpret_cast<const u32x4 *>(sb + brow + j * 16 * kRowBytes + sw1));
-      sx[j] = sb[sxoff + j * 16];
-    }
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i)
-      fa[i] = join(*reinterpret_cast<const u32x4 *>(sb + arow + i * 16 * kRowBytes + sw0),
-                   *reinterpret_cast<const u32x4 *>(sb + arow + i * 16 * kRowBytes + sw1));
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < TL::FN; ++j) acc[i][j] = mfma_coded(fa[i], fb[j], acc[i][j], sw, sx[j]);
   }
   wait_and_sync<0>();  // the ring is idle
 
@@ -368,13 +406,17 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
     float *P = a.P + static_cast<int64_t>(sl) * a.T * a.ldp;
 #pragma unroll
     for (int j = 0; j < TL::FN; ++j) {
-      const int tok = n0 + wn * TL::TN + j * 16 + r16;
+      const int tok = n0 + wn * TL::TN + j * 32 + r32;
       if (tok >= a.T) continue;
 #pragma unroll
-      for (int i = 0; i < TL::FM; ++i) {
-        const int row = m0 + wm * TL::TM + i * 16 + g * 4;
-        if (row < a.ldp) *reinterpret_cast<f32x4 *>(P + static_cast<int64_t>(tok) * a.ldp + row) = acc[i][j];
-      }
+      for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = m0 + wm * TL::TM + i * 32 + q * 8 + g * 4;
+          if (row < a.ldp)
+            *reinterpret_cast<f32x4 *>(P + static_cast<int64_t>(tok) * a.ldp + row) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
     }
     return;
   }
@@ -382,12 +424,14 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
 #pragma unroll
   for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
-    for (int i = 0; i < TL::FM; ++i) {
-      const int tl = wn * TL::TN + j * 16 + r16, fl = wm * TL::TM + i * 16 + g * 4;
-      *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) =
-          make_uint2(f32_to_bf16(acc[i][j][0]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][1])) << 16),
-                     f32_to_bf16(acc[i][j][2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][3])) << 16));
-    }
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int tl = wn * TL::TN + j * 32 + r32, fl = wm * TL::TM + i * 32 + q * 8 + g * 4;
+        *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) = make_uint2(
+            f32_to_bf16(acc[i][j][4 * q]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * q + 1])) << 16),
+            f32_to_bf16(acc[i][j][4 * q + 2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * q + 3])) << 16));
+      }
   __syncthreads();
   constexpr int CPR = TL::BM / 8;
   for (int c = threadIdx.x; c < TL::BN * CPR; c += TL::NW * 64) {
@@ -525,7 +569,10 @@ hipError_t launch_coded_linear(const CodedView &w, int N, const CodedView &x, in
   hipError_t e;
   switch (p.tile) {
     case 0: e = launch_coded_tile<CTile<256, 256, 2, 4, 2>>(a, stream); break;
-    case 1: e = launch_coded_tile<CTile<128, 128, 2, 4, 4>>(a, stream); break;
+    case 1:
+      e = p.nM * p.nT * p.ksplit > kCUs ? launch_coded_tile<CTile<128, 128, 2, 4, 2>>(a, stream)
+                                        : launch_coded_tile<CTile<128, 128, 2, 4, 4>>(a, stream);
+      break;
     default: e = launch_coded_tile<CTile<128, 64, 4, 2, 4>>(a, stream); break;
   }
   if (e != hipSuccess || p.ksplit == 1) return e;

@@ -62,14 +62,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void *base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, kBufRange, kBufWord3);
 }
 
-// BYTES (4 or 16) per lane from descriptor + offset to dst + BYTES * lane.
+// BYTES (4 or 16) per lane from descriptor + off (per lane) + soff (uniform) to
+// dst + BYTES * lane.
 template <int BYTES>
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint32_t off, uint8_t *dst) {
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint32_t off, uint8_t *dst, int soff) {
   static_assert(BYTES == 4 || BYTES == 16, "bytes per lane");
   if constexpr (BYTES == 16)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, off, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, off, soff, 0, 0);
   else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 4, off, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 4, off, soff, 0, 0);
 }
 
 template <int N>
@@ -86,6 +87,39 @@ __device__ __forceinline__ void wait_and_sync() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | (((N >> 4) & 3) << 14));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// Scheduling of a pipeline step of M MFMAs, R LDS reads and V loads into LDS:
+// MFMAs first (their operands are there), the reads and loads -- for later
+// steps -- spread among them, with the address arithmetic two at a time.
+template <int M, int R, int V>
+__device__ __forceinline__ void interleave_mfma() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+    if ((i + 1) * V / M > i * V / M) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // one load
+#pragma unroll
+    for (int k = i * R / M; k < (i + 1) * R / M; ++k) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+    __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // VALU
+  }
+}
+
+// For steps of few long MFMAs: after each, an even share of the reads so that
+// all are issued by three quarters of the step; the loads come first.
+template <int M, int R, int V>
+__device__ __forceinline__ void lead_mfma() {
+  constexpr int Q = M > 1 ? (3 * M + 3) / 4 : 1;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (V > 0) {
+      if (i == 0) __builtin_amdgcn_sched_group_barrier(0x020, V, 0);
+    }
+    if (i < Q) {
+#pragma unroll
+      for (int k = i * R / Q; k < (i + 1) * R / Q; ++k) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  }
 }
 
 // Workgroup index -> unit, XCD-major: hardware sends workgroup w to XCD w % 8;
