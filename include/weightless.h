@@ -361,10 +361,10 @@ wl_status weightless_weight_encode(const void *d_w, int32_t N, int32_t K, void *
  *    exactly what weightless_act_encode writes (a checkpoint to keep).
  *  d_ws: weightless_coded_linear_workspace_bytes(N, K, T) bytes, 256-byte
  *    aligned, no initialization, nothing kept; may be NULL if that is 0 bytes
- *    (always so for T <= 16).  Concurrent calls need distinct workspaces.
- *  T <= 16 streams the weights once through registers (one launch, and one for
- *  coding x); T > 16 runs LDS-tiled matrix-core products, K split over
- *  workgroups and summed by a second launch when there are few output tiles. */
+ *    (always so for T <= 4).  Concurrent calls need distinct workspaces.
+ *  T <= 16 streams the weights once through registers; T <= 4 is one launch,
+ *  x coded in it; T > 16 runs LDS-tiled matrix-core products.  K is split over
+ *  workgroups and summed by another launch when there are few output tiles. */
 size_t weightless_coded_linear_workspace_bytes(int32_t N, int32_t K, int32_t T);
 wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32_t N, int32_t K, const void *d_x,
                                   void *d_xcode, size_t xcode_bytes, int32_t T, void *d_y, void *d_ws,

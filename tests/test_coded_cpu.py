@@ -97,8 +97,9 @@ def test_coded_linear_arguments_refused(L):
 
 
 def test_workspace_is_zero_for_few_tokens_and_small_otherwise(L):
-    assert L.weightless_coded_linear_workspace_bytes(21504, 5376, 16) == 0
-    for T in (17, 64, 333, 2048):
+    for n, k in ((21504, 5376), (5376, 21504), (8, 1 << 20), (1 << 20, 8)):
+        assert all(L.weightless_coded_linear_workspace_bytes(n, k, T) == 0 for T in (0, 1, 4))
+    for T in (5, 16, 17, 64, 333, 2048):
         n = L.weightless_coded_linear_workspace_bytes(5376, 21504, T)
         assert n % 256 == 0 and n <= 16 * T * 5376 * 4
 

@@ -7,6 +7,7 @@ fails to load, every entry point raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Iterable, NamedTuple, Optional, Sequence, Tuple
@@ -215,6 +216,7 @@ class ThetaBundle:
         self._loaded = torch.cuda.Event()
         self._loaded.record(stream if stream is not None else torch.cuda.current_stream())
         self._ws = {}
+        self._backward_need = {}   # T -> workspace bytes
 
     def close(self):
         if getattr(self, "handle", None):
@@ -341,12 +343,15 @@ class ThetaBundle:
             elif dw0 is not None or accumulate:
                 raise WlError(-1, "dw0 is given but not wanted")
             if ws is None:
-                need = lib().weightless_backward_workspace_bytes(self.handle, T)
-                if need == 0:
-                    raise WlError(-1, last_error())
+                need = self._backward_need.get(T)
+                if need is None:
+                    need = lib().weightless_backward_workspace_bytes(self.handle, T)
+                    if need == 0:
+                        raise WlError(-1, last_error())
+                    self._backward_need[T] = need
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
             _check(fn(self.handle, layer, code, x.buf.data_ptr(), x.buf.numel(), dy.data_ptr(), T, ctypes.byref(g),
-                      ws.data_ptr(), ws.numel(), _stream_ptr(None)))
+                      ws.data_ptr(), ws.numel(), _raw_stream(dev)))
         return Grads(**out)
 
     def linear_backward(self, layer: int, family: str, x, dy, want=("dx", "ds", "du", "dv"), dw0=None,
@@ -439,22 +444,28 @@ def decompose(w, rank: int, omega=None, oversample: int = 16, power_iters: int =
 # ---- 8-bit coded operands -------------------------------------------------
 
 CODE_BLOCK = 128
+CODED_NO_WORKSPACE_T = 4     # weightless_coded_linear needs no workspace up to here
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _scope(device, stream):
     """The device and stream a call runs on: the given stream, or the current
     stream of the tensors' device.  Everything the call allocates is then
     allocated on that stream."""
-    import contextlib
-
     import torch
     if stream is not None:
         if stream.device != device:
             raise WlError(-1, f"stream is on {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(device) -> int:
+    """The current stream of `device` as a hipStream_t (inside its _scope)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check_tensor(t, name, shape, dtype, device=None):
@@ -479,10 +490,13 @@ class _Code:
         need = getattr(lib(), self._bytes)(rows, K)
         if need == 0:
             raise WlError(-2, last_error())
-        self.buf = torch.empty(need, dtype=torch.uint8, device=device) if buf is None else buf
-        _check_tensor(self.buf, "code buffer", (None,), torch.uint8)
-        if self.buf.numel() < need:
-            raise WlError(-5, f"code buffer has {self.buf.numel()} bytes, needs {need}")
+        if buf is None:
+            buf = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            _check_tensor(buf, "code buffer", (None,), torch.uint8)
+            if buf.numel() < need:
+                raise WlError(-5, f"code buffer has {buf.numel()} bytes, needs {need}")
+        self.buf = buf
 
     @property
     def blocks(self) -> int:
@@ -492,8 +506,7 @@ class _Code:
     def codes(self):
         """The E4M3 codes [rows, K] (a view)."""
         import torch
-        kq = self.blocks * CODE_BLOCK
-        return self.buf[:self.rows * kq].view(torch.float8_e4m3fn).view(self.rows, kq)[:, :self.K]
+        return self.buf.view(torch.float8_e4m3fn).as_strided((self.rows, self.K), (self.blocks * CODE_BLOCK, 1), self.buf.storage_offset())
 
     @property
     def scales(self):
@@ -501,7 +514,7 @@ class _Code:
         n = -(-self.rows // self._rows_per_scale)
         run = -(-n // self._run_multiple) * self._run_multiple
         at = -(-self.rows * self.blocks * CODE_BLOCK // 256) * 256
-        return self.buf[at:at + self.blocks * run].view(self.blocks, run)[:, :n].t()
+        return self.buf.as_strided((n, self.blocks), (1, run), self.buf.storage_offset() + at)
 
 
 class ActCode(_Code):
@@ -520,7 +533,7 @@ class ActCode(_Code):
                 out = torch.empty((self.rows, self.K), dtype=torch.bfloat16, device=self.buf.device)
             _check_tensor(out, "out", (self.rows, self.K), torch.bfloat16, self.buf.device)
             _check(lib().weightless_act_expand(self.buf.data_ptr(), self.buf.numel(), self.rows, self.K,
-                                               out.data_ptr(), _stream_ptr(None)))
+                                               out.data_ptr(), _raw_stream(self.buf.device)))
         return out
 
 
@@ -549,7 +562,7 @@ def encode_act(x, out: Optional[ActCode] = None, stream=None) -> ActCode:
     with _scope(x.device, stream):
         out = _code_out(ActCode, x.shape[0], x.shape[1], x.device, out)
         _check(lib().weightless_act_encode(x.data_ptr(), out.rows, out.K, out.buf.data_ptr(), out.buf.numel(),
-                                           _stream_ptr(None)))
+                                           _raw_stream(x.device)))
     return out
 
 
@@ -560,7 +573,7 @@ def encode_weight(w, out: Optional[WeightCode] = None, stream=None) -> WeightCod
     with _scope(w.device, stream):
         out = _code_out(WeightCode, w.shape[0], w.shape[1], w.device, out)
         _check(lib().weightless_weight_encode(w.data_ptr(), out.rows, out.K, out.buf.data_ptr(), out.buf.numel(),
-                                              _stream_ptr(None)))
+                                              _raw_stream(w.device)))
     return out
 
 
@@ -587,11 +600,11 @@ def coded_linear(w: WeightCode, x, y=None, code: Optional[ActCode] = None, ws=No
             y = torch.empty((T, w.rows), dtype=torch.bfloat16, device=dev)
         else:
             _check_tensor(y, "y", (T, w.rows), torch.bfloat16, dev)
-        if ws is None and T > DECODE_MAX_T:
+        if ws is None and T > CODED_NO_WORKSPACE_T:
             need = lib().weightless_coded_linear_workspace_bytes(w.rows, w.K, T)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         _check(lib().weightless_coded_linear(w.buf.data_ptr(), w.buf.numel(), w.rows, w.K, src, code.buf.data_ptr(),
                                              code.buf.numel(), T, y.data_ptr(),
                                              ws.data_ptr() if ws is not None else None,
-                                             ws.numel() if ws is not None else 0, _stream_ptr(None)))
+                                             ws.numel() if ws is not None else 0, _raw_stream(dev)))
     return y

@@ -191,67 +191,197 @@ __global__ __launch_bounds__(256) void expand_act_kernel(CodedView c, uint16_t *
 struct CodedArgs {
   const uint8_t *W, *sw;  // weight codes [N][K], scales [nb][ldsw]
   const uint8_t *X, *sx;  // activation codes [T][K], scales [nb][ldsx]
+  const uint16_t *x;      // coding fused: bf16 [T][Kx], coded into X and sx
+  int32_t Kx;
   uint16_t *Y;            // [T][N]
   float *P;               // K-split partials [ksplit][T][ldp] (null: none)
   int32_t ldsw, ldsx, ldp;
   int32_t N, T, K, nb;    // K = nb * 128
   int32_t nM, nT, ksplit, steps_per_slice;
+  int32_t rows;           // streaming: weight rows of a workgroup
 };
 
 // ---- few tokens (T <= 16): weight streaming -----------------------------------
-// A workgroup owns 16 weight rows over the whole K; its waves take blocks of
-// kStreamSteps k steps in turn, so that neighbouring waves read neighbouring
-// 512-byte runs of the same rows.  Rows go straight from HBM to registers
-// (A operand), the tokens' codes are the B operand (columns past T are zero),
-// and the waves' sums meet in LDS in a fixed order.
-constexpr int kStreamSteps = 4;
+// The weights go straight from HBM to registers as the A operand, each row
+// read in 128-byte blocks by four lanes; the tokens' codes are the B operand
+// (lanes past the last token repeat the first: their columns are not stored).
+// Bound by reading N K bytes: 21504 x 5376 in 20.5 us for loads alone.
 
-template <int NW>
-__global__ __launch_bounds__(NW * 64) void coded_stream_kernel(CodedArgs a) {
+// A workgroup's up to 16 rows over the whole K; its 16 waves take pairs of
+// blocks in turn, so that neighbouring waves read neighbouring runs of the same
+// rows, and their sums meet in LDS in wave order.  a.rows <= 16 is chosen so
+// that the workgroups are a multiple of the CUs (21504 rows: 14, 21.5 us
+// against 22.5 at 16; 8 waves of 4 blocks 23.5; loads one pair ahead 35).
+//
+// FUSE (T <= kFuseT): x comes as bf16 and every wave codes the blocks it needs
+// -- 16 lanes to a block, as encode_act_kernel -- through its part of LDS;
+// workgroup 0 also writes the coded buffer.  It saves the coding launch, and
+// the arithmetic, repeated by every workgroup, hides under the weight loads
+// while there are few tokens.
+constexpr int kStreamWaves = 16, kStreamPair = 2;
+constexpr int kFuseT = 4;
+
+template <bool FUSE>
+__global__ __launch_bounds__(kStreamWaves * 64) void coded_stream_kernel(CodedArgs a) {
+  constexpr int NW = kStreamWaves, S = kStreamPair;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const int row = min(n0 + r16, a.N - 1);
+  const int n0 = blockIdx.x * a.rows;
+  const bool live = r16 < a.rows && n0 + r16 < a.N;
+  const int row = live ? n0 + r16 : n0;
   const uint8_t *wp = a.W + static_cast<int64_t>(row) * a.K + g * 16;
-  const uint8_t *swp = a.sw + n0 / kBlk;
-  const bool live = r16 < a.T;
-  const uint8_t *xp = a.X + static_cast<int64_t>(live ? r16 : 0) * a.K + g * 16;
-  const uint8_t *sxp = a.sx + (live ? r16 : 0);
+  const uint8_t *swp = a.sw + row / kBlk;
+  const int tok = r16 < a.T ? r16 : 0;
+  const uint8_t *xp = a.X + static_cast<int64_t>(tok) * a.K + g * 16;
+  const uint8_t *sxp = a.sx + tok;
+  __shared__ __align__(16) uint8_t xc[FUSE ? NW : 1][kFuseT][S * kBlk];
+  __shared__ uint8_t xs[FUSE ? NW : 1][kFuseT][S];
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
   const u32x4 zero{0u, 0u, 0u, 0u};
-  for (int b = wave * kStreamSteps; b < a.nb; b += NW * kStreamSteps) {
-    u32x4 w[kStreamSteps][2], x[kStreamSteps][2];
-    int sw[kStreamSteps], sx[kStreamSteps];
+  for (int b = wave * S; b < a.nb; b += NW * S) {
+    u32x4 w[S][2], x[S][2];
+    int sw[S], sx[S];
+    // FUSE: block u of S * T per pass of four, its lanes 8 elements each
+    u32x4 v[FUSE ? kFuseT * S / 4 : 1];
+    if constexpr (FUSE) {
 #pragma unroll
-    for (int i = 0; i < kStreamSteps; ++i) {
-      const int kb = min(b + i, a.nb - 1);
-      w[i][0] = *reinterpret_cast<const u32x4 *>(wp + kb * kBlk);
-      w[i][1] = *reinterpret_cast<const u32x4 *>(wp + kb * kBlk + 64);
+      for (int p = 0; p < kFuseT * S / 4; ++p) {
+        if (p * 4 / S >= a.T) break;
+        const int u = p * 4 + g, t = u / S, k = (b + u % S) * kBlk + r16 * 8;
+        v[p] = zero;
+        if (t < a.T && k < a.Kx) v[p] = ld16(a.x + static_cast<int64_t>(t) * a.Kx + k);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kStreamSteps; ++i) {
+    for (int i = 0; i < S; ++i) {
       const int kb = min(b + i, a.nb - 1);
-      const bool in = live && b + i < a.nb;  // steps past the end multiply zeros
-      x[i][0] = in ? *reinterpret_cast<const u32x4 *>(xp + kb * kBlk) : zero;
-      x[i][1] = in ? *reinterpret_cast<const u32x4 *>(xp + kb * kBlk + 64) : zero;
+      w[i][0] = w[i][1] = zero;
+      if (live) {
+        w[i][0] = *reinterpret_cast<const u32x4 *>(wp + kb * kBlk);
+        w[i][1] = *reinterpret_cast<const u32x4 *>(wp + kb * kBlk + 64);
+      }
       sw[i] = swp[static_cast<int64_t>(kb) * a.ldsw];
-      sx[i] = sxp[static_cast<int64_t>(kb) * a.ldsx];
+    }
+    if constexpr (FUSE) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int p = 0; p < kFuseT * S / 4; ++p) {
+        if (p * 4 / S >= a.T) break;
+        const int u = p * 4 + g, t = u / S, i = u % S;
+        uint32_t m = amax_bits(v[p]);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 16)));
+        const int e = block_exponent(m);
+        const u32x2 c = code8(v[p], e);
+        *reinterpret_cast<u32x2 *>(&xc[wave][t][i * kBlk + r16 * 8]) = c;
+        if (r16 == 0) xs[wave][t][i] = static_cast<uint8_t>(e + 127);
+        if (blockIdx.x == 0 && b + i < a.nb) {
+          if (t < a.T)
+            *reinterpret_cast<u32x2 *>(const_cast<uint8_t *>(a.X) + static_cast<int64_t>(t) * a.K + (b + i) * kBlk + r16 * 8) = c;
+          // a block's 16 scale bytes: the tokens', and 127 behind them
+          uint8_t *so = const_cast<uint8_t *>(a.sx) + static_cast<int64_t>(b + i) * a.ldsx;
+          if (r16 == 0 && t < a.T) so[t] = static_cast<uint8_t>(e + 127);
+          if (t == 0 && r16 >= a.T) so[r16] = 127;
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        x[i][0] = *reinterpret_cast<const u32x4 *>(&xc[wave][tok][i * kBlk + g * 16]);
+        x[i][1] = *reinterpret_cast<const u32x4 *>(&xc[wave][tok][i * kBlk + g * 16 + 64]);
+        sx[i] = xs[wave][tok][i];  // a block past the end is zeros
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const int kb = min(b + i, a.nb - 1);
+        const bool in = b + i < a.nb;  // steps past the end multiply zeros
+        x[i][0] = in ? *reinterpret_cast<const u32x4 *>(xp + kb * kBlk) : zero;
+        x[i][1] = in ? *reinterpret_cast<const u32x4 *>(xp + kb * kBlk + 64) : zero;
+        sx[i] = sxp[static_cast<int64_t>(kb) * a.ldsx];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kStreamSteps; ++i)
+    for (int i = 0; i < S; ++i)
       acc = mfma_coded(join(w[i][0], w[i][1]), join(x[i][0], x[i][1]), acc, sw[i], sx[i]);
   }
-  // [wave][token][row]; the sums run over the waves in order
-  __shared__ float part[NW][16][16];
+  __shared__ float part[NW][16][16];  // [wave][token][row]
   *reinterpret_cast<f32x4 *>(&part[wave][r16][g * 4]) = acc;
   __syncthreads();
   if (threadIdx.x < 256) {
     const int t = threadIdx.x >> 4, r = threadIdx.x & 15;
-    if (t < a.T && n0 + r < a.N) {
+    if (t < a.T && r < a.rows && n0 + r < a.N) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) s += part[i][t][r];
       a.Y[static_cast<int64_t>(t) * a.N + n0 + r] = f32_to_bf16(s);
+    }
+  }
+}
+
+// Several tokens: every code of x is then real, and a wave that loads 16 x 128
+// of them per 16 x 128 weights is bound by the loads from L2, not HBM (5376 x
+// 21504 at T = 16: 42 us).  Here a wave multiplies four 16-row tiles by each x
+// fragment, a workgroup's 8 waves take blocks in turn, and K is cut into
+// slices so that the workgroups fill the CUs; their partial sums go through
+// coded_sum_kernel (252 workgroups of 3 slices and the sum: 26.4 us).  The
+// scale bytes of a slice (at most kStreamSlice blocks) wait in LDS.
+constexpr int kWideRows = 64, kWideWaves = 8, kStreamSlice = 256;
+
+__global__ __launch_bounds__(kWideWaves * 64) void coded_wide_kernel(CodedArgs a) {
+  constexpr int NW = kWideWaves, RT = kWideRows / 16;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r16 = lane & 15, g = lane >> 4;
+  const int tile = blockIdx.x / a.ksplit, sl = blockIdx.x % a.ksplit;
+  const int b0 = min(a.nb, sl * a.steps_per_slice), b1 = min(a.nb, b0 + a.steps_per_slice);
+  const int n0 = tile * kWideRows;  // 64 rows lie in one 128-row scale block
+  __shared__ __align__(16) uint8_t xs[kStreamSlice * 16];
+  __shared__ uint8_t ws[kStreamSlice];
+  for (int i = threadIdx.x; i < b1 - b0; i += NW * 64) {
+    *reinterpret_cast<u32x4 *>(xs + i * 16) = *reinterpret_cast<const u32x4 *>(a.sx + static_cast<int64_t>(b0 + i) * a.ldsx);
+    ws[i] = a.sw[static_cast<int64_t>(b0 + i) * a.ldsw + n0 / kBlk];
+  }
+  __syncthreads();
+  const uint8_t *wp[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    wp[r] = a.W + static_cast<int64_t>(min(n0 + r * 16 + r16, a.N - 1)) * a.K + g * 16;
+  const int tok = r16 < a.T ? r16 : 0;
+  const uint8_t *xp = a.X + static_cast<int64_t>(tok) * a.K + g * 16;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = b0 + wave; b < b1; b += NW) {
+    u32x4 w[RT][2], x[2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      w[r][0] = *reinterpret_cast<const u32x4 *>(wp[r] + b * kBlk);
+      w[r][1] = *reinterpret_cast<const u32x4 *>(wp[r] + b * kBlk + 64);
+    }
+    x[0] = *reinterpret_cast<const u32x4 *>(xp + b * kBlk);
+    x[1] = *reinterpret_cast<const u32x4 *>(xp + b * kBlk + 64);
+    const int sx = xs[(b - b0) * 16 + tok], sw = ws[b - b0];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = mfma_coded(join(w[r][0], w[r][1]), join(x[0], x[1]), acc[r], sw, sx);
+  }
+  __shared__ float part[NW][16][16];  // [wave][token][row], a row tile at a time
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    __syncthreads();
+    *reinterpret_cast<f32x4 *>(&part[wave][r16][g * 4]) = acc[r];
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      const int t = threadIdx.x >> 4, q = threadIdx.x & 15, n = n0 + r * 16 + q;
+      if (t < a.T && n < a.N) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) s += part[i][t][q];
+        if (a.P)
+          a.P[(static_cast<int64_t>(sl) * a.T + t) * a.ldp + n] = s;
+        else
+          a.Y[static_cast<int64_t>(t) * a.N + n] = f32_to_bf16(s);
+      }
     }
   }
 }
@@ -505,6 +635,33 @@ CPlan plan_coded(int N, int T, int nb) {
   return best;
 }
 
+// Slices of the several-token stream, 0 for the one-tile kernel (which needs
+// none): the fewest whose workgroups come within 15% of whole rounds of the
+// CUs, of at least 8 blocks (one per wave); calls too small to fill the CUs
+// that way take one-tile workgroups (4096 x 1152 at T = 16: 4.0 us against
+// 6.2).
+int wide_slices(int N, int T, int nb) {
+  if (T <= kFuseT) return 0;
+  const int tiles = (N + kWideRows - 1) / kWideRows;
+  const int least = (nb + kStreamSlice - 1) / kStreamSlice;
+  int best = 0;
+  double best_eff = 0.0;
+  for (int ks = least; ks <= std::max(least, 12); ++ks) {
+    const int per = (nb + ks - 1) / ks;
+    if (per < 8 && ks > least) break;
+    if ((ks - 1) * per >= nb) continue;  // an empty slice
+    const int units = tiles * ks, rounds = (units + kCUs - 1) / kCUs;
+    const double eff = static_cast<double>(units) / (rounds * kCUs);
+    if (units < 3 * kCUs / 4) continue;
+    if (eff > best_eff) {
+      best_eff = eff;
+      best = ks;
+    }
+    if (eff >= 0.85) break;
+  }
+  return best;
+}
+
 template <typename TL>
 hipError_t launch_coded_tile(const CodedArgs &a, hipStream_t stream) {
   const hipError_t e = ensure_lds<coded_gemm_kernel<TL>>(TL::LDS);
@@ -516,9 +673,9 @@ hipError_t launch_coded_tile(const CodedArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t coded_partial_bytes(int N, int T, int K) {
-  if (T <= kDecodeMaxT) return 0;
-  const CPlan p = plan_coded(N, T, (K + kBlk - 1) / kBlk);
-  return p.ksplit > 1 ? static_cast<size_t>(p.ksplit) * T * ((N + 3) & ~3) * 4 : 0;
+  const int nb = (K + kBlk - 1) / kBlk;
+  const int ks = T <= kDecodeMaxT ? wide_slices(N, T, nb) : plan_coded(N, T, nb).ksplit;
+  return ks > 1 ? static_cast<size_t>(ks) * T * ((N + 3) & ~3) * 4 : 0;
 }
 
 hipError_t launch_encode_act(const uint16_t *x, int T, int K, const CodedView &o, hipStream_t stream) {
@@ -541,8 +698,20 @@ hipError_t launch_expand_act(const CodedView &c, int T, uint16_t *x, int ldx, hi
   return hipGetLastError();
 }
 
-hipError_t launch_coded_linear(const CodedView &w, int N, const CodedView &x, int T, uint16_t *y, float *partials,
-                               hipStream_t stream) {
+namespace {
+
+// y = bf16 of the sum of the slices' partials
+hipError_t launch_coded_sum(const CodedArgs &a, hipStream_t stream) {
+  const int64_t n = static_cast<int64_t>(a.T) * (a.ldp / 4);
+  hipLaunchKernelGGL(coded_sum_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
+                     static_cast<const float *>(a.P), a.ksplit, a.T, a.N, a.ldp, a.Y);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_coded_linear(const CodedView &w, int N, const uint16_t *src, int K, const CodedView &x, int T,
+                               uint16_t *y, float *partials, hipStream_t stream) {
   CodedArgs a{};
   a.W = w.codes;
   a.sw = w.scales;
@@ -555,8 +724,33 @@ hipError_t launch_coded_linear(const CodedView &w, int N, const CodedView &x, in
   a.T = T;
   a.nb = w.nb;
   a.K = w.nb * kBlk;
+  a.ldp = (N + 3) & ~3;
+  hipError_t e;
+  const bool fuse = src && T <= kFuseT;
+  if (src && !fuse) {
+    e = launch_encode_act(src, T, K, x, stream);
+    if (e != hipSuccess) return e;
+  }
   if (T <= kDecodeMaxT) {
-    hipLaunchKernelGGL(coded_stream_kernel<8>, dim3((N + 15) / 16), dim3(512), 0, stream, a);
+    a.ksplit = wide_slices(N, T, a.nb);
+    if (a.ksplit) {
+      a.steps_per_slice = (a.nb + a.ksplit - 1) / a.ksplit;
+      a.P = a.ksplit > 1 ? partials : nullptr;
+      const int tiles = (N + kWideRows - 1) / kWideRows;
+      hipLaunchKernelGGL(coded_wide_kernel, dim3(tiles * a.ksplit), dim3(kWideWaves * 64), 0, stream, a);
+      e = hipGetLastError();
+      return e != hipSuccess || a.ksplit == 1 ? e : launch_coded_sum(a, stream);
+    }
+    const int rounds = (N + 16 * kCUs - 1) / (16 * kCUs);
+    a.rows = (N + rounds * kCUs - 1) / (rounds * kCUs);
+    const dim3 grid((N + a.rows - 1) / a.rows);
+    if (fuse) {
+      a.x = src;
+      a.Kx = K;
+      hipLaunchKernelGGL(coded_stream_kernel<true>, grid, dim3(kStreamWaves * 64), 0, stream, a);
+    } else {
+      hipLaunchKernelGGL(coded_stream_kernel<false>, grid, dim3(kStreamWaves * 64), 0, stream, a);
+    }
     return hipGetLastError();
   }
   const CPlan p = plan_coded(N, T, a.nb);
@@ -564,9 +758,7 @@ hipError_t launch_coded_linear(const CodedView &w, int N, const CodedView &x, in
   a.nT = p.nT;
   a.ksplit = p.ksplit;
   a.steps_per_slice = p.per;
-  a.ldp = (N + 3) & ~3;
   a.P = p.ksplit > 1 ? partials : nullptr;
-  hipError_t e;
   switch (p.tile) {
     case 0: e = launch_coded_tile<CTile<256, 256, 2, 4, 2>>(a, stream); break;
     case 1:
@@ -575,11 +767,7 @@ hipError_t launch_coded_linear(const CodedView &w, int N, const CodedView &x, in
       break;
     default: e = launch_coded_tile<CTile<128, 64, 4, 2, 4>>(a, stream); break;
   }
-  if (e != hipSuccess || p.ksplit == 1) return e;
-  const int64_t n = static_cast<int64_t>(T) * (a.ldp / 4);
-  hipLaunchKernelGGL(coded_sum_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
-                     static_cast<const float *>(a.P), p.ksplit, T, N, a.ldp, y);
-  return hipGetLastError();
+  return e != hipSuccess || p.ksplit == 1 ? e : launch_coded_sum(a, stream);
 }
 
 }  // namespace wl

@@ -641,12 +641,13 @@ wl_status run_backward(const wl_bundle *h, int32_t layer, int32_t family, int32_
   }
   const int nout = no;
   const CodeShape cs = code_shape(T, c.K, false);
-  size_t need = 0;
+  size_t need = 0, products = 0;
   if (T > 0) {
     if ((st = check_code_buffer(d_xcode, xcode_bytes, cs.bytes, "checkpoint")) != WL_OK) return st;
     if ((st = check_aligned(d_dy, 2, "dy")) != WL_OK) return st;
     if ((st = check_aligned(d_ws, 256, "workspace")) != WL_OK) return st;
-    need = ws_backward_bytes(h->lo, T);
+    products = align256(std::max<size_t>(256, wl::backward_workspace_bytes(c, T)));
+    need = products + ws_w0_expand_bytes(h->lo);
     if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
     r[no++] = Range{d_xcode, cs.bytes, "the checkpoint"};
     r[no++] = Range{d_dy, static_cast<size_t>(T) * rv.out_dim * 2, "dy"};
@@ -661,7 +662,7 @@ wl_status run_backward(const wl_bundle *h, int32_t layer, int32_t family, int32_
     }
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T > 0 && h->lo.coded() && (o.dx || o.ds)) {
-    uint16_t *w0 = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(d_ws) + ws_backward_products(h->lo, T));
+    uint16_t *w0 = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(d_ws) + products);
     const hipError_t e = h->lo.fp8 ? wl::launch_dequantize_rows(c.W0f8, c.ldw0, c.q, c.Ntot, c.K, w0, s)
                                    : wl::launch_dequantize_mxfp4(c.W0f4, 2 * c.ldw0, c.sc4, c.Ntot, c.K, w0, s);
     if (e != hipSuccess) return hip_fail(e, "W0 expand launch");
@@ -994,14 +995,9 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
   if (need && (overlap(d_ws, need, d_y, yb) || overlap(d_ws, need, d_x, xb) || overlap(d_ws, need, d_xcode, cx.bytes) ||
                overlap(d_ws, need, d_wcode, cw.bytes)))
     return fail(WL_EINVAL, "the workspace must not overlap x, y or the code buffers");
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const wl::CodedView x = code_view(d_xcode, cx);
-  if (d_x) {
-    const hipError_t e = wl::launch_encode_act(static_cast<const uint16_t *>(d_x), T, K, x, s);
-    if (e != hipSuccess) return hip_fail(e, "encode launch");
-  }
-  const hipError_t e = wl::launch_coded_linear(code_view(d_wcode, cw), N, x, T, static_cast<uint16_t *>(d_y),
-                                               static_cast<float *>(d_ws), s);
+  const hipError_t e = wl::launch_coded_linear(code_view(d_wcode, cw), N, static_cast<const uint16_t *>(d_x), K,
+                                               code_view(d_xcode, cx), T, static_cast<uint16_t *>(d_y),
+                                               static_cast<float *>(d_ws), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? WL_OK : hip_fail(e, "kernel launch");
 }
 
