@@ -213,16 +213,18 @@ struct CodedArgs {
 // that the workgroups are a multiple of the CUs (21504 rows: 14, 21.5 us
 // against 22.5 at 16; 8 waves of 4 blocks 23.5; loads one pair ahead 35).
 //
-// FUSE (T <= kFuseT): x comes as bf16 and every wave codes the blocks it needs
-// -- 16 lanes to a block, as encode_act_kernel -- through its part of LDS;
-// workgroup 0 also writes the coded buffer.  It saves the coding launch, and
-// the arithmetic, repeated by every workgroup, hides under the weight loads
-// while there are few tokens.
+// FUSE (T <= kFuseT): x comes as bf16 and every wave codes the blocks it needs,
+// 16 lanes to a block as encode_act_kernel, through its part of LDS; workgroup
+// 0 also writes the coded buffer.  It saves the coding launch and the x loads'
+// turn (21504 x 5376 at T = 1: 25.2 us against 24.9 + 4 for the two launches,
+// 4096 x 1152: 3.5 against 3.0 + 3).  Two blocks a lane group, which would take
+// 4 tokens, spills at 8 waves per SIMD: 47 us.
 constexpr int kStreamWaves = 16, kStreamPair = 2;
-constexpr int kFuseT = 4;
+constexpr int kFuseT = 4 / kStreamPair;  // a wave's 4 groups of 16 lanes code a pair's blocks at once
 
 template <bool FUSE>
-__global__ __launch_bounds__(kStreamWaves * 64) void coded_stream_kernel(CodedArgs a) {
+__global__ __launch_bounds__(kStreamWaves * 64) __attribute__((amdgpu_waves_per_eu(8, 8))) void
+coded_stream_kernel(CodedArgs a) {
   constexpr int NW = kStreamWaves, S = kStreamPair;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, g = lane >> 4;
@@ -241,16 +243,12 @@ __global__ __launch_bounds__(kStreamWaves * 64) void coded_stream_kernel(CodedAr
   for (int b = wave * S; b < a.nb; b += NW * S) {
     u32x4 w[S][2], x[S][2];
     int sw[S], sx[S];
-    // FUSE: block u of S * T per pass of four, its lanes 8 elements each
-    u32x4 v[FUSE ? kFuseT * S / 4 : 1];
+    // FUSE: 16 lanes to a block (token t, block i of the pair), 8 elements each
+    const int t = g / S, ti = g % S;
+    u32x4 v = zero;
     if constexpr (FUSE) {
-#pragma unroll
-      for (int p = 0; p < kFuseT * S / 4; ++p) {
-        if (p * 4 / S >= a.T) break;
-        const int u = p * 4 + g, t = u / S, k = (b + u % S) * kBlk + r16 * 8;
-        v[p] = zero;
-        if (t < a.T && k < a.Kx) v[p] = ld16(a.x + static_cast<int64_t>(t) * a.Kx + k);
-      }
+      const int k = (b + ti) * kBlk + r16 * 8;
+      if (t < a.T && k < a.Kx) v = ld16(a.x + static_cast<int64_t>(t) * a.Kx + k);
     }
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -264,25 +262,20 @@ __global__ __launch_bounds__(kStreamWaves * 64) void coded_stream_kernel(CodedAr
     }
     if constexpr (FUSE) {
       asm volatile("" ::: "memory");
+      uint32_t m = amax_bits(v);
 #pragma unroll
-      for (int p = 0; p < kFuseT * S / 4; ++p) {
-        if (p * 4 / S >= a.T) break;
-        const int u = p * 4 + g, t = u / S, i = u % S;
-        uint32_t m = amax_bits(v[p]);
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 16)));
-        const int e = block_exponent(m);
-        const u32x2 c = code8(v[p], e);
-        *reinterpret_cast<u32x2 *>(&xc[wave][t][i * kBlk + r16 * 8]) = c;
-        if (r16 == 0) xs[wave][t][i] = static_cast<uint8_t>(e + 127);
-        if (blockIdx.x == 0 && b + i < a.nb) {
-          if (t < a.T)
-            *reinterpret_cast<u32x2 *>(const_cast<uint8_t *>(a.X) + static_cast<int64_t>(t) * a.K + (b + i) * kBlk + r16 * 8) = c;
-          // a block's 16 scale bytes: the tokens', and 127 behind them
-          uint8_t *so = const_cast<uint8_t *>(a.sx) + static_cast<int64_t>(b + i) * a.ldsx;
-          if (r16 == 0 && t < a.T) so[t] = static_cast<uint8_t>(e + 127);
-          if (t == 0 && r16 >= a.T) so[r16] = 127;
-        }
+      for (int d = 1; d < 16; d <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 16)));
+      const int e = block_exponent(m);
+      const u32x2 c = code8(v, e);
+      *reinterpret_cast<u32x2 *>(&xc[wave][t][ti * kBlk + r16 * 8]) = c;
+      if (r16 == 0) xs[wave][t][ti] = static_cast<uint8_t>(e + 127);
+      if (blockIdx.x == 0 && b + ti < a.nb) {
+        if (t < a.T)
+          *reinterpret_cast<u32x2 *>(const_cast<uint8_t *>(a.X) + static_cast<int64_t>(t) * a.K + (b + ti) * kBlk + r16 * 8) = c;
+        // a block's 16 scale bytes: the tokens', and 127 behind them
+        uint8_t *so = const_cast<uint8_t *>(a.sx) + static_cast<int64_t>(b + ti) * a.ldsx;
+        if (r16 == 0 && t < a.T) so[t] = static_cast<uint8_t>(e + 127);
+        if (t == 0 && r16 >= a.T) so[r16] = 127;
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
@@ -328,6 +321,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void coded_stream_kernel(CodedAr
 // coded_sum_kernel (252 workgroups of 3 slices and the sum: 26.4 us).  The
 // scale bytes of a slice (at most kStreamSlice blocks) wait in LDS.
 constexpr int kWideRows = 64, kWideWaves = 8, kStreamSlice = 256;
+constexpr int kNarrowT = 4;  // up to here the one-tile kernel, which needs no workspace
 
 __global__ __launch_bounds__(kWideWaves * 64) void coded_wide_kernel(CodedArgs a) {
   constexpr int NW = kWideWaves, RT = kWideRows / 16;
@@ -636,12 +630,13 @@ CPlan plan_coded(int N, int T, int nb) {
 }
 
 // Slices of the several-token stream, 0 for the one-tile kernel (which needs
-// none): the fewest whose workgroups come within 15% of whole rounds of the
-// CUs, of at least 8 blocks (one per wave); calls too small to fill the CUs
-// that way take one-tile workgroups (4096 x 1152 at T = 16: 4.0 us against
-// 6.2).
+// none).  It pays for its summing launch (4 us) where the x loads it saves are
+// worth more: from 64 M codes on (21504 x 5376 at T = 16: 30.6 us against
+// 33.3, 5376 x 21504: 28.8 against 39.5; 8192 x 5376: 13.2 against 12.2, 4096 x
+// 5376: 10.4 against 7.3).  The slices are the fewest whose workgroups come
+// within 15% of whole rounds of the CUs, of at least 8 blocks (one per wave).
 int wide_slices(int N, int T, int nb) {
-  if (T <= kFuseT) return 0;
+  if (T <= kNarrowT || static_cast<int64_t>(N) * nb * kBlk < (int64_t{64} << 20)) return 0;
   const int tiles = (N + kWideRows - 1) / kWideRows;
   const int least = (nb + kStreamSlice - 1) / kStreamSlice;
   int best = 0;
