@@ -378,9 +378,10 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
  *   ds_n = sum_k G[n][k] W0[n][k],  dW0 = diag(s) G,  G = dy^T X
  *   dU  = dy^T (X V),  dV = X^T (dy U)
  * W0 is the block the bundle holds (FP8 and MXFP4 bundles: the values of its
- * codes).  Products of bf16 operands with float32 sums; dy (.) s, X V and
- * dy U are rounded to bf16 once as operands, dx, dU and dV once at the end;
- * G, ds and dW0 are float32 throughout.  Results are the same bits from run
+ * codes).  Products of bf16 operands with float32 sums; as operands dy (.) s
+ * is rounded to bf16 once and X V and dy U are kept as a pair of bf16 (16
+ * significant bits); dx, dU and dV are rounded once at the end; G, ds and dW0
+ * are float32 throughout.  Results are the same bits from run
  * to run. */
 typedef struct {
   void *dx;         /* bf16 [T, K] */

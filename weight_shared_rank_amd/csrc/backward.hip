@@ -4,7 +4,7 @@
 // children concatenated.  With X the values of the checkpoint (code * 2^e,
 // bf16 exactly) and dy the output's gradient:
 //
-//   z = X V,  g = dy U                      (thin products, bf16)
+//   z = X V,  g = dy U                      (thin products)
 //   dx  = (dy (.) s) W0 + g V^T
 //   G   = dy^T X                            (fp32, never stored)
 //   dW0 = diag(s) G        ds_n = sum_k G[n][k] W0[n][k]
@@ -23,9 +23,12 @@
 // transposed on its way to the registers by ds_read_b64_tr_b16, so no
 // transposed copy of a weight or of dy is ever written.
 //
-// What is rounded to bf16 on the way: dy (.) s, z and g, each once, as
-// operands of the matrix cores (z as in the forward).  G is exact products of
-// bf16 values summed in fp32, and dW0 and ds stay fp32.
+// What is rounded on the way, as the matrix cores take bf16 operands: dy (.) s
+// once to bf16, and z and g to a pair of bf16 (the value and what its rounding
+// left, 16 significant bits, as decode keeps z), which enter their products as
+// two runs of the contraction: with one bf16 the errors of dU and dV against
+// 64 bits were 1.5 times those of rounding the results alone.  G is exact
+// products of bf16 values summed in fp32, and dW0 and ds stay fp32.
 #include <algorithm>
 #include <type_traits>
 
@@ -45,7 +48,7 @@ typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 constexpr int kStep = 64;  // contraction values a product is planned and split in
 constexpr int kCUs = 256;
-constexpr int kMaxSeg = 4;
+constexpr int kMaxSeg = 5;  // dx: dy's slots (q, k and a tied v), then the pair of g
 constexpr int kMaxProb = 1 + 3 * kMaxChildren;  // dx; G, dU and dV of every child
 constexpr int kGroupN = 8;  // output tiles along b that run together
 
@@ -58,8 +61,8 @@ struct Seg {
 
 // How the operands lie: A and B k-rows; A k-columns, B k-rows; both k-columns.
 enum Kind : int32_t { kRowsRows = 0, kColsRows = 1, kColsCols = 2 };
-// What becomes of C: bf16 rows, or (G) dW0 and ds.
-enum ProbMode : int32_t { kBf16 = 0, kWeight = 1 };
+// What becomes of C: bf16 rows, a pair of bf16 rows, or (G) dW0 and ds.
+enum ProbMode : int32_t { kBf16 = 0, kPair = 1, kWeight = 2 };
 
 // One product C[N][M] of a launch.
 struct Prob {
@@ -69,8 +72,9 @@ struct Prob {
   int32_t kind, mode;
   int32_t nM, nN, ksplit, per;  // tiles, slices of the contraction, steps per slice
   int32_t unit0;      // first workgroup of its launch
-  uint16_t *out;      // kBf16: [N][ldo]
+  uint16_t *out;      // kBf16, kPair: [N][ldo]
   int64_t ldo;
+  int32_t lo;         // kPair: columns from a value to what its rounding left
   float *P;           // ksplit > 1: partials [ksplit][N][ldp]
   int32_t ldp;
   // kWeight: G's consumers
@@ -248,6 +252,41 @@ __device__ __forceinline__ void store_weight_grad(const f32x4 (&acc)[TL::FM][TL:
   }
 }
 
+// A bf16 tile in LDS, b-major, then whole 16-byte chunks of output rows, `at`
+// columns on.
+template <typename TL>
+__device__ __forceinline__ void store_rows(const f32x4 (&acc)[TL::FM][TL::FN], const Prob &p, int m0, int n0, int at,
+                                           uint8_t *lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WN, wn = wave % TL::WN, r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const int tl = wn * TL::TN + j * 16 + r16, fl = wm * TL::TM + i * 16 + g * 4;
+      *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) =
+          make_uint2(f32_to_bf16(acc[i][j][0]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][1])) << 16),
+                     f32_to_bf16(acc[i][j][2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][3])) << 16));
+    }
+  __syncthreads();
+  constexpr int CPR = TL::BM / 8;
+  for (int c = threadIdx.x; c < TL::BN * CPR; c += TL::NW * 64) {
+    const int tl = c / CPR, fl = (c % CPR) * 8;
+    const int n = n0 + tl, m = m0 + fl;
+    if (n >= p.N || m >= p.M) continue;
+    const uint4 val = *reinterpret_cast<const uint4 *>(lds + tl * TL::PITCH + fl * 2);
+    uint16_t *o = p.out + static_cast<int64_t>(n) * p.ldo + m + at;
+    if (m + 8 <= p.M && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+      *reinterpret_cast<uint4 *>(o) = val;
+    } else {
+      const uint32_t e[4] = {val.x, val.y, val.z, val.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (m + i < p.M) o[i] = static_cast<uint16_t>(e[i / 2] >> (16 * (i & 1)));
+    }
+  }
+}
+
 // Loads of a stage into `w`: all of it, or all but the last instruction (the
 // first of its two steps when a stage is two halves deep), or that last one.
 enum Part : int { kAll = 0, kFirst = 1, kLast = 2 };
@@ -397,32 +436,17 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
     if constexpr (ATR && BTR) store_weight_grad<TL>(acc, p, f, m0, n0);
     return;
   }
-  // bf16 tile in LDS, b-major, then whole 16-byte chunks of output rows
+  store_rows<TL>(acc, p, m0, n0, 0, lds);
+  if constexpr (TL::BM == 128) {  // pairs are planned on these tiles only
+    if (p.mode != kPair) return;
+    __syncthreads();
 #pragma unroll
-  for (int j = 0; j < TL::FN; ++j)
+    for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
-    for (int i = 0; i < TL::FM; ++i) {
-      const int tl = wn * TL::TN + j * 16 + r16, fl = wm * TL::TM + i * 16 + g * 4;
-      *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) =
-          make_uint2(f32_to_bf16(acc[i][j][0]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][1])) << 16),
-                     f32_to_bf16(acc[i][j][2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][3])) << 16));
-    }
-  __syncthreads();
-  constexpr int CPR = TL::BM / 8;
-  for (int c = threadIdx.x; c < TL::BN * CPR; c += TL::NW * 64) {
-    const int tl = c / CPR, fl = (c % CPR) * 8;
-    const int n = n0 + tl, m = m0 + fl;
-    if (n >= p.N || m >= p.M) continue;
-    const uint4 val = *reinterpret_cast<const uint4 *>(lds + tl * TL::PITCH + fl * 2);
-    uint16_t *o = p.out + static_cast<int64_t>(n) * p.ldo + m;
-    if (m + 8 <= p.M && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-      *reinterpret_cast<uint4 *>(o) = val;
-    } else {
-      const uint32_t e[4] = {val.x, val.y, val.z, val.w};
+      for (int i = 0; i < TL::FM; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (m + i < p.M) o[i] = static_cast<uint16_t>(e[i / 2] >> (16 * (i & 1)));
-    }
+        for (int e = 0; e < 4; ++e) acc[i][j][e] -= bf16_to_f32(f32_to_bf16(acc[i][j][e]));
+    store_rows<TL>(acc, p, m0, n0, p.lo, lds);
   }
 }
 
@@ -459,7 +483,7 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
 }
 
 // What is left after the products, one launch: for a split product the sum of
-// its slices' partials in slice order -- rows of C rounded to bf16 (a thread
+// its slices' partials in slice order -- rows of C as bf16 or a pair (a thread
 // per 4 elements), or dW0's row and ds[n] (a workgroup per row n of G) -- and
 // for an unsplit G ds from its column tiles' partial sums (16 rows n per
 // workgroup, 16 lanes per row each summing every 16th part, joined in order).
@@ -501,18 +525,26 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
     }
     return;
   }
-  if (p.mode == kBf16) {
+  if (p.mode != kWeight) {
     const int64_t id = b * 256 + threadIdx.x;
     if (id >= static_cast<int64_t>(p.N) * q) return;
     const int64_t n = id / q;
     const int m = static_cast<int>(id % q) * 4;
-    const f32x4 s = sum_slices(p, n, m);
-    uint16_t *o = p.out + n * p.ldo + m;
-    if (m + 4 <= p.M && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
-      *reinterpret_cast<uint2 *>(o) = make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
-                                                 f32_to_bf16(s[2]) | (static_cast<uint32_t>(f32_to_bf16(s[3])) << 16));
-    } else {
-      for (int e = 0; e < 4 && m + e < p.M; ++e) o[e] = f32_to_bf16(s[e]);
+    f32x4 s = sum_slices(p, n, m);
+    for (int pass = 0; pass < (p.mode == kPair ? 2 : 1); ++pass) {
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = f32_to_bf16(s[e]);
+      uint16_t *o = p.out + n * p.ldo + m + pass * p.lo;
+      if (m + 4 <= p.M && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (m + e < p.M) o[e] = static_cast<uint16_t>(v[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] -= bf16_to_f32(static_cast<uint16_t>(v[e]));
     }
     return;
   }
@@ -635,12 +667,12 @@ hipError_t launch_zero(void *p, int64_t halves, hipStream_t stream) {
 
 // ---- host side --------------------------------------------------------------
 
-// 256 x 256 tiles, a launch per kind.  Stage depth by the operands: k-column
+// 256 x 256 tiles, a launch per kind (A is k-columns).  Stage depth by B: k-column
 // rows are long whatever the depth, so four shallow stages keep more loads in
 // flight; a k-row operand wants whole 128-byte lines (with 64-byte rows a bare
 // load loop ran at 57 KB/us per CU instead of 92).
-template <bool ATR, bool BTR>
-using Big = std::conditional_t<ATR && BTR, BTile<256, 256, 2, 4, 32, 4>, BTile<256, 256, 2, 4, 64, 2>>;
+template <bool BTR>
+using Big = std::conditional_t<BTR, BTile<256, 256, 2, 4, 32, 4>, BTile<256, 256, 2, 4, 64, 2>>;
 // 128 x 128 tiles, every kind in one launch: with a ring of two stages two
 // workgroups share a CU, with four one keeps as many loads in flight.
 using Mid2 = BTile<128, 128, 2, 4, 64, 2>;
@@ -657,6 +689,7 @@ struct BPlan {
 // A product as the planner sees it: extents and contraction steps.
 struct Item {
   int M, N, steps;
+  bool pair;  // z and g: 128 x 128 tiles only, which store pairs
 };
 
 // Microseconds (fitted to the 31B and 1B shapes): a step and the fixed part of
@@ -698,7 +731,7 @@ void plan_batch(const Item *it, int n, BPlan *out) {
       }
     }
     const int mM = (it[i].M + 127) / 128, mN = (it[i].N + 127) / 128;
-    p.big = best < static_cast<double>(mM) * mN * (it[i].steps * kMidPairStep + kMidFix) / (2 * kCUs) &&
+    p.big = !it[i].pair && best < static_cast<double>(mM) * mN * (it[i].steps * kMidPairStep + kMidFix) / (2 * kCUs) &&
             tiles * p.ksplit * 2 >= kCUs;
     if (!p.big) {
       p.nM = mM;
@@ -789,9 +822,9 @@ Plans plans_of(const CallDesc &c, const Slots &s, int T) {
   Item it[kMaxProb];
   BPlan *to[kMaxProb], got[kMaxProb];
   int n = 0;
-  auto add = [&](int M, int N, int steps, BPlan &dst) {
+  auto add = [&](int M, int N, int steps, BPlan &dst, bool pair = false) {
     if (M == 0) return;
-    it[n] = Item{M, N, steps};
+    it[n] = Item{M, N, steps, pair};
     to[n++] = &dst;
   };
   auto done = [&] {
@@ -804,23 +837,23 @@ Plans plans_of(const CallDesc &c, const Slots &s, int T) {
     p.part = std::max(p.part, bytes);
     n = 0;
   };
-  add(c.Rz, T, steps_of(c.K), p.z);
-  for (int i = 0; i < c.nchild; ++i) add(c.ch[i].rpad, T, slots_of_child(s, i) * steps_of(c.ch[i].N), p.g[i]);
+  add(c.Rz, T, steps_of(c.K), p.z, true);
+  for (int i = 0; i < c.nchild; ++i) add(c.ch[i].rpad, T, slots_of_child(s, i) * steps_of(c.ch[i].N), p.g[i], true);
   done();
-  int dx_steps = steps_of(c.Rz);
+  int dx_steps = 2 * steps_of(c.Rz);  // g's pair
   for (int i = 0; i < s.n; ++i) dx_steps += steps_of(s.cols[i]);
   add(c.K, T, dx_steps, p.dx);
   for (int i = 0; i < c.nchild; ++i) {
     const int steps = slots_of_child(s, i) * steps_of(T);
     add(c.K, c.ch[i].N, steps, p.G[i]);
-    add(c.ch[i].rpad, c.ch[i].N, steps, p.du[i]);
-    add(c.ch[i].rpad, c.K, steps_of(T), p.dv[i]);
+    add(c.ch[i].rpad, c.ch[i].N, 2 * steps, p.du[i]);
+    add(c.ch[i].rpad, c.K, 2 * steps_of(T), p.dv[i]);
   }
   done();
   return p;
 }
 
-// Workspace: X bf16 [T][K], dy copies [T][ldd] x 2, z and g [T][Rz], the ds
+// Workspace: X bf16 [T][K], dy copies [T][ldd] x 2, z and g as pairs [T][2 Rz], the ds
 // partial sums, and the K-split partials of a batch.
 struct Offsets {
   size_t x, dyp, dys, z, g, dsp, part, bytes;
@@ -837,8 +870,8 @@ Offsets offsets_of(const CallDesc &c, const Slots &s, const Plans &p, int T) {
   o.x = take(static_cast<size_t>(T) * c.K * 2);
   o.dyp = take(static_cast<size_t>(T) * s.ldd * 2);
   o.dys = take(static_cast<size_t>(T) * s.ldd * 2);
-  o.z = take(static_cast<size_t>(T) * c.Rz * 2);
-  o.g = take(static_cast<size_t>(T) * c.Rz * 2);
+  o.z = take(static_cast<size_t>(T) * c.Rz * 4);
+  o.g = take(static_cast<size_t>(T) * c.Rz * 4);
   o.dsp = take(static_cast<size_t>((c.K + 127) / 128) * 2 * c.Ntot * 4);
   o.part = take(p.part);
   o.bytes = at;
@@ -860,9 +893,9 @@ hipError_t launch_kernel(const BwdArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool ATR, bool BTR>
+template <bool BTR>
 hipError_t launch_big(const BwdArgs &a, hipStream_t stream) {
-  return launch_kernel<Big<ATR, BTR>, product_kernel<Big<ATR, BTR>, ATR, BTR>>(a, stream);
+  return launch_kernel<Big<BTR>, product_kernel<Big<BTR>, true, BTR>>(a, stream);
 }
 
 void add_units(BwdArgs &a, const Prob &p) {
@@ -875,14 +908,12 @@ void add_units(BwdArgs &a, const Prob &p) {
 // workgroups first -- and the launch that sums what they left.
 hipError_t launch_batch(const Batch &b, hipStream_t stream) {
   hipError_t e;
-  for (int kind = kRowsRows; kind <= kColsCols; ++kind) {
+  for (int kind = kColsRows; kind <= kColsCols; ++kind) {  // (dx and G)
     BwdArgs a{};
     for (int i = 0; i < b.n; ++i)
       if (b.big[i] && b.p[i].kind == kind) add_units(a, b.p[i]);
     if (!a.nprob) continue;
-    e = kind == kColsCols   ? launch_big<true, true>(a, stream)
-        : kind == kColsRows ? launch_big<true, false>(a, stream)
-                            : launch_big<false, false>(a, stream);
+    e = kind == kColsCols ? launch_big<true>(a, stream) : launch_big<false>(a, stream);
     if (e != hipSuccess) return e;
   }
   int order[kMaxProb], nmid = 0;
@@ -1005,20 +1036,25 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }
+  const int64_t ldz = 2 * static_cast<int64_t>(c.Rz);  // z and g: the values, then the remainders
   auto column = [&](int slot) { return dyp + (direct ? s.from[slot] : s.start[slot]); };
   {
     // z = X V and g = dy U
     uint8_t *part = ws + at.part;
     Batch b;
     if (want_u) {
-      Prob &p = add_product(b, pl.z, kRowsRows, c.Rz, c.Rz, T, z, c.Rz, part);
+      Prob &p = add_product(b, pl.z, kRowsRows, c.Rz, c.Rz, T, z, ldz, part);
+      p.mode = kPair;
+      p.lo = c.Rz;
       add_seg(p, c.Vt, K, X, K, K);
     }
     if (want_g)
       for (int i = 0; i < c.nchild; ++i) {
         const ChildDesc &ch = c.ch[i];
         if (!ch.rpad) continue;
-        Prob &p = add_product(b, pl.g[i], kColsRows, ch.rpad, ch.rpad, T, g + ch.zoff, c.Rz, part);
+        Prob &p = add_product(b, pl.g[i], kColsRows, ch.rpad, ch.rpad, T, g + ch.zoff, ldz, part);
+        p.mode = kPair;
+        p.lo = c.Rz;
         for (int j = 0; j < s.n; ++j)
           if (s.child[j] == i) add_seg(p, ch.U, ch.rpad, column(j), ldp, ch.N);
       }
@@ -1031,7 +1067,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     Prob &p = add_product(b, pl.dx, kColsRows, K, K, T, o.dx, K, part);
     for (int j = 0; j < s.n; ++j)
       add_seg(p, c.W0 + static_cast<int64_t>(c.ch[s.child[j]].row_start) * K, K, dys + s.start[j], s.ldd, s.cols[j]);
-    if (c.Rz > 0) add_seg(p, c.Vt, K, g, c.Rz, c.Rz);
+    for (int lo = 0; lo < 2 && c.Rz > 0; ++lo) add_seg(p, c.Vt, K, g + lo * c.Rz, ldz, c.Rz);
   }
   for (int i = 0; i < c.nchild; ++i) {
     // G (dW0 and ds), dU and dV: contractions over the tokens
@@ -1054,11 +1090,11 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     }
     if (o.du[i] && o.r[i]) {
       Prob &p = add_product(b, pl.du[i], kColsCols, o.r[i], ch.rpad, ch.N, o.du[i], o.r[i], part);
-      add_tokens(p, z + ch.zoff, c.Rz);
+      for (int lo = 0; lo < 2; ++lo) add_tokens(p, z + ch.zoff + lo * c.Rz, ldz);
     }
     if (o.dv[i] && o.r[i]) {
       Prob &p = add_product(b, pl.dv[i], kColsCols, o.r[i], ch.rpad, K, o.dv[i], o.r[i], part);
-      add_seg(p, g + ch.zoff, c.Rz, X, K, T);
+      for (int lo = 0; lo < 2; ++lo) add_seg(p, g + ch.zoff + lo * c.Rz, ldz, X, K, T);
     }
   }
   return launch_batch(b, stream);
