@@ -265,8 +265,8 @@ __device__ __forceinline__ void store_rows(const f32x4 (&acc)[TL::FM][TL::FN], c
     for (int i = 0; i < TL::FM; ++i) {
       const int tl = wn * TL::TN + j * 16 + r16, fl = wm * TL::TM + i * 16 + g * 4;
       *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) =
-          make_uint2(f32_to_bf16(acc[i][j][0]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][1])) << 16),
-                     f32_to_bf16(acc[i][j][2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][3])) << 16));
+          make_uint2(pack_bf16(acc[i][j][0], acc[i][j][1]),
+                     pack_bf16(acc[i][j][2], acc[i][j][3]));
     }
   __syncthreads();
   constexpr int CPR = TL::BM / 8;
@@ -577,7 +577,9 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
 // dy [T][ldy] -> rows of ldd columns in which every child's slot starts at a
 // multiple of 8 (zeros behind a slot's last column): the plain copy `dyp`
 // and/or dy (.) s rounded to bf16, `dys`; and the checkpoint's values X (bf16
-// [T][K]).  One launch: the first dyb workgroups in y take dy, the others X.
+// [T][K]).  One launch: workgroups run along a group of tokens, its first dyb
+// take dy, the others X.  Bound by memory: the 31B gate|up call's 390 MB at
+// T = 2048 in 61 us (105 with s loaded element by element).
 struct PrepArgs {
   const uint16_t *dy;
   int32_t T, ldy, ldd, nslot;
@@ -586,35 +588,47 @@ struct PrepArgs {
   int32_t n[kMaxChildren];          // slot -> columns
   const float *s[kMaxChildren];
   uint16_t *dyp, *dys;
-  int32_t dyb;
+  int32_t dyb, cols;  // workgroups across dy's columns, and across all columns
   CodedView xc;
   int32_t K;
   uint16_t *X;
 };
 
-// A thread takes 8 columns of kPrepT tokens: s is read once for all of them.
+// A thread takes 8 columns of kPrepT tokens: s is read once for all of them (2
+// tokens 66 us, 8 115).
 constexpr int kPrepT = 4;
 
 __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
-  if (static_cast<int>(blockIdx.y) >= a.dyb) {
-    const int k = ((blockIdx.y - a.dyb) * 256 + threadIdx.x) * 8;
+  const int col = blockIdx.x % a.cols;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / a.cols) * kPrepT;
+  if (col >= a.dyb) {
+    const int k = ((col - a.dyb) * 256 + threadIdx.x) * 8;
     if (k >= a.K) return;
 #pragma unroll
     for (int i = 0; i < kPrepT; ++i) {
-      const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepT + i;
+      const int64_t t = t0 + i;
       if (t < a.T) *reinterpret_cast<u32x4 *>(a.X + t * a.K + k) = expand8(a.xc, t, k);
     }
     return;
   }
-  const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
+  const int c = (col * 256 + threadIdx.x) * 8;
   if (c >= a.ldd) return;
   int i = 0;
   while (i + 1 < a.nslot && c >= a.start[i + 1]) ++i;
   const int j = c - a.start[i], n = a.n[i] - j;  // n: columns of the slot from here on (>= 1)
   float s[8];
+  if (a.dys && n >= 8) {  // a slot's s starts at any row: 4-byte aligned
+    typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+    const f32x4 lo = *reinterpret_cast<const f32x4_any *>(a.s[i] + j), hi = *reinterpret_cast<const f32x4_any *>(a.s[i] + j + 4);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s[k] = a.dys && k < n ? a.s[i][j + k] : 0.f;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kPrepT;
+    for (int k = 0; k < 4; ++k) {
+      s[k] = lo[k];
+      s[4 + k] = hi[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = a.dys && k < n ? a.s[i][j + k] : 0.f;
+  }
   const uint16_t *src = a.dy + t0 * a.ldy + a.from[i] + j;
   const int nt = static_cast<int>(min<int64_t>(kPrepT, a.T - t0));
   u32x4 v[kPrepT];
@@ -640,13 +654,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
     if (a.dys) {
       u32x4 o;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = 2 * k >= n ? 0u
-                          : f32_to_bf16(__uint_as_float(v[t][k] << 16) * s[2 * k]) |
-                                (2 * k + 1 >= n ? 0u
-                                                : static_cast<uint32_t>(f32_to_bf16(
-                                                      __uint_as_float(v[t][k] & 0xffff0000u) * s[2 * k + 1]))
-                                                      << 16);
+      for (int k = 0; k < 4; ++k)  // columns past the slot: dy and s are 0
+        o[k] = pack_bf16(__uint_as_float(v[t][k] << 16) * s[2 * k], __uint_as_float(v[t][k] & 0xffff0000u) * s[2 * k + 1]);
       *reinterpret_cast<u32x4 *>(a.dys + at) = o;
     }
   }
@@ -1031,8 +1040,9 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     a.K = K;
     a.X = X;
     const int xb = want_u || want_v || want_w ? (K / 8 + 255) / 256 : 0;
-    if (a.dyb + xb > 0) {
-      hipLaunchKernelGGL(prepare_kernel, dim3((T + kPrepT - 1) / kPrepT, a.dyb + xb), dim3(256), 0, stream, a);
+    a.cols = a.dyb + xb;
+    if (a.cols > 0) {
+      hipLaunchKernelGGL(prepare_kernel, dim3((T + kPrepT - 1) / kPrepT * a.cols), dim3(256), 0, stream, a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

@@ -18,8 +18,8 @@ __device__ __forceinline__ u32x4 expand8(const CodedView &c, int64_t t, int k) {
   for (int h = 0; h < 2; ++h) {
     const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), false);
     const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), true);
-    o[2 * h] = f32_to_bf16(a[0] * f) | (static_cast<uint32_t>(f32_to_bf16(a[1] * f)) << 16);
-    o[2 * h + 1] = f32_to_bf16(b[0] * f) | (static_cast<uint32_t>(f32_to_bf16(b[1] * f)) << 16);
+    o[2 * h] = pack_bf16(a[0] * f, a[1] * f);
+    o[2 * h + 1] = pack_bf16(b[0] * f, b[1] * f);
   }
   return o;
 }

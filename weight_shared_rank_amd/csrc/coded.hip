@@ -553,8 +553,8 @@ coded_gemm_kernel(CodedArgs a) {
       for (int q = 0; q < 4; ++q) {
         const int tl = wn * TL::TN + j * 32 + r32, fl = wm * TL::TM + i * 32 + q * 8 + g * 4;
         *reinterpret_cast<uint2 *>(lds + tl * TL::PITCH + fl * 2) = make_uint2(
-            f32_to_bf16(acc[i][j][4 * q]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * q + 1])) << 16),
-            f32_to_bf16(acc[i][j][4 * q + 2]) | (static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * q + 3])) << 16));
+            pack_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+            pack_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
       }
   __syncthreads();
   constexpr int CPR = TL::BM / 8;
@@ -587,8 +587,8 @@ __global__ __launch_bounds__(256) void coded_sum_kernel(const float *P, int kspl
     s += *reinterpret_cast<const f32x4 *>(P + (static_cast<int64_t>(i) * T + tok) * ldp + row);
   uint16_t *p = Y + tok * N + row;
   if (row + 4 <= N && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
-                                               f32_to_bf16(s[2]) | (static_cast<uint32_t>(f32_to_bf16(s[3])) << 16));
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(s[0], s[1]),
+                                               pack_bf16(s[2], s[3]));
   } else {
     for (int e = 0; e < 4 && row + e < N; ++e) p[e] = f32_to_bf16(s[e]);
   }
