@@ -409,6 +409,8 @@ size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T);
  *    looked at.  dx and dw0 16-byte, ds 4-byte, du and dv 2-byte aligned; no
  *    output may overlap another, dy, the checkpoint, the workspace or the arena
  *    (WL_EINVAL).
+ *  The call's columns of dy number at most 2^21 - 256 and its padded ranks half
+ *    that (WL_ESHAPE).
  *  T = 0: ds, du, dv and dw0 (unless accumulated) are zeroed.
  *  d_ws: weightless_backward_workspace_bytes(bundle, T), 256-byte aligned, no
  *    initialization, nothing kept; concurrent calls need distinct workspaces. */

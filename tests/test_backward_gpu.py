@@ -159,6 +159,8 @@ def same_bits(a, b):
             same_bits(x, y)
         elif x is not None:
             assert torch.equal(x, y)
+        else:
+            assert y is None
 
 
 O, GU, QKV = ("o",), ("gate", "up"), ("q", "k", "v")
@@ -388,6 +390,38 @@ def test_forward_checkpoint_backward_together(gpu_lib):
     assert abs(full - (g.ds.double() ** 2).sum().item()) <= 2.0 ** -4 * mass
 
 
+def test_widest_calls(gpu_lib):
+    """More columns than a load can address are refused; just under it (one
+    family of 2^20 rows, beyond what 32-bit element offsets of a token reach)
+    the last rows are right."""
+    n = 1 << 20
+    wide = Layer(QKV, (n, n, n), 8, (0, 0, 0), seed=14)
+    code, dy = binding.encode_act(randn(60, 3, 8)), randn(61, 3, 3 * n)
+    announce("2^20 rows")
+    with pytest.raises(binding.WlError, match="WL_ESHAPE"):
+        wide.backward(code, dy)
+    g = wide.bundle.linear_backward(0, "v", code, dy[:, 2 * n:].contiguous(), want=("dx", "ds", "dw0"))
+    D, X, w, s = dy[:, 2 * n:].double(), code.expand().double(), wide.w0[2].double(), wide.s[2].double()
+    G = D.t().contiguous() @ X
+    mass = D.t().abs().contiguous() @ X.abs()
+    assert ((g.dw0 - s[:, None] * G).abs() <= 11 * F * s.abs()[:, None] * mass).all()
+    assert ((g.ds - (G * w).sum(1)).abs() <= 19 * F * (mass * w.abs()).sum(1)).all()
+    ref, top = (D * s) @ w, (D.abs() * s.abs()) @ w.abs()
+    assert ((g.dx - ref).abs() <= (H + (n + 8) * F) * top + H * ref.abs()).all()
+    assert (g.dx.double() - ref).norm() <= 2 * H * ref.norm()
+
+
+def test_dw0_alone_of_a_coded_block_needs_no_block(gpu_lib):
+    """dW0 of FP8 and MXFP4 bundles without dx or ds, split over the tokens or
+    not: W0 is not expanded and not read."""
+    for fmt in ("fp8", "mxfp4"):
+        for T, rows in ((40, 300), (2500, 24)):
+            lay = Layer(O, (rows,), 264, (8,), fmt=fmt, seed=15)
+            code, dy = binding.encode_act(randn(62, T, 264)), randn(63, T, rows)
+            announce(f"dw0 {fmt} T={T}")
+            same_bits(lay.backward(code, dy, want=("dw0",)), lay.backward(code, dy)._replace(dx=None, ds=None, du=None, dv=None))
+
+
 def test_binding_refusals(gpu_lib):
     lay = Layer(GU, (40, 40), 64, (4, 4), seed=13)
     code, dy = binding.encode_act(randn(50, 6, 64)), randn(51, 6, 80)
@@ -412,6 +446,8 @@ def test_binding_refusals(gpu_lib):
         lay.backward(code, dy, want=("dw0",), dw0=torch.zeros(80, 64, dtype=torch.bfloat16, device=DEV))
     with pytest.raises(E, match="WL_ENOSPACE"):
         lay.backward(code, dy, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(E, match="ws must be"):
+        lay.backward(code, dy, ws=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(E, match="WL_ERANGE"):
         lay.bundle.stacked_backward(0, "qkv", code, dy)
     # outputs that overlap an input or each other, and misaligned ones (host checks, nothing runs)

@@ -312,5 +312,7 @@ def test_binding_refusals(gpu_lib):
         binding.coded_linear(wc, x, code=binding.ActCode(9, 128))
     with pytest.raises(E, match="bytes"):
         binding.ActCode(9, 128, buf=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(E, match="ws must be"):
+        binding.coded_linear(wc, x, ws=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(E, match="expected|device tensor"):
         binding.coded_linear(wc, x, y=torch.empty(8, 64, dtype=torch.bfloat16))

@@ -350,6 +350,8 @@ class ThetaBundle:
                         raise WlError(-1, last_error())
                     self._backward_need[T] = need
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                _check_tensor(ws, "ws", (None,), torch.uint8, dev)
             _check(fn(self.handle, layer, code, x.buf.data_ptr(), x.buf.numel(), dy.data_ptr(), T, ctypes.byref(g),
                       ws.data_ptr(), ws.numel(), _raw_stream(dev)))
         return Grads(**out)
@@ -603,6 +605,8 @@ def coded_linear(w: WeightCode, x, y=None, code: Optional[ActCode] = None, ws=No
         if ws is None and T > CODED_NO_WORKSPACE_T:
             need = lib().weightless_coded_linear_workspace_bytes(w.rows, w.K, T)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        elif ws is not None:
+            _check_tensor(ws, "ws", (None,), torch.uint8, dev)
         _check(lib().weightless_coded_linear(w.buf.data_ptr(), w.buf.numel(), w.rows, w.K, src, code.buf.data_ptr(),
                                              code.buf.numel(), T, y.data_ptr(),
                                              ws.data_ptr() if ws is not None else None,

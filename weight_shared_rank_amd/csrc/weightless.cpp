@@ -560,6 +560,8 @@ bool overlap(const void *a, size_t an, const void *b, size_t bn) {
 
 // ---- backward ----
 
+constexpr int32_t kMaxBackwardColumns = (1 << 21) - 256;
+
 // Dimensions of a group's stacked call (first..last its children) as the
 // backward planner reads them; no pointers.
 wl::CallDesc call_shape(const GroupShape &gs, int first, int last, bool dup) {
@@ -608,6 +610,11 @@ wl_status run_backward(const wl_bundle *h, int32_t layer, int32_t family, int32_
   wl::CallDesc &c = rv.c;
   if ((st = check_act_shape(T, c.K)) != WL_OK) return st;
   c.T = T;
+  // a load instruction of the products addresses 256 rows of dy, or of the
+  // pair of dy U, within 2^30 bytes
+  if (rv.out_dim > kMaxBackwardColumns || 2 * static_cast<int64_t>(c.Rz) > kMaxBackwardColumns)
+    return fail(WL_ESHAPE, "%d output columns and %d ranks: the backward pass takes up to %d and %d", rv.out_dim, c.Rz,
+                kMaxBackwardColumns, kMaxBackwardColumns / 2);
   // the outputs: alignment, and ranges that must not meet
   struct Range {
     const void *p;
