@@ -169,7 +169,8 @@ CASES = [(O, (16,), 8, (1,), 1), (O, (40,), 64, (4,), 1), (O, (1,), 128, (0,), 3
          (O, (520,), 136, (130,), 300), (O, (72,), 72, (8,), 3000), (O, (2048,), 1024, (96,), 257),
          (GU, (200, 200), 264, (5, 33), 65), (GU, (513, 513), 520, (64, 0), 40), (GU, (1000, 1000), 904, (70, 40), 513),
          (QKV, (200, 72, 72), 264, (40, 33, 1), 100), (QKV, (33, 7, 9), 40, (5, 2, 3), 2),
-         (QKV, (1024, 256, 256), 1152, (64, 64, 64), 600)]
+         (QKV, (1024, 256, 256), 1152, (64, 64, 64), 600),
+         (O, (4090,), 4088, (24,), 4080)]  # the last: 256 x 256 tiles
 
 
 @pytest.mark.parametrize("fams,rows,K,ranks,T", CASES)

@@ -190,6 +190,18 @@ def test_long_k_splits(gpu_lib, T, N, K):
     check_product(binding.coded_linear(wc, xc), xc.expand().double(), wc.codes.double() * f)
 
 
+@pytest.mark.parametrize("T,N,K", [(2000, 8100, 264), (2048, 8200, 264), (11000, 600, 264), (700, 4000, 136),
+                                   (16, 8200, 8200), (5, 12300, 5464)])
+def test_sizes_that_take_the_other_tiles(gpu_lib, T, N, K):
+    """Enough output tiles for 256 x 256, 256 x 128 and pairs of 128 x 128
+    workgroups, and few tokens over 64 M codes; ragged in every dimension.  The
+    reference runs in float64 on the GPU on the call's own coded operands."""
+    announce(f"product {T} x {N} x {K}")
+    wc, xc = binding.encode_weight(randn(T, N, K, std=K ** -0.5).to(DEV)), binding.encode_act(randn(N, T, K).to(DEV))
+    f = torch.exp2(wc.scales.double() - 127).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    check_product(binding.coded_linear(wc, xc), xc.expand().double(), wc.codes.double() * f)
+
+
 def test_blocks_of_very_different_scale(gpu_lib):
     """Scales from 2^-60 to 2^60 along K, tokens and weight rows: each block's
     own two scales enter its products."""

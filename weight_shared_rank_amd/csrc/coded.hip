@@ -598,27 +598,36 @@ struct CPlan {
   int tile, ksplit, per, nM, nT;
 };
 
+// Tile shapes with the us of one k step of a workgroup alone on its CU (fitted
+// at K = 5376 and 21504); 128 x 128 workgroups also run two to a CU, on a ring
+// of two stages, when there are more of them than CUs.
 struct CShape {
   int BM, BN;
-  double step;  // us of one k step of one workgroup
+  double step;
 };
-constexpr CShape kShapes[] = {{256, 256, 1.6}, {128, 128, 0.8}, {128, 64, 0.7}};
+constexpr CShape kShapes[] = {{256, 256, 1.62}, {256, 128, 1.03}, {128, 128, 0.8}, {128, 64, 0.58}};
+constexpr int kShape128 = 2;
+constexpr double kPairStep = 1.15;
 
 // Tile shape and K split of the product: the smallest estimated time, rounds
-// of workgroups over the CUs times the steps of one, plus writing and summing
-// the partials when K is split.
+// of workgroups over the CUs times the steps of one (3 more for its start and
+// end), plus writing and summing the partials when K is split.  (21504 x 5376,
+// us by shape: T = 256 58, 49, 57, 68; T = 512 73, 88, 96, 125; 8192 x 5376 at T =
+// 1024 54, 43, 47, 79; 4096 x 1152 at T = 256 15, 11, 8, 7.)
 CPlan plan_coded(int N, int T, int nb) {
   CPlan best{};
   double best_us = 1e300;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const CShape &sh = kShapes[i];
     const int nM = (N + sh.BM - 1) / sh.BM, nT = (T + sh.BN - 1) / sh.BN;
     const int64_t tiles = static_cast<int64_t>(nM) * nT;
     for (int ks = 1; ks <= 16 && ks * 2 <= std::max(2, nb); ++ks) {
       const int per = (nb + ks - 1) / ks;
       if ((ks - 1) * per >= nb) continue;  // an empty slice
-      const double rounds = static_cast<double>((tiles * ks + kCUs - 1) / kCUs);
-      double us = rounds * (per + 3) * sh.step;
+      const bool pairs = i == kShape128 && tiles * ks > kCUs;
+      const int64_t slots = pairs ? 2 * kCUs : kCUs;
+      const double rounds = static_cast<double>((tiles * ks + slots - 1) / slots);
+      double us = rounds * (per + 3) * (pairs ? kPairStep : sh.step);
       if (ks > 1) us += 4.0 + 2.0 * ks * static_cast<double>(T) * N * 4 / 3e6;
       if (us < best_us) {
         best_us = us;
@@ -756,7 +765,8 @@ hipError_t launch_coded_linear(const CodedView &w, int N, const uint16_t *src, i
   a.P = p.ksplit > 1 ? partials : nullptr;
   switch (p.tile) {
     case 0: e = launch_coded_tile<CTile<256, 256, 2, 4, 2>>(a, stream); break;
-    case 1:
+    case 1: e = launch_coded_tile<CTile<256, 128, 4, 2, 3>>(a, stream); break;
+    case kShape128:
       e = p.nM * p.nT * p.ksplit > kCUs ? launch_coded_tile<CTile<128, 128, 2, 4, 2>>(a, stream)
                                         : launch_coded_tile<CTile<128, 128, 2, 4, 4>>(a, stream);
       break;
