@@ -362,9 +362,10 @@ wl_status weightless_weight_encode(const void *d_w, int32_t N, int32_t K, void *
  *  d_ws: weightless_coded_linear_workspace_bytes(N, K, T) bytes, 256-byte
  *    aligned, no initialization, nothing kept; may be NULL if that is 0 bytes
  *    (always so for T <= 4).  Concurrent calls need distinct workspaces.
- *  T <= 16 streams the weights once through registers; T <= 4 is one launch,
- *  x coded in it; T > 16 runs LDS-tiled matrix-core products.  K is split over
- *  workgroups and summed by another launch when there are few output tiles. */
+ *  T <= 16 streams the weights once through registers; T <= 2 is one launch,
+ *  x coded in it (T <= 4 with coded x); T > 16 runs LDS-tiled matrix-core
+ *  products.  K is split over workgroups and summed by another launch when
+ *  there are few output tiles. */
 size_t weightless_coded_linear_workspace_bytes(int32_t N, int32_t K, int32_t T);
 wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32_t N, int32_t K, const void *d_x,
                                   void *d_xcode, size_t xcode_bytes, int32_t T, void *d_y, void *d_ws,
@@ -381,8 +382,9 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
  * codes).  Products of bf16 operands with float32 sums; as operands dy (.) s
  * is rounded to bf16 once and X V and dy U are kept as a pair of bf16 (16
  * significant bits); dx, dU and dV are rounded once at the end; G, ds and dW0
- * are float32 throughout.  Results are the same bits from run
- * to run. */
+ * are float32 throughout.  Results are the same bits from run to run, whichever
+ * of them are asked for.  An element of dy or of the checkpoint that is not
+ * finite makes NaN or infinity of what it enters, and changes nothing else. */
 typedef struct {
   void *dx;         /* bf16 [T, K] */
   float *ds;        /* float32 [N] */

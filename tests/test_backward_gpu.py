@@ -391,6 +391,14 @@ def test_forward_checkpoint_backward_together(gpu_lib):
     assert abs(full - (g.ds.double() ** 2).sum().item()) <= 2.0 ** -4 * mass
 
 
+@pytest.mark.parametrize("T,K", [(1 << 20, 8), (5, 1 << 20)])
+def test_most_tokens_and_longest_rows(gpu_lib, T, K):
+    lay = Layer(O, (9,), K, (5,), seed=16)
+    code, dy = binding.encode_act(randn(64, T, K)), randn(65, T, 9)
+    announce(f"T={T} K={K}")
+    check(lay, code, dy, lay.backward(code, dy))
+
+
 def test_widest_calls(gpu_lib):
     """More columns than a load can address are refused; just under it (one
     family of 2^20 rows, beyond what 32-bit element offsets of a token reach)
@@ -449,6 +457,10 @@ def test_binding_refusals(gpu_lib):
         lay.backward(code, dy, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
     with pytest.raises(E, match="ws must be"):
         lay.backward(code, dy, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(E, match="WL_ERANGE"):
+        lay.bundle.stacked_backward(1, "gate_up", code, dy)
+    with pytest.raises(E, match="WL_ERANGE"):
+        lay.bundle.linear_backward(-1, "gate", code, dy)
     with pytest.raises(E, match="WL_ERANGE"):
         lay.bundle.stacked_backward(0, "qkv", code, dy)
     # outputs that overlap an input or each other, and misaligned ones (host checks, nothing runs)

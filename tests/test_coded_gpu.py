@@ -113,6 +113,8 @@ def test_every_bf16_value(gpu_lib):
 
 def group_max_sum(xv, wv):
     """sum over groups of 8 consecutive k of max|x w| in the group, [T, N]."""
+    if xv.shape[1] >= 1 << 16:  # few rows and columns
+        return (xv.abs()[:, None] * wv.abs()[None]).unflatten(-1, (-1, 8)).amax(-1).sum(-1)
     tops = torch.zeros(xv.shape[0], wv.shape[0], dtype=torch.float64, device=xv.device)
     for k in range(0, xv.shape[1], 8):
         top = torch.zeros_like(tops)
@@ -200,6 +202,24 @@ def test_sizes_that_take_the_other_tiles(gpu_lib, T, N, K):
     wc, xc = binding.encode_weight(randn(T, N, K, std=K ** -0.5).to(DEV)), binding.encode_act(randn(N, T, K).to(DEV))
     f = torch.exp2(wc.scales.double() - 127).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
     check_product(binding.coded_linear(wc, xc), xc.expand().double(), wc.codes.double() * f)
+
+
+@pytest.mark.parametrize("T,N,K", [(1 << 20, 9, 8), (2, 1 << 20, 8), (3, 1 << 20, 8), (40, 1 << 20, 8), (2, 16, 1 << 20),
+                                   (7, 16, 1 << 20), (40, 16, 1 << 20)])
+def test_largest_extents(gpu_lib, T, N, K):
+    """Each dimension at the largest the library takes."""
+    announce(f"product {T} x {N} x {K}")
+    w, x = randn(N, N, K, std=K ** -0.5).to(DEV), randn(T, T, K).to(DEV)
+    wc = binding.encode_weight(w)
+    code = binding.ActCode(T, K)
+    y = binding.coded_linear(wc, x, code=code)
+    f = torch.exp2(wc.scales.double() - 127).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    xv, wv = code.expand().double(), wc.codes.double() * f
+    # a code is within half a step of E4M3: 2^-4 of the value, or 2^-10 of the block's scale
+    for v, src in ((xv, x), (wv, w)):
+        step = 2.0 ** -4 * src.double().abs() + 2.0 ** -10 * 2.0 ** -8 * src.double().abs().max()
+        assert ((v - src.double()).abs() <= step).all()
+    check_product(y, xv, wv)
 
 
 def test_blocks_of_very_different_scale(gpu_lib):
@@ -314,6 +334,8 @@ def test_binding_refusals(gpu_lib):
         binding.encode_act(randn(14, 128, 8).to(DEV).t())
     with pytest.raises(E, match="bfloat16"):
         binding.encode_act(x.float())
+    with pytest.raises(E, match="WeightCode"):
+        binding.coded_linear(binding.encode_act(x), x)
     with pytest.raises(E, match="x must be"):
         binding.coded_linear(wc, randn(15, 8, 136).to(DEV))
     with pytest.raises(E, match="coded as"):

@@ -585,6 +585,8 @@ def coded_linear(w: WeightCode, x, y=None, code: Optional[ActCode] = None, ws=No
     x: bf16 [T, K], coded first (into `code`, if given: the checkpoint to
     keep), or an ActCode that already holds the coded activations."""
     import torch
+    if not isinstance(w, WeightCode):
+        raise WlError(-1, "w must be a WeightCode")
     dev = w.buf.device
     with _scope(dev, stream):
         if isinstance(x, ActCode):

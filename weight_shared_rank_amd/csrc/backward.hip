@@ -92,35 +92,33 @@ struct BwdArgs {
   Prob p[kMaxProb];
 };
 
-// One operand of a staged product: W rows of the tile by BK (32 or 64) of the
-// contraction per stage, in 1 KB load instructions.
-//
-// k-rows (TR false): LDS row r is the BK values of tile row r.  64-byte rows
-// keep 16-byte chunk c in slot c ^ (r / 4 % 4), 128-byte rows in c ^ (r % 8):
-// a fragment read (8 lanes per phase: 8 rows, one chunk) then touches every
-// bank once.
-//
-// k-columns (TR): LDS row k is W elements of contraction index k, its chunk c
-// in slot c ^ swz(k).  A transposing read takes 32-byte pieces of rows 8 g +
-// 0..3 (lane group g); two lane groups at once touch 8 rows, which the swizzle
-// puts in 8 different 32-byte places of the 256-byte bank period.  Rows of >=
-// 256 bytes all start at bank 0: swz = 2 (k & 3) + 8 (k >> 3 & 1).  128-byte
-// rows alternate between its halves: swz = 2 (k >> 1 & 1) + 4 (k >> 3 & 1).
-//
-// A lane's place in a load is a per-lane part (kept in two registers) and a
-// part of the instruction's number, so the addresses of the loads cost no
-// registers of their own.
 // A uniform value held in a scalar register: without it the compiler loads a
 // kernel argument again at every use, and a scalar load in the loop makes the
 // next use wait for every LDS read in flight (they share a counter).
 __device__ __forceinline__ int keep(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// One operand of a staged product: W rows of the tile by BK (32 or 64) of the
+// contraction per stage, in 1 KB load instructions.
+//
+// k-rows (TR false, BK = 64): LDS row r is the 64 values of tile row r, its
+// 16-byte chunk c in slot c ^ (r % 8): a fragment read (8 lanes per phase: 8
+// rows, one chunk) then touches every bank once.
+//
+// k-columns (TR): LDS row k is W elements of contraction index k, its chunk c
+// in slot c ^ swz(k).  A transposing read takes 32-byte pieces of rows 8 g +
+// 0..3 (lane group g); two lane groups at once touch 8 rows, which the swizzle
+// puts in 8 different 32-byte places of the 256-byte bank period (every row
+// starts at bank 0): swz = 2 (k & 3) + 8 (k >> 3 & 1).
+//
+// A lane's place in a load is a per-lane part (kept in two registers) and a
+// part of the instruction's number, so the addresses of the loads cost no
+// registers of their own.
 template <int W, bool TR, int BK>
 struct Operand {
   static constexpr int READS = TR ? 2 : 1;          // LDS reads of a fragment
   static constexpr int CPR = TR ? W / 8 : BK / 8;       // 16-byte chunks of an LDS row
   static constexpr int RPQ = 64 / CPR;              // LDS rows of a load instruction
-  static_assert(W == 64 || W == 128 || W == 256, "tile width");
+  static_assert((W == 128 || W == 256) && (TR || BK == 64), "operand shape");
 
   int lrow, chunk;   // this lane's row of a load and its chunk, without the instruction's swizzle
   uint32_t lo;       // byte offset of lrow's start
@@ -135,19 +133,19 @@ struct Operand {
     lo = static_cast<uint32_t>(lrow * ld * 2);
     const int slot = lane % CPR;
     if constexpr (TR) {
-      chunk = slot ^ (W >= 128 ? 2 * (lrow & 3) : 2 * ((lrow >> 1) & 1));
+      chunk = slot ^ (2 * (lrow & 3));
       const int k = 8 * g + (r16 >> 2);
-      const int sw = W >= 128 ? 2 * (k & 3) + 8 * ((k >> 3) & 1) : 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1);
+      const int sw = 2 * (k & 3) + 8 * ((k >> 3) & 1);
       rd = k * (2 * W) + (((mw / 8 + ((r16 >> 1) & 1)) ^ sw) * 16) + (r16 & 1) * 8;
     } else {
-      chunk = slot ^ (BK == 64 ? lrow & 7 : (lrow >> 2) & 3);
-      rd = (mw + r16) * (2 * BK) + (g ^ (BK == 64 ? r16 & 7 : (r16 >> 2) & 3)) * 16;
+      chunk = slot ^ (lrow & 7);
+      rd = (mw + r16) * (2 * BK) + (g ^ (r16 & 7)) * 16;
     }
   }
   // Swizzle part of load instruction q (the bits of its first row).
   static __device__ __forceinline__ int sw_of(int q) {
     if constexpr (!TR) return 0;
-    return W == 256 ? 4 * (q & 1) + 8 * ((q >> 2) & 1) : W == 128 ? 8 * ((q >> 1) & 1) : 4 * (q & 1);
+    return W == 256 ? 4 * (q & 1) + 8 * ((q >> 2) & 1) : 8 * ((q >> 1) & 1);
   }
   // Load instruction q of a stage at `base`; lim rows (k-rows) or columns
   // (k-columns) of the tile exist, `left` values of the contraction.
