@@ -71,7 +71,6 @@ struct Prob {
   int32_t M, N;       // extent along A (contiguous in C) and along B
   int32_t kind, mode;
   int32_t nM, nN, ksplit, per;  // tiles, slices of the contraction, steps per slice
-  int32_t unit0;      // first workgroup of its launch
   uint16_t *out;      // kBf16, kPair: [N][ldo]
   int64_t ldo;
   int32_t lo;         // kPair: columns from a value to what its rounding left
@@ -89,8 +88,10 @@ struct Prob {
 
 struct BwdArgs {
   int32_t nprob, total;
+  int32_t unit0[kMaxProb];  // first workgroup of each product (behind the last: kNoUnit)
   Prob p[kMaxProb];
 };
+constexpr int32_t kNoUnit = 0x7fffffff;
 
 // A uniform value held in a scalar register: without it the compiler loads a
 // kernel argument again at every use, and a scalar load in the loop makes the
@@ -451,10 +452,15 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
 // Workgroup -> product and its unit.  The units of each product are numbered
 // XCD-major, so that the tiles an XCD runs at a time share panels in its L2.
 __device__ __forceinline__ const Prob &find_unit(const BwdArgs &a, int &v) {
-  int pi = 0;
-  while (pi + 1 < a.nprob && static_cast<int>(blockIdx.x) >= a.p[pi + 1].unit0) ++pi;
+  int pi = 0, first = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxProb; ++i)  // (one run of arguments: no chain of loads)
+    if (static_cast<int>(blockIdx.x) >= a.unit0[i]) {
+      pi = i;
+      first = a.unit0[i];
+    }
   const Prob &p = a.p[pi];
-  v = xcd_unit(blockIdx.x - p.unit0, p.nM * p.nN * p.ksplit);
+  v = xcd_unit(blockIdx.x - first, p.nM * p.nN * p.ksplit);
   return p;
 }
 
@@ -487,7 +493,7 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
 // workgroup, 16 lanes per row each summing every 16th part, joined in order).
 struct SumArgs {
   int32_t nprob;
-  int32_t first[kMaxProb];  // first workgroup of each
+  int32_t first[kMaxProb];  // first workgroup of each (behind the last: kNoUnit)
   Prob p[kMaxProb];
 };
 
@@ -502,7 +508,9 @@ __device__ __forceinline__ f32x4 sum_slices(const Prob &p, int64_t n, int m) {
 
 __global__ __launch_bounds__(256) void sum_kernel(SumArgs a) {
   int pi = 0;
-  while (pi + 1 < a.nprob && static_cast<int>(blockIdx.x) >= a.first[pi + 1]) ++pi;
+#pragma unroll
+  for (int i = 1; i < kMaxProb; ++i)
+    if (static_cast<int>(blockIdx.x) >= a.first[i]) pi = i;
   const Prob &p = a.p[pi];
   const int64_t b = blockIdx.x - a.first[pi];
   const int q = p.ldp / 4;
@@ -893,21 +901,22 @@ struct Batch {
 };
 
 template <typename TL, auto KERN>
-hipError_t launch_kernel(const BwdArgs &a, hipStream_t stream) {
+hipError_t launch_kernel(BwdArgs &a, hipStream_t stream) {
   const hipError_t e = ensure_lds<KERN>(TL::LDS);
   if (e != hipSuccess) return e;
+  std::fill(a.unit0 + a.nprob, a.unit0 + kMaxProb, kNoUnit);
   hipLaunchKernelGGL(KERN, dim3(a.total), dim3(TL::NW * 64), TL::LDS, stream, a);
   return hipGetLastError();
 }
 
 template <bool BTR>
-hipError_t launch_big(const BwdArgs &a, hipStream_t stream) {
+hipError_t launch_big(BwdArgs &a, hipStream_t stream) {
   return launch_kernel<Big<BTR>, product_kernel<Big<BTR>, true, BTR>>(a, stream);
 }
 
 void add_units(BwdArgs &a, const Prob &p) {
-  a.p[a.nprob] = p;
-  a.p[a.nprob++].unit0 = a.total;
+  a.unit0[a.nprob] = a.total;
+  a.p[a.nprob++] = p;
   a.total += p.nM * p.nN * p.ksplit;
 }
 
@@ -946,6 +955,7 @@ hipError_t launch_batch(const Batch &b, hipStream_t stream) {
                                   : static_cast<int>((static_cast<int64_t>(p.N) * (p.ldp / 4) + 255) / 256);
   }
   if (!a.nprob) return hipSuccess;
+  std::fill(a.first + a.nprob, a.first + kMaxProb, kNoUnit);
   hipLaunchKernelGGL(sum_kernel, dim3(blocks), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
