@@ -199,24 +199,28 @@ struct BTile {
 // (Rows staged through LDS for whole-row accesses took 25 us per 256 x 256
 // tile: a load latency and five exchanges for every two rows.)
 template <typename TL>
-__device__ __forceinline__ void store_weight_grad(const f32x4 (&acc)[TL::FM][TL::FN], const Prob &p, int f, int m0,
+__device__ __forceinline__ void load_block(u32x2 (&w)[TL::FN][TL::FM], const Prob &p, int m0, int n0) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WN, wn = wave % TL::WN, r16 = lane & 15, g = lane >> 4;
+  const int k0 = m0 + wm * TL::TM + g * 4;  // M % 8 == 0: whole groups of 4
+#pragma unroll
+  for (int j = 0; j < TL::FN; ++j) {
+    const int n = n0 + wn * TL::TN + j * 16 + r16;
+    const uint16_t *src = p.W0 + static_cast<int64_t>(n < p.N ? n : 0) * p.M + k0;
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      w[j][i] = u32x2{0u, 0u};
+      if (n < p.N && k0 + 16 * i < p.M) w[j][i] = *reinterpret_cast<const u32x2 *>(src + 16 * i);
+    }
+  }
+}
+
+template <typename TL>
+__device__ __forceinline__ void store_weight_grad(const f32x4 (&acc)[TL::FM][TL::FN], const u32x2 (&w)[TL::FN][TL::FM], const Prob &p, int f, int m0,
                                                   int n0) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / TL::WN, wn = wave % TL::WN, r16 = lane & 15, g = lane >> 4;
   const int k0 = m0 + wm * TL::TM + g * 4;  // M % 8 == 0: whole groups of 4
-  u32x2 w[TL::FN][TL::FM];
-  if (p.ds) {
-#pragma unroll
-    for (int j = 0; j < TL::FN; ++j) {
-      const int n = n0 + wn * TL::TN + j * 16 + r16;
-      const uint16_t *src = p.W0 + static_cast<int64_t>(n < p.N ? n : 0) * p.M + k0;
-#pragma unroll
-      for (int i = 0; i < TL::FM; ++i) {
-        w[j][i] = u32x2{0u, 0u};
-        if (n < p.N && k0 + 16 * i < p.M) w[j][i] = *reinterpret_cast<const u32x2 *>(src + 16 * i);
-      }
-    }
-  }
   if (p.dw0) {
 #pragma unroll
     for (int j = 0; j < TL::FN; ++j) {
@@ -346,6 +350,10 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
 #pragma unroll
     for (int j = 0; j < TL::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  u32x2 w0[TL::FN][TL::FM];
+  if constexpr (ATR && BTR && TL::BM == 128) {
+    if (p.mode == kWeight && p.ksplit == 1 && p.ds) load_block<TL>(w0, p, m0, n0);
+  }
   for (int si = 0; si < p.nseg; ++si) {
     const Seg &sg = p.seg[si];
     const int steps = (sg.len + kStep - 1) / kStep;
@@ -432,7 +440,12 @@ __device__ __forceinline__ void product_unit(const Prob &p, int v, uint8_t *lds)
     return;
   }
   if (p.mode == kWeight) {
-    if constexpr (ATR && BTR) store_weight_grad<TL>(acc, p, f, m0, n0);
+    if constexpr (ATR && BTR) {
+      if constexpr (TL::BM != 128) {
+        if (p.ds) load_block<TL>(w0, p, m0, n0);
+      }
+      store_weight_grad<TL>(acc, w0, p, f, m0, n0);
+    }
     return;
   }
   store_rows<TL>(acc, p, m0, n0, 0, lds);
