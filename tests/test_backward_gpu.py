@@ -170,7 +170,11 @@ CASES = [(O, (16,), 8, (1,), 1), (O, (40,), 64, (4,), 1), (O, (1,), 128, (0,), 3
          (GU, (200, 200), 264, (5, 33), 65), (GU, (513, 513), 520, (64, 0), 40), (GU, (1000, 1000), 904, (70, 40), 513),
          (QKV, (200, 72, 72), 264, (40, 33, 1), 100), (QKV, (33, 7, 9), 40, (5, 2, 3), 2),
          (QKV, (1024, 256, 256), 1152, (64, 64, 64), 600),
-         (O, (4090,), 4088, (24,), 4080)]  # the last: 256 x 256 tiles
+         (O, (4090,), 4088, (24,), 4080),  # 256 x 256 tiles
+         # few tokens through a large block: one pass over it
+         (O, (4100,), 4104, (0,), 1), (O, (1030,), 16392, (129,), 33), (GU, (2101, 2101), 4008, (20, 0), 64),
+         (GU, (265, 265), 40000, (3, 40), 50), (QKV, (64000, 130, 63), 264, (33, 16, 8), 17),
+         (QKV, (12000, 3000, 2000), 1000, (8, 64, 1), 64), (O, (4100,), 4104, (4,), 65)]
 
 
 @pytest.mark.parametrize("fams,rows,K,ranks,T", CASES)
@@ -198,10 +202,10 @@ def test_tied_v_adds_to_k(gpu_lib, rows, T):
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
-@pytest.mark.parametrize("T", [5, 90])
-def test_coded_shared_blocks(gpu_lib, fmt, T):
-    lay = Layer(GU, (136, 136), 264, (9, 9), fmt=fmt, seed=4, layers=2)
-    code, dy = binding.encode_act(randn(3, T, 264)), randn(4, T, lay.width, std=T ** -0.5)
+@pytest.mark.parametrize("T,N,K", [(5, 136, 264), (90, 136, 264), (30, 2100, 4104)])
+def test_coded_shared_blocks(gpu_lib, fmt, T, N, K):
+    lay = Layer(GU, (N, N), K, (9, 9), fmt=fmt, seed=4, layers=2)
+    code, dy = binding.encode_act(randn(3, T, K)), randn(4, T, lay.width, std=T ** -0.5)
     announce(f"{fmt} T={T}")
     check(lay, code, dy, lay.backward(code, dy))
 
@@ -234,9 +238,10 @@ def test_gradients_match_differences(gpu_lib):
             assert abs(have - want) <= 2 * H * got[i].double().norm().item() * d.norm().item(), (name, i)
 
 
-def test_subsets_give_the_same_bits(gpu_lib):
-    lay = Layer(QKV, (200, 72, 40), 264, (40, 33, 8), seed=6)
-    code, dy = binding.encode_act(randn(7, 100, 264)), randn(8, 100, lay.width)
+@pytest.mark.parametrize("rows,K,T", [((200, 72, 40), 264, 100), ((6000, 2000, 333), 2104, 60)])
+def test_subsets_give_the_same_bits(gpu_lib, rows, K, T):
+    lay = Layer(QKV, rows, K, (40, 33, 8), seed=6)
+    code, dy = binding.encode_act(randn(7, T, K)), randn(8, T, lay.width)
     full = lay.backward(code, dy)
     for want in (("dx",), ("ds",), ("du",), ("dv",), ("dw0",), ("dx", "dv"), ("ds", "du"), ()):
         announce(f"want {want}")
@@ -248,34 +253,35 @@ def test_subsets_give_the_same_bits(gpu_lib):
                 same_bits((a,), (b,))
 
 
-@pytest.mark.parametrize("T,rows", [(40, 300), (2500, 24)])
-def test_accumulated_block_gradient(gpu_lib, T, rows):
+@pytest.mark.parametrize("T,rows,K", [(40, 300, 264), (2500, 24, 264), (40, 4100, 4104)])
+def test_accumulated_block_gradient(gpu_lib, T, rows, K):
     """dw0 += over the layers of a band: the sum of the calls' own gradients,
     one float32 rounding per addition; both with and without a split."""
-    lay = Layer(O, (rows,), 264, (8,), seed=7)
-    code, dy = binding.encode_act(randn(9, T, 264)), randn(10, T, rows)
+    lay = Layer(O, (rows,), K, (8,), seed=7)
+    code, dy = binding.encode_act(randn(9, T, K)), randn(10, T, rows)
     announce(f"accumulate T={T}")
     one = lay.backward(code, dy, want=("dw0",)).dw0
-    acc = randn(11, rows, 264, dtype=torch.float32)
+    acc = randn(11, rows, K, dtype=torch.float32)
     want = acc + one
     got = lay.backward(code, dy, want=("dw0", "ds"), dw0=acc, accumulate=True)
     assert got.dw0 is acc
     assert ((acc - want).abs() <= 2.0 ** -23 * (one.abs() + want.abs())).all()
 
 
-def test_unaligned_dy_and_neighbouring_memory(gpu_lib):
+@pytest.mark.parametrize("N,K", [(136, 264), (4104, 4104)])
+def test_unaligned_dy_and_neighbouring_memory(gpu_lib, N, K):
     """dy that starts at an odd element; outputs at odd places in larger
     buffers whose other elements stay as they were."""
-    lay = Layer(O, (136,), 264, (8,), seed=8)
+    lay = Layer(O, (N,), K, (8,), seed=8)
     T = 50
-    code, dy = binding.encode_act(randn(12, T, 264)), randn(13, T, 136)
+    code, dy = binding.encode_act(randn(12, T, K)), randn(13, T, N)
     want = lay.backward(code, dy)
-    flat = torch.empty(T * 136 + 1, dtype=torch.bfloat16, device=DEV)
+    flat = torch.empty(T * N + 1, dtype=torch.bfloat16, device=DEV)
     flat[1:] = dy.flatten()
     announce("unaligned dy")
-    same_bits(lay.backward(code, flat[1:].view(T, 136)), want)
+    same_bits(lay.backward(code, flat[1:].view(T, N)), want)
     # raw call with outputs inside larger buffers
-    sizes = {"dx": (T * 264, 2, 8), "du": (136 * 8, 2, 1), "dv": (264 * 8, 2, 1), "ds": (136, 4, 1), "dw0": (136 * 264, 4, 4)}
+    sizes = {"dx": (T * K, 2, 8), "du": (N * 8, 2, 1), "dv": (K * 8, 2, 1), "ds": (N, 4, 1), "dw0": (N * K, 4, 4)}
     bufs = {k: torch.full((n + 2 * o,), 7.0, dtype=torch.bfloat16 if b == 2 else torch.float32, device=DEV)
             for k, (n, b, o) in sizes.items()}
     g = binding.WlGrads()
@@ -300,20 +306,21 @@ def test_unaligned_dy_and_neighbouring_memory(gpu_lib):
         assert torch.equal(bufs[k][o:o + n], t.flatten()) and (bufs[k][:o] == 7).all() and (bufs[k][o + n:] == 7).all(), k
 
 
-def test_non_finite_values_stay_where_they_belong(gpu_lib):
-    lay = Layer(O, (77,), 264, (8,), seed=9)
+@pytest.mark.parametrize("N,K", [(77, 264), (4100, 4104)])
+def test_non_finite_values_stay_where_they_belong(gpu_lib, N, K):
+    lay = Layer(O, (N,), K, (8,), seed=9)
     T = 40
-    x, dy = randn(14, T, 264), randn(15, T, 77)
-    dy[3, 76] = float("nan")
-    x[5, 263] = float("inf")
+    x, dy = randn(14, T, K), randn(15, T, N)
+    dy[3, N - 1] = float("nan")
+    x[5, K - 1] = float("inf")
     announce("non-finite")
     g = lay.backward(binding.encode_act(x), dy)
     nan = torch.isnan(g.dx).any(1)
     assert nan[3] and nan.sum() == 1                       # dx: that token only (x does not enter dx)
     rows = torch.isnan(g.dw0)
-    assert rows[76].all() and rows[:, 263].all() and rows[:76, :263].sum() == 0
+    assert rows[N - 1].all() and rows[:, K - 1].all() and rows[:N - 1, :K - 1].sum() == 0
     assert torch.isnan(g.dv[0]).all() and torch.isnan(g.du[0]).all()   # g's and z's token enter every sum
-    assert torch.isfinite(lay.backward(binding.encode_act(randn(14, T, 264)), randn(15, T, 77)).dx).all()
+    assert torch.isfinite(lay.backward(binding.encode_act(randn(14, T, K)), randn(15, T, N)).dx).all()
 
 
 def test_no_tokens_zero_the_sums(gpu_lib):
@@ -327,10 +334,10 @@ def test_no_tokens_zero_the_sums(gpu_lib):
     assert (acc == 1).all()
 
 
-def test_side_stream_graph_and_two_at_once(gpu_lib):
-    lay = Layer(QKV, (256, 128, 128), 512, (32, 16, 16), seed=11)
-    T = 150
-    codes = [binding.encode_act(randn(20 + i, T, 512)) for i in range(3)]
+@pytest.mark.parametrize("rows,K,T", [((256, 128, 128), 512, 150), ((6000, 3000, 1900), 1544, 20)])
+def test_side_stream_graph_and_two_at_once(gpu_lib, rows, K, T):
+    lay = Layer(QKV, rows, K, (32, 16, 16), seed=11)
+    codes = [binding.encode_act(randn(20 + i, T, K)) for i in range(3)]
     dys = [randn(30 + i, T, lay.width) for i in range(3)]
     want = [lay.backward(c, d) for c, d in zip(codes, dys)]
     torch.cuda.synchronize()
@@ -344,7 +351,7 @@ def test_side_stream_graph_and_two_at_once(gpu_lib):
     for i in (0, 1):
         for g in got[i]:
             same_bits(g, want[i])
-    code, dy = binding.ActCode(T, 512, buf=codes[0].buf.clone()), dys[0].clone()
+    code, dy = binding.ActCode(T, K, buf=codes[0].buf.clone()), dys[0].clone()
     graph = torch.cuda.CUDAGraph()
     announce("capture")
     with torch.cuda.graph(graph):

@@ -82,7 +82,7 @@ struct Prob {
   float *dw0;         // [N][M] or null
   int32_t accumulate;
   float *ds;          // [N] (null: not wanted)
-  float *dsp;         // ksplit == 1: its partial sums [nM * 2][ldds], a row per wave row of the column tiles
+  float *dsp;         // ksplit == 1: its partial sums [nM * 2][ldds], a row per half of a column tile
   int32_t ldds;
 };
 
@@ -119,7 +119,7 @@ struct Operand {
   static constexpr int READS = TR ? 2 : 1;          // LDS reads of a fragment
   static constexpr int CPR = TR ? W / 8 : BK / 8;       // 16-byte chunks of an LDS row
   static constexpr int RPQ = 64 / CPR;              // LDS rows of a load instruction
-  static_assert((W == 128 || W == 256) && (TR || BK == 64), "operand shape");
+  static_assert(TR ? W == 128 || W == 256 : BK == 64, "operand shape");
 
   int lrow, chunk;   // this lane's row of a load and its chunk, without the instruction's swizzle
   uint32_t lo;       // byte offset of lrow's start
@@ -499,6 +499,201 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
     product_unit<TL, false, false>(p, v, lds);
 }
 
+// Few tokens (T <= kFewT): dx, dW0 and ds in one pass over W0.  A workgroup
+// owns 128 columns k and a slice of the rows n of W0; a stage is 64 rows.  From
+// it come dx's terms, with the 64 columns of dy (.) s that belong to the rows,
+// and the stage's G, whose contraction is the tokens alone: dy and X are at hand
+// transposed, [column][kFewT tokens], so G's operands need no LDS transpose and
+// X's stay in registers.  For dx a wave takes 16 k and all n, for G 64 k and 16
+// n.  dx's other terms (g V^T) are further stages without G.  Bound by W0 once
+// through and dW0's way out (43008 x 5376 at T = 16: 273 us, 5.1 TB/s); without
+// dW0 by the 48 KB of W0 a CU has in flight (133 us, 3.5 TB/s).
+constexpr int kFewT = 64, kFewStages = 4, kFewWaves = 8;
+constexpr int kFewY = 64 * 128 * 2, kFewD = kFewY + kFewT * 128, kFewS = kFewD + 64 * 128;  // dy (.) s, dy^T, s
+constexpr int kFewStage = kFewS + kFewWaves * 256, kFewRing = kFewStages * kFewStage;
+static_assert(kFewRing <= 160 * 1024, "ring");
+
+struct FewArgs {
+  Prob p;  // dx: M = K, N = T; its segments over dy's slots come first
+  int32_t nslot;
+  int32_t row[kMaxChildren];          // slot -> first row of W0, s, dW0 and ds
+  const uint16_t *dyt[kMaxChildren];  // slot -> dy^T [columns][kFewT]
+  const uint16_t *xt;                 // X^T [K][kFewT]
+};
+
+struct FewOperands {
+  Operand<128, true, 64> a;       // W0 (or V^T): 128 columns
+  Operand<kFewT, false, 64> b;    // dy (.) s (or g): the tokens
+  Operand<64, false, 64> d;       // dy^T: the stage's rows n
+};
+
+struct FewSource {
+  const uint16_t *a, *b, *d;
+  const float *s;
+  int lima, limb, left, leftd;  // columns, tokens; rows n left, of them with a G
+};
+
+struct FewFrags {
+  u32x4 a[2], b[kFewT / 16][2], d[2];
+  u32x2 w[4];
+  float s;
+};
+
+// A stage's loads into `w` and another's reads from `r` (restrict: move_stage).
+__device__ __forceinline__ void few_load(const FewOperands &o, const FewSource &f, int lane, int wave, lds_u8 *w) {
+  o.a.load(f.a, 2 * wave, f.lima, f.left, w);
+  o.a.load(f.a, 2 * wave + 1, f.lima, f.left, w);
+  o.b.load(f.b, wave, f.limb, f.left, w + kFewY);
+  o.d.load(f.d, wave, f.leftd, kFewT, w + kFewD);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_rsrc(f.s), (lds_void *)(w + kFewS + wave * 256), 4,
+                                           lane < f.leftd ? lane * 4 : kBufNoRow, 0, 0, 0);
+}
+
+__device__ __forceinline__ void few_step(const FewOperands &o, const FewSource &f, int lane, int wave,
+                                         lds_u8 *__restrict__ w, const lds_u8 *__restrict__ r, int stage,
+                                         FewFrags &x) {
+  few_load(o, f, lane, wave, w);
+  const int r16 = lane & 15, g = lane >> 4, n = (wave & 3) * 16 + r16;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    x.a[h] = o.a.frag(r, stage, 0, h);
+#pragma unroll
+    for (int j = 0; j < kFewT / 16; ++j) x.b[j][h] = o.b.frag(r, stage + kFewY, j, h);
+    x.d[h] = o.d.frag(r, stage + kFewD, wave & 3, h);
+  }
+  // W0[n][64 (wave / 4) + 16 i + 4 g ..]: chunk c of LDS row n lies in slot c ^ swz(n)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = (wave >> 2) * 8 + 2 * i + (g >> 1), swz = 2 * (n & 3) + 8 * ((n >> 3) & 1);
+    x.w[i] = *(const __attribute__((address_space(3))) u32x2 *)(r + stage + n * 256 + ((c ^ swz) * 16) + (g & 1) * 8);
+  }
+  x.s = *(const __attribute__((address_space(3))) float *)(r + stage + kFewS + wave * 256 + n * 4);
+}
+
+__global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(1, 2))) void few_kernel(FewArgs args) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  lds_u8 *const ring = (lds_u8 *)lds;
+  const Prob &p = args.p;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int v = xcd_unit(blockIdx.x, p.nM * p.ksplit);
+  const int sl = v / p.nM, f = v % p.nM, m0 = f * 128;
+  const bool want_x = p.out != nullptr, want_g = p.ds || p.dw0;
+  int s_lo = sl * p.per, s_hi = s_lo + p.per;
+  const int kg = m0 + (wave >> 2) * 64;  // G: this wave's columns
+  u32x4 xt[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = kg + 16 * i + r16;
+      xt[i][h] = u32x4{0u, 0u, 0u, 0u};
+      if (want_g && k < p.M) xt[i][h] = ld16(args.xt + static_cast<int64_t>(k) * kFewT + 32 * h + 8 * g);
+    }
+  f32x4 acc[kFewT / 16];
+#pragma unroll
+  for (int j = 0; j < kFewT / 16; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int si = 0; si < p.nseg; ++si) {
+    const Seg &sg = p.seg[si];
+    const int steps = (sg.len + kStep - 1) / kStep;
+    const int b0 = max(0, s_lo), ns = min(steps, s_hi) - b0;
+    s_lo -= steps;
+    s_hi -= steps;
+    if (ns <= 0) continue;
+    const bool with_g = want_g && si < args.nslot;
+    const FewOperands o{{lane, sg.lda, wave * 16}, {lane, sg.ldb, 0}, {lane, kFewT, 0}};
+    const int64_t n0 = static_cast<int64_t>(b0) * kStep;
+    const int64_t row = with_g ? args.row[si] + n0 : 0;
+    FewSource src;
+    src.a = sg.A + n0 * sg.lda + m0;
+    src.b = sg.B + n0;
+    src.d = with_g ? args.dyt[si] + n0 * kFewT : sg.B;
+    src.s = p.s + row;
+    src.lima = keep(want_x || (with_g && p.ds) ? p.M - m0 : 0);
+    src.limb = keep(want_x ? p.N : 0);
+    src.left = min(sg.len, (b0 + ns) * kStep) - b0 * kStep;
+    const int adv_a = keep(static_cast<int>(kStep * sg.lda));
+    int rows = src.left;  // of the stage computed and after it
+    auto advance = [&]() {
+      src.a += adv_a;
+      src.b += kStep;
+      src.d += kStep * kFewT;
+      src.s += kStep;
+      src.left -= kStep;
+      src.leftd = with_g ? src.left : 0;
+    };
+    src.leftd = with_g ? src.left : 0;
+#pragma unroll
+    for (int st = 0; st < kFewStages - 1; ++st) {
+      few_load(o, src, lane, wave, ring + st * kFewStage);
+      advance();
+    }
+    int cur = 0, nxt = (kFewStages - 1) * kFewStage;
+    for (int kt = 0; kt < ns; ++kt) {
+      // the stage has landed, and every wave is done with the one before
+      wait_and_sync<(kFewStages - 2) * 5>();
+      FewFrags x;
+      few_step(o, src, lane, wave, ring + nxt, ring, cur, x);
+      advance();
+      if (want_x) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < kFewT / 16; ++j) acc[j] = mfma16x16x32(x.a[h], x.b[j][h], acc[j]);
+      }
+      if (with_g) {
+        const int n = (wave & 3) * 16 + r16;
+        const int64_t at = row + static_cast<int64_t>(kt) * kStep + n;
+        const bool in = n < rows;
+        float t = 0.f;
+        f32x4 G[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          G[i] = mfma16x16x32(xt[i][0], x.d[0], f32x4{0.f, 0.f, 0.f, 0.f});
+          G[i] = mfma16x16x32(xt[i][1], x.d[1], G[i]);
+        }
+        if (p.dw0 && in) {
+          float *dst = p.dw0 + at * p.M + kg + 4 * g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (kg + 16 * i + 4 * g >= p.M) continue;
+            f32x4 q = G[i] * x.s;
+            if (p.accumulate) q += *reinterpret_cast<const f32x4 *>(dst + 16 * i);
+            *reinterpret_cast<f32x4 *>(dst + 16 * i) = q;
+          }
+        }
+        if (p.ds) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // columns past M: X^T is zero
+            t += G[i][0] * __uint_as_float(x.w[i][0] << 16) + G[i][1] * __uint_as_float(x.w[i][0] & 0xffff0000u) +
+                 G[i][2] * __uint_as_float(x.w[i][1] << 16) + G[i][3] * __uint_as_float(x.w[i][1] & 0xffff0000u);
+          t += __shfl_xor(t, 16, 64);
+          t += __shfl_xor(t, 32, 64);
+          if (g == 0 && in) p.dsp[static_cast<int64_t>(2 * f + (wave >> 2)) * p.ldds + at] = t;
+        }
+      }
+      rows -= kStep;
+      nxt = cur;
+      cur = cur + kFewStage == kFewRing ? 0 : cur + kFewStage;
+    }
+    wait_and_sync<0>();  // the ring is idle
+  }
+  if (!want_x) return;
+  const int k = m0 + wave * 16 + 4 * g;
+  if (k >= p.M) return;
+#pragma unroll
+  for (int j = 0; j < kFewT / 16; ++j) {
+    const int t = 16 * j + r16;
+    if (t >= p.N) continue;
+    if (p.ksplit > 1)
+      *reinterpret_cast<f32x4 *>(p.P + (static_cast<int64_t>(sl) * p.N + t) * p.ldp + k) = acc[j];
+    else
+      *reinterpret_cast<uint2 *>(p.out + t * p.ldo + k) =
+          make_uint2(pack_bf16(acc[j][0], acc[j][1]), pack_bf16(acc[j][2], acc[j][3]));
+  }
+}
+
 // What is left after the products, one launch: for a split product the sum of
 // its slices' partials in slice order -- rows of C as bf16 or a pair (a thread
 // per 4 elements), or dW0's row and ds[n] (a workgroup per row n of G) -- and
@@ -611,7 +806,19 @@ struct PrepArgs {
   CodedView xc;
   int32_t K;
   uint16_t *X;
+  uint16_t *dyt, *xt;  // few tokens: dy^T [ldd][kFewT] and X^T [K][kFewT], zeros past T (else null)
 };
+
+// 8 columns of kPrepT tokens as kPrepT tokens of 8 columns
+__device__ __forceinline__ void store_transposed(const u32x4 (&v)[4], uint16_t *p) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t e[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) e[t] = k & 1 ? v[t][k / 2] >> 16 : v[t][k / 2] & 0xffffu;
+    *reinterpret_cast<uint2 *>(p + k * kFewT) = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+  }
+}
 
 // A thread takes 8 columns of kPrepT tokens: s is read once for all of them (2
 // tokens 66 us, 8 115).
@@ -623,11 +830,17 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
   if (col >= a.dyb) {
     const int k = ((col - a.dyb) * 256 + threadIdx.x) * 8;
     if (k >= a.K) return;
+    u32x4 v[kPrepT];
 #pragma unroll
     for (int i = 0; i < kPrepT; ++i) {
       const int64_t t = t0 + i;
-      if (t < a.T) *reinterpret_cast<u32x4 *>(a.X + t * a.K + k) = expand8(a.xc, t, k);
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (t < a.T) {
+        v[i] = expand8(a.xc, t, k);
+        *reinterpret_cast<u32x4 *>(a.X + t * a.K + k) = v[i];
+      }
     }
+    if (a.xt) store_transposed(v, a.xt + static_cast<int64_t>(k) * kFewT + t0);
     return;
   }
   const int c = (col * 256 + threadIdx.x) * 8;
@@ -649,8 +862,10 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
     for (int k = 0; k < 8; ++k) s[k] = a.dys && k < n ? a.s[i][j + k] : 0.f;
   }
   const uint16_t *src = a.dy + t0 * a.ldy + a.from[i] + j;
-  const int nt = static_cast<int>(min<int64_t>(kPrepT, a.T - t0));
+  const int nt = static_cast<int>(min<int64_t>(kPrepT, a.T - t0));  // (past T: none)
   u32x4 v[kPrepT];
+#pragma unroll
+  for (int t = 0; t < kPrepT; ++t) v[t] = u32x4{0u, 0u, 0u, 0u};
   if (n >= 8 && a.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
 #pragma unroll
     for (int t = 0; t < kPrepT; ++t)
@@ -665,6 +880,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
         v[t][k] = lo | (hi << 16);
       }
   }
+  if (a.dyt) store_transposed(v, a.dyt + static_cast<int64_t>(c) * kFewT + t0);
 #pragma unroll
   for (int t = 0; t < kPrepT; ++t) {
     if (t >= nt) break;
@@ -705,6 +921,12 @@ using Big = std::conditional_t<BTR, BTile<256, 256, 2, 4, 32, 4>, BTile<256, 256
 // workgroups share a CU, with four one keeps as many loads in flight.
 using Mid2 = BTile<128, 128, 2, 4, 64, 2>;
 using Mid4 = BTile<128, 128, 2, 4, 64, 4>;
+
+// Elements of W0 from which few tokens take one pass over it: below, its own
+// launch costs more than the second read (43008 x 5376 at T = 16: 536 -> 341 us,
+// without dW0 315 -> 195; 5376 x 8192 111 -> 96, 85 -> 66; 8192 x 1152 49 -> 55,
+// 40 -> 47).
+constexpr int64_t kFewBlock = 16 << 20;
 
 struct BPlan {
   bool big;
@@ -842,8 +1064,32 @@ int slots_of_child(const Slots &s, int child) {
 // G, dU and dV.  A product of extent 0 (no rank) keeps its place.
 struct Plans {
   BPlan z, g[kMaxChildren], dx, G[kMaxChildren], du[kMaxChildren], dv[kMaxChildren];
+  bool few;     // dx (its plan) and every G in one pass
   size_t part;  // bytes of the larger batch's partials
 };
+
+// One pass over W0 for dx and G: few tokens, one dy slot per row of W0 (a tied
+// v slot would need G summed over two), and a block worth another launch.
+bool few_tokens(const CallDesc &c, const Slots &s, int T) {
+  return T <= kFewT && s.n == c.nchild && static_cast<int64_t>(c.Ntot) * c.K >= kFewBlock;
+}
+
+// Slices of its rows: the fewest rounds of steps over the CUs.
+void plan_few(int K, int steps, BPlan &p) {
+  p = BPlan{};
+  p.nM = (K + 127) / 128;
+  p.nN = 1;
+  int64_t best = INT64_MAX;
+  for (int ks = 1; ks <= 32 && ks <= std::max(1, steps / 4); ++ks) {
+    const int per = std::max(1, (steps + ks - 1) / ks), n = std::max(1, (steps + per - 1) / per);
+    const int64_t cost = (static_cast<int64_t>(p.nM) * n + kCUs - 1) / kCUs * (per + 6);
+    if (cost < best) {
+      best = cost;
+      p.per = per;
+      p.ksplit = n;
+    }
+  }
+}
 
 Plans plans_of(const CallDesc &c, const Slots &s, int T) {
   Plans p{};
@@ -855,9 +1101,8 @@ Plans plans_of(const CallDesc &c, const Slots &s, int T) {
     it[n] = Item{M, N, steps, pair};
     to[n++] = &dst;
   };
-  auto done = [&] {
+  auto done = [&](size_t bytes) {
     plan_batch(it, n, got);
-    size_t bytes = 0;
     for (int i = 0; i < n; ++i) {
       *to[i] = got[i];
       bytes += got[i].partial_bytes(it[i].M, it[i].N);
@@ -867,24 +1112,28 @@ Plans plans_of(const CallDesc &c, const Slots &s, int T) {
   };
   add(c.Rz, T, steps_of(c.K), p.z, true);
   for (int i = 0; i < c.nchild; ++i) add(c.ch[i].rpad, T, slots_of_child(s, i) * steps_of(c.ch[i].N), p.g[i], true);
-  done();
+  done(0);
   int dx_steps = 2 * steps_of(c.Rz);  // g's pair
   for (int i = 0; i < s.n; ++i) dx_steps += steps_of(s.cols[i]);
-  add(c.K, T, dx_steps, p.dx);
+  p.few = few_tokens(c, s, T);
+  if (p.few)
+    plan_few(c.K, dx_steps, p.dx);
+  else
+    add(c.K, T, dx_steps, p.dx);
   for (int i = 0; i < c.nchild; ++i) {
     const int steps = slots_of_child(s, i) * steps_of(T);
-    add(c.K, c.ch[i].N, steps, p.G[i]);
+    if (!p.few) add(c.K, c.ch[i].N, steps, p.G[i]);
     add(c.ch[i].rpad, c.ch[i].N, 2 * steps, p.du[i]);
     add(c.ch[i].rpad, c.K, 2 * steps_of(T), p.dv[i]);
   }
-  done();
+  done(p.few ? p.dx.partial_bytes(c.K, T) : 0);
   return p;
 }
 
 // Workspace: X bf16 [T][K], dy copies [T][ldd] x 2, z and g as pairs [T][2 Rz], the ds
 // partial sums, and the K-split partials of a batch.
 struct Offsets {
-  size_t x, dyp, dys, z, g, dsp, part, bytes;
+  size_t x, dyp, dys, z, g, dsp, dyt, xt, part, bytes;
 };
 
 Offsets offsets_of(const CallDesc &c, const Slots &s, const Plans &p, int T) {
@@ -901,6 +1150,8 @@ Offsets offsets_of(const CallDesc &c, const Slots &s, const Plans &p, int T) {
   o.z = take(static_cast<size_t>(T) * c.Rz * 4);
   o.g = take(static_cast<size_t>(T) * c.Rz * 4);
   o.dsp = take(static_cast<size_t>((c.K + 127) / 128) * 2 * c.Ntot * 4);
+  o.dyt = take(p.few ? static_cast<size_t>(s.ldd) * kFewT * 2 : 0);
+  o.xt = take(p.few ? static_cast<size_t>(c.K) * kFewT * 2 : 0);
   o.part = take(p.part);
   o.bytes = at;
   return o;
@@ -911,6 +1162,7 @@ struct Batch {
   int n = 0;
   Prob p[kMaxProb];
   bool big[kMaxProb];
+  const FewArgs *few = nullptr;  // dx and G in one pass
 };
 
 template <typename TL, auto KERN>
@@ -937,6 +1189,11 @@ void add_units(BwdArgs &a, const Prob &p) {
 // workgroups first -- and the launch that sums what they left.
 hipError_t launch_batch(const Batch &b, hipStream_t stream) {
   hipError_t e;
+  if (b.few) {
+    if ((e = ensure_lds<few_kernel>(kFewRing)) != hipSuccess) return e;
+    hipLaunchKernelGGL(few_kernel, dim3(b.few->p.nM * b.few->p.ksplit), dim3(kFewWaves * 64), kFewRing, stream, *b.few);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   for (int kind = kColsRows; kind <= kColsCols; ++kind) {  // (dx and G)
     BwdArgs a{};
     for (int i = 0; i < b.n; ++i)
@@ -958,14 +1215,22 @@ hipError_t launch_batch(const Batch &b, hipStream_t stream) {
   }
   SumArgs a{};
   int blocks = 0;
-  for (int i = 0; i < b.n; ++i) {
-    const Prob &p = b.p[i];
-    if (p.ksplit == 1 && !(p.mode == kWeight && p.ds)) continue;
+  auto add_sum = [&](const Prob &p) {
+    if (p.ksplit == 1 && !(p.mode == kWeight && p.ds)) return;
     a.first[a.nprob] = blocks;
     a.p[a.nprob++] = p;
     blocks += p.ksplit == 1       ? (p.N + 15) / 16
               : p.mode == kWeight ? p.N
                                   : static_cast<int>((static_cast<int64_t>(p.N) * (p.ldp / 4) + 255) / 256);
+  };
+  for (int i = 0; i < b.n; ++i) add_sum(b.p[i]);
+  if (b.few) {
+    Prob p = b.few->p;
+    if (p.out) add_sum(p);
+    p.mode = kWeight;  // ds, whose parts are not slices
+    p.ksplit = 1;
+    p.N = p.ldds;
+    add_sum(p);
   }
   if (!a.nprob) return hipSuccess;
   std::fill(a.first + a.nprob, a.first + kMaxProb, kNoUnit);
@@ -1056,14 +1321,19 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     a.start[s.n] = s.ldd;
     a.dyp = direct ? nullptr : reinterpret_cast<uint16_t *>(ws + at.dyp);
     a.dys = o.dx ? dys : nullptr;
-    a.dyb = o.dx || !direct ? (s.ldd / 8 + 255) / 256 : 0;
+    a.dyb = o.dx || !direct || a.dyt ? (s.ldd / 8 + 255) / 256 : 0;
     a.xc = xc;
     a.K = K;
     a.X = X;
+    if (pl.few && want_w) {
+      a.dyt = reinterpret_cast<uint16_t *>(ws + at.dyt);
+      a.xt = reinterpret_cast<uint16_t *>(ws + at.xt);
+    }
     const int xb = want_u || want_v || want_w ? (K / 8 + 255) / 256 : 0;
     a.cols = a.dyb + xb;
     if (a.cols > 0) {
-      hipLaunchKernelGGL(prepare_kernel, dim3((T + kPrepT - 1) / kPrepT * a.cols), dim3(256), 0, stream, a);
+      const int groups = ((a.xt ? kFewT : T) + kPrepT - 1) / kPrepT;
+      hipLaunchKernelGGL(prepare_kernel, dim3(groups * a.cols), dim3(256), 0, stream, a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }
@@ -1093,12 +1363,33 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
   }
   uint8_t *part = ws + at.part;
   Batch b;
-  if (o.dx) {
-    // dx = (dy (.) s) W0 + g V^T
-    Prob &p = add_product(b, pl.dx, kColsRows, K, K, T, o.dx, K, part);
+  auto dx_segments = [&](Prob &p) {  // dx = (dy (.) s) W0 + g V^T
     for (int j = 0; j < s.n; ++j)
       add_seg(p, c.W0 + static_cast<int64_t>(c.ch[s.child[j]].row_start) * K, K, dys + s.start[j], s.ldd, s.cols[j]);
     for (int lo = 0; lo < 2 && c.Rz > 0; ++lo) add_seg(p, c.Vt, K, g + lo * c.Rz, ldz, c.Rz);
+  };
+  FewArgs few{};
+  if (pl.few && (o.dx || want_w)) {
+    Batch one;
+    few.p = add_product(one, pl.dx, kColsRows, K, K, T, o.dx, K, part);
+    Prob &p = few.p;
+    dx_segments(p);
+    if (!o.dx) p.nseg = s.n;
+    p.s = c.s;
+    p.dw0 = o.dw0;
+    p.accumulate = o.dw0 ? o.accumulate : 0;
+    p.ds = o.ds;
+    p.dsp = reinterpret_cast<float *>(ws + at.dsp);
+    p.ldds = c.Ntot;
+    few.nslot = s.n;
+    for (int j = 0; j < s.n; ++j) {
+      few.row[j] = c.ch[s.child[j]].row_start;
+      few.dyt[j] = reinterpret_cast<const uint16_t *>(ws + at.dyt) + static_cast<int64_t>(s.start[j]) * kFewT;
+    }
+    few.xt = reinterpret_cast<const uint16_t *>(ws + at.xt);
+    b.few = &few;
+  } else if (o.dx) {
+    dx_segments(add_product(b, pl.dx, kColsRows, K, K, T, o.dx, K, part));
   }
   for (int i = 0; i < c.nchild; ++i) {
     // G (dW0 and ds), dU and dV: contractions over the tokens
@@ -1107,7 +1398,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
       for (int j = 0; j < s.n; ++j)
         if (s.child[j] == i) add_seg(p, A, lda, column(j), ldp, T);
     };
-    if (want_w) {
+    if (want_w && !pl.few) {
       Prob &p = add_product(b, pl.G[i], kColsCols, K, K, ch.N, nullptr, 0, part);
       add_tokens(p, X, K);
       p.mode = kWeight;
