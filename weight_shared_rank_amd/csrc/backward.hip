@@ -21,7 +21,8 @@
 // holds all a's, as W0, V^T and U are for dx and g, and dy and X for G).
 // Both come from HBM straight into LDS as they lie; a k-column operand is
 // transposed on its way to the registers by ds_read_b64_tr_b16, so no
-// transposed copy of a weight or of dy is ever written.
+// transposed copy of a weight is ever written (of dy and X only where few
+// tokens make it small: few_kernel).
 //
 // What is rounded on the way, as the matrix cores take bf16 operands: dy (.) s
 // once to bf16, and z and g to a pair of bf16 (the value and what its rounding
