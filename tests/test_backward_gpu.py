@@ -174,7 +174,9 @@ CASES = [(O, (16,), 8, (1,), 1), (O, (40,), 64, (4,), 1), (O, (1,), 128, (0,), 3
          # few tokens through a large block: one pass over it
          (O, (4100,), 4104, (0,), 1), (O, (1030,), 16392, (129,), 33), (GU, (2101, 2101), 4008, (20, 0), 64),
          (GU, (265, 265), 40000, (3, 40), 50), (QKV, (64000, 130, 63), 264, (33, 16, 8), 17),
-         (QKV, (12000, 3000, 2000), 1000, (8, 64, 1), 64), (O, (4100,), 4104, (4,), 65)]
+         (QKV, (12000, 3000, 2000), 1000, (8, 64, 1), 64), (O, (4100,), 4104, (4,), 65),
+         (GU, (2101, 2101), 4008, (20, 0), 128), (QKV, (12000, 3000, 2001), 1000, (8, 64, 1), 97),
+         (O, (4100,), 4104, (4,), 129)]
 
 
 @pytest.mark.parametrize("fams,rows,K,ranks,T", CASES)
@@ -238,7 +240,7 @@ def test_gradients_match_differences(gpu_lib):
             assert abs(have - want) <= 2 * H * got[i].double().norm().item() * d.norm().item(), (name, i)
 
 
-@pytest.mark.parametrize("rows,K,T", [((200, 72, 40), 264, 100), ((6000, 2000, 333), 2104, 60)])
+@pytest.mark.parametrize("rows,K,T", [((200, 72, 40), 264, 100), ((6000, 2000, 333), 2104, 60), ((6000, 2000, 333), 2104, 120)])
 def test_subsets_give_the_same_bits(gpu_lib, rows, K, T):
     lay = Layer(QKV, rows, K, (40, 33, 8), seed=6)
     code, dy = binding.encode_act(randn(7, T, K)), randn(8, T, lay.width)
@@ -253,7 +255,7 @@ def test_subsets_give_the_same_bits(gpu_lib, rows, K, T):
                 same_bits((a,), (b,))
 
 
-@pytest.mark.parametrize("T,rows,K", [(40, 300, 264), (2500, 24, 264), (40, 4100, 4104)])
+@pytest.mark.parametrize("T,rows,K", [(40, 300, 264), (2500, 24, 264), (40, 4100, 4104), (90, 4100, 4104)])
 def test_accumulated_block_gradient(gpu_lib, T, rows, K):
     """dw0 += over the layers of a band: the sum of the calls' own gradients,
     one float32 rounding per addition; both with and without a split."""

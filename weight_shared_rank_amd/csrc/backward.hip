@@ -500,67 +500,87 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
     product_unit<TL, false, false>(p, v, lds);
 }
 
-// Few tokens (T <= kFewT): dx, dW0 and ds in one pass over W0.  A workgroup
+// Few tokens (T <= 128): dx, dW0 and ds in one pass over W0.  A workgroup
 // owns 128 columns k and a slice of the rows n of W0; a stage is 64 rows.  From
 // it come dx's terms, with the 64 columns of dy (.) s that belong to the rows,
 // and the stage's G, whose contraction is the tokens alone: dy and X are at hand
-// transposed, [column][kFewT tokens], so G's operands need no LDS transpose and
-// X's stay in registers.  For dx a wave takes 16 k and all n, for G 64 k and 16
-// n.  dx's other terms (g V^T) are further stages without G.  Bound by W0 once
-// through and dW0's way out (43008 x 5376 at T = 16: 273 us, 5.1 TB/s); without
-// dW0 by the 48 KB of W0 a CU has in flight (133 us, 3.5 TB/s).
-constexpr int kFewT = 64, kFewStages = 4, kFewWaves = 8;
-constexpr int kFewY = 64 * 128 * 2, kFewD = kFewY + kFewT * 128, kFewS = kFewD + 64 * 128;  // dy (.) s, dy^T, s
-constexpr int kFewStage = kFewS + kFewWaves * 256, kFewRing = kFewStages * kFewStage;
-static_assert(kFewRing <= 160 * 1024, "ring");
+// transposed, in panels of 64 tokens [column][64], so G's operands need no LDS
+// transpose and X's stay in registers.  For dx a wave takes 16 k and all n, for
+// G 64 k and 16 n.  dx's other terms (g V^T) are further stages without G.
+// Bound by W0 once through and dW0's way out (43008 x 5376 at T = 16: 273 us,
+// 5.1 TB/s); without dW0 by the 48 KB of W0 a CU has in flight (133 us, 3.5
+// TB/s).  Past 64 tokens a stage holds two panels and the ring three stages
+// (the call at T = 128: 596 -> 430 us, without dW0 391 -> 292); three panels
+// would leave no ring.
+constexpr int kPanel = 64, kFewPanels = 2, kFewWaves = 8;
+
+// H panels of tokens.
+template <int H_>
+struct FewTile {
+  static constexpr int H = H_, T = H * kPanel, NST = H == 1 ? 4 : 3;
+  static constexpr int Y = 64 * 128 * 2, D = Y + T * 128, S = D + 64 * 2 * T;  // in a stage: dy (.) s, dy^T, s
+  static constexpr int STAGE = S + kFewWaves * 256, RING = NST * STAGE;
+  static constexpr int LPW = 2 + 2 * H + 1;  // load instructions of a wave per stage
+  static_assert(RING <= 160 * 1024, "ring");
+};
 
 struct FewArgs {
   Prob p;  // dx: M = K, N = T; its segments over dy's slots come first
   int32_t nslot;
   int32_t row[kMaxChildren];          // slot -> first row of W0, s, dW0 and ds
-  const uint16_t *dyt[kMaxChildren];  // slot -> dy^T [columns][kFewT]
-  const uint16_t *xt;                 // X^T [K][kFewT]
+  const uint16_t *dyt[kMaxChildren];  // slot -> dy^T [panel][columns][64]
+  const uint16_t *xt;                 // X^T [panel][K][64]
+  int64_t dpanel;                     // elements from a panel of dy^T to the next
 };
 
+template <typename TL>
 struct FewOperands {
   Operand<128, true, 64> a;       // W0 (or V^T): 128 columns
-  Operand<kFewT, false, 64> b;    // dy (.) s (or g): the tokens
+  Operand<TL::T, false, 64> b;    // dy (.) s (or g): the tokens
   Operand<64, false, 64> d;       // dy^T: the stage's rows n
 };
 
 struct FewSource {
   const uint16_t *a, *b, *d;
   const float *s;
+  int64_t dpanel;
   int lima, limb, left, leftd;  // columns, tokens; rows n left, of them with a G
 };
 
+template <typename TL>
 struct FewFrags {
-  u32x4 a[2], b[kFewT / 16][2], d[2];
+  u32x4 a[2], b[TL::T / 16][2], d[TL::H][2];
   u32x2 w[4];
   float s;
 };
 
 // A stage's loads into `w` and another's reads from `r` (restrict: move_stage).
-__device__ __forceinline__ void few_load(const FewOperands &o, const FewSource &f, int lane, int wave, lds_u8 *w) {
+template <typename TL>
+__device__ __forceinline__ void few_load(const FewOperands<TL> &o, const FewSource &f, int lane, int wave, lds_u8 *w) {
   o.a.load(f.a, 2 * wave, f.lima, f.left, w);
   o.a.load(f.a, 2 * wave + 1, f.lima, f.left, w);
-  o.b.load(f.b, wave, f.limb, f.left, w + kFewY);
-  o.d.load(f.d, wave, f.leftd, kFewT, w + kFewD);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_rsrc(f.s), (lds_void *)(w + kFewS + wave * 256), 4,
+#pragma unroll
+  for (int h = 0; h < TL::H; ++h) {
+    o.b.load(f.b, TL::H * wave + h, f.limb, f.left, w + TL::Y);
+    o.d.load(f.d + h * f.dpanel, wave, f.leftd, kPanel, w + TL::D + h * 64 * 2 * kPanel);
+  }
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_rsrc(f.s), (lds_void *)(w + TL::S + wave * 256), 4,
                                            lane < f.leftd ? lane * 4 : kBufNoRow, 0, 0, 0);
 }
 
-__device__ __forceinline__ void few_step(const FewOperands &o, const FewSource &f, int lane, int wave,
+template <typename TL>
+__device__ __forceinline__ void few_step(const FewOperands<TL> &o, const FewSource &f, int lane, int wave,
                                          lds_u8 *__restrict__ w, const lds_u8 *__restrict__ r, int stage,
-                                         FewFrags &x) {
-  few_load(o, f, lane, wave, w);
+                                         FewFrags<TL> &x) {
+  few_load<TL>(o, f, lane, wave, w);
   const int r16 = lane & 15, g = lane >> 4, n = (wave & 3) * 16 + r16;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     x.a[h] = o.a.frag(r, stage, 0, h);
 #pragma unroll
-    for (int j = 0; j < kFewT / 16; ++j) x.b[j][h] = o.b.frag(r, stage + kFewY, j, h);
-    x.d[h] = o.d.frag(r, stage + kFewD, wave & 3, h);
+    for (int j = 0; j < TL::T / 16; ++j) x.b[j][h] = o.b.frag(r, stage + TL::Y, j, h);
+#pragma unroll
+    for (int q = 0; q < TL::H; ++q) x.d[q][h] = o.d.frag(r, stage + TL::D + q * 64 * 2 * kPanel, wave & 3, h);
   }
   // W0[n][64 (wave / 4) + 16 i + 4 g ..]: chunk c of LDS row n lies in slot c ^ swz(n)
 #pragma unroll
@@ -568,9 +588,10 @@ __device__ __forceinline__ void few_step(const FewOperands &o, const FewSource &
     const int c = (wave >> 2) * 8 + 2 * i + (g >> 1), swz = 2 * (n & 3) + 8 * ((n >> 3) & 1);
     x.w[i] = *(const __attribute__((address_space(3))) u32x2 *)(r + stage + n * 256 + ((c ^ swz) * 16) + (g & 1) * 8);
   }
-  x.s = *(const __attribute__((address_space(3))) float *)(r + stage + kFewS + wave * 256 + n * 4);
+  x.s = *(const __attribute__((address_space(3))) float *)(r + stage + TL::S + wave * 256 + n * 4);
 }
 
+template <typename TL>
 __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(1, 2))) void few_kernel(FewArgs args) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   lds_u8 *const ring = (lds_u8 *)lds;
@@ -582,18 +603,19 @@ __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(
   const bool want_x = p.out != nullptr, want_g = p.ds || p.dw0;
   int s_lo = sl * p.per, s_hi = s_lo + p.per;
   const int kg = m0 + (wave >> 2) * 64;  // G: this wave's columns
-  u32x4 xt[4][2];
+  u32x4 xt[4][2 * TL::H];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * TL::H; ++h) {
       const int k = kg + 16 * i + r16;
       xt[i][h] = u32x4{0u, 0u, 0u, 0u};
-      if (want_g && k < p.M) xt[i][h] = ld16(args.xt + static_cast<int64_t>(k) * kFewT + 32 * h + 8 * g);
+      if (want_g && k < p.M)
+        xt[i][h] = ld16(args.xt + (static_cast<int64_t>(h / 2) * p.M + k) * kPanel + 32 * (h % 2) + 8 * g);
     }
-  f32x4 acc[kFewT / 16];
+  f32x4 acc[TL::T / 16];
 #pragma unroll
-  for (int j = 0; j < kFewT / 16; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < TL::T / 16; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   for (int si = 0; si < p.nseg; ++si) {
     const Seg &sg = p.seg[si];
@@ -603,13 +625,14 @@ __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(
     s_hi -= steps;
     if (ns <= 0) continue;
     const bool with_g = want_g && si < args.nslot;
-    const FewOperands o{{lane, sg.lda, wave * 16}, {lane, sg.ldb, 0}, {lane, kFewT, 0}};
+    const FewOperands<TL> o{{lane, sg.lda, wave * 16}, {lane, sg.ldb, 0}, {lane, kPanel, 0}};
     const int64_t n0 = static_cast<int64_t>(b0) * kStep;
     const int64_t row = with_g ? args.row[si] + n0 : 0;
     FewSource src;
     src.a = sg.A + n0 * sg.lda + m0;
     src.b = sg.B + n0;
-    src.d = with_g ? args.dyt[si] + n0 * kFewT : sg.B;
+    src.d = with_g ? args.dyt[si] + n0 * kPanel : sg.B;
+    src.dpanel = with_g ? args.dpanel : 0;
     src.s = p.s + row;
     src.lima = keep(want_x || (with_g && p.ds) ? p.M - m0 : 0);
     src.limb = keep(want_x ? p.N : 0);
@@ -619,29 +642,29 @@ __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(
     auto advance = [&]() {
       src.a += adv_a;
       src.b += kStep;
-      src.d += kStep * kFewT;
+      src.d += kStep * kPanel;
       src.s += kStep;
       src.left -= kStep;
       src.leftd = with_g ? src.left : 0;
     };
     src.leftd = with_g ? src.left : 0;
 #pragma unroll
-    for (int st = 0; st < kFewStages - 1; ++st) {
-      few_load(o, src, lane, wave, ring + st * kFewStage);
+    for (int st = 0; st < TL::NST - 1; ++st) {
+      few_load<TL>(o, src, lane, wave, ring + st * TL::STAGE);
       advance();
     }
-    int cur = 0, nxt = (kFewStages - 1) * kFewStage;
+    int cur = 0, nxt = (TL::NST - 1) * TL::STAGE;
     for (int kt = 0; kt < ns; ++kt) {
       // the stage has landed, and every wave is done with the one before
-      wait_and_sync<(kFewStages - 2) * 5>();
-      FewFrags x;
-      few_step(o, src, lane, wave, ring + nxt, ring, cur, x);
+      wait_and_sync<(TL::NST - 2) * TL::LPW>();
+      FewFrags<TL> x;
+      few_step<TL>(o, src, lane, wave, ring + nxt, ring, cur, x);
       advance();
       if (want_x) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < kFewT / 16; ++j) acc[j] = mfma16x16x32(x.a[h], x.b[j][h], acc[j]);
+          for (int j = 0; j < TL::T / 16; ++j) acc[j] = mfma16x16x32(x.a[h], x.b[j][h], acc[j]);
       }
       if (with_g) {
         const int n = (wave & 3) * 16 + r16;
@@ -651,8 +674,9 @@ __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(
         f32x4 G[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          G[i] = mfma16x16x32(xt[i][0], x.d[0], f32x4{0.f, 0.f, 0.f, 0.f});
-          G[i] = mfma16x16x32(xt[i][1], x.d[1], G[i]);
+          G[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2 * TL::H; ++h) G[i] = mfma16x16x32(xt[i][h], x.d[h / 2][h % 2], G[i]);
         }
         if (p.dw0 && in) {
           float *dst = p.dw0 + at * p.M + kg + 4 * g;
@@ -676,7 +700,7 @@ __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(
       }
       rows -= kStep;
       nxt = cur;
-      cur = cur + kFewStage == kFewRing ? 0 : cur + kFewStage;
+      cur = cur + TL::STAGE == TL::RING ? 0 : cur + TL::STAGE;
     }
     wait_and_sync<0>();  // the ring is idle
   }
@@ -684,7 +708,7 @@ __global__ __launch_bounds__(kFewWaves * 64) __attribute__((amdgpu_waves_per_eu(
   const int k = m0 + wave * 16 + 4 * g;
   if (k >= p.M) return;
 #pragma unroll
-  for (int j = 0; j < kFewT / 16; ++j) {
+  for (int j = 0; j < TL::T / 16; ++j) {
     const int t = 16 * j + r16;
     if (t >= p.N) continue;
     if (p.ksplit > 1)
@@ -807,7 +831,7 @@ struct PrepArgs {
   CodedView xc;
   int32_t K;
   uint16_t *X;
-  uint16_t *dyt, *xt;  // few tokens: dy^T [ldd][kFewT] and X^T [K][kFewT], zeros past T (else null)
+  uint16_t *dyt, *xt;  // few tokens: dy^T [panel][ldd][64] and X^T [panel][K][64], zeros past T (else null)
 };
 
 // 8 columns of kPrepT tokens as kPrepT tokens of 8 columns
@@ -817,7 +841,7 @@ __device__ __forceinline__ void store_transposed(const u32x4 (&v)[4], uint16_t *
     uint32_t e[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) e[t] = k & 1 ? v[t][k / 2] >> 16 : v[t][k / 2] & 0xffffu;
-    *reinterpret_cast<uint2 *>(p + k * kFewT) = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    *reinterpret_cast<uint2 *>(p + k * kPanel) = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
   }
 }
 
@@ -841,7 +865,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
         *reinterpret_cast<u32x4 *>(a.X + t * a.K + k) = v[i];
       }
     }
-    if (a.xt) store_transposed(v, a.xt + static_cast<int64_t>(k) * kFewT + t0);
+    if (a.xt) store_transposed(v, a.xt + (t0 / kPanel * a.K + k) * kPanel + t0 % kPanel);
     return;
   }
   const int c = (col * 256 + threadIdx.x) * 8;
@@ -881,7 +905,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepArgs a) {
         v[t][k] = lo | (hi << 16);
       }
   }
-  if (a.dyt) store_transposed(v, a.dyt + static_cast<int64_t>(c) * kFewT + t0);
+  if (a.dyt) store_transposed(v, a.dyt + (t0 / kPanel * a.ldd + c) * kPanel + t0 % kPanel);
 #pragma unroll
   for (int t = 0; t < kPrepT; ++t) {
     if (t >= nt) break;
@@ -1072,8 +1096,10 @@ struct Plans {
 // One pass over W0 for dx and G: few tokens, one dy slot per row of W0 (a tied
 // v slot would need G summed over two), and a block worth another launch.
 bool few_tokens(const CallDesc &c, const Slots &s, int T) {
-  return T <= kFewT && s.n == c.nchild && static_cast<int64_t>(c.Ntot) * c.K >= kFewBlock;
+  return T <= kFewPanels * kPanel && s.n == c.nchild && static_cast<int64_t>(c.Ntot) * c.K >= kFewBlock;
 }
+
+int few_panels(int T) { return T <= kPanel ? 1 : kFewPanels; }
 
 // Slices of its rows: the fewest rounds of steps over the CUs.
 void plan_few(int K, int steps, BPlan &p) {
@@ -1151,8 +1177,9 @@ Offsets offsets_of(const CallDesc &c, const Slots &s, const Plans &p, int T) {
   o.z = take(static_cast<size_t>(T) * c.Rz * 4);
   o.g = take(static_cast<size_t>(T) * c.Rz * 4);
   o.dsp = take(static_cast<size_t>((c.K + 127) / 128) * 2 * c.Ntot * 4);
-  o.dyt = take(p.few ? static_cast<size_t>(s.ldd) * kFewT * 2 : 0);
-  o.xt = take(p.few ? static_cast<size_t>(c.K) * kFewT * 2 : 0);
+  const size_t few = p.few ? static_cast<size_t>(few_panels(T)) * kPanel * 2 : 0;
+  o.dyt = take(s.ldd * few);
+  o.xt = take(c.K * few);
   o.part = take(p.part);
   o.bytes = at;
   return o;
@@ -1180,6 +1207,14 @@ hipError_t launch_big(BwdArgs &a, hipStream_t stream) {
   return launch_kernel<Big<BTR>, product_kernel<Big<BTR>, true, BTR>>(a, stream);
 }
 
+template <typename TL>
+hipError_t launch_few(const FewArgs &a, hipStream_t stream) {
+  const hipError_t e = ensure_lds<few_kernel<TL>>(TL::RING);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(few_kernel<TL>, dim3(a.p.nM * a.p.ksplit), dim3(kFewWaves * 64), TL::RING, stream, a);
+  return hipGetLastError();
+}
+
 void add_units(BwdArgs &a, const Prob &p) {
   a.unit0[a.nprob] = a.total;
   a.p[a.nprob++] = p;
@@ -1191,9 +1226,8 @@ void add_units(BwdArgs &a, const Prob &p) {
 hipError_t launch_batch(const Batch &b, hipStream_t stream) {
   hipError_t e;
   if (b.few) {
-    if ((e = ensure_lds<few_kernel>(kFewRing)) != hipSuccess) return e;
-    hipLaunchKernelGGL(few_kernel, dim3(b.few->p.nM * b.few->p.ksplit), dim3(kFewWaves * 64), kFewRing, stream, *b.few);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = b.few->p.N <= kPanel ? launch_few<FewTile<1>>(*b.few, stream) : launch_few<FewTile<kFewPanels>>(*b.few, stream);
+    if (e != hipSuccess) return e;
   }
   for (int kind = kColsRows; kind <= kColsCols; ++kind) {  // (dx and G)
     BwdArgs a{};
@@ -1333,7 +1367,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     const int xb = want_u || want_v || want_w ? (K / 8 + 255) / 256 : 0;
     a.cols = a.dyb + xb;
     if (a.cols > 0) {
-      const int groups = ((a.xt ? kFewT : T) + kPrepT - 1) / kPrepT;
+      const int groups = ((a.xt ? few_panels(T) * kPanel : T) + kPrepT - 1) / kPrepT;
       hipLaunchKernelGGL(prepare_kernel, dim3(groups * a.cols), dim3(256), 0, stream, a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -1385,8 +1419,9 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     few.nslot = s.n;
     for (int j = 0; j < s.n; ++j) {
       few.row[j] = c.ch[s.child[j]].row_start;
-      few.dyt[j] = reinterpret_cast<const uint16_t *>(ws + at.dyt) + static_cast<int64_t>(s.start[j]) * kFewT;
+      few.dyt[j] = reinterpret_cast<const uint16_t *>(ws + at.dyt) + static_cast<int64_t>(s.start[j]) * kPanel;
     }
+    few.dpanel = static_cast<int64_t>(s.ldd) * kPanel;
     few.xt = reinterpret_cast<const uint16_t *>(ws + at.xt);
     b.few = &few;
   } else if (o.dx) {
