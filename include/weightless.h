@@ -361,7 +361,7 @@ wl_status weightless_weight_encode(const void *d_w, int32_t N, int32_t K, void *
  *    exactly what weightless_act_encode writes (a checkpoint to keep).
  *  d_ws: weightless_coded_linear_workspace_bytes(N, K, T) bytes, 256-byte
  *    aligned, no initialization, nothing kept; may be NULL if that is 0 bytes
- *    (always so for T <= 4).  Concurrent calls need distinct workspaces.
+ *    (always so for T <= 4; fewer tokens can need more).  Concurrent calls need distinct workspaces.
  *  T <= 16 streams the weights once through registers; T <= 2 is one launch,
  *  x coded in it (T <= 4 with coded x); T > 16 runs LDS-tiled matrix-core
  *  products.  K is split over workgroups and summed by another launch when
@@ -395,7 +395,8 @@ typedef struct {
 } wl_grads;
 
 /* Workspace bytes of any backward call on this bundle with T tokens; 0 with
- * wl_last_error() set on error. */
+ * wl_last_error() set on error.  Fewer tokens can need more (another split of
+ * the sums): a workspace for several T has the largest of their sizes. */
 size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T);
 
 /* Gradients of weightless_linear (one family) and of weightless_stacked_linear.

@@ -431,11 +431,11 @@ def test_widest_calls(gpu_lib):
 
 def test_dw0_alone_of_a_coded_block_needs_no_block(gpu_lib):
     """dW0 of FP8 and MXFP4 bundles without dx or ds, split over the tokens or
-    not: W0 is not expanded and not read."""
+    not, or of few tokens: W0 is not expanded and not read."""
     for fmt in ("fp8", "mxfp4"):
-        for T, rows in ((40, 300), (2500, 24)):
-            lay = Layer(O, (rows,), 264, (8,), fmt=fmt, seed=15)
-            code, dy = binding.encode_act(randn(62, T, 264)), randn(63, T, rows)
+        for T, rows, K in ((40, 300, 264), (2500, 24, 264), (20, 4100, 4104), (70, 4100, 4104)):
+            lay = Layer(O, (rows,), K, (8,), fmt=fmt, seed=15)
+            code, dy = binding.encode_act(randn(62, T, K)), randn(63, T, rows)
             announce(f"dw0 {fmt} T={T}")
             same_bits(lay.backward(code, dy, want=("dw0",)), lay.backward(code, dy)._replace(dx=None, ds=None, du=None, dv=None))
 

@@ -1373,6 +1373,8 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     }
   }
   const int64_t ldz = 2 * static_cast<int64_t>(c.Rz);  // z and g: the values, then the remainders
+  // rows of W0 from `row` on (null where no gradient asked for reads W0)
+  auto block = [&](int row) { return c.W0 ? c.W0 + static_cast<int64_t>(row) * K : nullptr; };
   auto column = [&](int slot) { return dyp + (direct ? s.from[slot] : s.start[slot]); };
   {
     // z = X V and g = dy U
@@ -1400,7 +1402,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
   Batch b;
   auto dx_segments = [&](Prob &p) {  // dx = (dy (.) s) W0 + g V^T
     for (int j = 0; j < s.n; ++j)
-      add_seg(p, c.W0 + static_cast<int64_t>(c.ch[s.child[j]].row_start) * K, K, dys + s.start[j], s.ldd, s.cols[j]);
+      add_seg(p, block(c.ch[s.child[j]].row_start), K, dys + s.start[j], s.ldd, s.cols[j]);
     for (int lo = 0; lo < 2 && c.Rz > 0; ++lo) add_seg(p, c.Vt, K, g + lo * c.Rz, ldz, c.Rz);
   };
   FewArgs few{};
@@ -1439,7 +1441,7 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
       add_tokens(p, X, K);
       p.mode = kWeight;
       p.s = c.s + ch.row_start;
-      p.W0 = c.W0 + static_cast<int64_t>(ch.row_start) * K;
+      p.W0 = block(ch.row_start);
       p.dw0 = o.dw0 ? o.dw0 + static_cast<int64_t>(ch.row_start) * K : nullptr;
       p.accumulate = o.dw0 ? o.accumulate : 0;
       p.ds = o.ds ? o.ds + ch.row_start : nullptr;
