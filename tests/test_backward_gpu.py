@@ -400,6 +400,55 @@ def test_forward_checkpoint_backward_together(gpu_lib):
     assert abs(full - (g.ds.double() ** 2).sum().item()) <= 2.0 ** -4 * mass
 
 
+@pytest.mark.parametrize("T", [3, 16, 40, 300])
+def test_step_of_a_block_in_a_graph(gpu_lib, T):
+    """A block's step as a captured graph, replayed on new inputs: the shared
+    q|k|v call, a dense projection in 8 bits whose coded input is the checkpoint,
+    and both layers' gradients added into the band's one dW0.  Every replay
+    equals the calls made one by one."""
+    lay = Layer(QKV, (256, 64, 64), 520, (16, 8, 8), seed=18, layers=2)
+    wc = binding.encode_weight(randn(70, 200, 520, std=520 ** -0.5))
+    ins = [[randn(71 + 2 * i, T, 520), randn(72 + 2 * i, T, lay.width, std=T ** -0.5)] for i in range(3)]
+
+    def step(x, dy, dw0, ws):
+        dw0.zero_()
+        y = lay.bundle.stacked(1, "qkv", x)
+        code = binding.ActCode(T, 520)
+        d = binding.coded_linear(wc, x, code=code)
+        out = [y, d]
+        for l in (0, 1):
+            g = lay.bundle.stacked_backward(l, "qkv", code, dy, want=ALL, dw0=dw0, accumulate=True, ws=ws)
+            out += [g.dx, g.ds, *g.du, *g.dv]
+        return out
+    need = binding.lib().weightless_backward_workspace_bytes(lay.bundle.handle, T)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    want = []
+    for x, dy in ins:
+        dw0 = torch.empty(384, 520, device=DEV)
+        want.append([t.clone() for t in step(x, dy, dw0, ws)] + [dw0])
+    x, dy, dw0 = ins[0][0].clone(), ins[0][1].clone(), torch.empty(384, 520, device=DEV)
+    torch.cuda.synchronize()
+    announce(f"captured step T={T}")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, dy, dw0, ws)
+    for i in (1, 0, 2, 1):
+        x.copy_(ins[i][0])
+        dy.copy_(ins[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out + [dw0], want[i]):
+            assert torch.equal(a, b)
+        again = torch.empty_like(dw0)
+        step(ins[2 - i][0], ins[2 - i][1], again, ws)   # eager work between the replays, on the same workspace
+        assert torch.equal(again, want[2 - i][-1])
+    # the layers' gradients of the shared block add up
+    alone = [lay.bundle.stacked_backward(l, "qkv", binding.encode_act(ins[1][0]), ins[1][1], want=("dw0",)).dw0
+             for l in (0, 1)]
+    total = alone[0] + alone[1]
+    assert ((want[1][-1] - total).abs() <= 2 * F * (alone[0].abs() + alone[1].abs())).all()
+
+
 @pytest.mark.parametrize("T,K", [(1 << 20, 8), (5, 1 << 20)])
 def test_most_tokens_and_longest_rows(gpu_lib, T, K):
     lay = Layer(O, (9,), K, (5,), seed=16)

@@ -178,14 +178,12 @@ __global__ __launch_bounds__(256) void encode_weight_kernel(const uint16_t *w, i
     scales[static_cast<int64_t>(kb) * ldsc + blockIdx.y + threadIdx.x] = 127;
 }
 
-// x[t][k] = code * 2^e as bf16 (exact), 8 elements per thread; ldx >= K
-// columns per row, those at k >= K (up to Kq) written only if ldx covers them
-// (their codes are zero).
-__global__ __launch_bounds__(256) void expand_act_kernel(CodedView c, uint16_t *x, int ldx) {
+// x[t][k] = code * 2^e as bf16 (exact), 8 elements per thread.
+__global__ __launch_bounds__(256) void expand_act_kernel(CodedView c, uint16_t *x, int K) {
   const int k = (blockIdx.y * 256 + threadIdx.x) * 8;
   const int64_t tok = blockIdx.x;
-  if (k >= c.nb * kBlk || k >= ldx) return;
-  *reinterpret_cast<u32x4 *>(x + tok * ldx + k) = expand8(c, tok, k);
+  if (k >= K) return;
+  *reinterpret_cast<u32x4 *>(x + tok * K + k) = expand8(c, tok, k);
 }
 
 struct CodedArgs {
@@ -696,9 +694,9 @@ hipError_t launch_encode_weight(const uint16_t *w, int N, int K, const CodedView
   return hipGetLastError();
 }
 
-hipError_t launch_expand_act(const CodedView &c, int T, uint16_t *x, int ldx, hipStream_t stream) {
+hipError_t launch_expand_act(const CodedView &c, int T, uint16_t *x, int K, hipStream_t stream) {
   const dim3 grid(T, (c.nb * (kBlk / 8) + 255) / 256);
-  hipLaunchKernelGGL(expand_act_kernel, grid, dim3(256), 0, stream, c, x, ldx);
+  hipLaunchKernelGGL(expand_act_kernel, grid, dim3(256), 0, stream, c, x, K);
   return hipGetLastError();
 }
 

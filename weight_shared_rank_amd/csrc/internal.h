@@ -101,8 +101,8 @@ struct CodedView {
 };
 hipError_t launch_encode_act(const uint16_t *x, int T, int K, const CodedView &o, hipStream_t stream);
 hipError_t launch_encode_weight(const uint16_t *w, int N, int K, const CodedView &o, hipStream_t stream);
-// x [T][ldx] bf16 = code * 2^e (ldx >= K, a multiple of 8)
-hipError_t launch_expand_act(const CodedView &c, int T, uint16_t *x, int ldx, hipStream_t stream);
+// x [T][K] bf16 = code * 2^e
+hipError_t launch_expand_act(const CodedView &c, int T, uint16_t *x, int K, hipStream_t stream);
 // y [T][N] = x w^T; partials: coded_partial_bytes(N, T, K) bytes.  src: bf16
 // [T][K] to be coded into x first, or null if x holds coded activations.
 size_t coded_partial_bytes(int N, int T, int K);
