@@ -1016,7 +1016,7 @@ def main():
     line["detail"] = res
     if "prefill5" in res:
         p = res["prefill5"]
-        psha = source_sha("prefill.hip", "common.h", "internal.h")
+        psha = source_sha("prefill.hip", "lds_dma.h", "common.h", "internal.h")
         ptraffic, pt_rd, pt_wr = traffic_from_profile("prefill", psha)
         line["prefill"] = {"metric": "prefill TFLOP/s", "value": round(p["TFLOPs"], 2), "unit": "TFLOP/s",
                            "mfma_frac": round(p["mfma_frac"], 4), "peak": BF16_PEAK_TFLOPS,

@@ -33,10 +33,10 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.h"
-#include "internal.h"
 #include "coded.h"
+#include "common.h"
 #include "lds_dma.h"
+#include "training.h"
 
 namespace wl {
 

@@ -1,12 +1,21 @@
-// Device access to 8-bit coded activations (coded.hip describes the coding).
+// Device access to 8-bit coded activations (coded.hip describes the coding), and
+// the conversion to bf16 that goes with it.
 #pragma once
 
 #include "common.h"
-#include "internal.h"
+#include "training.h"
 
 namespace wl {
 
 constexpr int kCodeBlock = 128;
+
+// Two floats -> two bf16 in one instruction (nearest-even, NaN stays NaN); a in
+// the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
 
 // Elements k .. k + 7 (k % 8 == 0) of row t: code * 2^e as bf16, exact.
 __device__ __forceinline__ u32x4 expand8(const CodedView &c, int64_t t, int k) {

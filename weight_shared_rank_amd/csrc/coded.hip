@@ -32,8 +32,8 @@
 
 #include "coded.h"
 #include "common.h"
-#include "internal.h"
 #include "lds_dma.h"
+#include "training.h"
 
 namespace wl {
 

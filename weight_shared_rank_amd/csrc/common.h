@@ -28,14 +28,6 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return static_cast<uint16_t>(u >> 16);
 }
 
-// Two floats -> two bf16 in one instruction (nearest-even, NaN stays NaN); a in
-// the low half.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-
 // Activations of the fused gate|up epilogue, fp32 (act codes of the ABI:
 // 0 gelu with the tanh approximation, 1 silu, 2 gelu with erf).  The tanh
 // form is evaluated through 0.5 (1 + tanh u) = 1 / (1 + e^-2u), so

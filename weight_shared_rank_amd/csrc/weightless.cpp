@@ -37,6 +37,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "training.h"
 #include "weightless.h"
 
 namespace {
