@@ -255,6 +255,76 @@ def test_subsets_give_the_same_bits(gpu_lib, rows, K, T):
                 same_bits((a,), (b,))
 
 
+def poisoned(lay, code, dy, want=ALL, dw0=None):
+    """The call through the C ABI with every byte of the workspace and of the
+    outputs 0xFF (NaN as bf16 and as float32), so that nothing an earlier call
+    left can stand in for what this one must write; dw0: accumulated into."""
+    import ctypes
+    L, T = binding.lib(), code.T
+
+    def nans(*shape, dtype=torch.bfloat16):
+        return torch.full((int(np.prod(shape)) * dtype.itemsize,), 0xFF, dtype=torch.uint8, device=DEV).view(dtype).view(shape)
+    g, out = binding.WlGrads(), {}
+    for name, shape, dtype in (("dx", (T, lay.K), torch.bfloat16), ("ds", (sum(lay.rows),), torch.float32),
+                               ("dw0", (sum(lay.rows), lay.K), torch.float32)):
+        if name in want:
+            out[name] = dw0 if name == "dw0" and dw0 is not None else nans(*shape, dtype=dtype)
+            setattr(g, name, out[name].data_ptr())
+    g.accumulate_dw0 = dw0 is not None
+    for name, heights in (("du", lay.rows), ("dv", [lay.K] * len(lay.rows))):
+        if name in want:
+            out[name] = tuple(nans(h, r) for h, r in zip(heights, lay.ranks))
+            for i, t in enumerate(out[name]):
+                getattr(g, name)[i] = t.data_ptr() or None
+    need = L.weightless_backward_workspace_bytes(lay.bundle.handle, T)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    fn, which = (L.weightless_stacked_backward, binding.STACKS[lay.stack]) if lay.stack else \
+        (L.weightless_linear_backward, binding.FAMILY[lay.fams[0]])
+    st = fn(lay.bundle.handle, lay.layer, which, code.buf.data_ptr(), code.buf.numel(), dy.data_ptr(), T,
+            ctypes.byref(g), ws.data_ptr(), need, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0, binding.last_error()
+    return binding.Grads(**out)
+
+
+@pytest.mark.parametrize("T", [1, 16, 64, 65, 128])
+@pytest.mark.parametrize("fams,rows,K,ranks,fmt", [
+    (O, (4104,), 4104, (8,), "bf16"), (GU, (2104, 2104), 4008, (20, 0), "bf16"),
+    (QKV, (6000, 2000, 336), 2104, (40, 33, 8), "bf16"), (O, (4104,), 4104, (8,), "fp8")])
+def test_one_pass_without_dx_reads_dy_in_place(gpu_lib, fams, rows, K, ranks, fmt, T):
+    """Few tokens through a large block with rows in multiples of 8: dy is read
+    where it lies, and what the call then wants of it decides what is prepared."""
+    lay = Layer(fams, rows, K, ranks, fmt=fmt, seed=19)
+    code, dy = binding.encode_act(randn(80, T, K)), randn(81, T, lay.width, std=T ** -0.5)
+    announce(f"all of {rows} {fmt} T={T}")
+    full = poisoned(lay, code, dy)
+    check(lay, code, dy, full)
+    for want in (("ds",), ("dw0",), ("ds", "dw0"), ("ds", "du"), ("dw0", "dv"), ("du", "dv"), ("dx",), ("dx", "dw0")):
+        announce(f"want {want}")
+        part = poisoned(lay, code, dy, want)
+        for name in want:
+            same_bits((getattr(part, name),), (getattr(full, name),))
+    acc = randn(82, sum(rows), K, dtype=torch.float32)
+    total = acc + full.dw0
+    poisoned(lay, code, dy, ("dw0",), dw0=acc)
+    assert ((acc - total).abs() <= F * (full.dw0.abs() + total.abs())).all()
+
+
+@pytest.mark.parametrize("T,rows,K,ranks,tied", [(3, (24, 16), 264, (5, 13), False), (70, (21, 13), 136, (4, 0), False),
+                                                 (200, (304, 304), 520, (40, 8), False), (90, (64, 32), 264, (16, 8), True)])
+def test_every_subset_on_a_poisoned_workspace(gpu_lib, T, rows, K, ranks, tied):
+    """All 31 choices of gradients: each writes all it reads of its workspace."""
+    lay = Layer(QKV if tied else GU, rows, K, ranks, tied=tied, seed=20)
+    code, dy = binding.encode_act(randn(83, T, K)), randn(84, T, lay.width)
+    full = poisoned(lay, code, dy)
+    check(lay, code, dy, full)
+    for bits in range(1, 31):
+        want = tuple(n for i, n in enumerate(ALL) if bits >> i & 1)
+        announce(f"want {want}")
+        part = poisoned(lay, code, dy, want)
+        for name in want:
+            same_bits((getattr(part, name),), (getattr(full, name),))
+
+
 @pytest.mark.parametrize("T,rows,K", [(40, 300, 264), (2500, 24, 264), (40, 4100, 4104), (90, 4100, 4104)])
 def test_accumulated_block_gradient(gpu_lib, T, rows, K):
     """dw0 += over the layers of a band: the sum of the calls' own gradients,

@@ -1356,14 +1356,15 @@ hipError_t launch_backward(const CallDesc &c, const CodedView &xc, const uint16_
     a.start[s.n] = s.ldd;
     a.dyp = direct ? nullptr : reinterpret_cast<uint16_t *>(ws + at.dyp);
     a.dys = o.dx ? dys : nullptr;
-    a.dyb = o.dx || !direct || a.dyt ? (s.ldd / 8 + 255) / 256 : 0;
-    a.xc = xc;
-    a.K = K;
-    a.X = X;
     if (pl.few && want_w) {
       a.dyt = reinterpret_cast<uint16_t *>(ws + at.dyt);
       a.xt = reinterpret_cast<uint16_t *>(ws + at.xt);
     }
+    // dy's columns are visited if any form of them is written
+    a.dyb = a.dyp || a.dys || a.dyt ? (s.ldd / 8 + 255) / 256 : 0;
+    a.xc = xc;
+    a.K = K;
+    a.X = X;
     const int xb = want_u || want_v || want_w ? (K / 8 + 255) / 256 : 0;
     a.cols = a.dyb + xb;
     if (a.cols > 0) {
