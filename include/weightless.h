@@ -329,8 +329,8 @@ wl_status weightless_decompose_als(const void *d_w, int32_t m, int32_t N, int32_
  *          activations: Rp = T rounded up to 16, byte [b][t] for token t;
  *          weights: Rp = ceil(N / 128) rounded up to 4, byte [b][n / 128].
  * K % 8 == 0 as everywhere; N, K, T in [1, 2^20], T 0 allowed (no-op), and
- * T * nb < 2^30.  WL_ESHAPE otherwise.  Buffers of one call must not overlap
- * (WL_EINVAL). */
+ * Rp * nb < 2^30 for activations (T rounded up to 16, times nb).  WL_ESHAPE
+ * otherwise.  Buffers of one call must not overlap (WL_EINVAL). */
 
 /* Bytes of a coded buffer of activations x [T, K] (tokens are rows) or of a
  * weight [N, K]; 0 with wl_last_error() set on error. */

@@ -44,6 +44,18 @@ def test_act_shapes_refused(L, T, K, status, frag):
     assert L.weightless_coded_linear(A, BIG, 64, K, None, 2 * A, BIG, T, 3 * A, 4 * A, BIG, None) == status
 
 
+@pytest.mark.parametrize("T,nb", [((1 << 20) - 1, 1024), ((1 << 20) - 15, 1024), ((1 << 18) - 3, 4096)])
+def test_the_bound_on_blocks_counts_padded_tokens(L, T, nb):
+    """T rounded up to 16, times nb, stays below 2^30: refused at it, though T
+    itself times nb is below; taken with the next fewer multiple of 16."""
+    K = nb * 128
+    assert T * nb < 1 << 30 <= align(T, 16) * nb
+    assert L.weightless_act_code_bytes(T, K) == 0 and "rounded up to 16" in binding.last_error()
+    assert L.weightless_act_encode(A, T, K, 2 * A, 1 << 60, None) == -2
+    T = T // 16 * 16
+    assert L.weightless_act_code_bytes(T, K) == T * K + nb * T
+
+
 def test_weight_shapes_refused(L):
     for n, k in ((0, 8), (-1, 8), ((1 << 20) + 1, 8), (8, 4)):
         assert L.weightless_weight_code_bytes(n, k) == 0

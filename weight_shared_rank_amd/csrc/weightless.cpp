@@ -529,7 +529,8 @@ wl_status check_act_shape(int32_t T, int32_t K) {
   if (T < 0) return fail(WL_EINVAL, "T = %d is negative", T);
   if (T > kMaxDim) return fail(WL_ESHAPE, "T = %d too large", T);
   const CodeShape c = code_shape(T, K, false);
-  if (c.nb * c.rp >= (int64_t{1} << 30)) return fail(WL_ESHAPE, "T = %d by K = %d exceeds 2^30 blocks", T, K);
+  if (c.nb * c.rp >= (int64_t{1} << 30))
+    return fail(WL_ESHAPE, "T = %d (rounded up to 16) by K = %d makes 2^30 blocks or more", T, K);
   return WL_OK;
 }
 
