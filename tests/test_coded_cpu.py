@@ -1,6 +1,7 @@
 """8-bit coded operands on the host: sizes and layout of coded buffers, the
 refusals of the entry points (all returned before anything is enqueued), and
 the oracle's coding rule against hand values."""
+import contextlib
 import os
 
 import numpy as np
@@ -114,6 +115,31 @@ def test_workspace_is_zero_for_few_tokens_and_small_otherwise(L):
     for T in (5, 16, 17, 64, 333, 2048):
         n = L.weightless_coded_linear_workspace_bytes(5376, 21504, T)
         assert n % 256 == 0 and n <= 16 * T * 5376 * 4
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 40])
+def test_binding_gives_the_workspace_the_library_asks_for(L, monkeypatch, T):
+    """Whatever the library's rule: here every token count needs 512 bytes more
+    than it says."""
+    class Library:
+        def __getattr__(self, name):
+            return getattr(L, name)
+
+        def weightless_coded_linear_workspace_bytes(self, N, K, T):
+            return L.weightless_coded_linear_workspace_bytes(N, K, T) + 512
+
+        def weightless_coded_linear(self, *args):
+            given.append(args[9:11])
+            return 0
+    given = []
+    monkeypatch.setattr(binding, "_lib", Library())
+    monkeypatch.setattr(binding, "_scope", lambda device, stream: contextlib.nullcontext())
+    monkeypatch.setattr(binding, "_raw_stream", lambda device: 0)
+    w, x = binding.WeightCode(5376, 21504, device="cpu"), binding.ActCode(T, 21504, device="cpu")
+    for _ in range(2):
+        binding.coded_linear(w, x)
+    need = L.weightless_coded_linear_workspace_bytes(5376, 21504, T) + 512
+    assert len(given) == 2 and all(ptr and size == need for ptr, size in given)
 
 
 def test_binding_refuses_host_strided_and_mistyped_tensors(L):

@@ -446,7 +446,6 @@ def decompose(w, rank: int, omega=None, oversample: int = 16, power_iters: int =
 # ---- 8-bit coded operands -------------------------------------------------
 
 CODE_BLOCK = 128
-CODED_NO_WORKSPACE_T = 4     # weightless_coded_linear needs no workspace up to here
 
 
 _HERE = contextlib.nullcontext()
@@ -544,9 +543,21 @@ class WeightCode(_Code):
 
     _rows_per_scale, _run_multiple, _bytes = CODE_BLOCK, 4, "weightless_weight_code_bytes"
 
+    def __init__(self, rows: int, K: int, device="cuda", buf=None):
+        super().__init__(rows, K, device, buf)
+        self._linear_need = {}   # T -> workspace bytes
+
     @property
     def N(self) -> int:
         return self.rows
+
+    def workspace_bytes(self, T: int) -> int:
+        """Workspace bytes of coded_linear with T tokens (0: none needed)."""
+        need = self._linear_need.get(T)
+        if need is None:
+            need = lib().weightless_coded_linear_workspace_bytes(self.rows, self.K, T)
+            self._linear_need[T] = need
+        return need
 
 
 def _code_out(cls, rows, K, device, out):
@@ -604,11 +615,10 @@ def coded_linear(w: WeightCode, x, y=None, code: Optional[ActCode] = None, ws=No
             y = torch.empty((T, w.rows), dtype=torch.bfloat16, device=dev)
         else:
             _check_tensor(y, "y", (T, w.rows), torch.bfloat16, dev)
-        if ws is None and T > CODED_NO_WORKSPACE_T:
-            need = lib().weightless_coded_linear_workspace_bytes(w.rows, w.K, T)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif ws is not None:
+        if ws is not None:
             _check_tensor(ws, "ws", (None,), torch.uint8, dev)
+        elif w.workspace_bytes(T):
+            ws = torch.empty(w.workspace_bytes(T), dtype=torch.uint8, device=dev)
         _check(lib().weightless_coded_linear(w.buf.data_ptr(), w.buf.numel(), w.rows, w.K, src, code.buf.data_ptr(),
                                              code.buf.numel(), T, y.data_ptr(),
                                              ws.data_ptr() if ws is not None else None,
