@@ -384,7 +384,13 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
  * significant bits); dx, dU and dV are rounded once at the end; G, ds and dW0
  * are float32 throughout.  Results are the same bits from run to run, whichever
  * of them are asked for.  An element of dy or of the checkpoint that is not
- * finite makes NaN or infinity of what it enters, and changes nothing else. */
+ * finite makes NaN or infinity of what it enters, and changes nothing else.
+ *
+ * No entry point changes a loaded bundle.  A training step keeps its own s, U,
+ * V and W0, updates them, and calls theta_bundle_load again; the arena may be
+ * the same one if the load follows, on its stream, the calls that read the old
+ * values.  A load copies every source, W0 too: 43008 x 5376 at rank 256 (490 MB)
+ * takes 0.3 ms on the card. */
 typedef struct {
   void *dx;         /* bf16 [T, K] */
   float *ds;        /* float32 [N] */

@@ -470,6 +470,36 @@ def test_forward_checkpoint_backward_together(gpu_lib):
     assert abs(full - (g.ds.double() ** 2).sum().item()) <= 2.0 ** -4 * mass
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_updated_values_are_loaded_into_the_same_arena(gpu_lib, fmt):
+    """A step's update as the header describes it: the new values loaded over
+    the old on the same stream, behind the calls that read those, with no
+    synchronization between; the bits are a fresh bundle's."""
+    T, K, rows = 40, 520, (256, 256)
+    a, b = (Layer(GU, rows, K, (16, 8), fmt=fmt, seed=i) for i in (21, 22))
+    x, dy = randn(90, T, K), randn(91, T, sum(rows), std=T ** -0.5)
+    code = binding.encode_act(x)
+
+    def step(bundle):
+        g = bundle.stacked_backward(0, "gate_up", code, dy, want=ALL)
+        return [bundle.stacked(0, "gate_up", x), g.dx, g.ds, *g.du, *g.dv, g.dw0]
+
+    def sources(lay):
+        return [(kind, 0, 0, f, t[i]) for i, f in enumerate(GU)
+                for kind, t in (("w0", lay.w0), ("s", lay.s), ("u", lay.u), ("v", lay.v))]
+    spec = a.bundle.spec
+    want = [step(binding.ThetaBundle(spec, sources(l), device=DEV)) for l in (a, b)]
+    arena = torch.empty_like(a.bundle.arena)
+    announce(f"load over {fmt}")
+    bundles, got = [], []
+    for i in range(6):
+        bundles.append(binding.ThetaBundle(spec, sources((a, b)[i % 2]), device=DEV, arena=arena))
+        got.append(step(bundles[-1]))
+    for i, g in enumerate(got):
+        for p, q in zip(g, want[i % 2]):
+            assert torch.equal(p, q)
+
+
 @pytest.mark.parametrize("T", [3, 16, 40, 300])
 def test_step_of_a_block_in_a_graph(gpu_lib, T):
     """A block's step as a captured graph, replayed on new inputs: the shared
