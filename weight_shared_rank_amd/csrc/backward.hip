@@ -508,10 +508,14 @@ __global__ __launch_bounds__(TL::NW * 64) __attribute__((amdgpu_waves_per_eu(1, 
 // transpose and X's stay in registers.  For dx a wave takes 16 k and all n, for
 // G 64 k and 16 n.  dx's other terms (g V^T) are further stages without G.
 // Bound by W0 once through and dW0's way out (43008 x 5376 at T = 16: 273 us,
-// 5.1 TB/s); without dW0 by the 48 KB of W0 a CU has in flight (133 us, 3.5
-// TB/s).  Past 64 tokens a stage holds two panels and the ring three stages
-// (the call at T = 128: 596 -> 430 us, without dW0 391 -> 292); three panels
-// would leave no ring.
+// 5.1 TB/s; the counted wait on a stage also waits out dW0 stores of the steps
+// before).  Without dW0 bound by a step's own chain -- barrier, LDS reads,
+// MFMAs, ds's lane exchanges in turn, nothing read ahead -- of which a
+// workgroup runs 115, 1.15 us each (133 us, 3.5 TB/s): matrix cores busy 0.20
+// and LDS 0.24 of the cycles, waves waiting 0.47.  A step does 64 tokens' work
+// for any T <= 64.  Past 64 tokens a stage holds two panels and the ring three
+// stages (the call at T = 128: 596 -> 430 us, without dW0 391 -> 292; the pass
+// then 0.25, 0.23 and 0.47); three panels would leave no ring.
 constexpr int kPanel = 64, kFewPanels = 2, kFewWaves = 8;
 
 // H panels of tokens.

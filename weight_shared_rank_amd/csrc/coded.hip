@@ -203,7 +203,10 @@ struct CodedArgs {
 // The weights go straight from HBM to registers as the A operand, each row
 // read in 128-byte blocks by four lanes; the tokens' codes are the B operand
 // (lanes past the last token repeat the first: their columns are not stored).
-// Bound by reading N K bytes: 21504 x 5376 in 20.5 us for loads alone.
+// Bound by reading N K bytes.  21504 x 5376 at T = 1, calls in a graph: 20.3 us
+// over one weight again and again, 116 MB that stay in the 256 MB Infinity
+// Cache (5.7 TB/s; 20.5 us for loads alone), 23.9 us where six weights take
+// turns and each comes from HBM (4.8 TB/s).
 
 // A workgroup's up to 16 rows over the whole K; its 16 waves take pairs of
 // blocks in turn, so that neighbouring waves read neighbouring runs of the same
@@ -214,8 +217,8 @@ struct CodedArgs {
 // FUSE (T <= kFuseT): x comes as bf16 and every wave codes the blocks it needs,
 // 16 lanes to a block as encode_act_kernel, through its part of LDS; workgroup
 // 0 also writes the coded buffer.  It saves the coding launch and the x loads'
-// turn (21504 x 5376 at T = 1: 25.2 us against 24.9 + 4 for the two launches,
-// 4096 x 1152: 3.5 against 3.0 + 3).  Two blocks a lane group, which would take
+// turn (several weights in turn, 21504 x 5376 at T = 1: 25.2 us against 24.9 + 4
+// for the two launches, 4096 x 1152: 3.5 against 3.0 + 3).  Two blocks a lane group, which would take
 // 4 tokens, spills at 8 waves per SIMD: 47 us.
 constexpr int kStreamWaves = 16, kStreamPair = 2;
 constexpr int kFuseT = 4 / kStreamPair;  // a wave's 4 groups of 16 lanes code a pair's blocks at once
@@ -638,9 +641,9 @@ CPlan plan_coded(int N, int T, int nb) {
 
 // Slices of the several-token stream, 0 for the one-tile kernel (which needs
 // none).  It pays for its summing launch (4 us) where the x loads it saves are
-// worth more: from 64 M codes on (21504 x 5376 at T = 16: 30.6 us against
-// 33.3, 5376 x 21504: 28.8 against 39.5; 8192 x 5376: 13.2 against 12.2, 4096 x
-// 5376: 10.4 against 7.3).  The slices are the fewest whose workgroups come
+// worth more: from 64 M codes on (several weights in turn, 21504 x 5376 at T =
+// 16: 30.6 us against 33.3, 5376 x 21504: 28.8 against 39.5; 8192 x 5376: 13.2
+// against 12.2, 4096 x 5376: 10.4 against 7.3).  The slices are the fewest whose workgroups come
 // within 15% of whole rounds of the CUs, of at least 8 blocks (one per wave).
 int wide_slices(int N, int T, int nb) {
   if (T <= kNarrowT || static_cast<int64_t>(N) * nb * kBlk < (int64_t{64} << 20)) return 0;
