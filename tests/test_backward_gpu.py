@@ -557,6 +557,71 @@ def test_most_tokens_and_longest_rows(gpu_lib, T, K):
     check(lay, code, dy, lay.backward(code, dy))
 
 
+@pytest.mark.parametrize("N,K", [(520, 8192), (8200, 136)])
+def test_more_than_2_31_elements(gpu_lib, N, K):
+    """270000 tokens: x, then dy, hold more than 2^31 elements, and their bytes
+    pass 2^32.  Against float64 sums over runs of tokens, by norms: the matrix
+    cores round a sum of T terms T / 32 times, each by at most 2^-24 of it, and
+    the slices' sums add less than as many again."""
+    T, run = 270000, 10000
+    lay = Layer(O, (N,), K, (8,), seed=23)
+    gen = torch.Generator(DEV).manual_seed(92)
+
+    def rand(width, std):
+        t = torch.empty(T, width, dtype=torch.bfloat16, device=DEV)
+        for i in range(0, T, run):
+            t[i:i + run] = torch.randn(run, width, generator=gen, device=DEV) * std
+        return t
+    x, dy = rand(K, 1.0), rand(N, T ** -0.5)
+    announce(f"T={T} {N} x {K}")
+    code = binding.encode_act(x)
+    X = code.expand()
+    for i in range(0, T, run):
+        assert torch.equal(X[i:i + run], binding.encode_act(x[i:i + run]).expand())
+    del x
+    g = lay.backward(code, dy)
+    w, s, u, v = lay.w0[0].double(), lay.s[0].double(), lay.u[0].double(), lay.v[0].double()
+    G = torch.zeros(N, K, dtype=torch.float64, device=DEV)
+    for i in range(0, T, run):
+        d, a = dy[i:i + run].double(), X[i:i + run].double()
+        G += d.t().contiguous() @ a
+        ref = (d * s) @ w + (d @ u) @ v.t().contiguous()
+        assert (g.dx[i:i + run].double() - ref).norm() <= 2 * H * ref.norm(), i
+    sums = T / 16 * 2.0 ** -24
+    for got, want, tol in ((g.dw0, s[:, None] * G, sums), (g.ds, (G * w).sum(1), 2 * sums),
+                           (g.du[0], G @ v, H + sums), (g.dv[0], G.t().contiguous() @ u, H + sums)):
+        assert (got.double() - want).norm() <= tol * want.norm()
+
+
+@pytest.mark.parametrize("T", [20, 200])
+def test_a_block_of_more_than_2_31_elements(gpu_lib, T):
+    """W0 and dW0 of 2.4e9 elements, in one pass over W0 and as products; the
+    tolerances of this file's head over runs of rows."""
+    N, K, run = 290000, 8320, 10000
+    gen = torch.Generator(DEV).manual_seed(94)
+    w0 = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, N, run):
+        w0[i:i + run] = torch.randn(run, K, generator=gen, device=DEV) * K ** -0.5
+    s = 1 + 0.2 * randn(95, N, dtype=torch.float32)
+    bundle = binding.ThetaBundle(binding.make_spec(1, 1, {(0, "o"): (N, K)}, {}),
+                                 [("w0", 0, 0, "o", w0), ("s", 0, 0, "o", s)], device=DEV)
+    code, dy = binding.encode_act(randn(96, T, K)), randn(97, T, N, std=T ** -0.5)
+    announce(f"{N} x {K} T={T}")
+    g = bundle.linear_backward(0, "o", code, dy, want=("dx", "ds", "dw0"))
+    X = code.expand().double()
+    dx, top = torch.zeros_like(X), torch.zeros_like(X)
+    for i in range(0, N, run):
+        at = slice(i, i + run)
+        d, w, si = dy[:, at].double(), w0[at].double(), s[at].double()
+        G, mass = d.t().contiguous() @ X, d.t().abs().contiguous() @ X.abs()
+        assert ((g.dw0[at] - si[:, None] * G).abs() <= (T + 8) * F * si.abs()[:, None] * mass).all(), i
+        assert ((g.ds[at] - (G * w).sum(1)).abs() <= (T + K + 8) * F * (mass * w.abs()).sum(1)).all(), i
+        dx += (d * si) @ w
+        top += (d * si).abs() @ w.abs()
+    assert ((g.dx - dx).abs() <= (H + (N + 8) * F) * top + H * dx.abs()).all()
+    assert (g.dx.double() - dx).norm() <= 2 * H * dx.norm()
+
+
 def test_widest_calls(gpu_lib):
     """More columns than a load can address are refused; just under it (one
     family of 2^20 rows, beyond what 32-bit element offsets of a token reach)

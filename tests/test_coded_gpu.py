@@ -222,6 +222,56 @@ def test_largest_extents(gpu_lib, T, N, K):
     check_product(y, xv, wv)
 
 
+@pytest.mark.parametrize("N,K", [(200, 8192), (8200, 136)])
+def test_more_than_2_31_elements(gpu_lib, N, K):
+    """270000 tokens: x, then y, hold more than 2^31 elements, and their bytes
+    pass 2^32; each run of rows against its own coded values."""
+    T, run = 270000, 30000
+    gen = torch.Generator(DEV).manual_seed(93)
+    x = torch.empty(T, K, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, T, run):
+        x[i:i + run] = torch.randn(run, K, generator=gen, device=DEV)
+    announce(f"product {T} x {N} x {K}")
+    wc, code = binding.encode_weight(randn(94, N, K, std=K ** -0.5).to(DEV)), binding.ActCode(T, K)
+    y = binding.coded_linear(wc, x, code=code)
+    f = torch.exp2(wc.scales.double() - 127).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    wv = wc.codes.double() * f
+    for i in range(0, T, run):
+        part = binding.encode_act(x[i:i + run])
+        assert torch.equal(code.codes[i:i + run].view(torch.uint8), part.codes.view(torch.uint8))
+        assert torch.equal(code.scales[i:i + run], part.scales)
+        for at in (i, i + run - 40):  # the first and the last 40 rows of the run
+            check_product(y[at:at + 40], part.expand()[at - i:at - i + 40].double(), wv)
+
+
+def test_a_weight_of_more_than_2_32_codes(gpu_lib):
+    """550000 rows of 8192 codes: each run of rows against its own coding, and
+    the products' first, middle and last columns against the coded values."""
+    N, K, run = 550000, 8192, 12800  # whole blocks of rows, the last run short
+    gen = torch.Generator(DEV).manual_seed(95)
+    w = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, N, run):
+        w[i:i + run] = torch.randn(w[i:i + run].shape, generator=gen, device=DEV) * K ** -0.5
+    announce(f"code {N} x {K}")
+    wc = binding.encode_weight(w)
+    parts = {}
+    for i in range(0, N, run):
+        part = binding.encode_weight(w[i:i + run])
+        assert torch.equal(wc.codes[i:i + run].view(torch.uint8), part.codes.view(torch.uint8))
+        assert torch.equal(wc.scales[i // 128:i // 128 + part.scales.shape[0]], part.scales)
+        if i in (0, N // 2 // run * run, N // run * run):
+            parts[i] = part
+    assert len(parts) == 3
+    for T in (1, 12, 60):
+        announce(f"product {T} x {N} x {K}")
+        xc = binding.encode_act(randn(96, T, K).to(DEV))
+        y, xv = binding.coded_linear(wc, xc), xc.expand().double()
+        for i, part in parts.items():
+            f = torch.exp2(part.scales.double() - 127).repeat_interleave(128, 0)[:part.N].repeat_interleave(128, 1)
+            at = slice(part.N - 40, part.N)
+            check_product(y[:, i:i + part.N][:, at], xv, (part.codes.double() * f)[at].contiguous())
+
+
 def test_blocks_of_very_different_scale(gpu_lib):
     """Scales from 2^-60 to 2^60 along K, tokens and weight rows: each block's
     own two scales enter its products."""
