@@ -430,6 +430,46 @@ wl_status weightless_stacked_backward(const wl_bundle *bundle, int32_t layer, in
                                       size_t xcode_bytes, const void *d_dy, int32_t T, const wl_grads *grads,
                                       void *d_ws, size_t ws_bytes, void *stream);
 
+/* ---- Norm before a projection, with the residual's addition and a coded output ----
+ * For each of T token rows of K elements (bf16):
+ *   h = bf16(x + res)                        (h = x if d_res is NULL)
+ *   a = 1 / sqrt(mean_k h_k^2 + eps)         (the mean and a in float64, a stored as float32)
+ *   y = bf16(h a (offset + w))               (a in full, one rounding)
+ *   code = what weightless_act_encode writes for y, byte for byte: the operand
+ *          of weightless_coded_linear and the checkpoint of the backward calls.
+ *  d_w: [K], w_dtype WL_DTYPE_BF16 or WL_DTYPE_F32 (else WL_EDTYPE); offset 1
+ *    for models that store the weight less one, 0 otherwise; finite.
+ *  eps: positive and finite (WL_EINVAL).
+ *  d_h, d_y, d_code (code_bytes >= weightless_act_code_bytes(T, K), else
+ *    WL_ENOSPACE) and d_rstd (float32 [T], the row's a): the outputs wanted,
+ *    each may be NULL but not all.  d_h may be exactly d_x or exactly d_res (the
+ *    residual stream updated in place); nothing else may overlap (WL_EINVAL).
+ *  8 <= K <= 32768 and K % 8 == 0 (WL_ESHAPE), T as for coded activations (0: a
+ *    no-op).  x, res, w, h and y 16-byte aligned.
+ *  A row is normed by itself: an infinity or NaN in it changes no other row.
+ *  One launch. */
+wl_status weightless_norm(const void *d_x, const void *d_res, int32_t T, int32_t K, const void *d_w, int32_t w_dtype,
+                          float offset, float eps, void *d_h, void *d_y, void *d_code, size_t code_bytes,
+                          float *d_rstd, void *stream);
+
+/* Gradients of weightless_norm, with n = h a and g = dy (offset + w):
+ *   dx = bf16(a (g - n mean_k(g n)) + dh)    the gradient of h, so of x and of res alike
+ *   dw = sum_t dy n                          float32 [K]
+ *  d_h, d_rstd: what the forward pass gave; d_dy bf16 [T, K] the gradient of y
+ *    (dx of a projection's backward call); d_dh bf16 [T, K], or NULL for none,
+ *    the gradient that reaches h past the norm (the residual stream's).
+ *  d_dx bf16 [T, K] (16-byte aligned; may be exactly d_dy or exactly d_dh) and
+ *    d_dw (16-byte aligned): either may be NULL, not both.  T = 0: dw is zeroed.
+ *  d_ws: weightless_norm_backward_workspace_bytes(T, K) bytes (0 with
+ *    wl_last_error() set on error), 256-byte aligned, no initialization, nothing
+ *    kept; concurrent calls need distinct workspaces.  May be NULL without dw.
+ *  Sums in float32 in a fixed order: the same bits from run to run, whichever of
+ *  the two are asked for.  One launch, another for the sum of dw. */
+size_t weightless_norm_backward_workspace_bytes(int32_t T, int32_t K);
+wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const float *d_rstd, const void *d_dh, int32_t T,
+                                   int32_t K, const void *d_w, int32_t w_dtype, float offset, void *d_dx, float *d_dw,
+                                   void *d_ws, size_t ws_bytes, void *stream);
+
 /* Output width N of a single-family call, or of a stacked call (stack >= 0
  * with family < 0); 0 on error.  Host-only. */
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack);

@@ -39,7 +39,8 @@ EXPORTS = ("theta_bundle_arena_bytes", "theta_bundle_load", "theta_bundle_free",
            "weightless_act_code_bytes", "weightless_weight_code_bytes", "weightless_act_encode",
            "weightless_act_expand", "weightless_weight_encode",
            "weightless_coded_linear_workspace_bytes", "weightless_coded_linear",
-           "weightless_backward_workspace_bytes", "weightless_linear_backward", "weightless_stacked_backward")
+           "weightless_backward_workspace_bytes", "weightless_linear_backward", "weightless_stacked_backward",
+           "weightless_norm", "weightless_norm_backward_workspace_bytes", "weightless_norm_backward")
 
 
 class WlBundleSpec(ctypes.Structure):
@@ -93,7 +94,7 @@ def lib():
     # second runtime finds no device.
     import torch  # noqa: F401
     L = ctypes.CDLL(LIBPATH)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
     sig = {
         "theta_bundle_arena_bytes": (sz, [ctypes.POINTER(WlBundleSpec)]),
         "theta_bundle_load": (i32, [ctypes.POINTER(WlBundleSpec), ctypes.POINTER(WlSrc), sz, vp, sz, vp,
@@ -122,6 +123,9 @@ def lib():
         "weightless_backward_workspace_bytes": (sz, [vp, i32]),
         "weightless_linear_backward": (i32, [vp, i32, i32, vp, sz, vp, i32, ctypes.POINTER(WlGrads), vp, sz, vp]),
         "weightless_stacked_backward": (i32, [vp, i32, i32, vp, sz, vp, i32, ctypes.POINTER(WlGrads), vp, sz, vp]),
+        "weightless_norm": (i32, [vp, vp, i32, i32, vp, i32, f32, f32, vp, vp, vp, sz, vp, vp]),
+        "weightless_norm_backward_workspace_bytes": (sz, [i32, i32]),
+        "weightless_norm_backward": (i32, [vp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -624,3 +628,106 @@ def coded_linear(w: WeightCode, x, y=None, code: Optional[ActCode] = None, ws=No
                                              ws.data_ptr() if ws is not None else None,
                                              ws.numel() if ws is not None else 0, _raw_stream(dev)))
     return y
+
+
+# ---- norm before a projection ----------------------------------------------
+
+class Normed(NamedTuple):
+    """Outputs of norm_act (None: not asked for)."""
+    y: object = None
+    code: object = None
+    h: object = None
+    rstd: object = None
+
+
+class NormGrads(NamedTuple):
+    """Gradients of norm_act (None: not asked for)."""
+    dx: object = None
+    dw: object = None
+
+
+def _norm_weight(w, K, dev):
+    import torch
+    _check_tensor(w, "weight", (K,), torch.float32 if w.dtype == torch.float32 else torch.bfloat16, dev)
+    return w.data_ptr(), WL_DTYPE_F32 if w.dtype == torch.float32 else WL_DTYPE_BF16
+
+
+def _output(t, name, shape, dtype, dev):
+    """The caller's tensor for an output, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check_tensor(t, name, shape, dtype, dev)
+    return t
+
+
+def _only_wanted(want, known, given):
+    unknown = set(want) - set(known)
+    if unknown or not want:
+        raise WlError(-1, f"unknown outputs {sorted(unknown)}" if unknown else "no output is asked for")
+    for name, t in given.items():
+        if t is not None and name not in want:
+            raise WlError(-1, f"{name} is given but not wanted")
+
+
+def norm_act(x, weight, eps: float = 1e-6, residual=None, offset: float = 0.0, want=("y",), y=None,
+             code: Optional[ActCode] = None, h=None, rstd=None, stream=None) -> Normed:
+    """Root-mean-square norm of x (+ residual), bf16 [T, K] (weightless_norm).
+
+    weight: bf16 or float32 [K], added to `offset`.  want: which of y (bf16),
+    code (ActCode of y: coded_linear's operand and the backward calls'
+    checkpoint), h (bf16, x + residual) and rstd (float32 [T]); y, code, h and
+    rstd are written if given, allocated otherwise.  h may be x or residual."""
+    import torch
+    _check_tensor(x, "x", (None, None), torch.bfloat16)
+    dev, (T, K) = x.device, x.shape
+    _only_wanted(want, Normed._fields, {"y": y, "code": code, "h": h, "rstd": rstd})
+    with _scope(dev, stream):
+        if residual is not None:
+            _check_tensor(residual, "residual", (T, K), torch.bfloat16, dev)
+        w, wt = _norm_weight(weight, K, dev)
+        y = _output(y, "y", (T, K), torch.bfloat16, dev) if "y" in want else None
+        code = _code_out(ActCode, T, K, dev, code) if "code" in want else None
+        h = _output(h, "h", (T, K), torch.bfloat16, dev) if "h" in want else None
+        rstd = _output(rstd, "rstd", (T,), torch.float32, dev) if "rstd" in want else None
+        _check(lib().weightless_norm(x.data_ptr(), None if residual is None else residual.data_ptr(), T, K, w, wt,
+                                     offset, eps, None if h is None else h.data_ptr(),
+                                     None if y is None else y.data_ptr(), None if code is None else code.buf.data_ptr(),
+                                     0 if code is None else code.buf.numel(),
+                                     None if rstd is None else rstd.data_ptr(), _raw_stream(dev)))
+    return Normed(y, code, h, rstd)
+
+
+def norm_backward(dy, h, rstd, weight, offset: float = 0.0, dh=None, want=("dx", "dw"), dx=None, dw=None, ws=None,
+                  stream=None) -> NormGrads:
+    """Gradients of norm_act (weightless_norm_backward).
+
+    dy: bf16 [T, K], the gradient of y; h, rstd: norm_act's; dh: the gradient
+    that reaches h past the norm, or None.  dx is the gradient of x and of the
+    residual alike, bf16 (may be given as dy or dh); dw float32 [K]."""
+    import torch
+    _check_tensor(dy, "dy", (None, None), torch.bfloat16)
+    dev, (T, K) = dy.device, dy.shape
+    _only_wanted(want, NormGrads._fields, {"dx": dx, "dw": dw})
+    with _scope(dev, stream):
+        _check_tensor(h, "h", (T, K), torch.bfloat16, dev)
+        _check_tensor(rstd, "rstd", (T,), torch.float32, dev)
+        if dh is not None:
+            _check_tensor(dh, "dh", (T, K), torch.bfloat16, dev)
+        w, wt = _norm_weight(weight, K, dev)
+        dx = _output(dx, "dx", (T, K), torch.bfloat16, dev) if "dx" in want else None
+        dw = _output(dw, "dw", (K,), torch.float32, dev) if "dw" in want else None
+        if ws is not None:
+            _check_tensor(ws, "ws", (None,), torch.uint8, dev)
+        elif dw is not None:
+            need = lib().weightless_norm_backward_workspace_bytes(T, K)
+            if need == 0:
+                raise WlError(-2, last_error())
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().weightless_norm_backward(dy.data_ptr(), h.data_ptr(), rstd.data_ptr(),
+                                              None if dh is None else dh.data_ptr(), T, K, w, wt, offset,
+                                              None if dx is None else dx.data_ptr(),
+                                              None if dw is None else dw.data_ptr(),
+                                              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                              _raw_stream(dev)))
+    return NormGrads(dx, dw)

@@ -1,0 +1,43 @@
+// Launches of what stands before and beside a projection: the norm with the
+// residual's addition and a coded output (norm.hip), and the low-rank adapters
+// of many requests (adapters.hip).
+#pragma once
+
+#include "training.h"
+
+namespace wl {
+
+constexpr int kNormMaxK = 32768;
+
+// The weight of a norm: bf16 or float32 [K], added to `offset`.
+struct NormWeight {
+  const void *w;
+  bool f32;
+  float offset;
+};
+
+struct NormCall {
+  const uint16_t *x, *res;  // [T][K] bf16; res may be null
+  int32_t T, K;
+  NormWeight w;
+  float eps;
+  uint16_t *h, *y;          // [T][K] bf16, each may be null
+  float *rstd;              // [T] or null
+  bool coded;
+  CodedView code;           // written if coded
+};
+hipError_t launch_norm(const NormCall &c, hipStream_t stream);
+
+struct NormBackward {
+  const uint16_t *dy, *h;  // [T][K] bf16
+  const float *rstd;       // [T]
+  const uint16_t *dh;      // [T][K] bf16 or null
+  int32_t T, K;
+  NormWeight w;
+  uint16_t *dx;            // [T][K] bf16 or null
+  float *dw;               // [K] or null
+};
+size_t norm_backward_partial_bytes(int T, int K);
+hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStream_t stream);
+
+}  // namespace wl

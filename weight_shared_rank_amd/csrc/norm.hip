@@ -1,0 +1,341 @@
+// Root-mean-square norm with the residual's addition and a coded output, and
+// its backward pass.
+//
+// Forward, for each token row:
+//   h = bf16(x + res)            (h = x without a residual)
+//   a = 1 / sqrt(mean_k h_k^2 + eps)
+//   y = bf16(h a (offset + w))   code = the 8-bit coding of y (coded.h)
+// Backward, with g = dy (offset + w) and n = h a:
+//   dx = a (g - n mean_k(g n)) + dh      dw = sum_t dy n
+//
+// Both are bound by memory: a row is read once into registers, 16 bytes a lane
+// and load, and everything that follows comes from there.  One to sixteen
+// waves share a row (rows of up to 32768 elements); a coded block of 128 is 16
+// neighbouring lanes, so its maximum is four lane exchanges and the bf16 output
+// is coded without being read again.
+#include <type_traits>
+
+#include "beside.h"
+#include "coded.h"
+#include "common.h"
+
+namespace wl {
+
+namespace {
+
+constexpr int kRowsOneWave = 4;  // rows of a workgroup where a wave takes a row
+
+__device__ __forceinline__ float lo_f32(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// 8 elements of the weight from k on, plus the offset.
+template <bool F32>
+__device__ __forceinline__ void load_weight(const NormWeight &nw, int k, float (&w)[8]) {
+  if constexpr (F32) {
+    const float *p = static_cast<const float *>(nw.w) + k;
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = nw.offset + a[i];
+      w[4 + i] = nw.offset + b[i];
+    }
+  } else {
+    const u32x4 v = ld16(static_cast<const uint16_t *>(nw.w) + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[2 * i] = nw.offset + lo_f32(v[i]);
+      w[2 * i + 1] = nw.offset + hi_f32(v[i]);
+    }
+  }
+}
+
+// Sum over the lanes of a wave, then over the W waves of a row, in a fixed order.
+template <int W, typename F>
+__device__ __forceinline__ F row_sum(F v, F *lds, int wave) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) lds[wave] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v += lds[i];
+  }
+  return v;
+}
+
+// W waves to a row (1: kRowsOneWave rows to a workgroup), V vectors of 8 a lane.
+// The sum of squares and a are taken in 64 bits and a enters the product as a
+// pair of floats: y's only rounding of note is the one to bf16, so the codes
+// that depend on it hardly ever differ from those of exact arithmetic.  It costs
+// two 64-bit operations an element where memory takes the time of thirty.
+template <int W, int V, bool F32>
+__global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kernel(NormCall c) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = W == 1 ? static_cast<int64_t>(blockIdx.x) * kRowsOneWave + wave : blockIdx.x;
+  if (W == 1 && t >= c.T) return;  // (no barrier in that form)
+  const int at = (W == 1 ? lane : static_cast<int>(threadIdx.x)) * 8;
+  __shared__ double part[W];
+  const int64_t row = t * c.K;
+  u32x4 h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int k = at + i * W * 512;
+    h[i] = u32x4{0u, 0u, 0u, 0u};
+    if (k < c.K) h[i] = ld16(c.x + row + k);
+  }
+  if (c.res) {
+    u32x4 r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      r[i] = u32x4{0u, 0u, 0u, 0u};
+      if (k < c.K) r[i] = ld16(c.res + row + k);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[i][j] = pack_bf16(lo_f32(h[i][j]) + lo_f32(r[i][j]), hi_f32(h[i][j]) + hi_f32(r[i][j]));
+  }
+  if (c.h) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      if (k < c.K) *reinterpret_cast<u32x4 *>(c.h + row + k) = h[i];
+    }
+  }
+  double q = 0.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double a = lo_f32(h[i][j]), b = hi_f32(h[i][j]);
+      q = __builtin_fma(a, a, q);
+      q = __builtin_fma(b, b, q);
+    }
+  q = row_sum<W>(q, part, wave);
+  const double a = rsqrt(q / c.K + static_cast<double>(c.eps));
+  const float ah = static_cast<float>(a), al = static_cast<float>(a - static_cast<double>(ah));
+  if (c.rstd && at == 0) c.rstd[t] = ah;
+  if (!c.y && !c.coded) return;
+  const int Kq = c.code.nb * kCodeBlock;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int k = at + i * W * 512;
+    u32x4 y{0u, 0u, 0u, 0u};
+    if (k < c.K) {
+      float w[8], o[8];
+      load_weight<F32>(c.w, k, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = j & 1 ? hi_f32(h[i][j / 2]) : lo_f32(h[i][j / 2]);
+        const float p = v * ah, e = __builtin_fmaf(v, al, __builtin_fmaf(v, ah, -p));  // v a = p + e
+        // (an infinite weight times e = 0 would be NaN)
+        o[j] = __builtin_fmaf(p, w[j], e * (fabsf(w[j]) < __builtin_inff() ? w[j] : 0.f));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
+      if (c.y) *reinterpret_cast<u32x4 *>(c.y + row + k) = y;
+    }
+    if (c.coded) {
+      uint32_t m = amax_bits(y);
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 16)));
+      const int e = block_exponent(m), l = lane & 15;
+      if (k < Kq) {
+        *reinterpret_cast<u32x2 *>(const_cast<uint8_t *>(c.code.codes) + t * Kq + k) = code8(y, e);
+        uint8_t *s = const_cast<uint8_t *>(c.code.scales) + static_cast<int64_t>(k / kCodeBlock) * c.code.ldsc + t;
+        if (l == 0) *s = static_cast<uint8_t>(e + 127);
+        // behind the last token the run of a block is filled up with scale 1
+        else if (t == c.T - 1 && t + l < c.code.ldsc) s[l] = 127;
+      }
+    }
+  }
+}
+
+// Backward.  A team of W waves walks the rows `team`, `team` + teams, ...; its
+// sum of dy n stays in registers, the workgroup's sums (a row of K floats) go to
+// `part` (dw itself if there is one workgroup).
+template <int W, int V, bool F32>
+__global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_backward_kernel(NormBackward c, float *part) {
+  constexpr int R = W == 1 ? kRowsOneWave : 1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int at = (W == 1 ? lane : static_cast<int>(threadIdx.x)) * 8;
+  __shared__ float sum[2][W];
+  float w[V][8], dw[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int k = at + i * W * 512;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.f;
+    if (k < c.K) load_weight<F32>(c.w, k, w[i]);
+  }
+  const int64_t teams = static_cast<int64_t>(gridDim.x) * R;
+  int turn = 0;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * R + (W == 1 ? wave : 0); t < c.T; t += teams, turn ^= 1) {
+    const int64_t row = t * c.K;
+    u32x4 d[V], h[V], r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      d[i] = h[i] = r[i] = u32x4{0u, 0u, 0u, 0u};
+      if (k < c.K) {
+        d[i] = ld16(c.dy + row + k);
+        h[i] = ld16(c.h + row + k);
+        if (c.dh) r[i] = ld16(c.dh + row + k);
+      }
+    }
+    const float a = c.rstd[t];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = (j & 1 ? hi_f32(h[i][j / 2]) : lo_f32(h[i][j / 2])) * a;
+        const float g = j & 1 ? hi_f32(d[i][j / 2]) : lo_f32(d[i][j / 2]);
+        dot = __builtin_fmaf(g * w[i][j], n, dot);
+        dw[i][j] = __builtin_fmaf(g, n, dw[i][j]);
+      }
+    if (!c.dx) continue;
+    const float mean = row_sum<W>(dot, sum[turn], wave) / c.K;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      if (k >= c.K) continue;
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float n0 = lo_f32(h[i][j]) * a, n1 = hi_f32(h[i][j]) * a;
+        const float g0 = lo_f32(d[i][j]) * w[i][2 * j], g1 = hi_f32(d[i][j]) * w[i][2 * j + 1];
+        o[j] = pack_bf16(__builtin_fmaf(a, __builtin_fmaf(-n0, mean, g0), lo_f32(r[i][j])),
+                         __builtin_fmaf(a, __builtin_fmaf(-n1, mean, g1), hi_f32(r[i][j])));
+      }
+      *reinterpret_cast<u32x4 *>(c.dx + row + k) = o;
+    }
+  }
+  if (!c.dw) return;
+  float *out = (gridDim.x == 1 ? c.dw : part) + static_cast<int64_t>(blockIdx.x) * c.K;
+  if constexpr (R == 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      if (k >= c.K) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<f32x4 *>(out + k + 4 * j) = f32x4{dw[i][4 * j], dw[i][4 * j + 1], dw[i][4 * j + 2], dw[i][4 * j + 3]};
+    }
+  } else {
+    __shared__ f32x4 rows[R - 1][64 * 2];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      __syncthreads();
+      if (wave > 0)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          rows[wave - 1][lane + 64 * j] = f32x4{dw[i][4 * j], dw[i][4 * j + 1], dw[i][4 * j + 2], dw[i][4 * j + 3]};
+      __syncthreads();
+      if (wave == 0 && k < c.K)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f32x4 s = f32x4{dw[i][4 * j], dw[i][4 * j + 1], dw[i][4 * j + 2], dw[i][4 * j + 3]};
+#pragma unroll
+          for (int q = 0; q < R - 1; ++q) s += rows[q][lane + 64 * j];
+          *reinterpret_cast<f32x4 *>(out + k + 4 * j) = s;
+        }
+    }
+  }
+}
+
+// dw [K] = sum over G rows of part [G][K]: 16 columns a workgroup, its 16
+// groups of 16 lanes take rows in turn and meet in LDS, in a fixed order.
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float *part, int G, int K, float *dw) {
+  const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int k = blockIdx.x * 16 + l;
+  __shared__ float s[16][17];
+  float v = 0.f;
+  if (k < K)
+    for (int i = g; i < G; i += 16) v += part[static_cast<int64_t>(i) * K + k];
+  s[g][l] = v;
+  __syncthreads();
+  if (g == 0 && k < K) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += s[i][l];
+    dw[k] = v;
+  }
+}
+
+__global__ __launch_bounds__(256) void fill_zero_f32(float *p, int n) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.f;
+}
+
+// Waves and vectors of a row: a wave up to 2048 elements (no barrier), four up
+// to 8192, sixteen above.
+template <typename F>
+hipError_t with_row_shape(int K, F &&f) {
+  const int v1 = (K + 511) / 512, v4 = (K + 2047) / 2048, v16 = (K + 8191) / 8192;
+  if (v1 == 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  if (v1 == 2) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
+  if (v1 == 3) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 3>{});
+  if (v1 == 4) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+  if (v4 == 2) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  if (v4 == 3) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 3>{});
+  if (v4 == 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+  if (v16 == 2) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+  if (v16 == 3) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 3>{});
+  return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+}
+
+int rows_of_workgroup(int K) { return K <= 2048 ? kRowsOneWave : 1; }
+
+// Workgroups of the backward pass: enough to fill the CUs, few enough that the
+// partial sums stay small beside the rows.
+int backward_groups(int T, int K) {
+  const int64_t groups = (static_cast<int64_t>(T) + rows_of_workgroup(K) - 1) / rows_of_workgroup(K);
+  return static_cast<int>(groups < 1024 ? groups : 1024);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormCall &c, hipStream_t stream) {
+  return with_row_shape(c.K, [&](auto w, auto v) {
+    constexpr int W = decltype(w)::value, V = decltype(v)::value;
+    const int R = rows_of_workgroup(c.K);
+    const dim3 grid((c.T + R - 1) / R), block(R * W * 64);
+    if (c.w.f32)
+      norm_kernel<W, V, true><<<grid, block, 0, stream>>>(c);
+    else
+      norm_kernel<W, V, false><<<grid, block, 0, stream>>>(c);
+    return hipGetLastError();
+  });
+}
+
+size_t norm_backward_partial_bytes(int T, int K) {
+  const int G = backward_groups(T, K);
+  return G > 1 ? static_cast<size_t>(G) * K * sizeof(float) : 0;
+}
+
+hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStream_t stream) {
+  if (c.T == 0) {
+    if (!c.dw) return hipSuccess;
+    fill_zero_f32<<<(c.K + 255) / 256, 256, 0, stream>>>(c.dw, c.K);
+    return hipGetLastError();
+  }
+  const int G = backward_groups(c.T, c.K);
+  const hipError_t e = with_row_shape(c.K, [&](auto w, auto v) {
+    constexpr int W = decltype(w)::value, V = decltype(v)::value;
+    const dim3 block(rows_of_workgroup(c.K) * W * 64);
+    if (c.w.f32)
+      norm_backward_kernel<W, V, true><<<G, block, 0, stream>>>(c, partials);
+    else
+      norm_backward_kernel<W, V, false><<<G, block, 0, stream>>>(c, partials);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || !c.dw || G == 1) return e;
+  norm_dw_kernel<<<(c.K + 15) / 16, 256, 0, stream>>>(partials, G, c.K, c.dw);
+  return hipGetLastError();
+}
+
+}  // namespace wl

@@ -27,15 +27,19 @@
 
 #include <algorithm>
 #include <array>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <memory>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
+#include "beside.h"
 #include "internal.h"
 #include "training.h"
 #include "weightless.h"
@@ -560,6 +564,55 @@ bool overlap(const void *a, size_t an, const void *b, size_t bn) {
   return a && b && an && bn && x < y + bn && y < x + an;
 }
 
+// The memory of a call: ranges that must not meet.
+struct Ranges {
+  struct Range {
+    const void *p;
+    size_t n;
+    const char *what;
+    bool written;
+  } r[16];
+  int n = 0;
+  void add(const void *p, size_t bytes, const char *what, bool written) {
+    if (p && bytes) r[n++] = Range{p, bytes, what, written};
+  }
+  // No written range may meet another, but for an output that is exactly one of
+  // its own inputs (the pairs of names in `in_place`).
+  wl_status check(std::initializer_list<std::pair<const char *, const char *>> in_place) const {
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j) {
+        if (!r[i].written && !r[j].written) continue;
+        if (!overlap(r[i].p, r[i].n, r[j].p, r[j].n)) continue;
+        bool same = false;
+        for (const auto &q : in_place)
+          same = same || (r[i].p == r[j].p && r[i].n == r[j].n &&
+                          ((!std::strcmp(q.first, r[i].what) && !std::strcmp(q.second, r[j].what)) ||
+                           (!std::strcmp(q.first, r[j].what) && !std::strcmp(q.second, r[i].what))));
+        if (!same) return fail(WL_EINVAL, "%s must not overlap %s", r[i].what, r[j].what);
+      }
+    return WL_OK;
+  }
+};
+
+// ---- norm ----
+
+wl_status check_norm(int32_t T, int32_t K, const void *d_w, int32_t w_dtype, float offset, wl::NormWeight &w) {
+  if (K < 1 || K > wl::kNormMaxK) return fail(WL_ESHAPE, "K = %d outside [8, %d]", K, wl::kNormMaxK);
+  const wl_status st = check_act_shape(T, K);
+  if (st != WL_OK) return st;
+  if (w_dtype != WL_DTYPE_BF16 && w_dtype != WL_DTYPE_F32) return fail(WL_EDTYPE, "weight dtype %d", w_dtype);
+  if (!std::isfinite(offset)) return fail(WL_EINVAL, "offset is not finite");
+  w = wl::NormWeight{d_w, w_dtype == WL_DTYPE_F32, offset};
+  return WL_OK;
+}
+
+size_t norm_weight_bytes(const wl::NormWeight &w, int32_t K) { return static_cast<size_t>(K) * (w.f32 ? 4 : 2); }
+
+// An optional argument: NULL, or aligned.
+wl_status check_optional(const void *p, size_t align, const char *what) {
+  return p ? check_aligned(p, align, what) : WL_OK;
+}
+
 // ---- backward ----
 
 constexpr int32_t kMaxBackwardColumns = (1 << 21) - 256;
@@ -1008,6 +1061,94 @@ wl_status weightless_coded_linear(const void *d_wcode, size_t wcode_bytes, int32
                                                code_view(d_xcode, cx), T, static_cast<uint16_t *>(d_y),
                                                static_cast<float *>(d_ws), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? WL_OK : hip_fail(e, "kernel launch");
+}
+
+wl_status weightless_norm(const void *d_x, const void *d_res, int32_t T, int32_t K, const void *d_w, int32_t w_dtype,
+                          float offset, float eps, void *d_h, void *d_y, void *d_code, size_t code_bytes,
+                          float *d_rstd, void *stream) {
+  wl::NormCall c{};
+  wl_status st = check_norm(T, K, d_w, w_dtype, offset, c.w);
+  if (st != WL_OK) return st;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(WL_EINVAL, "eps must be positive and finite");
+  if (T == 0) return WL_OK;
+  const size_t rows = static_cast<size_t>(T) * K * 2;
+  const CodeShape cs = code_shape(T, K, false);
+  if ((st = check_aligned(d_x, 16, "x")) != WL_OK || (st = check_aligned(d_w, 16, "w")) != WL_OK ||
+      (st = check_optional(d_res, 16, "res")) != WL_OK || (st = check_optional(d_h, 16, "h")) != WL_OK ||
+      (st = check_optional(d_y, 16, "y")) != WL_OK || (st = check_optional(d_rstd, 4, "rstd")) != WL_OK)
+    return st;
+  if (d_code && (st = check_code_buffer(d_code, code_bytes, cs.bytes, "code buffer")) != WL_OK) return st;
+  if (!d_h && !d_y && !d_code && !d_rstd) return fail(WL_EINVAL, "no output is asked for");
+  Ranges r;
+  r.add(d_x, rows, "x", false);
+  r.add(d_res, rows, "res", false);
+  r.add(d_w, norm_weight_bytes(c.w, K), "w", false);
+  r.add(d_h, rows, "h", true);
+  r.add(d_y, rows, "y", true);
+  r.add(d_code, cs.bytes, "the code buffer", true);
+  r.add(d_rstd, static_cast<size_t>(T) * 4, "rstd", true);
+  if ((st = r.check({{"h", "x"}, {"h", "res"}})) != WL_OK) return st;
+  c.x = static_cast<const uint16_t *>(d_x);
+  c.res = static_cast<const uint16_t *>(d_res);
+  c.T = T;
+  c.K = K;
+  c.eps = eps;
+  c.h = static_cast<uint16_t *>(d_h);
+  c.y = static_cast<uint16_t *>(d_y);
+  c.rstd = d_rstd;
+  c.coded = d_code != nullptr;
+  c.code = code_view(d_code, cs);
+  const hipError_t e = wl::launch_norm(c, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "norm launch");
+}
+
+size_t weightless_norm_backward_workspace_bytes(int32_t T, int32_t K) {
+  wl::NormWeight w;
+  if (check_norm(T, K, nullptr, WL_DTYPE_F32, 0.f, w) != WL_OK) return 0;
+  g_err.clear();
+  return std::max<size_t>(256, align256(wl::norm_backward_partial_bytes(T, K)));
+}
+
+wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const float *d_rstd, const void *d_dh, int32_t T,
+                                   int32_t K, const void *d_w, int32_t w_dtype, float offset, void *d_dx, float *d_dw,
+                                   void *d_ws, size_t ws_bytes, void *stream) {
+  wl::NormBackward c{};
+  wl_status st = check_norm(T, K, d_w, w_dtype, offset, c.w);
+  if (st != WL_OK) return st;
+  if (!d_dx && !d_dw) return fail(WL_EINVAL, "no output is asked for");
+  if ((st = check_optional(d_dw, 16, "dw")) != WL_OK || (st = check_optional(d_dx, 16, "dx")) != WL_OK) return st;
+  const size_t rows = static_cast<size_t>(T) * K * 2;
+  if (T > 0) {
+    if ((st = check_aligned(d_dy, 16, "dy")) != WL_OK || (st = check_aligned(d_h, 16, "h")) != WL_OK ||
+        (st = check_aligned(d_rstd, 4, "rstd")) != WL_OK || (st = check_aligned(d_w, 16, "w")) != WL_OK ||
+        (st = check_optional(d_dh, 16, "dh")) != WL_OK)
+      return st;
+    const size_t need = d_dw ? align256(wl::norm_backward_partial_bytes(T, K)) : 0;
+    if (need) {
+      if ((st = check_aligned(d_ws, 256, "workspace")) != WL_OK) return st;
+      if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
+    }
+    Ranges r;
+    r.add(d_dy, rows, "dy", false);
+    r.add(d_h, rows, "h", false);
+    r.add(d_rstd, static_cast<size_t>(T) * 4, "rstd", false);
+    r.add(d_dh, rows, "dh", false);
+    r.add(d_w, norm_weight_bytes(c.w, K), "w", false);
+    r.add(d_dx, rows, "dx", true);
+    r.add(d_dw, static_cast<size_t>(K) * 4, "dw", true);
+    r.add(d_ws, need, "the workspace", true);
+    if ((st = r.check({{"dx", "dy"}, {"dx", "dh"}})) != WL_OK) return st;
+  }
+  c.dy = static_cast<const uint16_t *>(d_dy);
+  c.h = static_cast<const uint16_t *>(d_h);
+  c.rstd = d_rstd;
+  c.dh = static_cast<const uint16_t *>(d_dh);
+  c.T = T;
+  c.K = K;
+  c.dx = static_cast<uint16_t *>(d_dx);
+  c.dw = d_dw;
+  const hipError_t e = wl::launch_norm_backward(c, static_cast<float *>(d_ws), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "norm backward launch");
 }
 
 size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T) {
