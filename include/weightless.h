@@ -470,6 +470,54 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
                                    int32_t K, const void *d_w, int32_t w_dtype, float offset, void *d_dx, float *d_dw,
                                    void *d_ws, size_t ws_bytes, void *stream);
 
+/* ---- Low-rank adapters of many requests beside one projection ----
+ * A pool of adapters for one projection, or for one stacked call (children as
+ * there: their outputs side by side).  Token t runs with slot a = d_index[t]:
+ *   y[t] = bf16(base[t] + c_a U_a (V_a^T x[t]))     per child
+ * and y[t] = base[t], bit for bit, without an adapter: where d_index[t] lies
+ * outside [0, num_slots) or the slot's rank is not positive.  base is what the
+ * shared projection gave (weightless_linear, weightless_stacked_linear,
+ * weightless_coded_linear).  Slots change between calls as their owner
+ * likes (the memory is the caller's; a captured call reads what it holds when
+ * it is replayed, as it does for d_index, d_scale and d_rank).
+ *  num_slots in [1, 4096]; rank (the room of every slot) a multiple of 16 in
+ *    [16, 256]; in_dim K a multiple of 8; num_children 1 to 3, out_dim[c] rows of
+ *    child c; K and rows in [1, 2^20] (WL_ESHAPE otherwise).
+ *  d_vt: bf16 [num_slots][num_children][rank][K], V^T: an adapter's down
+ *    projection as its rows.  d_u: bf16 [num_slots][sum of out_dim][rank], the
+ *    children's rows one after the other.  Both 16-byte aligned.
+ *  d_scale: float32 [num_slots], c.
+ *  d_rank: int32 [num_slots], or NULL: every slot uses the whole rank.  Rows of
+ *    V^T and columns of U from a slot's rank on are not used, whatever they hold.
+ *    A value past `rank` counts as rank. */
+typedef struct {
+  int32_t num_slots, rank, in_dim, num_children;
+  int32_t out_dim[3];
+  const void *d_vt, *d_u;
+  const float *d_scale;
+  const int32_t *d_rank;
+} wl_adapters;
+
+/* Workspace bytes of weightless_adapters_add with T tokens; 0 with
+ * wl_last_error() set on error.  Fewer tokens can need more. */
+size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t T);
+
+/*  d_x bf16 [T, K] (16-byte aligned), d_index int32 [T], d_base and d_y bf16
+ *    [T, sum of out_dim] (2-byte aligned; whole 16-byte accesses where they are
+ *    16-byte aligned and rows and children a multiple of 8 wide).  d_y may be
+ *    exactly d_base (in place: rows without an adapter are then not touched);
+ *    otherwise no output may overlap an input (WL_EINVAL).  T = 0: a no-op.
+ *  d_ws: weightless_adapters_workspace_bytes(adapters, T) bytes, 256-byte
+ *    aligned, no initialization, nothing kept; concurrent calls, and graphs that
+ *    may run at the same time, need distinct workspaces.
+ *  Products of bf16 operands with float32 sums; c (V^T x) enters the second one
+ *  as a pair of bf16 (16 significant bits); y is rounded once.  A token's result
+ *  is the same bits whichever tokens stand beside it in a call of as many tokens.
+ *  What is not finite in a slot or a token's x reaches that slot's or that token's
+ *  rows alone.  Two launches up to 256 tokens, three above. */
+wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, const int32_t *d_index, int32_t T,
+                                  const void *d_base, void *d_y, void *d_ws, size_t ws_bytes, void *stream);
+
 /* Output width N of a single-family call, or of a stacked call (stack >= 0
  * with family < 0); 0 on error.  Host-only. */
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack);

@@ -40,7 +40,8 @@ EXPORTS = ("theta_bundle_arena_bytes", "theta_bundle_load", "theta_bundle_free",
            "weightless_act_expand", "weightless_weight_encode",
            "weightless_coded_linear_workspace_bytes", "weightless_coded_linear",
            "weightless_backward_workspace_bytes", "weightless_linear_backward", "weightless_stacked_backward",
-           "weightless_norm", "weightless_norm_backward_workspace_bytes", "weightless_norm_backward")
+           "weightless_norm", "weightless_norm_backward_workspace_bytes", "weightless_norm_backward",
+           "weightless_adapters_workspace_bytes", "weightless_adapters_add")
 
 
 class WlBundleSpec(ctypes.Structure):
@@ -60,6 +61,13 @@ class WlSrc(ctypes.Structure):
 class WlGrads(ctypes.Structure):
     _fields_ = [("dx", ctypes.c_void_p), ("ds", ctypes.c_void_p), ("du", ctypes.c_void_p * 3),
                 ("dv", ctypes.c_void_p * 3), ("dw0", ctypes.c_void_p), ("accumulate_dw0", ctypes.c_int32)]
+
+
+class WlAdapters(ctypes.Structure):
+    _fields_ = [("num_slots", ctypes.c_int32), ("rank", ctypes.c_int32), ("in_dim", ctypes.c_int32),
+                ("num_children", ctypes.c_int32), ("out_dim", ctypes.c_int32 * 3),
+                ("d_vt", ctypes.c_void_p), ("d_u", ctypes.c_void_p), ("d_scale", ctypes.c_void_p),
+                ("d_rank", ctypes.c_void_p)]
 
 
 class Grads(NamedTuple):
@@ -125,6 +133,8 @@ def lib():
         "weightless_stacked_backward": (i32, [vp, i32, i32, vp, sz, vp, i32, ctypes.POINTER(WlGrads), vp, sz, vp]),
         "weightless_norm": (i32, [vp, vp, i32, i32, vp, i32, f32, f32, vp, vp, vp, sz, vp, vp]),
         "weightless_norm_backward_workspace_bytes": (sz, [i32, i32]),
+        "weightless_adapters_workspace_bytes": (sz, [ctypes.POINTER(WlAdapters), i32]),
+        "weightless_adapters_add": (i32, [ctypes.POINTER(WlAdapters), vp, vp, i32, vp, vp, vp, sz, vp]),
         "weightless_norm_backward": (i32, [vp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -731,3 +741,102 @@ def norm_backward(dy, h, rstd, weight, offset: float = 0.0, dh=None, want=("dx",
                                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
                                               _raw_stream(dev)))
     return NormGrads(dx, dw)
+
+
+# ---- low-rank adapters of many requests -------------------------------------
+
+class AdapterPool:
+    """Slots of low-rank adapters beside one projection or one stacked call
+    (wl_adapters): y[t] = base[t] + scale U (V^T x[t]) with the slot index[t].
+
+    vt: bf16 [slots, children * rank, K], the children's V^T rows one after the
+    other; u: bf16 [slots, sum of out_dims, rank]; scale: float32 [slots]; rank:
+    int32 [slots], the ranks in use, or None for all of them (what vt and u hold
+    from a slot's rank on is not used).  The pool keeps these tensors and reads
+    what they hold when a call runs."""
+
+    def __init__(self, vt, u, scale, out_dims: Sequence[int], rank=None):
+        import torch
+        _check_tensor(vt, "vt", (None, None, None), torch.bfloat16)
+        dev, n, kids = vt.device, vt.shape[0], len(out_dims)
+        if not 1 <= kids <= 3 or vt.shape[1] % kids:
+            raise WlError(-2, f"{vt.shape[1]} rows of vt for {kids} children")
+        room = vt.shape[1] // kids
+        _check_tensor(u, "u", (n, sum(out_dims), room), torch.bfloat16, dev)
+        _check_tensor(scale, "scale", (n,), torch.float32, dev)
+        if rank is not None:
+            _check_tensor(rank, "rank", (n,), torch.int32, dev)
+        self.vt, self.u, self.scale, self.rank, self.out_dims = vt, u, scale, rank, tuple(out_dims)
+        self.device, self.slots, self.room, self.K, self.width = dev, n, room, vt.shape[2], sum(out_dims)
+        self.spec = WlAdapters(n, room, self.K, kids, (ctypes.c_int32 * 3)(*out_dims), vt.data_ptr(), u.data_ptr(),
+                               scale.data_ptr(), None if rank is None else rank.data_ptr())
+        self._ref = ctypes.byref(self.spec)
+        self._need = {}          # T -> workspace bytes
+        self.workspace_bytes(1)  # refuses dimensions the library does not take
+
+    @classmethod
+    def empty(cls, slots: int, rank: int, K: int, out_dims: Sequence[int], device="cuda") -> "AdapterPool":
+        """A pool whose slots are all free (rank 0): tokens sent to them run
+        without an adapter until load() fills them."""
+        import torch
+        dev = torch.device(device)
+        return cls(torch.zeros((slots, len(out_dims) * rank, K), dtype=torch.bfloat16, device=dev),
+                   torch.zeros((slots, sum(out_dims), rank), dtype=torch.bfloat16, device=dev),
+                   torch.zeros((slots,), dtype=torch.float32, device=dev), out_dims,
+                   torch.zeros((slots,), dtype=torch.int32, device=dev))
+
+    def load(self, slot: int, down, up, scale: float = 1.0):
+        """Fill a slot on the current stream.  down: per child [r, K] (V^T); up:
+        per child [N, r] (U); one rank r <= the pool's for all children."""
+        kids = len(self.out_dims)
+        r = down[0].shape[0] if len(down) else 0
+        if not 0 <= slot < self.slots or len(down) != kids or len(up) != kids or not 1 <= r <= self.room \
+                or any(tuple(a.shape) != (r, self.K) or tuple(b.shape) != (n, r) for a, b, n in zip(down, up, self.out_dims)):
+            raise WlError(-1, f"slot {slot} takes {kids} pairs of [r, {self.K}] and [N, r], N = {self.out_dims}, r <= {self.room}")
+        if self.rank is None and r != self.room:
+            raise WlError(-1, f"this pool has no ranks: every slot takes rank {self.room}")
+        at = 0
+        for c, (a, b, n) in enumerate(zip(down, up, self.out_dims)):
+            self.vt[slot, c * self.room:c * self.room + r].copy_(a)
+            self.u[slot, at:at + n, :r].copy_(b)
+            at += n
+        self.scale[slot] = scale
+        if self.rank is not None:
+            self.rank[slot] = r
+
+    def clear(self, slot: int):
+        """Free a slot: tokens sent to it run without an adapter."""
+        if self.rank is None or not 0 <= slot < self.slots:
+            raise WlError(-1, f"slot {slot} of a pool with{'' if self.rank is not None else 'out'} ranks cannot be cleared")
+        self.rank[slot] = 0
+
+    def workspace_bytes(self, T: int) -> int:
+        """Workspace bytes of add() with T tokens."""
+        need = self._need.get(T)
+        if need is None:
+            need = lib().weightless_adapters_workspace_bytes(self._ref, T)
+            if need == 0:
+                raise WlError(-2, last_error())
+            self._need[T] = need
+        return need
+
+    def add(self, x, index, base, y=None, ws=None, stream=None):
+        """y[t] = base[t] + scale U (V^T x[t]), bf16 [T, N] (weightless_adapters_add).
+
+        x: bf16 [T, K]; index: int32 [T], each token's slot (outside the pool:
+        none); base: bf16 [T, N], the shared projection's output; y may be base."""
+        import torch
+        dev = self.device
+        _check_tensor(x, "x", (None, self.K), torch.bfloat16, dev)
+        T = x.shape[0]
+        with _scope(dev, stream):
+            _check_tensor(index, "index", (T,), torch.int32, dev)
+            _check_tensor(base, "base", (T, self.width), torch.bfloat16, dev)
+            y = _output(y, "y", (T, self.width), torch.bfloat16, dev)
+            if ws is None:
+                ws = torch.empty(self.workspace_bytes(T), dtype=torch.uint8, device=dev)
+            else:
+                _check_tensor(ws, "ws", (None,), torch.uint8, dev)
+            _check(lib().weightless_adapters_add(self._ref, x.data_ptr(), index.data_ptr(), T, base.data_ptr(),
+                                                 y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev)))
+        return y

@@ -40,4 +40,20 @@ struct NormBackward {
 size_t norm_backward_partial_bytes(int T, int K);
 hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStream_t stream);
 
+// A pool of low-rank adapters beside one projection, or one stacked call.
+struct AdapterPool {
+  const uint16_t *vt;   // [n][nchild * r][K]
+  const uint16_t *u;    // [n][Ntot][r]
+  const float *scale;   // [n]
+  const int32_t *rank;  // [n] or null: all r
+  int32_t n, r, K, nchild;
+  int32_t N[kMaxChildren];
+  int32_t Ntot;
+};
+size_t adapters_workspace_bytes(const AdapterPool &p, int T);
+// y = base + scale U (V^T x) row by row, with the adapter index[t] (none if
+// outside [0, n)); y may be base.
+hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_t *index, int T, const uint16_t *base,
+                           uint16_t *y, void *ws, hipStream_t stream);
+
 }  // namespace wl

@@ -613,6 +613,52 @@ wl_status check_optional(const void *p, size_t align, const char *what) {
   return p ? check_aligned(p, align, what) : WL_OK;
 }
 
+// ---- adapters ----
+
+constexpr int32_t kMaxAdapterSlots = 4096, kMaxAdapterRank = 256;
+
+// Dimensions of a pool (T: the call's tokens); its pointers are checked apart.
+wl_status check_adapters(const wl_adapters *ad, int32_t T, wl::AdapterPool &p) {
+  if (!ad) return fail(WL_EINVAL, "adapters is NULL");
+  if (ad->num_slots < 1 || ad->num_slots > kMaxAdapterSlots)
+    return fail(WL_ESHAPE, "%d slots outside [1, %d]", ad->num_slots, kMaxAdapterSlots);
+  if (ad->rank < 16 || ad->rank > kMaxAdapterRank || ad->rank % 16)
+    return fail(WL_ESHAPE, "rank %d is not a multiple of 16 in [16, %d]", ad->rank, kMaxAdapterRank);
+  if (ad->num_children < 1 || ad->num_children > wl::kMaxChildren)
+    return fail(WL_ESHAPE, "%d children outside [1, %d]", ad->num_children, wl::kMaxChildren);
+  const wl_status st = check_act_shape(T, ad->in_dim);
+  if (st != WL_OK) return st;
+  p = wl::AdapterPool{};
+  p.n = ad->num_slots;
+  p.r = ad->rank;
+  p.K = ad->in_dim;
+  p.nchild = ad->num_children;
+  for (int c = 0; c < p.nchild; ++c) {
+    if (ad->out_dim[c] < 1 || ad->out_dim[c] > kMaxDim) return fail(WL_ESHAPE, "out_dim[%d] = %d out of range", c, ad->out_dim[c]);
+    p.N[c] = ad->out_dim[c];
+    p.Ntot += ad->out_dim[c];
+  }
+  p.vt = static_cast<const uint16_t *>(ad->d_vt);
+  p.u = static_cast<const uint16_t *>(ad->d_u);
+  p.scale = ad->d_scale;
+  p.rank = ad->d_rank;
+  return WL_OK;
+}
+
+// The pool's pointers, and its memory as inputs of a call.
+wl_status check_adapter_memory(const wl::AdapterPool &p, Ranges &r) {
+  wl_status st;
+  if ((st = check_aligned(p.vt, 16, "vt")) != WL_OK || (st = check_aligned(p.u, 16, "u")) != WL_OK ||
+      (st = check_aligned(p.scale, 4, "scale")) != WL_OK || (st = check_optional(p.rank, 4, "rank")) != WL_OK)
+    return st;
+  const size_t n = static_cast<size_t>(p.n), row = static_cast<size_t>(p.r) * 2;
+  r.add(p.vt, n * p.nchild * row * p.K, "vt", false);
+  r.add(p.u, n * p.Ntot * row, "u", false);
+  r.add(p.scale, n * 4, "scale", false);
+  r.add(p.rank, n * 4, "rank", false);
+  return WL_OK;
+}
+
 // ---- backward ----
 
 constexpr int32_t kMaxBackwardColumns = (1 << 21) - 256;
@@ -1149,6 +1195,38 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
   c.dw = d_dw;
   const hipError_t e = wl::launch_norm_backward(c, static_cast<float *>(d_ws), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? WL_OK : hip_fail(e, "norm backward launch");
+}
+
+size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t T) {
+  wl::AdapterPool p;
+  if (check_adapters(adapters, T, p) != WL_OK) return 0;
+  g_err.clear();
+  return wl::adapters_workspace_bytes(p, T);
+}
+
+wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, const int32_t *d_index, int32_t T,
+                                  const void *d_base, void *d_y, void *d_ws, size_t ws_bytes, void *stream) {
+  wl::AdapterPool p;
+  wl_status st = check_adapters(adapters, T, p);
+  if (st != WL_OK || T == 0) return st;
+  Ranges r;
+  if ((st = check_adapter_memory(p, r)) != WL_OK || (st = check_aligned(d_x, 16, "x")) != WL_OK ||
+      (st = check_aligned(d_index, 4, "index")) != WL_OK || (st = check_aligned(d_base, 2, "base")) != WL_OK ||
+      (st = check_aligned(d_y, 2, "y")) != WL_OK || (st = check_aligned(d_ws, 256, "workspace")) != WL_OK)
+    return st;
+  const size_t need = wl::adapters_workspace_bytes(p, T);
+  if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
+  const size_t yb = static_cast<size_t>(T) * p.Ntot * 2;
+  r.add(d_x, static_cast<size_t>(T) * p.K * 2, "x", false);
+  r.add(d_index, static_cast<size_t>(T) * 4, "index", false);
+  r.add(d_base, yb, "base", false);
+  r.add(d_y, yb, "y", true);
+  r.add(d_ws, need, "the workspace", true);
+  if ((st = r.check({{"y", "base"}})) != WL_OK) return st;
+  const hipError_t e = wl::launch_adapters(p, static_cast<const uint16_t *>(d_x), d_index, T,
+                                           static_cast<const uint16_t *>(d_base), static_cast<uint16_t *>(d_y), d_ws,
+                                           static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "adapters launch");
 }
 
 size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T) {
