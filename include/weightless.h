@@ -518,6 +518,42 @@ size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t 
 wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, const int32_t *d_index, int32_t T,
                                   const void *d_base, void *d_y, void *d_ws, size_t ws_bytes, void *stream);
 
+/* Gradients of weightless_adapters_add from the 8-bit checkpoint of x, beside the
+ * backward pass of the shared projection.  With X the values the checkpoint
+ * stands for, dy the gradient of y, and per token of slot a
+ * z = c_a V_a^T X[t] and g = c_a U_a^T dy[t] (per child):
+ *   dx[t] = bf16(base[t] + sum over the children V_a g)
+ *   dU_a = sum of dy[t] z^T,  dV_a^T = sum of g X[t]^T   over the slot's tokens
+ * Tokens without an adapter leave dx[t] = base[t], bit for bit, and enter nothing
+ * else; a slot without tokens has zero gradients, and so have the rows and
+ * columns from a slot's rank on.  Sums in float32, z and g as pairs of bf16 (16
+ * significant bits) where they enter the second products; every output is rounded
+ * once.  The sums over tokens run in the order of the tokens: the same bits from
+ * run to run, whichever gradients are asked for.  What is not finite in a token
+ * reaches its own dx and its slot's dU and dV alone. */
+typedef struct {
+  const void *base; /* bf16 [T, K]: dx of the shared projection's backward call (needed with dx) */
+  void *dx;         /* bf16 [T, K]; may be exactly base (in place) */
+  void *du;         /* bf16 [num_slots][sum of out_dim][rank] */
+  void *dv;         /* bf16 [num_slots][num_children][rank][K], V^T's gradient */
+} wl_adapter_grads;
+
+/* Workspace bytes with T tokens; 0 with wl_last_error() set on error. */
+size_t weightless_adapters_backward_workspace_bytes(const wl_adapters *adapters, int32_t T);
+
+/*  d_xcode: coded activations [T, K] (weightless_act_encode, weightless_norm;
+ *    xcode_bytes >= weightless_act_code_bytes); d_dy bf16 [T, sum of out_dim]
+ *    (2-byte aligned); d_index as in the forward call.
+ *  grads: the outputs wanted, NULL members are not computed (not all NULL); 16-byte
+ *    aligned; no output may overlap another, an input or the workspace but dx its
+ *    base (WL_EINVAL).  T = 0: du and dv are zeroed.
+ *  d_ws: weightless_adapters_backward_workspace_bytes(adapters, T) bytes, 256-byte
+ *    aligned, no initialization, nothing kept; concurrent calls need distinct
+ *    workspaces.  Four launches. */
+wl_status weightless_adapters_backward(const wl_adapters *adapters, const void *d_xcode, size_t xcode_bytes,
+                                       const void *d_dy, const int32_t *d_index, int32_t T,
+                                       const wl_adapter_grads *grads, void *d_ws, size_t ws_bytes, void *stream);
+
 /* Output width N of a single-family call, or of a stacked call (stack >= 0
  * with family < 0); 0 on error.  Host-only. */
 int32_t weightless_out_dim(const wl_bundle *bundle, int32_t layer, int32_t family, int32_t stack);

@@ -48,6 +48,7 @@ def test_shapes_refused(L):
 def test_no_tokens(L):
     assert norm(L, T=0, x=None, w=None, y=None) == 0
     assert back(L, T=0, dw=None, dy=None, h=None, rstd=None, w=None) == 0
+    assert back(L, T=0, dx=None, dw=None) == 0
 
 
 def test_norm_arguments_refused(L):

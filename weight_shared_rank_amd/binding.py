@@ -41,7 +41,8 @@ EXPORTS = ("theta_bundle_arena_bytes", "theta_bundle_load", "theta_bundle_free",
            "weightless_coded_linear_workspace_bytes", "weightless_coded_linear",
            "weightless_backward_workspace_bytes", "weightless_linear_backward", "weightless_stacked_backward",
            "weightless_norm", "weightless_norm_backward_workspace_bytes", "weightless_norm_backward",
-           "weightless_adapters_workspace_bytes", "weightless_adapters_add")
+           "weightless_adapters_workspace_bytes", "weightless_adapters_add",
+           "weightless_adapters_backward_workspace_bytes", "weightless_adapters_backward")
 
 
 class WlBundleSpec(ctypes.Structure):
@@ -68,6 +69,10 @@ class WlAdapters(ctypes.Structure):
                 ("num_children", ctypes.c_int32), ("out_dim", ctypes.c_int32 * 3),
                 ("d_vt", ctypes.c_void_p), ("d_u", ctypes.c_void_p), ("d_scale", ctypes.c_void_p),
                 ("d_rank", ctypes.c_void_p)]
+
+
+class WlAdapterGrads(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("du", ctypes.c_void_p), ("dv", ctypes.c_void_p)]
 
 
 class Grads(NamedTuple):
@@ -135,6 +140,9 @@ def lib():
         "weightless_norm_backward_workspace_bytes": (sz, [i32, i32]),
         "weightless_adapters_workspace_bytes": (sz, [ctypes.POINTER(WlAdapters), i32]),
         "weightless_adapters_add": (i32, [ctypes.POINTER(WlAdapters), vp, vp, i32, vp, vp, vp, sz, vp]),
+        "weightless_adapters_backward_workspace_bytes": (sz, [ctypes.POINTER(WlAdapters), i32]),
+        "weightless_adapters_backward": (i32, [ctypes.POINTER(WlAdapters), vp, sz, vp, vp, i32,
+                                               ctypes.POINTER(WlAdapterGrads), vp, sz, vp]),
         "weightless_norm_backward": (i32, [vp, vp, vp, vp, i32, i32, vp, i32, f32, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -745,6 +753,13 @@ def norm_backward(dy, h, rstd, weight, offset: float = 0.0, dh=None, want=("dx",
 
 # ---- low-rank adapters of many requests -------------------------------------
 
+class AdapterGrads(NamedTuple):
+    """Gradients of AdapterPool.add (None: not asked for)."""
+    dx: object = None
+    du: object = None
+    dv: object = None
+
+
 class AdapterPool:
     """Slots of low-rank adapters beside one projection or one stacked call
     (wl_adapters): y[t] = base[t] + scale U (V^T x[t]) with the slot index[t].
@@ -772,6 +787,7 @@ class AdapterPool:
                                scale.data_ptr(), None if rank is None else rank.data_ptr())
         self._ref = ctypes.byref(self.spec)
         self._need = {}          # T -> workspace bytes
+        self._backward_need = {}
         self.workspace_bytes(1)  # refuses dimensions the library does not take
 
     @classmethod
@@ -840,3 +856,52 @@ class AdapterPool:
             _check(lib().weightless_adapters_add(self._ref, x.data_ptr(), index.data_ptr(), T, base.data_ptr(),
                                                  y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev)))
         return y
+
+    def backward_workspace_bytes(self, T: int) -> int:
+        """Workspace bytes of backward() with T tokens."""
+        need = self._backward_need.get(T)
+        if need is None:
+            need = lib().weightless_adapters_backward_workspace_bytes(self._ref, T)
+            if need == 0:
+                raise WlError(-2, last_error())
+            self._backward_need[T] = need
+        return need
+
+    def backward(self, x: ActCode, dy, index, base=None, want=("dx", "du", "dv"), dx=None, du=None, dv=None, ws=None,
+                 stream=None) -> AdapterGrads:
+        """Gradients of add() (weightless_adapters_backward).
+
+        x: the ActCode checkpoint of the call's input; dy: bf16 [T, N]; base: bf16
+        [T, K], the shared projection's dx, which dx adds to (dx may be base).
+        du and dv have u's and vt's shapes, bf16; outputs are allocated if not
+        given."""
+        import torch
+        dev = self.device
+        if not isinstance(x, ActCode) or x.K != self.K or x.buf.device != dev:
+            raise WlError(-1, f"x must be an ActCode of K = {self.K} on {dev}")
+        T = x.T
+        _only_wanted(want, AdapterGrads._fields, {"dx": dx, "du": du, "dv": dv})
+        if (base is not None) != ("dx" in want):
+            raise WlError(-1, "base goes with dx")
+        with _scope(dev, stream):
+            _check_tensor(dy, "dy", (T, self.width), torch.bfloat16, dev)
+            _check_tensor(index, "index", (T,), torch.int32, dev)
+            g = WlAdapterGrads()
+            if "dx" in want:
+                _check_tensor(base, "base", (T, self.K), torch.bfloat16, dev)
+                dx = _output(dx, "dx", (T, self.K), torch.bfloat16, dev)
+                g.base, g.dx = base.data_ptr(), dx.data_ptr()
+            if "du" in want:
+                du = _output(du, "du", tuple(self.u.shape), torch.bfloat16, dev)
+                g.du = du.data_ptr()
+            if "dv" in want:
+                dv = _output(dv, "dv", tuple(self.vt.shape), torch.bfloat16, dev)
+                g.dv = dv.data_ptr()
+            if ws is None:
+                ws = torch.empty(self.backward_workspace_bytes(T), dtype=torch.uint8, device=dev)
+            else:
+                _check_tensor(ws, "ws", (None,), torch.uint8, dev)
+            _check(lib().weightless_adapters_backward(self._ref, x.buf.data_ptr(), x.buf.numel(), dy.data_ptr(),
+                                                      index.data_ptr(), T, ctypes.byref(g), ws.data_ptr(), ws.numel(),
+                                                      _raw_stream(dev)))
+        return AdapterGrads(dx, du, dv)

@@ -56,4 +56,16 @@ size_t adapters_workspace_bytes(const AdapterPool &p, int T);
 hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_t *index, int T, const uint16_t *base,
                            uint16_t *y, void *ws, hipStream_t stream);
 
+// Gradients of launch_adapters (adapters.hip has the formulas); every output may
+// be null.
+struct AdapterGrads {
+  const uint16_t *base;  // [T][K], what dx adds to
+  uint16_t *dx;          // [T][K], may be base
+  uint16_t *du;          // [n][Ntot][r]
+  uint16_t *dv;          // [n][nchild * r][K]
+};
+size_t adapters_backward_workspace_bytes(const AdapterPool &p, int T);
+hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, const uint16_t *dy, const int32_t *index,
+                                    int T, const AdapterGrads &o, void *ws, hipStream_t stream);
+
 }  // namespace wl

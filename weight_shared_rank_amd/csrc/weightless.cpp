@@ -1161,7 +1161,7 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
   wl::NormBackward c{};
   wl_status st = check_norm(T, K, d_w, w_dtype, offset, c.w);
   if (st != WL_OK) return st;
-  if (!d_dx && !d_dw) return fail(WL_EINVAL, "no output is asked for");
+  if (!d_dx && !d_dw) return T == 0 ? WL_OK : fail(WL_EINVAL, "no output is asked for");
   if ((st = check_optional(d_dw, 16, "dw")) != WL_OK || (st = check_optional(d_dx, 16, "dx")) != WL_OK) return st;
   const size_t rows = static_cast<size_t>(T) * K * 2;
   if (T > 0) {
@@ -1227,6 +1227,56 @@ wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, 
                                            static_cast<const uint16_t *>(d_base), static_cast<uint16_t *>(d_y), d_ws,
                                            static_cast<hipStream_t>(stream));
   return e == hipSuccess ? WL_OK : hip_fail(e, "adapters launch");
+}
+
+size_t weightless_adapters_backward_workspace_bytes(const wl_adapters *adapters, int32_t T) {
+  wl::AdapterPool p;
+  if (check_adapters(adapters, T, p) != WL_OK) return 0;
+  g_err.clear();
+  return wl::adapters_backward_workspace_bytes(p, T);
+}
+
+wl_status weightless_adapters_backward(const wl_adapters *adapters, const void *d_xcode, size_t xcode_bytes,
+                                       const void *d_dy, const int32_t *d_index, int32_t T,
+                                       const wl_adapter_grads *grads, void *d_ws, size_t ws_bytes, void *stream) {
+  wl::AdapterPool p;
+  wl_status st = check_adapters(adapters, T, p);
+  if (st != WL_OK) return st;
+  if (!grads) return fail(WL_EINVAL, "grads is NULL");
+  if (!grads->dx && !grads->du && !grads->dv) return T == 0 ? WL_OK : fail(WL_EINVAL, "no output is asked for");
+  if ((st = check_optional(grads->dx, 16, "dx")) != WL_OK || (st = check_optional(grads->du, 16, "du")) != WL_OK ||
+      (st = check_optional(grads->dv, 16, "dv")) != WL_OK)
+    return st;
+  const CodeShape cs = code_shape(T, p.K, false);
+  const size_t rows = static_cast<size_t>(T) * p.K * 2, n = static_cast<size_t>(p.n), row = static_cast<size_t>(p.r) * 2;
+  Ranges r;
+  r.add(grads->du, n * p.Ntot * row, "du", true);
+  r.add(grads->dv, n * p.nchild * row * p.K, "dv", true);
+  if (T > 0) {
+    if ((st = check_adapter_memory(p, r)) != WL_OK ||
+        (st = check_code_buffer(d_xcode, xcode_bytes, cs.bytes, "checkpoint")) != WL_OK ||
+        (st = check_aligned(d_dy, 2, "dy")) != WL_OK || (st = check_aligned(d_index, 4, "index")) != WL_OK ||
+        (st = check_aligned(d_ws, 256, "workspace")) != WL_OK)
+      return st;
+    if (grads->dx && (st = check_aligned(grads->base, 16, "base")) != WL_OK) return st;
+    const size_t need = wl::adapters_backward_workspace_bytes(p, T);
+    if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
+    r.add(grads->dx, rows, "dx", true);
+    if (grads->dx) r.add(grads->base, rows, "base", false);
+    r.add(d_xcode, cs.bytes, "the checkpoint", false);
+    r.add(d_dy, static_cast<size_t>(T) * p.Ntot * 2, "dy", false);
+    r.add(d_index, static_cast<size_t>(T) * 4, "index", false);
+    r.add(d_ws, need, "the workspace", true);
+  }
+  if ((st = r.check({{"dx", "base"}})) != WL_OK) return st;
+  wl::AdapterGrads o{};
+  o.base = static_cast<const uint16_t *>(grads->base);
+  o.dx = static_cast<uint16_t *>(grads->dx);
+  o.du = static_cast<uint16_t *>(grads->du);
+  o.dv = static_cast<uint16_t *>(grads->dv);
+  const hipError_t e = wl::launch_adapters_backward(p, code_view(d_xcode, cs), static_cast<const uint16_t *>(d_dy), d_index,
+                                                    T, o, d_ws, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? WL_OK : hip_fail(e, "adapters backward launch");
 }
 
 size_t weightless_backward_workspace_bytes(const wl_bundle *bundle, int32_t T) {
