@@ -5,1059 +5,840 @@
 // with U_a [N][r], V_a^T [r][K] of slot a in the pool; a stacked call's children
 // have their own U and V over one x.  Tokens without an adapter keep base.
 //
-// Tokens are taken in tiles of up to M that share a slot, so that an adapter is
-// read once for M tokens and its products run on the matrix cores: the tokens
-// are the columns of a product, the rows of V^T or U its rows.  Where a call has
-// few tokens (kLeaderT) there is nothing to prepare: workgroup t looks through
-// the whole index and works if token t is the first, the 17th, ... of its slot.
-// A longer call is grouped first (group_kernel).
+// Tokens are taken in tiles that share a slot: the columns of matrix products whose
+// rows are V^T's and U's.  c z enters the second product as a pair of bf16 (the
+// value and what its rounding left, 16 significant bits); y is rounded once.
 //
-// Two launches: thin_kernel gives z in float32 (K cut into slices that the
-// reader adds up in a fixed order), expand_kernel turns c z into a pair of bf16
-// (the value and what its rounding left, 16 significant bits), multiplies by U
-// and adds base, rounding once.
+// Few tokens (up to kLeaderT): nothing is prepared and there is one launch.
+// Workgroup t looks through the whole index and works if token t is the first, the
+// 17th, ... of its slot.  It makes z of its tile itself, as do the others along the
+// children's rows: V^T comes from L2 then, and a launch that hands z over costs more
+// (64 tokens through gate|up of 2 x 21504 x 5376 at rank 16: 7.5 + 25 us in two).
+// Many tokens: a grouping (group_kernel), then z (thin_kernel, K cut into slices that
+// the reader adds up in a fixed order), then the products with U and base
+// (expand_kernel), in tiles of 64 tokens.  (In one launch, tiles of 16: 4096 tokens
+// through 5376 x 8192 at rank 64 56 us, of one round of the CUs 28, against 20 + 30.)
+//
+// Everything moves as rows, 8 lanes to a cache line, and reaches the matrix cores
+// through LDS: fragments loaded as they are used (16 rows of 64 bytes a load) pass
+// the first-level cache at a quarter of the rate (9.5 against 35 TB/s over the
+// card).  The loops are short, so what surrounds their loads counts: none is
+// conditional and no path leaves a loop early (where paths meet, the compiler cannot
+// count the loads in flight and waits for all of them), addresses are a scalar plus
+// a fixed offset of the lane, and what masks a partial stage or row is kept apart.
 //
 // What bounds it: few tokens, reading the adapters in use; many, reading and
 // writing base and y.  The products are far below the matrix cores' rate.
-#include <algorithm>
 #include <type_traits>
 
-#include "beside.h"
-#include "coded.h"
-#include "common.h"
-#include "lds_dma.h"
+#include "adapter_tiles.h"
 
 namespace wl {
 
 namespace {
 
-constexpr int kCUs = 256;
-constexpr int kLeaderT = 256;    // up to here no grouping launch (a thread of a workgroup for each token)
-constexpr int kLeaderM = 16;     // tokens of a tile there
-constexpr int kMaxSlots = 4096;
-constexpr int kStage = 8192;     // tokens whose slots a grouping workgroup holds at a time
+constexpr int kWaves = 8, kThreads = kWaves * 64;
+constexpr int kTileM = 16;   // tokens of a tile of a call of few tokens
+constexpr int kGroupM = 64;  // and of a grouped one
+constexpr int kDeep = 4;     // stages of x and V^T under way
 
-struct TileSource {
-  const int32_t *index;  // [T]
-  const int32_t *rank;   // [n] or null
-  int32_t T, n, r;
-  int32_t copies;        // tokens without an adapter are tiles too (y is not base)
-  // grouped calls (else null): tile i has the slot and count tiles[i] and the
-  // tokens perm[i * M ..], -1 behind the last
-  const int2 *tiles;
-  const int32_t *ntiles;
-  const int32_t *perm;
-};
-
-struct Tile {
-  int slot;   // -1: no adapter
-  int count;  // tokens
-  int rank;   // of the slot
-  int rank16; // rounded up to 16
-};
-
-// Rank of a slot, in [0, r].
-__device__ __forceinline__ int slot_rank(const int32_t *rank, int r, int a) {
-  return rank ? min(max(rank[a], 0), r) : r;
-}
-
-// 16 bytes at an address that is 2-byte aligned (rows of an odd width): the
-// memory path takes them whole.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-__device__ __forceinline__ u32x4 ld16_any(const uint16_t *p) { return *reinterpret_cast<const u32x4_any *>(p); }
-__device__ __forceinline__ void st16_any(uint16_t *p, u32x4 v) { *reinterpret_cast<u32x4_any *>(p) = v; }
-
-// The first n of 8 bf16, zeros behind them.
-__device__ __forceinline__ u32x4 first_of_8(u32x4 v, int n) {
-  if (n >= 8) return v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] &= n >= 2 * i + 2 ? 0xffffffffu : n > 2 * i ? 0xffffu : 0u;
-  return v;
-}
-
-// Tile `id` of M tokens for a workgroup of 256 threads; its tokens go to tok
-// (-1 behind the last).  False (for the whole workgroup): nothing to do.
-template <int M>
-__device__ __forceinline__ bool get_tile(const TileSource &s, int id, Tile &t, int *tok) {
-  if (s.tiles) {
-    if (id >= *s.ntiles) return false;
-    const int2 e = s.tiles[id];
-    t.slot = e.x;
-    t.count = e.y;
-    if (threadIdx.x < M) tok[threadIdx.x] = s.perm[static_cast<int64_t>(id) * M + threadIdx.x];
-  } else {
-    __shared__ uint64_t member[kLeaderT / 64];
-    const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
-    // slots outside the pool count as slot n, no adapter
-    const int of_id = s.index[id], of_i = i < s.T ? s.index[i] : 0;
-    const int a = static_cast<uint32_t>(of_id) < static_cast<uint32_t>(s.n) ? of_id : s.n;
-    const int b = static_cast<uint32_t>(of_i) < static_cast<uint32_t>(s.n) ? of_i : s.n;
-    const uint64_t m = __builtin_amdgcn_ballot_w64(i < s.T && a == b);
-    if (lane == 0) member[wave] = m;
-    if (i < M) tok[i] = -1;
-    __syncthreads();
-    int before = 0, at = 0, total = 0;  // members before token id, before token i, in all
-#pragma unroll
-    for (int w = 0; w < kLeaderT / 64; ++w) {
-      const uint64_t v = member[w];
-      const int c = __builtin_popcountll(v);
-      total += c;
-      at += w < wave ? c : w == wave ? __builtin_popcountll(v & ((uint64_t{1} << lane) - 1)) : 0;
-      before += w < (id >> 6) ? c : w == (id >> 6) ? __builtin_popcountll(v & ((uint64_t{1} << (id & 63)) - 1)) : 0;
-    }
-    if (before % M) return false;
-    if (i < s.T && a == b && at >= before && at < before + M) tok[at - before] = i;
-    t.slot = a < s.n ? a : -1;
-    t.count = min(M, total - before);
-  }
-  t.rank = 0;
-  if (t.slot >= 0) {
-    t.rank = slot_rank(s.rank, s.r, t.slot);
-    if (t.rank == 0) t.slot = -1;
-  }
-  t.rank16 = (t.rank + 15) & ~15;
-  if (t.slot < 0 && !s.copies) return false;
-  __syncthreads();
-  return true;
-}
-
-// Grouping of a long call.  A wave takes one slot (n: no adapter): it counts the
-// tokens of every slot (the workgroup's histogram), so its first tile is known
-// without waiting for anyone, and writes its tokens in ascending order.  The
-// slots of up to kStage tokens at a time sit in LDS, where all four waves look
-// through them.
-struct GroupArgs {
+struct AdapterArgs {
   TileSource s;
-  int2 *tiles;
-  int32_t *ntiles, *perm;
-  int32_t *first, *count;  // per slot [n]: its first tile and tokens (null: not wanted)
+  const uint16_t *x;     // [T][K]
+  const uint16_t *vt;    // [n][nchild * r][K]
+  const uint16_t *u;     // [n][Ntot][r]
+  const float *scale;    // [n]
+  const uint16_t *base;  // [T][Ntot]
+  uint16_t *y;           // [T][Ntot]
+  float *P;              // grouped calls: z [slices][rows][R]
+  int64_t rows;
+  int32_t R, slices, per;                     // R: nchild * r; per: k of a slice
+  int32_t K, Ntot, nchild, turns;             // turns: times a wave takes 64 rows of U
+  int32_t N[kMaxChildren], n0[kMaxChildren];  // rows and first row of a child
+  int32_t block0[kMaxChildren];               // first workgroup (y) of a child
 };
 
-__device__ __forceinline__ uint16_t stage_slot(const TileSource &s, int64_t t) {
-  const uint32_t v = static_cast<uint32_t>(s.index[t]);
-  return static_cast<uint16_t>(v < static_cast<uint32_t>(s.n) ? v : s.n);
+// Elements of a row of c z in LDS: as many ranks as RowWalk reads at most (a power
+// of two, 32 or more), and 16 bytes more, which spread the fragment reads over the
+// banks.
+__host__ __device__ constexpr int z_pitch(int r) { return (r <= 32 ? 32 : r <= 64 ? 64 : r <= 128 ? 128 : 256) + 8; }
+
+// c z of NF row tiles of V^T (from row j0 of the slot's child on) to zs [2][16][pitch].
+// A stage is KS values of k: rows of 64 k (128 bytes), chunk c of row t in slot
+// c ^ t % 8, so that fragment reads touch every bank.  It waits in registers while
+// the kDeep - 1 before it are used.  A wave multiplies two row tiles (one where there
+// is no more) over 32 k of a stage: what it reads of LDS bounds the loop.  The waves'
+// sums meet in LDS in wave order.
+// (A stage of 20 KB with conditional loads: 0.42 us, with masks and 64-bit addresses
+// throughout 0.39, as it is 0.27.)
+template <int NF>
+__device__ __forceinline__ void form_z(const AdapterArgs &a, const Tile &t, const int *tok, int c, int j0, uint8_t *lds,
+                                       uint16_t *zs) {
+  constexpr int FR = NF == 1 ? 1 : 2, FP = NF / FR, H = kWaves / FP;  // row tiles of a wave, pairs, waves along k
+  constexpr int KS = 32 * H, SUBS = KS / 64;
+  constexpr int XB = SUBS * kTileM * 128, AB = SUBS * NF * 2048, STAGE = XB + AB;  // bytes of a stage
+  constexpr int AP = AB / 16 / kThreads;                                           // pieces of V^T of a thread
+  static_assert(XB / 16 <= kThreads && AP * kThreads * 16 == AB && kDeep % 2 == 0, "stage shape");
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4, K = a.K;
+  const u32x4 zero{0u, 0u, 0u, 0u};
+  // pieces of 16 bytes: 64 k (sub), row, chunk
+  const int chunk = threadIdx.x & 7;
+  const int xrow = threadIdx.x / 8 % kTileM, xsub = threadIdx.x / (8 * kTileM) % SUBS;  // (NF 4: every piece twice)
+  const int xtoken = tok[xrow] < 0 ? tok[0] : tok[xrow];  // (columns without a token are not stored)
+  const uint16_t *xrowp = a.x + static_cast<int64_t>(xtoken) * K;
+  const int xk = xsub * 64 + chunk * 8;
+  const uint16_t *av0 = a.vt + ((static_cast<int64_t>(t.slot) * a.nchild + c) * a.s.r + j0) * K;
+  uint32_t arow[AP];  // bytes from av0 to the piece's row; row tiles past the slot's rank repeat the last (masked)
+  int ak[AP];
+  uint8_t *aput[AP];
+#pragma unroll
+  for (int i = 0; i < AP; ++i) {
+    const int p = i * kThreads + static_cast<int>(threadIdx.x), row = p / 8 % (16 * NF), sub = p / (128 * NF);
+    arow[i] = static_cast<uint32_t>(min(row, t.rank16 - 1 - j0)) * static_cast<uint32_t>(K) * 2u;
+    ak[i] = sub * 64 + chunk * 8;
+    aput[i] = lds + XB + (sub * 16 * NF + row) * 128 + (chunk ^ (row & 7)) * 16;
+  }
+  uint8_t *const xput = lds + (xsub * kTileM + xrow) * 128 + (chunk ^ (xrow & 7)) * 16;
+  const int fp = wave % FP, h = wave / FP, frag = (((4 * h + g) & 7) ^ (r16 & 7)) * 16;  // this wave's 32 k
+  const uint8_t *fa = lds + XB + ((h >> 1) * 16 * NF + 16 * FR * fp + r16) * 128 + frag, *fx = lds + ((h >> 1) * kTileM + r16) * 128 + frag;
+  u32x4 xv[kDeep], av[kDeep][AP];
+  f32x4 acc[FR];
+#pragma unroll
+  for (int f = 0; f < FR; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int buf) {
+    wait_and_sync<63>();  // this stage is in LDS; loads stay under way
+    const u32x4 x = *reinterpret_cast<const u32x4 *>(fx + buf);
+#pragma unroll
+    for (int f = 0; f < FR; ++f) acc[f] = mfma16x16x32(*reinterpret_cast<const u32x4 *>(fa + buf + f * 2048), x, acc[f]);
+  };
+  // whole stages
+  const uint16_t *xp = xrowp + xk, *ap = av0;
+  uint32_t aoff[AP];
+#pragma unroll
+  for (int i = 0; i < AP; ++i) aoff[i] = arow[i] + ak[i] * 2;
+  auto load = [&](int d) {
+    xv[d] = ld16(xp + d * KS);
+#pragma unroll
+    for (int i = 0; i < AP; ++i) av[d][i] = ld16_at(ap + d * KS, aoff[i]);
+  };
+  auto use = [&](int d) {
+    *reinterpret_cast<u32x4 *>(xput + (d & 1) * STAGE) = xv[d];
+#pragma unroll
+    for (int i = 0; i < AP; ++i) *reinterpret_cast<u32x4 *>(aput[i] + (d & 1) * STAGE) = av[d][i];
+  };
+  // the last ones: pieces past K read the row's first and are zeroed on their way to LDS
+  auto load_last = [&](int stage, int d) {
+    const int k = stage * KS;
+    xv[d] = ld16(xrowp + (k + xk < K ? k + xk : 0));
+#pragma unroll
+    for (int i = 0; i < AP; ++i) av[d][i] = ld16_at(av0, arow[i] + (k + ak[i] < K ? k + ak[i] : 0) * 2u);
+  };
+  auto use_last = [&](int stage, int d) {
+    const int k = stage * KS;
+    *reinterpret_cast<u32x4 *>(xput + (d & 1) * STAGE) = k + xk < K ? xv[d] : zero;
+#pragma unroll
+    for (int i = 0; i < AP; ++i) *reinterpret_cast<u32x4 *>(aput[i] + (d & 1) * STAGE) = k + ak[i] < K ? av[d][i] : zero;
+  };
+  const int groups = K / (KS * kDeep), stages = (K + KS - 1) / KS;  // groups of kDeep whole stages; all stages
+  if (groups > 0) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) load(d);
+    for (int i = 1; i < groups; ++i) {
+      xp += KS * kDeep;
+      ap += KS * kDeep;
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        use(d);
+        load(d);
+        multiply((d & 1) * STAGE);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      use(d);
+      load_last(groups * kDeep + d, d);
+      multiply((d & 1) * STAGE);
+    }
+  } else {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) load_last(d, d);
+  }
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    if (groups * kDeep + d >= stages) break;
+    use_last(groups * kDeep + d, d);
+    multiply((d & 1) * STAGE);
+  }
+  f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [wave][FR][64]
+  __syncthreads();
+#pragma unroll
+  for (int f = 0; f < FR; ++f) part[(wave * FR + f) * 64 + lane] = acc[f];
+  __syncthreads();
+  if (wave < NF) {  // row tile `wave`
+    f32x4 sum = part[(wave / FR * FR + wave % FR) * 64 + lane];
+#pragma unroll
+    for (int q = 1; q < H; ++q) sum += part[((q * FP + wave / FR) * FR + wave % FR) * 64 + lane];
+    const int j = j0 + 16 * wave + 4 * g, pitch = z_pitch(a.s.r);
+    if (j < pitch - 8) {
+      const float scale = a.scale[t.slot];
+      f32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? sum[k] * scale : 0.f;
+      split4(v, *reinterpret_cast<u32x2 *>(zs + r16 * pitch + j), *reinterpret_cast<u32x2 *>(zs + (kTileM + r16) * pitch + j));
+    }
+  }
+  __syncthreads();
 }
 
-template <int M>
-__global__ __launch_bounds__(256) void group_kernel(GroupArgs g) {
-  const TileSource &s = g.s;
-  __shared__ int hist[kMaxSlots + 1];
-  __shared__ uint16_t of[kStage];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int mine = blockIdx.x * 4 + wave;
-  for (int b = threadIdx.x; b <= s.n; b += 256) hist[b] = 0;
-  __syncthreads();
-  for (int t0 = 0; t0 < s.T; t0 += kStage) {
-    const int len = min(kStage, s.T - t0);
-#pragma unroll 8
-    for (int i = threadIdx.x; i < len; i += 256) {
-      const uint16_t v = stage_slot(s, t0 + i);
-      of[i] = v;
-      atomicAdd(&hist[v], 1);
+// z of a tile of up to NT tokens whose slot's rows are only read once: dot products
+// in registers, no matrix cores (a tile of 16 tokens would use a sixteenth of them),
+// no staging.  A wave takes 8 RS rows of V^T, 8 lanes a row, and a share of K; the
+// lanes' and the waves' sums meet at the end.
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float c) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, static_cast<uint32_t>(a[i])),
+                                        __builtin_bit_cast(bf16x2, static_cast<uint32_t>(b[i])), c, false);
+  return c;
+}
+
+template <int RS, int NT>
+__device__ __forceinline__ void dot_z(const AdapterArgs &a, const Tile &t, const int *tok, int c, uint8_t *lds, uint16_t *zs) {
+  constexpr int ROWS = 8 * RS, AHEAD = 4;  // steps of loads under way
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), K = a.K;
+  // groups of rows, and waves that share K for one
+  const int need = (t.rank16 + ROWS - 1) / ROWS, groups = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8, share = kWaves / groups;
+  const int group = wave % groups, part = wave / groups;
+  const uint16_t *v0 = a.vt + ((static_cast<int64_t>(t.slot) * a.nchild + c) * a.s.r) * K;
+  const int chunk = (lane & 7) * 8;
+  uint32_t voff[RS];
+#pragma unroll
+  for (int s = 0; s < RS; ++s)  // (rows past the rank repeat the last and are masked)
+    voff[s] = (static_cast<uint32_t>(min(group * ROWS + 8 * s + (lane >> 3), t.rank16 - 1)) * static_cast<uint32_t>(K) + chunk) * 2u;
+  const uint16_t *xp[NT];
+#pragma unroll
+  for (int m = 0; m < NT; ++m) xp[m] = a.x + static_cast<int64_t>(keep(tok[m] < 0 ? tok[0] : tok[m])) * K;
+  float acc[RS][NT];
+#pragma unroll
+  for (int s = 0; s < RS; ++s)
+#pragma unroll
+    for (int m = 0; m < NT; ++m) acc[s][m] = 0.f;
+  const int stride = share * 64, whole = K / (stride * AHEAD);
+  u32x4 v[AHEAD][RS], x[AHEAD][NT];
+  int k = part * 64;
+  for (int i = 0; i < whole; ++i) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d, k += stride) {
+#pragma unroll
+      for (int s = 0; s < RS; ++s) v[d][s] = ld16_at(v0 + k, voff[s]);
+#pragma unroll
+      for (int m = 0; m < NT; ++m) x[d][m] = ld16_at(xp[m] + k, chunk * 2u);
     }
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d)
+#pragma unroll
+      for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) acc[s][m] = dot8(v[d][s], x[d][m], acc[s][m]);
   }
-  __syncthreads();
-  const int cnt = mine <= s.n ? hist[mine] : 0;
-  int tile0 = 0, tiles = 0;
-  for (int b = lane; b <= min(mine, s.n); b += 64) {
-    const bool copy = b == s.n || slot_rank(s.rank, s.r, b) == 0;
-    const int k = copy && !s.copies ? 0 : (hist[b] + M - 1) / M;
-    if (b < mine)
-      tile0 += k;
-    else
-      tiles = k;
+  const u32x4 zero{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) {
+    const bool in = k + d * stride + chunk < K;
+    const uint32_t at = in ? (k + d * stride) * 2u : 0u;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) v[d][s] = in ? ld16_at(v0, voff[s] + at) : zero;
+#pragma unroll
+    for (int m = 0; m < NT; ++m) x[d][m] = in ? ld16_at(xp[m], chunk * 2u + at) : zero;
   }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    tile0 += __shfl_xor(tile0, d, 64);
-    tiles += __shfl_xor(tiles, d, 64);
-  }
-  if (mine <= s.n) {
-    const int slot = mine < s.n && slot_rank(s.rank, s.r, mine) > 0 ? mine : -1;
-    for (int i = lane; i < tiles; i += 64) g.tiles[tile0 + i] = int2{slot, min(M, cnt - i * M)};
-    if (mine == s.n && lane == 0) *g.ntiles = tile0 + tiles;
-    if (g.first && mine < s.n && lane == 0) {
-      g.first[mine] = tile0;
-      g.count[mine] = slot >= 0 ? cnt : 0;
-    }
-    for (int i = cnt + lane; i < tiles * M; i += 64) g.perm[static_cast<int64_t>(tile0) * M + i] = -1;
-  }
-  // the tokens; every wave goes through every stage (the barriers are the workgroup's)
-  int found = 0;
-  int32_t *out = g.perm + static_cast<int64_t>(tile0) * M;
-  for (int t0 = 0; t0 < s.T; t0 += kStage) {
-    const int len = min(kStage, s.T - t0);
-    if (s.T > kStage) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < len; i += 256) of[i] = stage_slot(s, t0 + i);
-      __syncthreads();
-    }
-    if (!tiles) continue;
-    for (int i0 = 0; i0 < len && found < cnt; i0 += 256) {
+  for (int d = 0; d < AHEAD; ++d)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 64 * j + lane;
-        const bool hit = i < len && of[i] == mine;
-        const uint64_t m = __builtin_amdgcn_ballot_w64(hit);
-        if (hit) out[found + __builtin_popcountll(m & ((uint64_t{1} << lane) - 1))] = t0 + i;
-        found += __builtin_popcountll(m);
+    for (int s = 0; s < RS; ++s)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) acc[s][m] = dot8(v[d][s], x[d][m], acc[s][m]);
+  float *sums = reinterpret_cast<float *>(lds);  // [wave][row][token]
+#pragma unroll
+  for (int s = 0; s < RS; ++s)
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      float w = acc[s][m];
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) w += __shfl_xor(w, d, 64);
+      if ((lane & 7) == 0) sums[(wave * ROWS + 8 * s + (lane >> 3)) * NT + m] = w;
+    }
+  __syncthreads();
+  const float scale = a.scale[t.slot];
+  const int pitch = z_pitch(a.s.r);
+  // four ranks of a token a thread
+  for (int i = threadIdx.x; i < groups * (ROWS / 4) * NT; i += kThreads) {
+    const int m = i % NT, j = i / NT * 4;  // j: row of V^T
+    if (j >= t.rank16) continue;
+    f32x4 v{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < share; ++q)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += sums[((q * groups + j / ROWS) * ROWS + j % ROWS + k) * NT + m];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? v[k] * scale : 0.f;
+    split4(v, *reinterpret_cast<u32x2 *>(zs + m * pitch + j), *reinterpret_cast<u32x2 *>(zs + (kTileM + m) * pitch + j));
+  }
+  __syncthreads();
+}
+
+// y[t][n] = base[t][n] + sum_j c z[t][j] U_a[n][j] of the wave's turns, 64 n each.
+// U, 32 ranks at a time, and the sums pass through a piece of LDS of the wave's own,
+// so that U is read as rows and base and y as 128 bytes a token.  UNITS times 32 CW
+// ranks hold the slot's (CW 0: one unit of 16, rows of 32 bytes); the loads of the
+// next unit are under way while one is used, base's a turn ahead, and the first
+// (of U up to 32 ranks) leave before form() makes z.  A child's last, partial 64 n are a turn of their own.
+constexpr int kUPitch = 80, kOutPitch = 272, kWaveLds = 64 * kUPitch;  // bytes
+static_assert(16 * kOutPitch <= kWaveLds, "the sums fit the piece");
+
+template <int UNITS, int CW>
+struct RowWalk {
+  static constexpr int CHUNKS = CW ? CW : 1, PER = CW ? 4 : 2, LOADS = PER * CHUNKS, ROWS = CW ? 16 : 32;
+  static constexpr int COLS = CW ? 32 * CW * UNITS : 16;  // ranks it reads
+  static constexpr bool EARLY = CW < 2;                   // (more would cost form() registers)
+  const AdapterArgs &a;
+  const Tile &t;
+  const uint16_t *zs, *U;
+  uint8_t *mine;
+  int N, r, pitch, lane, r16, g, wave, urow, ucol;
+  uint32_t uoff[PER];  // bytes from the first row of a turn
+  // as rows: lane -> row lane / 8 (of 8) of base and y, 8 n from 8 (lane % 8) on
+  int64_t at[2];
+  bool has[2];
+
+  __device__ __forceinline__ RowWalk(const AdapterArgs &a_, const Tile &t_, int c, const int *tok, const uint16_t *zs_, uint8_t *lds)
+      : a(a_), t(t_), zs(zs_) {
+    lane = threadIdx.x & 63;
+    wave = keep(threadIdx.x >> 6);
+    r16 = lane & 15;
+    g = lane >> 4;
+    urow = CW ? lane >> 2 : lane >> 1;
+    ucol = CW ? (lane & 3) * 8 : (lane & 1) * 8;
+    mine = lds + wave * kWaveLds;
+    N = a.N[c];
+    r = a.s.r;
+    pitch = z_pitch(r);
+    U = a.u + (static_cast<int64_t>(max(t.slot, 0)) * a.Ntot + a.n0[c]) * r;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) uoff[q] = static_cast<uint32_t>((ROWS * q + urow) * r + ucol) * 2u;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int token = tok[8 * q + (lane >> 3)];
+      has[q] = token >= 0;
+      at[q] = static_cast<int64_t>(has[q] ? token : tok[0]) * a.Ntot + a.n0[c] + (lane & 7) * 8;
+    }
+  }
+  // FULL: 64 rows exist, and where ranks are read past the room one more (what they
+  // find, the next row's, is masked).  Otherwise rows past the last repeat it (not
+  // stored) and ranks past the room the first.
+  template <bool FULL>
+  __device__ __forceinline__ void load_u(int nw, int unit, u32x4 (&o)[LOADS]) const {
+    const uint16_t *p = U + static_cast<int64_t>(nw) * r;
+#pragma unroll
+    for (int ch = 0; ch < CHUNKS; ++ch)
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int k0 = (unit * CHUNKS + ch) * 32;
+        if constexpr (FULL)
+          o[ch * PER + q] = ld16_at(p + k0, uoff[q]);
+        else
+          o[ch * PER + q] = ld16(U + static_cast<int64_t>(min(nw + ROWS * q + urow, N - 1)) * r + (k0 + ucol < r ? k0 + ucol : 0));
+      }
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void load_base(int nw, u32x4 (&o)[2]) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      o[q] = FULL ? ld16_any(a.base + at[q] + nw) : load_some(a.base + at[q] + nw, N - (nw + (lane & 7) * 8));
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void store(int nw, const u32x4 (&o)[2]) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (!has[q]) continue;
+      if constexpr (FULL)
+        st16_any(a.y + at[q] + nw, o[q]);
+      else
+        store_some(a.y + at[q] + nw, o[q], N - (nw + (lane & 7) * 8));
+    }
+  }
+  // One turn: un holds its first unit of U, bn its base; afterwards both hold those
+  // of the turn at `next`.
+  template <bool FULL>
+  __device__ __forceinline__ void turn(int nw, u32x4 (&un)[LOADS], u32x4 (&bn)[2], int next) const {
+    const u32x4 zero{0u, 0u, 0u, 0u};
+    f32x4 acc[4];
+    u32x4 b[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) b[q] = bn[q];
+#pragma unroll
+    for (int unit = 0; unit < UNITS; ++unit) {
+#pragma unroll
+      for (int ch = 0; ch < CHUNKS; ++ch) {
+        const int k0 = (unit * CHUNKS + ch) * 32;
+        if (k0 + (CW ? 32 : 16) > t.rank) {
+#pragma unroll
+          for (int q = 0; q < PER; ++q) un[ch * PER + q] = first_of_8(un[ch * PER + q], t.rank - (k0 + ucol));
+        }
+#pragma unroll
+        for (int q = 0; q < PER; ++q) *reinterpret_cast<u32x4 *>(mine + (ROWS * q + urow) * kUPitch + ucol * 2) = un[ch * PER + q];
+        if (ch == CHUNKS - 1) {
+          load_u<FULL>(unit + 1 < UNITS ? nw : next, (unit + 1) % UNITS, un);
+          if (unit == 0) load_base<FULL>(next, bn);
+        }
+        const bool in = CW || g < 2;  // (16 ranks: the other half of the contraction is zeros)
+        u32x4 uv[4], zv[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) zv[p] = in ? ld16(zs + (p * kTileM + r16) * pitch + k0 + 8 * g) : zero;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) uv[j] = in ? *reinterpret_cast<const u32x4 *>(mine + (16 * j + r16) * kUPitch + 16 * g) : zero;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma16x16x32(uv[j], zv[p], acc[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(mine + r16 * kOutPitch + (16 * j + 4 * g) * 4) = acc[j];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f32x4 *o = reinterpret_cast<const f32x4 *>(mine + (8 * q + (lane >> 3)) * kOutPitch + (lane & 7) * 32);
+      b[q] = add_8(b[q], o[0], o[1]);
+    }
+    store<FULL>(nw, b);
+  }
+  // Every wave calls form(), which has barriers.
+  template <typename Z>
+  __device__ __forceinline__ void run(int first, Z &&form) const {
+    const int end = min(N, first + a.turns * kThreads), full = min(end, (N - (COLS > r ? 1 : 0)) / 64 * 64);
+    int nw = first + wave * 64;
+    u32x4 un[LOADS], bn[2];
+    if (nw < full) {
+      if (EARLY) load_u<true>(nw, 0, un);
+      load_base<true>(nw, bn);
+    }
+    form();
+    if (!EARLY && nw < full) load_u<true>(nw, 0, un);
+    for (; nw < full; nw += kThreads) turn<true>(nw, un, bn, nw + kThreads < full ? nw + kThreads : nw);  // (the last loads itself again)
+    if (nw >= end) return;
+    load_u<false>(nw, 0, un);
+    load_base<false>(nw, bn);
+    turn<false>(nw, un, bn, nw);
+  }
+  // Tokens without an adapter.
+  __device__ __forceinline__ void copy(int first) const {
+    const int end = min(N, first + a.turns * kThreads);
+    for (int nw = first + wave * 64; nw < end; nw += kThreads) {
+      u32x4 b[2];
+      if (nw + 64 <= N) {
+        load_base<true>(nw, b);
+        store<true>(nw, b);
+      } else {
+        load_base<false>(nw, b);
+        store<false>(nw, b);
       }
     }
   }
-}
-
-// ---- thin products ------------------------------------------------------------
-// P[slice][row][col] = sum over the slice's k of A_a[col][k] x[token][k]: A the
-// rows of V^T of all children.  A workgroup takes a tile of 16 MF tokens, a
-// K slice and up to 16 NF rows of A; its four waves take steps of 64 k in turn
-// and meet in LDS.  16-row tiles past a slot's rank are left out.  Both operands go
-// straight to registers: a lane's two loads of a step are 32 neighbouring bytes
-// of its row, four lanes a cache line.
-struct ThinArgs {
-  TileSource s;
-  const uint16_t *x;   // [T][K]
-  const uint16_t *A;   // [n][nchild * r][K]
-  int32_t K, nchild;
-  int32_t slices, per; // slices of K, steps of each
-  float *P;            // [slices][rows][R]
-  int32_t R;           // nchild * r
-  int64_t rows;
 };
 
-template <int MF, int NF>
-__global__ __launch_bounds__(256) void thin_kernel(ThinArgs a) {
-  constexpr int M = 16 * MF;
-  __shared__ int tok[M];
-  __shared__ f32x4 part[3][MF * NF][64];
-  Tile t;
-  if (!get_tile<M>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int per_child = t.rank16 / 16, live = a.nchild * per_child;  // 16-row tiles of A in use
-  const int f0 = blockIdx.z * NF;
-  if (f0 >= live) return;
-  const uint16_t *xr[MF], *ar[NF];
-  bool xin[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int token = tok[16 * i + r16];
-    xin[i] = token >= 0;
-    xr[i] = a.x + static_cast<int64_t>(max(token, 0)) * a.K;
-  }
-  int col[NF];  // first row of A (column of P) of a tile
-#pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    const int v = min(f0 + f, live - 1);  // tiles past the last repeat it and are not stored
-    col[f] = (v / per_child) * a.s.r + (v % per_child) * 16;
-    ar[f] = a.A + (static_cast<int64_t>(t.slot) * a.R + col[f] + r16) * a.K;
-  }
-  f32x4 acc[NF][MF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < MF; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  const int steps = (a.K + 63) / 64;
-  const int end = min(steps, static_cast<int>(blockIdx.y + 1) * a.per);
-  u32x4 xv[2][MF][2], av[2][NF][2];
-  auto load = [&](int step, u32x4(&xo)[MF][2], u32x4(&ao)[NF][2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = step * 64 + g * 16 + h * 8;
-      const bool in = step < end && k < a.K;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) ao[f][h] = in ? ld16(ar[f] + k) : zero;
-#pragma unroll
-      for (int i = 0; i < MF; ++i) xo[i][h] = in && xin[i] ? ld16(xr[i] + k) : zero;
-    }
-  };
-  auto multiply = [&](const u32x4(&xo)[MF][2], const u32x4(&ao)[NF][2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int i = 0; i < MF; ++i) acc[f][i] = mfma16x16x32(ao[f][h], xo[i][h], acc[f][i]);
-  };
-  int step = blockIdx.y * a.per + wave;
-  load(step, xv[0], av[0]);
-  for (; step < end; step += 8) {
-    load(step + 4, xv[1], av[1]);
-    multiply(xv[0], av[0]);
-    load(step + 8, xv[0], av[0]);
-    multiply(xv[1], av[1]);
-  }
-  if (wave > 0) {
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-#pragma unroll
-      for (int i = 0; i < MF; ++i) part[wave - 1][f * MF + i][lane] = acc[f][i];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      f32x4 v = acc[f][i];
-#pragma unroll
-      for (int w = 0; w < 3; ++w) v += part[w][f * MF + i][lane];
-      const int c = 16 * i + r16;
-      if (f0 + f >= live || c >= t.count) continue;
-      const int64_t row = a.s.tiles ? static_cast<int64_t>(blockIdx.x) * M + c : tok[c];
-      *reinterpret_cast<f32x4 *>(a.P + (blockIdx.y * a.rows + row) * a.R + col[f] + g * 4) = v;
-    }
-}
-
-// ---- the products with U, and base ---------------------------------------------
-// y[t][n] = base[t][n] + sum_j c z[t][j] U_a[n][j].  A wave takes 64 n at a time,
-// `turns` times, as four row tiles whose rows are numbered so that a lane ends
-// up with 8 neighbouring n of its token twice: base and y move as 16 bytes a
-// lane, 64 to a row and load.  c z is the workgroup's, as a pair of bf16 in LDS.
-struct ExpandArgs {
-  TileSource s;
-  const float *P;        // [slices][rows][R]
-  int32_t slices, R;
-  int64_t rows;
-  const float *scale;    // [n]
-  const uint16_t *U;     // [n][Ntot][r]
-  const uint16_t *base;  // [T][Ntot]
-  uint16_t *y;           // [T][Ntot]
-  int32_t Ntot, nchild, turns;
-  int32_t N[kMaxChildren], n0[kMaxChildren];  // rows and first row of a child
-  int32_t block0[kMaxChildren];               // first workgroup (x) of a child
-};
-
-// What a float leaves over its bf16: 0 for infinity and NaN.
-__device__ __forceinline__ float left_over(float v, uint16_t h) {
-  const float d = v - bf16_to_f32(h);
-  return fabsf(d) < __builtin_inff() ? d : 0.f;
-}
-
-template <int MF>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
-  constexpr int M = 16 * MF;
-  __shared__ int tok[M];
-  extern __shared__ __align__(16) uint16_t zs[];  // [2][M][pitch]
-  Tile t;
-  if (!get_tile<M>(a.s, blockIdx.y, t, tok)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
+// Child of workgroup blockIdx.y.
+__device__ __forceinline__ int child_of(const AdapterArgs &a) {
   int c = 0;
 #pragma unroll
   for (int i = 1; i < kMaxChildren; ++i)
-    if (i < a.nchild && static_cast<int>(blockIdx.x) >= a.block0[i]) c = i;
-  const int N = a.N[c], r = a.s.r;
-  const int first = (static_cast<int>(blockIdx.x) - a.block0[c]) * a.turns * 256;
-  const bool adapted = t.slot >= 0;
-  const int pitch = r + 8;  // 16 bytes more than the row: fragment reads spread over the banks
-  if (adapted) {
+    if (i < a.nchild && static_cast<int>(blockIdx.y) >= a.block0[i]) c = i;
+  return c;
+}
+
+// c z [2][M][pitch] all zeros, which ranks past the slot's stay.
+template <int M>
+__device__ __forceinline__ void clear_z(const AdapterArgs &a, uint16_t *zs) {
+  for (int i = threadIdx.x; i < 2 * M * z_pitch(a.s.r) / 8; i += kThreads) reinterpret_cast<u32x4 *>(zs)[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+// ---- few tokens ------------------------------------------------------------------
+constexpr int kRing = 2 * 24 * 1024;  // two stages of form_z<2>, the largest
+static_assert(kWaves * kWaveLds <= kRing, "the waves' pieces lie over the stages");
+
+// ROOM: the pool's rank rounded up to 16, 64 or 256 (what a slot of a larger rank
+// needs costs the others registers; at 16 two workgroups fit a CU).
+template <int ROOM>
+__global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(AdapterArgs a) {
+  __shared__ int tok[kTileM];
+  __shared__ __align__(16) uint8_t lds[kRing];
+  extern __shared__ __align__(16) uint16_t zs[];  // [2][kTileM][pitch]
+  Tile t;
+  if (!get_tile<kTileM>(a.s, blockIdx.x, t, tok)) return;
+  const int c = child_of(a), first = (static_cast<int>(blockIdx.y) - a.block0[c]) * a.turns * kThreads;
+  const auto form = [&] {
+    // c z all zeros, which ranks past the slot's stay (barriers stand between this and the stores of z)
+    for (int i = threadIdx.x; i < 2 * kTileM * z_pitch(a.s.r) / 8; i += kThreads) reinterpret_cast<u32x4 *>(zs)[i] = u32x4{0u, 0u, 0u, 0u};
+    if (t.count == 1) {
+      if (ROOM == 16 || t.rank16 == 16)
+        dot_z<2, 1>(a, t, tok, c, lds, zs);
+      else
+        dot_z<4, 1>(a, t, tok, c, lds, zs);
+      return;
+    }
+    for (int f = 0; f < t.rank16 / 16;) {
+      const int live = t.rank16 / 16 - f;
+      if (ROOM > 16 && live >= 3) {
+        form_z<4>(a, t, tok, c, 16 * f, lds, zs);
+        f += 4;
+      } else if (ROOM > 16 && live == 2) {
+        form_z<2>(a, t, tok, c, 16 * f, lds, zs);
+        f += 2;
+      } else {
+        form_z<1>(a, t, tok, c, 16 * f, lds, zs);
+        f += 1;
+      }
+    }
+  };
+  if (t.slot < 0)
+    RowWalk<1, 0>(a, t, c, tok, zs, lds).copy(first);
+  else if (ROOM == 16 || t.rank16 <= 16)
+    RowWalk<1, 0>(a, t, c, tok, zs, lds).run(first, form);
+  else if (t.rank16 <= 32)
+    RowWalk<1, 1>(a, t, c, tok, zs, lds).run(first, form);
+  else if (ROOM == 64 || t.rank16 <= 64)
+    RowWalk<1, 2>(a, t, c, tok, zs, lds).run(first, form);
+  else if (t.rank16 <= 128)
+    RowWalk<2, 2>(a, t, c, tok, zs, lds).run(first, form);
+  else
+    RowWalk<4, 2>(a, t, c, tok, zs, lds).run(first, form);
+}
+
+// ---- many tokens -------------------------------------------------------------------
+// P[slice][row][col] = sum over the slice's k of V^T[col][k] x[token][k], the rows of
+// V^T of all children, up to 16 NF of them a workgroup.  Stages as in form_z; a wave
+// multiplies two row tiles (one where there is no more) and 32 tokens over 32 k.
+template <int NF>
+__global__ __launch_bounds__(kThreads) void thin_kernel(AdapterArgs a) {
+  constexpr int M = kGroupM, KS = NF == 4 ? 64 : 128, SUBS = KS / 64;
+  constexpr int XB = SUBS * M * 128, AB = SUBS * NF * 2048, STAGE = XB + AB;
+  constexpr int FP = NF == 4 ? 2 : 1, FR = NF == 1 ? 1 : 2, H = kWaves / (2 * FP);  // pairs of row tiles, tiles of a wave, waves along k
+  static_assert(H * 32 == KS && XB == SUBS * kThreads * 16, "stage shape");
+  __shared__ int tok[M];
+  __shared__ __align__(16) uint8_t lds[2 * STAGE];
+  static_assert(kWaves * FR * 2 * 1024 <= 2 * STAGE, "the waves' sums lie over the stages");
+  Tile t;
+  if (!get_tile<M>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4, K = a.K;
+  const int per_child = t.rank16 / 16, live = a.nchild * per_child, f0 = blockIdx.z * NF;
+  if (f0 >= live) return;
+  auto column = [&](int f) {  // first row of V^T (column of P) of row tile f0 + f; those past the last repeat it
+    const int v = min(f0 + f, live - 1);
+    return v / per_child * a.s.r + v % per_child * 16;
+  };
+  const u32x4 zero{0u, 0u, 0u, 0u};
+  const int chunk = threadIdx.x & 7, xrow = threadIdx.x >> 3;
+  const uint16_t *xrowp = a.x + static_cast<int64_t>(tok[xrow] < 0 ? tok[0] : tok[xrow]) * K;
+  const int arow = (threadIdx.x >> 3) % (16 * NF), asub = threadIdx.x / (128 * NF) % SUBS;  // (NF 1: every piece twice)
+  const uint16_t *a0 = a.vt + static_cast<int64_t>(t.slot) * a.R * K;
+  const uint32_t arowb = static_cast<uint32_t>(column(arow >> 4) + (arow & 15)) * static_cast<uint32_t>(K) * 2u;
+  const int ak = asub * 64 + chunk * 8;
+  const uint32_t aoff = arowb + ak * 2u;
+  uint8_t *const xput = lds + xrow * 128 + (chunk ^ (xrow & 7)) * 16;
+  uint8_t *const aput = lds + XB + (asub * 16 * NF + arow) * 128 + (chunk ^ (arow & 7)) * 16;
+  const int fp = wave % FP, ip = wave / FP & 1, h = wave / (2 * FP);
+  const int at = (((4 * h + g) & 7) ^ (r16 & 7)) * 16;  // this wave's 32 k, in 64 k number h / 2
+  const uint8_t *fa = lds + XB + ((h >> 1) * 16 * NF + 16 * FR * fp + r16) * 128 + at, *fx = lds + ((h >> 1) * M + 32 * ip + r16) * 128 + at;
+  f32x4 acc[FR][2];
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int buf) {
+    wait_and_sync<63>();  // this stage is in LDS; loads stay under way
+    u32x4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const u32x4 *>(fx + buf + i * 2048);
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(fa + buf + f * 2048);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[f][i] = mfma16x16x32(v, x[i], acc[f][i]);
+    }
+  };
+  const int k0 = static_cast<int>(blockIdx.y) * a.per, k1 = min(K, k0 + a.per);
+  const uint16_t *xp = xrowp + k0 + chunk * 8, *ap = a0 + k0;
+  u32x4 xv[kDeep][SUBS], av[kDeep];
+  auto load = [&](int d) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) xv[d][s] = ld16(xp + d * KS + s * 64);
+    av[d] = ld16_at(ap + d * KS, aoff);
+  };
+  auto use = [&](int d) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) *reinterpret_cast<u32x4 *>(xput + (d & 1) * STAGE + s * M * 128) = xv[d][s];
+    *reinterpret_cast<u32x4 *>(aput + (d & 1) * STAGE) = av[d];
+  };
+  // the last stages: pieces past the slice read its row's first and are zeroed on their way to LDS
+  auto load_last = [&](int k, int d) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) xv[d][s] = ld16(xrowp + (k + s * 64 + chunk * 8 < k1 ? k + s * 64 + chunk * 8 : 0));
+    av[d] = ld16_at(a0, arowb + (k + ak < k1 ? (k + ak) * 2u : 0u));
+  };
+  auto use_last = [&](int k, int d) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+      *reinterpret_cast<u32x4 *>(xput + (d & 1) * STAGE + s * M * 128) = k + s * 64 + chunk * 8 < k1 ? xv[d][s] : zero;
+    *reinterpret_cast<u32x4 *>(aput + (d & 1) * STAGE) = k + ak < k1 ? av[d] : zero;
+  };
+  const int groups = (k1 - k0) / (KS * kDeep);
+  const int kl = k0 + groups * KS * kDeep;
+  if (groups > 0) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) load(d);
+    for (int i = 1; i < groups; ++i) {
+      xp += KS * kDeep;
+      ap += KS * kDeep;
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        use(d);
+        load(d);
+        multiply((d & 1) * STAGE);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      use(d);
+      load_last(kl + d * KS, d);
+      multiply((d & 1) * STAGE);
+    }
+  } else {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) load_last(kl + d * KS, d);
+  }
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    if (kl + d * KS >= k1) break;
+    use_last(kl + d * KS, d);
+    multiply((d & 1) * STAGE);
+  }
+  // the sums along k, in wave order
+  f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [wave][FR][2][64]
+  __syncthreads();
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) part[((wave * FR + f) * 2 + i) * 64 + lane] = acc[f][i];
+  __syncthreads();
+  if (h > 0) return;
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f32x4 v = acc[f][i];
+#pragma unroll
+      for (int q = 1; q < H; ++q) v += part[(((q * 2 * FP + wave) * FR + f) * 2 + i) * 64 + lane];
+      const int tile = FR * fp + f, m = 32 * ip + 16 * i + r16;
+      if (f0 + tile >= live || m >= t.count) continue;
+      *reinterpret_cast<f32x4 *>(a.P + (blockIdx.y * a.rows + static_cast<int64_t>(blockIdx.x) * M + m) * a.R + column(tile) + g * 4) = v;
+    }
+}
+
+// 16 FRAGS of a tile's 64 tokens by 256 rows of U, 64 a wave, up to 32 CH ranks.  U
+// passes through the wave's piece of LDS into registers, where it serves the tokens,
+// 16 at a time; their sums pass through the piece again.  All of base is under way
+// from the start.
+constexpr int kExpandWaves = 4;
+
+template <int CH, int FRAGS>
+__global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a) {
+  constexpr int M = kGroupM, MW = 16 * FRAGS;
+  __shared__ int tok[M];
+  __shared__ __align__(16) uint8_t lds[kExpandWaves * kWaveLds];
+  extern __shared__ __align__(16) uint16_t zs[];  // [2][MW][pitch]
+  Tile t;
+  const int m0 = blockIdx.z * MW;
+  if (!get_tile<M>(a.s, blockIdx.x, t, tok) || m0 >= t.count) return;
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
+  const int c = child_of(a), N = a.N[c], r = a.s.r, pitch = z_pitch(r);
+  const int nw = ((static_cast<int>(blockIdx.y) - a.block0[c]) * kExpandWaves + wave) * 64;
+  const int chunks = t.slot >= 0 ? (t.rank16 + 31) / 32 : 0;
+  uint8_t *const mine = lds + wave * kWaveLds;
+  // as rows: lane -> row lane / 8 (of 8) of base and y, 8 n from 8 (lane % 8) on;
+  // row lane / 4 (of 16) of U, 8 ranks from 8 (lane % 4) on
+  const int orow = lane >> 3, ocol = (lane & 7) * 8, urow = lane >> 2, ucol = (lane & 3) * 8;
+  const uint16_t *U = a.u + (static_cast<int64_t>(max(t.slot, 0)) * a.Ntot + a.n0[c]) * r;
+  uint32_t uoff[4];  // bytes to the lanes' rows; rows past the last repeat it (not stored)
+#pragma unroll
+  for (int q = 0; q < 4; ++q) uoff[q] = static_cast<uint32_t>(max(0, min(16 * q + urow, N - 1 - nw)) * r) * 2u;
+  const uint16_t *urows = U + static_cast<int64_t>(min(nw, N - 1)) * r;
+  u32x4 un[4], u[CH][4];
+  auto load_u = [&](int chunk) {  // (ranks past the room: the row's first, masked)
+    const int k = chunk * 32 + ucol;
+    const uint32_t kb = k < r ? k * 2u : 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) un[q] = ld16_at(urows, uoff[q] + kb);
+  };
+  u32x4 b[FRAGS][2];
+  int64_t at[FRAGS][2];
+#pragma unroll
+  for (int i = 0; i < FRAGS; ++i)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int token = tok[m0 + 16 * i + 8 * q + orow];
+      at[i][q] = static_cast<int64_t>(token < 0 ? tok[0] : token) * a.Ntot + a.n0[c] + nw + ocol;
+    }
+  if (chunks) load_u(0);
+  const bool full = nw + 64 <= N;
+  if (full) {
+#pragma unroll
+    for (int i = 0; i < FRAGS; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) b[i][q] = ld16_any(a.base + at[i][q]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < FRAGS; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) b[i][q] = load_some(a.base + at[i][q], N - (nw + ocol));
+  }
+  if (chunks) {
     const float scale = a.scale[t.slot];
-    const int quads = t.rank16 / 4;
-    for (int i = threadIdx.x; i < M * quads; i += 256) {
-      const int m = i / quads, j = (i % quads) * 4;
+    const int shift = 31 - __builtin_clz(pitch - 8) - 2;  // quads of a row, a power of two
+    const int j = (threadIdx.x & ((1 << shift) - 1)) * 4;
+    const float *row0 = a.P + (static_cast<int64_t>(blockIdx.x) * M + m0) * a.R + c * r + j;
+    for (int m = threadIdx.x >> shift; m < MW; m += (kExpandWaves * 64) >> shift) {
       f32x4 v{0.f, 0.f, 0.f, 0.f};
-      if (m < t.count) {
-        const int64_t row = a.s.tiles ? static_cast<int64_t>(blockIdx.y) * M + m : tok[m];
-        const float *p = a.P + row * a.R + c * r + j;
-        for (int sl = 0; sl < a.slices; ++sl) v += *reinterpret_cast<const f32x4 *>(p + sl * a.rows * a.R);
+      if (m0 + m < t.count && j < t.rank16) {
+        const float *p = row0 + m * a.R;
+#pragma unroll 4
+        for (int s = 0; s < a.slices; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * a.rows * a.R);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? v[k] * scale : 0.f;
-      uint16_t h[4], l[4];
+      split4(v, *reinterpret_cast<u32x2 *>(zs + m * pitch + j), *reinterpret_cast<u32x2 *>(zs + (MW + m) * pitch + j));
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = f32_to_bf16(v[k]);
-        l[k] = f32_to_bf16(left_over(v[k], h[k]));
-      }
-      *reinterpret_cast<u32x2 *>(zs + m * pitch + j) = u32x2{h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
-      *reinterpret_cast<u32x2 *>(zs + (M + m) * pitch + j) = u32x2{l[0] | static_cast<uint32_t>(l[1]) << 16, l[2] | static_cast<uint32_t>(l[3]) << 16};
+    for (int ch = 0; ch < CH; ++ch) {
+      if (ch >= chunks) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x4 *>(mine + (16 * q + urow) * kUPitch + ucol * 2) = first_of_8(un[q], t.rank - (ch * 32 + ucol));
+      if (ch + 1 < CH) load_u(min(ch + 1, chunks - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[ch][j] = *reinterpret_cast<const u32x4 *>(mine + (16 * j + r16) * kUPitch + 16 * g);
     }
     __syncthreads();
   }
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  const int lrow = 8 * (r16 >> 2) + (r16 & 3);
-  for (int turn = 0; turn < a.turns; ++turn) {
-    const int nw = first + (turn * 4 + wave) * 64;
-    if (nw >= N) break;
-    // base: [token tile][half of the 64 n]
-    u32x4 b[MF][2];
-    bool whole[2];
-    int64_t at[MF];
+  if (nw >= N) return;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) whole[h] = nw + 32 * h + 8 * g + 8 <= N;
+  for (int i = 0; i < FRAGS; ++i) {
+    if (m0 + 16 * i >= t.count) break;
+    if (chunks) {
+      f32x4 acc[4];
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const int token = tok[16 * i + r16];
-      at[i] = token < 0 ? -1 : static_cast<int64_t>(token) * a.Ntot + a.n0[c] + nw + 8 * g;
+      for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        b[i][h] = zero;
-        if (token >= 0 && whole[h]) {
-          b[i][h] = ld16_any(a.base + at[i] + 32 * h);
-        } else if (token >= 0) {
-          const int lim = N - (nw + 32 * h + 8 * g);
+      for (int ch = 0; ch < CH; ++ch) {
+        if (ch >= chunks) break;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < lim) b[i][h][e / 2] |= static_cast<uint32_t>(a.base[at[i] + 32 * h + e]) << (16 * (e & 1));
+        for (int p = 0; p < 2; ++p) {
+          const u32x4 zv = ld16(zs + (p * MW + 16 * i + r16) * pitch + 32 * ch + 8 * g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma16x16x32(u[ch][j], zv, acc[j]);
         }
       }
-    }
-    if (adapted) {
-      f32x4 acc[4][MF];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(mine + r16 * kOutPitch + (16 * j + 4 * g) * 4) = acc[j];
 #pragma unroll
-        for (int i = 0; i < MF; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const uint16_t *U = a.U + (static_cast<int64_t>(t.slot) * a.Ntot + a.n0[c]) * r;
-      for (int k = 8 * g; k - 8 * g < t.rank16; k += 32) {
-        u32x4 uv[4], zv[MF][2];
-        const bool in = k < t.rank16;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = nw + 32 * (j >> 1) + lrow + 4 * (j & 1);
-          uv[j] = in && n < N ? ld16(U + static_cast<int64_t>(n) * r + k) : zero;
-        }
-        if (k + 8 > t.rank) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) uv[j] = first_of_8(uv[j], t.rank - k);
-        }
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) zv[i][h] = in ? ld16(zs + (h * M + 16 * i + r16) * pitch + k) : zero;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j][i] = mfma16x16x32(uv[j], zv[i][h], acc[j][i]);
-      }
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4 p = acc[2 * h][i], q = acc[2 * h + 1][i];
-          u32x4 &v = b[i][h];
-          v = u32x4{pack_bf16(__uint_as_float(v[0] << 16) + p[0], __uint_as_float(v[0] & 0xffff0000u) + p[1]),
-                    pack_bf16(__uint_as_float(v[1] << 16) + p[2], __uint_as_float(v[1] & 0xffff0000u) + p[3]),
-                    pack_bf16(__uint_as_float(v[2] << 16) + q[0], __uint_as_float(v[2] & 0xffff0000u) + q[1]),
-                    pack_bf16(__uint_as_float(v[3] << 16) + q[2], __uint_as_float(v[3] & 0xffff0000u) + q[3])};
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (at[i] < 0) continue;
-        if (whole[h]) {
-          st16_any(a.y + at[i] + 32 * h, b[i][h]);
-        } else {
-          const int lim = N - (nw + 32 * h + 8 * g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < lim) a.y[at[i] + 32 * h + e] = static_cast<uint16_t>(b[i][h][e / 2] >> (16 * (e & 1)));
-        }
-      }
-  }
-}
-
-// ---- backward --------------------------------------------------------------------
-// With X the values of the checkpoint, dy the gradient of y and c the scale, per
-// token z = c V^T X and g = c U^T dy, and
-//   dx = base + V g,   dU_a = sum over the slot's tokens dy z^T,   dV_a^T = sum g X^T
-// Launches: the grouping; project_kernel, z and g in float32 slices;
-// finish_kernel, their sums as pairs of bf16 in the layouts the products read;
-// gradient_kernel, dx, dU and dV.  Positions are the grouped order: tile * M + i.
-//
-// U (for g), V^T (for dx) and dy and X (for dU and dV) enter a product along
-// their slow dimension.  They come from memory as they lie, 16 bytes a lane, go
-// through a piece of LDS of the wave's own, and are transposed on the way to the
-// registers by ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 elements, and lane
-// l gets the 4 of column l.  Row 8 g + 4 h + i of 32 is kept at place 16 h + 4 g + i,
-// so that the two reads of a fragment give lane group g its contraction values
-// 8 g .. 8 g + 7 in order (what the other operand's 16-byte loads hold), each
-// from 16 places in a row; with an odd multiple of 32 bytes from place to place,
-// 8 neighbouring places lie in 8 different parts of the 256-byte bank period.
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-
-// Place of a row (any number of 32s), in rows.
-__device__ __forceinline__ int place(int row) {
-  return (row & ~31) | ((row & 4) << 2) | ((row & 24) >> 1) | (row & 3);
-}
-
-// 16 columns of rows 32 b .. 32 b + 31: lane (r16, g) gets rows 8 g .. 8 g + 7 of
-// column `r16` of those; at: byte offset of the four columns that lanes with
-// these r16 & 3 read.
-template <int PITCH>
-__device__ __forceinline__ u32x4 read_transposed(const lds_u8 *tile, int b, int at) {
-  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-  const lds_u8 *p = tile + (32 * b + 4 * g + (r16 >> 2)) * PITCH + at;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * PITCH));
-  const u32x2 x = __builtin_bit_cast(u32x2, lo), y = __builtin_bit_cast(u32x2, hi);
-  return u32x4{x[0], x[1], y[0], y[1]};
-}
-
-// Up to 8 bf16 at p, of which `left` exist.
-__device__ __forceinline__ u32x4 load_some(const uint16_t *p, int left) {
-  u32x4 v{0u, 0u, 0u, 0u};
-  if (left >= 8) return ld16_any(p);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) v[e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
-  return v;
-}
-
-struct ProjectArgs {
-  TileSource s;
-  CodedView x;          // the checkpoint
-  const uint16_t *vt;   // [n][nchild * r][K]
-  const uint16_t *dy;   // [T][Ntot]
-  const uint16_t *u;    // [n][Ntot][r]
-  int32_t K, Ntot, nchild, N[kMaxChildren], n0[kMaxChildren];
-  int32_t R;            // nchild * r
-  int64_t rows;
-  int32_t zgroups, zslices, zper;  // z: groups of NF row tiles, K slices, steps of each (zslices 0: no z)
-  int32_t ggroups, gslices, gper;  // g: groups of NF row tiles of a child, slices of N, steps of each
-  float *Pz, *Pg;       // [slices][rows][R]
-};
-
-constexpr int kM = 32, kMF = 2;  // tokens of a tile in the backward pass
-
-// The waves' sums of a tile meet in LDS; wave 0 stores them.
-template <int NF>
-__device__ __forceinline__ void store_thin(const f32x4 (&acc)[NF][kMF], f32x4 *part, const int (&col)[NF], int live, int count,
-                                           float *P, int64_t row0, int R) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  __syncthreads();
-  if (wave > 0) {
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-#pragma unroll
-      for (int i = 0; i < kMF; ++i) part[((wave - 1) * NF * kMF + f * kMF + i) * 64 + lane] = acc[f][i];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < kMF; ++i) {
-      f32x4 v = acc[f][i];
-#pragma unroll
-      for (int w = 0; w < 3; ++w) v += part[(w * NF * kMF + f * kMF + i) * 64 + lane];
-      if (f < live && 16 * i + r16 < count) *reinterpret_cast<f32x4 *>(P + (row0 + 16 * i + r16) * R + col[f] + g * 4) = v;
-    }
-}
-
-template <int NF>
-__global__ __launch_bounds__(256) void project_kernel(ProjectArgs a) {
-  constexpr int PITCH = 32 * (NF | 1), ROWS = NF == 8 ? 32 : 64, B = ROWS / 32;  // g: a wave's piece of U
-  constexpr int PART = 3 * NF * kMF * 1024, PIECES = 4 * ROWS * PITCH;
-  __shared__ int tok[kM];
-  __shared__ __align__(16) uint8_t lds[PART > PIECES ? PART : PIECES];
-  Tile t;
-  if (!get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int per_child = t.rank16 / 16;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kM;
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  f32x4 acc[NF][kMF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < kMF; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int token[kMF], col[NF];
-#pragma unroll
-  for (int i = 0; i < kMF; ++i) token[i] = tok[16 * i + r16];
-  int unit = blockIdx.y;
-  const int zunits = a.zgroups * a.zslices;
-  if (unit < zunits) {
-    const int f0 = unit % a.zgroups * NF, slice = unit / a.zgroups, live = a.nchild * per_child - f0;
-    if (live <= 0) return;
-    const uint16_t *ar[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const int v = f0 + min(f, live - 1);
-      col[f] = v / per_child * a.s.r + v % per_child * 16;
-      ar[f] = a.vt + (static_cast<int64_t>(t.slot) * a.R + col[f] + r16) * a.K;
-    }
-    const int end = min((a.K + 63) / 64, (slice + 1) * a.zper);
-    u32x4 xv[2][kMF][2], av[2][NF][2];
-    auto load = [&](int step, u32x4(&xo)[kMF][2], u32x4(&ao)[NF][2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = step * 64 + g * 16 + h * 8;
-        const bool in = step < end && k < a.K;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) ao[f][h] = in ? ld16(ar[f] + k) : zero;
-#pragma unroll
-        for (int i = 0; i < kMF; ++i) xo[i][h] = in && token[i] >= 0 ? expand8(a.x, token[i], k) : zero;
-      }
-    };
-    auto multiply = [&](const u32x4(&xo)[kMF][2], const u32x4(&ao)[NF][2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-#pragma unroll
-          for (int i = 0; i < kMF; ++i) acc[f][i] = mfma16x16x32(ao[f][h], xo[i][h], acc[f][i]);
-    };
-    int step = slice * a.zper + wave;
-    load(step, xv[0], av[0]);
-    for (; step < end; step += 8) {
-      load(step + 4, xv[1], av[1]);
-      multiply(xv[0], av[0]);
-      load(step + 8, xv[0], av[0]);
-      multiply(xv[1], av[1]);
-    }
-    store_thin<NF>(acc, reinterpret_cast<f32x4 *>(lds), col, live, t.count, a.Pz + slice * a.rows * a.R, row0, a.R);
-    return;
-  }
-  unit -= zunits;
-  const int c = unit % a.nchild, j0 = unit / a.nchild % a.ggroups * NF * 16, slice = unit / a.nchild / a.ggroups;
-  const int live = per_child - j0 / 16, N = a.N[c];
-  if (live <= 0) return;
-#pragma unroll
-  for (int f = 0; f < NF; ++f) col[f] = c * a.s.r + j0 + 16 * f;
-  const uint16_t *U = a.u + (static_cast<int64_t>(t.slot) * a.Ntot + a.n0[c]) * a.s.r + j0;
-  lds_u8 *piece = (lds_u8 *)lds + wave * (ROWS * PITCH);
-  const int end = min((N + ROWS - 1) / ROWS, (slice + 1) * a.gper);
-  constexpr int Q = ROWS * 2 * NF / 64;  // 16-byte loads of U a step and lane
-  u32x4 uv[Q], dv[kMF][B];
-  auto load = [&](int step) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int v = q * 64 + lane, row = step * ROWS + v / (2 * NF), j = v % (2 * NF) * 8;
-      uv[q] = step < end && row < N && j0 + j < a.s.r ? ld16(U + static_cast<int64_t>(row) * a.s.r + j) : zero;
-    }
-#pragma unroll
-    for (int i = 0; i < kMF; ++i)
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const int n = step * ROWS + 32 * b + 8 * g;
-        dv[i][b] = zero;
-        if (step < end && token[i] >= 0 && n < N)
-          dv[i][b] = load_some(a.dy + static_cast<int64_t>(token[i]) * a.Ntot + a.n0[c] + n, N - n);
-      }
-  };
-  int step = slice * a.gper + wave;
-  load(step);
-  for (; step < end; step += 4) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int v = q * 64 + lane;
-      *(lds_u32x4 *)(piece + place(v / (2 * NF)) * PITCH + v % (2 * NF) * 16) = uv[q];
-    }
-    u32x4 d[kMF][B];
-#pragma unroll
-    for (int i = 0; i < kMF; ++i)
-#pragma unroll
-      for (int b = 0; b < B; ++b) d[i][b] = dv[i][b];
-    load(step + 4);
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const u32x4 av = read_transposed<PITCH>(piece, b, 32 * f + 8 * (r16 & 3));
-#pragma unroll
-        for (int i = 0; i < kMF; ++i) acc[f][i] = mfma16x16x32(av, d[i][b], acc[f][i]);
-      }
-  }
-  store_thin<NF>(acc, reinterpret_cast<f32x4 *>(lds), col, live, t.count, a.Pg + slice * a.rows * a.R, row0, a.R);
-}
-
-// z and g summed over their slices, times c, as pairs of bf16: transposed [2][R][rows]
-// (dU, dV) and, for g, as rows [rows][2][R] (dx).  Columns past the slot's rank
-// and positions behind the tile's tokens are zeros.
-struct FinishArgs {
-  TileSource s;
-  const float *scale;
-  const float *P[2];     // z, g
-  int32_t slices[2];     // 0: not wanted
-  int32_t R;
-  int64_t rows;
-  uint16_t *T[2];        // [2][R][rows]
-  uint16_t *grows;       // [rows][2][R]
-};
-
-__global__ __launch_bounds__(256) void finish_kernel(FinishArgs a) {
-  __shared__ int tok[kM];
-  __shared__ uint16_t pair[2][32][kM + 2];
-  Tile t;
-  const int which = blockIdx.z;
-  if (!a.slices[which] || !get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kM;
-  const float scale = a.scale[t.slot];
-  const int j0 = blockIdx.y * 32, l = threadIdx.x & 31;
-  const int j = j0 + l;
-#pragma unroll
-  for (int m = threadIdx.x >> 5; m < kM; m += 8) {
-    float v = 0.f;
-    if (j < a.R && m < t.count && j % a.s.r < t.rank) {
-      const float *p = a.P[which] + (row0 + m) * a.R + j;
-      for (int s = 0; s < a.slices[which]; ++s) v += p[s * a.rows * a.R];
-      v *= scale;
-    }
-    const uint16_t h = f32_to_bf16(v), lo = f32_to_bf16(left_over(v, h));
-    pair[0][l][m] = h;
-    pair[1][l][m] = lo;
-    if (which == 1 && a.grows && j < a.R) {
-      a.grows[(row0 + m) * 2 * a.R + j] = h;
-      a.grows[((row0 + m) * 2 + 1) * a.R + j] = lo;
-    }
-  }
-  if (!a.T[which]) return;
-  __syncthreads();
-  // 32 rows of 32 positions, twice; 4 positions a thread
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = threadIdx.x >> 3, m = (threadIdx.x & 7) * 4;
-    if (j0 + row >= a.R) continue;
-    const uint16_t *p = &pair[i][row][m];
-    *reinterpret_cast<u32x2 *>(a.T[which] + (static_cast<int64_t>(i) * a.R + j0 + row) * a.rows + row0 + m) =
-        u32x2{p[0] | static_cast<uint32_t>(p[1]) << 16, p[2] | static_cast<uint32_t>(p[3]) << 16};
-  }
-}
-
-struct GradArgs {
-  TileSource s;
-  const int32_t *first, *count;  // per slot: first tile, tokens
-  CodedView x;
-  const uint16_t *vt, *dy;
-  const uint16_t *zT, *gT, *grows;
-  int32_t K, Ntot, nchild, N[kMaxChildren], n0[kMaxChildren];
-  int32_t R;
-  int64_t rows;
-  const uint16_t *base;
-  uint16_t *dx, *du, *dv;
-  // workgroups: dx [tiles][K blocks of 256], then dU and dV [slots][column tiles
-  // of 64][groups of 16 JF ranks]
-  int32_t tiles, kblocks;
-  int32_t jgroups;              // groups of ranks of a child
-  int32_t ublock0[kMaxChildren + 1], vblocks;  // column tiles of the children's rows (running), of K
-  int64_t units[3];             // dx, dU, dV
-};
-
-// dx of one tile: a wave takes 64 k.  V^T rows of 32 ranks at a time go through
-// the wave's piece of LDS.
-__device__ __forceinline__ void dx_unit(const GradArgs &a, int id, uint8_t *lds, int *tok) {
-  Tile t;
-  if (!get_tile<kM>(a.s, id / a.kblocks, t, tok)) return;
-  constexpr int PITCH = 160;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int k0 = (id % a.kblocks * 4 + wave) * 64;
-  if (k0 >= a.K) return;
-  lds_u8 *piece = (lds_u8 *)lds + wave * (32 * PITCH);
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  u32x4 b[kMF][2];
-  int64_t at[kMF];
-#pragma unroll
-  for (int i = 0; i < kMF; ++i) {
-    const int token = tok[16 * i + r16];
-    at[i] = token < 0 ? -1 : static_cast<int64_t>(token) * a.K + k0 + 8 * g;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      b[i][h] = token >= 0 && k0 + 32 * h + 8 * g < a.K ? ld16(a.base + at[i] + 32 * h) : zero;
-  }
-  if (t.slot >= 0) {
-    f32x4 acc[4][kMF];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < kMF; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int64_t row0 = static_cast<int64_t>(id / a.kblocks) * kM;
-    const int chunks = (t.rank16 + 31) / 32, steps = a.nchild * chunks;
-    u32x4 vv[4], gv[kMF][2];
-    auto load = [&](int step) {
-      const int j0 = step % chunks * 32, c0 = step / chunks * a.s.r;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = q * 8 + (lane >> 3), k = k0 + (lane & 7) * 8;
-        vv[q] = step < steps && j0 + row < t.rank && k < a.K
-                    ? ld16(a.vt + (static_cast<int64_t>(t.slot) * a.R + c0 + j0 + row) * a.K + k) : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < kMF; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          gv[i][h] = step < steps && j0 + 8 * g < t.rank16
-                         ? ld16(a.grows + ((row0 + 16 * i + r16) * 2 + h) * a.R + c0 + j0 + 8 * g) : zero;
-    };
-    load(0);
-    for (int step = 0; step < steps; ++step) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) *(lds_u32x4 *)(piece + place(q * 8 + (lane >> 3)) * PITCH + (lane & 7) * 16) = vv[q];
-      u32x4 gg[kMF][2];
-#pragma unroll
-      for (int i = 0; i < kMF; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) gg[i][h] = gv[i][h];
-      load(step + 1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const u32x4 av = read_transposed<PITCH>(piece, 0, 64 * (j >> 1) + 16 * (r16 & 3) + 8 * (j & 1));
-#pragma unroll
-        for (int i = 0; i < kMF; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) acc[j][i] = mfma16x16x32(av, gg[i][h], acc[j][i]);
+      for (int q = 0; q < 2; ++q) {
+        const f32x4 *o = reinterpret_cast<const f32x4 *>(mine + (8 * q + orow) * kOutPitch + ocol * 4);
+        b[i][q] = add_8(b[i][q], o[0], o[1]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kMF; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 p = acc[2 * h][i], q = acc[2 * h + 1][i];
-        u32x4 &v = b[i][h];
-        v = u32x4{pack_bf16(__uint_as_float(v[0] << 16) + p[0], __uint_as_float(v[0] & 0xffff0000u) + p[1]),
-                  pack_bf16(__uint_as_float(v[1] << 16) + p[2], __uint_as_float(v[1] & 0xffff0000u) + p[3]),
-                  pack_bf16(__uint_as_float(v[2] << 16) + q[0], __uint_as_float(v[2] & 0xffff0000u) + q[1]),
-                  pack_bf16(__uint_as_float(v[3] << 16) + q[2], __uint_as_float(v[3] & 0xffff0000u) + q[3])};
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < kMF; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (at[i] >= 0 && k0 + 32 * h + 8 * g < a.K) *reinterpret_cast<u32x4 *>(a.dx + at[i] + 32 * h) = b[i][h];
-}
-
-// 64 columns of dy (VGRAD false: dU) or of X (dV) by 16 JF ranks of one slot: the
-// sum over its tokens, 32 at a time, taken in turn by the four waves.
-template <int JF, bool VGRAD>
-__device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds) {
-  constexpr int PITCH = 160;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int r = a.s.r;
-  // column tiles fastest: the tiles of a slot run together
-  const int ctiles = VGRAD ? a.nchild * a.vblocks : a.ublock0[a.nchild];
-  int ct = static_cast<int>(id % ctiles);
-  const int64_t rest = id / ctiles;
-  const int j0 = static_cast<int>(rest % a.jgroups) * JF * 16, slot = static_cast<int>(rest / a.jgroups);
-  int c = 0;
-  if constexpr (VGRAD) {
-    c = ct / a.vblocks;
-    ct %= a.vblocks;
-  } else {
-#pragma unroll
-    for (int i = 1; i < kMaxChildren; ++i)
-      if (i < a.nchild && ct >= a.ublock0[i]) c = i;
-    ct -= a.ublock0[c];
-  }
-  const int col0 = ct * 64, cols = VGRAD ? a.K : a.N[c];
-  const int count = a.count[slot];
-  const int64_t pos0 = static_cast<int64_t>(a.first[slot]) * kM;
-  const int32_t *perm = a.s.perm + pos0;
-  lds_u8 *piece = (lds_u8 *)lds + wave * (32 * PITCH);
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  // the thin operand, from column c * r + j0 of z (dU) or g (dV) on
-  const uint16_t *thin = (VGRAD ? a.gT : a.zT) + (static_cast<int64_t>(c) * r + j0) * a.rows + pos0;
-  const int64_t lo = static_cast<int64_t>(a.R) * a.rows;
-  f32x4 acc[4][JF];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int f = 0; f < JF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int steps = (count + 31) / 32;
-  u32x4 wv[4], tv[JF][2];
-  int token[4];  // of the step after the one in wv
-  auto tokens = [&](int step) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) token[q] = step < steps ? perm[step * 32 + q * 8 + (lane >> 3)] : -1;
-  };
-  auto load = [&](int step) {
-    const int k = col0 + (lane & 7) * 8;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      wv[q] = zero;
-      if (token[q] >= 0 && k < cols) {
-        if constexpr (VGRAD)
-          wv[q] = expand8(a.x, token[q], k);
-        else
-          wv[q] = load_some(a.dy + static_cast<int64_t>(token[q]) * a.Ntot + a.n0[c] + k, cols - k);
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < JF; ++f)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        tv[f][h] = step < steps && j0 + 16 * f < r ? ld16(thin + h * lo + (16 * f + r16) * a.rows + step * 32 + 8 * g) : zero;
-  };
-  tokens(wave);
-  load(wave);
-  tokens(wave + 4);
-  for (int step = wave; step < steps; step += 4) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) *(lds_u32x4 *)(piece + place(q * 8 + (lane >> 3)) * PITCH + (lane & 7) * 16) = wv[q];
-    u32x4 tt[JF][2];
-#pragma unroll
-    for (int f = 0; f < JF; ++f)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tt[f][h] = tv[f][h];
-    load(step + 4);
-    tokens(step + 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // dV: 8 neighbouring k of a row end up in two accumulators of a lane
-      const u32x4 w = read_transposed<PITCH>(piece, 0, VGRAD ? 64 * (i >> 1) + 16 * (r16 & 3) + 8 * (i & 1) : 32 * i + 8 * (r16 & 3));
-#pragma unroll
-      for (int f = 0; f < JF; ++f)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[i][f] = VGRAD ? mfma16x16x32(w, tt[f][h], acc[i][f]) : mfma16x16x32(tt[f][h], w, acc[i][f]);
+    for (int q = 0; q < 2; ++q) {
+      if (m0 + 16 * i + 8 * q + orow >= t.count) continue;
+      if (full)
+        st16_any(a.y + at[i][q], b[i][q]);
+      else
+        store_some(a.y + at[i][q], b[i][q], N - (nw + ocol));
     }
   }
-  // the waves' sums: two rank tiles at a time through LDS, in wave order
-  constexpr int JC = JF < 2 ? JF : 2;
-  f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [4 waves][4 column tiles][JC][64]
-  for (int f0 = 0; f0 < JF; f0 += JC) {
-    __syncthreads();
-#pragma unroll
-    for (int f = 0; f < JF; ++f)
-      if (f >= f0 && f < f0 + JC)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[((wave * 4 + i) * JC + f - f0) * 64 + lane] = acc[i][f];
-    __syncthreads();
-    const int f = f0 + (wave >> 1);
-    if ((wave >> 1) >= JC || j0 + 16 * f >= r) continue;
-    f32x4 s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 *p = part + ((2 * (wave & 1) + h) * JC + (wave >> 1)) * 64 + lane;
-      s[h] = p[0];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) s[h] += p[w * 4 * JC * 64];
-    }
-    if constexpr (VGRAD) {
-      const int k = col0 + 32 * (wave & 1) + 8 * g, j = c * r + j0 + 16 * f + r16;
-      if (k < a.K)
-        *reinterpret_cast<u32x4 *>(a.dv + (static_cast<int64_t>(slot) * a.R + j) * a.K + k) =
-            u32x4{pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = col0 + 16 * (2 * (wave & 1) + h) + r16;
-        if (n < cols)
-          *reinterpret_cast<u32x2 *>(a.du + (static_cast<int64_t>(slot) * a.Ntot + a.n0[c] + n) * r + j0 + 16 * f + 4 * g) =
-              u32x2{pack_bf16(s[h][0], s[h][1]), pack_bf16(s[h][2], s[h][3])};
-      }
-    }
-  }
-}
-
-template <int JF>
-__global__ __launch_bounds__(256) void gradient_kernel(GradArgs a) {
-  constexpr int SUM = 4 * 4 * (JF < 2 ? JF : 2) * 1024, PIECES = 4 * 32 * 160;
-  __shared__ int tok[kM];
-  __shared__ __align__(16) uint8_t lds[SUM > PIECES ? SUM : PIECES];
-  int64_t id = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-  if (id >= a.units[0] + a.units[1] + a.units[2]) return;
-  if (id < a.units[0]) return dx_unit(a, static_cast<int>(id), lds, tok);
-  id -= a.units[0];
-  if (id < a.units[1]) return weight_unit<JF, false>(a, id, lds);
-  weight_unit<JF, true>(a, id - a.units[1], lds);
-}
-
-__global__ __launch_bounds__(256) void fill_zero_16(u32x4 *p, int64_t n) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
-    p[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
 // ---- plan ----------------------------------------------------------------------
-
-constexpr int kGroupMF = 2;  // token fragments of a tile of a grouped call
+constexpr int kMaxSlices = 6;
 
 struct Plan {
   bool grouped;
-  int M, tiles;          // tokens of a tile, most tiles there can be
-  int NF, zgroups;       // thin: 16-row tiles of a workgroup, workgroups for all rows
-  int slices, per;
-  int64_t rows;          // rows of P
-  size_t tiles_at, perm_at, p_at, bytes;
+  int tiles;          // most tiles there can be
+  int blocks, turns;  // workgroups along the children's rows, turns of a wave
+  int across;         // rows of a workgroup
+  int NF, zgroups, slices, per, frags;
+  int64_t rows;
+  size_t perm_at, p_at, bytes;
 };
-
-size_t align256(size_t n) { return (n + 255) & ~size_t{255}; }
 
 Plan make_plan(const AdapterPool &p, int T) {
   Plan q{};
   q.grouped = T > kLeaderT;
-  q.M = q.grouped ? 16 * kGroupMF : kLeaderM;
-  q.tiles = q.grouped ? T / q.M + std::min(p.n + 1, T) : T;
-  const int row_tiles = p.nchild * p.r / 16;
-  q.NF = row_tiles >= 8 ? 8 : row_tiles >= 3 ? 4 : row_tiles;
+  q.turns = 1;
+  auto count_blocks = [&](int across) {
+    q.across = across;
+    q.blocks = 0;
+    for (int c = 0; c < p.nchild; ++c) q.blocks += (p.N[c] + across - 1) / across;
+  };
+  if (!q.grouped) {
+    // (a token's workgroups on one XCD: they read the same V^T)
+    q.tiles = T < 8 ? T : tile_places(T);
+    // A workgroup for each CU, or two where they fit and have enough to walk over: 4
+    // tokens through 2 x 21504 rows at rank 16 in 168 workgroups 7.3 us, in 336 10.0;
+    // 64 tokens in 228 workgroups 30.0, in 456 27.8.
+    count_blocks(kThreads);
+    const int64_t all = static_cast<int64_t>(q.blocks) * T;
+    q.turns = static_cast<int>((all + kCUs - 1) / kCUs);
+    if (p.r == 16 && q.turns > 8) q.turns = static_cast<int>((all + 2 * kCUs - 1) / (2 * kCUs));
+    count_blocks(kThreads * q.turns);
+    q.bytes = 256;
+    return q;
+  }
+  count_blocks(kExpandWaves * 64);
+  q.tiles = tile_places(T / kGroupM + std::min(p.n + 1, T));
+  const int busy = (T + kGroupM - 1) / kGroupM, row_tiles = p.nchild * p.r / 16;
+  q.NF = row_tiles >= 3 ? 4 : row_tiles;
   q.zgroups = (row_tiles + q.NF - 1) / q.NF;
-  // K slices until the workgroups fill the CUs a few times over, none shorter
-  // than a step for each wave
-  const int steps = (p.K + 63) / 64;
-  const int busy = (q.grouped ? (T + q.M - 1) / q.M : T) * q.zgroups;
-  int want = std::min({8, (4 * kCUs + busy - 1) / busy, (steps + 3) / 4});
-  q.per = (steps + want - 1) / want;
-  q.slices = (steps + q.per - 1) / q.per;
-  q.rows = q.grouped ? static_cast<int64_t>(q.tiles) * q.M : T;
-  q.tiles_at = 256;  // ntiles first
-  q.perm_at = q.tiles_at + (q.grouped ? align256(sizeof(int2) * q.tiles) : 0);
-  q.p_at = q.perm_at + (q.grouped ? align256(sizeof(int32_t) * q.rows) : 0);
+  // Four fragments of tokens serve a workgroup's rows of U, one where the tiles are too
+  // few to fill the CUs (333 tokens through 1001 rows: 5.1 us, with four 10.5).
+  q.frags = static_cast<int64_t>(q.blocks) * busy >= 2 * kCUs ? 4 : 1;
+  // K slices until there are some workgroups for every CU
+  const int stage = q.NF == 4 ? 64 : 128, stages = (p.K + stage - 1) / stage;
+  const int want = std::max(1, std::min({kMaxSlices, (3 * kCUs / 2 + busy * q.zgroups - 1) / (busy * q.zgroups), stages / kDeep}));
+  q.per = (stages + want - 1) / want * stage;
+  q.slices = (p.K + q.per - 1) / q.per;
+  q.rows = static_cast<int64_t>(q.tiles) * kGroupM;
+  q.perm_at = align256(sizeof(int4) * q.tiles);  // the tiles come first
+  q.p_at = q.perm_at + align256(sizeof(int32_t) * q.rows);
   q.bytes = q.p_at + align256(sizeof(float) * q.slices * q.rows * p.nchild * p.r);
   return q;
 }
 
-struct BackPlan {
-  int tiles, NF, zgroups, zslices, zper, ggroups, gslices, gper;
-  int64_t rows;
-  size_t perm_at, slots_at, pz_at, pg_at, zt_at, gt_at, grows_at, bytes;
-};
-
-BackPlan make_back_plan(const AdapterPool &p, int T) {
-  BackPlan q{};
-  q.tiles = T / kM + std::min(p.n + 1, T);
-  q.rows = static_cast<int64_t>(q.tiles) * kM;
-  const int row_tiles = p.r / 16, R = p.nchild * p.r;
-  q.NF = row_tiles >= 8 ? 8 : row_tiles >= 3 ? 4 : row_tiles;
-  q.zgroups = (p.nchild * row_tiles + q.NF - 1) / q.NF;
-  q.ggroups = (row_tiles + q.NF - 1) / q.NF;
-  int widest = 0;
-  for (int c = 0; c < p.nchild; ++c) widest = std::max(widest, p.N[c]);
-  const int zsteps = (p.K + 63) / 64, rows = q.NF == 8 ? 32 : 64, gsteps = (widest + rows - 1) / rows;
-  const int busy = (T + kM - 1) / kM;
-  auto cut = [&](int steps, int workgroups, int &slices, int &per) {
-    const int want = std::min({8, (4 * kCUs + workgroups - 1) / workgroups, (steps + 3) / 4});
-    per = (steps + want - 1) / want;
-    slices = (steps + per - 1) / per;
-  };
-  cut(zsteps, busy * q.zgroups, q.zslices, q.zper);
-  cut(gsteps, busy * q.ggroups * p.nchild, q.gslices, q.gper);
-  size_t at = 256 + align256(sizeof(int2) * q.tiles);
-  auto take = [&](size_t bytes) {
-    const size_t here = at;
-    at += align256(bytes);
-    return here;
-  };
-  q.perm_at = take(sizeof(int32_t) * q.rows);
-  q.slots_at = take(2 * sizeof(int32_t) * p.n);
-  q.pz_at = take(sizeof(float) * q.zslices * q.rows * R);
-  q.pg_at = take(sizeof(float) * q.gslices * q.rows * R);
-  q.zt_at = take(2 * sizeof(uint16_t) * q.rows * R);
-  q.gt_at = take(2 * sizeof(uint16_t) * q.rows * R);
-  q.grows_at = take(2 * sizeof(uint16_t) * q.rows * R);
-  q.bytes = at;
-  return q;
+template <int CH, int FRAGS>
+hipError_t launch_expand(const AdapterArgs &a, const Plan &q, hipStream_t stream) {
+  constexpr size_t lds = sizeof(uint16_t) * 2 * 16 * FRAGS * z_pitch(32 * CH);
+  const hipError_t e = ensure_lds<expand_kernel<CH, FRAGS>>(lds);
+  if (e != hipSuccess) return e;
+  expand_kernel<CH, FRAGS><<<dim3(q.tiles, q.blocks, kGroupM / (16 * FRAGS)), kExpandWaves * 64, lds, stream>>>(a);
+  return hipGetLastError();
 }
 
-template <int MF>
-hipError_t launch_thin(const ThinArgs &a, const Plan &q, hipStream_t stream) {
-  const dim3 grid(q.tiles, q.slices, q.zgroups);
-  switch (q.NF) {
-    case 1: thin_kernel<MF, 1><<<grid, 256, 0, stream>>>(a); break;
-    case 2: thin_kernel<MF, 2><<<grid, 256, 0, stream>>>(a); break;
-    case 4: thin_kernel<MF, 4><<<grid, 256, 0, stream>>>(a); break;
-    default: thin_kernel<MF, 8><<<grid, 256, 0, stream>>>(a); break;
-  }
-  return hipGetLastError();
+template <int FRAGS>
+hipError_t launch_expand(const AdapterArgs &a, const Plan &q, hipStream_t stream) {
+  if (a.s.r <= 32) return launch_expand<1, FRAGS>(a, q, stream);
+  if (a.s.r <= 64) return launch_expand<2, FRAGS>(a, q, stream);
+  if (a.s.r <= 128) return launch_expand<4, FRAGS>(a, q, stream);
+  return launch_expand<8, FRAGS>(a, q, stream);
 }
 
 }  // namespace
@@ -1068,201 +849,66 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
                            uint16_t *y, void *ws, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const Plan q = make_plan(p, T);
-  uint8_t *w = static_cast<uint8_t *>(ws);
-  TileSource s{};
-  s.index = index;
-  s.rank = p.rank;
-  s.T = T;
-  s.n = p.n;
-  s.r = p.r;
-  s.copies = base != y;
-  hipError_t e = hipSuccess;
-  if (q.grouped) {
-    GroupArgs g{};
-    g.s = s;
-    g.ntiles = reinterpret_cast<int32_t *>(w);
-    g.tiles = reinterpret_cast<int2 *>(w + q.tiles_at);
-    g.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
-    group_kernel<16 * kGroupMF><<<(p.n + 4) / 4, 256, 0, stream>>>(g);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    s.tiles = g.tiles;
-    s.ntiles = g.ntiles;
-    s.perm = g.perm;
-  }
-  ThinArgs t{};
-  t.s = s;
-  t.x = x;
-  t.A = p.vt;
-  t.K = p.K;
-  t.nchild = p.nchild;
-  t.slices = q.slices;
-  t.per = q.per;
-  t.P = reinterpret_cast<float *>(w + q.p_at);
-  t.R = p.nchild * p.r;
-  t.rows = q.rows;
-  e = q.grouped ? launch_thin<kGroupMF>(t, q, stream) : launch_thin<1>(t, q, stream);
-  if (e != hipSuccess) return e;
-  ExpandArgs a{};
-  a.s = s;
-  a.P = t.P;
-  a.slices = q.slices;
-  a.R = t.R;
-  a.rows = q.rows;
-  a.scale = p.scale;
-  a.U = p.u;
-  a.base = base;
-  a.y = y;
-  a.Ntot = p.Ntot;
-  a.nchild = p.nchild;
-  int blocks = 0;
-  for (int c = 0; c < p.nchild; ++c) blocks += (p.N[c] + 255) / 256;
-  const int busy = q.grouped ? (T + q.M - 1) / q.M : T;
-  a.turns = std::max(1, std::min<int>(8, static_cast<int>(static_cast<int64_t>(blocks) * busy / (8 * kCUs))));
-  blocks = 0;
-  for (int c = 0, n0 = 0; c < p.nchild; ++c) {
-    a.N[c] = p.N[c];
-    a.n0[c] = n0;
-    a.block0[c] = blocks;
-    blocks += (p.N[c] + 256 * a.turns - 1) / (256 * a.turns);
-    n0 += p.N[c];
-  }
-  const dim3 grid(blocks, q.tiles);
-  const size_t lds = sizeof(uint16_t) * 2 * q.M * (p.r + 8);
-  if (q.grouped)
-    expand_kernel<kGroupMF><<<grid, 256, lds, stream>>>(a);
-  else
-    expand_kernel<1><<<grid, 256, lds, stream>>>(a);
-  return hipGetLastError();
-}
-
-size_t adapters_backward_workspace_bytes(const AdapterPool &p, int T) { return T > 0 ? make_back_plan(p, T).bytes : 256; }
-
-hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, const uint16_t *dy, const int32_t *index, int T,
-                                    const AdapterGrads &o, void *ws, hipStream_t stream) {
-  const size_t ub = static_cast<size_t>(p.n) * p.Ntot * p.r * 2, vb = static_cast<size_t>(p.n) * p.nchild * p.r * p.K * 2;
-  if (T == 0) {
-    if (!o.du && !o.dv) return hipSuccess;
-    auto clear = [&](uint16_t *out, size_t bytes) {
-      const int64_t n = static_cast<int64_t>(bytes / 16);
-      if (out) fill_zero_16<<<static_cast<uint32_t>(std::min<int64_t>((n + 255) / 256, 8 * kCUs)), 256, 0, stream>>>(reinterpret_cast<u32x4 *>(out), n);
-    };
-    clear(o.du, ub);
-    clear(o.dv, vb);
-    return hipGetLastError();
-  }
-  const BackPlan q = make_back_plan(p, T);
-  const bool want_z = o.du, want_g = o.dx || o.dv;
-  uint8_t *w = static_cast<uint8_t *>(ws);
-  TileSource s{};
-  s.index = index;
-  s.rank = p.rank;
-  s.T = T;
-  s.n = p.n;
-  s.r = p.r;
-  s.copies = o.dx && o.dx != o.base;
-  GroupArgs gr{};
-  gr.s = s;
-  gr.ntiles = reinterpret_cast<int32_t *>(w);
-  gr.tiles = reinterpret_cast<int2 *>(w + 256);
-  gr.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
-  gr.first = reinterpret_cast<int32_t *>(w + q.slots_at);
-  gr.count = gr.first + p.n;
-  group_kernel<kM><<<(p.n + 4) / 4, 256, 0, stream>>>(gr);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  s.tiles = gr.tiles;
-  s.ntiles = gr.ntiles;
-  s.perm = gr.perm;
-  const int R = p.nchild * p.r;
-  ProjectArgs a{};
-  a.s = s;
+  AdapterArgs a{};
+  a.s.index = index;
+  a.s.rank = p.rank;
+  a.s.T = T;
+  a.s.n = p.n;
+  a.s.r = p.r;
+  a.s.copies = base != y;
   a.x = x;
   a.vt = p.vt;
-  a.dy = dy;
   a.u = p.u;
+  a.scale = p.scale;
+  a.base = base;
+  a.y = y;
+  a.R = p.nchild * p.r;
   a.K = p.K;
   a.Ntot = p.Ntot;
   a.nchild = p.nchild;
-  for (int c = 0, n0 = 0; c < p.nchild; ++c) {
+  a.turns = q.turns;
+  for (int c = 0, n0 = 0, b0 = 0; c < p.nchild; ++c) {
     a.N[c] = p.N[c];
     a.n0[c] = n0;
+    a.block0[c] = b0;
     n0 += p.N[c];
+    b0 += (p.N[c] + q.across - 1) / q.across;
   }
-  a.R = R;
+  if (!q.grouped) {
+    const dim3 grid(q.tiles, q.blocks);
+    const size_t lds = sizeof(uint16_t) * 2 * kTileM * z_pitch(p.r);
+    if (p.r == 16)
+      few_kernel<16><<<grid, kThreads, lds, stream>>>(a);
+    else if (p.r <= 64)
+      few_kernel<64><<<grid, kThreads, lds, stream>>>(a);
+    else
+      few_kernel<256><<<grid, kThreads, lds, stream>>>(a);
+    return hipGetLastError();
+  }
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  a.s.max_tiles = q.tiles;
+  GroupArgs g{};
+  g.s = a.s;
+  g.tiles = reinterpret_cast<int4 *>(w);
+  g.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
+  group_kernel<kGroupM><<<group_workgroups(p.n), kGroupWaves * 64, 0, stream>>>(g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.s.tiles = g.tiles;
+  a.s.perm = g.perm;
+  a.P = reinterpret_cast<float *>(w + q.p_at);
   a.rows = q.rows;
-  a.zgroups = q.zgroups;
-  a.zslices = want_z ? q.zslices : 0;
-  a.zper = q.zper;
-  a.ggroups = q.ggroups;
-  a.gslices = want_g ? q.gslices : 0;
-  a.gper = q.gper;
-  a.Pz = reinterpret_cast<float *>(w + q.pz_at);
-  a.Pg = reinterpret_cast<float *>(w + q.pg_at);
-  const dim3 grid(q.tiles, a.zgroups * a.zslices + a.ggroups * p.nchild * a.gslices);
-  switch (q.NF) {
-    case 1: project_kernel<1><<<grid, 256, 0, stream>>>(a); break;
-    case 2: project_kernel<2><<<grid, 256, 0, stream>>>(a); break;
-    case 4: project_kernel<4><<<grid, 256, 0, stream>>>(a); break;
-    default: project_kernel<8><<<grid, 256, 0, stream>>>(a); break;
-  }
+  a.slices = q.slices;
+  a.per = q.per;
+  const dim3 thin(q.tiles, q.slices, q.zgroups);
+  if (q.NF == 1)
+    thin_kernel<1><<<thin, kThreads, 0, stream>>>(a);
+  else if (q.NF == 2)
+    thin_kernel<2><<<thin, kThreads, 0, stream>>>(a);
+  else
+    thin_kernel<4><<<thin, kThreads, 0, stream>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  FinishArgs f{};
-  f.s = s;
-  f.scale = p.scale;
-  f.P[0] = a.Pz;
-  f.P[1] = a.Pg;
-  f.slices[0] = a.zslices;
-  f.slices[1] = a.gslices;
-  f.R = R;
-  f.rows = q.rows;
-  f.T[0] = reinterpret_cast<uint16_t *>(w + q.zt_at);
-  f.T[1] = o.dv ? reinterpret_cast<uint16_t *>(w + q.gt_at) : nullptr;
-  f.grows = o.dx ? reinterpret_cast<uint16_t *>(w + q.grows_at) : nullptr;
-  finish_kernel<<<dim3(q.tiles, (R + 31) / 32, 2), 256, 0, stream>>>(f);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  GradArgs d{};
-  d.s = s;
-  d.first = gr.first;
-  d.count = gr.count;
-  d.x = x;
-  d.vt = p.vt;
-  d.dy = dy;
-  d.zT = f.T[0];
-  d.gT = reinterpret_cast<uint16_t *>(w + q.gt_at);
-  d.grows = f.grows;
-  d.K = p.K;
-  d.Ntot = p.Ntot;
-  d.nchild = p.nchild;
-  d.R = R;
-  d.rows = q.rows;
-  d.base = o.base;
-  d.dx = o.dx;
-  d.du = o.du;
-  d.dv = o.dv;
-  d.tiles = q.tiles;
-  d.kblocks = (p.K + 255) / 256;
-  d.vblocks = (p.K + 63) / 64;
-  for (int c = 0; c < p.nchild; ++c) {
-    d.N[c] = a.N[c];
-    d.n0[c] = a.n0[c];
-    d.ublock0[c + 1] = d.ublock0[c] + (p.N[c] + 63) / 64;
-  }
-  const int JF = q.NF;
-  d.jgroups = q.ggroups;
-  d.units[0] = o.dx ? static_cast<int64_t>(q.tiles) * d.kblocks : 0;
-  d.units[1] = o.du ? static_cast<int64_t>(p.n) * d.jgroups * d.ublock0[p.nchild] : 0;
-  d.units[2] = o.dv ? static_cast<int64_t>(p.n) * d.jgroups * p.nchild * d.vblocks : 0;
-  const int64_t total = d.units[0] + d.units[1] + d.units[2];
-  // (a launch holds fewer than 2^32 threads along x)
-  constexpr int64_t kAcross = int64_t{1} << 20;
-  const dim3 blocks(static_cast<uint32_t>(std::min(total, kAcross)), static_cast<uint32_t>((total + kAcross - 1) / kAcross));
-  switch (JF) {
-    case 1: gradient_kernel<1><<<blocks, 256, 0, stream>>>(d); break;
-    case 2: gradient_kernel<2><<<blocks, 256, 0, stream>>>(d); break;
-    case 4: gradient_kernel<4><<<blocks, 256, 0, stream>>>(d); break;
-    default: gradient_kernel<8><<<blocks, 256, 0, stream>>>(d); break;
-  }
-  return hipGetLastError();
+  return q.frags == 1 ? launch_expand<1>(a, q, stream) : launch_expand<4>(a, q, stream);
 }
 
 }  // namespace wl

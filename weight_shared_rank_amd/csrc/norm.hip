@@ -255,8 +255,10 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float *part, int G, 
   const int k = blockIdx.x * 16 + l;
   __shared__ float s[16][17];
   float v = 0.f;
-  if (k < K)
+  if (k < K) {
+#pragma unroll 16
     for (int i = g; i < G; i += 16) v += part[static_cast<int64_t>(i) * K + k];
+  }
   s[g][l] = v;
   __syncthreads();
   if (g == 0 && k < K) {
