@@ -93,6 +93,28 @@ def test_gradients(gpu_lib, T, rows, K, r, n, ranked):
     assert torch.equal(p.backward(code, dy, index, b2, want=("dx",), dx=b2).dx, g.dx)
 
 
+SPLITS = [  # few slots and many tokens; many column tiles; long contractions of z, of g, of both
+    (2100, (70, 40), 40, 16, 1), (4500, (130,), 200, 64, 2), (6200, (65, 1), 72, 32, 3), (300, (1001,), 8, 32, 256),
+    (300, (520, 130), 264, 16, 260), (200, (700,), 72, 128, 200), (70, (2100, 30), 2056, 32, 3), (40, (1100,), 1160, 48, 2),
+    (130, (4100,), 64, 16, 4), (130, (100,), 4104, 64, 4)]
+
+
+@pytest.mark.parametrize("T,rows,K,r,n", SPLITS)
+@pytest.mark.parametrize("ranked", [False, True])
+def test_gradients_of_split_sums(gpu_lib, T, rows, K, r, n, ranked):
+    test_gradients(gpu_lib, T, rows, K, r, n, ranked)
+
+
+def test_gradients_past_a_rank_are_zero_for_an_infinite_dy(gpu_lib):
+    T = 70
+    p = make_pool(2, 48, 136, (70,), ranks=[5, 33])
+    dy = randn(2, T, 70)
+    dy[3, 7], dy[40] = float("inf"), float("nan")
+    g = p.backward(binding.encode_act(randn(1, T, 136)), dy, mixed_index(T, 2, 3), want=("du", "dv"))
+    for a, r in enumerate(p.rank.tolist()):
+        assert (g.du[a, :, r:] == 0).all() and (g.dv[a, r:] == 0).all()
+
+
 @pytest.mark.parametrize("T", [1, 32, 65, 700])
 @pytest.mark.parametrize("kind", ["none", "one", "last", "sorted"])
 def test_index_patterns(gpu_lib, T, kind):

@@ -891,8 +891,7 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
   g.s = a.s;
   g.tiles = reinterpret_cast<int4 *>(w);
   g.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
-  group_kernel<kGroupM><<<group_workgroups(p.n), kGroupWaves * 64, 0, stream>>>(g);
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch_group<kGroupM>(g, stream);
   if (e != hipSuccess) return e;
   a.s.tiles = g.tiles;
   a.s.perm = g.perm;

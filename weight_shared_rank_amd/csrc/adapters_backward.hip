@@ -3,19 +3,24 @@
 // With X the values of the checkpoint, dy the gradient of y and c the scale, per
 // token z = c V^T X and g = c U^T dy, and
 //   dx = base + V g,   dU_a = sum over the slot's tokens dy z^T,   dV_a^T = sum g X^T
-// Launches: the grouping; project_kernel, z and g in float32 slices;
-// finish_kernel, their sums as pairs of bf16 in the layouts the products read;
-// gradient_kernel, dx, dU and dV.  Positions are the grouped order: tile * M + i.
+// Launches: the grouping, in tiles of 64 tokens; project_kernel, z and g in float32
+// slices; finish_kernel, their sums as pairs of bf16 (the value and what its rounding
+// left), each 16 x 32 piece of them stored as the 64 lanes' operand of a matrix
+// instruction, so that the products load it as 1 KB; gradient_kernel, dx, dU and dV.
 //
 // U (for g), V^T (for dx) and dy and X (for dU and dV) enter a product along
-// their slow dimension.  They come from memory as they lie, 16 bytes a lane, go
-// through a piece of LDS of the wave's own, and are transposed on the way to the
-// registers by ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 elements, and lane
-// l gets the 4 of column l.  Row 8 g + 4 h + i of 32 is kept at place 16 h + 4 g + i,
-// so that the two reads of a fragment give lane group g its contraction values
-// 8 g .. 8 g + 7 in order (what the other operand's 16-byte loads hold), each
-// from 16 places in a row; with an odd multiple of 32 bytes from place to place,
-// 8 neighbouring places lie in 8 different parts of the 256-byte bank period.
+// their slow dimension.  They come from memory as rows, 16 bytes a lane, go through
+// LDS, and are transposed on the way to the registers by ds_read_b64_tr_b16: 16 lanes
+// read 4 rows of 16 elements, and lane l gets the 4 of column l.  Row 8 g + 4 h + i of
+// 32 is kept at place 16 h + 4 g + i, so that the two reads of a fragment give lane
+// group g its contraction values 8 g .. 8 g + 7 in order (what the other operand's 16
+// bytes hold); with an odd multiple of 32 bytes from place to place, 8 neighbouring
+// places lie in 8 different parts of the 256-byte bank period.
+//
+// Bound by memory: dy is read twice, for g and for dU, and everything else once.  As
+// in the forward pass no load of a loop is conditional.
+#include <type_traits>
+
 #include "adapter_tiles.h"
 
 namespace wl {
@@ -25,7 +30,10 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+
+constexpr int kM = 64;    // tokens of a tile
+constexpr int kDeep = 4;  // stages under way in project_kernel
+constexpr int kWaves = 8, kThreads = kWaves * 64;
 
 // Place of a row (any number of 32s), in rows.
 __device__ __forceinline__ int place(int row) {
@@ -36,15 +44,79 @@ __device__ __forceinline__ int place(int row) {
 // column `r16` of those; at: byte offset of the four columns that lanes with
 // these r16 & 3 read.
 template <int PITCH>
-__device__ __forceinline__ u32x4 read_transposed(const lds_u8 *tile, int b, int at) {
+__device__ __forceinline__ u32x4 read_transposed(const uint8_t *tile, int b, int at) {
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-  const lds_u8 *p = tile + (32 * b + 4 * g + (r16 >> 2)) * PITCH + at;
+  const lds_u8 *p = (const lds_u8 *)tile + (32 * b + 4 * g + (r16 >> 2)) * PITCH + at;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * PITCH));
   const u32x2 x = __builtin_bit_cast(u32x2, lo), y = __builtin_bit_cast(u32x2, hi);
   return u32x4{x[0], x[1], y[0], y[1]};
 }
 
+// 8 codes and their scale byte as bf16, exact.
+__device__ __forceinline__ u32x4 expand_codes(u32x2 v, uint8_t scale) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const float f = __uint_as_float(static_cast<uint32_t>(scale) << 23);
+  u32x4 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), false);
+    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(v[h]), true);
+    o[2 * h] = pack_bf16(a[0] * f, a[1] * f);
+    o[2 * h + 1] = pack_bf16(b[0] * f, b[1] * f);
+  }
+  return o;
+}
+
+// z and g summed over their slices, times c, as pairs of bf16 in the operands' order.
+// A piece is 64 lanes of 8 values:
+//   transposed (for dU and dV): lane (r16, g) has rank 16 jt + r16 of positions
+//     32 s + 8 g .. + 7 of the place: piece ((place * 2 + s) * RT + jt) * 2 + p
+//   rows (g, for dx): lane (r16, g) has position 16 i + r16, ranks 32 ch + 8 g .. + 7 of
+//     a child: piece ((place * 4 + i) * nchild * RC + child * RC + ch) * 2 + p
+// with RT = R / 16, RC = r / 32 rounded up, p 0 the value and 1 what its rounding left.
+// Ranks past the slot's and positions behind the tile's tokens are zeros.
+struct Factors {
+  const float *scale;
+  uint16_t *T[2];        // transposed z, g (null: not wanted)
+  uint16_t *grows;       // rows (null: not wanted)
+  int32_t RT, nchild, RC;
+};
+
+// A lane's 8 values of a piece, and what is left of them in the next.
+__device__ __forceinline__ void store_piece(uint16_t *to, const float (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+  u32x2 hi[2], lo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) split4(f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}, hi[h], lo[h]);
+  *reinterpret_cast<u32x4 *>(to + lane * 8) = u32x4{hi[0][0], hi[0][1], hi[1][0], hi[1][1]};
+  *reinterpret_cast<u32x4 *>(to + 512 + lane * 8) = u32x4{lo[0][0], lo[0][1], lo[1][0], lo[1][1]};
+}
+
+// sum: [kM][pitch] floats of a place; a wave stores columns 16 f .. + 15 of positions
+// 32 s .. + 31 as piece (place, s, jt), and columns 32 ch .. + 31 of positions 16 i ..
+// + 15 as the rows piece `to`.
+__device__ __forceinline__ void store_transposed(const Factors &o, int which, int place0, int s, int jt, const float *sum, int pitch, int f) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = sum[(32 * s + 8 * g + k) * pitch + 16 * f + r16];
+  store_piece(o.T[which] + ((static_cast<int64_t>(place0) * 2 + s) * o.RT + jt) * 1024, v);
+}
+__device__ __forceinline__ void store_rows(const Factors &o, int place0, int i, int chunk, const float *sum, int pitch, int ch) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = sum[(16 * i + r16) * pitch + 32 * ch + 8 * g + k];
+  store_piece(o.grows + ((static_cast<int64_t>(place0) * 4 + i) * o.nchild * o.RC + chunk) * 1024, v);
+}
+
+// ---- z and g -------------------------------------------------------------------------
+// P[slice][row][col] = sum over the slice of a thin operand's rows (V^T for z, U^T for
+// g) times the tokens' x or dy.  A workgroup takes a tile, a slice and 16 NF columns; a
+// stage of KS contraction values comes as rows, waits in registers while the kDeep - 1
+// before it are used, and goes through LDS.  A wave multiplies two column tiles (one
+// where there is no more) and 32 tokens over 32 values.
 struct ProjectArgs {
   TileSource s;
   CodedView x;          // the checkpoint
@@ -54,210 +126,332 @@ struct ProjectArgs {
   int32_t K, Ntot, nchild, N[kMaxChildren], n0[kMaxChildren];
   int32_t R;            // nchild * r
   int64_t rows;
-  int32_t zgroups, zslices, zper;  // z: groups of NF row tiles, K slices, steps of each (zslices 0: no z)
-  int32_t ggroups, gslices, gper;  // g: groups of NF row tiles of a child, slices of N, steps of each
+  int32_t zgroups, zslices, zper;  // z: groups of NF column tiles, slices of K (0: no z), k of each
+  int32_t ggroups, gslices, gper;  // g: groups of NF column tiles of a child, slices of N, n of each
   float *Pz, *Pg;       // [slices][rows][R]
+  Factors out;
 };
 
-constexpr int kM = 32, kMF = 2;  // tokens of a tile in the backward pass
-
-// The waves' sums of a tile meet in LDS; wave 0 stores them.
 template <int NF>
-__device__ __forceinline__ void store_thin(const f32x4 (&acc)[NF][kMF], f32x4 *part, const int (&col)[NF], int live, int count,
-                                           float *P, int64_t row0, int R) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+struct Stage {
+  static constexpr int KS = NF == 4 ? 64 : 128, SUBS = KS / 64, XB = SUBS * kM * 128;
+  static constexpr int FP = NF == 4 ? 2 : 1, FR = NF == 1 ? 1 : 2, H = kWaves / (2 * FP);  // pairs of column tiles, tiles of a wave, waves along the contraction
+  static constexpr int VB = SUBS * NF * 2048;                  // V^T: rows of 64 k
+  static constexpr int UPITCH = 32 * (NF | 1), UB = KS * UPITCH;  // U: rows of 16 NF ranks
+  static constexpr int BYTES = XB + (VB > UB ? VB : UB), SUMS = kWaves * FR * 2 * 1024;
+  static constexpr int PITCH = 32 * ((NF + 1) / 2) + 1;  // of the sums, in floats
+  static constexpr int LDS = 2 * BYTES > SUMS ? 2 * BYTES : SUMS;
+  static_assert(kM * PITCH * 4 <= LDS, "the sums fit");
+  static_assert(H * 32 == KS && XB == SUBS * kThreads * 16, "stage shape");
+};
+
+// Stages k0, k0 + KS, ... below k1 of a workgroup, kDeep under way: whole(d) loads the
+// next whole stage, next() moves on by kDeep of them, last(k, d) loads a stage of which
+// a part may lie past the end; put(d) and put_last(k, d) bring them to LDS, use(d)
+// multiplies.
+template <int KS, typename W, typename X, typename L, typename P, typename Q, typename U>
+__device__ __forceinline__ void run_stages(int k0, int k1, W &&whole, X &&next, L &&last, P &&put, Q &&put_last, U &&use) {
+  const int groups = (k1 - k0) / (KS * kDeep), kl = k0 + groups * KS * kDeep;
+  if (groups > 0) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) whole(d);
+    for (int i = 1; i < groups; ++i) {
+      next();
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        put(d);
+        whole(d);
+        use(d);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      put(d);
+      last(kl + d * KS, d);
+      use(d);
+    }
+  } else {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) last(kl + d * KS, d);
+  }
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    if (kl + d * KS >= k1) break;
+    put_last(kl + d * KS, d);
+    use(d);
+  }
+}
+
+// The waves' sums along the contraction meet in LDS in wave order.  Column tile f of
+// the workgroup is columns col(f) on of P's R, ranks rank0(f) on; with one slice alone
+// they leave as finish_kernel would have them.
+template <int NF, typename C, typename J>
+__device__ __forceinline__ void store_sums(const ProjectArgs &a, const Tile &t, int which, int slice, const f32x4 (&acc)[Stage<NF>::FR][2],
+                                           uint8_t *lds, int live, C &&col, J &&rank0) {
+  using S = Stage<NF>;
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
+  const int fp = wave % S::FP, ip = wave / S::FP & 1, h = wave / (2 * S::FP);
+  const bool one = (which ? a.gslices : a.zslices) == 1;
+  f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [wave][FR][2][64]
   __syncthreads();
-  if (wave > 0) {
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
+  for (int f = 0; f < S::FR; ++f)
 #pragma unroll
-      for (int i = 0; i < kMF; ++i) part[((wave - 1) * NF * kMF + f * kMF + i) * 64 + lane] = acc[f][i];
+    for (int i = 0; i < 2; ++i) part[((wave * S::FR + f) * 2 + i) * 64 + lane] = acc[f][i];
+  __syncthreads();
+  f32x4 v[S::FR][2];
+  if (h == 0) {
+#pragma unroll
+    for (int f = 0; f < S::FR; ++f)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[f][i] = acc[f][i];
+#pragma unroll
+        for (int q = 1; q < S::H; ++q) v[f][i] += part[(((q * 2 * S::FP + wave) * S::FR + f) * 2 + i) * 64 + lane];
+        const int tile = S::FR * fp + f, m = 32 * ip + 16 * i + r16;
+        if (!one && tile < live && m < t.count)
+          *reinterpret_cast<f32x4 *>((which ? a.Pg : a.Pz) + (slice * a.rows + static_cast<int64_t>(blockIdx.x) * kM + m) * a.R + col(tile) + g * 4) = v[f][i];
+      }
+  }
+  if (!one) return;
+  __syncthreads();
+  float *sum = reinterpret_cast<float *>(lds);  // [kM][PITCH]
+  if (h == 0) {
+    const float scale = a.out.scale[t.slot];
+#pragma unroll
+    for (int f = 0; f < S::FR; ++f)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tile = S::FR * fp + f, m = 32 * ip + 16 * i + r16;
+          sum[m * S::PITCH + 16 * tile + 4 * g + k] = tile < live && m < t.count && rank0(tile) + 4 * g + k < t.rank ? v[f][i][k] * scale : 0.f;
+        }
+  } else if (NF == 1) {  // the chunk's second half
+    for (int i = threadIdx.x - 128; i < kM * 16; i += kThreads - 128) sum[(i >> 4) * S::PITCH + 16 + (i & 15)] = 0.f;
   }
   __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < kMF; ++i) {
-      f32x4 v = acc[f][i];
-#pragma unroll
-      for (int w = 0; w < 3; ++w) v += part[(w * NF * kMF + f * kMF + i) * 64 + lane];
-      if (f < live && 16 * i + r16 < count) *reinterpret_cast<f32x4 *>(P + (row0 + 16 * i + r16) * R + col[f] + g * 4) = v;
-    }
+  if (a.out.T[which] && wave < 2 * NF && (wave >> 1) < live)
+    store_transposed(a.out, which, blockIdx.x, wave & 1, col(wave >> 1) / 16, sum, S::PITCH, wave >> 1);
+  if (which && a.out.grows && wave < 4 * ((NF + 1) / 2) && 2 * (wave >> 2) < live)
+    store_rows(a.out, blockIdx.x, wave & 3, col(0) / a.s.r * a.out.RC + rank0(0) / 32 + (wave >> 2), sum, S::PITCH, wave >> 2);
 }
 
 template <int NF>
-__global__ __launch_bounds__(256) void project_kernel(ProjectArgs a) {
-  constexpr int PITCH = 32 * (NF | 1), ROWS = NF == 8 ? 32 : 64, B = ROWS / 32;  // g: a wave's piece of U
-  constexpr int PART = 3 * NF * kMF * 1024, PIECES = 4 * ROWS * PITCH;
+__device__ __forceinline__ void project_z(const ProjectArgs &a, const Tile &t, const int *tok, int unit, uint8_t *lds) {
+  using S = Stage<NF>;
+  constexpr int KS = S::KS, SUBS = S::SUBS;
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4, K = a.K;
+  const int f0 = unit % a.zgroups * NF, slice = unit / a.zgroups, per_child = t.rank16 / 16, live = a.nchild * per_child - f0;
+  if (live <= 0) return;
+  auto column = [&](int f) {  // tiles past the last repeat it
+    const int v = f0 + min(f, live - 1);
+    return v / per_child * a.s.r + v % per_child * 16;
+  };
+  const u32x4 zero{0u, 0u, 0u, 0u};
+  const int chunk = threadIdx.x & 7, xrow = threadIdx.x >> 3;
+  const int token = tok[xrow] < 0 ? tok[0] : tok[xrow];  // (columns without a token are not stored)
+  const uint8_t *codes = a.x.codes + static_cast<int64_t>(token) * a.x.nb * kCodeBlock;
+  const uint8_t *scales = a.x.scales + token;
+  const int arow = (threadIdx.x >> 3) % (16 * NF), asub = threadIdx.x / (128 * NF) % SUBS;  // (NF 1: every piece twice)
+  const uint16_t *a0 = a.vt + static_cast<int64_t>(t.slot) * a.R * K;
+  const uint32_t arowb = static_cast<uint32_t>(column(arow >> 4) + (arow & 15)) * static_cast<uint32_t>(K) * 2u;
+  const int ak = asub * 64 + chunk * 8;
+  uint8_t *const xput = lds + xrow * 128 + (chunk ^ (xrow & 7)) * 16;
+  uint8_t *const aput = lds + S::XB + (asub * 16 * NF + arow) * 128 + (chunk ^ (arow & 7)) * 16;
+  const int fp = wave % S::FP, ip = wave / S::FP & 1, h = wave / (2 * S::FP), at = (((4 * h + g) & 7) ^ (r16 & 7)) * 16;
+  const uint8_t *fa = lds + S::XB + ((h >> 1) * 16 * NF + 16 * S::FR * fp + r16) * 128 + at, *fx = lds + ((h >> 1) * kM + 32 * ip + r16) * 128 + at;
+  f32x4 acc[S::FR][2];
+#pragma unroll
+  for (int f = 0; f < S::FR; ++f)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int k0 = slice * a.zper, k1 = min(K, k0 + a.zper);
+  u32x2 xv[kDeep][SUBS];
+  uint8_t xs[kDeep];  // (a stage starts at a multiple of 64, SUBS 2: of 128: one block of codes)
+  u32x4 av[kDeep];
+  int k = k0;
+  auto load = [&](int at_k, int d, bool whole) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) {
+      const int kk = at_k + s * 64 + chunk * 8;
+      xv[d][s] = *reinterpret_cast<const u32x2 *>(codes + (whole || kk < k1 ? kk : 0));
+    }
+    xs[d] = scales[static_cast<int64_t>(whole || at_k < k1 ? at_k / kCodeBlock : 0) * a.x.ldsc];
+    av[d] = whole ? ld16_at(a0 + at_k, arowb + ak * 2u) : ld16_at(a0, arowb + (at_k + ak < k1 ? (at_k + ak) * 2u : 0u));
+  };
+  auto put = [&](int at_k, int d, bool whole) {
+    uint8_t *const to = lds + (d & 1) * S::BYTES;
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) {
+      const u32x4 v = expand_codes(xv[d][s], xs[d]);
+      *reinterpret_cast<u32x4 *>(xput - lds + to + s * kM * 128) = whole || at_k + s * 64 + chunk * 8 < k1 ? v : zero;
+    }
+    *reinterpret_cast<u32x4 *>(aput - lds + to) = whole || at_k + ak < k1 ? av[d] : zero;
+  };
+  run_stages<KS>(
+      k0, k1, [&](int d) { load(k + d * KS, d, true); }, [&] { k += KS * kDeep; }, [&](int at_k, int d) { load(at_k, d, false); },
+      [&](int d) { put(0, d, true); }, [&](int at_k, int d) { put(at_k, d, false); },
+      [&](int d) {
+        wait_and_sync<63>();  // this stage is in LDS; loads stay under way
+        const int buf = (d & 1) * S::BYTES;
+        u32x4 x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const u32x4 *>(fx + buf + i * 2048);
+#pragma unroll
+        for (int f = 0; f < S::FR; ++f) {
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(fa + buf + f * 2048);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[f][i] = mfma16x16x32(v, x[i], acc[f][i]);
+        }
+      });
+  store_sums<NF>(a, t, 0, slice, acc, lds, live, column, [&](int f) { return (f0 + min(f, live - 1)) % per_child * 16; });
+}
+
+template <int NF>
+__device__ __forceinline__ void project_g(const ProjectArgs &a, const Tile &t, const int *tok, int unit, uint8_t *lds) {
+  using S = Stage<NF>;
+  constexpr int KS = S::KS, SUBS = S::SUBS, LPR = 2 * NF;  // lanes of a row of U
+  constexpr int UP = KS * LPR / kThreads ? KS * LPR / kThreads : 1;  // pieces of U of a thread (NF 1: every piece twice)
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
+  const int c = unit % a.nchild, j0 = unit / a.nchild % a.ggroups * NF * 16, slice = unit / a.nchild / a.ggroups;
+  const int live = t.rank16 / 16 - j0 / 16, N = a.N[c], r = a.s.r;
+  const int n0 = slice * a.gper, n1 = min(N, n0 + a.gper);
+  if (live <= 0) return;
+  const u32x4 zero{0u, 0u, 0u, 0u};
+  const int chunk = threadIdx.x & 7, xrow = threadIdx.x >> 3;
+  const uint16_t *dyrow = a.dy + static_cast<int64_t>(tok[xrow] < 0 ? tok[0] : tok[xrow]) * a.Ntot + a.n0[c] + chunk * 8;
+  const uint16_t *U = a.u + (static_cast<int64_t>(t.slot) * a.Ntot + a.n0[c]) * r + j0;
+  int urow[UP], ucol;
+  uint32_t uoff[UP];
+  uint8_t *uput[UP];
+  ucol = threadIdx.x % LPR * 8;
+#pragma unroll
+  for (int i = 0; i < UP; ++i) {
+    urow[i] = (i * kThreads + static_cast<int>(threadIdx.x)) / LPR % KS;
+    uoff[i] = static_cast<uint32_t>(urow[i] * r + (j0 + ucol < r ? ucol : 0)) * 2u;  // (columns past the room: not stored)
+    uput[i] = lds + S::XB + place(urow[i]) * S::UPITCH + ucol * 2;
+  }
+  uint8_t *const xput = lds + xrow * 128 + (chunk ^ (xrow & 7)) * 16;
+  const int fp = wave % S::FP, ip = wave / S::FP & 1, h = wave / (2 * S::FP), at = (((4 * h + g) & 7) ^ (r16 & 7)) * 16;
+  const uint8_t *fx = lds + ((h >> 1) * kM + 32 * ip + r16) * 128 + at;
+  f32x4 acc[S::FR][2];
+#pragma unroll
+  for (int f = 0; f < S::FR; ++f)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 xv[kDeep][SUBS], uv[kDeep][UP];
+  int n = n0;
+  run_stages<KS>(
+      n0, max(n0, n1),
+      [&](int d) {
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) xv[d][s] = ld16_any(dyrow + n + d * KS + s * 64);
+#pragma unroll
+        for (int i = 0; i < UP; ++i) uv[d][i] = ld16_at(U + static_cast<int64_t>(n + d * KS) * r, uoff[i]);
+      },
+      [&] { n += KS * kDeep; },
+      [&](int at_n, int d) {  // the last stages: zeros past the slice
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) xv[d][s] = load_some(dyrow + at_n + s * 64, n1 - (at_n + s * 64 + chunk * 8));
+#pragma unroll
+        for (int i = 0; i < UP; ++i)
+          uv[d][i] = at_n + urow[i] < n1 ? ld16_at(U + static_cast<int64_t>(at_n) * r, uoff[i]) : zero;
+      },
+      [&](int d) {
+        const int buf = (d & 1) * S::BYTES;
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) *reinterpret_cast<u32x4 *>(xput + buf + s * kM * 128) = xv[d][s];
+#pragma unroll
+        for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4 *>(uput[i] + buf) = uv[d][i];
+      },
+      [&](int, int d) {
+        const int buf = (d & 1) * S::BYTES;
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) *reinterpret_cast<u32x4 *>(xput + buf + s * kM * 128) = xv[d][s];
+#pragma unroll
+        for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4 *>(uput[i] + buf) = uv[d][i];
+      },
+      [&](int d) {
+        wait_and_sync<63>();
+        const int buf = (d & 1) * S::BYTES;
+        u32x4 x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const u32x4 *>(fx + buf + i * 2048);
+#pragma unroll
+        for (int f = 0; f < S::FR; ++f) {
+          const u32x4 v = read_transposed<S::UPITCH>(lds + buf + S::XB, h, 32 * (S::FR * fp + f) + 8 * (r16 & 3));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[f][i] = mfma16x16x32(v, x[i], acc[f][i]);
+        }
+      });
+  store_sums<NF>(a, t, 1, slice, acc, lds, live, [&](int f) { return c * r + j0 + 16 * f; }, [&](int f) { return j0 + 16 * f; });
+}
+
+template <int NF>
+__global__ __launch_bounds__(kThreads, 4) void project_kernel(ProjectArgs a) {
   __shared__ int tok[kM];
-  __shared__ __align__(16) uint8_t lds[PART > PIECES ? PART : PIECES];
+  __shared__ __align__(16) uint8_t lds[Stage<NF>::LDS];
   Tile t;
   if (!get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int per_child = t.rank16 / 16;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kM;
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  f32x4 acc[NF][kMF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < kMF; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int token[kMF], col[NF];
-#pragma unroll
-  for (int i = 0; i < kMF; ++i) token[i] = tok[16 * i + r16];
-  int unit = blockIdx.y;
-  const int zunits = a.zgroups * a.zslices;
-  if (unit < zunits) {
-    const int f0 = unit % a.zgroups * NF, slice = unit / a.zgroups, live = a.nchild * per_child - f0;
-    if (live <= 0) return;
-    const uint16_t *ar[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const int v = f0 + min(f, live - 1);
-      col[f] = v / per_child * a.s.r + v % per_child * 16;
-      ar[f] = a.vt + (static_cast<int64_t>(t.slot) * a.R + col[f] + r16) * a.K;
-    }
-    const int end = min((a.K + 63) / 64, (slice + 1) * a.zper);
-    u32x4 xv[2][kMF][2], av[2][NF][2];
-    auto load = [&](int step, u32x4(&xo)[kMF][2], u32x4(&ao)[NF][2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = step * 64 + g * 16 + h * 8;
-        const bool in = step < end && k < a.K;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) ao[f][h] = in ? ld16(ar[f] + k) : zero;
-#pragma unroll
-        for (int i = 0; i < kMF; ++i) xo[i][h] = in && token[i] >= 0 ? expand8(a.x, token[i], k) : zero;
-      }
-    };
-    auto multiply = [&](const u32x4(&xo)[kMF][2], const u32x4(&ao)[NF][2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-#pragma unroll
-          for (int i = 0; i < kMF; ++i) acc[f][i] = mfma16x16x32(ao[f][h], xo[i][h], acc[f][i]);
-    };
-    int step = slice * a.zper + wave;
-    load(step, xv[0], av[0]);
-    for (; step < end; step += 8) {
-      load(step + 4, xv[1], av[1]);
-      multiply(xv[0], av[0]);
-      load(step + 8, xv[0], av[0]);
-      multiply(xv[1], av[1]);
-    }
-    store_thin<NF>(acc, reinterpret_cast<f32x4 *>(lds), col, live, t.count, a.Pz + slice * a.rows * a.R, row0, a.R);
-    return;
-  }
-  unit -= zunits;
-  const int c = unit % a.nchild, j0 = unit / a.nchild % a.ggroups * NF * 16, slice = unit / a.nchild / a.ggroups;
-  const int live = per_child - j0 / 16, N = a.N[c];
-  if (live <= 0) return;
-#pragma unroll
-  for (int f = 0; f < NF; ++f) col[f] = c * a.s.r + j0 + 16 * f;
-  const uint16_t *U = a.u + (static_cast<int64_t>(t.slot) * a.Ntot + a.n0[c]) * a.s.r + j0;
-  lds_u8 *piece = (lds_u8 *)lds + wave * (ROWS * PITCH);
-  const int end = min((N + ROWS - 1) / ROWS, (slice + 1) * a.gper);
-  constexpr int Q = ROWS * 2 * NF / 64;  // 16-byte loads of U a step and lane
-  u32x4 uv[Q], dv[kMF][B];
-  auto load = [&](int step) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int v = q * 64 + lane, row = step * ROWS + v / (2 * NF), j = v % (2 * NF) * 8;
-      uv[q] = step < end && row < N && j0 + j < a.s.r ? ld16(U + static_cast<int64_t>(row) * a.s.r + j) : zero;
-    }
-#pragma unroll
-    for (int i = 0; i < kMF; ++i)
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const int n = step * ROWS + 32 * b + 8 * g;
-        dv[i][b] = zero;
-        if (step < end && token[i] >= 0 && n < N)
-          dv[i][b] = load_some(a.dy + static_cast<int64_t>(token[i]) * a.Ntot + a.n0[c] + n, N - n);
-      }
-  };
-  int step = slice * a.gper + wave;
-  load(step);
-  for (; step < end; step += 4) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int v = q * 64 + lane;
-      *(lds_u32x4 *)(piece + place(v / (2 * NF)) * PITCH + v % (2 * NF) * 16) = uv[q];
-    }
-    u32x4 d[kMF][B];
-#pragma unroll
-    for (int i = 0; i < kMF; ++i)
-#pragma unroll
-      for (int b = 0; b < B; ++b) d[i][b] = dv[i][b];
-    load(step + 4);
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const u32x4 av = read_transposed<PITCH>(piece, b, 32 * f + 8 * (r16 & 3));
-#pragma unroll
-        for (int i = 0; i < kMF; ++i) acc[f][i] = mfma16x16x32(av, d[i][b], acc[f][i]);
-      }
-  }
-  store_thin<NF>(acc, reinterpret_cast<f32x4 *>(lds), col, live, t.count, a.Pg + slice * a.rows * a.R, row0, a.R);
+  const int zunits = a.zgroups * a.zslices, unit = blockIdx.y;
+  if (unit < zunits)
+    project_z<NF>(a, t, tok, unit, lds);
+  else
+    project_g<NF>(a, t, tok, unit - zunits, lds);
 }
 
-// z and g summed over their slices, times c, as pairs of bf16: transposed [2][R][rows]
-// (dU, dV) and, for g, as rows [rows][2][R] (dx).  Columns past the slot's rank
-// and positions behind the tile's tokens are zeros.
+// ---- sums of the slices, where there are some -----------------------------------------------
 struct FinishArgs {
   TileSource s;
-  const float *scale;
   const float *P[2];     // z, g
-  int32_t slices[2];     // 0: not wanted
+  int32_t slices[2];     // below 2: nothing to do
   int32_t R;
   int64_t rows;
-  uint16_t *T[2];        // [2][R][rows]
-  uint16_t *grows;       // [rows][2][R]
+  Factors out;
 };
 
 __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a) {
+  constexpr int PITCH = 33;
   __shared__ int tok[kM];
-  __shared__ uint16_t pair[2][32][kM + 2];
+  __shared__ float sum[kM * PITCH];
   Tile t;
   const int which = blockIdx.z;
-  if (!a.slices[which] || !get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kM;
-  const float scale = a.scale[t.slot];
-  const int j0 = blockIdx.y * 32, l = threadIdx.x & 31;
-  const int j = j0 + l;
+  if (a.slices[which] < 2 || !get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
+  const int c = blockIdx.y / a.out.RC, ch = blockIdx.y % a.out.RC, j0 = ch * 32;  // ranks j0 .. + 31 of child c
+  const float scale = a.out.scale[t.slot];
+  {
+    const int j = j0 + (threadIdx.x & 7) * 4;
+    const bool in = j < a.s.r && j < t.rank16;
+    const float *p = a.P[which] + (static_cast<int64_t>(blockIdx.x) * kM + (threadIdx.x >> 3)) * a.R + c * a.s.r + (in ? j : 0);
+    const int64_t half = static_cast<int64_t>(32) * a.R, step = a.rows * a.R;
+    f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    if (in) {
+#pragma unroll 4
+      for (int s = 0; s < a.slices[which]; ++s) {
+        v[0] += *reinterpret_cast<const f32x4 *>(p + s * step);
+        v[1] += *reinterpret_cast<const f32x4 *>(p + s * step + half);
+      }
+    }
 #pragma unroll
-  for (int m = threadIdx.x >> 5; m < kM; m += 8) {
-    float v = 0.f;
-    if (j < a.R && m < t.count && j % a.s.r < t.rank) {
-      const float *p = a.P[which] + (row0 + m) * a.R + j;
-      for (int s = 0; s < a.slices[which]; ++s) v += p[s * a.rows * a.R];
-      v *= scale;
-    }
-    u32x2 hi2, lo2;
-    split4(f32x4{v, 0.f, 0.f, 0.f}, hi2, lo2);
-    const uint16_t h = static_cast<uint16_t>(hi2[0]), lo = static_cast<uint16_t>(lo2[0]);
-    pair[0][l][m] = h;
-    pair[1][l][m] = lo;
-    if (which == 1 && a.grows && j < a.R) {
-      a.grows[(row0 + m) * 2 * a.R + j] = h;
-      a.grows[((row0 + m) * 2 + 1) * a.R + j] = lo;
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int m = 32 * h + (threadIdx.x >> 3);
+        sum[m * PITCH + (threadIdx.x & 7) * 4 + k] = m < t.count && in && j + k < t.rank ? v[h][k] * scale : 0.f;
+      }
   }
-  if (!a.T[which]) return;
   __syncthreads();
-  // 32 rows of 32 positions, twice; 4 positions a thread
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = threadIdx.x >> 3, m = (threadIdx.x & 7) * 4;
-    if (j0 + row >= a.R) continue;
-    const uint16_t *p = &pair[i][row][m];
-    *reinterpret_cast<u32x2 *>(a.T[which] + (static_cast<int64_t>(i) * a.R + j0 + row) * a.rows + row0 + m) =
-        u32x2{p[0] | static_cast<uint32_t>(p[1]) << 16, p[2] | static_cast<uint32_t>(p[3]) << 16};
-  }
+  const int w = threadIdx.x >> 6;
+  if (a.out.T[which] && j0 + 16 * (w & 1) < a.s.r)
+    store_transposed(a.out, which, blockIdx.x, w >> 1, (c * a.s.r + j0) / 16 + (w & 1), sum, PITCH, w & 1);
+  if (which == 1 && a.out.grows) store_rows(a.out, blockIdx.x, w, c * a.out.RC + ch, sum, PITCH, 0);
 }
+
+// ---- dx, dU, dV -----------------------------------------------------------------------------
+constexpr int kGradWaves = 4, kPitch = 160, kPiece = 32 * kPitch;  // a wave's piece of LDS: 32 rows of 64 elements
+constexpr int kOutPitch = 272;                                      // of sums: 16 rows of 64 floats
+static_assert(16 * kOutPitch <= kPiece, "the sums fit the piece");
 
 struct GradArgs {
   TileSource s;
@@ -267,106 +461,214 @@ struct GradArgs {
   const uint16_t *vt, *dy;
   const uint16_t *zT, *gT, *grows;
   int32_t K, Ntot, nchild, N[kMaxChildren], n0[kMaxChildren];
-  int32_t R;
-  int64_t rows;
+  int32_t R, RC;
   const uint16_t *base;
   uint16_t *dx, *du, *dv;
-  // workgroups: dx [tiles][K blocks of 256], then dU and dV [slots][column tiles
-  // of 64][groups of 16 JF ranks]
+  // sums of a cut of a slot's tokens: float [cuts][part], dU's elements, then from vat on dV's
+  float *parts;
+  int64_t part, vat;
+  int32_t cuts;
+  // workgroups: dU and dV [slots][cuts][groups of 16 JF ranks][column tiles of 64, or four
+  // of them], then dx [K blocks of 256][half tiles]
   int32_t tiles, kblocks;
   int32_t jgroups;              // groups of ranks of a child
   int32_t ublock0[kMaxChildren + 1], vblocks;  // column tiles of the children's rows (running), of K
-  int64_t units[3];             // dx, dU, dV
+  int64_t units[3];             // dU, dV, dx
 };
 
-// dx of one tile: a wave takes 64 k.  V^T rows of 32 ranks at a time go through
-// the wave's piece of LDS.
-__device__ __forceinline__ void dx_unit(const GradArgs &a, int id, uint8_t *lds, int *tok) {
+// dx of 32 of a tile's tokens by 256 k, 64 a wave.  V^T rows of 32 ranks at a time and
+// the sums pass through the wave's piece of LDS; base and dx move as 128 bytes a token.
+__device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *lds, int *tok) {
   Tile t;
-  if (!get_tile<kM>(a.s, id / a.kblocks, t, tok)) return;
-  constexpr int PITCH = 160;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int k0 = (id % a.kblocks * 4 + wave) * 64;
-  if (k0 >= a.K) return;
-  lds_u8 *piece = (lds_u8 *)lds + wave * (32 * PITCH);
+  const int place0 = static_cast<int>(id % a.tiles), m0 = static_cast<int>(id / a.tiles % 2) * 32, kb = static_cast<int>(id / a.tiles / 2);
+  if (!get_tile<kM>(a.s, place0, t, tok) || m0 >= t.count) return;
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
+  const int k0 = (kb * kGradWaves + wave) * 64, K = a.K;
+  if (k0 >= K) return;
+  uint8_t *const piece = lds + wave * kPiece;
+  const int orow = lane >> 3, ocol = (lane & 7) * 8;
+  const bool in = k0 + ocol < K;
   const u32x4 zero{0u, 0u, 0u, 0u};
-  u32x4 b[kMF][2];
-  int64_t at[kMF];
+  u32x4 b[2][2];
+  int64_t at[2][2];
 #pragma unroll
-  for (int i = 0; i < kMF; ++i) {
-    const int token = tok[16 * i + r16];
-    at[i] = token < 0 ? -1 : static_cast<int64_t>(token) * a.K + k0 + 8 * g;
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      b[i][h] = token >= 0 && k0 + 32 * h + 8 * g < a.K ? ld16(a.base + at[i] + 32 * h) : zero;
-  }
+    for (int q = 0; q < 2; ++q) {
+      const int token = tok[m0 + 16 * i + 8 * q + orow];
+      at[i][q] = static_cast<int64_t>(token < 0 ? tok[0] : token) * K + (in ? k0 + ocol : 0);
+      b[i][q] = ld16(a.base + at[i][q]);
+    }
   if (t.slot >= 0) {
-    f32x4 acc[4][kMF];
+    f32x4 acc[4][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < kMF; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int64_t row0 = static_cast<int64_t>(id / a.kblocks) * kM;
+      for (int i = 0; i < 2; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int chunks = (t.rank16 + 31) / 32, steps = a.nchild * chunks;
-    u32x4 vv[4], gv[kMF][2];
+    const uint16_t *v0 = a.vt + static_cast<int64_t>(t.slot) * a.R * K;
+    const uint16_t *g0 = a.grows + (static_cast<int64_t>(place0) * 4 + m0 / 16) * a.nchild * a.RC * 1024;
+    const uint32_t col = (in ? k0 + ocol : 0) * 2u;
+    u32x4 vv[4], gv[2][2];
     auto load = [&](int step) {
-      const int j0 = step % chunks * 32, c0 = step / chunks * a.s.r;
+      const int ch = step % chunks, c = step / chunks;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = q * 8 + (lane >> 3), k = k0 + (lane & 7) * 8;
-        vv[q] = step < steps && j0 + row < t.rank && k < a.K
-                    ? ld16(a.vt + (static_cast<int64_t>(t.slot) * a.R + c0 + j0 + row) * a.K + k) : zero;
-      }
+      for (int q = 0; q < 4; ++q)  // (rows past the rank repeat the last and are zeroed)
+        vv[q] = ld16_at(v0, static_cast<uint32_t>(c * a.s.r + min(ch * 32 + q * 8 + orow, t.rank - 1)) * static_cast<uint32_t>(K) * 2u + col);
 #pragma unroll
-      for (int i = 0; i < kMF; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          gv[i][h] = step < steps && j0 + 8 * g < t.rank16
-                         ? ld16(a.grows + ((row0 + 16 * i + r16) * 2 + h) * a.R + c0 + j0 + 8 * g) : zero;
+        for (int p = 0; p < 2; ++p) gv[i][p] = ld16_at(g0 + ((i * a.nchild * a.RC + c * a.RC + ch) * 2 + p) * 512, lane * 16u);
     };
     load(0);
     for (int step = 0; step < steps; ++step) {
+      const int left = t.rank - step % chunks * 32;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) *(lds_u32x4 *)(piece + place(q * 8 + (lane >> 3)) * PITCH + (lane & 7) * 16) = vv[q];
-      u32x4 gg[kMF][2];
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x4 *>(piece + place(q * 8 + orow) * kPitch + (lane & 7) * 16) = in && q * 8 + orow < left ? vv[q] : zero;
+      u32x4 gg[2][2];
 #pragma unroll
-      for (int i = 0; i < kMF; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) gg[i][h] = gv[i][h];
-      load(step + 1);
+        for (int p = 0; p < 2; ++p) gg[i][p] = gv[i][p];
+      load(min(step + 1, steps - 1));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const u32x4 av = read_transposed<PITCH>(piece, 0, 64 * (j >> 1) + 16 * (r16 & 3) + 8 * (j & 1));
+        const u32x4 v = read_transposed<kPitch>(piece, 0, 32 * j + 8 * (r16 & 3));
 #pragma unroll
-        for (int i = 0; i < kMF; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) acc[j][i] = mfma16x16x32(av, gg[i][h], acc[j][i]);
+          for (int p = 0; p < 2; ++p) acc[j][i] = mfma16x16x32(v, gg[i][p], acc[j][i]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kMF; ++i)
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) b[i][h] = add_8(b[i][h], acc[2 * h][i], acc[2 * h + 1][i]);
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(piece + r16 * kOutPitch + (16 * j + 4 * g) * 4) = acc[j][i];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const f32x4 *o = reinterpret_cast<const f32x4 *>(piece + (8 * q + orow) * kOutPitch + ocol * 4);
+        b[i][q] = add_8(b[i][q], o[0], o[1]);
+      }
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kMF; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (at[i] >= 0 && k0 + 32 * h + 8 * g < a.K) *reinterpret_cast<u32x4 *>(a.dx + at[i] + 32 * h) = b[i][h];
+    for (int q = 0; q < 2; ++q)
+      if (in && m0 + 16 * i + 8 * q + orow < t.count) *reinterpret_cast<u32x4 *>(a.dx + at[i][q]) = b[i][q];
 }
 
-// 64 columns of dy (VGRAD false: dU) or of X (dV) by 16 JF ranks of one slot: the
-// sum over its tokens, 32 at a time, taken in turn by the four waves.
-template <int JF, bool VGRAD>
+// The sum over a slot's tokens for 64 columns of dy (dU) or of X (VGRAD: dV), by 16 JF
+// ranks: 32 positions a step, every stride-th one from `from` on.  FULL: 64 columns exist.
+template <int JF, bool VGRAD, bool FULL>
+__device__ __forceinline__ void sum_tokens(const GradArgs &a, int slot, int c, int j0, int col0, int cols, int from, int stride, uint8_t *piece,
+                                           f32x4 (&acc)[4][JF]) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15;
+  const int count = keep(a.count[slot]), tile0 = keep(a.first[slot]), ntiles = keep(*a.total);
+  const int steps = (count + 31) / 32, RT = a.R / 16, col = col0 + (lane & 7) * 8;
+  const u32x4 zero{0u, 0u, 0u, 0u};
+  // the thin operand's pieces, from column tile (c r + j0) / 16 of z or g on
+  const uint16_t *thin = (VGRAD ? a.gT : a.zT) + static_cast<int64_t>((c * a.s.r + j0) / 16) * 1024;
+  struct Rows {  // a step's place (halves of tiles), and the tokens of this lane's rows 8 q + lane / 8
+    int half, token[4];
+  };
+  auto rows = [&](int step, Rows &o) {
+    const bool real = step < steps;
+    const int at = real ? step : from;
+    o.half = tile_place(tile0 + (at >> 1), ntiles) * 2 + (at & 1);
+    const int32_t *p = a.s.perm + static_cast<int64_t>(o.half) * 32 + (lane >> 3);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int token = p[8 * q];
+      o.token[q] = real ? token : -1;
+    }
+  };
+  struct Loaded {
+    u32x4 w[VGRAD ? 1 : 4];
+    u32x2 x[VGRAD ? 4 : 1];
+    uint8_t s[VGRAD ? 4 : 1];
+    u32x4 t[JF][2];
+    uint32_t in;  // bits: the rows that are tokens
+  };
+  auto load = [&](const Rows &rw, Loaded &o) {
+    o.in = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t row = max(rw.token[q], 0);  // (rows without a token are zeroed)
+      o.in |= rw.token[q] >= 0 ? 1u << q : 0u;
+      if constexpr (VGRAD) {
+        const int kk = FULL || col < cols ? col : 0;
+        o.x[q] = *reinterpret_cast<const u32x2 *>(a.x.codes + row * (a.x.nb * kCodeBlock) + kk);
+        o.s[q] = a.x.scales[static_cast<int64_t>(kk / kCodeBlock) * a.x.ldsc + row];
+      } else {
+        const uint16_t *p = a.dy + row * a.Ntot + a.n0[c] + col;
+        o.w[q] = FULL ? ld16_any(p) : load_some(p, cols - col);
+      }
+    }
+    const uint16_t *p = thin + static_cast<int64_t>(rw.half) * RT * 1024;
+#pragma unroll
+    for (int f = 0; f < JF; ++f) {
+      const int ff = j0 + 16 * f < a.s.r ? f : 0;  // (not stored)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) o.t[f][q] = ld16_at(p + ff * 1024 + q * 512, lane * 16u);
+    }
+  };
+  auto put = [&](const Loaded &o) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      u32x4 v;
+      if constexpr (VGRAD)
+        v = expand_codes(o.x[q], o.s[q]);
+      else
+        v = o.w[q];
+      const bool in = (o.in >> q & 1) && (FULL || !VGRAD || col < cols);
+      *reinterpret_cast<u32x4 *>(piece + place(q * 8 + (lane >> 3)) * kPitch + (lane & 7) * 16) = in ? v : zero;
+    }
+  };
+  if (from >= steps) return;
+  Rows next;
+  Loaded l;
+  rows(from, next);
+  load(next, l);
+  rows(from + stride, next);
+  for (int step = from; step < steps; step += stride) {
+    put(l);
+    u32x4 t[JF][2];
+#pragma unroll
+    for (int f = 0; f < JF; ++f)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) t[f][q] = l.t[f][q];
+    load(next, l);
+    rows(step + 2 * stride, next);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // dV: 8 neighbouring k of a row end up in two accumulators of a lane
+      const u32x4 w = read_transposed<kPitch>(piece, 0, VGRAD ? 64 * (i >> 1) + 16 * (r16 & 3) + 8 * (i & 1) : 32 * i + 8 * (r16 & 3));
+#pragma unroll
+      for (int f = 0; f < JF; ++f)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          acc[i][f] = VGRAD ? mfma16x16x32(w, t[f][q], acc[i][f]) : mfma16x16x32(t[f][q], w, acc[i][f]);
+    }
+  }
+}
+
+// WAYS 1: a wave has its own column tile; 4: the waves of a.cuts workgroups share one, a
+// part of the tokens each; with more than one cut their sums leave as floats.
+template <int JF, bool VGRAD, int WAYS>
 __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds) {
-  constexpr int PITCH = 160;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
   const int r = a.s.r;
   // column tiles fastest: the tiles of a slot run together
-  const int ctiles = VGRAD ? a.nchild * a.vblocks : a.ublock0[a.nchild];
+  const int blocks = VGRAD ? a.nchild * a.vblocks : a.ublock0[a.nchild], ctiles = (blocks * WAYS + 3) / 4;
   int ct = static_cast<int>(id % ctiles);
   const int64_t rest = id / ctiles;
-  const int j0 = static_cast<int>(rest % a.jgroups) * JF * 16, slot = static_cast<int>(rest / a.jgroups);
+  const int j0 = static_cast<int>(rest % a.jgroups) * JF * 16, sc = static_cast<int>(rest / a.jgroups), slot = sc / a.cuts, cut = sc % a.cuts;
+  if constexpr (WAYS == 1) {
+    ct = ct * 4 + wave;
+    if (ct >= blocks) return;
+  }
   int c = 0;
   if constexpr (VGRAD) {
     c = ct / a.vblocks;
@@ -378,118 +680,117 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
     ct -= a.ublock0[c];
   }
   const int col0 = ct * 64, cols = VGRAD ? a.K : a.N[c];
-  const int count = a.count[slot];
-  const int tile0 = a.first[slot], ntiles = *a.total;
-  lds_u8 *piece = (lds_u8 *)lds + wave * (32 * PITCH);
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  // the thin operand, from column c * r + j0 of z (dU) or g (dV) on
-  const uint16_t *thin = (VGRAD ? a.gT : a.zT) + (static_cast<int64_t>(c) * r + j0) * a.rows;
-  const int64_t lo = static_cast<int64_t>(a.R) * a.rows;
   f32x4 acc[4][JF];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int f = 0; f < JF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int steps = (count + 31) / 32;
-  u32x4 wv[4], tv[JF][2];
-  int token[4];  // of the step after the one in wv
-  auto tokens = [&](int step) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      token[q] = step < steps ? a.s.perm[static_cast<int64_t>(tile_place(tile0 + step, ntiles)) * kM + q * 8 + (lane >> 3)] : -1;
-  };
-  auto load = [&](int step) {
-    const int k = col0 + (lane & 7) * 8;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      wv[q] = zero;
-      if (token[q] >= 0 && k < cols) {
-        if constexpr (VGRAD)
-          wv[q] = expand8(a.x, token[q], k);
-        else
-          wv[q] = load_some(a.dy + static_cast<int64_t>(token[q]) * a.Ntot + a.n0[c] + k, cols - k);
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < JF; ++f)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        tv[f][h] = step < steps && j0 + 16 * f < r
-                       ? ld16(thin + h * lo + (16 * f + r16) * a.rows + static_cast<int64_t>(tile_place(tile0 + step, ntiles)) * kM + 8 * g) : zero;
-  };
-  tokens(wave);
-  load(wave);
-  tokens(wave + 4);
-  for (int step = wave; step < steps; step += 4) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) *(lds_u32x4 *)(piece + place(q * 8 + (lane >> 3)) * PITCH + (lane & 7) * 16) = wv[q];
-    u32x4 tt[JF][2];
-#pragma unroll
-    for (int f = 0; f < JF; ++f)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tt[f][h] = tv[f][h];
-    load(step + 4);
-    tokens(step + 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // dV: 8 neighbouring k of a row end up in two accumulators of a lane
-      const u32x4 w = read_transposed<PITCH>(piece, 0, VGRAD ? 64 * (i >> 1) + 16 * (r16 & 3) + 8 * (i & 1) : 32 * i + 8 * (r16 & 3));
-#pragma unroll
-      for (int f = 0; f < JF; ++f)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[i][f] = VGRAD ? mfma16x16x32(w, tt[f][h], acc[i][f]) : mfma16x16x32(tt[f][h], w, acc[i][f]);
-    }
-  }
-  // the waves' sums: two rank tiles at a time through LDS, in wave order
-  constexpr int JC = JF < 2 ? JF : 2;
-  f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [4 waves][4 column tiles][JC][64]
-  for (int f0 = 0; f0 < JF; f0 += JC) {
-    __syncthreads();
-#pragma unroll
-    for (int f = 0; f < JF; ++f)
-      if (f >= f0 && f < f0 + JC)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[((wave * 4 + i) * JC + f - f0) * 64 + lane] = acc[i][f];
-    __syncthreads();
-    const int f = f0 + (wave >> 1);
-    if ((wave >> 1) >= JC || j0 + 16 * f >= r) continue;
-    f32x4 s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 *p = part + ((2 * (wave & 1) + h) * JC + (wave >> 1)) * 64 + lane;
-      s[h] = p[0];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) s[h] += p[w * 4 * JC * 64];
-    }
+  uint8_t *const piece = lds + wave * kPiece;
+  const int from = WAYS == 1 ? 0 : cut * 4 + wave, stride = WAYS == 1 ? 1 : 4 * a.cuts;
+  if (col0 + 64 <= cols)
+    sum_tokens<JF, VGRAD, true>(a, slot, c, j0, col0, cols, from, stride, piece, acc);
+  else
+    sum_tokens<JF, VGRAD, false>(a, slot, c, j0, col0, cols, from, stride, piece, acc);
+  // zeros past the slot's rank, also where dy is not finite
+  const int rank = slot_rank(a.s.rank, r, slot);
+  // two neighbouring column tiles of rank tile f to memory
+  auto store = [&](f32x4 (&s)[2], int pair, int f) {
+    if (j0 + 16 * f >= r) return;
     if constexpr (VGRAD) {
-      const int k = col0 + 32 * (wave & 1) + 8 * g, j = c * r + j0 + 16 * f + r16;
-      if (k < a.K)
-        *reinterpret_cast<u32x4 *>(a.dv + (static_cast<int64_t>(slot) * a.R + j) * a.K + k) =
+      const int k = col0 + 32 * pair + 8 * g, j = j0 + 16 * f + r16;
+      if (j >= rank) s[0] = s[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int64_t at = (static_cast<int64_t>(slot) * a.R + c * r + j) * a.K + k;
+      if (k >= a.K) return;
+      if (WAYS == 4 && a.cuts > 1) {
+        f32x4 *o = reinterpret_cast<f32x4 *>(a.parts + cut * a.part + a.vat + at);
+        o[0] = s[0];
+        o[1] = s[1];
+      } else {
+        *reinterpret_cast<u32x4 *>(a.dv + at) =
             u32x4{pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
+      }
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int n = col0 + 16 * (2 * (wave & 1) + h) + r16;
-        if (n < cols)
-          *reinterpret_cast<u32x2 *>(a.du + (static_cast<int64_t>(slot) * a.Ntot + a.n0[c] + n) * r + j0 + 16 * f + 4 * g) =
-              u32x2{pack_bf16(s[h][0], s[h][1]), pack_bf16(s[h][2], s[h][3])};
+        const int n = col0 + 16 * (2 * pair + h) + r16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[h][k] = j0 + 16 * f + 4 * g + k < rank ? s[h][k] : 0.f;
+        const int64_t at = (static_cast<int64_t>(slot) * a.Ntot + a.n0[c] + n) * r + j0 + 16 * f + 4 * g;
+        if (n >= cols) continue;
+        if (WAYS == 4 && a.cuts > 1)
+          *reinterpret_cast<f32x4 *>(a.parts + cut * a.part + at) = s[h];
+        else
+          *reinterpret_cast<u32x2 *>(a.du + at) = u32x2{pack_bf16(s[h][0], s[h][1]), pack_bf16(s[h][2], s[h][3])};
       }
+    }
+  };
+  if constexpr (WAYS == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+#pragma unroll
+      for (int f = 0; f < JF; ++f) {
+        f32x4 s[2] = {acc[i][f], acc[i + 1][f]};
+        store(s, i / 2, f);
+      }
+  } else {
+    // the waves' sums: two rank tiles at a time through LDS, in wave order
+    constexpr int JC = JF < 2 ? JF : 2;
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [4 waves][4 column tiles][JC][64]
+#pragma unroll
+    for (int f0 = 0; f0 < JF; f0 += JC) {
+      __syncthreads();
+#pragma unroll
+      for (int f = 0; f < JC; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[((wave * 4 + i) * JC + f) * 64 + lane] = acc[i][f0 + f];
+      __syncthreads();
+      if ((wave >> 1) >= JC) continue;
+      f32x4 s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 *p = part + ((2 * (wave & 1) + h) * JC + (wave >> 1)) * 64 + lane;
+        s[h] = p[0];
+#pragma unroll
+        for (int w = 1; w < kGradWaves; ++w) s[h] += p[w * 4 * JC * 64];
+      }
+      store(s, wave & 1, f0 + (wave >> 1));
     }
   }
 }
 
-template <int JF>
-__global__ __launch_bounds__(256) void gradient_kernel(GradArgs a) {
-  constexpr int SUM = 4 * 4 * (JF < 2 ? JF : 2) * 1024, PIECES = 4 * 32 * 160;
+template <int JF, int WAYS>
+__global__ __launch_bounds__(kGradWaves * 64, JF == 4 ? 2 : 4) void gradient_kernel(GradArgs a) {
+  constexpr int SUM = WAYS == 1 ? 0 : kGradWaves * 4 * (JF < 2 ? JF : 2) * 1024, PIECES = kGradWaves * kPiece;
   __shared__ int tok[kM];
   __shared__ __align__(16) uint8_t lds[SUM > PIECES ? SUM : PIECES];
   int64_t id = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-  if (id >= a.units[0] + a.units[1] + a.units[2]) return;
-  if (id < a.units[0]) return dx_unit(a, static_cast<int>(id), lds, tok);
+  if (id < a.units[0]) return weight_unit<JF, false, WAYS>(a, id, lds);
   id -= a.units[0];
-  if (id < a.units[1]) return weight_unit<JF, false>(a, id, lds);
-  weight_unit<JF, true>(a, id - a.units[1], lds);
+  if (id < a.units[1]) return weight_unit<JF, true, WAYS>(a, id, lds);
+  id -= a.units[1];
+  if (id < a.units[2]) dx_unit(a, id, lds, tok);
+}
+
+// dU and dV from the cuts' sums, in order.
+struct JoinArgs {
+  const float *parts;
+  int64_t part, vat;
+  int32_t cuts;
+  uint16_t *du, *dv;
+};
+
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < a.part; i += static_cast<int64_t>(gridDim.x) * 2048) {
+    f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 4
+    for (int c = 0; c < a.cuts; ++c) {
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.parts + c * a.part + i);
+      s[0] += p[0];
+      s[1] += p[1];
+    }
+    *reinterpret_cast<u32x4 *>(i < a.vat ? a.du + i : a.dv + (i - a.vat)) =
+        u32x4{pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
+  }
 }
 
 __global__ __launch_bounds__(256) void fill_zero_16(u32x4 *p, int64_t n) {
@@ -497,10 +798,13 @@ __global__ __launch_bounds__(256) void fill_zero_16(u32x4 *p, int64_t n) {
     p[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
+// ---- plan -----------------------------------------------------------------------------------
 struct BackPlan {
-  int tiles, NF, zgroups, zslices, zper, ggroups, gslices, gper;
-  int64_t rows;
-  size_t perm_at, slots_at, pz_at, pg_at, zt_at, gt_at, grows_at, bytes;
+  int tiles, NF, zgroups, zslices, zper, ggroups, gslices, gper, RC;
+  int ublock0[kMaxChildren + 1], vblocks, cuts;
+  bool own;  // gradient_kernel's waves have column tiles of their own
+  int64_t rows, u_elements, v_elements;
+  size_t perm_at, slots_at, pz_at, pg_at, zt_at, gt_at, grows_at, parts_at, bytes;
 };
 
 BackPlan make_back_plan(const AdapterPool &p, int T) {
@@ -508,20 +812,36 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
   q.tiles = tile_places(T / kM + std::min(p.n + 1, T));
   q.rows = static_cast<int64_t>(q.tiles) * kM;
   const int row_tiles = p.r / 16, R = p.nchild * p.r;
-  q.NF = row_tiles >= 8 ? 8 : row_tiles >= 3 ? 4 : row_tiles;
+  q.NF = row_tiles >= 3 ? 4 : row_tiles;
   q.zgroups = (p.nchild * row_tiles + q.NF - 1) / q.NF;
   q.ggroups = (row_tiles + q.NF - 1) / q.NF;
+  q.RC = (p.r + 31) / 32;
   int widest = 0;
   for (int c = 0; c < p.nchild; ++c) widest = std::max(widest, p.N[c]);
-  const int zsteps = (p.K + 63) / 64, rows = q.NF == 8 ? 32 : 64, gsteps = (widest + rows - 1) / rows;
-  const int busy = (T + kM - 1) / kM;
-  auto cut = [&](int steps, int workgroups, int &slices, int &per) {
-    const int want = std::min({8, (4 * kCUs + workgroups - 1) / workgroups, (steps + 3) / 4});
-    per = (steps + want - 1) / want;
-    slices = (steps + per - 1) / per;
+  const int stage = q.NF == 4 ? 64 : 128, busy = (T + kM - 1) / kM;
+  // Slices until there are some workgroups for every CU, none shorter than twice the
+  // stages under way: one slice alone needs no finish_kernel (77 tokens, 712 -> 1001: 21.1
+  // -> 18.0 us; 2048 tokens through 1B q|k|v 31.2 -> 26.3).
+  auto cut = [&](int length, int workgroups, int most, int &slices, int &per) {
+    const int stages = (length + stage - 1) / stage;
+    const int want = std::max(1, std::min({most, (3 * kCUs / 2 + workgroups - 1) / workgroups, stages / (2 * kDeep)}));
+    per = (stages + want - 1) / want * stage;
+    slices = (length + per - 1) / per;
   };
-  cut(zsteps, busy * q.zgroups, q.zslices, q.zper);
-  cut(gsteps, busy * q.ggroups * p.nchild, q.gslices, q.gper);
+  cut(p.K, busy * q.zgroups, 4, q.zslices, q.zper);
+  cut(widest, busy * q.ggroups * p.nchild, 8, q.gslices, q.gper);
+  for (int c = 0; c < p.nchild; ++c) q.ublock0[c + 1] = q.ublock0[c] + (p.N[c] + 63) / 64;
+  q.vblocks = (p.K + 63) / 64;
+  const int64_t blocks = static_cast<int64_t>(p.n) * q.ggroups * (q.ublock0[p.nchild] + p.nchild * q.vblocks);
+  // Column tiles of their own save the waves the sums between them, where there are many
+  // (16 adapters of 31B gate|up 134 -> 109 us, 32 of 8192 -> 5376 at rank 64 100 -> 75; but
+  // 8 of 2048 -> 4096, 768 tiles, 12.2 -> 20.0, one of 31B gate|up, 840, 108 -> 133).
+  // With few, the tokens are cut until 4 workgroups of a CU are busy and a wave has 8 steps
+  // (8192 tokens of one 1B q|k|v adapter: 53 -> 27 us and 4 for the joining).
+  q.own = blocks >= 4096;
+  q.cuts = q.own ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 4 * kCUs / blocks, T / (static_cast<int64_t>(p.n) * 128) / 8})));
+  q.u_elements = static_cast<int64_t>(p.n) * p.Ntot * p.r;
+  q.v_elements = static_cast<int64_t>(p.n) * R * p.K;
   size_t at = align256(sizeof(int4) * q.tiles);  // the tiles come first
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -534,7 +854,8 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
   q.pg_at = take(sizeof(float) * q.gslices * q.rows * R);
   q.zt_at = take(2 * sizeof(uint16_t) * q.rows * R);
   q.gt_at = take(2 * sizeof(uint16_t) * q.rows * R);
-  q.grows_at = take(2 * sizeof(uint16_t) * q.rows * R);
+  q.grows_at = take(2 * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32);
+  q.parts_at = take(q.cuts > 1 ? sizeof(float) * q.cuts * (q.u_elements + q.v_elements) : 0);
   q.bytes = at;
   return q;
 }
@@ -545,15 +866,14 @@ size_t adapters_backward_workspace_bytes(const AdapterPool &p, int T) { return T
 
 hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, const uint16_t *dy, const int32_t *index, int T,
                                     const AdapterGrads &o, void *ws, hipStream_t stream) {
-  const size_t ub = static_cast<size_t>(p.n) * p.Ntot * p.r * 2, vb = static_cast<size_t>(p.n) * p.nchild * p.r * p.K * 2;
   if (T == 0) {
     if (!o.du && !o.dv) return hipSuccess;
-    auto clear = [&](uint16_t *out, size_t bytes) {
-      const int64_t n = static_cast<int64_t>(bytes / 16);
+    auto clear = [&](uint16_t *out, int64_t elements) {
+      const int64_t n = elements / 8;
       if (out) fill_zero_16<<<static_cast<uint32_t>(std::min<int64_t>((n + 255) / 256, 8 * kCUs)), 256, 0, stream>>>(reinterpret_cast<u32x4 *>(out), n);
     };
-    clear(o.du, ub);
-    clear(o.dv, vb);
+    clear(o.du, static_cast<int64_t>(p.n) * p.Ntot * p.r);
+    clear(o.dv, static_cast<int64_t>(p.n) * p.nchild * p.r * p.K);
     return hipGetLastError();
   }
   const BackPlan q = make_back_plan(p, T);
@@ -574,8 +894,7 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   gr.first = reinterpret_cast<int32_t *>(w + q.slots_at);
   gr.count = gr.first + p.n;
   gr.total = gr.count + p.n;
-  group_kernel<kM><<<group_workgroups(p.n), kGroupWaves * 64, 0, stream>>>(gr);
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch_group<kM>(gr, stream);
   if (e != hipSuccess) return e;
   s.tiles = gr.tiles;
   s.perm = gr.perm;
@@ -604,28 +923,34 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   a.gper = q.gper;
   a.Pz = reinterpret_cast<float *>(w + q.pz_at);
   a.Pg = reinterpret_cast<float *>(w + q.pg_at);
+  a.out.scale = p.scale;
+  a.out.T[0] = reinterpret_cast<uint16_t *>(w + q.zt_at);
+  a.out.T[1] = o.dv ? reinterpret_cast<uint16_t *>(w + q.gt_at) : nullptr;
+  a.out.grows = o.dx ? reinterpret_cast<uint16_t *>(w + q.grows_at) : nullptr;
+  a.out.RT = R / 16;
+  a.out.nchild = p.nchild;
+  a.out.RC = q.RC;
   const dim3 grid(q.tiles, a.zgroups * a.zslices + a.ggroups * p.nchild * a.gslices);
-  switch (q.NF) {
-    case 1: project_kernel<1><<<grid, 256, 0, stream>>>(a); break;
-    case 2: project_kernel<2><<<grid, 256, 0, stream>>>(a); break;
-    case 4: project_kernel<4><<<grid, 256, 0, stream>>>(a); break;
-    default: project_kernel<8><<<grid, 256, 0, stream>>>(a); break;
+  if (q.NF == 1)
+    project_kernel<1><<<grid, kThreads, 0, stream>>>(a);
+  else if (q.NF == 2)
+    project_kernel<2><<<grid, kThreads, 0, stream>>>(a);
+  else
+    project_kernel<4><<<grid, kThreads, 0, stream>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.zslices > 1 || a.gslices > 1) {
+    FinishArgs f{};
+    f.s = s;
+    f.P[0] = a.Pz;
+    f.P[1] = a.Pg;
+    f.slices[0] = a.zslices;
+    f.slices[1] = a.gslices;
+    f.R = R;
+    f.rows = q.rows;
+    f.out = a.out;
+    finish_kernel<<<dim3(q.tiles, p.nchild * q.RC, 2), 256, 0, stream>>>(f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  FinishArgs f{};
-  f.s = s;
-  f.scale = p.scale;
-  f.P[0] = a.Pz;
-  f.P[1] = a.Pg;
-  f.slices[0] = a.zslices;
-  f.slices[1] = a.gslices;
-  f.R = R;
-  f.rows = q.rows;
-  f.T[0] = reinterpret_cast<uint16_t *>(w + q.zt_at);
-  f.T[1] = o.dv ? reinterpret_cast<uint16_t *>(w + q.gt_at) : nullptr;
-  f.grows = o.dx ? reinterpret_cast<uint16_t *>(w + q.grows_at) : nullptr;
-  finish_kernel<<<dim3(q.tiles, (R + 31) / 32, 2), 256, 0, stream>>>(f);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   GradArgs d{};
   d.s = s;
   d.first = gr.first;
@@ -634,41 +959,60 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   d.x = x;
   d.vt = p.vt;
   d.dy = dy;
-  d.zT = f.T[0];
-  d.gT = reinterpret_cast<uint16_t *>(w + q.gt_at);
-  d.grows = f.grows;
+  d.zT = a.out.T[0];
+  d.gT = a.out.T[1];
+  d.grows = a.out.grows;
   d.K = p.K;
   d.Ntot = p.Ntot;
   d.nchild = p.nchild;
   d.R = R;
-  d.rows = q.rows;
+  d.RC = q.RC;
   d.base = o.base;
   d.dx = o.dx;
   d.du = o.du;
   d.dv = o.dv;
   d.tiles = q.tiles;
   d.kblocks = (p.K + 255) / 256;
-  d.vblocks = (p.K + 63) / 64;
+  d.vblocks = q.vblocks;
+  for (int c = 0; c <= p.nchild; ++c) d.ublock0[c] = q.ublock0[c];
   for (int c = 0; c < p.nchild; ++c) {
     d.N[c] = a.N[c];
     d.n0[c] = a.n0[c];
-    d.ublock0[c + 1] = d.ublock0[c] + (p.N[c] + 63) / 64;
   }
-  const int JF = q.NF;
   d.jgroups = q.ggroups;
-  d.units[0] = o.dx ? static_cast<int64_t>(q.tiles) * d.kblocks : 0;
-  d.units[1] = o.du ? static_cast<int64_t>(p.n) * d.jgroups * d.ublock0[p.nchild] : 0;
-  d.units[2] = o.dv ? static_cast<int64_t>(p.n) * d.jgroups * p.nchild * d.vblocks : 0;
+  d.cuts = q.cuts;
+  d.parts = reinterpret_cast<float *>(w + q.parts_at);
+  d.vat = o.du ? q.u_elements : 0;
+  d.part = d.vat + (o.dv ? q.v_elements : 0);
+  auto units = [&](int blocks) { return static_cast<int64_t>(p.n) * d.jgroups * (q.own ? (blocks + 3) / 4 : blocks * d.cuts); };
+  d.units[0] = o.du ? units(d.ublock0[p.nchild]) : 0;
+  d.units[1] = o.dv ? units(p.nchild * d.vblocks) : 0;
+  d.units[2] = o.dx ? static_cast<int64_t>(q.tiles) * 2 * d.kblocks : 0;
   const int64_t total = d.units[0] + d.units[1] + d.units[2];
   // (a launch holds fewer than 2^32 threads along x)
   constexpr int64_t kAcross = int64_t{1} << 20;
   const dim3 blocks(static_cast<uint32_t>(std::min(total, kAcross)), static_cast<uint32_t>((total + kAcross - 1) / kAcross));
-  switch (JF) {
-    case 1: gradient_kernel<1><<<blocks, 256, 0, stream>>>(d); break;
-    case 2: gradient_kernel<2><<<blocks, 256, 0, stream>>>(d); break;
-    case 4: gradient_kernel<4><<<blocks, 256, 0, stream>>>(d); break;
-    default: gradient_kernel<8><<<blocks, 256, 0, stream>>>(d); break;
-  }
+  auto run = [&](auto jf) {
+    if (q.own)
+      gradient_kernel<decltype(jf)::value, 1><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+    else
+      gradient_kernel<decltype(jf)::value, 4><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+  };
+  if (q.NF == 1)
+    run(std::integral_constant<int, 1>{});
+  else if (q.NF == 2)
+    run(std::integral_constant<int, 2>{});
+  else
+    run(std::integral_constant<int, 4>{});
+  if ((e = hipGetLastError()) != hipSuccess || q.cuts == 1 || d.part == 0) return e;
+  JoinArgs j{};
+  j.parts = d.parts;
+  j.part = d.part;
+  j.vat = d.vat;
+  j.cuts = d.cuts;
+  j.du = o.du;
+  j.dv = o.dv;
+  join_kernel<<<static_cast<uint32_t>(std::min<int64_t>((d.part + 2047) / 2048, 8 * kCUs)), 256, 0, stream>>>(j);
   return hipGetLastError();
 }
 
