@@ -119,6 +119,17 @@ def test_add(gpu_lib, T, rows, K, r, n, ranked):
     assert p.add(x, index, again, y=again) is again and torch.equal(again.view(torch.int16), y.view(torch.int16))
 
 
+LONG = [  # enough rows for whole tiles of tokens: K cut into slices, and short
+    (2100, (4100,), 1032, 16, 3), (1100, (3000, 4700), 696, 64, 3), (600, (14000,), 520, 128, 2), (1100, (8200,), 520, 256, 2),
+    (2100, (4100,), 64, 32, 3), (1100, (8200,), 72, 48, 2), (700, (12000,), 8, 112, 2), (1100, (8200,), 136, 176, 2), (600, (264,), 264, 16, 600)]
+
+
+@pytest.mark.parametrize("T,rows,K,r,n", LONG)
+@pytest.mark.parametrize("ranked", [False, True])
+def test_add_long(gpu_lib, T, rows, K, r, n, ranked):
+    test_add(gpu_lib, T, rows, K, r, n, ranked)
+
+
 @pytest.mark.parametrize("T", [1, 16, 40, 256, 257, 700])
 @pytest.mark.parametrize("kind", ["none", "one", "last", "sorted"])
 def test_index_patterns(gpu_lib, T, kind):

@@ -29,18 +29,13 @@
 //
 // What bounds it: few tokens, reading the adapters in use; many, reading and
 // writing base and y.  The products are far below the matrix cores' rate.
-#include <type_traits>
-
-#include "adapter_tiles.h"
+#include "adapter_factors.h"
 
 namespace wl {
 
 namespace {
 
-constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int kTileM = 16;   // tokens of a tile of a call of few tokens
-constexpr int kGroupM = 64;  // and of a grouped one
-constexpr int kDeep = 4;     // stages of x and V^T under way
+constexpr int kTileM = 16;  // tokens of a tile of a call of few tokens
 
 struct AdapterArgs {
   TileSource s;
@@ -50,9 +45,11 @@ struct AdapterArgs {
   const float *scale;    // [n]
   const uint16_t *base;  // [T][Ntot]
   uint16_t *y;           // [T][Ntot]
-  float *P;              // grouped calls: z [slices][rows][R]
+  const float *P;        // grouped calls: z [slices][rows][R]
   int64_t rows;
-  int32_t R, slices, per;                     // R: nchild * r; per: k of a slice
+  int32_t R, slices;     // R: nchild * r
+  const uint16_t *z;     // or c z, the rows of Factors, of RC chunks of a child
+  int32_t RC;
   int32_t K, Ntot, nchild, turns;             // turns: times a wave takes 64 rows of U
   int32_t N[kMaxChildren], n0[kMaxChildren];  // rows and first row of a child
   int32_t block0[kMaxChildren];               // first workgroup (y) of a child
@@ -516,151 +513,33 @@ __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(Adapt
 }
 
 // ---- many tokens -------------------------------------------------------------------
-// P[slice][row][col] = sum over the slice's k of V^T[col][k] x[token][k], the rows of
-// V^T of all children, up to 16 NF of them a workgroup.  Stages as in form_z; a wave
-// multiplies two row tiles (one where there is no more) and 32 tokens over 32 k.
 template <int NF>
-__global__ __launch_bounds__(kThreads) void thin_kernel(AdapterArgs a) {
-  constexpr int M = kGroupM, KS = NF == 4 ? 64 : 128, SUBS = KS / 64;
-  constexpr int XB = SUBS * M * 128, AB = SUBS * NF * 2048, STAGE = XB + AB;
-  constexpr int FP = NF == 4 ? 2 : 1, FR = NF == 1 ? 1 : 2, H = kWaves / (2 * FP);  // pairs of row tiles, tiles of a wave, waves along k
-  static_assert(H * 32 == KS && XB == SUBS * kThreads * 16, "stage shape");
-  __shared__ int tok[M];
-  __shared__ __align__(16) uint8_t lds[2 * STAGE];
-  static_assert(kWaves * FR * 2 * 1024 <= 2 * STAGE, "the waves' sums lie over the stages");
+__global__ __launch_bounds__(kThreads, 4) void thin_kernel(ProjectArgs a) {
+  __shared__ int tok[kM];
+  __shared__ __align__(16) uint8_t lds[Stage<NF>::LDS];
   Tile t;
-  if (!get_tile<M>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6);
-  const int r16 = lane & 15, g = lane >> 4, K = a.K;
-  const int per_child = t.rank16 / 16, live = a.nchild * per_child, f0 = blockIdx.z * NF;
-  if (f0 >= live) return;
-  auto column = [&](int f) {  // first row of V^T (column of P) of row tile f0 + f; those past the last repeat it
-    const int v = min(f0 + f, live - 1);
-    return v / per_child * a.s.r + v % per_child * 16;
-  };
-  const u32x4 zero{0u, 0u, 0u, 0u};
-  const int chunk = threadIdx.x & 7, xrow = threadIdx.x >> 3;
-  const uint16_t *xrowp = a.x + static_cast<int64_t>(tok[xrow] < 0 ? tok[0] : tok[xrow]) * K;
-  const int arow = (threadIdx.x >> 3) % (16 * NF), asub = threadIdx.x / (128 * NF) % SUBS;  // (NF 1: every piece twice)
-  const uint16_t *a0 = a.vt + static_cast<int64_t>(t.slot) * a.R * K;
-  const uint32_t arowb = static_cast<uint32_t>(column(arow >> 4) + (arow & 15)) * static_cast<uint32_t>(K) * 2u;
-  const int ak = asub * 64 + chunk * 8;
-  const uint32_t aoff = arowb + ak * 2u;
-  uint8_t *const xput = lds + xrow * 128 + (chunk ^ (xrow & 7)) * 16;
-  uint8_t *const aput = lds + XB + (asub * 16 * NF + arow) * 128 + (chunk ^ (arow & 7)) * 16;
-  const int fp = wave % FP, ip = wave / FP & 1, h = wave / (2 * FP);
-  const int at = (((4 * h + g) & 7) ^ (r16 & 7)) * 16;  // this wave's 32 k, in 64 k number h / 2
-  const uint8_t *fa = lds + XB + ((h >> 1) * 16 * NF + 16 * FR * fp + r16) * 128 + at, *fx = lds + ((h >> 1) * M + 32 * ip + r16) * 128 + at;
-  f32x4 acc[FR][2];
-#pragma unroll
-  for (int f = 0; f < FR; ++f)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](int buf) {
-    wait_and_sync<63>();  // this stage is in LDS; loads stay under way
-    u32x4 x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const u32x4 *>(fx + buf + i * 2048);
-#pragma unroll
-    for (int f = 0; f < FR; ++f) {
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(fa + buf + f * 2048);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) acc[f][i] = mfma16x16x32(v, x[i], acc[f][i]);
-    }
-  };
-  const int k0 = static_cast<int>(blockIdx.y) * a.per, k1 = min(K, k0 + a.per);
-  const uint16_t *xp = xrowp + k0 + chunk * 8, *ap = a0 + k0;
-  u32x4 xv[kDeep][SUBS], av[kDeep];
-  auto load = [&](int d) {
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) xv[d][s] = ld16(xp + d * KS + s * 64);
-    av[d] = ld16_at(ap + d * KS, aoff);
-  };
-  auto use = [&](int d) {
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) *reinterpret_cast<u32x4 *>(xput + (d & 1) * STAGE + s * M * 128) = xv[d][s];
-    *reinterpret_cast<u32x4 *>(aput + (d & 1) * STAGE) = av[d];
-  };
-  // the last stages: pieces past the slice read its row's first and are zeroed on their way to LDS
-  auto load_last = [&](int k, int d) {
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) xv[d][s] = ld16(xrowp + (k + s * 64 + chunk * 8 < k1 ? k + s * 64 + chunk * 8 : 0));
-    av[d] = ld16_at(a0, arowb + (k + ak < k1 ? (k + ak) * 2u : 0u));
-  };
-  auto use_last = [&](int k, int d) {
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s)
-      *reinterpret_cast<u32x4 *>(xput + (d & 1) * STAGE + s * M * 128) = k + s * 64 + chunk * 8 < k1 ? xv[d][s] : zero;
-    *reinterpret_cast<u32x4 *>(aput + (d & 1) * STAGE) = k + ak < k1 ? av[d] : zero;
-  };
-  const int groups = (k1 - k0) / (KS * kDeep);
-  const int kl = k0 + groups * KS * kDeep;
-  if (groups > 0) {
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) load(d);
-    for (int i = 1; i < groups; ++i) {
-      xp += KS * kDeep;
-      ap += KS * kDeep;
-#pragma unroll
-      for (int d = 0; d < kDeep; ++d) {
-        use(d);
-        load(d);
-        multiply((d & 1) * STAGE);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      use(d);
-      load_last(kl + d * KS, d);
-      multiply((d & 1) * STAGE);
-    }
-  } else {
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) load_last(kl + d * KS, d);
-  }
-#pragma unroll
-  for (int d = 0; d < kDeep; ++d) {
-    if (kl + d * KS >= k1) break;
-    use_last(kl + d * KS, d);
-    multiply((d & 1) * STAGE);
-  }
-  // the sums along k, in wave order
-  f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [wave][FR][2][64]
-  __syncthreads();
-#pragma unroll
-  for (int f = 0; f < FR; ++f)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) part[((wave * FR + f) * 2 + i) * 64 + lane] = acc[f][i];
-  __syncthreads();
-  if (h > 0) return;
-#pragma unroll
-  for (int f = 0; f < FR; ++f)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f32x4 v = acc[f][i];
-#pragma unroll
-      for (int q = 1; q < H; ++q) v += part[(((q * 2 * FP + wave) * FR + f) * 2 + i) * 64 + lane];
-      const int tile = FR * fp + f, m = 32 * ip + 16 * i + r16;
-      if (f0 + tile >= live || m >= t.count) continue;
-      *reinterpret_cast<f32x4 *>(a.P + (blockIdx.y * a.rows + static_cast<int64_t>(blockIdx.x) * M + m) * a.R + column(tile) + g * 4) = v;
-    }
+  if (!get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
+  project_z<NF, false>(a, t, tok, blockIdx.y, lds);
 }
 
 // 16 FRAGS of a tile's 64 tokens by 256 rows of U, 64 a wave, up to 32 CH ranks.  U
 // passes through the wave's piece of LDS into registers, where it serves the tokens,
 // 16 at a time; their sums pass through the piece again.  All of base is under way
-// from the start.
+// from the start.  c z comes from finish_kernel's pieces (PIECES), or each workgroup adds
+// up z's slices into LDS.  (With the next 256 rows sent for while these are worked on,
+// 2 to 6 times: registers for 2 workgroups on a CU, 4096 tokens through 5376 rows at
+// rank 64 40 us, as it is 26 and 33.)
 constexpr int kExpandWaves = 4;
 
-template <int CH, int FRAGS>
+template <int CH, int FRAGS, bool PIECES>
 __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a) {
-  constexpr int M = kGroupM, MW = 16 * FRAGS;
-  __shared__ int tok[M];
+  constexpr int MW = 16 * FRAGS;
+  __shared__ int tok[kM];
   __shared__ __align__(16) uint8_t lds[kExpandWaves * kWaveLds];
-  extern __shared__ __align__(16) uint16_t zs[];  // [2][MW][pitch]
+  extern __shared__ __align__(16) uint16_t zs[];  // without pieces: [2][MW][pitch]
   Tile t;
   const int m0 = blockIdx.z * MW;
-  if (!get_tile<M>(a.s, blockIdx.x, t, tok) || m0 >= t.count) return;
+  if (!get_tile<kM>(a.s, blockIdx.x, t, tok) || m0 >= t.count) return;
   const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
   const int c = child_of(a), N = a.N[c], r = a.s.r, pitch = z_pitch(r);
   const int nw = ((static_cast<int>(blockIdx.y) - a.block0[c]) * kExpandWaves + wave) * 64;
@@ -680,6 +559,12 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
     const uint32_t kb = k < r ? k * 2u : 0u;
 #pragma unroll
     for (int q = 0; q < 4; ++q) un[q] = ld16_at(urows, uoff[q] + kb);
+  };
+  const uint16_t *z0 = a.z + ((static_cast<int64_t>(blockIdx.x) * 4 + m0 / 16) * a.nchild + c) * a.RC * 1024;
+  u32x4 zn[2];
+  auto load_z = [&](int i, int chunk) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) zn[p] = ld16_at(z0 + ((i * a.nchild * a.RC + chunk) * 2 + p) * 512, lane * 16u);
   };
   u32x4 b[FRAGS][2];
   int64_t at[FRAGS][2];
@@ -704,20 +589,24 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
       for (int q = 0; q < 2; ++q) b[i][q] = load_some(a.base + at[i][q], N - (nw + ocol));
   }
   if (chunks) {
-    const float scale = a.scale[t.slot];
-    const int shift = 31 - __builtin_clz(pitch - 8) - 2;  // quads of a row, a power of two
-    const int j = (threadIdx.x & ((1 << shift) - 1)) * 4;
-    const float *row0 = a.P + (static_cast<int64_t>(blockIdx.x) * M + m0) * a.R + c * r + j;
-    for (int m = threadIdx.x >> shift; m < MW; m += (kExpandWaves * 64) >> shift) {
-      f32x4 v{0.f, 0.f, 0.f, 0.f};
-      if (m0 + m < t.count && j < t.rank16) {
-        const float *p = row0 + m * a.R;
+    if constexpr (PIECES) {
+      load_z(0, 0);
+    } else {
+      const float scale = a.scale[t.slot];
+      const int shift = 31 - __builtin_clz(pitch - 8) - 2;  // quads of a row, a power of two
+      const int j = (threadIdx.x & ((1 << shift) - 1)) * 4;
+      const float *row0 = a.P + (static_cast<int64_t>(blockIdx.x) * kM + m0) * a.R + c * r + j;
+      for (int m = threadIdx.x >> shift; m < MW; m += (kExpandWaves * 64) >> shift) {
+        f32x4 v{0.f, 0.f, 0.f, 0.f};
+        if (m0 + m < t.count && j < t.rank16) {
+          const float *p = row0 + m * a.R;
 #pragma unroll 4
-        for (int s = 0; s < a.slices; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * a.rows * a.R);
-      }
+          for (int s = 0; s < a.slices; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * a.rows * a.R);
+        }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? v[k] * scale : 0.f;
-      split4(v, *reinterpret_cast<u32x2 *>(zs + m * pitch + j), *reinterpret_cast<u32x2 *>(zs + (MW + m) * pitch + j));
+        for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? v[k] * scale : 0.f;
+        split4(v, *reinterpret_cast<u32x2 *>(zs + m * pitch + j), *reinterpret_cast<u32x2 *>(zs + (MW + m) * pitch + j));
+      }
     }
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
@@ -729,7 +618,7 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
 #pragma unroll
       for (int j = 0; j < 4; ++j) u[ch][j] = *reinterpret_cast<const u32x4 *>(mine + (16 * j + r16) * kUPitch + 16 * g);
     }
-    __syncthreads();
+    if constexpr (!PIECES) __syncthreads();
   }
   if (nw >= N) return;
 #pragma unroll
@@ -742,12 +631,22 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         if (ch >= chunks) break;
+        u32x4 z[2];
+        if constexpr (PIECES) {
+          z[0] = zn[0];
+          z[1] = zn[1];
+          if (ch + 1 < CH && ch + 1 < chunks)
+            load_z(i, ch + 1);
+          else
+            load_z(min(i + 1, FRAGS - 1), 0);
+        } else {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const u32x4 zv = ld16(zs + (p * MW + 16 * i + r16) * pitch + 32 * ch + 8 * g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = mfma16x16x32(u[ch][j], zv, acc[j]);
+          for (int p = 0; p < 2; ++p) z[p] = ld16(zs + (p * MW + 16 * i + r16) * pitch + 32 * ch + 8 * g);
         }
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma16x16x32(u[ch][j], z[p], acc[j]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(mine + r16 * kOutPitch + (16 * j + 4 * g) * 4) = acc[j];
@@ -776,9 +675,10 @@ struct Plan {
   int tiles;          // most tiles there can be
   int blocks, turns;  // workgroups along the children's rows, turns of a wave
   int across;         // rows of a workgroup
-  int NF, zgroups, slices, per, frags;
+  int NF, zgroups, slices, per, frags, RC;
+  bool pieces;
   int64_t rows;
-  size_t perm_at, p_at, bytes;
+  size_t perm_at, z_at, p_at, bytes;
 };
 
 Plan make_plan(const AdapterPool &p, int T) {
@@ -805,40 +705,42 @@ Plan make_plan(const AdapterPool &p, int T) {
     return q;
   }
   count_blocks(kExpandWaves * 64);
-  q.tiles = tile_places(T / kGroupM + std::min(p.n + 1, T));
-  const int busy = (T + kGroupM - 1) / kGroupM, row_tiles = p.nchild * p.r / 16;
+  q.tiles = tile_places(T / kM + std::min(p.n + 1, T));
+  const int busy = (T + kM - 1) / kM, row_tiles = p.nchild * p.r / 16;
   q.NF = row_tiles >= 3 ? 4 : row_tiles;
   q.zgroups = (row_tiles + q.NF - 1) / q.NF;
   // Four fragments of tokens serve a workgroup's rows of U, one where the tiles are too
   // few to fill the CUs (333 tokens through 1001 rows: 5.1 us, with four 10.5).
   q.frags = static_cast<int64_t>(q.blocks) * busy >= 2 * kCUs ? 4 : 1;
-  // K slices until there are some workgroups for every CU
-  const int stage = q.NF == 4 ? 64 : 128, stages = (p.K + stage - 1) / stage;
-  const int want = std::max(1, std::min({kMaxSlices, (3 * kCUs / 2 + busy * q.zgroups - 1) / (busy * q.zgroups), stages / kDeep}));
-  q.per = (stages + want - 1) / want * stage;
-  q.slices = (p.K + q.per - 1) / q.per;
-  q.rows = static_cast<int64_t>(q.tiles) * kGroupM;
+  cut_slices(p.K, q.NF == 4 ? 64 : 128, kDeep, busy * q.zgroups, kMaxSlices, q.slices, q.per);
+  q.RC = (p.r + 31) / 32;
+  // Where many workgroups would add up the same slices, finish_kernel does, once (4096
+  // tokens, 2 x 21504 rows at rank 16: 173 -> 152 us and 5 for it; 5376 rows at rank 64, 21
+  // workgroups: 33 -> 26 and 6; 1536 rows of 2048 tokens: 6.9 -> 5.1 and 4).
+  q.pieces = q.frags == 4 && q.slices > 1 && q.blocks >= 16;
+  q.rows = static_cast<int64_t>(q.tiles) * kM;
   q.perm_at = align256(sizeof(int4) * q.tiles);  // the tiles come first
-  q.p_at = q.perm_at + align256(sizeof(int32_t) * q.rows);
+  q.z_at = q.perm_at + align256(sizeof(int32_t) * q.rows);
+  q.p_at = q.z_at + (q.pieces ? align256(2 * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32) : 0);
   q.bytes = q.p_at + align256(sizeof(float) * q.slices * q.rows * p.nchild * p.r);
   return q;
 }
 
-template <int CH, int FRAGS>
+template <int CH, int FRAGS, bool PIECES>
 hipError_t launch_expand(const AdapterArgs &a, const Plan &q, hipStream_t stream) {
-  constexpr size_t lds = sizeof(uint16_t) * 2 * 16 * FRAGS * z_pitch(32 * CH);
-  const hipError_t e = ensure_lds<expand_kernel<CH, FRAGS>>(lds);
+  constexpr size_t lds = PIECES ? 0 : sizeof(uint16_t) * 2 * 16 * FRAGS * z_pitch(32 * CH);
+  const hipError_t e = ensure_lds<expand_kernel<CH, FRAGS, PIECES>>(lds);
   if (e != hipSuccess) return e;
-  expand_kernel<CH, FRAGS><<<dim3(q.tiles, q.blocks, kGroupM / (16 * FRAGS)), kExpandWaves * 64, lds, stream>>>(a);
+  expand_kernel<CH, FRAGS, PIECES><<<dim3(q.tiles, q.blocks, 4 / FRAGS), kExpandWaves * 64, lds, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int FRAGS>
+template <int FRAGS, bool PIECES>
 hipError_t launch_expand(const AdapterArgs &a, const Plan &q, hipStream_t stream) {
-  if (a.s.r <= 32) return launch_expand<1, FRAGS>(a, q, stream);
-  if (a.s.r <= 64) return launch_expand<2, FRAGS>(a, q, stream);
-  if (a.s.r <= 128) return launch_expand<4, FRAGS>(a, q, stream);
-  return launch_expand<8, FRAGS>(a, q, stream);
+  if (a.s.r <= 32) return launch_expand<1, FRAGS, PIECES>(a, q, stream);
+  if (a.s.r <= 64) return launch_expand<2, FRAGS, PIECES>(a, q, stream);
+  if (a.s.r <= 128) return launch_expand<4, FRAGS, PIECES>(a, q, stream);
+  return launch_expand<8, FRAGS, PIECES>(a, q, stream);
 }
 
 }  // namespace
@@ -891,23 +793,52 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
   g.s = a.s;
   g.tiles = reinterpret_cast<int4 *>(w);
   g.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
-  hipError_t e = launch_group<kGroupM>(g, stream);
+  hipError_t e = launch_group<kM>(g, stream);
   if (e != hipSuccess) return e;
   a.s.tiles = g.tiles;
   a.s.perm = g.perm;
-  a.P = reinterpret_cast<float *>(w + q.p_at);
+  ProjectArgs z{};
+  z.s = a.s;
+  z.xb = x;
+  z.vt = p.vt;
+  z.K = p.K;
+  z.nchild = p.nchild;
+  z.R = a.R;
+  z.rows = q.rows;
+  z.zgroups = q.zgroups;
+  z.zslices = q.slices;
+  z.zper = q.per;
+  z.Pz = reinterpret_cast<float *>(w + q.p_at);
+  const dim3 thin(q.tiles, q.zgroups * q.slices);
+  if (q.NF == 1)
+    thin_kernel<1><<<thin, kThreads, 0, stream>>>(z);
+  else if (q.NF == 2)
+    thin_kernel<2><<<thin, kThreads, 0, stream>>>(z);
+  else
+    thin_kernel<4><<<thin, kThreads, 0, stream>>>(z);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a.P = z.Pz;
   a.rows = q.rows;
   a.slices = q.slices;
-  a.per = q.per;
-  const dim3 thin(q.tiles, q.slices, q.zgroups);
-  if (q.NF == 1)
-    thin_kernel<1><<<thin, kThreads, 0, stream>>>(a);
-  else if (q.NF == 2)
-    thin_kernel<2><<<thin, kThreads, 0, stream>>>(a);
-  else
-    thin_kernel<4><<<thin, kThreads, 0, stream>>>(a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  return q.frags == 1 ? launch_expand<1>(a, q, stream) : launch_expand<4>(a, q, stream);
+  if (q.pieces) {
+    FinishArgs f{};
+    f.s = a.s;
+    f.P[0] = z.Pz;
+    f.slices[0] = q.slices;
+    f.R = a.R;
+    f.rows = q.rows;
+    f.out.scale = p.scale;
+    f.out.rows[0] = reinterpret_cast<uint16_t *>(w + q.z_at);
+    f.out.RT = a.R / 16;
+    f.out.nchild = p.nchild;
+    f.out.RC = q.RC;
+    finish_kernel<<<dim3(q.tiles, p.nchild * q.RC), 256, 0, stream>>>(f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    a.z = f.out.rows[0];
+    a.RC = q.RC;
+    return launch_expand<4, true>(a, q, stream);
+  }
+  return q.frags == 1 ? launch_expand<1, false>(a, q, stream) : launch_expand<4, false>(a, q, stream);
 }
 
 }  // namespace wl
