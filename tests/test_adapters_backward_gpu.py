@@ -16,7 +16,7 @@ import sys
 import pytest
 import torch
 
-from test_adapters_gpu import DEV, F, H, each_slot, make_pool, mixed_index, randn, slots_of
+from test_adapters_gpu import DEV, F, H, check_add, each_slot, make_pool, mixed_index, randn, slots_of
 from weight_shared_rank_amd import binding
 
 pytestmark = pytest.mark.gpu
@@ -96,13 +96,24 @@ def test_gradients(gpu_lib, T, rows, K, r, n, ranked):
 SPLITS = [  # few slots and many tokens; many column tiles; long contractions of z, of g, of both
     (2100, (70, 40), 40, 16, 1), (4500, (130,), 200, 64, 2), (6200, (65, 1), 72, 32, 3), (300, (1001,), 8, 32, 256),
     (300, (520, 130), 264, 16, 260), (200, (700,), 72, 128, 200), (70, (2100, 30), 2056, 32, 3), (40, (1100,), 1160, 48, 2),
-    (130, (4100,), 64, 16, 4), (130, (100,), 4104, 64, 4)]
+    (130, (4100,), 64, 16, 4), (130, (100,), 4104, 64, 4), (250, (1001,), 8, 32, 256), (120, (520, 130), 264, 16, 260),
+    (8, (2100, 30), 2056, 32, 3), (12, (4100,), 64, 16, 4), (100, (70,), 2600, 16, 3)]
 
 
 @pytest.mark.parametrize("T,rows,K,r,n", SPLITS)
 @pytest.mark.parametrize("ranked", [False, True])
 def test_gradients_of_split_sums(gpu_lib, T, rows, K, r, n, ranked):
     test_gradients(gpu_lib, T, rows, K, r, n, ranked)
+
+
+def test_as_many_tokens_and_slots_as_there_can_be(gpu_lib):
+    T, n = 1 << 20, 4096
+    announce(f"adapters T={T} n={n}")
+    p = make_pool(n, 16, 8, (1, 3))
+    x, dy, base, index = randn(1, T, 8), randn(2, T, 4, std=0.1), randn(3, T, 8), mixed_index(T, n, 4)
+    code = binding.encode_act(x)
+    check(p, code, dy, index, base, p.backward(code, dy, index, base))
+    check_add(p, x, index, dy, p.add(x, index, dy))
 
 
 def test_gradients_past_a_rank_are_zero_for_an_infinite_dy(gpu_lib):
@@ -250,6 +261,25 @@ def test_replayed_from_a_graph_and_on_other_streams(gpu_lib):
     got = [[p.backward(code, dy, index, base, stream=st) for _ in range(8)] for st in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(getattr(x, n), getattr(eager, n)) for xs in got for x in xs for n in ALL)
+
+
+def test_few_tokens_replayed_with_other_slots_and_ranks(gpu_lib):
+    T, K, rows, n = 40, 264, (72, 40), 6
+    p = make_pool(n, 32, K, rows, ranks=[32] * n)
+    code, dy, base, index = binding.encode_act(randn(1, T, K)), randn(2, T, 112), randn(3, T, K), mixed_index(T, n, 3)
+    p.backward(code, dy, index, base)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = p.backward(code, dy, index, base)
+    for seed in (4, 5, 6, 7):
+        index.copy_(mixed_index(T, n, seed) if seed < 7 else torch.full((T,), 2, dtype=torch.int32))
+        p.rank.copy_(torch.tensor([32, 0, 7, 16, 31, 17], dtype=torch.int32).roll(seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(p, code, dy, index, base, g)
+        eager = p.backward(code, dy, index, base)
+        assert all(torch.equal(getattr(g, name), getattr(eager, name)) for name in ALL)
 
 
 def test_binding_refusals(gpu_lib):

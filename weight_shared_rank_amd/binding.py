@@ -672,11 +672,11 @@ def _norm_weight(w, K, dev):
     return w.data_ptr(), WL_DTYPE_F32 if w.dtype == torch.float32 else WL_DTYPE_BF16
 
 
-def _output(t, name, shape, dtype, dev):
-    """The caller's tensor for an output, or a new one."""
+def _output(t, name, shape, dtype, dev, like=None):
+    """The caller's tensor for an output, or a new one (like: a tensor of that kind)."""
     import torch
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
     _check_tensor(t, name, shape, dtype, dev)
     return t
 
@@ -706,9 +706,9 @@ def norm_act(x, weight, eps: float = 1e-6, residual=None, offset: float = 0.0, w
         if residual is not None:
             _check_tensor(residual, "residual", (T, K), torch.bfloat16, dev)
         w, wt = _norm_weight(weight, K, dev)
-        y = _output(y, "y", (T, K), torch.bfloat16, dev) if "y" in want else None
+        y = _output(y, "y", (T, K), torch.bfloat16, dev, x) if "y" in want else None
         code = _code_out(ActCode, T, K, dev, code) if "code" in want else None
-        h = _output(h, "h", (T, K), torch.bfloat16, dev) if "h" in want else None
+        h = _output(h, "h", (T, K), torch.bfloat16, dev, x) if "h" in want else None
         rstd = _output(rstd, "rstd", (T,), torch.float32, dev) if "rstd" in want else None
         _check(lib().weightless_norm(x.data_ptr(), None if residual is None else residual.data_ptr(), T, K, w, wt,
                                      offset, eps, None if h is None else h.data_ptr(),
@@ -735,7 +735,7 @@ def norm_backward(dy, h, rstd, weight, offset: float = 0.0, dh=None, want=("dx",
         if dh is not None:
             _check_tensor(dh, "dh", (T, K), torch.bfloat16, dev)
         w, wt = _norm_weight(weight, K, dev)
-        dx = _output(dx, "dx", (T, K), torch.bfloat16, dev) if "dx" in want else None
+        dx = _output(dx, "dx", (T, K), torch.bfloat16, dev, dy) if "dx" in want else None
         dw = _output(dw, "dw", (K,), torch.float32, dev) if "dw" in want else None
         if ws is not None:
             _check_tensor(ws, "ws", (None,), torch.uint8, dev)
@@ -850,7 +850,7 @@ class AdapterPool:
         with _scope(dev, stream):
             _check_tensor(index, "index", (T,), torch.int32, dev)
             _check_tensor(base, "base", (T, self.width), torch.bfloat16, dev)
-            y = _output(y, "y", (T, self.width), torch.bfloat16, dev)
+            y = _output(y, "y", (T, self.width), torch.bfloat16, dev, base)
             if ws is None:
                 ws = torch.empty(self.workspace_bytes(T), dtype=torch.uint8, device=dev)
             else:
@@ -891,13 +891,13 @@ class AdapterPool:
             g = WlAdapterGrads()
             if "dx" in want:
                 _check_tensor(base, "base", (T, self.K), torch.bfloat16, dev)
-                dx = _output(dx, "dx", (T, self.K), torch.bfloat16, dev)
+                dx = _output(dx, "dx", (T, self.K), torch.bfloat16, dev, base)
                 g.base, g.dx = base.data_ptr(), dx.data_ptr()
             if "du" in want:
-                du = _output(du, "du", tuple(self.u.shape), torch.bfloat16, dev)
+                du = _output(du, "du", tuple(self.u.shape), torch.bfloat16, dev, self.u)
                 g.du = du.data_ptr()
             if "dv" in want:
-                dv = _output(dv, "dv", tuple(self.vt.shape), torch.bfloat16, dev)
+                dv = _output(dv, "dv", tuple(self.vt.shape), torch.bfloat16, dev, self.vt)
                 g.dv = dv.data_ptr()
             if ws is None:
                 ws = torch.empty(self.backward_workspace_bytes(T), dtype=torch.uint8, device=dev)

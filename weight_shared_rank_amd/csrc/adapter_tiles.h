@@ -15,7 +15,6 @@ namespace {
 
 constexpr int kCUs = 256;
 constexpr int kLeaderT = 256;    // up to here no grouping launch (a thread of a workgroup for each token)
-constexpr int kLeaderM = 16;     // tokens of a tile there
 constexpr int kMaxSlots = 4096;
 constexpr int kGroupWaves = 8;   // slots of a grouping workgroup
 constexpr int kStage = 8192;     // tokens whose slots it holds at a time
@@ -148,6 +147,28 @@ __device__ __forceinline__ bool get_tile(const TileSource &s, int id, Tile &t, i
   if (t.slot < 0 && !s.copies) return false;
   __syncthreads();
   return true;
+}
+
+// All tokens of a slot, in order, to list [kLeaderT], for a workgroup of 256 threads
+// in a call that is not grouped; how many there are (0 for a slot of rank 0).
+__device__ __forceinline__ int list_tokens(const TileSource &s, int slot, int *list) {
+  __shared__ uint64_t of_slot[kLeaderT / 64];
+  const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+  const bool is = i < s.T && s.index[i < s.T ? i : 0] == slot;
+  const uint64_t m = __builtin_amdgcn_ballot_w64(is);
+  if (lane == 0) of_slot[wave] = m;
+  const int rank = slot_rank(s.rank, s.r, slot);
+  __syncthreads();
+  int at = __builtin_popcountll(m & ((uint64_t{1} << lane) - 1)), total = 0;
+#pragma unroll
+  for (int w = 0; w < kLeaderT / 64; ++w) {
+    const int c = __builtin_popcountll(of_slot[w]);
+    at += w < wave ? c : 0;
+    total += c;
+  }
+  if (is) list[at] = i;
+  __syncthreads();
+  return rank > 0 ? total : 0;
 }
 
 // Grouping of a long call.  A wave takes one slot (n: no adapter), or a workgroup

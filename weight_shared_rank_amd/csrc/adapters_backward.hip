@@ -254,13 +254,18 @@ __device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *
       if (in && m0 + 16 * i + 8 * q + orow < t.count) *reinterpret_cast<u32x4 *>(a.dx + at[i][q]) = b[i][q];
 }
 
+// Tokens of a slot.
+struct Segment {
+  int count, tile0, ntiles;  // tile0: its first tile of ntiles
+  const int *list;           // or (FEW) the tokens, in LDS
+};
+
 // The sum over a slot's tokens for 64 columns of dy (dU) or of X (VGRAD: dV), by 16 JF
 // ranks: 32 positions a step, every stride-th one from `from` on.  FULL: 64 columns exist.
-template <int JF, bool VGRAD, bool FULL>
-__device__ __forceinline__ void sum_tokens(const GradArgs &a, int slot, int c, int j0, int col0, int cols, int from, int stride, uint8_t *piece,
-                                           f32x4 (&acc)[4][JF]) {
-  const int lane = threadIdx.x & 63, r16 = lane & 15;
-  const int count = keep(a.count[slot]), tile0 = keep(a.first[slot]), ntiles = keep(*a.total);
+template <int JF, bool VGRAD, bool FEW, bool FULL>
+__device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg, int c, int j0, int col0, int cols, int from, int stride,
+                                           uint8_t *piece, f32x4 (&acc)[4][JF]) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, count = seg.count;
   const int steps = (count + 31) / 32, RT = a.R / 16, col = col0 + (lane & 7) * 8;
   const u32x4 zero{0u, 0u, 0u, 0u};
   // the thin operand's pieces, from column tile (c r + j0) / 16 of z or g on
@@ -271,12 +276,21 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, int slot, int c, i
   auto rows = [&](int step, Rows &o) {
     const bool real = step < steps;
     const int at = real ? step : from;
-    o.half = tile_place(tile0 + (at >> 1), ntiles) * 2 + (at & 1);
-    const int32_t *p = a.s.perm + static_cast<int64_t>(o.half) * 32 + (lane >> 3);
+    if constexpr (FEW) {  // (a tile's place is its first token)
+      o.half = keep(seg.list[(at >> 1) * kM]) * 2 + (at & 1);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int token = p[8 * q];
-      o.token[q] = real ? token : -1;
+      for (int q = 0; q < 4; ++q) {
+        const int i = 32 * at + 8 * q + (lane >> 3), token = seg.list[min(i, count - 1)];
+        o.token[q] = real && i < count ? token : -1;
+      }
+    } else {
+      o.half = tile_place(seg.tile0 + (at >> 1), seg.ntiles) * 2 + (at & 1);
+      const int32_t *p = a.s.perm + static_cast<int64_t>(o.half) * 32 + (lane >> 3);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int token = p[8 * q];
+        o.token[q] = real ? token : -1;
+      }
     }
   };
   struct Loaded {
@@ -351,8 +365,8 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, int slot, int c, i
 
 // WAYS 1: a wave has its own column tile; 4: the waves of a.cuts workgroups share one, a
 // part of the tokens each; with more than one cut their sums leave as floats.
-template <int JF, bool VGRAD, int WAYS>
-__device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds) {
+template <int JF, bool VGRAD, int WAYS, bool FEW>
+__device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds, int *list) {
   const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
   const int r = a.s.r;
   // column tiles fastest: the tiles of a slot run together
@@ -360,6 +374,15 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
   int ct = static_cast<int>(id % ctiles);
   const int64_t rest = id / ctiles;
   const int j0 = static_cast<int>(rest % a.jgroups) * JF * 16, sc = static_cast<int>(rest / a.jgroups), slot = sc / a.cuts, cut = sc % a.cuts;
+  Segment seg{};
+  if constexpr (FEW) {
+    seg.count = keep(list_tokens(a.s, slot, list));
+    seg.list = list;
+  } else {
+    seg.count = keep(a.count[slot]);
+    seg.tile0 = keep(a.first[slot]);
+    seg.ntiles = keep(*a.total);
+  }
   if constexpr (WAYS == 1) {
     ct = ct * 4 + wave;
     if (ct >= blocks) return;
@@ -383,9 +406,9 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
   uint8_t *const piece = lds + wave * kPiece;
   const int from = WAYS == 1 ? 0 : cut * 4 + wave, stride = WAYS == 1 ? 1 : 4 * a.cuts;
   if (col0 + 64 <= cols)
-    sum_tokens<JF, VGRAD, true>(a, slot, c, j0, col0, cols, from, stride, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, true>(a, seg, c, j0, col0, cols, from, stride, piece, acc);
   else
-    sum_tokens<JF, VGRAD, false>(a, slot, c, j0, col0, cols, from, stride, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, false>(a, seg, c, j0, col0, cols, from, stride, piece, acc);
   // zeros past the slot's rank, also where dy is not finite
   const int rank = slot_rank(a.s.rank, r, slot);
   // two neighbouring column tiles of rank tile f to memory
@@ -453,15 +476,15 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
   }
 }
 
-template <int JF, int WAYS>
+template <int JF, int WAYS, bool FEW>
 __global__ __launch_bounds__(kGradWaves * 64, JF == 4 ? 2 : 4) void gradient_kernel(GradArgs a) {
   constexpr int SUM = WAYS == 1 ? 0 : kGradWaves * 4 * (JF < 2 ? JF : 2) * 1024, PIECES = kGradWaves * kPiece;
-  __shared__ int tok[kM];
+  __shared__ int tok[FEW ? kLeaderT : kM];
   __shared__ __align__(16) uint8_t lds[SUM > PIECES ? SUM : PIECES];
   int64_t id = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-  if (id < a.units[0]) return weight_unit<JF, false, WAYS>(a, id, lds);
+  if (id < a.units[0]) return weight_unit<JF, false, WAYS, FEW>(a, id, lds, tok);
   id -= a.units[0];
-  if (id < a.units[1]) return weight_unit<JF, true, WAYS>(a, id, lds);
+  if (id < a.units[1]) return weight_unit<JF, true, WAYS, FEW>(a, id, lds, tok);
   id -= a.units[1];
   if (id < a.units[2]) dx_unit(a, id, lds, tok);
 }
@@ -495,6 +518,7 @@ __global__ __launch_bounds__(256) void fill_zero_16(u32x4 *p, int64_t n) {
 
 // ---- plan -----------------------------------------------------------------------------------
 struct BackPlan {
+  bool few;  // no grouping launch
   int tiles, NF, zgroups, zslices, zper, ggroups, gslices, gper, RC;
   int ublock0[kMaxChildren + 1], vblocks, cuts;
   bool own;  // gradient_kernel's waves have column tiles of their own
@@ -504,7 +528,12 @@ struct BackPlan {
 
 BackPlan make_back_plan(const AdapterPool &p, int T) {
   BackPlan q{};
-  q.tiles = tile_places(T / kM + std::min(p.n + 1, T));
+  // Without the grouping a tile's place is its first token's, and workgroups at the other
+  // places look and leave: pays for dx's while they are few (77 tokens, 712 -> 1001, 480
+  // workgroups: 17.4 -> 14.1 us; 8 of 4096 -> 4096, 256: 21.6 -> 19.1; 64 of them, 2048:
+  // 24.2 -> 25.1; 256, 8192: 26.4 -> 39.6).
+  q.few = T <= kLeaderT && static_cast<int64_t>(tile_places(T)) * 2 * ((p.K + 255) / 256) <= 4 * kCUs;
+  q.tiles = q.few ? tile_places(T) : tile_places(T / kM + std::min(p.n + 1, T));
   q.rows = static_cast<int64_t>(q.tiles) * kM;
   const int row_tiles = p.r / 16, R = p.nchild * p.r;
   q.NF = row_tiles >= 3 ? 4 : row_tiles;
@@ -583,10 +612,12 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   gr.first = reinterpret_cast<int32_t *>(w + q.slots_at);
   gr.count = gr.first + p.n;
   gr.total = gr.count + p.n;
-  hipError_t e = launch_group<kM>(gr, stream);
-  if (e != hipSuccess) return e;
-  s.tiles = gr.tiles;
-  s.perm = gr.perm;
+  hipError_t e = hipSuccess;
+  if (!q.few) {
+    if ((e = launch_group<kM>(gr, stream)) != hipSuccess) return e;
+    s.tiles = gr.tiles;
+    s.perm = gr.perm;
+  }
   const int R = p.nchild * p.r;
   ProjectArgs a{};
   a.s = s;
@@ -682,10 +713,11 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   constexpr int64_t kAcross = int64_t{1} << 20;
   const dim3 blocks(static_cast<uint32_t>(std::min(total, kAcross)), static_cast<uint32_t>((total + kAcross - 1) / kAcross));
   auto run = [&](auto jf) {
-    if (q.own)
-      gradient_kernel<decltype(jf)::value, 1><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+    constexpr int JF = decltype(jf)::value;
+    if (q.few)
+      q.own ? gradient_kernel<JF, 1, true><<<blocks, kGradWaves * 64, 0, stream>>>(d) : gradient_kernel<JF, 4, true><<<blocks, kGradWaves * 64, 0, stream>>>(d);
     else
-      gradient_kernel<decltype(jf)::value, 4><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+      q.own ? gradient_kernel<JF, 1, false><<<blocks, kGradWaves * 64, 0, stream>>>(d) : gradient_kernel<JF, 4, false><<<blocks, kGradWaves * 64, 0, stream>>>(d);
   };
   if (q.NF == 1)
     run(std::integral_constant<int, 1>{});
