@@ -136,11 +136,13 @@ __global__ __launch_bounds__(kThreads, 4) void project_kernel(ProjectArgs a) {
   __shared__ __align__(16) uint8_t lds[Stage<NF>::LDS];
   Tile t;
   if (!get_tile<kM>(a.s, blockIdx.x, t, tok) || t.slot < 0) return;
-  const int zunits = a.zgroups * a.zslices, unit = blockIdx.y;
-  if (unit < zunits)
-    project_z<NF, true>(a, t, tok, unit, lds);
+  // the longer slices first (31B gate|up, g: 99 -> 96 us; 8192 -> 5376, z: 35 -> 31)
+  const int units[2] = {a.zgroups * a.zslices, a.ggroups * a.nchild * a.gslices}, unit = blockIdx.y;
+  const bool g_first = a.gper > a.zper;
+  if (g_first ? unit < units[1] : unit >= units[0])
+    project_g<NF>(a, t, tok, g_first ? unit : unit - units[0], lds);
   else
-    project_g<NF>(a, t, tok, unit - zunits, lds);
+    project_z<NF, true>(a, t, tok, g_first ? unit - units[1] : unit, lds);
 }
 
 // ---- dx, dU, dV -----------------------------------------------------------------------------
