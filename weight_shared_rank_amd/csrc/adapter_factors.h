@@ -11,7 +11,7 @@ namespace wl {
 namespace {
 
 constexpr int kM = 64;    // tokens of a tile
-constexpr int kDeep = 4;  // stages under way in project_kernel
+constexpr int kDeep = 4;  // stages under way
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 
 // 8 codes and their scale byte as bf16, exact.

@@ -14,10 +14,14 @@
 // 17th, ... of its slot.  It makes z of its tile itself, as do the others along the
 // children's rows: V^T comes from L2 then, and a launch that hands z over costs more
 // (64 tokens through gate|up of 2 x 21504 x 5376 at rank 16: 7.5 + 25 us in two).
-// Many tokens: a grouping (group_kernel), then z (thin_kernel, K cut into slices that
-// the reader adds up in a fixed order), then the products with U and base
-// (expand_kernel), in tiles of 64 tokens.  (In one launch, tiles of 16: 4096 tokens
-// through 5376 x 8192 at rank 64 56 us, of one round of the CUs 28, against 20 + 30.)
+// Many tokens: a grouping (group_kernel), z in float32 slices of K (thin_kernel), the
+// products with U and base (expand_kernel), in tiles of 64 tokens; between them, where
+// many workgroups would add up the same slices, finish_kernel.  (In one launch, tiles
+// of 16: 4096 tokens through 5376 x 8192 at rank 64 56 us, of one round of the CUs 28.)
+//
+// Measured: 1 token through 1B q|k|v 5.2 us, of which a launch is most; 64 tokens of 57
+// adapters through 31B gate|up 25 (103 MB read, 4.1 TB/s); 4096 tokens of 12 through 31B
+// o at rank 64 6.7 + 20 + 5.5 + 26 (thin_kernel 80 MB at 4 TB/s, expand_kernel 100 at 3.9).
 //
 // Everything moves as rows, 8 lanes to a cache line, and reaches the matrix cores
 // through LDS: fragments loaded as they are used (16 rows of 64 bytes a load) pass
@@ -454,12 +458,6 @@ __device__ __forceinline__ int child_of(const AdapterArgs &a) {
   return c;
 }
 
-// c z [2][M][pitch] all zeros, which ranks past the slot's stay.
-template <int M>
-__device__ __forceinline__ void clear_z(const AdapterArgs &a, uint16_t *zs) {
-  for (int i = threadIdx.x; i < 2 * M * z_pitch(a.s.r) / 8; i += kThreads) reinterpret_cast<u32x4 *>(zs)[i] = u32x4{0u, 0u, 0u, 0u};
-}
-
 // ---- few tokens ------------------------------------------------------------------
 constexpr int kRing = 2 * 24 * 1024;  // two stages of form_z<2>, the largest
 static_assert(kWaves * kWaveLds <= kRing, "the waves' pieces lie over the stages");
@@ -513,6 +511,7 @@ __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(Adapt
 }
 
 // ---- many tokens -------------------------------------------------------------------
+// z of a tile, a slice of K and 16 NF rows of V^T of all children.
 template <int NF>
 __global__ __launch_bounds__(kThreads, 4) void thin_kernel(ProjectArgs a) {
   __shared__ int tok[kM];

@@ -1,6 +1,6 @@
 // Launches of what stands before and beside a projection: the norm with the
 // residual's addition and a coded output (norm.hip), and the low-rank adapters
-// of many requests (adapters.hip).
+// of many requests (adapters.hip) and their gradients (adapters_backward.hip).
 #pragma once
 
 #include "training.h"
@@ -56,8 +56,7 @@ size_t adapters_workspace_bytes(const AdapterPool &p, int T);
 hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_t *index, int T, const uint16_t *base,
                            uint16_t *y, void *ws, hipStream_t stream);
 
-// Gradients of launch_adapters (adapters.hip has the formulas); every output may
-// be null.
+// Gradients of launch_adapters; every output may be null.
 struct AdapterGrads {
   const uint16_t *base;  // [T][K], what dx adds to
   uint16_t *dx;          // [T][K], may be base

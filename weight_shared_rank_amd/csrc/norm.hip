@@ -13,11 +13,15 @@
 // waves share a row (rows of up to 32768 elements); a coded block of 128 is 16
 // neighbouring lanes, so its maximum is four lane exchanges and the bf16 output
 // is coded without being read again.
+// Measured: 8192 x 5376 with residual, h, y and code 76.5 us (5.2 TB/s, a copy's rate);
+// its backward pass 69 (5.1 TB/s) and 5.5 for the sum of dw; 1 x 1152 2.9 us, a launch.
+#include <algorithm>
 #include <type_traits>
 
 #include "beside.h"
 #include "coded.h"
 #include "common.h"
+#include "lds_dma.h"
 
 namespace wl {
 
@@ -84,6 +88,8 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
     h[i] = u32x4{0u, 0u, 0u, 0u};
     if (k < c.K) h[i] = ld16(c.x + row + k);
   }
+  float w[8];  // (one vector a lane: under way with the row)
+  if (V == 1 && at < c.K) load_weight<F32>(c.w, at, w);
   if (c.res) {
     u32x4 r[V];
 #pragma unroll
@@ -125,8 +131,8 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
     const int k = at + i * W * 512;
     u32x4 y{0u, 0u, 0u, 0u};
     if (k < c.K) {
-      float w[8], o[8];
-      load_weight<F32>(c.w, k, w);
+      float o[8];
+      if (V > 1) load_weight<F32>(c.w, k, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v = j & 1 ? hi_f32(h[i][j / 2]) : lo_f32(h[i][j / 2]);
@@ -154,6 +160,22 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
   }
 }
 
+__device__ __forceinline__ void load_8(const float *p, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const f32x4 x = reinterpret_cast<const f32x4 *>(p)[j];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * j + i] = x[i];
+  }
+}
+__device__ __forceinline__ void store_8(float *p, const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) reinterpret_cast<f32x4 *>(p)[j] = f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+}
+
+template <int W, int V>
+constexpr bool in_lds() { return W == 16 && V > 2; }
+
 // Backward.  A team of W waves walks the rows `team`, `team` + teams, ...; its
 // sum of dy n stays in registers, the workgroup's sums (a row of K floats) go to
 // `part` (dw itself if there is one workgroup).
@@ -163,13 +185,21 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int at = (W == 1 ? lane : static_cast<int>(threadIdx.x)) * 8;
   __shared__ float sum[2][W];
-  float w[V][8], dw[V][8];
+  // the weight stays in registers but for sixteen waves of several vectors, which read
+  // it again for each row (kept, it spills)
+  constexpr bool KEPT = W < 16 || V == 1;
+  // and dw but for the longest rows, each lane's in LDS (2048 rows of 21504: 136 us with
+  // dw in registers, which spill, so 79)
+  constexpr bool IN_LDS = in_lds<W, V>();
+  extern __shared__ __align__(16) float sums[];  // [K]
+  float w[KEPT ? V : 1][8], dw[IN_LDS ? 1 : V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int k = at + i * W * 512;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.f;
-    if (k < c.K) load_weight<F32>(c.w, k, w[i]);
+    for (int j = 0; j < 8; ++j) w[KEPT ? i : 0][j] = dw[IN_LDS ? 0 : i][j] = 0.f;
+    if (KEPT && k < c.K) load_weight<F32>(c.w, k, w[KEPT ? i : 0]);
+    if (IN_LDS && k < c.K) store_8(sums + k, dw[0]);
   }
   const int64_t teams = static_cast<int64_t>(gridDim.x) * R;
   int turn = 0;
@@ -183,31 +213,42 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
       if (k < c.K) {
         d[i] = ld16(c.dy + row + k);
         h[i] = ld16(c.h + row + k);
-        if (c.dh) r[i] = ld16(c.dh + row + k);
+        if (c.dh && !IN_LDS) r[i] = ld16(c.dh + row + k);
       }
     }
     const float a = c.rstd[t];
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+      const int k = at + i * W * 512;
+      float(&wi)[8] = w[KEPT ? i : 0];
+      if (!KEPT && k < c.K) load_weight<F32>(c.w, k, wi);
+      float(&dwi)[8] = dw[IN_LDS ? 0 : i];
+      if (IN_LDS && k < c.K) load_8(sums + k, dwi);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float n = (j & 1 ? hi_f32(h[i][j / 2]) : lo_f32(h[i][j / 2])) * a;
         const float g = j & 1 ? hi_f32(d[i][j / 2]) : lo_f32(d[i][j / 2]);
-        dot = __builtin_fmaf(g * w[i][j], n, dot);
-        dw[i][j] = __builtin_fmaf(g, n, dw[i][j]);
+        // (past the row g is 0 and w of the vector before it may not be finite)
+        dot = KEPT || k < c.K ? __builtin_fmaf(g * wi[j], n, dot) : dot;
+        dwi[j] = __builtin_fmaf(g, n, dwi[j]);
       }
+      if (IN_LDS && k < c.K) store_8(sums + k, dwi);
+    }
     if (!c.dx) continue;
     const float mean = row_sum<W>(dot, sum[turn], wave) / c.K;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int k = at + i * W * 512;
       if (k >= c.K) continue;
+      float(&wi)[8] = w[KEPT ? i : 0];
+      if (!KEPT) load_weight<F32>(c.w, k, wi);
+      if (c.dh && IN_LDS) r[i] = ld16(c.dh + row + k);
       u32x4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float n0 = lo_f32(h[i][j]) * a, n1 = hi_f32(h[i][j]) * a;
-        const float g0 = lo_f32(d[i][j]) * w[i][2 * j], g1 = hi_f32(d[i][j]) * w[i][2 * j + 1];
+        const float g0 = lo_f32(d[i][j]) * wi[2 * j], g1 = hi_f32(d[i][j]) * wi[2 * j + 1];
         o[j] = pack_bf16(__builtin_fmaf(a, __builtin_fmaf(-n0, mean, g0), lo_f32(r[i][j])),
                          __builtin_fmaf(a, __builtin_fmaf(-n1, mean, g1), hi_f32(r[i][j])));
       }
@@ -221,9 +262,8 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
     for (int i = 0; i < V; ++i) {
       const int k = at + i * W * 512;
       if (k >= c.K) continue;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<f32x4 *>(out + k + 4 * j) = f32x4{dw[i][4 * j], dw[i][4 * j + 1], dw[i][4 * j + 2], dw[i][4 * j + 3]};
+      if constexpr (IN_LDS) load_8(sums + k, dw[0]);
+      store_8(out + k, dw[IN_LDS ? 0 : i]);
     }
   } else {
     __shared__ f32x4 rows[R - 1][64 * 2];
@@ -273,36 +313,47 @@ __global__ __launch_bounds__(256) void fill_zero_f32(float *p, int n) {
   if (i < n) p[i] = 0.f;
 }
 
-// Waves and vectors of a row: a wave up to 2048 elements (no barrier), four up
-// to 8192, sixteen above.
+// Waves and vectors of a row.  One vector a lane while that takes four waves or fewer
+// (1 row of 2048: 5.2 -> 2.7 us, 8192 rows 30.4 -> 28.6, against one wave), and with few
+// rows up to sixteen (1 row of 8192 5.6 -> 4.2, 256 rows 8.6 -> 6.9; 512 level; 2048 rows
+// of 5376 20.1 -> 22.5, 8192 rows 76 -> 85); else four waves up to 8192 elements.
+constexpr int kFewRows = 512;
+
 template <typename F>
-hipError_t with_row_shape(int K, F &&f) {
-  const int v1 = (K + 511) / 512, v4 = (K + 2047) / 2048, v16 = (K + 8191) / 8192;
-  if (v1 == 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  if (v1 == 2) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-  if (v1 == 3) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 3>{});
-  if (v1 == 4) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  if (v4 == 2) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-  if (v4 == 3) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 3>{});
-  if (v4 == 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
-  if (v16 == 2) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-  if (v16 == 3) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 3>{});
-  return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+hipError_t with_row_shape(int T, int K, F &&f) {
+  const auto shape = [&](auto w, auto v) { return f(w, v); };
+  const std::integral_constant<int, 1> i1{};
+  const std::integral_constant<int, 2> i2{};
+  const std::integral_constant<int, 3> i3{};
+  const std::integral_constant<int, 4> i4{};
+  const std::integral_constant<int, 16> i16{};
+  if (K <= 512) return shape(i1, i1);
+  if (K <= 1024) return shape(i2, i1);
+  if (K <= 2048) return shape(i4, i1);
+  if (T <= kFewRows && K <= 4096) return shape(std::integral_constant<int, 8>{}, i1);
+  if (T <= kFewRows && K <= 8192) return shape(i16, i1);
+  if (K <= 4096) return shape(i4, i2);
+  if (K <= 6144) return shape(i4, i3);
+  if (K <= 8192) return shape(i4, i4);
+  if (K <= 16384) return shape(i16, i2);
+  if (K <= 24576) return shape(i16, i3);
+  return shape(i16, i4);
 }
 
-int rows_of_workgroup(int K) { return K <= 2048 ? kRowsOneWave : 1; }
+int rows_of_workgroup(int K) { return K <= 512 ? kRowsOneWave : 1; }
 
-// Workgroups of the backward pass: enough to fill the CUs, few enough that the
-// partial sums stay small beside the rows.
+// Workgroups of the backward pass: enough to fill the CUs, few enough that the partial
+// sums stay small beside the rows (8192 rows of 5376 with 384, 512, 768, 1024: 74, 74, 82,
+// 81 us in both launches; of 1536, smaller workgroups: 30, 25, 21, 22).
 int backward_groups(int T, int K) {
   const int64_t groups = (static_cast<int64_t>(T) + rows_of_workgroup(K) - 1) / rows_of_workgroup(K);
-  return static_cast<int>(groups < 1024 ? groups : 1024);
+  return static_cast<int>(std::min<int64_t>(groups, K <= 2048 ? 768 : K <= 16384 ? 512 : 256));
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormCall &c, hipStream_t stream) {
-  return with_row_shape(c.K, [&](auto w, auto v) {
+  return with_row_shape(c.T, c.K, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     const int R = rows_of_workgroup(c.K);
     const dim3 grid((c.T + R - 1) / R), block(R * W * 64);
@@ -326,13 +377,18 @@ hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStrea
     return hipGetLastError();
   }
   const int G = backward_groups(c.T, c.K);
-  const hipError_t e = with_row_shape(c.K, [&](auto w, auto v) {
+  const hipError_t e = with_row_shape(c.T, c.K, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     const dim3 block(rows_of_workgroup(c.K) * W * 64);
+    constexpr size_t lds = in_lds<W, V>() ? sizeof(float) * W * V * 512 : 0;
+    if constexpr (lds > 0) {
+      const hipError_t e = c.w.f32 ? ensure_lds<norm_backward_kernel<W, V, true>>(lds) : ensure_lds<norm_backward_kernel<W, V, false>>(lds);
+      if (e != hipSuccess) return e;
+    }
     if (c.w.f32)
-      norm_backward_kernel<W, V, true><<<G, block, 0, stream>>>(c, partials);
+      norm_backward_kernel<W, V, true><<<G, block, lds, stream>>>(c, partials);
     else
-      norm_backward_kernel<W, V, false><<<G, block, 0, stream>>>(c, partials);
+      norm_backward_kernel<W, V, false><<<G, block, lds, stream>>>(c, partials);
     return hipGetLastError();
   });
   if (e != hipSuccess || !c.dw || G == 1) return e;
