@@ -447,7 +447,8 @@ wl_status weightless_stacked_backward(const wl_bundle *bundle, int32_t layer, in
  *  8 <= K <= 32768 and K % 8 == 0 (WL_ESHAPE), T as for coded activations (0: a
  *    no-op).  x, res, w, h and y 16-byte aligned.
  *  A row is normed by itself: an infinity or NaN in it changes no other row.
- *  One launch. */
+ *  One launch.  (Rows of 2049 to 8192 elements share more waves in calls of up to
+ *  512, so the order of the mean's sum depends on T there.) */
 wl_status weightless_norm(const void *d_x, const void *d_res, int32_t T, int32_t K, const void *d_w, int32_t w_dtype,
                           float offset, float eps, void *d_h, void *d_y, void *d_code, size_t code_bytes,
                           float *d_rstd, void *stream);
@@ -503,10 +504,9 @@ typedef struct {
 size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t T);
 
 /*  d_x bf16 [T, K] (16-byte aligned), d_index int32 [T], d_base and d_y bf16
- *    [T, sum of out_dim] (2-byte aligned; whole 16-byte accesses where they are
- *    16-byte aligned and rows and children a multiple of 8 wide).  d_y may be
- *    exactly d_base (in place: rows without an adapter are then not touched);
- *    otherwise no output may overlap an input (WL_EINVAL).  T = 0: a no-op.
+ *    [T, sum of out_dim] (2-byte aligned).  d_y may be exactly d_base (in place:
+ *    rows without an adapter are then not touched); otherwise no output may
+ *    overlap an input (WL_EINVAL).  T = 0: a no-op.
  *  d_ws: weightless_adapters_workspace_bytes(adapters, T) bytes, 256-byte
  *    aligned, no initialization, nothing kept; concurrent calls, and graphs that
  *    may run at the same time, need distinct workspaces.
@@ -514,7 +514,7 @@ size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t 
  *  as a pair of bf16 (16 significant bits); y is rounded once.  A token's result
  *  is the same bits whichever tokens stand beside it in a call of as many tokens.
  *  What is not finite in a slot or a token's x reaches that slot's or that token's
- *  rows alone.  Two launches up to 256 tokens, three above. */
+ *  rows alone.  One launch up to 256 tokens, three or four above. */
 wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, const int32_t *d_index, int32_t T,
                                   const void *d_base, void *d_y, void *d_ws, size_t ws_bytes, void *stream);
 
@@ -528,8 +528,8 @@ wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, 
  * else; a slot without tokens has zero gradients, and so have the rows and
  * columns from a slot's rank on.  Sums in float32, z and g as pairs of bf16 (16
  * significant bits) where they enter the second products; every output is rounded
- * once.  The sums over tokens run in the order of the tokens: the same bits from
- * run to run, whichever gradients are asked for.  What is not finite in a token
+ * once.  The sums over tokens have a fixed order: the same bits from run to run,
+ * whichever gradients are asked for.  What is not finite in a token
  * reaches its own dx and its slot's dU and dV alone. */
 typedef struct {
   const void *base; /* bf16 [T, K]: dx of the shared projection's backward call (needed with dx) */
@@ -549,7 +549,7 @@ size_t weightless_adapters_backward_workspace_bytes(const wl_adapters *adapters,
  *    base (WL_EINVAL).  T = 0: du and dv are zeroed.
  *  d_ws: weightless_adapters_backward_workspace_bytes(adapters, T) bytes, 256-byte
  *    aligned, no initialization, nothing kept; concurrent calls need distinct
- *    workspaces.  Four launches. */
+ *    workspaces.  Two to five launches. */
 wl_status weightless_adapters_backward(const wl_adapters *adapters, const void *d_xcode, size_t xcode_bytes,
                                        const void *d_dy, const int32_t *d_index, int32_t T,
                                        const wl_adapter_grads *grads, void *d_ws, size_t ws_bytes, void *stream);
