@@ -14,7 +14,7 @@ namespace wl {
 namespace {
 
 constexpr int kCUs = 256;
-constexpr int kLeaderT = 256;    // up to here no grouping launch (a thread of a workgroup for each token)
+constexpr int kLeaderT = 256;    // most tokens without a grouping launch for workgroups of as many threads
 constexpr int kMaxSlots = 4096;
 constexpr int kGroupWaves = 8;   // slots of a grouping workgroup
 constexpr int kStage = 8192;     // tokens whose slots it holds at a time
@@ -101,9 +101,10 @@ __device__ __forceinline__ int tile_place(int t, int n) {
 }
 inline int tile_places(int64_t n) { return static_cast<int>((n + 7) & ~int64_t{7}); }
 
-// Tile `id` of M tokens for a workgroup of 256 threads or more; its tokens go to
-// tok (-1 behind the last).  False (for the whole workgroup): nothing to do.
-template <int M>
+// Tile `id` of M tokens for a workgroup of 256 threads or more (of MOST, where there are
+// so many tokens that are not grouped); its tokens go to tok (-1 behind the last).
+// False (for the whole workgroup): nothing to do.
+template <int M, int MOST = kLeaderT>
 __device__ __forceinline__ bool get_tile(const TileSource &s, int id, Tile &t, int *tok) {
   if (s.tiles) {
     if (id >= s.max_tiles) return false;
@@ -117,19 +118,19 @@ __device__ __forceinline__ bool get_tile(const TileSource &s, int id, Tile &t, i
     if (threadIdx.x < M) tok[threadIdx.x] = token;
   } else {
     if (id >= s.T) return false;
-    __shared__ uint64_t member[kLeaderT / 64];
+    __shared__ uint64_t member[MOST / 64];
     const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
     // slots outside the pool count as slot n, no adapter
     const int of_id = s.index[id], of_i = i < s.T ? s.index[i] : 0;
     const int a = static_cast<uint32_t>(of_id) < static_cast<uint32_t>(s.n) ? of_id : s.n;
     const int b = static_cast<uint32_t>(of_i) < static_cast<uint32_t>(s.n) ? of_i : s.n;
     const uint64_t m = __builtin_amdgcn_ballot_w64(i < s.T && a == b);
-    if (lane == 0 && wave < kLeaderT / 64) member[wave] = m;
+    if (lane == 0 && wave < MOST / 64) member[wave] = m;
     if (i < M) tok[i] = -1;
     __syncthreads();
     int before = 0, at = 0, total = 0;  // members before token id, before token i, in all
 #pragma unroll
-    for (int w = 0; w < kLeaderT / 64; ++w) {
+    for (int w = 0; w < MOST / 64; ++w) {
       const uint64_t v = member[w];
       const int c = __builtin_popcountll(v);
       total += c;

@@ -9,7 +9,7 @@
 // rows are V^T's and U's.  c z enters the second product as a pair of bf16 (the
 // value and what its rounding left, 16 significant bits); y is rounded once.
 //
-// Few tokens (up to kLeaderT): nothing is prepared and there is one launch.
+// Few tokens (one_launch): nothing is prepared and there is one launch.
 // Workgroup t looks through the whole index and works if token t is the first, the
 // 17th, ... of its slot.  It makes z of its tile itself, as do the others along the
 // children's rows: V^T comes from L2 then, and a launch that hands z over costs more
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(Adapt
   __shared__ __align__(16) uint8_t lds[kRing];
   extern __shared__ __align__(16) uint16_t zs[];  // [2][kTileM][pitch]
   Tile t;
-  if (!get_tile<kTileM>(a.s, blockIdx.x, t, tok)) return;
+  if (!get_tile<kTileM, kThreads>(a.s, blockIdx.x, t, tok)) return;
   const int c = child_of(a), first = (static_cast<int>(blockIdx.y) - a.block0[c]) * a.turns * kThreads;
   const auto form = [&] {
     // c z all zeros, which ranks past the slot's stay (barriers stand between this and the stores of z)
@@ -680,9 +680,31 @@ struct Plan {
   size_t perm_at, z_at, p_at, bytes;
 };
 
+// Whether few_kernel alone is faster than the launches of a grouped call.  It makes z
+// once a workgroup (31 thousand products of V^T a microsecond, 46 for one token), and
+// takes 1 us for 512 rows of U a CU (more where a higher rank leaves it fewer waves),
+// counted for as many tiles as there can be; the others 10 us for their launches and 4
+// for every 900 workgroups of expand_kernel.  Measured in us, one launch and grouped:
+//   64 tokens of 4096 -> 4096, rank 16 9.2 and 14.0, 256 15.0 and 15.6, 333 16.2 and 15.8;
+//   128 of 4096 -> 16384, rank 32, 21.2 and 20.3; 64 of 4096 -> 4096, rank 128, 26.6 and 17.2;
+//   128 tokens of 57 adapters through 31B gate|up 43.6 and 67, 256 90 and 66;
+//   512 of 1160 -> 1001, rank 32, 11.2 and 14.5.
+bool one_launch(const AdapterPool &p, int T) {
+  if (T > kThreads) return false;
+  int64_t turns = 0, blocks = 0;
+  for (int c = 0; c < p.nchild; ++c) {
+    turns += (p.N[c] + kThreads - 1) / kThreads;
+    blocks += (p.N[c] + kExpandWaves * 64 - 1) / (kExpandWaves * 64);
+  }
+  const int64_t z = static_cast<int64_t>(p.K) * p.r / (T == 1 ? 46 : 31);  // ns
+  const int64_t walk = turns * T * (p.r <= 32 ? 950 : p.r <= 64 ? 1500 : 2400) / kCUs;
+  const int64_t tiles = std::min(T, p.n + 1 + T / kM);
+  return z + walk <= 10000 + std::max<int64_t>(0, tiles * blocks * 4000 / 900 - 4000);
+}
+
 Plan make_plan(const AdapterPool &p, int T) {
   Plan q{};
-  q.grouped = T > kLeaderT;
+  q.grouped = !one_launch(p, T);
   q.turns = 1;
   auto count_blocks = [&](int across) {
     q.across = across;
