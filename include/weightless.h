@@ -514,7 +514,7 @@ size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t 
  *  as a pair of bf16 (16 significant bits); y is rounded once.  A token's result
  *  is the same bits whichever tokens stand beside it in a call of as many tokens.
  *  What is not finite in a slot or a token's x reaches that slot's or that token's
- *  rows alone.  One launch up to 256 tokens, three or four above. */
+ *  rows alone.  One launch with few tokens, else three or four. */
 wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, const int32_t *d_index, int32_t T,
                                   const void *d_base, void *d_y, void *d_ws, size_t ws_bytes, void *stream);
 
