@@ -465,7 +465,7 @@ wl_status weightless_norm(const void *d_x, const void *d_res, int32_t T, int32_t
  *    wl_last_error() set on error), 256-byte aligned, no initialization, nothing
  *    kept; concurrent calls need distinct workspaces.  May be NULL without dw.
  *  Sums in float32 in a fixed order: the same bits from run to run, whichever of
- *  the two are asked for.  One launch, another for the sum of dw. */
+ *  the two are asked for.  One launch up to 1024 rows (two with dx over dy), then two. */
 size_t weightless_norm_backward_workspace_bytes(int32_t T, int32_t K);
 wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const float *d_rstd, const void *d_dh, int32_t T,
                                    int32_t K, const void *d_w, int32_t w_dtype, float offset, void *d_dx, float *d_dw,

@@ -163,6 +163,17 @@ def test_backward(gpu_lib, T, K, with_dh, f32, offset):
         assert torch.equal(got.dx, o.dx) and torch.equal(got.dw, o.dw)
 
 
+@pytest.mark.parametrize("T,K", [(2, 8), (5, 256), (4, 256), (512, 4096), (513, 4104), (1024, 72), (1025, 72), (1024, 8200), (1100, 17000), (1030, 25000), (40, 32768)])
+def test_backward_with_few_and_many_rows(gpu_lib, T, K):
+    test_backward(gpu_lib, T, K, True, False, 1.0)
+
+
+@pytest.mark.parametrize("T,K", [(512, 4096), (513, 4104), (512, 8192), (513, 6152), (3, 16384)])
+def test_forward_with_few_and_many_rows(gpu_lib, T, K):
+    x, r, w = randn(1, T, K), randn(2, T, K), randn(3, K)
+    check_forward(binding.norm_act(x, w, residual=r, want=ALL), x, w, r, 0.0, EPS)
+
+
 def test_gradients_against_differences(gpu_lib):
     """<dx, v> and <dw, u> against central differences of the float64 forward.
     With a step of 1e-4 they are off by about 1e-8 of the second derivative's

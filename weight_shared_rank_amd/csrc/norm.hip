@@ -14,7 +14,8 @@
 // neighbouring lanes, so its maximum is four lane exchanges and the bf16 output
 // is coded without being read again.
 // Measured: 8192 x 5376 with residual, h, y and code 76.5 us (5.2 TB/s, a copy's rate);
-// its backward pass 69 (5.1 TB/s) and 5.5 for the sum of dw; 1 x 1152 2.9 us, a launch.
+// its backward pass 69 (5.1 TB/s) and 5.5 for the sum of dw; 1 x 1152 2.8 us, a launch;
+// the backward pass of 333 x 1160 4.0.
 #include <algorithm>
 #include <type_traits>
 
@@ -176,11 +177,58 @@ __device__ __forceinline__ void store_8(float *p, const float (&v)[8]) {
 template <int W, int V>
 constexpr bool in_lds() { return W == 16 && V > 2; }
 
+// dw of 64 columns from all rows, which the waves take in turn, 8 at a time.
+template <int WAVES>
+__device__ __forceinline__ void dw_columns(const NormBackward &c, int unit) {
+  constexpr int AHEAD = 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = unit * 64 + (lane & 7) * 8;
+  const bool in = col < c.K;
+  float dw[8] = {};
+  for (int t0 = wave * 8 + (lane >> 3); t0 < c.T; t0 += 8 * WAVES * AHEAD) {
+    u32x4 d[AHEAD], h[AHEAD];
+    float a[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int64_t t = min(t0 + 8 * WAVES * i, c.T - 1), at = t * c.K + (in ? col : 0);
+      d[i] = ld16(c.dy + at);
+      h[i] = ld16(c.h + at);
+      a[i] = c.rstd[t];
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const bool row = t0 + 8 * WAVES * i < c.T;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = (j & 1 ? hi_f32(h[i][j / 2]) : lo_f32(h[i][j / 2])) * a[i];
+        const float g = j & 1 ? hi_f32(d[i][j / 2]) : lo_f32(d[i][j / 2]);
+        dw[j] = row ? __builtin_fmaf(g, n, dw[j]) : dw[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int x = 8; x < 64; x <<= 1) dw[j] += __shfl_xor(dw[j], x, 64);
+  __shared__ float part[WAVES][64];
+  if (lane < 8) store_8(&part[wave][lane * 8], dw);
+  __syncthreads();
+  const int k = unit * 64 + static_cast<int>(threadIdx.x);
+  if (threadIdx.x < 64 && k < c.K) {
+    float s = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += part[w][threadIdx.x];
+    c.dw[k] = s;
+  }
+}
+
 // Backward.  A team of W waves walks the rows `team`, `team` + teams, ...; its
-// sum of dy n stays in registers, the workgroup's sums (a row of K floats) go to
-// `part` (dw itself if there is one workgroup).
+// sum of dy n stays with it, the workgroup's sums (a row of K floats) go to
+// `part` (dw itself if there is one workgroup).  With few rows dw has workgroups of
+// its own, 64 columns each, behind the `groups` of the rows: they read the rows again,
+// from the caches, and no second launch is needed.
 template <int W, int V, bool F32>
-__global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_backward_kernel(NormBackward c, float *part) {
+__global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_backward_kernel(NormBackward c, float *part, int groups) {
+  if (static_cast<int>(blockIdx.x) >= groups) return dw_columns<W == 1 ? kRowsOneWave : W>(c, blockIdx.x - groups);
   constexpr int R = W == 1 ? kRowsOneWave : 1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int at = (W == 1 ? lane : static_cast<int>(threadIdx.x)) * 8;
@@ -201,7 +249,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
     if (KEPT && k < c.K) load_weight<F32>(c.w, k, w[KEPT ? i : 0]);
     if (IN_LDS && k < c.K) store_8(sums + k, dw[0]);
   }
-  const int64_t teams = static_cast<int64_t>(gridDim.x) * R;
+  const int64_t teams = static_cast<int64_t>(groups) * R;
   int turn = 0;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * R + (W == 1 ? wave : 0); t < c.T; t += teams, turn ^= 1) {
     const int64_t row = t * c.K;
@@ -255,8 +303,8 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
       *reinterpret_cast<u32x4 *>(c.dx + row + k) = o;
     }
   }
-  if (!c.dw) return;
-  float *out = (gridDim.x == 1 ? c.dw : part) + static_cast<int64_t>(blockIdx.x) * c.K;
+  if (!c.dw || gridDim.x > static_cast<uint32_t>(groups)) return;
+  float *out = (groups == 1 ? c.dw : part) + static_cast<int64_t>(blockIdx.x) * c.K;
   if constexpr (R == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -350,6 +398,11 @@ int backward_groups(int T, int K) {
   return static_cast<int>(std::min<int64_t>(groups, K <= 2048 ? 768 : K <= 16384 ? 512 : 256));
 }
 
+// dw beside dx in one launch: both launches of 16 x 5376 8.3 us, this 3.3; 333 x 1160 8.2
+// and 4.0; 1024 x 1160 10.3 and 9.1, x 5376 17.9 and 14.9, x 21504 50.9 and 51.9.
+constexpr int kOneLaunchRows = 1024;
+bool one_backward_launch(int T, int K) { return T > rows_of_workgroup(K) && T <= kOneLaunchRows; }
+
 }  // namespace
 
 hipError_t launch_norm(const NormCall &c, hipStream_t stream) {
@@ -367,7 +420,7 @@ hipError_t launch_norm(const NormCall &c, hipStream_t stream) {
 
 size_t norm_backward_partial_bytes(int T, int K) {
   const int G = backward_groups(T, K);
-  return G > 1 ? static_cast<size_t>(G) * K * sizeof(float) : 0;
+  return G > 1 && !one_backward_launch(T, K) ? static_cast<size_t>(G) * K * sizeof(float) : 0;
 }
 
 hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStream_t stream) {
@@ -377,6 +430,17 @@ hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStrea
     return hipGetLastError();
   }
   const int G = backward_groups(c.T, c.K);
+  const bool one = one_backward_launch(c.T, c.K);
+  if (one && c.dw && c.dx == c.dy) {  // dw has to be done with dy before dx takes its place
+    NormBackward part = c;
+    part.dx = nullptr;
+    const hipError_t e = launch_norm_backward(part, partials, stream);
+    if (e != hipSuccess) return e;
+    part = c;
+    part.dw = nullptr;
+    return launch_norm_backward(part, partials, stream);
+  }
+  const int rows = one && !c.dx ? 0 : G, blocks = rows + (one && c.dw ? (c.K + 63) / 64 : 0);
   const hipError_t e = with_row_shape(c.T, c.K, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     const dim3 block(rows_of_workgroup(c.K) * W * 64);
@@ -386,12 +450,12 @@ hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStrea
       if (e != hipSuccess) return e;
     }
     if (c.w.f32)
-      norm_backward_kernel<W, V, true><<<G, block, lds, stream>>>(c, partials);
+      norm_backward_kernel<W, V, true><<<blocks, block, lds, stream>>>(c, partials, rows);
     else
-      norm_backward_kernel<W, V, false><<<G, block, lds, stream>>>(c, partials);
+      norm_backward_kernel<W, V, false><<<blocks, block, lds, stream>>>(c, partials, rows);
     return hipGetLastError();
   });
-  if (e != hipSuccess || !c.dw || G == 1) return e;
+  if (e != hipSuccess || !c.dw || G == 1 || one) return e;
   norm_dw_kernel<<<(c.K + 15) / 16, 256, 0, stream>>>(partials, G, c.K, c.dw);
   return hipGetLastError();
 }

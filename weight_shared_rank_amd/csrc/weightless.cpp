@@ -1148,11 +1148,15 @@ wl_status weightless_norm(const void *d_x, const void *d_res, int32_t T, int32_t
   return e == hipSuccess ? WL_OK : hip_fail(e, "norm launch");
 }
 
+static size_t norm_backward_bytes(int32_t T, int32_t K) {
+  return std::max<size_t>(256, align256(wl::norm_backward_partial_bytes(T, K)));
+}
+
 size_t weightless_norm_backward_workspace_bytes(int32_t T, int32_t K) {
   wl::NormWeight w;
   if (check_norm(T, K, nullptr, WL_DTYPE_F32, 0.f, w) != WL_OK) return 0;
   g_err.clear();
-  return std::max<size_t>(256, align256(wl::norm_backward_partial_bytes(T, K)));
+  return norm_backward_bytes(T, K);
 }
 
 wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const float *d_rstd, const void *d_dh, int32_t T,
@@ -1169,8 +1173,8 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
         (st = check_aligned(d_rstd, 4, "rstd")) != WL_OK || (st = check_aligned(d_w, 16, "w")) != WL_OK ||
         (st = check_optional(d_dh, 16, "dh")) != WL_OK)
       return st;
-    const size_t need = d_dw ? align256(wl::norm_backward_partial_bytes(T, K)) : 0;
-    if (need) {
+    const size_t need = d_dw ? norm_backward_bytes(T, K) : 0;
+    if (d_dw) {  // (asked for at every size, whether or not the call's form uses it)
       if ((st = check_aligned(d_ws, 256, "workspace")) != WL_OK) return st;
       if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
     }
