@@ -97,7 +97,8 @@ SPLITS = [  # few slots and many tokens; many column tiles; long contractions of
     (2100, (70, 40), 40, 16, 1), (4500, (130,), 200, 64, 2), (6200, (65, 1), 72, 32, 3), (300, (1001,), 8, 32, 256),
     (300, (520, 130), 264, 16, 260), (200, (700,), 72, 128, 200), (70, (2100, 30), 2056, 32, 3), (40, (1100,), 1160, 48, 2),
     (130, (4100,), 64, 16, 4), (130, (100,), 4104, 64, 4), (250, (1001,), 8, 32, 256), (120, (520, 130), 264, 16, 260),
-    (8, (2100, 30), 2056, 32, 3), (12, (4100,), 64, 16, 4), (100, (70,), 2600, 16, 3)]
+    (8, (2100, 30), 2056, 32, 3), (12, (4100,), 64, 16, 4), (100, (70,), 2600, 16, 3),
+    (300, (1001,), 520, 32, 256), (300, (700,), 520, 128, 200)]
 
 
 @pytest.mark.parametrize("T,rows,K,r,n", SPLITS)

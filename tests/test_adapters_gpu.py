@@ -131,6 +131,19 @@ def test_add_long(gpu_lib, T, rows, K, r, n, ranked):
     test_add(gpu_lib, T, rows, K, r, n, ranked)
 
 
+TILES_OF_64 = [  # long contractions, high ranks, and outputs large enough for tiles of 64 tokens
+    (300, (64,), 40000, 16, 1), (40, (72,), 16384, 32, 2), (1600, (30000,), 64, 16, 1), (1600, (30000,), 72, 32, 1),
+    (1600, (30000,), 1032, 16, 1), (1600, (30000,), 1160, 32, 1), (1000, (30000,), 264, 64, 2), (1000, (30000,), 520, 64, 2),
+    (1000, (20000,), 264, 128, 2), (1100, (12000,), 264, 256, 2), (60, (264,), 4096, 128, 5), (900, (9000, 300), 2056, 96, 3),
+    (450, (4104,), 4096, 48, 2)]
+
+
+@pytest.mark.parametrize("T,rows,K,r,n", TILES_OF_64)
+@pytest.mark.parametrize("ranked", [False, True])
+def test_add_in_tiles_of_64(gpu_lib, T, rows, K, r, n, ranked):
+    test_add(gpu_lib, T, rows, K, r, n, ranked)
+
+
 @pytest.mark.parametrize("T", [1, 16, 40, 256, 257, 700])
 @pytest.mark.parametrize("kind", ["none", "one", "last", "sorted"])
 def test_index_patterns(gpu_lib, T, kind):

@@ -9,15 +9,15 @@
 // rows are V^T's and U's.  c z enters the second product as a pair of bf16 (the
 // value and what its rounding left, 16 significant bits); y is rounded once.
 //
-// Few tokens (one_launch): nothing is prepared and there is one launch.
-// Workgroup t looks through the whole index and works if token t is the first, the
-// 17th, ... of its slot.  It makes z of its tile itself, as do the others along the
-// children's rows: V^T comes from L2 then, and a launch that hands z over costs more
-// (64 tokens through gate|up of 2 x 21504 x 5376 at rank 16: 7.5 + 25 us in two).
-// Many tokens: a grouping (group_kernel), z in float32 slices of K (thin_kernel), the
+// Few tokens: nothing is prepared and there is one launch, few_kernel.  Workgroup t
+// looks through the whole index and works if token t is the first, the 17th, ... of its
+// slot.  It makes z of its tile itself, as do the others along the children's rows: V^T
+// comes from L2 then, and a launch that hands z over costs more (64 tokens through
+// gate|up of 2 x 21504 x 5376 at rank 16: 7.5 + 25 us in two).
+// More tokens: a grouping (group_kernel) tells few_kernel the tiles.
+// Many tokens, or a high rank: the grouping, z in float32 slices of K (thin_kernel), the
 // products with U and base (expand_kernel), in tiles of 64 tokens; between them, where
-// many workgroups would add up the same slices, finish_kernel.  (In one launch, tiles
-// of 16: 4096 tokens through 5376 x 8192 at rank 64 56 us, of one round of the CUs 28.)
+// many workgroups would add up the same slices, finish_kernel.
 //
 // Measured: 1 token through 1B q|k|v 5.2 us, of which a launch is most; 64 tokens of 57
 // adapters through 31B gate|up 25 (103 MB read, 4.1 TB/s); 4096 tokens of 12 through 31B
@@ -670,7 +670,8 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
 constexpr int kMaxSlices = 6;
 
 struct Plan {
-  bool grouped;
+  bool few;           // few_kernel
+  bool grouped;       // group_kernel first
   int tiles;          // most tiles there can be
   int blocks, turns;  // workgroups along the children's rows, turns of a wave
   int across;         // rows of a workgroup
@@ -680,49 +681,66 @@ struct Plan {
   size_t perm_at, z_at, p_at, bytes;
 };
 
-// Whether few_kernel alone is faster than the launches of a grouped call.  It makes z
-// once a workgroup (31 thousand products of V^T a microsecond, 46 for one token), and
-// takes 1 us for 512 rows of U a CU (more where a higher rank leaves it fewer waves),
-// counted for as many tiles as there can be; the others 10 us for their launches and 4
-// for every 900 workgroups of expand_kernel.  Measured in us, one launch and grouped:
-//   64 tokens of 4096 -> 4096, rank 16 9.2 and 14.0, 256 15.0 and 15.6, 333 16.2 and 15.8;
-//   128 of 4096 -> 16384, rank 32, 21.2 and 20.3; 64 of 4096 -> 4096, rank 128, 26.6 and 17.2;
-//   128 tokens of 57 adapters through 31B gate|up 43.6 and 67, 256 90 and 66;
-//   512 of 1160 -> 1001, rank 32, 11.2 and 14.5.
-bool one_launch(const AdapterPool &p, int T) {
-  if (T > kThreads) return false;
+// Which launches: few_kernel alone, few_kernel over tiles of 16 that group_kernel has
+// made, or tiles of 64 with z in a launch of its own.  The least of three estimates, in ns:
+//   few_kernel    5000, z once a workgroup (31 products of V^T a ns, 46 for one token), 1000
+//                 for 512 rows of U a CU (more where a higher rank leaves it fewer waves),
+//                 counted for as many tiles as there can be, base and y at 6 TB/s, x at 5
+//   group_kernel  5000
+//   the others    15000, x and V^T, expand_kernel's workgroups (900 in 4300 ns) or base
+//                 and y, U, and 5000 for finish_kernel
+// Kernels' times in us, in that order (most within 20% of the estimates):
+//   333 tokens of 1160 -> 1001, rank 32            9.6  12.5  14.8
+//   64 tokens of 57 adapters, 31B gate|up, rank 16  28    33    66;  400: 87, 59, 70;  1600: -, 106, 125
+//   4096 -> 4096, rank 16, 200 tokens 13.9, 12.5, 15.8;  3200: -, 24, 33
+//   31B gate|up, 8 adapters, 400 tokens -, 27, 42;  800: -, 59, 53;  3200: -, 164, 151
+//   4096 -> 4096, rank 128, 200 tokens 37, 30, 22;  8192 -> 5376, rank 64, 400: 35, 30, 24
+enum class Form { kAlone, kGrouped16, kGrouped64 };
+
+Form fastest_form(const AdapterPool &p, int T) {
   int64_t turns = 0, blocks = 0;
   for (int c = 0; c < p.nchild; ++c) {
     turns += (p.N[c] + kThreads - 1) / kThreads;
     blocks += (p.N[c] + kExpandWaves * 64 - 1) / (kExpandWaves * 64);
   }
-  const int64_t z = static_cast<int64_t>(p.K) * p.r / (T == 1 ? 46 : 31);  // ns
-  const int64_t walk = turns * T * (p.r <= 32 ? 950 : p.r <= 64 ? 1500 : 2400) / kCUs;
-  const int64_t tiles = std::min(T, p.n + 1 + T / kM);
-  return z + walk <= 10000 + std::max<int64_t>(0, tiles * blocks * 4000 / 900 - 4000);
+  const int64_t K = p.K, N = p.Ntot, live = std::min(p.n, T);
+  const int64_t x = T * K / 2500, out = T * N / 1250;  // 2 and 4 bytes at 5 TB/s
+  const auto few = [&](int64_t tiles) {
+    return 5000 + K * p.r / (T == 1 ? 46 : 31) + turns * tiles * (p.r <= 32 ? 950 : p.r <= 64 ? 1500 : 2400) / kCUs + out * 4 / 5 + x;
+  };
+  const int64_t alone = few(T), grouped16 = 5000 + few(std::min(T, p.n + 1 + T / kTileM));
+  const int64_t busy = (T + kM - 1) / kM, tiles = std::min(T, p.n + 1 + T / kM);
+  const int64_t grouped64 = 14500 + x * 13 / 10 + live * p.nchild * p.r * K / 5000 + live * N * p.r / 5000 +
+                            std::max(tiles * blocks * 48 / 10, out * 11 / 10) + (blocks >= 16 && blocks * busy >= 2 * kCUs ? 5000 : 0);
+  if (T <= kThreads && alone <= std::min(grouped16, grouped64)) return Form::kAlone;
+  return grouped16 <= grouped64 ? Form::kGrouped16 : Form::kGrouped64;
 }
 
 Plan make_plan(const AdapterPool &p, int T) {
   Plan q{};
-  q.grouped = !one_launch(p, T);
+  const Form form = fastest_form(p, T);
+  q.few = form != Form::kGrouped64;
+  q.grouped = form != Form::kAlone;
   q.turns = 1;
   auto count_blocks = [&](int across) {
     q.across = across;
     q.blocks = 0;
     for (int c = 0; c < p.nchild; ++c) q.blocks += (p.N[c] + across - 1) / across;
   };
-  if (!q.grouped) {
+  if (q.few) {
     // (a token's workgroups on one XCD: they read the same V^T)
-    q.tiles = T < 8 ? T : tile_places(T);
+    const int most = q.grouped ? std::min(T, p.n + 1 + T / kTileM) : T;
+    q.tiles = most < 8 && !q.grouped ? most : tile_places(most);
     // A workgroup for each CU, or two where they fit and have enough to walk over: 4
     // tokens through 2 x 21504 rows at rank 16 in 168 workgroups 7.3 us, in 336 10.0;
     // 64 tokens in 228 workgroups 30.0, in 456 27.8.
     count_blocks(kThreads);
-    const int64_t all = static_cast<int64_t>(q.blocks) * T;
+    const int64_t all = static_cast<int64_t>(q.blocks) * most;
     q.turns = static_cast<int>((all + kCUs - 1) / kCUs);
     if (p.r == 16 && q.turns > 8) q.turns = static_cast<int>((all + 2 * kCUs - 1) / (2 * kCUs));
     count_blocks(kThreads * q.turns);
-    q.bytes = 256;
+    q.perm_at = align256(sizeof(int4) * q.tiles);  // (the tiles come first)
+    q.bytes = q.grouped ? q.perm_at + align256(sizeof(int32_t) * q.tiles * kTileM) : 256;
     return q;
   }
   count_blocks(kExpandWaves * 64);
@@ -797,7 +815,19 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
     n0 += p.N[c];
     b0 += (p.N[c] + q.across - 1) / q.across;
   }
-  if (!q.grouped) {
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  if (q.grouped) {
+    GroupArgs g{};
+    a.s.max_tiles = q.tiles;
+    g.s = a.s;
+    g.tiles = reinterpret_cast<int4 *>(w);
+    g.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
+    const hipError_t e = q.few ? launch_group<kTileM>(g, stream) : launch_group<kM>(g, stream);
+    if (e != hipSuccess) return e;
+    a.s.tiles = g.tiles;
+    a.s.perm = g.perm;
+  }
+  if (q.few) {
     const dim3 grid(q.tiles, q.blocks);
     const size_t lds = sizeof(uint16_t) * 2 * kTileM * z_pitch(p.r);
     if (p.r == 16)
@@ -808,16 +838,7 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
       few_kernel<256><<<grid, kThreads, lds, stream>>>(a);
     return hipGetLastError();
   }
-  uint8_t *w = static_cast<uint8_t *>(ws);
-  a.s.max_tiles = q.tiles;
-  GroupArgs g{};
-  g.s = a.s;
-  g.tiles = reinterpret_cast<int4 *>(w);
-  g.perm = reinterpret_cast<int32_t *>(w + q.perm_at);
-  hipError_t e = launch_group<kM>(g, stream);
-  if (e != hipSuccess) return e;
-  a.s.tiles = g.tiles;
-  a.s.perm = g.perm;
+  hipError_t e = hipSuccess;
   ProjectArgs z{};
   z.s = a.s;
   z.xb = x;
