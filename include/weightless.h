@@ -512,8 +512,8 @@ size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t 
  *    may run at the same time, need distinct workspaces.
  *  Products of bf16 operands with float32 sums; c (V^T x) enters the second one
  *  as a pair of bf16 (16 significant bits); y is rounded once.  A token's result
- *  does not depend on what the other tokens hold, nor on their order (the order of
- *  its own sums can depend on T and on how many tokens share its slot).
+ *  does not depend on what the other tokens hold (the order of its own sums can
+ *  depend on T and on its place among the tokens of its slot).
  *  What is not finite in a slot or a token's x reaches that slot's or that token's
  *  rows alone.  One launch with few tokens, else two to four. */
 wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, const int32_t *d_index, int32_t T,
