@@ -107,6 +107,22 @@ def test_gradients_of_split_sums(gpu_lib, T, rows, K, r, n, ranked):
     test_gradients(gpu_lib, T, rows, K, r, n, ranked)
 
 
+@pytest.mark.parametrize("T,rows,K,r,n", [(2100, (70, 40), 40, 16, 9), (3000, (200,), 264, 48, 5), (2600, (66, 1, 5), 72, 32, 4), (1000, (1001,), 264, 32, 300),
+                                          (900, (700,), 520, 128, 200), (1300, (300, 300), 520, 16, 300), (5000, (40,), 24, 16, 600)])
+@pytest.mark.parametrize("uneven", ["one", "half", "last"])
+def test_tokens_spread_unevenly(gpu_lib, T, rows, K, r, n, uneven):
+    """Slots whose tokens are cut into parts beside slots that are not."""
+    announce(f"adapters backward T={T} rows={rows} K={K} r={r} n={n} {uneven}")
+    p = make_pool(n, r, K, rows, ranks=[(r, 3, r - 1)[i % 3] for i in range(n)])
+    index = mixed_index(T, n, 3)
+    index[torch.arange(T, device=DEV) % 8 < {"one": 8, "half": 5, "last": 7}[uneven]] = n - 1 if uneven == "last" else n // 2
+    code, dy, base = binding.encode_act(randn(7, T, K)), randn(8, T, sum(rows), std=T ** -0.5), randn(10, T, K, std=T ** -0.5)
+    g = p.backward(code, dy, index, base)
+    check(p, code, dy, index, base, g)
+    for want in ("du", "dv"):
+        assert torch.equal(getattr(p.backward(code, dy, index, want=(want,)), want), getattr(g, want))
+
+
 def test_as_many_tokens_and_slots_as_there_can_be(gpu_lib):
     T, n = 1 << 20, 4096
     announce(f"adapters T={T} n={n}")
@@ -276,6 +292,24 @@ def test_few_tokens_replayed_with_other_slots_and_ranks(gpu_lib):
     for seed in (4, 5, 6, 7):
         index.copy_(mixed_index(T, n, seed) if seed < 7 else torch.full((T,), 2, dtype=torch.int32))
         p.rank.copy_(torch.tensor([32, 0, 7, 16, 31, 17], dtype=torch.int32).roll(seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(p, code, dy, index, base, g)
+        eager = p.backward(code, dy, index, base)
+        assert all(torch.equal(getattr(g, name), getattr(eager, name)) for name in ALL)
+
+
+def test_many_tokens_replayed_between_one_slot_and_many(gpu_lib):
+    T, K, rows, n = 2300, 136, (72,), 9
+    p = make_pool(n, 16, K, rows)
+    code, dy, base, index = binding.encode_act(randn(1, T, K)), randn(2, T, 72, std=0.1), randn(3, T, K), mixed_index(T, n, 3)
+    p.backward(code, dy, index, base)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = p.backward(code, dy, index, base)
+    for i in range(5):
+        index.copy_(torch.full((T,), i, dtype=torch.int32) if i % 2 else mixed_index(T, n, i))
         graph.replay()
         torch.cuda.synchronize()
         check(p, code, dy, index, base, g)

@@ -182,7 +182,12 @@ struct GroupArgs {
   int4 *tiles;
   int32_t *perm;
   int32_t *first, *count;  // per slot [n]: its first tile and tokens (null: not wanted)
-  int32_t *total;          // how many tiles there are, with these
+  int32_t *total;          // with these: how many tiles there are, items, and places
+  // with these too: sums over a slot's tokens, in cuts of at most `cut` steps of 32 tokens:
+  // slot, cut, how many cuts, and (more than one) the cut's place among all such cuts
+  int4 *items;
+  int4 *joins;             // of a place: slot, how many cuts (0 but at the slot's first)
+  int32_t cut;
 };
 
 // Slots of up to kStage tokens from t0 on into LDS; eight loads at a time, none
@@ -231,22 +236,32 @@ __global__ __launch_bounds__(kGroupWaves * 64) void group_kernel(GroupArgs g) {
   }
   __syncthreads();
   __shared__ int tiles_of[kMaxSlots + 1];
+  __shared__ uint16_t cuts_of[kMaxSlots + 1];  // (of steps of 32 tokens, 2^20 at most)
   for (int b = threadIdx.x; b <= s.n; b += kGroupWaves * 64) {
     const bool copy = b == s.n || slot_rank(s.rank, s.r, b) == 0;
     tiles_of[b] = copy && !s.copies ? 0 : (hist[b] + M - 1) / M;
+    if (g.first) {
+      const int steps = copy ? 0 : (hist[b] + 31) / 32;
+      cuts_of[b] = static_cast<uint16_t>(b == s.n ? 0 : steps > g.cut ? (steps + g.cut - 1) / g.cut : 1);
+    }
   }
   __syncthreads();
   const int cnt = mine <= s.n ? hist[mine] : 0, tiles = mine <= s.n ? tiles_of[mine] : 0;
-  int tile0 = 0, total = 0;
+  int tile0 = 0, total = 0, item0 = 0, place0 = 0;
   for (int b = lane; b <= s.n; b += 64) {
     const int k = tiles_of[b];
     total += k;
     tile0 += b < mine ? k : 0;
+    const int c = g.first && b < mine ? cuts_of[b] : 0;
+    item0 += c;
+    place0 += c > 1 ? c : 0;
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     tile0 += __shfl_xor(tile0, d, 64);
     total += __shfl_xor(total, d, 64);
+    item0 += __shfl_xor(item0, d, 64);
+    place0 += __shfl_xor(place0, d, 64);
   }
   if (mine <= s.n) {
     const int rank = mine < s.n ? slot_rank(s.rank, s.r, mine) : 0, slot = rank > 0 ? mine : -1;
@@ -257,7 +272,18 @@ __global__ __launch_bounds__(kGroupWaves * 64) void group_kernel(GroupArgs g) {
       g.first[mine] = tile0;
       g.count[mine] = slot >= 0 ? cnt : 0;
     }
-    if (g.first && mine == s.n && id == 0) *g.total = total;
+    if (g.first && mine == s.n && id == 0) {
+      g.total[0] = total;
+      g.total[1] = item0;
+      g.total[2] = place0;
+    }
+    if (g.first && mine < s.n) {
+      const int cuts = cuts_of[mine];
+      for (int q = id; q < cuts; q += width) {
+        g.items[item0 + q] = int4{mine, q, cuts, place0 + q};
+        if (cuts > 1) g.joins[place0 + q] = int4{mine, q == 0 ? cuts : 0, 0, 0};
+      }
+    }
     if (tiles) {
       int32_t *last = g.perm + static_cast<int64_t>(tile_place(tile0 + tiles - 1, total)) * M;
       for (int i = cnt - (tiles - 1) * M + id; i < M; i += width) last[i] = -1;

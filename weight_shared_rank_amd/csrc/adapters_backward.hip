@@ -8,7 +8,7 @@
 // (with one slice of both, project_kernel's own end) as pairs of bf16 (the value and what
 // its rounding left), each 16 x 32 piece of them stored as the 64 lanes' operand of a
 // matrix instruction, so that the products load it as 1 KB; gradient_kernel, dx, dU and
-// dV; join_kernel, where the tokens of a slot were cut for dU and dV.
+// dV; with many tokens join_kernel, for slots whose tokens were cut for dU and dV.
 //
 // U (for g), V^T (for dx) and dy and X (for dU and dV) enter a product along
 // their slow dimension.  They come from memory as rows, 16 bytes a lane, go through
@@ -21,7 +21,7 @@
 //
 // Bound by memory: dy is read twice, for g and for dU, and everything else once.  As
 // in the forward pass no load of a loop is conditional.  4096 tokens of 16 adapters
-// through 31B gate|up, rank 32: 7 + 96 + 6 + 105 us; project_kernel reads 418 MB (4.4
+// through 31B gate|up, rank 32: 7 + 96 + 6 + 106 + 4 us; project_kernel reads 418 MB (4.4
 // TB/s, its last workgroups alone), gradient_kernel moves 560 MB (5.3 TB/s).  2048 tokens
 // through 1B q|k|v: 6.3 + 9 + 11.  One pass over dy would hold dU of 64 columns and all
 // ranks in a wave and write g of each 512 columns, 176 MB for the 352 it saves; not built.
@@ -159,7 +159,8 @@ static_assert(16 * kOutPitch <= kPiece, "the sums fit the piece");
 struct GradArgs {
   TileSource s;
   const int32_t *first, *count;  // per slot: first tile, tokens
-  const int32_t *total;          // tiles
+  const int32_t *total;          // tiles, items, places
+  const int4 *items;             // slot, cut, cuts, place among the slots' with more than one
   CodedView x;
   const uint16_t *vt, *dy;
   const uint16_t *zT, *gT, *grows;
@@ -167,16 +168,17 @@ struct GradArgs {
   int32_t R, RC;
   const uint16_t *base;
   uint16_t *dx, *du, *dv;
-  // sums of a cut of a slot's tokens: float [cuts][part], dU's elements, then from vat on dV's
-  float *parts;
-  int64_t part, vat;
-  int32_t cuts;
-  // workgroups: dU and dV [slots][cuts][groups of 16 JF ranks][column tiles of 64, or four
-  // of them], then dx [K blocks of 256][half tiles]
+  // the cuts of slots that have several: their sums, as the lanes hold them, KB by KB of
+  // place * units + unit
+  const int4 *joins;
+  f32x4 *parts;
+  int32_t units;  // a slot's column tiles times groups of ranks, dU's and then dV's
+  // workgroups: dU and dV [items][groups of 16 JF ranks][column tiles of 64, or four of
+  // them], then dx [K blocks of 256][half tiles]
   int32_t tiles, kblocks;
   int32_t jgroups;              // groups of ranks of a child
   int32_t ublock0[kMaxChildren + 1], vblocks;  // column tiles of the children's rows (running), of K
-  int64_t units[3];             // dU, dV, dx
+  int64_t blocks[3];            // of dU, dV, dx
 };
 
 // dx of 32 of a tile's tokens by 256 k, 64 a wave.  V^T rows of 32 ranks at a time and
@@ -265,16 +267,17 @@ __device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *
 // Tokens of a slot.
 struct Segment {
   int count, tile0, ntiles;  // tile0: its first tile of ntiles
+  int from, stride, end;     // steps of 32 to take
   const int *list;           // or (FEW) the tokens, in LDS
 };
 
 // The sum over a slot's tokens for 64 columns of dy (dU) or of X (VGRAD: dV), by 16 JF
-// ranks: 32 positions a step, every stride-th one from `from` on.  FULL: 64 columns exist.
+// ranks: 32 positions a step.  FULL: 64 columns exist.
 template <int JF, bool VGRAD, bool FEW, bool FULL>
-__device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg, int c, int j0, int col0, int cols, int from, int stride,
-                                           uint8_t *piece, f32x4 (&acc)[4][JF]) {
-  const int lane = threadIdx.x & 63, r16 = lane & 15, count = seg.count;
-  const int steps = (count + 31) / 32, RT = a.R / 16, col = col0 + (lane & 7) * 8;
+__device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg, int c, int j0, int col0, int cols, uint8_t *piece,
+                                           f32x4 (&acc)[4][JF]) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, count = seg.count, from = seg.from, stride = seg.stride, steps = seg.end;
+  const int RT = a.R / 16, col = col0 + (lane & 7) * 8;
   const u32x4 zero{0u, 0u, 0u, 0u};
   // the thin operand's pieces, from column tile (c r + j0) / 16 of z or g on
   const uint16_t *thin = (VGRAD ? a.gT : a.zT) + static_cast<int64_t>((c * a.s.r + j0) / 16) * 1024;
@@ -371,30 +374,34 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
   }
 }
 
-// WAYS 1: a wave has its own column tile; 4: the waves of a.cuts workgroups share one, a
-// part of the tokens each; with more than one cut their sums leave as floats.
-template <int JF, bool VGRAD, int WAYS, bool FEW>
-__device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds, int *list) {
-  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6), r16 = lane & 15, g = lane >> 4;
-  const int r = a.s.r;
-  // column tiles fastest: the tiles of a slot run together
-  const int blocks = VGRAD ? a.nchild * a.vblocks : a.ublock0[a.nchild], ctiles = (blocks * WAYS + 3) / 4;
-  int ct = static_cast<int>(id % ctiles);
-  const int64_t rest = id / ctiles;
-  const int j0 = static_cast<int>(rest % a.jgroups) * JF * 16, sc = static_cast<int>(rest / a.jgroups), slot = sc / a.cuts, cut = sc % a.cuts;
-  Segment seg{};
-  if constexpr (FEW) {
-    seg.count = keep(list_tokens(a.s, slot, list));
-    seg.list = list;
+// Two neighbouring 16-column tiles (number `pair` of 64 from col0 on) of the 16 ranks from
+// j on of child c to memory; zeros past the slot's rank, also where dy is not finite.
+template <bool VGRAD>
+__device__ __forceinline__ void store_sums_of(const GradArgs &a, int slot, int rank, int c, int j, int col0, int pair, f32x4 (&s)[2]) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4, r = a.s.r;
+  if (j >= r) return;
+  if constexpr (VGRAD) {
+    const int k = col0 + 32 * pair + 8 * g;
+    if (j + r16 >= rank) s[0] = s[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (k < a.K)
+      *reinterpret_cast<u32x4 *>(a.dv + (static_cast<int64_t>(slot) * a.R + c * r + j + r16) * a.K + k) =
+          u32x4{pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
   } else {
-    seg.count = keep(a.count[slot]);
-    seg.tile0 = keep(a.first[slot]);
-    seg.ntiles = keep(*a.total);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int n = col0 + 16 * (2 * pair + h) + r16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[h][k] = j + 4 * g + k < rank ? s[h][k] : 0.f;
+      if (n < a.N[c])
+        *reinterpret_cast<u32x2 *>(a.du + (static_cast<int64_t>(slot) * a.Ntot + a.n0[c] + n) * r + j + 4 * g) =
+            u32x2{pack_bf16(s[h][0], s[h][1]), pack_bf16(s[h][2], s[h][3])};
+    }
   }
-  if constexpr (WAYS == 1) {
-    ct = ct * 4 + wave;
-    if (ct >= blocks) return;
-  }
+}
+
+// Child of a column tile, which becomes the child's.
+template <bool VGRAD>
+__device__ __forceinline__ int child_of_tile(const GradArgs &a, int &ct) {
   int c = 0;
   if constexpr (VGRAD) {
     c = ct / a.vblocks;
@@ -405,6 +412,46 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
       if (i < a.nchild && ct >= a.ublock0[i]) c = i;
     ct -= a.ublock0[c];
   }
+  return c;
+}
+
+// WAYS 1: a wave has its own column tile; 4: the waves of a workgroup share one, a part of
+// the tokens each.
+template <int JF, bool VGRAD, int WAYS, bool FEW>
+__device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds, int *list) {
+  const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6);
+  const int r = a.s.r;
+  // column tiles fastest: the tiles of a slot run together
+  const int blocks = VGRAD ? a.nchild * a.vblocks : a.ublock0[a.nchild], ctiles = (blocks * WAYS + 3) / 4;
+  int ct = static_cast<int>(id % ctiles);
+  const int64_t rest = id / ctiles;
+  const int jg = static_cast<int>(rest % a.jgroups), j0 = jg * JF * 16, item = static_cast<int>(rest / a.jgroups);
+  int slot = item, cut = 0, cuts = 1, place = 0;
+  Segment seg{};
+  if constexpr (FEW) {
+    seg.count = keep(list_tokens(a.s, slot, list));
+    seg.list = list;
+  } else {
+    if (item >= keep(a.total[1])) return;
+    const int4 e = a.items[item];
+    slot = keep(e.x);
+    cut = keep(e.y);
+    cuts = keep(e.z);
+    place = keep(e.w);
+    seg.count = keep(a.count[slot]);
+    seg.tile0 = keep(a.first[slot]);
+    seg.ntiles = keep(a.total[0]);
+  }
+  if constexpr (WAYS == 1) {
+    ct = ct * 4 + wave;
+    if (ct >= blocks) return;
+  }
+  const int unit = (VGRAD ? a.ublock0[a.nchild] * a.jgroups : 0) + jg * blocks + ct;
+  const int steps = (seg.count + 31) / 32, per = (steps + cuts - 1) / cuts, lo = cut * per;
+  seg.end = min(lo + per, steps);
+  seg.from = WAYS == 1 ? lo : lo + wave;
+  seg.stride = WAYS;
+  const int c = child_of_tile<VGRAD>(a, ct);
   const int col0 = ct * 64, cols = VGRAD ? a.K : a.N[c];
   f32x4 acc[4][JF];
 #pragma unroll
@@ -412,42 +459,19 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
 #pragma unroll
     for (int f = 0; f < JF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint8_t *const piece = lds + wave * kPiece;
-  const int from = WAYS == 1 ? 0 : cut * 4 + wave, stride = WAYS == 1 ? 1 : 4 * a.cuts;
   if (col0 + 64 <= cols)
-    sum_tokens<JF, VGRAD, FEW, true>(a, seg, c, j0, col0, cols, from, stride, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, true>(a, seg, c, j0, col0, cols, piece, acc);
   else
-    sum_tokens<JF, VGRAD, FEW, false>(a, seg, c, j0, col0, cols, from, stride, piece, acc);
-  // zeros past the slot's rank, also where dy is not finite
+    sum_tokens<JF, VGRAD, FEW, false>(a, seg, c, j0, col0, cols, piece, acc);
   const int rank = slot_rank(a.s.rank, r, slot);
-  // two neighbouring column tiles of rank tile f to memory
+  // a pair of column tiles of rank tile f: the cut's sums for join_kernel, or the gradient
+  f32x4 *const parts = a.parts + (static_cast<int64_t>(place) * a.units + unit) * 4 * JF * 64 + lane;
   auto store = [&](f32x4 (&s)[2], int pair, int f) {
-    if (j0 + 16 * f >= r) return;
-    if constexpr (VGRAD) {
-      const int k = col0 + 32 * pair + 8 * g, j = j0 + 16 * f + r16;
-      if (j >= rank) s[0] = s[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int64_t at = (static_cast<int64_t>(slot) * a.R + c * r + j) * a.K + k;
-      if (k >= a.K) return;
-      if (WAYS == 4 && a.cuts > 1) {
-        f32x4 *o = reinterpret_cast<f32x4 *>(a.parts + cut * a.part + a.vat + at);
-        o[0] = s[0];
-        o[1] = s[1];
-      } else {
-        *reinterpret_cast<u32x4 *>(a.dv + at) =
-            u32x4{pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
-      }
+    if (cuts > 1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) parts[((2 * pair + h) * JF + f) * 64] = s[h];
     } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = col0 + 16 * (2 * pair + h) + r16;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[h][k] = j0 + 16 * f + 4 * g + k < rank ? s[h][k] : 0.f;
-        const int64_t at = (static_cast<int64_t>(slot) * a.Ntot + a.n0[c] + n) * r + j0 + 16 * f + 4 * g;
-        if (n >= cols) continue;
-        if (WAYS == 4 && a.cuts > 1)
-          *reinterpret_cast<f32x4 *>(a.parts + cut * a.part + at) = s[h];
-        else
-          *reinterpret_cast<u32x2 *>(a.du + at) = u32x2{pack_bf16(s[h][0], s[h][1]), pack_bf16(s[h][2], s[h][3])};
-      }
+      store_sums_of<VGRAD>(a, slot, rank, c, j0 + 16 * f, col0, pair, s);
     }
   };
   if constexpr (WAYS == 1) {
@@ -471,15 +495,16 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
         for (int i = 0; i < 4; ++i) part[((wave * 4 + i) * JC + f) * 64 + lane] = acc[i][f0 + f];
       __syncthreads();
       if ((wave >> 1) >= JC) continue;
+      const int pair = wave & 1;
       f32x4 s[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const f32x4 *p = part + ((2 * (wave & 1) + h) * JC + (wave >> 1)) * 64 + lane;
+        const f32x4 *p = part + ((2 * pair + h) * JC + (wave >> 1)) * 64 + lane;
         s[h] = p[0];
 #pragma unroll
         for (int w = 1; w < kGradWaves; ++w) s[h] += p[w * 4 * JC * 64];
       }
-      store(s, wave & 1, f0 + (wave >> 1));
+      store(s, pair, f0 + (wave >> 1));
     }
   }
 }
@@ -490,32 +515,45 @@ __global__ __launch_bounds__(kGradWaves * 64, JF == 4 ? 2 : 4) void gradient_ker
   __shared__ int tok[FEW ? kLeaderT : kM];
   __shared__ __align__(16) uint8_t lds[SUM > PIECES ? SUM : PIECES];
   int64_t id = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-  if (id < a.units[0]) return weight_unit<JF, false, WAYS, FEW>(a, id, lds, tok);
-  id -= a.units[0];
-  if (id < a.units[1]) return weight_unit<JF, true, WAYS, FEW>(a, id, lds, tok);
-  id -= a.units[1];
-  if (id < a.units[2]) dx_unit(a, id, lds, tok);
+  if (id < a.blocks[0]) return weight_unit<JF, false, WAYS, FEW>(a, id, lds, tok);
+  id -= a.blocks[0];
+  if (id < a.blocks[1]) return weight_unit<JF, true, WAYS, FEW>(a, id, lds, tok);
+  id -= a.blocks[1];
+  if (id < a.blocks[2]) dx_unit(a, id, lds, tok);
 }
 
-// dU and dV from the cuts' sums, in order.
-struct JoinArgs {
-  const float *parts;
-  int64_t part, vat;
-  int32_t cuts;
-  uint16_t *du, *dv;
-};
-
-__global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < a.part; i += static_cast<int64_t>(gridDim.x) * 2048) {
-    f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+// The sums of a slot's cuts, in their order: a wave takes 32 columns of a unit and one
+// rank tile.
+template <int JF>
+__global__ __launch_bounds__(256) void join_kernel(GradArgs a) {
+  const int lane = threadIdx.x & 63, place = blockIdx.y;
+  const int id = static_cast<int>(blockIdx.x) * 4 + keep(threadIdx.x >> 6), f = id / 2 % JF, pair = id & 1;
+  int unit = id / (2 * JF);
+  if (place >= keep(a.total[2]) || unit >= a.units) return;
+  const int4 e = a.joins[place];
+  const int slot = keep(e.x), cuts = keep(e.y);
+  if (cuts == 0) return;
+  const f32x4 *p = a.parts + ((static_cast<int64_t>(place) * a.units + unit) * 4 * JF + 2 * pair * JF + f) * 64 + lane;
+  const int64_t next = static_cast<int64_t>(a.units) * 4 * JF * 64;
+  f32x4 s[2] = {p[0], p[JF * 64]};
 #pragma unroll 4
-    for (int c = 0; c < a.cuts; ++c) {
-      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.parts + c * a.part + i);
-      s[0] += p[0];
-      s[1] += p[1];
-    }
-    *reinterpret_cast<u32x4 *>(i < a.vat ? a.du + i : a.dv + (i - a.vat)) =
-        u32x4{pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
+  for (int q = 1; q < cuts; ++q) {
+    s[0] += p[q * next];
+    s[1] += p[q * next + JF * 64];
+  }
+  const int rank = slot_rank(a.s.rank, a.s.r, slot), ublocks = a.ublock0[a.nchild];
+  if (unit < ublocks * a.jgroups) {
+    if (!a.du) return;
+    int ct = unit % ublocks;
+    const int j = (unit / ublocks * JF + f) * 16, c = child_of_tile<false>(a, ct);
+    store_sums_of<false>(a, slot, rank, c, j, ct * 64, pair, s);
+  } else {
+    if (!a.dv) return;
+    unit -= ublocks * a.jgroups;
+    const int blocks = a.nchild * a.vblocks;
+    int ct = unit % blocks;
+    const int j = (unit / blocks * JF + f) * 16, c = child_of_tile<true>(a, ct);
+    store_sums_of<true>(a, slot, rank, c, j, ct * 64, pair, s);
   }
 }
 
@@ -528,10 +566,11 @@ __global__ __launch_bounds__(256) void fill_zero_16(u32x4 *p, int64_t n) {
 struct BackPlan {
   bool few;  // no grouping launch
   int tiles, NF, zgroups, zslices, zper, ggroups, gslices, gper, RC;
-  int ublock0[kMaxChildren + 1], vblocks, cuts;
+  int ublock0[kMaxChildren + 1], vblocks;
+  int units, cut, places;  // of a slot; most steps of a cut; most cuts of slots that have several
   bool own;  // gradient_kernel's waves have column tiles of their own
-  int64_t rows, u_elements, v_elements;
-  size_t perm_at, slots_at, pz_at, pg_at, zt_at, gt_at, grows_at, parts_at, bytes;
+  int64_t rows;
+  size_t perm_at, slots_at, pz_at, pg_at, zt_at, gt_at, grows_at, items_at, joins_at, parts_at, bytes;
 };
 
 BackPlan make_back_plan(const AdapterPool &p, int T) {
@@ -558,16 +597,27 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
   cut_slices(widest, stage, kShortest, busy * q.ggroups * p.nchild, 8, q.gslices, q.gper);
   for (int c = 0; c < p.nchild; ++c) q.ublock0[c + 1] = q.ublock0[c] + (p.N[c] + 63) / 64;
   q.vblocks = (p.K + 63) / 64;
-  const int64_t blocks = static_cast<int64_t>(p.n) * q.ggroups * (q.ublock0[p.nchild] + p.nchild * q.vblocks);
+  q.units = q.ggroups * (q.ublock0[p.nchild] + p.nchild * q.vblocks);
   // Column tiles of their own save the waves the sums between them, where there are many
   // (16 adapters of 31B gate|up 134 -> 109 us, 32 of 8192 -> 5376 at rank 64 100 -> 75; but
   // 8 of 2048 -> 4096, 768 tiles, 12.2 -> 20.0, one of 31B gate|up, 840, 108 -> 133).
-  // With few, the tokens are cut until 4 workgroups of a CU are busy and a wave has 8 steps
-  // (8192 tokens of one 1B q|k|v adapter: 53 -> 27 us and 4 for the joining).
-  q.own = blocks >= 4096;
-  q.cuts = q.own ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 4 * kCUs / blocks, T / (static_cast<int64_t>(p.n) * 128) / 8})));
-  q.u_elements = static_cast<int64_t>(p.n) * p.Ntot * p.r;
-  q.v_elements = static_cast<int64_t>(p.n) * R * p.K;
+  q.own = static_cast<int64_t>(p.n) * q.units >= 4096;
+  // How a call's tokens spread over the slots is not known here.  If one slot has them
+  // all, its cuts are to keep 4 workgroups, or 16 waves, of a CU busy (3409 tokens in one
+  // of 23 slots, 2 x 169 x 64 at rank 48: 85 -> 32 us; 8192 of one 1B q|k|v adapter 77 ->
+  // 58; 4096 in one of 16 of 31B gate|up 288 -> 235).  Joining takes 4 us, cut or not (2048
+  // tokens of 8 1B q|k|v adapters 26.7 -> 31.8), so shorter calls go without (one of 8
+  // slots of 4096 -> 2048 would gain 3 us from 2048 tokens; with own column tiles 1071
+  // tokens in one of 34 slots 137 -> 85).  Cuts of 16 steps or 8, and of 24, 16 or 12 with
+  // own tiles, differ by 10%.
+  const int64_t steps = (T + 31) / 32;
+  const int shortest = q.own ? 16 : 8, fewest = q.own ? 24 : 64;
+  q.cut = static_cast<int>(std::max<int64_t>(shortest, steps * q.units / ((q.own ? 16 : 4) * kCUs)));
+  if (steps <= fewest) q.cut = static_cast<int>(steps + 1);
+  // Slots of more than `cut` steps: L of them have more than L cut of the steps + L there
+  // can be, and s steps make at most s / cut + (cut - 1) / cut cuts.
+  const int64_t L = steps / (q.cut - 1);
+  q.places = steps > q.cut ? static_cast<int>((steps + L) / q.cut + L + 1) : 0;
   size_t at = align256(sizeof(int4) * q.tiles);  // the tiles come first
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -575,13 +625,15 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
     return here;
   };
   q.perm_at = take(sizeof(int32_t) * q.rows);
-  q.slots_at = take(sizeof(int32_t) * (2 * static_cast<size_t>(p.n) + 1));
+  q.slots_at = take(sizeof(int32_t) * (2 * static_cast<size_t>(p.n) + 3));
+  q.items_at = take(sizeof(int4) * (static_cast<size_t>(p.n) + q.places));
+  q.joins_at = take(sizeof(int4) * q.places);
   q.pz_at = take(sizeof(float) * q.zslices * q.rows * R);
   q.pg_at = take(sizeof(float) * q.gslices * q.rows * R);
   q.zt_at = take(2 * sizeof(uint16_t) * q.rows * R);
   q.gt_at = take(2 * sizeof(uint16_t) * q.rows * R);
   q.grows_at = take(2 * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32);
-  q.parts_at = take(q.cuts > 1 ? sizeof(float) * q.cuts * (q.u_elements + q.v_elements) : 0);
+  q.parts_at = take(size_t{4096} * q.NF * q.places * q.units);
   q.bytes = at;
   return q;
 }
@@ -620,6 +672,9 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   gr.first = reinterpret_cast<int32_t *>(w + q.slots_at);
   gr.count = gr.first + p.n;
   gr.total = gr.count + p.n;
+  gr.items = reinterpret_cast<int4 *>(w + q.items_at);
+  gr.cut = q.cut;
+  gr.joins = reinterpret_cast<int4 *>(w + q.joins_at);
   hipError_t e = hipSuccess;
   if (!q.few) {
     if ((e = launch_group<kM>(gr, stream)) != hipSuccess) return e;
@@ -708,15 +763,16 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
     d.n0[c] = a.n0[c];
   }
   d.jgroups = q.ggroups;
-  d.cuts = q.cuts;
-  d.parts = reinterpret_cast<float *>(w + q.parts_at);
-  d.vat = o.du ? q.u_elements : 0;
-  d.part = d.vat + (o.dv ? q.v_elements : 0);
-  auto units = [&](int blocks) { return static_cast<int64_t>(p.n) * d.jgroups * (q.own ? (blocks + 3) / 4 : blocks * d.cuts); };
-  d.units[0] = o.du ? units(d.ublock0[p.nchild]) : 0;
-  d.units[1] = o.dv ? units(p.nchild * d.vblocks) : 0;
-  d.units[2] = o.dx ? static_cast<int64_t>(q.tiles) * 2 * d.kblocks : 0;
-  const int64_t total = d.units[0] + d.units[1] + d.units[2];
+  d.items = gr.items;
+  d.joins = gr.joins;
+  d.parts = reinterpret_cast<f32x4 *>(w + q.parts_at);
+  d.units = q.units;
+  const int64_t items = p.n + (q.few ? 0 : q.places);
+  auto blocks_of = [&](int tiles) { return items * d.jgroups * (q.own ? (tiles + 3) / 4 : tiles); };
+  d.blocks[0] = o.du ? blocks_of(d.ublock0[p.nchild]) : 0;
+  d.blocks[1] = o.dv ? blocks_of(p.nchild * d.vblocks) : 0;
+  d.blocks[2] = o.dx ? static_cast<int64_t>(q.tiles) * 2 * d.kblocks : 0;
+  const int64_t total = d.blocks[0] + d.blocks[1] + d.blocks[2];
   // (a launch holds fewer than 2^32 threads along x)
   constexpr int64_t kAcross = int64_t{1} << 20;
   const dim3 blocks(static_cast<uint32_t>(std::min(total, kAcross)), static_cast<uint32_t>((total + kAcross - 1) / kAcross));
@@ -733,15 +789,14 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
     run(std::integral_constant<int, 2>{});
   else
     run(std::integral_constant<int, 4>{});
-  if ((e = hipGetLastError()) != hipSuccess || q.cuts == 1 || d.part == 0) return e;
-  JoinArgs j{};
-  j.parts = d.parts;
-  j.part = d.part;
-  j.vat = d.vat;
-  j.cuts = d.cuts;
-  j.du = o.du;
-  j.dv = o.dv;
-  join_kernel<<<static_cast<uint32_t>(std::min<int64_t>((d.part + 2047) / 2048, 8 * kCUs)), 256, 0, stream>>>(j);
+  if ((e = hipGetLastError()) != hipSuccess || q.places == 0 || d.blocks[0] + d.blocks[1] == 0) return e;
+  const dim3 joins((q.units * 2 * q.NF + 3) / 4, q.places);
+  if (q.NF == 1)
+    join_kernel<1><<<joins, 256, 0, stream>>>(d);
+  else if (q.NF == 2)
+    join_kernel<2><<<joins, 256, 0, stream>>>(d);
+  else
+    join_kernel<4><<<joins, 256, 0, stream>>>(d);
   return hipGetLastError();
 }
 
