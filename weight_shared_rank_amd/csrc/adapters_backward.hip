@@ -575,13 +575,6 @@ struct BackPlan {
 
 BackPlan make_back_plan(const AdapterPool &p, int T) {
   BackPlan q{};
-  // Without the grouping a tile's place is its first token's, and workgroups at the other
-  // places look and leave: pays for dx's while they are few (77 tokens, 712 -> 1001, 480
-  // workgroups: 17.4 -> 14.1 us; 8 of 4096 -> 4096, 256: 21.6 -> 19.1; 64 of them, 2048:
-  // 24.2 -> 25.1; 256, 8192: 26.4 -> 39.6).
-  q.few = T <= kLeaderT && static_cast<int64_t>(tile_places(T)) * 2 * ((p.K + 255) / 256) <= 4 * kCUs;
-  q.tiles = q.few ? tile_places(T) : tile_places(T / kM + std::min(p.n + 1, T));
-  q.rows = static_cast<int64_t>(q.tiles) * kM;
   const int row_tiles = p.r / 16, R = p.nchild * p.r;
   q.NF = row_tiles >= 3 ? 4 : row_tiles;
   q.zgroups = (p.nchild * row_tiles + q.NF - 1) / q.NF;
@@ -595,6 +588,15 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
   constexpr int kShortest = 2 * kDeep;
   cut_slices(p.K, stage, kShortest, busy * q.zgroups, 4, q.zslices, q.zper);
   cut_slices(widest, stage, kShortest, busy * q.ggroups * p.nchild, 8, q.gslices, q.gper);
+  // Without the grouping a tile's place is its first token's, and workgroups at the other
+  // places look and leave: pays while they are few (dx's for 77 tokens, 712 -> 1001, 480:
+  // 17.4 -> 14.1 us; 8 of 4096 -> 4096, 256: 21.6 -> 19.1; 64 of them, 2048: 24.2 -> 25.1;
+  // 256, 8192: 26.4 -> 39.6).
+  const int64_t places = tile_places(T);
+  q.few = T <= kLeaderT && places * 2 * ((p.K + 255) / 256) <= 4 * kCUs &&
+          places * (q.zgroups * q.zslices + q.ggroups * p.nchild * q.gslices) <= 4 * kCUs;
+  q.tiles = q.few ? tile_places(T) : tile_places(T / kM + std::min(p.n + 1, T));
+  q.rows = static_cast<int64_t>(q.tiles) * kM;
   for (int c = 0; c < p.nchild; ++c) q.ublock0[c + 1] = q.ublock0[c] + (p.N[c] + 63) / 64;
   q.vblocks = (p.K + 63) / 64;
   q.units = q.ggroups * (q.ublock0[p.nchild] + p.nchild * q.vblocks);
