@@ -122,7 +122,8 @@ def test_add(gpu_lib, T, rows, K, r, n, ranked):
 LONG = [  # enough rows for whole tiles of tokens: K cut into slices, and short
     (2100, (4100,), 1032, 16, 3), (1100, (3000, 4700), 696, 64, 3), (600, (14000,), 520, 128, 2), (1100, (8200,), 520, 256, 2),
     (2100, (4100,), 64, 32, 3), (1100, (8200,), 72, 48, 2), (700, (12000,), 8, 112, 2), (1100, (8200,), 136, 176, 2), (600, (264,), 264, 16, 600), (512, (40, 72), 136, 16, 3), (513, (40, 72), 136, 16, 3),
-    (512, (300,), 264, 48, 40), (1, (264,), 8192, 256, 2), (1, (264,), 4096, 64, 2), (60, (264,), 8192, 64, 5), (40, (30000,), 264, 32, 30)]
+    (512, (300,), 264, 48, 40), (1, (264,), 8192, 256, 2), (1, (264,), 4096, 64, 2), (60, (264,), 8192, 64, 5), (40, (30000,), 264, 32, 30),
+    (40, (30000,), 264, 16, 40), (300, (29999, 9), 264, 16, 40)]
 
 
 @pytest.mark.parametrize("T,rows,K,r,n", LONG)

@@ -174,6 +174,17 @@ def test_forward_with_few_and_many_rows(gpu_lib, T, K):
     check_forward(binding.norm_act(x, w, residual=r, want=ALL), x, w, r, 0.0, EPS)
 
 
+@pytest.mark.parametrize("T,K", [(70000, 512), (36000, 1000), (20000, 2048), (20000, 2056), (9000, 5376), (6000, 8192), (3600, 12000), (2400, 24584)])
+def test_rows_past_what_the_caches_hold(gpu_lib, T, K):
+    announce(f"norm {T} x {K}")
+    x, r, w = randn(1, T, K), randn(2, T, K), randn(3, K)
+    o = binding.norm_act(x, w, residual=r, want=ALL)
+    check_forward(o, x, w, r, 0.0, EPS)
+    g = binding.norm_backward(x, o.h, o.rstd, w, 0.0, r)
+    check_backward(g, x, o.h, o.rstd, w, 0.0, r)
+    assert torch.equal(binding.norm_backward(x, o.h, o.rstd, w, 0.0, r, dx=r).dx, g.dx)
+
+
 def test_gradients_against_differences(gpu_lib):
     """<dx, v> and <dw, u> against central differences of the float64 forward.
     With a step of 1e-4 they are off by about 1e-8 of the second derivative's

@@ -46,6 +46,10 @@ __device__ __forceinline__ u32x4 ld16_at(const uint16_t *base, uint32_t bytes) {
   return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint8_t *>(base) + bytes);
 }
 
+__device__ __forceinline__ u32x4 ld16_once_at(const uint16_t *base, uint32_t bytes) {
+  return ld16_once(reinterpret_cast<const uint16_t *>(reinterpret_cast<const uint8_t *>(base) + bytes));
+}
+
 // Rank of a slot, in [0, r].
 __device__ __forceinline__ int slot_rank(const int32_t *rank, int r, int a) {
   return rank ? min(max(rank[a], 0), r) : r;
@@ -55,6 +59,9 @@ __device__ __forceinline__ int slot_rank(const int32_t *rank, int r, int a) {
 // memory path takes them whole.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 __device__ __forceinline__ u32x4 ld16_any(const uint16_t *p) { return *reinterpret_cast<const u32x4_any *>(p); }
+__device__ __forceinline__ u32x4 ld16_any_once(const uint16_t *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+}
 __device__ __forceinline__ void st16_any(uint16_t *p, u32x4 v) { *reinterpret_cast<u32x4_any *>(p) = v; }
 
 // The first n of 8 bf16, zeros behind them.

@@ -20,8 +20,8 @@
 // many workgroups would add up the same slices, finish_kernel.
 //
 // Measured: 1 token through 1B q|k|v 5.2 us, of which a launch is most; 64 tokens of 57
-// adapters through 31B gate|up 25 (103 MB read, 4.1 TB/s); 4096 tokens of 12 through 31B
-// o at rank 64 6.7 + 20 + 5.5 + 26 (thin_kernel 80 MB at 4 TB/s, expand_kernel 100 at 3.9).
+// adapters through 31B gate|up 26.5 (103 MB read, 114 moved); 4096 tokens of 12 through 31B
+// o at rank 64 6.9 + 19 + 5 + 26 (thin_kernel 80 MB at 4.2 TB/s, expand_kernel 100 at 3.9).
 //
 // Everything moves as rows, 8 lanes to a cache line, and reaches the matrix cores
 // through LDS: fragments loaded as they are used (16 rows of 64 bytes a load) pass
@@ -297,7 +297,7 @@ __device__ __forceinline__ void dot_z(const AdapterArgs &a, const Tile &t, const
 constexpr int kUPitch = 80, kOutPitch = 272, kWaveLds = 64 * kUPitch;  // bytes
 static_assert(16 * kOutPitch <= kWaveLds, "the sums fit the piece");
 
-template <int UNITS, int CW>
+template <int UNITS, int CW, bool ONCE>
 struct RowWalk {
   static constexpr int CHUNKS = CW ? CW : 1, PER = CW ? 4 : 2, LOADS = PER * CHUNKS, ROWS = CW ? 16 : 32;
   static constexpr int COLS = CW ? 32 * CW * UNITS : 16;  // ranks it reads
@@ -346,7 +346,7 @@ struct RowWalk {
       for (int q = 0; q < PER; ++q) {
         const int k0 = (unit * CHUNKS + ch) * 32;
         if constexpr (FULL)
-          o[ch * PER + q] = ld16_at(p + k0, uoff[q]);
+          o[ch * PER + q] = ONCE ? ld16_once_at(p + k0, uoff[q]) : ld16_at(p + k0, uoff[q]);
         else
           o[ch * PER + q] = ld16(U + static_cast<int64_t>(min(nw + ROWS * q + urow, N - 1)) * r + (k0 + ucol < r ? k0 + ucol : 0));
       }
@@ -463,8 +463,12 @@ constexpr int kRing = 2 * 24 * 1024;  // two stages of form_z<2>, the largest
 static_assert(kWaves * kWaveLds <= kRing, "the waves' pieces lie over the stages");
 
 // ROOM: the pool's rank rounded up to 16, 64 or 256 (what a slot of a larger rank
-// needs costs the others registers; at 16 two workgroups fit a CU).
-template <int ROOM>
+// needs costs the others registers; at 16 two workgroups fit a CU).  ONCE: much of
+// U, rank 16 (whole lines a load), is read past the caches, for slots with hardly more
+// than one tile (64 tokens of 57 adapters through 31B gate|up 28.6 -> 26.8 us, 400 of
+// them 52.5 -> 48; but 3200 tokens of 4 through 4096 x 4096 17.8 -> 22.7, 400 of 64 at
+// rank 64 34 -> 38).
+template <int ROOM, bool ONCE>
 __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(AdapterArgs a) {
   __shared__ int tok[kTileM];
   __shared__ __align__(16) uint8_t lds[kRing];
@@ -497,17 +501,17 @@ __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(Adapt
     }
   };
   if (t.slot < 0)
-    RowWalk<1, 0>(a, t, c, tok, zs, lds).copy(first);
+    RowWalk<1, 0, ONCE>(a, t, c, tok, zs, lds).copy(first);
   else if (ROOM == 16 || t.rank16 <= 16)
-    RowWalk<1, 0>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<1, 0, ONCE>(a, t, c, tok, zs, lds).run(first, form);
   else if (t.rank16 <= 32)
-    RowWalk<1, 1>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<1, 1, ONCE>(a, t, c, tok, zs, lds).run(first, form);
   else if (ROOM == 64 || t.rank16 <= 64)
-    RowWalk<1, 2>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<1, 2, ONCE>(a, t, c, tok, zs, lds).run(first, form);
   else if (t.rank16 <= 128)
-    RowWalk<2, 2>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<2, 2, ONCE>(a, t, c, tok, zs, lds).run(first, form);
   else
-    RowWalk<4, 2>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<4, 2, ONCE>(a, t, c, tok, zs, lds).run(first, form);
 }
 
 // ---- many tokens -------------------------------------------------------------------
@@ -580,7 +584,7 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
 #pragma unroll
     for (int i = 0; i < FRAGS; ++i)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) b[i][q] = ld16_any(a.base + at[i][q]);
+      for (int q = 0; q < 2; ++q) b[i][q] = PIECES ? ld16_any_once(a.base + at[i][q]) : ld16_any(a.base + at[i][q]);  // (31B o 59 -> 57 us)
   } else {
 #pragma unroll
     for (int i = 0; i < FRAGS; ++i)
@@ -830,12 +834,15 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
   if (q.few) {
     const dim3 grid(q.tiles, q.blocks);
     const size_t lds = sizeof(uint16_t) * 2 * kTileM * z_pitch(p.r);
-    if (p.r == 16)
-      few_kernel<16><<<grid, kThreads, lds, stream>>>(a);
+    const bool once = p.r == 16 && T <= kTileM * p.n && static_cast<int64_t>(std::min(p.n, T)) * p.Ntot * 32 >= 32 << 20;
+    if (once)
+      few_kernel<16, true><<<grid, kThreads, lds, stream>>>(a);
+    else if (p.r == 16)
+      few_kernel<16, false><<<grid, kThreads, lds, stream>>>(a);
     else if (p.r <= 64)
-      few_kernel<64><<<grid, kThreads, lds, stream>>>(a);
+      few_kernel<64, false><<<grid, kThreads, lds, stream>>>(a);
     else
-      few_kernel<256><<<grid, kThreads, lds, stream>>>(a);
+      few_kernel<256, false><<<grid, kThreads, lds, stream>>>(a);
     return hipGetLastError();
   }
   hipError_t e = hipSuccess;

@@ -21,8 +21,8 @@
 //
 // Bound by memory: dy is read twice, for g and for dU, and everything else once.  As
 // in the forward pass no load of a loop is conditional.  4096 tokens of 16 adapters
-// through 31B gate|up, rank 32: 7 + 96 + 6 + 106 + 4 us; project_kernel reads 418 MB (4.4
-// TB/s, its last workgroups alone), gradient_kernel moves 560 MB (5.3 TB/s).  2048 tokens
+// through 31B gate|up, rank 32: 7 + 96 + 6 + 98 + 4 us; project_kernel reads 418 MB (4.4
+// TB/s), gradient_kernel moves 560 MB (5.7 TB/s).  2048 tokens
 // through 1B q|k|v: 6.3 + 9 + 11.  One pass over dy would hold dU of 64 columns and all
 // ranks in a wave and write g of each 512 columns, 176 MB for the 352 it saves; not built.
 #include <type_traits>
@@ -272,8 +272,9 @@ struct Segment {
 };
 
 // The sum over a slot's tokens for 64 columns of dy (dU) or of X (VGRAD: dV), by 16 JF
-// ranks: 32 positions a step.  FULL: 64 columns exist.
-template <int JF, bool VGRAD, bool FEW, bool FULL>
+// ranks: 32 positions a step.  FULL: 64 columns exist.  ONCE: dy, too large to be found
+// in a cache, is read past it (31B gate|up 107 -> 99 us).
+template <int JF, bool VGRAD, bool FEW, bool FULL, bool ONCE>
 __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg, int c, int j0, int col0, int cols, uint8_t *piece,
                                            f32x4 (&acc)[4][JF]) {
   const int lane = threadIdx.x & 63, r16 = lane & 15, count = seg.count, from = seg.from, stride = seg.stride, steps = seg.end;
@@ -323,7 +324,7 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
         o.s[q] = a.x.scales[static_cast<int64_t>(kk / kCodeBlock) * a.x.ldsc + row];
       } else {
         const uint16_t *p = a.dy + row * a.Ntot + a.n0[c] + col;
-        o.w[q] = FULL ? ld16_any(p) : load_some(p, cols - col);
+        o.w[q] = !FULL ? load_some(p, cols - col) : ONCE ? ld16_any_once(p) : ld16_any(p);
       }
     }
     const uint16_t *p = thin + static_cast<int64_t>(rw.half) * RT * 1024;
@@ -460,9 +461,9 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
     for (int f = 0; f < JF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint8_t *const piece = lds + wave * kPiece;
   if (col0 + 64 <= cols)
-    sum_tokens<JF, VGRAD, FEW, true>(a, seg, c, j0, col0, cols, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, true, WAYS == 1>(a, seg, c, j0, col0, cols, piece, acc);
   else
-    sum_tokens<JF, VGRAD, FEW, false>(a, seg, c, j0, col0, cols, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, false, WAYS == 1>(a, seg, c, j0, col0, cols, piece, acc);
   const int rank = slot_rank(a.s.rank, r, slot);
   // a pair of column tiles of rank tile f: the cut's sums for join_kernel, or the gradient
   f32x4 *const parts = a.parts + (static_cast<int64_t>(place) * a.units + unit) * 4 * JF * 64 + lane;

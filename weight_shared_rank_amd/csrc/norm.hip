@@ -13,9 +13,10 @@
 // waves share a row (rows of up to 32768 elements); a coded block of 128 is 16
 // neighbouring lanes, so its maximum is four lane exchanges and the bf16 output
 // is coded without being read again.
-// Measured: 8192 x 5376 with residual, h, y and code 76.5 us (5.2 TB/s, a copy's rate);
-// its backward pass 69 (5.1 TB/s) and 5.5 for the sum of dw; 1 x 1152 2.8 us, a launch;
-// the backward pass of 333 x 1160 4.0.
+// Measured: 8192 x 5376 with residual, h, y and code 76 us (5.2 TB/s, a copy's rate), or
+// 66 where the outputs' memory was written by the call before; its backward pass 60 (5.9
+// TB/s) and 5.5 for the sum of dw; 1 x 1152 2.8 us, a launch; the backward pass of
+// 333 x 1160 4.0.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,6 +33,12 @@ constexpr int kRowsOneWave = 4;  // rows of a workgroup where a wave takes a row
 
 __device__ __forceinline__ float lo_f32(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// ONCE: past the caches (kLastCache).
+template <bool ONCE>
+__device__ __forceinline__ u32x4 ld_row(const uint16_t *p) {
+  return ONCE ? ld16_once(p) : ld16(p);
+}
 
 // 8 elements of the weight from k on, plus the offset.
 template <bool F32>
@@ -74,7 +81,7 @@ __device__ __forceinline__ F row_sum(F v, F *lds, int wave) {
 // pair of floats: y's only rounding of note is the one to bf16, so the codes
 // that depend on it hardly ever differ from those of exact arithmetic.  It costs
 // two 64-bit operations an element where memory takes the time of thirty.
-template <int W, int V, bool F32>
+template <int W, int V, bool F32, bool ONCE>
 __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kernel(NormCall c) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = W == 1 ? static_cast<int64_t>(blockIdx.x) * kRowsOneWave + wave : blockIdx.x;
@@ -87,7 +94,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
   for (int i = 0; i < V; ++i) {
     const int k = at + i * W * 512;
     h[i] = u32x4{0u, 0u, 0u, 0u};
-    if (k < c.K) h[i] = ld16(c.x + row + k);
+    if (k < c.K) h[i] = ld_row<ONCE>(c.x + row + k);
   }
   float w[8];  // (one vector a lane: under way with the row)
   if (V == 1 && at < c.K) load_weight<F32>(c.w, at, w);
@@ -97,7 +104,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
     for (int i = 0; i < V; ++i) {
       const int k = at + i * W * 512;
       r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (k < c.K) r[i] = ld16(c.res + row + k);
+      if (k < c.K) r[i] = ld_row<ONCE>(c.res + row + k);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -226,7 +233,7 @@ __device__ __forceinline__ void dw_columns(const NormBackward &c, int unit) {
 // `part` (dw itself if there is one workgroup).  With few rows dw has workgroups of
 // its own, 64 columns each, behind the `groups` of the rows: they read the rows again,
 // from the caches, and no second launch is needed.
-template <int W, int V, bool F32>
+template <int W, int V, bool F32, bool ONCE>
 __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_backward_kernel(NormBackward c, float *part, int groups) {
   if (static_cast<int>(blockIdx.x) >= groups) return dw_columns<W == 1 ? kRowsOneWave : W>(c, blockIdx.x - groups);
   constexpr int R = W == 1 ? kRowsOneWave : 1;
@@ -259,9 +266,9 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
       const int k = at + i * W * 512;
       d[i] = h[i] = r[i] = u32x4{0u, 0u, 0u, 0u};
       if (k < c.K) {
-        d[i] = ld16(c.dy + row + k);
-        h[i] = ld16(c.h + row + k);
-        if (c.dh && !IN_LDS) r[i] = ld16(c.dh + row + k);
+        d[i] = ld_row<ONCE>(c.dy + row + k);
+        h[i] = ld_row<ONCE>(c.h + row + k);
+        if (c.dh && !IN_LDS) r[i] = ld_row<ONCE>(c.dh + row + k);
       }
     }
     const float a = c.rstd[t];
@@ -291,7 +298,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
       if (k >= c.K) continue;
       float(&wi)[8] = w[KEPT ? i : 0];
       if (!KEPT) load_weight<F32>(c.w, k, wi);
-      if (c.dh && IN_LDS) r[i] = ld16(c.dh + row + k);
+      if (c.dh && IN_LDS) r[i] = ld_row<ONCE>(c.dh + row + k);
       u32x4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -403,18 +410,34 @@ int backward_groups(int T, int K) {
 constexpr int kOneLaunchRows = 1024;
 bool one_backward_launch(int T, int K) { return T > rows_of_workgroup(K) && T <= kOneLaunchRows; }
 
+// Calls that move more than the last cache holds load past it, so that it keeps what
+// they write (8192 x 5376 backward 69 -> 60 us; forward 77 -> 76, and 78 -> 66 where the
+// outputs' memory is used again; stores past it too: 70); the inputs of smaller calls
+// often lie in it (backward of 800 x 5376, so loaded: 13 -> 15 us).
+constexpr int64_t kLastCache = int64_t{256} << 20;
+
+// f(F32, ONCE); the shapes for few rows have no ONCE.
+template <int W, int V, typename F>
+hipError_t with_loads(bool f32, bool once, F &&f) {
+  constexpr bool kCan = W < 8 || V > 1;
+  const auto with = [&](auto o) { return f32 ? f(std::true_type{}, o) : f(std::false_type{}, o); };
+  if (kCan && once) return with(std::integral_constant<bool, kCan>{});
+  return with(std::false_type{});
+}
+
 }  // namespace
 
 hipError_t launch_norm(const NormCall &c, hipStream_t stream) {
+  const int rows = 1 + (c.res != nullptr) + (c.h != nullptr) + (c.y != nullptr);
+  const bool once = static_cast<int64_t>(c.T) * c.K * (2 * rows + c.coded) > kLastCache;
   return with_row_shape(c.T, c.K, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     const int R = rows_of_workgroup(c.K);
     const dim3 grid((c.T + R - 1) / R), block(R * W * 64);
-    if (c.w.f32)
-      norm_kernel<W, V, true><<<grid, block, 0, stream>>>(c);
-    else
-      norm_kernel<W, V, false><<<grid, block, 0, stream>>>(c);
-    return hipGetLastError();
+    return with_loads<W, V>(c.w.f32, once, [&](auto f32, auto o) {
+      norm_kernel<W, V, decltype(f32)::value, decltype(o)::value><<<grid, block, 0, stream>>>(c);
+      return hipGetLastError();
+    });
   });
 }
 
@@ -440,20 +463,21 @@ hipError_t launch_norm_backward(const NormBackward &c, float *partials, hipStrea
     part.dw = nullptr;
     return launch_norm_backward(part, partials, stream);
   }
+  const bool once = static_cast<int64_t>(c.T) * c.K * 2 * (2 + (c.dh != nullptr) + (c.dx != nullptr)) > kLastCache;
   const int rows = one && !c.dx ? 0 : G, blocks = rows + (one && c.dw ? (c.K + 63) / 64 : 0);
   const hipError_t e = with_row_shape(c.T, c.K, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     const dim3 block(rows_of_workgroup(c.K) * W * 64);
     constexpr size_t lds = in_lds<W, V>() ? sizeof(float) * W * V * 512 : 0;
-    if constexpr (lds > 0) {
-      const hipError_t e = c.w.f32 ? ensure_lds<norm_backward_kernel<W, V, true>>(lds) : ensure_lds<norm_backward_kernel<W, V, false>>(lds);
-      if (e != hipSuccess) return e;
-    }
-    if (c.w.f32)
-      norm_backward_kernel<W, V, true><<<blocks, block, lds, stream>>>(c, partials, rows);
-    else
-      norm_backward_kernel<W, V, false><<<blocks, block, lds, stream>>>(c, partials, rows);
-    return hipGetLastError();
+    return with_loads<W, V>(c.w.f32, once, [&](auto f32, auto o) {
+      constexpr auto kernel = norm_backward_kernel<W, V, decltype(f32)::value, decltype(o)::value>;
+      if constexpr (lds > 0) {
+        const hipError_t e = ensure_lds<kernel>(lds);
+        if (e != hipSuccess) return e;
+      }
+      kernel<<<blocks, block, lds, stream>>>(c, partials, rows);
+      return hipGetLastError();
+    });
   });
   if (e != hipSuccess || !c.dw || G == 1 || one) return e;
   norm_dw_kernel<<<(c.K + 15) / 16, 256, 0, stream>>>(partials, G, c.K, c.dw);
