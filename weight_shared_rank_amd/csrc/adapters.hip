@@ -19,7 +19,7 @@
 // products with U and base (expand_kernel), in tiles of 64 tokens; between them, where
 // many workgroups would add up the same slices, finish_kernel.
 //
-// Measured: 1 token through 1B q|k|v 5.2 us, of which a launch is most; 64 tokens of 57
+// Measured: 1 token through 1B q|k|v 5.5 us, of which a launch is most; 64 tokens of 57
 // adapters through 31B gate|up 26.5 (103 MB read, 114 moved); 4096 tokens of 12 through 31B
 // o at rank 64 6.9 + 19 + 5 + 26 (thin_kernel 80 MB at 4.2 TB/s, expand_kernel 100 at 3.9).
 //
