@@ -511,7 +511,7 @@ size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t 
  *    aligned, no initialization, nothing kept; concurrent calls, and graphs that
  *    may run at the same time, need distinct workspaces.
  *  Products of bf16 operands with float32 sums; c (V^T x) enters the second one
- *  as a pair of bf16 (16 significant bits); y is rounded once.  A token's result
+ *  in three parts of bf16, all 24 bits of its float32; y is rounded once.  A token's result
  *  does not depend on what the other tokens hold (the order of its own sums can
  *  depend on T and on its place among the tokens of its slot).
  *  What is not finite in a slot or a token's x reaches that slot's or that token's
@@ -527,8 +527,8 @@ wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, 
  *   dU_a = sum of dy[t] z^T,  dV_a^T = sum of g X[t]^T   over the slot's tokens
  * Tokens without an adapter leave dx[t] = base[t], bit for bit, and enter nothing
  * else; a slot without tokens has zero gradients, and so have the rows and
- * columns from a slot's rank on.  Sums in float32, z and g as pairs of bf16 (16
- * significant bits) where they enter the second products; every output is rounded
+ * columns from a slot's rank on.  Sums in float32, z and g in three parts of bf16 (all
+ * 24 bits of a float32) where they enter the second products; every output is rounded
  * once.  The sums over tokens have a fixed order: the same bits from run to run,
  * whichever gradients are asked for.  What is not finite in a token
  * reaches its own dx and its slot's dU and dV alone. */

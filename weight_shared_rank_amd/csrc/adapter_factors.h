@@ -29,13 +29,13 @@ __device__ __forceinline__ u32x4 expand_codes(u32x2 v, uint8_t scale) {
   return o;
 }
 
-// z and g summed over their slices, times c, as pairs of bf16 in the operands' order.
+// z and g summed over their slices, times c, in parts of bf16 in the operands' order.
 // A piece is 64 lanes of 8 values:
 //   transposed (for dU and dV): lane (r16, g) has rank 16 jt + r16 of positions
-//     32 s + 8 g .. + 7 of the place: piece ((place * 2 + s) * RT + jt) * 2 + p
+//     32 s + 8 g .. + 7 of the place: piece ((place * 2 + s) * RT + jt) * kParts + p
 //   rows (for y and dx): lane (r16, g) has position 16 i + r16, ranks 32 ch + 8 g .. + 7 of
-//     a child: piece ((place * 4 + i) * nchild * RC + child * RC + ch) * 2 + p
-// with RT = R / 16, RC = r / 32 rounded up, p 0 the value and 1 what its rounding left.
+//     a child: piece ((place * 4 + i) * nchild * RC + child * RC + ch) * kParts + p
+// with RT = R / 16, RC = r / 32 rounded up, p the part.
 // Ranks past the slot's and positions behind the tile's tokens are zeros.
 struct Factors {
   const float *scale;
@@ -44,13 +44,15 @@ struct Factors {
   int32_t RT, nchild, RC;
 };
 
-// A lane's 8 values of a piece, and what is left of them in the next.
+constexpr int kPieces = kParts * 512;  // elements of the pieces of a float's parts
+
+// A lane's 8 values, their parts to as many pieces.
 __device__ __forceinline__ void store_piece(uint16_t *to, int lane, const float (&v)[8]) {
-  u32x2 hi[2], lo[2];
+  u32x2 o[2][kParts];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) split4(f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}, hi[h], lo[h]);
-  *reinterpret_cast<u32x4 *>(to + lane * 8) = u32x4{hi[0][0], hi[0][1], hi[1][0], hi[1][1]};
-  *reinterpret_cast<u32x4 *>(to + 512 + lane * 8) = u32x4{lo[0][0], lo[0][1], lo[1][0], lo[1][1]};
+  for (int h = 0; h < 2; ++h) split4(f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}, o[h]);
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x4 *>(to + p * 512 + lane * 8) = u32x4{o[0][p][0], o[0][p][1], o[1][p][0], o[1][p][1]};
 }
 
 // sum: [kM][pitch] floats of a place, column tile f of them is rank tile jt (of a
@@ -63,11 +65,11 @@ __device__ __forceinline__ void store_factors(const Factors &o, int which, int p
   if (o.T[which]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = sum[(32 * s + 8 * g + k) * pitch + 16 * f + r16];
-    store_piece(o.T[which] + ((static_cast<int64_t>(place0) * 2 + s) * o.RT + col / 16) * 1024, lane, v);
+    store_piece(o.T[which] + ((static_cast<int64_t>(place0) * 2 + s) * o.RT + col / 16) * kPieces, lane, v);
   }
   if (o.rows[which]) {
     const int i = 2 * s + (g >> 1), child = (col / 16 - jt) / (o.RT / o.nchild), to = r16 + 16 * (2 * (jt & 1) + (g & 1));
-    uint16_t *piece = o.rows[which] + ((static_cast<int64_t>(place0) * 4 + i) * o.nchild * o.RC + child * o.RC + jt / 2) * 1024;
+    uint16_t *piece = o.rows[which] + ((static_cast<int64_t>(place0) * 4 + i) * o.nchild * o.RC + child * o.RC + jt / 2) * kPieces;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = sum[(16 * i + r16) * pitch + 16 * f + 8 * (g & 1) + k];
     store_piece(piece, to, v);

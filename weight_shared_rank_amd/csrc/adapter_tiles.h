@@ -369,20 +369,30 @@ hipError_t launch_group(const GroupArgs &g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Four floats as pairs of bf16: hi their values, lo what that rounding left (0 where
-// hi is not finite).
-__device__ __forceinline__ void split4(f32x4 v, u32x2 &hi, u32x2 &lo) {
-  float d[4];
+// z and g enter the second products as kParts bf16 each: what the first leaves of the
+// float goes to the next, and three of 8 significant bits hold all 24 (each is cut off, not
+// rounded, so nothing is left over; an infinity or NaN is the first part alone).
+constexpr int kParts = 3;
+__device__ __forceinline__ void split4(f32x4 v, u32x2 (&o)[kParts]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t h = pack_bf16(v[2 * i], v[2 * i + 1]);
-    hi[i] = h;
-    d[2 * i] = v[2 * i] - __uint_as_float(h << 16);
-    d[2 * i + 1] = v[2 * i + 1] - __uint_as_float(h & 0xffff0000u);
+  for (int p = 0; p < kParts; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = __float_as_uint(v[i]) & 0xffff0000u;
+      const float d = v[i] - __uint_as_float(w[i]);
+      v[i] = fabsf(d) < __builtin_inff() ? d : 0.f;
+    }
+    o[p] = u32x2{w[0] >> 16 | w[1], w[2] >> 16 | w[3]};
   }
+}
+
+// The parts of four floats to `to`, `next` elements apart.
+__device__ __forceinline__ void store_parts(f32x4 v, uint16_t *to, int next) {
+  u32x2 o[kParts];
+  split4(v, o);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = fabsf(d[i]) < __builtin_inff() ? d[i] : 0.f;
-  lo = u32x2{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
+  for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x2 *>(to + p * next) = o[p];
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t{255}; }

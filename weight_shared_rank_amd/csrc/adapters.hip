@@ -6,8 +6,8 @@
 // have their own U and V over one x.  Tokens without an adapter keep base.
 //
 // Tokens are taken in tiles that share a slot: the columns of matrix products whose
-// rows are V^T's and U's.  c z enters the second product as a pair of bf16 (the
-// value and what its rounding left, 16 significant bits); y is rounded once.
+// rows are V^T's and U's.  c z enters the second product in three parts of bf16, which
+// hold all of its float32; y is rounded once.
 //
 // Few tokens: nothing is prepared and there is one launch, few_kernel.  Workgroup t
 // looks through the whole index and works if token t is the first, the 17th, ... of its
@@ -64,7 +64,7 @@ struct AdapterArgs {
 // banks.
 __host__ __device__ constexpr int z_pitch(int r) { return (r <= 32 ? 32 : r <= 64 ? 64 : r <= 128 ? 128 : 256) + 8; }
 
-// c z of NF row tiles of V^T (from row j0 of the slot's child on) to zs [2][16][pitch].
+// c z of NF row tiles of V^T (from row j0 of the slot's child on) to zs [kParts][16][pitch].
 // A stage is KS values of k: rows of 64 k (128 bytes), chunk c of row t in slot
 // c ^ t % 8, so that fragment reads touch every bank.  It waits in registers while
 // the kDeep - 1 before it are used.  A wave multiplies two row tiles (one where there
@@ -186,7 +186,7 @@ __device__ __forceinline__ void form_z(const AdapterArgs &a, const Tile &t, cons
       f32x4 v;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? sum[k] * scale : 0.f;
-      split4(v, *reinterpret_cast<u32x2 *>(zs + r16 * pitch + j), *reinterpret_cast<u32x2 *>(zs + (kTileM + r16) * pitch + j));
+      store_parts(v, zs + r16 * pitch + j, kTileM * pitch);
     }
   }
   __syncthreads();
@@ -283,7 +283,7 @@ __device__ __forceinline__ void dot_z(const AdapterArgs &a, const Tile &t, const
       for (int k = 0; k < 4; ++k) v[k] += sums[((q * groups + j / ROWS) * ROWS + j % ROWS + k) * NT + m];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? v[k] * scale : 0.f;
-    split4(v, *reinterpret_cast<u32x2 *>(zs + m * pitch + j), *reinterpret_cast<u32x2 *>(zs + (kTileM + m) * pitch + j));
+    store_parts(v, zs + m * pitch + j, kTileM * pitch);
   }
   __syncthreads();
 }
@@ -395,13 +395,13 @@ struct RowWalk {
           if (unit == 0) load_base<FULL>(next, bn);
         }
         const bool in = CW || g < 2;  // (16 ranks: the other half of the contraction is zeros)
-        u32x4 uv[4], zv[2];
+        u32x4 uv[4], zv[kParts];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) zv[p] = in ? ld16(zs + (p * kTileM + r16) * pitch + k0 + 8 * g) : zero;
+        for (int p = 0; p < kParts; ++p) zv[p] = in ? ld16(zs + (p * kTileM + r16) * pitch + k0 + 8 * g) : zero;
 #pragma unroll
         for (int j = 0; j < 4; ++j) uv[j] = in ? *reinterpret_cast<const u32x4 *>(mine + (16 * j + r16) * kUPitch + 16 * g) : zero;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < kParts; ++p)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = mfma16x16x32(uv[j], zv[p], acc[j]);
       }
@@ -472,13 +472,13 @@ template <int ROOM, bool ONCE>
 __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(AdapterArgs a) {
   __shared__ int tok[kTileM];
   __shared__ __align__(16) uint8_t lds[kRing];
-  extern __shared__ __align__(16) uint16_t zs[];  // [2][kTileM][pitch]
+  extern __shared__ __align__(16) uint16_t zs[];  // [kParts][kTileM][pitch]
   Tile t;
   if (!get_tile<kTileM, kThreads>(a.s, blockIdx.x, t, tok)) return;
   const int c = child_of(a), first = (static_cast<int>(blockIdx.y) - a.block0[c]) * a.turns * kThreads;
   const auto form = [&] {
     // c z all zeros, which ranks past the slot's stay (barriers stand between this and the stores of z)
-    for (int i = threadIdx.x; i < 2 * kTileM * z_pitch(a.s.r) / 8; i += kThreads) reinterpret_cast<u32x4 *>(zs)[i] = u32x4{0u, 0u, 0u, 0u};
+    for (int i = threadIdx.x; i < kParts * kTileM * z_pitch(a.s.r) / 8; i += kThreads) reinterpret_cast<u32x4 *>(zs)[i] = u32x4{0u, 0u, 0u, 0u};
     if (t.count == 1) {
       if (ROOM == 16 || t.rank16 == 16)
         dot_z<2, 1>(a, t, tok, c, lds, zs);
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
   constexpr int MW = 16 * FRAGS;
   __shared__ int tok[kM];
   __shared__ __align__(16) uint8_t lds[kExpandWaves * kWaveLds];
-  extern __shared__ __align__(16) uint16_t zs[];  // without pieces: [2][MW][pitch]
+  extern __shared__ __align__(16) uint16_t zs[];  // without pieces: [kParts][MW][pitch]
   Tile t;
   const int m0 = blockIdx.z * MW;
   if (!get_tile<kM>(a.s, blockIdx.x, t, tok) || m0 >= t.count) return;
@@ -563,11 +563,11 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
 #pragma unroll
     for (int q = 0; q < 4; ++q) un[q] = ld16_at(urows, uoff[q] + kb);
   };
-  const uint16_t *z0 = a.z + ((static_cast<int64_t>(blockIdx.x) * 4 + m0 / 16) * a.nchild + c) * a.RC * 1024;
-  u32x4 zn[2];
+  const uint16_t *z0 = a.z + ((static_cast<int64_t>(blockIdx.x) * 4 + m0 / 16) * a.nchild + c) * a.RC * kPieces;
+  u32x4 zn[kParts];
   auto load_z = [&](int i, int chunk) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) zn[p] = ld16_at(z0 + ((i * a.nchild * a.RC + chunk) * 2 + p) * 512, lane * 16u);
+    for (int p = 0; p < kParts; ++p) zn[p] = ld16_at(z0 + ((i * a.nchild * a.RC + chunk) * kParts + p) * 512, lane * 16u);
   };
   u32x4 b[FRAGS][2];
   int64_t at[FRAGS][2];
@@ -608,7 +608,7 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = j + k < t.rank ? v[k] * scale : 0.f;
-        split4(v, *reinterpret_cast<u32x2 *>(zs + m * pitch + j), *reinterpret_cast<u32x2 *>(zs + (MW + m) * pitch + j));
+        store_parts(v, zs + m * pitch + j, MW * pitch);
       }
     }
 #pragma unroll
@@ -634,20 +634,20 @@ __global__ __launch_bounds__(kExpandWaves * 64) void expand_kernel(AdapterArgs a
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         if (ch >= chunks) break;
-        u32x4 z[2];
+        u32x4 z[kParts];
         if constexpr (PIECES) {
-          z[0] = zn[0];
-          z[1] = zn[1];
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) z[p] = zn[p];
           if (ch + 1 < CH && ch + 1 < chunks)
             load_z(i, ch + 1);
           else
             load_z(min(i + 1, FRAGS - 1), 0);
         } else {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) z[p] = ld16(zs + (p * MW + 16 * i + r16) * pitch + 32 * ch + 8 * g);
+          for (int p = 0; p < kParts; ++p) z[p] = ld16(zs + (p * MW + 16 * i + r16) * pitch + 32 * ch + 8 * g);
         }
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < kParts; ++p)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = mfma16x16x32(u[ch][j], z[p], acc[j]);
       }
@@ -764,14 +764,14 @@ Plan make_plan(const AdapterPool &p, int T) {
   q.rows = static_cast<int64_t>(q.tiles) * kM;
   q.perm_at = align256(sizeof(int4) * q.tiles);  // the tiles come first
   q.z_at = q.perm_at + align256(sizeof(int32_t) * q.rows);
-  q.p_at = q.z_at + (q.pieces ? align256(2 * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32) : 0);
+  q.p_at = q.z_at + (q.pieces ? align256(kParts * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32) : 0);
   q.bytes = q.p_at + align256(sizeof(float) * q.slices * q.rows * p.nchild * p.r);
   return q;
 }
 
 template <int CH, int FRAGS, bool PIECES>
 hipError_t launch_expand(const AdapterArgs &a, const Plan &q, hipStream_t stream) {
-  constexpr size_t lds = PIECES ? 0 : sizeof(uint16_t) * 2 * 16 * FRAGS * z_pitch(32 * CH);
+  constexpr size_t lds = PIECES ? 0 : sizeof(uint16_t) * kParts * 16 * FRAGS * z_pitch(32 * CH);
   const hipError_t e = ensure_lds<expand_kernel<CH, FRAGS, PIECES>>(lds);
   if (e != hipSuccess) return e;
   expand_kernel<CH, FRAGS, PIECES><<<dim3(q.tiles, q.blocks, 4 / FRAGS), kExpandWaves * 64, lds, stream>>>(a);
@@ -833,7 +833,7 @@ hipError_t launch_adapters(const AdapterPool &p, const uint16_t *x, const int32_
   }
   if (q.few) {
     const dim3 grid(q.tiles, q.blocks);
-    const size_t lds = sizeof(uint16_t) * 2 * kTileM * z_pitch(p.r);
+    const size_t lds = sizeof(uint16_t) * kParts * kTileM * z_pitch(p.r);
     const bool once = p.r == 16 && T <= kTileM * p.n && static_cast<int64_t>(std::min(p.n, T)) * p.Ntot * 32 >= 32 << 20;
     if (once)
       few_kernel<16, true><<<grid, kThreads, lds, stream>>>(a);

@@ -5,8 +5,8 @@
 //   dx = base + V g,   dU_a = sum over the slot's tokens dy z^T,   dV_a^T = sum g X^T
 // Launches, in tiles of 64 tokens: the grouping (not with few tokens); project_kernel, z
 // and g, in float32 slices of the contraction where it is long; finish_kernel, their sums
-// (with one slice of both, project_kernel's own end) as pairs of bf16 (the value and what
-// its rounding left), each 16 x 32 piece of them stored as the 64 lanes' operand of a
+// (with one slice of both, project_kernel's own end) in three parts of bf16, which
+// hold all of a float32, each 16 x 32 piece of them stored as the 64 lanes' operand of a
 // matrix instruction, so that the products load it as 1 KB; gradient_kernel, dx, dU and
 // dV; with many tokens join_kernel, for slots whose tokens were cut for dU and dV.
 //
@@ -212,9 +212,9 @@ __device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *
       for (int i = 0; i < 2; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int chunks = (t.rank16 + 31) / 32, steps = a.nchild * chunks;
     const uint16_t *v0 = a.vt + static_cast<int64_t>(t.slot) * a.R * K;
-    const uint16_t *g0 = a.grows + (static_cast<int64_t>(place0) * 4 + m0 / 16) * a.nchild * a.RC * 1024;
+    const uint16_t *g0 = a.grows + (static_cast<int64_t>(place0) * 4 + m0 / 16) * a.nchild * a.RC * kPieces;
     const uint32_t col = (in ? k0 + ocol : 0) * 2u;
-    u32x4 vv[4], gv[2][2];
+    u32x4 vv[4], gv[2][kParts];
     auto load = [&](int step) {
       const int ch = step % chunks, c = step / chunks;
 #pragma unroll
@@ -223,7 +223,7 @@ __device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) gv[i][p] = ld16_at(g0 + ((i * a.nchild * a.RC + c * a.RC + ch) * 2 + p) * 512, lane * 16u);
+        for (int p = 0; p < kParts; ++p) gv[i][p] = ld16_at(g0 + ((i * a.nchild * a.RC + c * a.RC + ch) * kParts + p) * 512, lane * 16u);
     };
     load(0);
     for (int step = 0; step < steps; ++step) {
@@ -231,11 +231,11 @@ __device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *reinterpret_cast<u32x4 *>(piece + place(q * 8 + orow) * kPitch + (lane & 7) * 16) = in && q * 8 + orow < left ? vv[q] : zero;
-      u32x4 gg[2][2];
+      u32x4 gg[2][kParts];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) gg[i][p] = gv[i][p];
+        for (int p = 0; p < kParts; ++p) gg[i][p] = gv[i][p];
       load(min(step + 1, steps - 1));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -243,7 +243,7 @@ __device__ __forceinline__ void dx_unit(const GradArgs &a, int64_t id, uint8_t *
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) acc[j][i] = mfma16x16x32(v, gg[i][p], acc[j][i]);
+          for (int p = 0; p < kParts; ++p) acc[j][i] = mfma16x16x32(v, gg[i][p], acc[j][i]);
       }
     }
 #pragma unroll
@@ -281,7 +281,7 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
   const int RT = a.R / 16, col = col0 + (lane & 7) * 8;
   const u32x4 zero{0u, 0u, 0u, 0u};
   // the thin operand's pieces, from column tile (c r + j0) / 16 of z or g on
-  const uint16_t *thin = (VGRAD ? a.gT : a.zT) + static_cast<int64_t>((c * a.s.r + j0) / 16) * 1024;
+  const uint16_t *thin = (VGRAD ? a.gT : a.zT) + static_cast<int64_t>((c * a.s.r + j0) / 16) * kPieces;
   struct Rows {  // a step's place (halves of tiles), and the tokens of this lane's rows 8 q + lane / 8
     int half, token[4];
   };
@@ -309,7 +309,7 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
     u32x4 w[VGRAD ? 1 : 4];
     u32x2 x[VGRAD ? 4 : 1];
     uint8_t s[VGRAD ? 4 : 1];
-    u32x4 t[JF][2];
+    u32x4 t[JF][kParts];
     uint32_t in;  // bits: the rows that are tokens
   };
   auto load = [&](const Rows &rw, Loaded &o) {
@@ -327,12 +327,12 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
         o.w[q] = !FULL ? load_some(p, cols - col) : ONCE ? ld16_any_once(p) : ld16_any(p);
       }
     }
-    const uint16_t *p = thin + static_cast<int64_t>(rw.half) * RT * 1024;
+    const uint16_t *p = thin + static_cast<int64_t>(rw.half) * RT * kPieces;
 #pragma unroll
     for (int f = 0; f < JF; ++f) {
       const int ff = j0 + 16 * f < a.s.r ? f : 0;  // (not stored)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) o.t[f][q] = ld16_at(p + ff * 1024 + q * 512, lane * 16u);
+      for (int q = 0; q < kParts; ++q) o.t[f][q] = ld16_at(p + ff * kPieces + q * 512, lane * 16u);
     }
   };
   auto put = [&](const Loaded &o) {
@@ -355,11 +355,11 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
   rows(from + stride, next);
   for (int step = from; step < steps; step += stride) {
     put(l);
-    u32x4 t[JF][2];
+    u32x4 t[JF][kParts];
 #pragma unroll
     for (int f = 0; f < JF; ++f)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) t[f][q] = l.t[f][q];
+      for (int q = 0; q < kParts; ++q) t[f][q] = l.t[f][q];
     load(next, l);
     rows(step + 2 * stride, next);
 #pragma unroll
@@ -369,7 +369,7 @@ __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg
 #pragma unroll
       for (int f = 0; f < JF; ++f)
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < kParts; ++q)
           acc[i][f] = VGRAD ? mfma16x16x32(w, t[f][q], acc[i][f]) : mfma16x16x32(t[f][q], w, acc[i][f]);
     }
   }
@@ -633,9 +633,9 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
   q.joins_at = take(sizeof(int4) * q.places);
   q.pz_at = take(sizeof(float) * q.zslices * q.rows * R);
   q.pg_at = take(sizeof(float) * q.gslices * q.rows * R);
-  q.zt_at = take(2 * sizeof(uint16_t) * q.rows * R);
-  q.gt_at = take(2 * sizeof(uint16_t) * q.rows * R);
-  q.grows_at = take(2 * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32);
+  q.zt_at = take(kParts * sizeof(uint16_t) * q.rows * R);
+  q.gt_at = take(kParts * sizeof(uint16_t) * q.rows * R);
+  q.grows_at = take(kParts * sizeof(uint16_t) * q.rows * p.nchild * q.RC * 32);
   q.parts_at = take(size_t{4096} * q.NF * q.places * q.units);
   q.bytes = at;
   return q;
