@@ -13,9 +13,9 @@
 // waves share a row (rows of up to 32768 elements); a coded block of 128 is 16
 // neighbouring lanes, so its maximum is four lane exchanges and the bf16 output
 // is coded without being read again.
-// Measured: 8192 x 5376 with residual, h, y and code 76 us (5.2 TB/s, a copy's rate), or
-// 66 where the outputs' memory was written by the call before; its backward pass 60 (5.9
-// TB/s) and 5.5 for the sum of dw; 1 x 1152 2.8 us, a launch; the backward pass of
+// Measured: 8192 x 5376 with residual, h, y and code 79 us (5.0 TB/s), or 70
+// where the outputs' memory was written by the call before; its backward pass 60 (5.9
+// TB/s) and 5.5 for the sum of dw; 1 x 1152 2.9 us, a launch; the backward pass of
 // 333 x 1160 4.0.
 #include <algorithm>
 #include <type_traits>
@@ -40,23 +40,23 @@ __device__ __forceinline__ u32x4 ld_row(const uint16_t *p) {
   return ONCE ? ld16_once(p) : ld16(p);
 }
 
-// 8 elements of the weight from k on, plus the offset.
+// 8 elements of the weight from k on, plus `offset`.
 template <bool F32>
-__device__ __forceinline__ void load_weight(const NormWeight &nw, int k, float (&w)[8]) {
+__device__ __forceinline__ void load_weight(const NormWeight &nw, int k, float (&w)[8], float offset) {
   if constexpr (F32) {
     const float *p = static_cast<const float *>(nw.w) + k;
     const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = nw.offset + a[i];
-      w[4 + i] = nw.offset + b[i];
+      w[i] = offset + a[i];
+      w[4 + i] = offset + b[i];
     }
   } else {
     const u32x4 v = ld16(static_cast<const uint16_t *>(nw.w) + k);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[2 * i] = nw.offset + lo_f32(v[i]);
-      w[2 * i + 1] = nw.offset + hi_f32(v[i]);
+      w[2 * i] = offset + lo_f32(v[i]);
+      w[2 * i + 1] = offset + hi_f32(v[i]);
     }
   }
 }
@@ -76,11 +76,36 @@ __device__ __forceinline__ F row_sum(F v, F *lds, int wave) {
   return v;
 }
 
+// Two doubles to bf16 with one rounding: first to float32, an inexact one towards the
+// neighbour whose last bit is odd, which is never halfway between two bf16.
+__device__ __forceinline__ uint32_t pack_bf16_once(double a, double b) {
+  const auto odd = [](double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = static_cast<uint32_t>(u), cut = lo & 0xe0000000u;
+    const uint64_t o = (u & 0xffffffff00000000u) | (lo != cut ? cut | 0x20000000u : cut);
+    return static_cast<float>(__builtin_bit_cast(double, o));
+  };
+  return pack_bf16(odd(a), odd(b));
+}
+
+// y of 8 elements h of a row: h a (offset + w), rounded once, so that y and its codes are
+// those of exact arithmetic.
+__device__ __forceinline__ u32x4 scale_row(u32x4 h, double a, const float (&w)[8], double offset) {
+  u32x4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t v = h[j];
+    asm("" : "+v"(v));  // (converted again here: kept from the sum of squares they take twice the registers)
+    y[j] = pack_bf16_once(lo_f32(v) * a * (offset + w[2 * j]), hi_f32(v) * a * (offset + w[2 * j + 1]));
+  }
+  return y;
+}
+
 // W waves to a row (1: kRowsOneWave rows to a workgroup), V vectors of 8 a lane.
-// The sum of squares and a are taken in 64 bits and a enters the product as a
-// pair of floats: y's only rounding of note is the one to bf16, so the codes
-// that depend on it hardly ever differ from those of exact arithmetic.  It costs
-// two 64-bit operations an element where memory takes the time of thirty.
+// The sum of squares, a and the product are taken in 64 bits: about a dozen such
+// operations an element.  (With the product in float32, rounded a second time, 12 to 26 of
+// the 44 million codes of 8192 x 5376 were others, and 65.6 us instead of 70; only the
+// vectors next to a halfway value in 64 bits: 69.5.)
 template <int W, int V, bool F32, bool ONCE>
 __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kernel(NormCall c) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -97,7 +122,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
     if (k < c.K) h[i] = ld_row<ONCE>(c.x + row + k);
   }
   float w[8];  // (one vector a lane: under way with the row)
-  if (V == 1 && at < c.K) load_weight<F32>(c.w, at, w);
+  if (V == 1 && at < c.K) load_weight<F32>(c.w, at, w, 0.f);
   if (c.res) {
     u32x4 r[V];
 #pragma unroll
@@ -130,8 +155,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
     }
   q = row_sum<W>(q, part, wave);
   const double a = rsqrt(q / c.K + static_cast<double>(c.eps));
-  const float ah = static_cast<float>(a), al = static_cast<float>(a - static_cast<double>(ah));
-  if (c.rstd && at == 0) c.rstd[t] = ah;
+  if (c.rstd && at == 0) c.rstd[t] = static_cast<float>(a);
   if (!c.y && !c.coded) return;
   const int Kq = c.code.nb * kCodeBlock;
 #pragma unroll
@@ -139,17 +163,8 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_kern
     const int k = at + i * W * 512;
     u32x4 y{0u, 0u, 0u, 0u};
     if (k < c.K) {
-      float o[8];
-      if (V > 1) load_weight<F32>(c.w, k, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = j & 1 ? hi_f32(h[i][j / 2]) : lo_f32(h[i][j / 2]);
-        const float p = v * ah, e = __builtin_fmaf(v, al, __builtin_fmaf(v, ah, -p));  // v a = p + e
-        // (an infinite weight times e = 0 would be NaN)
-        o[j] = __builtin_fmaf(p, w[j], e * (fabsf(w[j]) < __builtin_inff() ? w[j] : 0.f));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
+      if (V > 1) load_weight<F32>(c.w, k, w, 0.f);
+      y = scale_row(h[i], a, w, c.w.offset);
       if (c.y) *reinterpret_cast<u32x4 *>(c.y + row + k) = y;
     }
     if (c.coded) {
@@ -253,7 +268,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
     const int k = at + i * W * 512;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[KEPT ? i : 0][j] = dw[IN_LDS ? 0 : i][j] = 0.f;
-    if (KEPT && k < c.K) load_weight<F32>(c.w, k, w[KEPT ? i : 0]);
+    if (KEPT && k < c.K) load_weight<F32>(c.w, k, w[KEPT ? i : 0], c.w.offset);
     if (IN_LDS && k < c.K) store_8(sums + k, dw[0]);
   }
   const int64_t teams = static_cast<int64_t>(groups) * R;
@@ -277,7 +292,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
     for (int i = 0; i < V; ++i) {
       const int k = at + i * W * 512;
       float(&wi)[8] = w[KEPT ? i : 0];
-      if (!KEPT && k < c.K) load_weight<F32>(c.w, k, wi);
+      if (!KEPT && k < c.K) load_weight<F32>(c.w, k, wi, c.w.offset);
       float(&dwi)[8] = dw[IN_LDS ? 0 : i];
       if (IN_LDS && k < c.K) load_8(sums + k, dwi);
 #pragma unroll
@@ -297,7 +312,7 @@ __global__ __launch_bounds__(W == 1 ? kRowsOneWave * 64 : W * 64) void norm_back
       const int k = at + i * W * 512;
       if (k >= c.K) continue;
       float(&wi)[8] = w[KEPT ? i : 0];
-      if (!KEPT) load_weight<F32>(c.w, k, wi);
+      if (!KEPT) load_weight<F32>(c.w, k, wi, c.w.offset);
       if (c.dh && IN_LDS) r[i] = ld_row<ONCE>(c.dh + row + k);
       u32x4 o;
 #pragma unroll
