@@ -645,18 +645,21 @@ wl_status check_adapters(const wl_adapters *ad, int32_t T, wl::AdapterPool &p) {
   return WL_OK;
 }
 
-// The pool's pointers, and its memory as inputs of a call.
-wl_status check_adapter_memory(const wl::AdapterPool &p, Ranges &r) {
+wl_status check_adapter_pointers(const wl::AdapterPool &p) {
   wl_status st;
   if ((st = check_aligned(p.vt, 16, "vt")) != WL_OK || (st = check_aligned(p.u, 16, "u")) != WL_OK ||
       (st = check_aligned(p.scale, 4, "scale")) != WL_OK || (st = check_optional(p.rank, 4, "rank")) != WL_OK)
     return st;
+  return WL_OK;
+}
+
+// The pool's memory as inputs of a call.
+void add_adapter_memory(const wl::AdapterPool &p, Ranges &r) {
   const size_t n = static_cast<size_t>(p.n), row = static_cast<size_t>(p.r) * 2;
   r.add(p.vt, n * p.nchild * row * p.K, "vt", false);
   r.add(p.u, n * p.Ntot * row, "u", false);
   r.add(p.scale, n * 4, "scale", false);
   r.add(p.rank, n * 4, "rank", false);
-  return WL_OK;
 }
 
 // ---- backward ----
@@ -1168,6 +1171,9 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
   if (!d_dx && !d_dw) return T == 0 ? WL_OK : fail(WL_EINVAL, "no output is asked for");
   if ((st = check_optional(d_dw, 16, "dw")) != WL_OK || (st = check_optional(d_dx, 16, "dx")) != WL_OK) return st;
   const size_t rows = static_cast<size_t>(T) * K * 2;
+  Ranges r;
+  r.add(d_w, norm_weight_bytes(c.w, K), "w", false);  // (without tokens too, where dw is zeroed)
+  r.add(d_dw, static_cast<size_t>(K) * 4, "dw", true);
   if (T > 0) {
     if ((st = check_aligned(d_dy, 16, "dy")) != WL_OK || (st = check_aligned(d_h, 16, "h")) != WL_OK ||
         (st = check_aligned(d_rstd, 4, "rstd")) != WL_OK || (st = check_aligned(d_w, 16, "w")) != WL_OK ||
@@ -1178,17 +1184,14 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
       if ((st = check_aligned(d_ws, 256, "workspace")) != WL_OK) return st;
       if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
     }
-    Ranges r;
     r.add(d_dy, rows, "dy", false);
     r.add(d_h, rows, "h", false);
     r.add(d_rstd, static_cast<size_t>(T) * 4, "rstd", false);
     r.add(d_dh, rows, "dh", false);
-    r.add(d_w, norm_weight_bytes(c.w, K), "w", false);
     r.add(d_dx, rows, "dx", true);
-    r.add(d_dw, static_cast<size_t>(K) * 4, "dw", true);
     r.add(d_ws, need, "the workspace", true);
-    if ((st = r.check({{"dx", "dy"}, {"dx", "dh"}})) != WL_OK) return st;
   }
+  if ((st = r.check({{"dx", "dy"}, {"dx", "dh"}})) != WL_OK) return st;
   c.dy = static_cast<const uint16_t *>(d_dy);
   c.h = static_cast<const uint16_t *>(d_h);
   c.rstd = d_rstd;
@@ -1213,14 +1216,15 @@ wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, 
   wl::AdapterPool p;
   wl_status st = check_adapters(adapters, T, p);
   if (st != WL_OK || T == 0) return st;
-  Ranges r;
-  if ((st = check_adapter_memory(p, r)) != WL_OK || (st = check_aligned(d_x, 16, "x")) != WL_OK ||
+  if ((st = check_adapter_pointers(p)) != WL_OK || (st = check_aligned(d_x, 16, "x")) != WL_OK ||
       (st = check_aligned(d_index, 4, "index")) != WL_OK || (st = check_aligned(d_base, 2, "base")) != WL_OK ||
       (st = check_aligned(d_y, 2, "y")) != WL_OK || (st = check_aligned(d_ws, 256, "workspace")) != WL_OK)
     return st;
   const size_t need = wl::adapters_workspace_bytes(p, T);
   if (ws_bytes < need) return fail(WL_ENOSPACE, "workspace has %zu bytes, call needs %zu", ws_bytes, need);
   const size_t yb = static_cast<size_t>(T) * p.Ntot * 2;
+  Ranges r;
+  add_adapter_memory(p, r);
   r.add(d_x, static_cast<size_t>(T) * p.K * 2, "x", false);
   r.add(d_index, static_cast<size_t>(T) * 4, "index", false);
   r.add(d_base, yb, "base", false);
@@ -1256,8 +1260,9 @@ wl_status weightless_adapters_backward(const wl_adapters *adapters, const void *
   Ranges r;
   r.add(grads->du, n * p.Ntot * row, "du", true);
   r.add(grads->dv, n * p.nchild * row * p.K, "dv", true);
+  add_adapter_memory(p, r);  // (without tokens too, where du and dv are zeroed)
   if (T > 0) {
-    if ((st = check_adapter_memory(p, r)) != WL_OK ||
+    if ((st = check_adapter_pointers(p)) != WL_OK ||
         (st = check_code_buffer(d_xcode, xcode_bytes, cs.bytes, "checkpoint")) != WL_OK ||
         (st = check_aligned(d_dy, 2, "dy")) != WL_OK || (st = check_aligned(d_index, 4, "index")) != WL_OK ||
         (st = check_aligned(d_ws, 256, "workspace")) != WL_OK)
