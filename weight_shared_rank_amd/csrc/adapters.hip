@@ -464,10 +464,12 @@ static_assert(kWaves * kWaveLds <= kRing, "the waves' pieces lie over the stages
 
 // ROOM: the pool's rank rounded up to 16, 64 or 256 (what a slot of a larger rank
 // needs costs the others registers; at 16 two workgroups fit a CU).  ONCE: much of
-// U, rank 16 (whole lines a load), is read past the caches, for slots with hardly more
-// than one tile (64 tokens of 57 adapters through 31B gate|up 28.6 -> 26.8 us, 400 of
-// them 52.5 -> 48; but 3200 tokens of 4 through 4096 x 4096 17.8 -> 22.7, 400 of 64 at
-// rank 64 34 -> 38).
+// U, rank 16 (whole lines a load), is read past the caches, in calls whose slots are many
+// for their tokens (64 tokens of 57 adapters through 31B gate|up 30.5 -> 27.2 us; but 3200
+// tokens of 4 through 4096 x 4096 17.8 -> 22.7, 400 of 64 at rank 64 34 -> 38) and there by
+// tiles that are not full: a full one's slot is likely to have more, which read the same
+// rows (1000 tokens in one of 64 slots of gate|up, past the caches 86, so 74; 64 of them 30
+// and 27.8).
 template <int ROOM, bool ONCE>
 __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(AdapterArgs a) {
   __shared__ int tok[kTileM];
@@ -502,16 +504,18 @@ __global__ __launch_bounds__(kThreads, ROOM == 16 ? 4 : 2) void few_kernel(Adapt
   };
   if (t.slot < 0)
     RowWalk<1, 0, ONCE>(a, t, c, tok, zs, lds).copy(first);
-  else if (ROOM == 16 || t.rank16 <= 16)
+  else if (ONCE && t.count < kTileM)
     RowWalk<1, 0, ONCE>(a, t, c, tok, zs, lds).run(first, form);
+  else if (ROOM == 16 || t.rank16 <= 16)
+    RowWalk<1, 0, false>(a, t, c, tok, zs, lds).run(first, form);
   else if (t.rank16 <= 32)
-    RowWalk<1, 1, ONCE>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<1, 1, false>(a, t, c, tok, zs, lds).run(first, form);
   else if (ROOM == 64 || t.rank16 <= 64)
-    RowWalk<1, 2, ONCE>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<1, 2, false>(a, t, c, tok, zs, lds).run(first, form);
   else if (t.rank16 <= 128)
-    RowWalk<2, 2, ONCE>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<2, 2, false>(a, t, c, tok, zs, lds).run(first, form);
   else
-    RowWalk<4, 2, ONCE>(a, t, c, tok, zs, lds).run(first, form);
+    RowWalk<4, 2, false>(a, t, c, tok, zs, lds).run(first, form);
 }
 
 // ---- many tokens -------------------------------------------------------------------
