@@ -272,8 +272,7 @@ struct Segment {
 };
 
 // The sum over a slot's tokens for 64 columns of dy (dU) or of X (VGRAD: dV), by 16 JF
-// ranks: 32 positions a step.  FULL: 64 columns exist.  ONCE: dy, too large to be found
-// in a cache, is read past it (31B gate|up 107 -> 99 us).
+// ranks: 32 positions a step.  FULL: 64 columns exist.  ONCE: dy is read past the caches.
 template <int JF, bool VGRAD, bool FEW, bool FULL, bool ONCE>
 __device__ __forceinline__ void sum_tokens(const GradArgs &a, const Segment &seg, int c, int j0, int col0, int cols, uint8_t *piece,
                                            f32x4 (&acc)[4][JF]) {
@@ -418,7 +417,7 @@ __device__ __forceinline__ int child_of_tile(const GradArgs &a, int &ct) {
 
 // WAYS 1: a wave has its own column tile; 4: the waves of a workgroup share one, a part of
 // the tokens each.
-template <int JF, bool VGRAD, int WAYS, bool FEW>
+template <int JF, bool VGRAD, int WAYS, bool FEW, bool ONCE>
 __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8_t *lds, int *list) {
   const int lane = threadIdx.x & 63, wave = keep(threadIdx.x >> 6);
   const int r = a.s.r;
@@ -461,9 +460,9 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
     for (int f = 0; f < JF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint8_t *const piece = lds + wave * kPiece;
   if (col0 + 64 <= cols)
-    sum_tokens<JF, VGRAD, FEW, true, WAYS == 1>(a, seg, c, j0, col0, cols, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, true, ONCE>(a, seg, c, j0, col0, cols, piece, acc);
   else
-    sum_tokens<JF, VGRAD, FEW, false, WAYS == 1>(a, seg, c, j0, col0, cols, piece, acc);
+    sum_tokens<JF, VGRAD, FEW, false, ONCE>(a, seg, c, j0, col0, cols, piece, acc);
   const int rank = slot_rank(a.s.rank, r, slot);
   // a pair of column tiles of rank tile f: the cut's sums for join_kernel, or the gradient
   f32x4 *const parts = a.parts + (static_cast<int64_t>(place) * a.units + unit) * 4 * JF * 64 + lane;
@@ -510,15 +509,15 @@ __device__ __forceinline__ void weight_unit(const GradArgs &a, int64_t id, uint8
   }
 }
 
-template <int JF, int WAYS, bool FEW>
+template <int JF, int WAYS, bool FEW, bool ONCE>
 __global__ __launch_bounds__(kGradWaves * 64, JF == 4 ? 2 : 4) void gradient_kernel(GradArgs a) {
   constexpr int SUM = WAYS == 1 ? 0 : kGradWaves * 4 * (JF < 2 ? JF : 2) * 1024, PIECES = kGradWaves * kPiece;
   __shared__ int tok[FEW ? kLeaderT : kM];
   __shared__ __align__(16) uint8_t lds[SUM > PIECES ? SUM : PIECES];
   int64_t id = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-  if (id < a.blocks[0]) return weight_unit<JF, false, WAYS, FEW>(a, id, lds, tok);
+  if (id < a.blocks[0]) return weight_unit<JF, false, WAYS, FEW, ONCE>(a, id, lds, tok);
   id -= a.blocks[0];
-  if (id < a.blocks[1]) return weight_unit<JF, true, WAYS, FEW>(a, id, lds, tok);
+  if (id < a.blocks[1]) return weight_unit<JF, true, WAYS, FEW, ONCE>(a, id, lds, tok);
   id -= a.blocks[1];
   if (id < a.blocks[2]) dx_unit(a, id, lds, tok);
 }
@@ -564,6 +563,12 @@ __global__ __launch_bounds__(256) void fill_zero_16(u32x4 *p, int64_t n) {
 }
 
 // ---- plan -----------------------------------------------------------------------------------
+// dy, just read for g, is found in the caches while it is small; a larger one is read past
+// them for dU, unless several groups of ranks read it (gradients of 31B gate|up with 16
+// adapters of rank 16, through the caches and past them: 300 tokens, 26 MB, 51.6 and 53.6 us;
+// 1000, 86 MB, 82.9 and 79.1; 4096, 352 MB, 193 and 186; of rank 128, two groups, 530 and 550).
+constexpr int64_t kCachedDy = int64_t{64} << 20;
+
 struct BackPlan {
   bool few;  // no grouping launch
   int tiles, NF, zgroups, zslices, zper, ggroups, gslices, gper, RC;
@@ -782,9 +787,13 @@ hipError_t launch_adapters_backward(const AdapterPool &p, const CodedView &x, co
   auto run = [&](auto jf) {
     constexpr int JF = decltype(jf)::value;
     if (q.few)
-      q.own ? gradient_kernel<JF, 1, true><<<blocks, kGradWaves * 64, 0, stream>>>(d) : gradient_kernel<JF, 4, true><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+      q.own ? gradient_kernel<JF, 1, true, false><<<blocks, kGradWaves * 64, 0, stream>>>(d)
+            : gradient_kernel<JF, 4, true, false><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+    else if (q.own && d.jgroups == 1 && static_cast<int64_t>(T) * p.Ntot * 2 > kCachedDy)
+      gradient_kernel<JF, 1, false, true><<<blocks, kGradWaves * 64, 0, stream>>>(d);
     else
-      q.own ? gradient_kernel<JF, 1, false><<<blocks, kGradWaves * 64, 0, stream>>>(d) : gradient_kernel<JF, 4, false><<<blocks, kGradWaves * 64, 0, stream>>>(d);
+      q.own ? gradient_kernel<JF, 1, false, false><<<blocks, kGradWaves * 64, 0, stream>>>(d)
+            : gradient_kernel<JF, 4, false, false><<<blocks, kGradWaves * 64, 0, stream>>>(d);
   };
   if (q.NF == 1)
     run(std::integral_constant<int, 1>{});
