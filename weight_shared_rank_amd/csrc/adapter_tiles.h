@@ -8,6 +8,7 @@
 #include "coded.h"
 #include "common.h"
 #include "lds_dma.h"
+#include "streams.h"
 
 namespace wl {
 

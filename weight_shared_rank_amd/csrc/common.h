@@ -16,11 +16,6 @@ __device__ __forceinline__ u32x4 ld16(const uint16_t *p) {
   return *reinterpret_cast<const u32x4 *>(p);
 }
 
-// 16 bytes of a stream that is read once: they leave the caches to the others.
-__device__ __forceinline__ u32x4 ld16_once(const uint16_t *p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-}
-
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) {
   return __uint_as_float(static_cast<uint32_t>(h) << 16);
 }

@@ -24,6 +24,7 @@
 #include "coded.h"
 #include "common.h"
 #include "lds_dma.h"
+#include "streams.h"
 
 namespace wl {
 
