@@ -431,7 +431,8 @@ wl_status weightless_stacked_backward(const wl_bundle *bundle, int32_t layer, in
                                       void *d_ws, size_t ws_bytes, void *stream);
 
 /* ---- Norm before a projection, with the residual's addition and a coded output ----
- * For each of T token rows of K elements (bf16):
+ * For each of T token rows of K elements (bf16; x, res, h and y are contiguous [T, K],
+ * so heads within wider rows are copied out first):
  *   h = bf16(x + res)                        (h = x if d_res is NULL)
  *   a = 1 / sqrt(mean_k h_k^2 + eps)         (the mean and a in float64, a stored as float32)
  *   y = bf16(h a (offset + w))               (a in full, one rounding)
@@ -478,7 +479,8 @@ wl_status weightless_norm_backward(const void *d_dy, const void *d_h, const floa
  * and y[t] = base[t], bit for bit, without an adapter: where d_index[t] lies
  * outside [0, num_slots) or the slot's rank is not positive.  base is what the
  * shared projection gave (weightless_linear, weightless_stacked_linear,
- * weightless_coded_linear).  Slots change between calls as their owner
+ * weightless_coded_linear); weightless_gate_up_act has applied its activation by then,
+ * so with adapters on gate|up the activation is the caller's.  Slots change between calls as their owner
  * likes (the memory is the caller's; a captured call reads what it holds when
  * it is replayed, as it does for d_index, d_scale and d_rank).
  *  num_slots in [1, 4096]; rank (the room of every slot) a multiple of 16 in
@@ -500,7 +502,8 @@ typedef struct {
 } wl_adapters;
 
 /* Workspace bytes of weightless_adapters_add with T tokens; 0 with
- * wl_last_error() set on error.  Fewer tokens can need more. */
+ * wl_last_error() set on error.  Fewer tokens can need more: a workspace for several T
+ * has the largest of their sizes. */
 size_t weightless_adapters_workspace_bytes(const wl_adapters *adapters, int32_t T);
 
 /*  d_x bf16 [T, K] (16-byte aligned), d_index int32 [T], d_base and d_y bf16
@@ -527,7 +530,8 @@ wl_status weightless_adapters_add(const wl_adapters *adapters, const void *d_x, 
  *   dU_a = sum of dy[t] z^T,  dV_a^T = sum of g X[t]^T   over the slot's tokens
  * Tokens without an adapter leave dx[t] = base[t], bit for bit, and enter nothing
  * else; a slot without tokens has zero gradients, and so have the rows and
- * columns from a slot's rank on.  Sums in float32, z and g in three parts of bf16 (all
+ * columns from a slot's rank on: dU and dV are written whole, for every slot of the
+ * pool, and not added to what they held.  Sums in float32, z and g in three parts of bf16 (all
  * 24 bits of a float32) where they enter the second products; every output is rounded
  * once.  The sums over tokens have a fixed order: the same bits from run to run,
  * whichever gradients are asked for.  What is not finite in a token
@@ -539,7 +543,8 @@ typedef struct {
   void *dv;         /* bf16 [num_slots][num_children][rank][K], V^T's gradient */
 } wl_adapter_grads;
 
-/* Workspace bytes with T tokens; 0 with wl_last_error() set on error. */
+/* Workspace bytes with T tokens; 0 with wl_last_error() set on error.  Fewer tokens can
+ * need more: a workspace for several T has the largest of their sizes. */
 size_t weightless_adapters_backward_workspace_bytes(const wl_adapters *adapters, int32_t T);
 
 /*  d_xcode: coded activations [T, K] (weightless_act_encode, weightless_norm;

@@ -692,7 +692,7 @@ def _only_wanted(want, known, given):
 
 def norm_act(x, weight, eps: float = 1e-6, residual=None, offset: float = 0.0, want=("y",), y=None,
              code: Optional[ActCode] = None, h=None, rstd=None, stream=None) -> Normed:
-    """Root-mean-square norm of x (+ residual), bf16 [T, K] (weightless_norm).
+    """Root-mean-square norm of x (+ residual), bf16 [T, K], contiguous (weightless_norm).
 
     weight: bf16 or float32 [K], added to `offset`.  want: which of y (bf16),
     code (ActCode of y: coded_linear's operand and the backward calls'
@@ -829,7 +829,7 @@ class AdapterPool:
         self.rank[slot] = 0
 
     def workspace_bytes(self, T: int) -> int:
-        """Workspace bytes of add() with T tokens."""
+        """Workspace bytes of add() with T tokens (fewer can need more)."""
         need = self._need.get(T)
         if need is None:
             need = lib().weightless_adapters_workspace_bytes(self._ref, T)
@@ -860,7 +860,7 @@ class AdapterPool:
         return y
 
     def backward_workspace_bytes(self, T: int) -> int:
-        """Workspace bytes of backward() with T tokens."""
+        """Workspace bytes of backward() with T tokens (fewer can need more)."""
         need = self._backward_need.get(T)
         if need is None:
             need = lib().weightless_adapters_backward_workspace_bytes(self._ref, T)
@@ -875,8 +875,8 @@ class AdapterPool:
 
         x: the ActCode checkpoint of the call's input; dy: bf16 [T, N]; base: bf16
         [T, K], the shared projection's dx, which dx adds to (dx may be base).
-        du and dv have u's and vt's shapes, bf16; outputs are allocated if not
-        given."""
+        du and dv have u's and vt's shapes, bf16, written for every slot; outputs are
+        allocated if not given."""
         import torch
         dev = self.device
         if not isinstance(x, ActCode) or x.K != self.K or x.buf.device != dev:

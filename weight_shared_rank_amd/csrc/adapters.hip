@@ -19,9 +19,9 @@
 // products with U and base (expand_kernel), in tiles of 64 tokens; between them, where
 // many workgroups would add up the same slices, finish_kernel.
 //
-// Measured: 1 token through 1B q|k|v 5.5 us, of which a launch is most; 64 tokens of 57
-// adapters through 31B gate|up 26.5 (103 MB read, 114 moved); 4096 tokens of 12 through 31B
-// o at rank 64 6.9 + 19 + 5 + 26 (thin_kernel 80 MB at 4.2 TB/s, expand_kernel 100 at 3.9).
+// Measured: 1 token through 1B q|k|v 5.6 us, of which a launch is most; 64 tokens of 57
+// adapters through 31B gate|up 27 (103 MB read, 114 moved); 4096 tokens of 12 through 31B
+// o at rank 64 6.6 + 19 + 5 + 26.6 (thin_kernel 80 MB at 4.2 TB/s, expand_kernel 100 at 3.8).
 //
 // Everything moves as rows, 8 lanes to a cache line, and reaches the matrix cores
 // through LDS: fragments loaded as they are used (16 rows of 64 bytes a load) pass
@@ -697,12 +697,14 @@ struct Plan {
 //   group_kernel  5000
 //   the others    15000, x and V^T, expand_kernel's workgroups (900 in 4300 ns) or base
 //                 and y, U, and 5000 for finish_kernel
-// Kernels' times in us, in that order (most within 20% of the estimates):
+// Kernels' times in us, in that order (most within 20% of the estimates; over 60 drawn calls
+// the choice is 2% slower than the best of the three, in 10 of them more than 5%, at worst 32%;
+// tiles of 64 that are mostly part-filled are counted too low: the third figure of 1600):
 //   333 tokens of 1160 -> 1001, rank 32            9.6  12.5  14.8
-//   64 tokens of 57 adapters, 31B gate|up, rank 16  28    33    66;  400: 87, 59, 70;  1600: -, 106, 125
-//   4096 -> 4096, rank 16, 200 tokens 13.9, 12.5, 15.8;  3200: -, 24, 33
+//   64 tokens of 57 adapters, 31B gate|up, rank 16  28    33    66;  400: 81, 54, 72;  1600: -, 106, 124
+//   4096 -> 4096, rank 16, 200 tokens 13.8, 12.8, 15.2;  3200: -, 25, 34
 //   31B gate|up, 8 adapters, 400 tokens -, 27, 42;  800: -, 59, 53;  3200: -, 164, 151
-//   4096 -> 4096, rank 128, 200 tokens 37, 30, 22;  8192 -> 5376, rank 64, 400: 35, 30, 24
+//   4096 -> 4096, rank 128, 200 tokens 37, 31, 23;  8192 -> 5376, rank 64, 400: 36, 30, 27
 enum class Form { kAlone, kGrouped16, kGrouped64 };
 
 Form fastest_form(const AdapterPool &p, int T) {

@@ -21,10 +21,11 @@
 //
 // Bound by memory: dy is read twice, for g and for dU, and everything else once.  As
 // in the forward pass no load of a loop is conditional.  4096 tokens of 16 adapters
-// through 31B gate|up, rank 32: 7 + 96 + 6 + 98 + 4 us; project_kernel reads 418 MB (4.4
-// TB/s), gradient_kernel moves 560 MB (5.7 TB/s).  2048 tokens
-// through 1B q|k|v: 6.3 + 9 + 11.  One pass over dy would hold dU of 64 columns and all
-// ranks in a wave and write g of each 512 columns, 176 MB for the 352 it saves; not built.
+// through 31B gate|up, rank 32: 7 + 97 + 7 + 107 + 4 us; project_kernel reads 418 MB (4.3
+// TB/s), gradient_kernel moves 560 MB (5.2 TB/s).  2048 tokens
+// through 1B q|k|v: 6.4 + 9.4 + 11.7.  One pass over dy would hold dU of 64 columns and the
+// child's ranks in a wave and write g of each 512 columns, 44 MB to and 44 from memory for the
+// 352 it saves; not built.
 #include <type_traits>
 
 #include "adapter_factors.h"
@@ -613,8 +614,8 @@ BackPlan make_back_plan(const AdapterPool &p, int T) {
   // How a call's tokens spread over the slots is not known here.  If one slot has them
   // all, its cuts are to keep 4 workgroups, or 16 waves, of a CU busy (3409 tokens in one
   // of 23 slots, 2 x 169 x 64 at rank 48: 85 -> 32 us; 8192 of one 1B q|k|v adapter 77 ->
-  // 58; 4096 in one of 16 of 31B gate|up 288 -> 235).  Joining takes 4 us, cut or not (2048
-  // tokens of 8 1B q|k|v adapters 26.7 -> 31.8), so shorter calls go without (one of 8
+  // 58; 4096 in one of 16 of 31B gate|up 288 -> 235, evenly spread 221).  Joining takes 4 us, cut
+  // or not (2048 tokens of 8 1B q|k|v adapters 26.7 -> 31.8), so shorter calls go without (one of 8
   // slots of 4096 -> 2048 would gain 3 us from 2048 tokens; with own column tiles 1071
   // tokens in one of 34 slots 137 -> 85).  Cuts of 16 steps or 8, and of 24, 16 or 12 with
   // own tiles, differ by 10%.
