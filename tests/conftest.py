@@ -14,7 +14,8 @@ def pytest_configure(config):
 
 # Tests of refusals with made-up device addresses: a refusal that got lost would launch a
 # kernel on them, so they run only where no GPU is visible.
-MADE_UP_ADDRESSES = {"test_coded_cpu.py", "test_norm_cpu.py", "test_adapters_cpu.py", "test_empty_calls_cpu.py"}
+MADE_UP_ADDRESSES = {"test_coded_cpu.py", "test_norm_cpu.py", "test_adapters_cpu.py", "test_empty_calls_cpu.py",
+                     "test_adapter_workspaces_cpu.py"}
 
 
 def pytest_runtest_setup(item):
