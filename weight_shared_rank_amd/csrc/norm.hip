@@ -427,7 +427,7 @@ constexpr int kOneLaunchRows = 1024;
 bool one_backward_launch(int T, int K) { return T > rows_of_workgroup(K) && T <= kOneLaunchRows; }
 
 // Calls that move more than the last cache holds load past it, so that it keeps what
-// they write (8192 x 5376 backward 69 -> 60 us; forward 77 -> 76, and 78 -> 66 where the
+// they write (8192 x 5376 backward 69 -> 60 us; forward 79 -> 78, and 81 -> 70 where the
 // outputs' memory is used again; stores past it too: 70); the inputs of smaller calls
 // often lie in it (backward of 800 x 5376, so loaded: 13 -> 15 us).
 constexpr int64_t kLastCache = int64_t{256} << 20;
